@@ -334,6 +334,163 @@ void cp_destroy(cp_handle* h);
  * works" (a step the kernel cannot take runs the loop instead). */
 const char* cp_strerror(int status);
 
+/* ============================================================ paged cache
+ * Keys and values of the rows' longer context: a talker's layers run one step
+ * (or read one piece of a prompt) for the rows whose frame follows, and each
+ * row attends over thousands of cached positions. The frame's own K/V lives
+ * for one frame inside the handle; this cache outlives it. It is kept in
+ * pages that the caller owns, in bfloat16 or in 8 bits, and has three calls:
+ * cp_cache_append normalises, rotates, quantises and writes the rows of a qkv
+ * projection, cp_cache_attend lets each sequence's new rows attend over its
+ * cached positions, cp_cache_read returns cached rows as bfloat16. */
+enum cp_cache_dtype {
+  CP_CACHE_BF16 = 0,
+  CP_CACHE_E4M3 = 1     /* 8-bit float (1-4-3) times a power of two that each
+                           position and kv head has for its key and for its
+                           value: the least 2^e with max |x| <= 448 * 2^e over
+                           the head's finite elements, e >= -110, kept as the
+                           byte e + 127. Each element is rounded once, to the
+                           nearest, ties to even; a power of two costs a float
+                           format no precision, and every element is a
+                           bfloat16 exactly. An infinity or NaN is kept as
+                           NaN */
+};
+
+/* Layout of a cache. Pages are [pages][kv_heads][page_size][head_dim], with
+ * the same strides for keys and values; strides count elements, 0 means
+ * contiguous. Scales are [pages][kv_heads][page_size] bytes. Limits
+ * (CP_ERR_UNSUPPORTED outside): head_dim 64 or 128, page_size 16, 32, 64 or
+ * 128, 1 <= kv_heads <= 128, k and v aligned to 16 bytes and the strides
+ * multiples of 16 bytes. */
+typedef struct cp_cache_desc {
+  int dtype;                  /* enum cp_cache_dtype                         */
+  int kv_heads;
+  int head_dim;
+  int page_size;              /* positions per page                          */
+  int pages;                  /* pages in the pool                           */
+  void* k;                    /* device, caller-owned for the cache's life   */
+  void* v;
+  int64_t page_stride, head_stride, token_stride;
+  uint8_t* k_scale;           /* device, CP_CACHE_E4M3 only (else NULL)      */
+  uint8_t* v_scale;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+} cp_cache_desc;
+
+/* A ragged batch. Sequence i has the rows start[i] .. start[i+1]-1 of the
+ * calls' row arrays (none is fine), and length[i] cached positions, these
+ * rows' own included: row r is at position length[i] - (start[i+1] - r).
+ * Rows from start[sequences] on belong to nobody and are left as they are.
+ * Position t of sequence i is in place t % page_size of page
+ * page_table[i * table_stride + t / page_size]; entries past its length are
+ * never read. Sequences may share pages (a common prefix), as long as no two
+ * rows of one cp_cache_append land on the same place.
+ * The arrays are read on the device when the call runs there, so a captured
+ * call follows what they hold at each replay; what a launch is sized by is
+ * rows, max_new and max_length. Checked on the device, without leaving any
+ * array's bounds: a start that descends or passes rows, more new rows than
+ * max_new, a length outside 0 .. max_length, a page outside the pool and a
+ * row of cp_cache_append or cp_cache_read at a negative position set the
+ * cache's sticky CP_ERR_DEVICE_BOUNDS; bad starts and lengths are clamped, a
+ * bad page reads as zeros and is not written. */
+typedef struct cp_batch {
+  int sequences;              /* 1 .. 65535                                  */
+  int rows;                   /* rows of the row arrays, >= 1                */
+  int max_new;                /* most new rows of any sequence (0: rows)     */
+  int max_length;             /* largest length (0: all that the table holds,
+                                 table_width * page_size)                    */
+  int table_width;            /* entries per sequence in page_table          */
+  int64_t table_stride;       /* entries from one sequence to the next (0:
+                                 table_width)                                */
+  const int32_t* start;       /* device [sequences + 1], start[0] = 0        */
+  const int32_t* length;      /* device [sequences]                          */
+  const int32_t* page_table;  /* device                                      */
+} cp_batch;
+
+typedef struct cp_append {
+  const void* qkv;            /* device bf16 [rows][(q_heads + 2 kv_heads) *
+                                 head_dim]: q | k | v, as w_qkv's rows       */
+  int64_t qkv_stride;         /* elements from row to row (0: contiguous)    */
+  void* q_out;                /* device bf16 [rows][q_heads][head_dim]       */
+  int64_t q_stride;           /* elements from row to row (0: contiguous)    */
+  int q_heads;                /* 0 .. 1024; 0 with q_out NULL: only k | v    */
+  const void* q_norm;         /* device bf16 [head_dim] or NULL: no norm     */
+  const void* k_norm;
+  float rms_eps;
+  float rope_base;            /* 0: no rotation                              */
+} cp_append;
+
+typedef struct cp_attend {
+  const void* q;              /* device bf16 [rows][q_heads][head_dim]       */
+  void* out;                  /* device bf16, the same shape                 */
+  int64_t q_stride, q_head_stride;      /* elements; 0: contiguous           */
+  int64_t out_stride, out_head_stride;
+  int q_heads;                /* a multiple of kv_heads, up to 64 times; q
+                                 head h reads kv head h / (q_heads/kv_heads) */
+  float scale;                /* of the scores, > 0 (0: head_dim^-1/2)       */
+  int causal;                 /* nonzero: a row sees positions up to its own;
+                                 zero: all length[i] positions               */
+  int window;                 /* > 0: only positions after its own position
+                                 minus window; 0: no window                  */
+} cp_attend;
+
+typedef struct cp_cache cp_cache; /* opaque, owned by the library */
+
+/* Make a cache object for pages that the caller owns (device memory, kept
+ * for the object's life; what they hold is not touched). Errors:
+ * CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (layout or device), CP_ERR_NOMEM,
+ * CP_ERR_CUDA. The calls below run on the cache's device, whichever is
+ * current. The object holds no scratch: calls on several streams may overlap
+ * as far as their arrays, pages and workspaces do. */
+int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out);
+
+/* Write the batch's rows to the cache: q and k of each row are normalised
+ * over the head (x * (mean(x^2) + eps)^(-1/2) * gain, if a gain is given) and
+ * rotated by the row's position (rotate-half, pairs (j, j + head_dim/2),
+ * angle position * rope_base^(-2j/head_dim)), as in the frame's layer, in
+ * fp32; q is rounded to q_out, k and v are rounded or quantised into the
+ * row's place. One launch. qkv, q_out and the gains are 16-byte aligned,
+ * strides multiples of 8 elements. */
+int cp_cache_append(cp_cache* c, const cp_batch* batch, const cp_append* args, cp_stream_t stream);
+
+/* The key and value cached at each of the batch's rows' positions, device
+ * bf16 [rows][kv_heads][head_dim] (either may be NULL): a batch whose start
+ * counts each sequence's last n positions reads those back, whole sequences
+ * with n = length. One launch. */
+int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, cp_stream_t stream);
+
+/* Attention of the batch's rows over their sequences' cached positions, the
+ * rows' own among them (append them first): softmax over the visible
+ * positions t of scale * q . k_t, times v_t; a row that sees none (no cached
+ * position, or a negative position of its own) gives zeros. What a masked
+ * position holds does not matter, infinities and NaN included. Scores,
+ * softmax statistics and sums are fp32; the weights are rounded to bfloat16
+ * (fp16 over an e4m3 cache) for the product with v, and the result once to
+ * bfloat16. Results are bit-identical run to run. `workspace`: device memory
+ * of at least cp_cache_check's workspace_bytes, 16-byte aligned, nothing kept
+ * in it between calls; calls that may overlap, captured ones included, need
+ * workspaces of their own. q and out are 16-byte aligned, strides multiples
+ * of 8 elements. Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA;
+ * a wait inside the kernel that gives up sets the sticky CP_ERR_TIMEOUT. */
+int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, void* workspace,
+                    size_t workspace_bytes, cp_stream_t stream);
+
+/* Synchronise the device and return the cache's sticky device status (CP_OK,
+ * CP_ERR_DEVICE_BOUNDS or CP_ERR_TIMEOUT; CP_ERR_CUDA if the synchronisation
+ * fails); reset it. Calls on a cache whose status is set still run. */
+int cp_cache_status(cp_cache* c);
+int cp_cache_clear_status(cp_cache* c);
+
+/* Release the object (synchronises its device), not the pages. */
+void cp_cache_destroy(cp_cache* c);
+
+/* Host only: the status that the calls return for these arguments, without a
+ * GPU. batch, append and attend may each be NULL (not checked; the latter two
+ * need batch). *workspace_bytes (may be NULL) is what cp_cache_attend needs
+ * for batch and attend: it depends on sequences, rows, max_new, max_length
+ * and attend's heads and mask, not on what the arrays hold. */
+int cp_cache_check(const cp_cache_desc* desc, const cp_batch* batch, const cp_append* append,
+                   const cp_attend* attend, size_t* workspace_bytes);
+
 /* ------------------------------------------------------------ host checks */
 /* Build the static schedule for `shape` with `grid` CTAs in clusters of
  * `cluster`, without a GPU, and check it: every wait is matched by exactly
@@ -373,6 +530,12 @@ int cp_test_philox(const uint32_t* ctr, const uint32_t* key, int n, int use_cura
  * int32 codes [rows]. 1 <= rows, vocab a multiple of 256 up to 2048. */
 int cp_test_draw(const float* logits, int rows, int vocab, const cp_sampler* sampler,
                  int group, int32_t* codes, cp_stream_t stream);
+
+/* The kernels' own look-up of a cached position, run on the host: the element
+ * offset of position `pos` of a sequence whose table row is `table` (host,
+ * table_width entries), for kv head `head`, or -1 where the kernels would set
+ * CP_ERR_DEVICE_BOUNDS and skip the access. */
+int64_t cp_test_slot(const cp_cache_desc* desc, const int32_t* table, int table_width, int pos, int head);
 
 #ifdef __cplusplus
 }

@@ -5,4 +5,4 @@ its ctypes binding, ``build`` compiles it in-tree and ``torch_io`` turns numpy
 inputs into the torch tensors the binding takes.
 """
 from . import cp  # noqa: F401
-from .cp import Frame, CPError  # noqa: F401
+from .cp import Batch, Cache, CPError, Frame  # noqa: F401

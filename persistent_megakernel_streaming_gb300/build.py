@@ -27,6 +27,8 @@ SOURCES = [
     ("cp_kernel.cu", "cp_kernel_1p7b_r128.cu.o", ["-DCP_SHAPE_1P7B", "-DCP_ROWS_128"]),
     ("cp_host.cu", "cp_host.cu.o", []),
     ("cp_plan.cpp", "cp_plan.cpp.o", []),
+    ("cp_cache.cu", "cp_cache.cu.o", []),
+    ("cp_attend.cu", "cp_attend.cu.o", []),
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -23,7 +23,9 @@ CP_ERR_RANGE = 10
 
 EXPORTS = ["cp_create", "cp_frame", "cp_frame_split", "cp_debug_logits", "cp_debug_state", "cp_status",
            "cp_clear_status", "cp_get_info", "cp_trace", "cp_destroy", "cp_strerror",
-           "cp_plan_check", "cp_test_philox", "cp_test_draw", "cp_frame_static"]
+           "cp_plan_check", "cp_test_philox", "cp_test_draw", "cp_frame_static",
+           "cp_cache_create", "cp_cache_append", "cp_cache_read", "cp_cache_attend", "cp_cache_status",
+           "cp_cache_clear_status", "cp_cache_destroy", "cp_cache_check", "cp_test_slot"]
 
 
 class Shape(C.Structure):
@@ -66,6 +68,32 @@ class PlanStats(C.Structure):
                 ("max_tasks_per_cta", C.c_int), ("message", C.c_char * 160)]
 
 
+class CacheDesc(C.Structure):
+    _fields_ = [("dtype", C.c_int), ("kv_heads", C.c_int), ("head_dim", C.c_int), ("page_size", C.c_int),
+                ("pages", C.c_int), ("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("token_stride", C.c_int64), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("scale_page_stride", C.c_int64), ("scale_head_stride", C.c_int64),
+                ("scale_token_stride", C.c_int64)]
+
+
+class BatchDesc(C.Structure):
+    _fields_ = [("sequences", C.c_int), ("rows", C.c_int), ("max_new", C.c_int), ("max_length", C.c_int),
+                ("table_width", C.c_int), ("table_stride", C.c_int64), ("start", C.c_void_p), ("length", C.c_void_p),
+                ("page_table", C.c_void_p)]
+
+
+class AppendArgs(C.Structure):
+    _fields_ = [("qkv", C.c_void_p), ("qkv_stride", C.c_int64), ("q_out", C.c_void_p), ("q_stride", C.c_int64),
+                ("q_heads", C.c_int), ("q_norm", C.c_void_p), ("k_norm", C.c_void_p), ("rms_eps", C.c_float),
+                ("rope_base", C.c_float)]
+
+
+class AttendArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("out", C.c_void_p), ("q_stride", C.c_int64), ("q_head_stride", C.c_int64),
+                ("out_stride", C.c_int64), ("out_head_stride", C.c_int64), ("q_heads", C.c_int), ("scale", C.c_float),
+                ("causal", C.c_int), ("window", C.c_int)]
+
+
 class CPError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -100,6 +128,18 @@ def lib() -> C.CDLL:
         L.cp_plan_check.argtypes = [C.POINTER(Shape), i, i, i, i, C.POINTER(PlanStats)]
         L.cp_test_philox.argtypes = [vp, vp, i, i, vp, st]
         L.cp_test_draw.argtypes = [vp, i, i, C.POINTER(Sampler), i, vp, st]
+        L.cp_cache_create.argtypes = [C.POINTER(CacheDesc), i, C.POINTER(vp)]
+        L.cp_cache_append.argtypes = [vp, C.POINTER(BatchDesc), C.POINTER(AppendArgs), st]
+        L.cp_cache_read.argtypes = [vp, C.POINTER(BatchDesc), vp, vp, st]
+        L.cp_cache_attend.argtypes = [vp, C.POINTER(BatchDesc), C.POINTER(AttendArgs), vp, C.c_size_t, st]
+        L.cp_cache_status.argtypes = [vp]
+        L.cp_cache_clear_status.argtypes = [vp]
+        L.cp_cache_destroy.argtypes = [vp]
+        L.cp_cache_destroy.restype = None
+        L.cp_cache_check.argtypes = [C.POINTER(CacheDesc), C.POINTER(BatchDesc), C.POINTER(AppendArgs),
+                                     C.POINTER(AttendArgs), C.POINTER(C.c_size_t)]
+        L.cp_test_slot.argtypes = [C.POINTER(CacheDesc), C.POINTER(C.c_int32), i, i, i]
+        L.cp_test_slot.restype = C.c_int64
         _lib = L
     return _lib
 
@@ -212,6 +252,169 @@ class Frame:
     def close(self):
         if getattr(self, "_h", None):
             lib().cp_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _bits(t, what: str, size: int):
+    """t, checked to hold `size`-byte elements (bf16 or their bit patterns; e4m3 or theirs)."""
+    if t.element_size() != size or t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what}: {size}-byte elements, the last axis contiguous")
+    return t
+
+
+def _stride(t, axis: int) -> int:
+    """Elements between t's entries along `axis`; 0 (the C side's "contiguous") where there is one at most."""
+    if t.shape[axis] <= 1:
+        return 0
+    if t.stride(axis) <= 0:
+        raise ValueError("a tensor whose entries share memory (an expanded one)")
+    return t.stride(axis)
+
+
+class Batch:
+    """A ragged batch (cp_batch): row ``start[i] + j`` of the calls' row arrays is sequence i's new row j.
+
+    ``start`` int32 [sequences + 1], ``length`` int32 [sequences] (cached positions, the new rows' own included),
+    ``pages`` int32 [sequences][width]; device tensors, read when a call runs on the device. ``rows`` is the row
+    arrays' length, ``max_new`` and ``max_len`` bound the new rows and the length of any sequence (0: no bound
+    but the arrays' own)."""
+
+    def __init__(self, start, length, pages, rows: int, max_new: int = 0, max_len: int = 0):
+        import torch
+        for name, t in (("start", start), ("length", length), ("pages", pages)):
+            if t.dtype != torch.int32 or t.stride(-1) != 1 and t.shape[-1] > 1:
+                raise ValueError(f"{name}: int32, contiguous")
+        if length.dim() != 1 or start.dim() != 1 or pages.dim() != 2 or start.numel() != length.numel() + 1 or \
+                pages.shape[0] != length.numel():
+            raise ValueError("start [n + 1], length [n] and pages [n][width]")
+        self.start, self.length, self.pages, self.rows = start, length, pages, int(rows)
+        self.desc = BatchDesc(length.numel(), int(rows), int(max_new), int(max_len), pages.shape[1],
+                              _stride(pages, 0), _ptr(start), _ptr(length), _ptr(pages))
+
+
+class Cache:
+    """A paged K/V cache (cp_cache_create) over the caller's tensors.
+
+    ``k``, ``v``: [pages][kv_heads][page_size][head_dim] bf16 (or int16 bit patterns), or e4m3 (or uint8) with
+    ``k_scale``, ``v_scale`` uint8 [pages][kv_heads][page_size]; both of the same strides. See include/cp.h for
+    what the calls compute."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        size = k.element_size()
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.device != v.device or \
+                k.device.type != "cuda":
+            raise ValueError("k and v: [pages][kv_heads][page_size][head_dim] of the same strides, on one GPU")
+        if size not in (1, 2) or (size == 1) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("bf16 pages without scales, or e4m3 pages with k_scale and v_scale")
+        _bits(k, "k", size)
+        _bits(v, "v", size)
+        scale_strides = (0, 0, 0)
+        if size == 1:
+            for t in (k_scale, v_scale):
+                if t.element_size() != 1 or t.shape != k.shape[:3] or t.stride() != k_scale.stride() or t.device != k.device:
+                    raise ValueError("scales: uint8 [pages][kv_heads][page_size] of the same strides")
+            scale_strides = [_stride(k_scale, i) for i in range(3)]
+        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.keep = (k, v, k_scale, v_scale)
+        self.device = k.device
+        self.desc = CacheDesc(int(size == 1), self.kv_heads, self.head_dim, self.page_size, self.pages, _ptr(k), _ptr(v),
+                              *(_stride(k, i) for i in range(3)), _ptr(k_scale), _ptr(v_scale), *scale_strides)
+        h = C.c_void_p()
+        _check(lib().cp_cache_create(C.byref(self.desc), k.device.index, C.byref(h)), "cp_cache_create")
+        self._h = h
+
+    def append(self, batch: Batch, qkv, q_out=None, q_norm=None, k_norm=None, rms_eps: float = 1e-6,
+               rope_base: float = 0.0, stream=None):
+        """qkv [rows][(q_heads + 2 kv_heads) * head_dim] into the cache, its q into q_out [rows][q_heads][head_dim]."""
+        heads = 0 if q_out is None else q_out.shape[1]
+        self._rows(batch, _bits(qkv, "qkv", 2), (heads + 2 * self.kv_heads) * self.head_dim)
+        if q_out is not None:
+            self._rows(batch, _bits(q_out, "q_out", 2), heads, self.head_dim)
+            if heads > 1 and q_out.stride(1) != self.head_dim:
+                raise ValueError("q_out: contiguous heads")
+        for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if t is not None and (t.shape != (self.head_dim,) or t.device != self.device or _bits(t, name, 2) is None):
+                raise ValueError(f"{name}: [head_dim] on the cache's device")
+        a = AppendArgs(_ptr(qkv), _stride(qkv, 0), _ptr(q_out), 0 if q_out is None else _stride(q_out, 0), heads, _ptr(q_norm),
+                       _ptr(k_norm), float(rms_eps), float(rope_base))
+        _check(lib().cp_cache_append(self._h, C.byref(batch.desc), C.byref(a), self._stream(stream)), "cp_cache_append")
+
+    def read(self, batch: Batch, k_out=None, v_out=None, stream=None):
+        """The batch's rows' cached keys and values as bf16 [rows][kv_heads][head_dim]."""
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is not None:
+                self._rows(batch, _bits(t, name, 2), self.kv_heads, self.head_dim)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name}: contiguous")
+        _check(lib().cp_cache_read(self._h, C.byref(batch.desc), _ptr(k_out), _ptr(v_out), self._stream(stream)),
+               "cp_cache_read")
+
+    def attend(self, batch: Batch, q, out, scale: float = 0.0, causal: bool = True, window: int = 0, workspace=None,
+               stream=None):
+        """Attention of q [rows][q_heads][head_dim] over the cache into out (the same shape). Without a
+        ``workspace`` (device bytes, see workspace_bytes) one is taken from torch's allocator for this call."""
+        for name, t in (("q", q), ("out", out)):
+            self._rows(batch, _bits(t, name, 2), q.shape[1], self.head_dim)
+        a = AttendArgs(_ptr(q), _ptr(out), _stride(q, 0), _stride(q, 1), _stride(out, 0), _stride(out, 1), q.shape[1], float(scale),
+                       int(causal), int(window))
+        need = C.c_size_t()
+        _check(lib().cp_cache_check(C.byref(self.desc), C.byref(batch.desc), None, C.byref(a), C.byref(need)),
+               "cp_cache_attend")
+        if workspace is None and need.value:
+            workspace = self._workspace(need.value, stream)
+        if workspace is not None and (workspace.device != self.device or not workspace.is_contiguous()):
+            raise ValueError("workspace: contiguous, on the cache's device")
+        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib().cp_cache_attend(self._h, C.byref(batch.desc), C.byref(a), _ptr(workspace), size, self._stream(stream)),
+               "cp_cache_attend")
+
+    def workspace_bytes(self, batch: Batch, q_heads: int, causal: bool = True, window: int = 0) -> int:
+        """What ``attend`` needs for this batch, whatever its arrays hold."""
+        a = AttendArgs(16, 32, 0, 0, 0, 0, int(q_heads), 0.0, int(causal), int(window))
+        need = C.c_size_t()
+        _check(lib().cp_cache_check(C.byref(self.desc), C.byref(batch.desc), None, C.byref(a), C.byref(need)),
+               "cp_cache_check")
+        return need.value
+
+    def _rows(self, batch, t, *shape):
+        if batch.start.device != self.device or batch.length.device != self.device or batch.pages.device != self.device:
+            raise ValueError("a batch on another device than the cache's")
+        if t.shape != (batch.rows, *shape):
+            raise ValueError(f"rows of shape {(batch.rows, *shape)} are wanted, got {tuple(t.shape)}")
+        if t.device != self.device:
+            raise ValueError("a tensor on another device than the cache's")
+
+    def _stream(self, stream) -> int:
+        if stream is None:
+            import torch
+            return int(torch.cuda.current_stream(self.device).cuda_stream)
+        return _stream(stream)
+
+    def _workspace(self, size, stream):
+        # allocated on the stream that uses it, so that the allocator hands it on in that stream's order
+        import torch
+        if stream is None:
+            return torch.empty(size, dtype=torch.uint8, device=self.device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(size, dtype=torch.uint8, device=self.device)
+
+    def status(self) -> int:
+        return lib().cp_cache_status(self._h)
+
+    def clear_status(self):
+        _check(lib().cp_cache_clear_status(self._h), "cp_cache_clear_status")
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().cp_cache_destroy(self._h)
             self._h = None
 
     def __del__(self):

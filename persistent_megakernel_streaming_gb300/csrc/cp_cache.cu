@@ -1,0 +1,539 @@
+// cp_cache.cu -- the paged K/V cache: its C ABI (checks and launches), the
+// append kernel (QK-norm, RoPE, quantisation, write) and the read-back kernel.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "cp.h"
+#include "cp_cache.cuh"
+
+using namespace cp;
+using namespace cp::cache;
+
+struct cp_cache {
+  int device = 0;
+  cp_cache_desc d{};
+  CacheView view{};
+};
+
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kReadThreads = 256;
+constexpr int kMaxRowsPerBlock = 8;    // one warp finds one row's sequence
+
+// ------------------------------------------------------------------ rows
+// Where a row goes: its sequence's table entry resolved to byte offsets.
+struct Slot {
+  int64_t at;        // byte offset of head 0 in K and V, -1: the row is skipped
+  int64_t scale;     // the same in the scales
+  int pos;
+  int row;
+};
+
+// One warp finds row r's sequence (the count of sequences that end at or
+// before it: lanes test 32 starts at a time, so a batch of 64 costs two loads)
+// and its place. The last lane-0 write is the block's; callers synchronise.
+__device__ __forceinline__ void find_slot(const CacheView& c, const BatchView& b, int r, Slot* out) {
+  const int lane = threadIdx.x & 31;
+  int seq = 0;
+  for (int i0 = 0; i0 < b.n; i0 += 32) {
+    const int i = i0 + lane;
+    const bool before = i < b.n && b.start[i + 1] <= r;
+    seq += __popc(__ballot_sync(0xffffffffu, before));
+  }
+  if (lane) return;
+  Slot s;
+  s.at = s.scale = -1;
+  s.row = r;
+  s.pos = 0;
+  if (r < b.rows && seq < b.n) {
+    const Seq q = seq_of(b, seq, c.status);
+    if (r >= q.row0 && r < q.row0 + q.n) {
+      s.pos = q.first + (r - q.row0);
+      const int page = page_of(b.table + (int64_t)seq * b.table_stride, b.width, c.pages, c.page_shift, s.pos);
+      if (page >= 0) {
+        s.at = slot_bytes(c, page, 0, s.pos);
+        s.scale = slot_scale(c, page, 0, s.pos);
+      } else {
+        set_status(c.status, CP_ERR_DEVICE_BOUNDS);
+        s.pos = max(s.pos, 0);
+      }
+    } else {
+      s.row = -1;
+    }
+  } else {
+    s.row = -1;
+  }
+  *out = s;
+}
+
+// ------------------------------------------------------------------ append
+struct AppendParams {
+  CacheView c;
+  BatchView b;
+  const uint16_t* qkv;
+  uint16_t* q_out;
+  const uint16_t* q_norm;
+  const uint16_t* k_norm;
+  int64_t qkv_row, q_row;
+  int q_heads;
+  int rope;
+  float eps;
+  int rows_per_block;
+  uint64_t turn[64];   // base^(-2j/D) / (2 pi) as a 64-bit fraction of a turn
+};
+
+// A row is heads of D elements, D/8 lanes a head with 16 bytes each: the
+// norm's sum and the absolute maximum are shuffles over those lanes, and RoPE's
+// partner (j, j + D/2) is the lane D/16 away. The rotary angle is kept in
+// turns as a 64-bit fraction, position * turn[j] modulo 2^64, which wraps
+// exactly: far positions lose nothing, and no 64-bit float is needed. Each
+// row's D/2 sines and cosines are made once and shared by its heads.
+// Bound by HBM: one read of qkv, one write of q and of the pages.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 8;
+  __shared__ Slot slots[kMaxRowsPerBlock];
+  __shared__ float2 cs[kMaxRowsPerBlock][D / 2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nrow = p.rows_per_block;
+  if (warp < nrow) find_slot(p.c, p.b, blockIdx.x * nrow + warp, &slots[warp]);
+  __syncthreads();
+  if (p.rope) {
+    for (int i = threadIdx.x; i < nrow * (D / 2); i += kAppendThreads) {
+      const int t = i / (D / 2), j = i % (D / 2);
+      const int64_t frac = (int64_t)((uint64_t)slots[t].pos * p.turn[j]);   // turns in [-1/2, 1/2) * 2^64
+      float sn, co;
+      sincospif((float)frac * 0x1p-63f, &sn, &co);
+      cs[t][j] = make_float2(co, sn);
+    }
+    __syncthreads();
+  }
+  const int heads = p.q_heads + 2 * p.c.heads;
+  const int units = nrow * heads;
+  const int l = lane % kLanes;
+  constexpr int kPerWarp = 32 / kLanes;
+  for (int u0 = warp * kPerWarp; u0 < units; u0 += (kAppendThreads / 32) * kPerWarp) {
+    const int u = u0 + lane / kLanes;
+    const int t = min(u, units - 1) / heads, h = min(u, units - 1) % heads;
+    const Slot s = slots[t];
+    const bool on = u < units && s.row >= 0;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    if (on) raw = *reinterpret_cast<const uint4*>(p.qkv + (int64_t)s.row * p.qkv_row + (int64_t)h * D + l * 8);
+    float x[8] = {bf_lo(raw.x), bf_hi(raw.x), bf_lo(raw.y), bf_hi(raw.y),
+                  bf_lo(raw.z), bf_hi(raw.z), bf_lo(raw.w), bf_hi(raw.w)};
+    const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.c.heads;
+    const uint16_t* gain = is_q ? p.q_norm : p.k_norm;
+    // the shuffles are the whole warp's: a head of v goes through them unchanged
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!is_v && gain) {
+      const float r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
+      const uint4 g = *reinterpret_cast<const uint4*>(gain + l * 8);
+      x[0] = x[0] * r * bf_lo(g.x); x[1] = x[1] * r * bf_hi(g.x);
+      x[2] = x[2] * r * bf_lo(g.y); x[3] = x[3] * r * bf_hi(g.y);
+      x[4] = x[4] * r * bf_lo(g.z); x[5] = x[5] * r * bf_hi(g.z);
+      x[6] = x[6] * r * bf_lo(g.w); x[7] = x[7] * r * bf_hi(g.w);
+    }
+    if (p.rope) {
+      const bool low = l < kLanes / 2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, x[i], kLanes / 2);
+        const float2 a = cs[t][(l % (kLanes / 2)) * 8 + i];
+        if (!is_v) x[i] = low ? x[i] * a.x - other * a.y : x[i] * a.x + other * a.y;
+      }
+    }
+    if (!E4M3 || is_q) {
+      const uint4 y = make_uint4(bf_pack(x[0], x[1]), bf_pack(x[2], x[3]), bf_pack(x[4], x[5]), bf_pack(x[6], x[7]));
+      if (on && is_q)
+        *reinterpret_cast<uint4*>(p.q_out + (int64_t)s.row * p.q_row + (int64_t)h * D + l * 8) = y;
+      if (!E4M3 && on && !is_q && s.at >= 0) {
+        const int kv = is_v ? h - p.q_heads - p.c.heads : h - p.q_heads;
+        *reinterpret_cast<uint4*>((is_v ? p.c.v : p.c.k) + s.at + kv * p.c.head_b + l * 16) = y;
+      }
+    }
+    if (E4M3) {
+      // the least e with max <= 448 * 2^e = 1.75 * 2^(e+8), from the maximum's bits: exact
+      int top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int a = __float_as_int(x[i]) & 0x7fffffff;
+        if (a >= 0x7f800000) x[i] = __int_as_float(0x7fc00000);   // infinities are kept as NaN
+        else top = max(top, a);
+      }
+#pragma unroll
+      for (int o = kLanes / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      int e = (top >> 23) - 127 - 8 + ((top & 0x7fffff) > 0x600000 ? 1 : 0);
+      e = max(e, kMinExp);
+      const float inv = pow2i(-e);
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint16_t two;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(x[2 * i + 1] * inv), "f"(x[2 * i] * inv));
+        w[i] = two;
+      }
+      if (on && !is_q && s.at >= 0) {
+        const int kv = is_v ? h - p.q_heads - p.c.heads : h - p.q_heads;
+        *reinterpret_cast<uint2*>((is_v ? p.c.v : p.c.k) + s.at + kv * p.c.head_b + l * 8) =
+            make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        if (l == 0) (is_v ? p.c.vs : p.c.ks)[s.scale + kv * p.c.sc_head] = (uint8_t)(e + 127);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ read back
+struct ReadParams {
+  CacheView c;
+  BatchView b;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  int rows_per_block;
+};
+
+// 16 cached bytes a lane: 8 bf16 copied, or 16 e4m3 widened to fp32, scaled by
+// the power of two and packed (exact: 4 significant bits). Bound by HBM.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int kElems = E4M3 ? 16 : 8;
+  constexpr int kLanes = D / kElems;
+  __shared__ Slot slots[kMaxRowsPerBlock];
+  const int warp = threadIdx.x >> 5;
+  const int nrow = p.rows_per_block;
+  if (warp < nrow) find_slot(p.c, p.b, blockIdx.x * nrow + warp, &slots[warp]);
+  __syncthreads();
+  const int units = nrow * p.c.heads * 2 * kLanes;
+#pragma unroll 4
+  for (int u = threadIdx.x; u < units; u += kReadThreads) {
+    const int l = u % kLanes, rest = u / kLanes;
+    const int t = rest % nrow, hv = rest / nrow;       // rows of one head lie side by side in a page
+    const int h = hv >> 1, is_v = hv & 1;
+    const Slot s = slots[t];
+    uint16_t* out = is_v ? p.v_out : p.k_out;
+    if (s.at < 0 || !out) continue;
+    const uint4 raw = *reinterpret_cast<const uint4*>((is_v ? p.c.v : p.c.k) + s.at + h * p.c.head_b + l * 16);
+    uint4* dst = reinterpret_cast<uint4*>(out + ((int64_t)s.row * p.c.heads + h) * D + l * kElems);
+    if (!E4M3) {
+      dst[0] = raw;
+    } else {
+      const float sc = pow2i((int)(is_v ? p.c.vs : p.c.ks)[s.scale + h * p.c.sc_head] - 127);
+      float f[16];
+      e4m3x4_f32(raw.x, f); e4m3x4_f32(raw.y, f + 4); e4m3x4_f32(raw.z, f + 8); e4m3x4_f32(raw.w, f + 12);
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = bf_pack(f[2 * i] * sc, f[2 * i + 1] * sc);
+      dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ checks
+struct DeviceGuard {
+  int prev = -1;
+  explicit DeviceGuard(int dev) {
+    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
+    cudaSetDevice(dev);
+  }
+  ~DeviceGuard() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+int check_desc(const cp_cache_desc* in, cp_cache_desc* d) {
+  if (!in || !in->k || !in->v) return CP_ERR_INVALID_ARG;
+  *d = *in;
+  if (d->dtype != CP_CACHE_BF16 && d->dtype != CP_CACHE_E4M3) return CP_ERR_INVALID_ARG;
+  if (d->kv_heads < 1 || d->head_dim < 1 || d->page_size < 1 || d->pages < 1) return CP_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return CP_ERR_UNSUPPORTED;
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return CP_ERR_UNSUPPORTED;
+  if (d->kv_heads > 128) return CP_ERR_UNSUPPORTED;
+  const bool e4m3 = d->dtype == CP_CACHE_E4M3;
+  if (e4m3 ? (!d->k_scale || !d->v_scale) : (d->k_scale || d->v_scale)) return CP_ERR_INVALID_ARG;
+  if (!d->token_stride) d->token_stride = d->head_dim;
+  if (!d->head_stride) d->head_stride = (int64_t)d->page_size * d->head_dim;
+  if (!d->page_stride) d->page_stride = (int64_t)d->kv_heads * d->page_size * d->head_dim;
+  if (!d->scale_token_stride) d->scale_token_stride = 1;
+  if (!d->scale_head_stride) d->scale_head_stride = d->page_size;
+  if (!d->scale_page_stride) d->scale_page_stride = (int64_t)d->kv_heads * d->page_size;
+  if (d->token_stride < 0 || d->head_stride < 0 || d->page_stride < 0 || d->scale_token_stride < 0 ||
+      d->scale_head_stride < 0 || d->scale_page_stride < 0)
+    return CP_ERR_INVALID_ARG;
+  const int per16 = e4m3 ? 16 : 8;
+  if (d->token_stride % per16 || d->head_stride % per16 || d->page_stride % per16 || !aligned16(d->k) || !aligned16(d->v))
+    return CP_ERR_UNSUPPORTED;
+  return CP_OK;
+}
+
+CacheView view_of(const cp_cache_desc& d, int32_t* status) {
+  const int64_t es = d.dtype == CP_CACHE_E4M3 ? 1 : 2;
+  CacheView v{};
+  v.k = static_cast<uint8_t*>(d.k);
+  v.v = static_cast<uint8_t*>(d.v);
+  v.ks = d.k_scale;
+  v.vs = d.v_scale;
+  v.page_b = d.page_stride * es;
+  v.head_b = d.head_stride * es;
+  v.tok_b = d.token_stride * es;
+  v.sc_page = d.scale_page_stride;
+  v.sc_head = d.scale_head_stride;
+  v.sc_tok = d.scale_token_stride;
+  v.pages = d.pages;
+  v.heads = d.kv_heads;
+  v.page_shift = d.page_size == 16 ? 4 : d.page_size == 32 ? 5 : d.page_size == 64 ? 6 : 7;
+  v.status = status;
+  return v;
+}
+
+int check_batch(const cp_cache_desc& d, const cp_batch* in, BatchView* b) {
+  if (!in || !in->start || !in->length || !in->page_table) return CP_ERR_INVALID_ARG;
+  if (in->sequences < 1 || in->sequences > 65535 || in->rows < 1 || in->table_width < 1) return CP_ERR_INVALID_ARG;
+  if (in->max_new < 0 || in->max_length < 0 || in->table_stride < 0) return CP_ERR_INVALID_ARG;
+  const int64_t held = (int64_t)in->table_width * d.page_size;
+  if (in->max_length > held) return CP_ERR_INVALID_ARG;
+  if (in->table_stride && in->sequences > 1 && in->table_stride < in->table_width) return CP_ERR_INVALID_ARG;
+  b->start = in->start;
+  b->length = in->length;
+  b->table = in->page_table;
+  b->table_stride = in->table_stride ? in->table_stride : in->table_width;
+  b->n = in->sequences;
+  b->rows = in->rows;
+  b->width = in->table_width;
+  b->max_new = in->max_new ? std::min(in->max_new, in->rows) : in->rows;
+  // positions are 32-bit, with room for a tile past the last
+  b->max_len = in->max_length ? in->max_length : (int)std::min<int64_t>(held, INT32_MAX - 1024);
+  if (b->max_len > INT32_MAX - 1024) return CP_ERR_UNSUPPORTED;
+  return CP_OK;
+}
+
+int check_append(const cp_cache_desc& d, const BatchView& b, const cp_append* a, AppendParams* p) {
+  if (!a || !a->qkv || a->q_heads < 0) return CP_ERR_INVALID_ARG;
+  if (a->q_heads > 1024) return CP_ERR_UNSUPPORTED;
+  if ((a->q_heads > 0) != (a->q_out != nullptr)) return CP_ERR_INVALID_ARG;
+  if (!(a->rms_eps >= 0.f) || !std::isfinite(a->rms_eps) || !(a->rope_base >= 0.f) || !std::isfinite(a->rope_base))
+    return CP_ERR_INVALID_ARG;
+  const int64_t wide = (int64_t)(a->q_heads + 2 * d.kv_heads) * d.head_dim, qw = (int64_t)a->q_heads * d.head_dim;
+  p->qkv_row = a->qkv_stride ? a->qkv_stride : wide;
+  p->q_row = a->q_stride ? a->q_stride : qw;
+  if (p->qkv_row < wide || p->q_row < qw) return CP_ERR_INVALID_ARG;
+  if (p->qkv_row % 8 || p->q_row % 8 || !aligned16(a->qkv) || !aligned16(a->q_out) || !aligned16(a->q_norm) ||
+      !aligned16(a->k_norm))
+    return CP_ERR_UNSUPPORTED;
+  p->b = b;
+  p->qkv = static_cast<const uint16_t*>(a->qkv);
+  p->q_out = static_cast<uint16_t*>(a->q_out);
+  p->q_norm = static_cast<const uint16_t*>(a->q_norm);
+  p->k_norm = static_cast<const uint16_t*>(a->k_norm);
+  p->q_heads = a->q_heads;
+  p->eps = a->rms_eps;
+  p->rope = a->rope_base > 0.f;
+  if (p->rope)
+    for (int j = 0; j < d.head_dim / 2; ++j) {
+      // turns per position modulo one; 53 bits of them: position 2^31 is still good to 2^-25 turns
+      const double turns = std::pow((double)a->rope_base, -2.0 * j / d.head_dim) / 6.283185307179586;
+      p->turn[j] = (uint64_t)std::ldexp(turns - std::floor(turns), 64);
+    }
+  return CP_OK;
+}
+
+int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a, AttendParams* p) {
+  if (!a || !a->q || !a->out || a->q_heads < 1 || a->window < 0) return CP_ERR_INVALID_ARG;
+  if (a->q_heads % d.kv_heads) return CP_ERR_INVALID_ARG;
+  if (a->q_heads / d.kv_heads > 64) return CP_ERR_UNSUPPORTED;
+  if (!(a->scale >= 0.f) || !std::isfinite(a->scale)) return CP_ERR_INVALID_ARG;
+  p->q_head = a->q_head_stride ? a->q_head_stride : d.head_dim;
+  p->o_head = a->out_head_stride ? a->out_head_stride : d.head_dim;
+  p->q_row = a->q_stride ? a->q_stride : (int64_t)a->q_heads * d.head_dim;
+  p->o_row = a->out_stride ? a->out_stride : (int64_t)a->q_heads * d.head_dim;
+  if (p->q_head < 0 || p->o_head < 0 || p->q_row < 0 || p->o_row < 0) return CP_ERR_INVALID_ARG;
+  if (p->q_head % 8 || p->o_head % 8 || p->q_row % 8 || p->o_row % 8 || !aligned16(a->q) || !aligned16(a->out))
+    return CP_ERR_UNSUPPORTED;
+  p->b = b;
+  p->q = static_cast<const uint16_t*>(a->q);
+  p->out = static_cast<uint16_t*>(a->out);
+  p->q_heads = a->q_heads;
+  p->group = a->q_heads / d.kv_heads;
+  const double scale = a->scale > 0.f ? (double)a->scale : 1.0 / std::sqrt((double)d.head_dim);
+  p->scale_log2 = (float)(scale * 1.4426950408889634);
+  p->causal = a->causal != 0;
+  p->window = a->window;
+  return CP_OK;
+}
+
+int cuda_err(cudaError_t e) { return e == cudaSuccess ? CP_OK : CP_ERR_CUDA; }
+
+// Rows per block: one until every SM has two blocks, then up to eight, which
+// share the look-ups.
+int rows_per_block(int rows) { return std::max(1, std::min(kMaxRowsPerBlock, rows / 304)); }
+
+}  // namespace
+
+extern "C" {
+
+int cp_cache_check(const cp_cache_desc* desc, const cp_batch* batch, const cp_append* append, const cp_attend* attend,
+                   size_t* workspace_bytes) {
+  if (workspace_bytes) *workspace_bytes = 0;
+  cp_cache_desc d;
+  int st = check_desc(desc, &d);
+  if (st) return st;
+  if (!batch) return append || attend ? CP_ERR_INVALID_ARG : CP_OK;
+  BatchView b{};
+  if ((st = check_batch(d, batch, &b))) return st;
+  AppendParams ap{};
+  if (append && (st = check_append(d, b, append, &ap))) return st;
+  AttendParams at{};
+  if (attend && (st = check_attend(d, b, attend, &at))) return st;
+  return CP_OK;
+}
+
+int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out) {
+  if (!out) return CP_ERR_INVALID_ARG;
+  *out = nullptr;
+  cp_cache_desc d;
+  const int st = check_desc(desc, &d);
+  if (st) return st;
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) return CP_ERR_UNSUPPORTED;
+  DeviceGuard guard(device);
+  int major = 0, minor = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess)
+    return CP_ERR_CUDA;
+  if (major != 10 || minor != 3) return CP_ERR_UNSUPPORTED;
+  for (const void* ptr : {(const void*)d.k, (const void*)d.v, (const void*)d.k_scale, (const void*)d.v_scale}) {
+    cudaPointerAttributes a{};
+    if (!ptr) continue;
+    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess || a.type != cudaMemoryTypeDevice || a.device != device) {
+      cudaGetLastError();
+      return CP_ERR_INVALID_ARG;
+    }
+  }
+  cp_cache* c = new (std::nothrow) cp_cache();
+  if (!c) return CP_ERR_NOMEM;
+  c->device = device;
+  c->d = d;
+  void* status = nullptr;
+  if (cudaMalloc(&status, 16) != cudaSuccess) {
+    delete c;
+    return CP_ERR_NOMEM;
+  }
+  c->view = view_of(d, static_cast<int32_t*>(status));
+  if (cudaMemset(status, 0, 16) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    cp_cache_destroy(c);
+    return CP_ERR_CUDA;
+  }
+  *out = c;
+  return CP_OK;
+}
+
+void cp_cache_destroy(cp_cache* c) {
+  if (!c) return;
+  {
+    DeviceGuard g(c->device);
+    cudaDeviceSynchronize();
+    cudaFree(c->view.status);
+  }
+  delete c;
+}
+
+int cp_cache_status(cp_cache* c) {
+  if (!c) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(c->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return CP_ERR_CUDA;
+  int32_t v = 0;
+  if (cudaMemcpy(&v, c->view.status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return CP_ERR_CUDA;
+  return v;
+}
+
+int cp_cache_clear_status(cp_cache* c) {
+  if (!c) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(c->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return CP_ERR_CUDA;
+  if (cudaMemset(c->view.status, 0, 16) != cudaSuccess) return CP_ERR_CUDA;
+  return cuda_err(cudaDeviceSynchronize());
+}
+
+int cp_cache_append(cp_cache* c, const cp_batch* batch, const cp_append* args, cp_stream_t stream) {
+  if (!c) return CP_ERR_INVALID_ARG;
+  BatchView b{};
+  AppendParams p{};
+  int st = check_batch(c->d, batch, &b);
+  if (!st) st = check_append(c->d, b, args, &p);
+  if (st) return st;
+  DeviceGuard g(c->device);
+  p.c = c->view;
+  p.rows_per_block = rows_per_block(b.rows);
+  const int grid = (b.rows + p.rows_per_block - 1) / p.rows_per_block;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool e4m3 = c->d.dtype == CP_CACHE_E4M3;
+  if (c->d.head_dim == 128) {
+    if (e4m3) append_kernel<128, true><<<grid, kAppendThreads, 0, s>>>(p);
+    else append_kernel<128, false><<<grid, kAppendThreads, 0, s>>>(p);
+  } else {
+    if (e4m3) append_kernel<64, true><<<grid, kAppendThreads, 0, s>>>(p);
+    else append_kernel<64, false><<<grid, kAppendThreads, 0, s>>>(p);
+  }
+  return cuda_err(cudaGetLastError());
+}
+
+int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, cp_stream_t stream) {
+  if (!c || (!k_out && !v_out)) return CP_ERR_INVALID_ARG;
+  BatchView b{};
+  const int st = check_batch(c->d, batch, &b);
+  if (st) return st;
+  if (!aligned16(k_out) || !aligned16(v_out)) return CP_ERR_UNSUPPORTED;
+  DeviceGuard g(c->device);
+  ReadParams p{};
+  p.c = c->view;
+  p.b = b;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.rows_per_block = rows_per_block(b.rows);
+  const int grid = (b.rows + p.rows_per_block - 1) / p.rows_per_block;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const bool e4m3 = c->d.dtype == CP_CACHE_E4M3;
+  if (c->d.head_dim == 128) {
+    if (e4m3) read_kernel<128, true><<<grid, kReadThreads, 0, s>>>(p);
+    else read_kernel<128, false><<<grid, kReadThreads, 0, s>>>(p);
+  } else {
+    if (e4m3) read_kernel<64, true><<<grid, kReadThreads, 0, s>>>(p);
+    else read_kernel<64, false><<<grid, kReadThreads, 0, s>>>(p);
+  }
+  return cuda_err(cudaGetLastError());
+}
+
+int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, void* workspace, size_t workspace_bytes,
+                    cp_stream_t stream) {
+  if (!c) return CP_ERR_INVALID_ARG;
+  BatchView b{};
+  AttendParams p{};
+  int st = check_batch(c->d, batch, &b);
+  if (!st) st = check_attend(c->d, b, args, &p);
+  if (st) return st;
+  (void)workspace;
+  (void)workspace_bytes;
+  DeviceGuard g(c->device);
+  p.c = c->view;
+  return cuda_err(launch_attend(p, c->d.head_dim, c->d.dtype == CP_CACHE_E4M3, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int64_t cp_test_slot(const cp_cache_desc* desc, const int32_t* table, int table_width, int pos, int head) {
+  cp_cache_desc d;
+  if (check_desc(desc, &d) || !table || head < 0 || head >= d.kv_heads) return -1;
+  const CacheView v = view_of(d, nullptr);
+  const int page = page_of(table, table_width, v.pages, v.page_shift, pos);
+  return page < 0 ? -1 : slot_bytes(v, page, head, pos) / (d.dtype == CP_CACHE_E4M3 ? 1 : 2);
+}
+
+}  // extern "C"

@@ -1,0 +1,129 @@
+// cp_cache.cuh -- what the paged cache's kernels share: the cache's and the
+// batch's view on the device, the look-ups with their bounds checks, and the
+// element formats.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cp.h"
+
+namespace cp {
+namespace cache {
+
+constexpr int kMinExp = -110;    // smallest exponent of a stored scale (byte 17)
+
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* ks;                          // scales (e4m3) or null
+  uint8_t* vs;
+  int64_t page_b, head_b, tok_b;        // bytes between pages, heads, positions
+  int64_t sc_page, sc_head, sc_tok;     // the same of the scales
+  int pages, heads, page_shift;         // page size 1 << page_shift
+  int32_t* status;                      // sticky status word of the cache
+};
+
+struct BatchView {
+  const int32_t* start;
+  const int32_t* length;
+  const int32_t* table;
+  int64_t table_stride;
+  int n, rows, width, max_new, max_len;
+};
+
+// One sequence of the batch as the kernels use it: rows row0 .. row0 + n - 1,
+// len cached positions, row row0 + i at position first + i.
+struct Seq {
+  int row0, n, len, first;
+};
+
+__device__ __forceinline__ void set_status(int32_t* status, int code) { atomicCAS(status, 0, code); }
+
+// Starts, lengths and row counts are device data: whatever they hold, the
+// returned rows lie in [0, rows] and the positions in [0, max_len].
+__device__ __forceinline__ Seq seq_of(const BatchView& b, int i, int32_t* status) {
+  const int s0 = b.start[i], s1 = b.start[i + 1], l = b.length[i];
+  Seq s;
+  s.row0 = min(max(s0, 0), b.rows);
+  const int end = min(max(s1, s.row0), b.rows);
+  s.n = min(end - s.row0, b.max_new);
+  s.len = min(max(l, 0), b.max_len);
+  if (s.row0 != s0 || end != s1 || s.n != end - s.row0 || s.len != l) set_status(status, CP_ERR_DEVICE_BOUNDS);
+  s.first = s.len - s.n;
+  return s;
+}
+
+// Page of position `pos` in a table row of `width` entries, or -1: a position
+// outside the table or a page outside the pool (run on the host by
+// cp_test_slot too).
+__host__ __device__ __forceinline__ int page_of(const int32_t* table, int width, int pages, int page_shift, int pos) {
+  if (pos < 0 || (pos >> page_shift) >= width) return -1;
+  const int p = table[pos >> page_shift];
+  return (uint32_t)p < (uint32_t)pages ? p : -1;
+}
+// Byte offset of a position in K or V: 64-bit, a pool may pass 4 GB.
+__host__ __device__ __forceinline__ int64_t slot_bytes(const CacheView& c, int page, int head, int pos) {
+  return (int64_t)page * c.page_b + (int64_t)head * c.head_b + (int64_t)(pos & ((1 << c.page_shift) - 1)) * c.tok_b;
+}
+__host__ __device__ __forceinline__ int64_t slot_scale(const CacheView& c, int page, int head, int pos) {
+  return (int64_t)page * c.sc_page + (int64_t)head * c.sc_head + (int64_t)(pos & ((1 << c.page_shift) - 1)) * c.sc_tok;
+}
+
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ uint32_t bf_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t hf_pack(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 bytes of the low 16 bits as fp16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ void e4m3x4_f32(uint32_t four, float* f) {
+  const uint32_t a = e4m3x2_f16x2(four & 0xffffu), b = e4m3x2_f16x2(four >> 16);
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  f[0] = x.x; f[1] = x.y; f[2] = y.x; f[3] = y.y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// ------------------------------------------------------------------ attention
+struct AttendParams {
+  CacheView c;
+  BatchView b;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_row, q_head, o_row, o_head;   // element strides
+  int group;                              // query heads per kv head
+  int q_heads;
+  float scale_log2;                       // scale * log2(e)
+  int causal, window;
+};
+
+// Positions [lo, hi) that the row at position `pos` sees.
+__device__ __forceinline__ void visible(const AttendParams& p, int pos, int len, int* lo, int* hi) {
+  *hi = p.causal ? min(pos + 1, len) : len;
+  *lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+}
+
+cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s);
+
+}  // namespace cache
+}  // namespace cp
