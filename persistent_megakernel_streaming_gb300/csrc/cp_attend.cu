@@ -1,21 +1,513 @@
-// cp_attend.cu -- attention of a batch's new rows over the paged cache.
-#include "cp_cache.cuh"
+// cp_attend.cu -- attention of a batch's new rows over the paged cache: the
+// plan of a call, the step kernel (up to 16 rows a kv head, bound by reading
+// the cache once) and the kernel that joins an item's parts.
+#include <algorithm>
+
+#include "cp_attend.cuh"
 
 namespace cp {
 namespace cache {
+
+// ------------------------------------------------------------------ plan
+constexpr int kStepBlocks = 304;      // step blocks resident at once: two on each of 152 SMs
+constexpr int kMaxStepChunk = 4096;   // positions a step block holds page numbers for
+
+static int step_tile(int head_dim, bool e4m3) { return 4 * (e4m3 ? 32 : 16) * (128 / head_dim); }
+
+AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, int window) {
+  AttendPlan a{};
+  const int group = q_heads / kv_heads;
+  a.use_step = group <= kStepRows;
+  a.use_chunk = (int64_t)b.max_new * group > kStepRows;
+  // the most positions an item spans: all, or a window and the rows behind it
+  const int64_t rows = std::min(b.max_new, kStepRows / std::min(group, kStepRows));
+  int64_t span = b.max_len;
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + rows + 15);
+  const int tile = step_tile(head_dim, e4m3);
+  const int64_t items = (int64_t)b.n * kv_heads;
+  const int64_t want = std::max<int64_t>(1, kStepBlocks * 8 / items);
+  int64_t chunk = (span + want - 1) / want;
+  chunk = std::min<int64_t>(std::max<int64_t>((chunk + tile - 1) / tile * tile, tile), kMaxStepChunk);
+  a.step_chunk = (int)chunk;
+  a.step_parts = a.use_step ? (int)std::max<int64_t>(1, (span + chunk - 1) / chunk) : 0;
+  return a;
+}
+
+size_t attend_workspace(const AttendPlan& a, const BatchView& b, int q_heads, int head_dim) {
+  const int parts = std::max(a.step_parts, a.chunk_parts);
+  return parts > 1 ? (size_t)parts * b.rows * q_heads * (head_dim + 1) * sizeof(float) : 0;
+}
+
 namespace {
 
-constexpr int kWarps = 8;
+// ------------------------------------------------------------------ step kernel
+constexpr int kStepWarps = 4;
+constexpr int kStages = 3;
+constexpr int kStageBytes = 8192;     // a warp's tile: K and V, 4 KB each
+constexpr int kGroups = kMaxStepChunk / 16;
 
-// One warp a (row, query head): lanes share the head's D elements and walk the
-// visible positions with a running maximum and sum. Right for every case, and
-// bound by the shuffles of each score's sum and by reading the cache once per
-// query head.
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t* r) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+template <bool HALF>
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  if (HALF)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kStepSmem = kStepWarps * kStages * kStageBytes;
+static_assert(kStepSmem >= kStepWarps * kStepRows * (128 + 4) * 4, "the ring holds the warps' averages");
+
+struct StepShared {
+  float scale_k[kStepWarps][64];      // e4m3: per position of the warp's tile, its key's scale times the softmax's
+  float scale_v[kStepWarps][64];      // and its value's scale relative to the warp's reference
+  int pages[kGroups];                 // page of each 16 positions of the part, -1: none
+  float m[kStepWarps][kStepRows], l[kStepWarps][kStepRows];
+  uint16_t rows_pad[8];
+};
+
+// One block a (part, kv head, sequence); its four warps take the part's tiles
+// in turn, each with a running maximum, sum and product of its own and its own
+// ring of asynchronous copies, so that nothing in the loop waits for another
+// warp; they are joined once at the end. The 16 rows of the matrix
+// instruction are the sequence's rows times the kv head's query heads.
+//
+// K and V go to shared memory as they lie (16-byte units exchanged within a
+// row so that ldmatrix meets no bank twice) and from there into mma fragments:
+// keys as they are, values transposed on the way. e4m3 is widened to fp16 in
+// registers (exact): q is fp16 times a power of two of its row, the key's
+// scale multiplies the score, the value's scale the weight, relative to the
+// largest seen (so that weight * scale stays in fp16's range; weights start
+// at 2^8 to use it). A 4-byte fragment of e4m3 is four neighbouring elements
+// where the instruction wants two and two: the sum over the head does not
+// mind the order, so q is loaded in it, and the output columns come out
+// four neighbours a thread.
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kWarps * 32) attend_rows_kernel(const __grid_constant__ AttendParams p) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const __grid_constant__ AttendParams p) {
+  constexpr int TK = (E4M3 ? 32 : 16) * (128 / D);    // positions a tile
+  constexpr int ES = E4M3 ? 1 : 2;
+  constexpr int UPR = D * ES / 16;                    // 16-byte units a row: 16, 8 or 4
+  constexpr int NT = TK / 8;                          // score tiles of 8 positions
+  constexpr int KS = D / 16;                          // steps over the head
+  constexpr int RPL = 32 / UPR;                       // rows that one copy of the warp covers
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ StepShared sh;
+
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int seq = blockIdx.z, kv = blockIdx.y, part = blockIdx.x;
+  const Seq s = seq_of(p.b, seq, p.c.status);
+  const int nrows = s.n * p.group;
+  if (s.n == 0 || nrows > kStepRows) return;
+  const Range range = item_range(p, s.first, s.first + s.n - 1, s.len);
+  const int parts = parts_of(range, p.a.step_chunk);
+  if (part >= max(parts, 1)) return;
+  const int t_begin = range.base + part * p.a.step_chunk;
+  const int t_end = min(t_begin + p.a.step_chunk, range.hi);
+  // every row sees [lo_all, hi_all) of the item; outside it a tile is masked by row
+  int lo_all, hi_all, unused;
+  visible(p, s.first + s.n - 1, s.len, &lo_all, &unused);
+  visible(p, s.first, s.len, &unused, &hi_all);
+
+  const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
+  for (int i = threadIdx.x; t_begin + i * 16 < t_end; i += kStepWarps * 32) {
+    const int pg = page_of(table, p.b.width, p.c.pages, p.c.page_shift, t_begin + i * 16);
+    if (pg < 0) set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
+    sh.pages[i] = pg;
+  }
+  __syncthreads();
+
+  const uint32_t my_ring = smem_u32(ring) + warp * (kStages * kStageBytes);
+  const int ntiles = t_end > t_begin ? (t_end - t_begin + TK - 1) / TK : 0;
+  const int mine = ntiles > warp ? (ntiles - warp + kStepWarps - 1) / kStepWarps : 0;
+  const uint8_t* kb = p.c.k + (int64_t)kv * p.c.head_b;
+  const uint8_t* vb = p.c.v + (int64_t)kv * p.c.head_b;
+  const int mask = (1 << p.c.page_shift) - 1;
+
+  auto swz = [](int row, int unit) { return UPR == 4 ? unit ^ ((row >> 1) & 3) : unit ^ (row & 7); };
+  uint32_t sc_next[2] = {0, 0}, sc_cur[2] = {0, 0};   // scale bytes (key | value << 8) of the lane's positions
+  // Tile i of this warp into its ring slot: rows outside [lo, t_end) or on no page are zeros.
+  auto issue = [&](int i) {
+    if (i < mine) {
+      const int t0 = t_begin + (i * kStepWarps + warp) * TK;
+      const uint32_t dst = my_ring + (i % kStages) * kStageBytes;
+      const int u = lane % UPR, r0 = lane / UPR;
+#pragma unroll
+      for (int gr = 0; gr < TK / 16; ++gr) {
+        const int tg = t0 + gr * 16;
+        const int pg = tg < t_end ? sh.pages[(tg - t_begin) >> 4] : -1;
+        const int64_t off = (int64_t)max(pg, 0) * p.c.page_b + (int64_t)((tg & mask) + r0) * p.c.tok_b + u * 16;
+#pragma unroll
+        for (int j = 0; j < 16 / RPL; ++j) {
+          const int row = gr * 16 + j * RPL + r0, t = t0 + row;
+          const bool on = pg >= 0 && t >= range.lo && t < t_end;
+          const int64_t o = on ? off + (int64_t)(j * RPL) * p.c.tok_b : 0;
+          const uint32_t d = dst + row * (UPR * 16) + swz(row, u) * 16;
+          cp16(d, kb + o, on);
+          cp16(d + kStageBytes / 2, vb + o, on);
+        }
+      }
+      if (E4M3) {
+#pragma unroll
+        for (int x = 0; x < (TK + 31) / 32; ++x) {
+          const int t = t0 + x * 32 + lane;
+          uint32_t b = 0;
+          if (t >= range.lo && t < t_end) {
+            const int pg = sh.pages[(t - t_begin) >> 4];
+            if (pg >= 0) {
+              const int64_t so = slot_scale(p.c, pg, kv, t);
+              b = p.c.ks[so] | (uint32_t)p.c.vs[so] << 8;
+            }
+          }
+          sc_next[x] = b;
+        }
+      }
+    }
+    cp_commit();
+  };
+
+  // q fragments, and for e4m3 the power of two taken out of each row
+  uint32_t qf[KS][4];
+  float qs[2] = {p.scale_log2, p.scale_log2};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = g + half * 8;
+    const bool on = r < nrows;
+    const uint16_t* qp = p.q + (int64_t)(s.row0 + (on ? r / p.group : 0)) * p.q_row +
+                         (int64_t)(kv * p.group + (on ? r % p.group : 0)) * p.q_head;
+    if (!E4M3) {
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[k][half] = on ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 2 * c) : 0u;
+        qf[k][half + 2] = on ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8 + 2 * c) : 0u;
+      }
+    } else {
+      uint2 raw[KS];
+      int top = 0;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        raw[k] = on ? *reinterpret_cast<const uint2*>(qp + k * 16 + 4 * c) : make_uint2(0u, 0u);
+        const uint32_t w[2] = {raw[k].x, raw[k].y};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          top = max(top, finite_exp(w[j] & 0xffffu));
+          top = max(top, finite_exp(w[j] >> 16));
+        }
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(max(top - 127, -100), 100);
+      const float inv = pow2i(-e);
+      qs[half] = p.scale_log2 * pow2i(e);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        qf[k][half] = hf_pack(bf_lo(raw[k].x) * inv, bf_hi(raw[k].x) * inv);
+        qf[k][half + 2] = hf_pack(bf_lo(raw[k].y) * inv, bf_hi(raw[k].y) * inv);
+      }
+    }
+  }
+  // the positions that this thread's two rows see
+  int lo[2], hi[2];
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = g + half * 8;
+    if (r < nrows) visible(p, s.first + r / p.group, s.len, &lo[half], &hi[half]);
+    else lo[half] = hi[half] = 0;
+  }
+
+  constexpr float kBias = E4M3 ? 8.f : 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float o[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  int ev_ref = -1000;
+  bool bad = false;
+
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) {
+    if (E4M3) sc_cur[0] = sc_next[0], sc_cur[1] = sc_next[1];
+    issue(i);
+  }
+  for (int i = 0; i < mine; ++i) {
+    const int t0 = t_begin + (i * kStepWarps + warp) * TK;
+    if (E4M3) {
+      // this tile's scales to shared memory, where the lanes find the ones of their columns
+      const uint32_t now[2] = {sc_cur[0], sc_cur[1]};
+      sc_cur[0] = sc_next[0];
+      sc_cur[1] = sc_next[1];
+      int top = -1000;
+#pragma unroll
+      for (int x = 0; x < (TK + 31) / 32; ++x) top = max(top, (int)(now[x] >> 8) - 127);
+      const int ref = max(ev_ref, __reduce_max_sync(0xffffffffu, top));
+      if (ref != ev_ref) {
+        const float f = pow2i(max(ev_ref - ref, -127));
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) o[n][0] *= f, o[n][1] *= f, o[n][2] *= f, o[n][3] *= f;
+        ev_ref = ref;
+      }
+#pragma unroll
+      for (int x = 0; x < (TK + 31) / 32; ++x) {
+        sh.scale_k[warp][x * 32 + lane] = pow2i((int)(now[x] & 255) - 127);
+        sh.scale_v[warp][x * 32 + lane] = pow2i(max((int)(now[x] >> 8) - 127 - ref, -127));
+      }
+    }
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    const uint32_t tile = my_ring + (i % kStages) * kStageBytes;
+    const uint32_t vtile = tile + kStageBytes / 2;
+    const bool edge = t0 < lo_all || t0 + TK > hi_all;
+    if (edge && nrows > p.group) {
+      // a value that some row must not see may not be multiplied, not even by zero, unless it is finite
+      const int u = lane % UPR, r0 = lane / UPR;
+      for (int row = r0; row < TK; row += RPL)
+        bad |= any_nonfinite<E4M3>(vtile + row * (UPR * 16) + u * 16);
+    }
+    // scores
+    float sc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) {
+      if (!E4M3) {
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t b[4];
+          const int row = n * 8 + (lane >> 4) * 8 + (lane & 7), unit = k * 2 + ((lane >> 3) & 1);
+          ldsm4(tile + row * (UPR * 16) + swz(row, unit) * 16, b);
+          mma16816<false>(sc[n], qf[k], b[0], b[1]);
+          mma16816<false>(sc[n + 1], qf[k], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; n += 4) {
+          uint32_t b[4];
+          const int row = n * 8 + lane;
+          ldsm4(tile + row * (UPR * 16) + swz(row, k) * 16, b);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma16816<true>(sc[n + j], qf[k], e4m3x2_f16x2(b[j] & 0xffffu), e4m3x2_f16x2(b[j] >> 16));
+        }
+      }
+    }
+    // scale, mask, running maximum
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float2 fk = make_float2(1.f, 1.f);
+      if (E4M3) fk = *reinterpret_cast<const float2*>(&sh.scale_k[warp][n * 8 + 2 * c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sc[n][j] = sc[n][j] * qs[j >> 1] * (j & 1 ? fk.y : fk.x);
+        const int t = t0 + n * 8 + 2 * c + (j & 1);
+        if (edge && (t < lo[j >> 1] || t >= hi[j >> 1])) sc[n][j] = -INFINITY;
+        mx[j >> 1] = fmaxf(mx[j >> 1], sc[n][j]);
+      }
+    }
+    float ref[2];
+    bool moved = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      moved |= mx[h] > m[h];
+      ref[h] = (mx[h] == -INFINITY ? 0.f : mx[h]) - kBias;
+    }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = mx[h] == m[h] ? 1.f : ex2(m[h] - mx[h]);
+        l[h] *= f;
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+        m[h] = mx[h];
+      }
+    }
+    // weights
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        w[j] = ex2(sc[n][j] - ref[j >> 1]);
+        l[j >> 1] += w[j];
+      }
+      if (E4M3) {
+        const float2 fv = *reinterpret_cast<const float2*>(&sh.scale_v[warp][n * 8 + 2 * c]);
+        pf[n][0] = hf_pack(w[0] * fv.x, w[1] * fv.y);
+        pf[n][1] = hf_pack(w[2] * fv.x, w[3] * fv.y);
+      } else {
+        pf[n][0] = bf_pack(w[0], w[1]);
+        pf[n][1] = bf_pack(w[2], w[3]);
+      }
+    }
+    // weights times values
+#pragma unroll
+    for (int k = 0; k < TK / 16; k += E4M3 ? 2 : 1) {
+      if (!E4M3) {
+        const uint32_t a[4] = {pf[2 * k][0], pf[2 * k][1], pf[2 * k + 1][0], pf[2 * k + 1][1]};
+#pragma unroll
+        for (int n = 0; n < D / 8; n += 2) {
+          uint32_t b[4];
+          const int row = k * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), unit = n + (lane >> 4);
+          ldsm4t(vtile + row * (UPR * 16) + swz(row, unit) * 16, b);
+          mma16816<false>(o[n], a, b[0], b[1]);
+          mma16816<false>(o[n + 1], a, b[2], b[3]);
+        }
+      } else {
+        const uint32_t a0[4] = {pf[2 * k][0], pf[2 * k][1], pf[2 * k + 1][0], pf[2 * k + 1][1]};
+        const uint32_t a1[4] = {pf[2 * k + 2][0], pf[2 * k + 2][1], pf[2 * k + 3][0], pf[2 * k + 3][1]};
+#pragma unroll
+        for (int n = 0; n < D / 16; ++n) {
+          uint32_t b[4];
+          const int row = k * 16 + lane;
+          ldsm4t(vtile + row * (UPR * 16) + swz(row, n) * 16, b);
+          // a register: two columns of position 2c, then of 2c + 1; split by column
+#pragma unroll
+          for (int j = 0; j < 4; ++j) b[j] = __byte_perm(b[j], 0, 0x3120);
+          mma16816<true>(o[2 * n], a0, e4m3x2_f16x2(b[0] & 0xffffu), e4m3x2_f16x2(b[1] & 0xffffu));
+          mma16816<true>(o[2 * n + 1], a0, e4m3x2_f16x2(b[0] >> 16), e4m3x2_f16x2(b[1] >> 16));
+          mma16816<true>(o[2 * n], a1, e4m3x2_f16x2(b[2] & 0xffffu), e4m3x2_f16x2(b[3] & 0xffffu));
+          mma16816<true>(o[2 * n + 1], a1, e4m3x2_f16x2(b[2] >> 16), e4m3x2_f16x2(b[3] >> 16));
+        }
+      }
+    }
+    __syncwarp();
+    issue(i + kStages - 1);
+  }
+  cp_wait<0>();
+  const bool whole = parts <= 1;
+  if (__syncthreads_or(bad)) {
+    plain_rows<D, E4M3>(p, s, seq, kv, 0, nrows, t_begin, t_end, part, whole, warp, kStepWarps);
+    return;
+  }
+
+  // join the warps: each leaves its average and its sum, the block weighs them
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    const int r = g + h * 8;
+    if (c == 0) {
+      sh.m[warp][r] = m[h];
+      sh.l[warp][r] = l[h];
+    }
+    const float f = l[h] == 0.f ? 0.f : 1.f / l[h];
+    const float e = E4M3 ? pow2i(min(max(ev_ref, -126), 127)) : 1.f;
+    float* dst = reinterpret_cast<float*>(ring) + (warp * kStepRows + r) * (D + 4);
+#pragma unroll
+    for (int n = 0; n < D / 8; n += 2) {
+      if (!E4M3) {
+        *reinterpret_cast<float2*>(dst + n * 8 + 2 * c) = make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
+        *reinterpret_cast<float2*>(dst + n * 8 + 8 + 2 * c) = make_float2(o[n + 1][2 * h] * f, o[n + 1][2 * h + 1] * f);
+      } else {
+        *reinterpret_cast<float4*>(dst + n * 8 + 4 * c) =
+            make_float4(o[n][2 * h] * f * e, o[n + 1][2 * h] * f * e, o[n][2 * h + 1] * f * e, o[n + 1][2 * h + 1] * f * e);
+      }
+    }
+  }
+  __syncthreads();
+  constexpr int TPR = kStepWarps * 32 / kStepRows;    // threads a row
+  const int r = threadIdx.x / TPR, d0 = threadIdx.x % TPR * 4;
+  if (r >= nrows) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kStepWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+  float fw[kStepWarps], sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kStepWarps; ++w) {
+    fw[w] = sh.m[w][r] == -INFINITY ? sh.l[w][r] : sh.l[w][r] * ex2(sh.m[w][r] - top);
+    sum += fw[w];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t row = s.row0 + r / p.group;
+  const int head = kv * p.group + r % p.group;
+#pragma unroll
+  for (int d = d0; d < D; d += TPR * 4) {
+    float x[4] = {};
+#pragma unroll
+    for (int w = 0; w < kStepWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring) + (w * kStepRows + r) * (D + 4) + d);
+      const float f = fw[w] * inv;
+      x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
+    }
+    store4<D>(p, part, whole, row, head, d, x);
+  }
+  if (!whole && d0 == 0) store_lse(p, part, row, head, sum == 0.f ? -INFINITY : top + log2f(sum) - kBias);
+}
+
+// ------------------------------------------------------------------ join
+// One warp a (row, query head) whose item was cut: the parts' averages weighed
+// by their sums. Bound by reading the parts once, small next to the cache.
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
+  pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t row = unit / p.q_heads;
+  const int head = (int)(unit % p.q_heads);
+  if (row >= p.b.rows) return;
+  int seq = 0;
+  for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+    const int i = i0 + lane;
+    seq += __popc(__ballot_sync(0xffffffffu, i < p.b.n && p.b.start[i + 1] <= row));
+  }
+  if (seq >= p.b.n) return;
+  const Seq s = seq_of(p.b, seq, p.c.status);
+  if (row < s.row0 || row >= s.row0 + s.n) return;
+  int parts = 0;
+  if (s.n * p.group <= kStepRows) parts = parts_of(item_range(p, s.first, s.first + s.n - 1, s.len), p.a.step_chunk);
+  if (parts <= 1) return;
+  const int64_t n = (int64_t)p.b.rows * p.q_heads;
+  float top = -INFINITY;
+  for (int i = lane; i < parts; i += 32) top = fmaxf(top, p.part_lse[i * n + unit]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  constexpr int E = D / 32;
+  float acc[E] = {}, sum = 0.f;
+  for (int i = 0; i < parts; ++i) {
+    const float lse = p.part_lse[i * n + unit];
+    const float w = lse == -INFINITY ? 0.f : ex2(lse - top);
+    sum += w;
+    const float* src = p.part_o + (i * n + unit) * D + lane * E;
+#pragma unroll
+    for (int j = 0; j < E; ++j) acc[j] += w * src[j];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t w[E / 2];
+#pragma unroll
+  for (int j = 0; j < E / 2; ++j) w[j] = bf_pack(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+  uint16_t* dst = p.out + row * p.o_row + head * p.o_head + lane * E;
+  if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1 % (E / 2)]);
+  else *reinterpret_cast<uint32_t*>(dst) = w[0];
+}
+
+// Rows of sequences that the step kernel does not take, one warp each.
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(256) attend_rows_kernel(const __grid_constant__ AttendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int r = (int)(unit / p.q_heads), h = (int)(unit % p.q_heads);
   if (r >= p.b.rows) return;
   int seq = 0;
@@ -26,72 +518,50 @@ __global__ void __launch_bounds__(kWarps * 32) attend_rows_kernel(const __grid_c
   if (seq >= p.b.n) return;
   const Seq s = seq_of(p.b, seq, p.c.status);
   if (r < s.row0 || r >= s.row0 + s.n) return;
-  int lo, hi;
-  visible(p, s.first + r - s.row0, s.len, &lo, &hi);
-  const int kv = h / p.group;
-  const uint16_t* qp = p.q + r * p.q_row + h * p.q_head + lane * E;
-  float q[E], acc[E] = {};
-#pragma unroll
-  for (int i = 0; i < E; ++i) q[i] = __uint_as_float((uint32_t)qp[i] << 16) * p.scale_log2;
-  float m = -INFINITY, l = 0.f;
-  const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
-  for (int t = lo; t < hi; ++t) {
-    const int page = page_of(table, p.b.width, p.c.pages, p.c.page_shift, t);
-    float k[E] = {}, v[E] = {};
-    if (page < 0) {
-      set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
-    } else {
-      const int64_t at = slot_bytes(p.c, page, kv, t);
-      if (E4M3) {
-        const int64_t sc = slot_scale(p.c, page, kv, t);
-        const float fk = pow2i((int)p.c.ks[sc] - 127), fv = pow2i((int)p.c.vs[sc] - 127);
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          float f[4];
-          e4m3x4_f32(p.c.k[at + lane * E + i], f);
-          k[i] = f[0] * fk;
-          e4m3x4_f32(p.c.v[at + lane * E + i], f);
-          v[i] = f[0] * fv;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          k[i] = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.c.k + at)[lane * E + i] << 16);
-          v[i] = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.c.v + at)[lane * E + i] << 16);
-        }
-      }
-    }
-    float d = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) d += q[i] * k[i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    const float mn = fmaxf(m, d), ref = mn == -INFINITY ? 0.f : mn;
-    const float a = ex2(m - ref), w = ex2(d - ref);
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = acc[i] * a + w * v[i];
-    m = mn;
+  if (s.n * p.group <= kStepRows && p.a.use_step) return;
+  const int kv = h / p.group, i = (r - s.row0) * p.group + h % p.group;
+  plain_rows<D, E4M3>(p, s, seq, kv, i, i + 1, 0, s.len, 0, true, 0, 1);
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const AttendParams& p, cudaStream_t s) {
+  if (p.a.use_step)
+    attend_step_kernel<D, E4M3><<<dim3(p.a.step_parts, p.c.heads, p.b.n), kStepWarps * 32, kStepSmem, s>>>(p);
+  const int64_t units = (int64_t)p.b.rows * p.q_heads;
+  const unsigned grid = (unsigned)((units + 7) / 8);
+  if (p.a.use_chunk) attend_rows_kernel<D, E4M3><<<grid, 256, 0, s>>>(p);
+  if (std::max(p.a.step_parts, p.a.chunk_parts) > 1) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, p);
+    if (e != cudaSuccess) return e;
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint16_t* op = p.out + r * p.o_row + h * p.o_head + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) op[i] = (uint16_t)bf_pack(acc[i] * inv, 0.f);
+  return cudaGetLastError();
+}
+
+template <int D, bool E4M3>
+cudaError_t prepare() {
+  return cudaFuncSetAttribute(attend_step_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
 }
 
 }  // namespace
 
+cudaError_t prepare_attend() {
+  for (cudaError_t e : {prepare<64, false>(), prepare<64, true>(), prepare<128, false>(), prepare<128, true>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
 cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s) {
-  const int64_t units = (int64_t)p.b.rows * p.q_heads;
-  const unsigned grid = (unsigned)((units + kWarps - 1) / kWarps);
-  if (head_dim == 128) {
-    if (e4m3) attend_rows_kernel<128, true><<<grid, kWarps * 32, 0, s>>>(p);
-    else attend_rows_kernel<128, false><<<grid, kWarps * 32, 0, s>>>(p);
-  } else {
-    if (e4m3) attend_rows_kernel<64, true><<<grid, kWarps * 32, 0, s>>>(p);
-    else attend_rows_kernel<64, false><<<grid, kWarps * 32, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  if (head_dim == 128) return e4m3 ? launch<128, true>(p, s) : launch<128, false>(p, s);
+  return e4m3 ? launch<64, true>(p, s) : launch<64, false>(p, s);
 }
 
 }  // namespace cache

@@ -1,0 +1,124 @@
+// cp_attend.cuh -- what the attention kernels share: the plain path of rows
+// next to masked non-finite values, and how a part's result is stored.
+#pragma once
+#include "cp_cache.cuh"
+#include "cp_ptx.cuh"
+
+namespace cp {
+namespace cache {
+
+using ptx::pdl_trigger;
+using ptx::pdl_wait;
+
+// Biased exponent of a bf16 pattern, 0 for infinities and NaN.
+__device__ __forceinline__ int finite_exp(uint32_t h) {
+  const int e = (int)(h >> 7) & 255;
+  return e == 255 ? 0 : e;
+}
+
+// Whether 16 bytes of shared memory hold an element that is not finite.
+template <bool E4M3>
+__device__ __forceinline__ bool any_nonfinite(uint32_t addr) {
+  uint32_t w[4];
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (E4M3) bad |= __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+    else bad |= __vcmpeq2(w[i] & 0x7f807f80u, 0x7f807f80u) != 0;
+  }
+  return bad;
+}
+
+// Four neighbouring elements of a row's result: the answer itself, rounded, or
+// a part's average in fp32.
+template <int D>
+__device__ __forceinline__ void store4(const AttendParams& p, int part, bool whole, int64_t row, int head, int d,
+                                       const float* x) {
+  if (whole)
+    *reinterpret_cast<uint2*>(p.out + row * p.o_row + head * p.o_head + d) = make_uint2(bf_pack(x[0], x[1]), bf_pack(x[2], x[3]));
+  else
+    *reinterpret_cast<float4*>(p.part_o + (((int64_t)part * p.b.rows + row) * p.q_heads + head) * D + d) =
+        make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store_lse(const AttendParams& p, int part, int64_t row, int head, float lse) {
+  p.part_lse[((int64_t)part * p.b.rows + row) * p.q_heads + head] = lse;
+}
+
+// Rows i0 .. i1-1 of a sequence and kv head (row i: new row i / group, query
+// head i % group of the kv head) over positions [t_begin, t_end), a warp a
+// row: lanes share the head's elements, walk the positions the row sees and
+// read no other, with a running maximum and sum. The matrix kernels multiply
+// masked values by zero, which is wrong where one is infinite or NaN; a block
+// that finds one next to a mask runs this instead.
+template <int D, bool E4M3>
+__device__ __noinline__ void plain_rows(const AttendParams& p, const Seq& s, int seq, int kv, int i0, int i1, int t_begin,
+                                        int t_end, int part, bool whole, int warp, int warps) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
+  for (int i = i0 + warp; i < i1; i += warps) {
+    const int64_t row = s.row0 + i / p.group;
+    const int head = kv * p.group + i % p.group;
+    int lo, hi;
+    visible(p, s.first + i / p.group, s.len, &lo, &hi);
+    lo = max(lo, t_begin);
+    hi = min(hi, t_end);
+    const uint16_t* qp = p.q + row * p.q_row + head * p.q_head + lane * E;
+    float q[E], acc[E] = {};
+#pragma unroll
+    for (int j = 0; j < E; ++j) q[j] = __uint_as_float((uint32_t)qp[j] << 16) * p.scale_log2;
+    float m = -INFINITY, l = 0.f;
+    for (int t = lo; t < hi; ++t) {
+      const int page = page_of(table, p.b.width, p.c.pages, p.c.page_shift, t);
+      float k[E] = {}, v[E] = {};
+      if (page < 0) {
+        set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
+      } else {
+        const int64_t at = slot_bytes(p.c, page, kv, t);
+        if (E4M3) {
+          const int64_t sc = slot_scale(p.c, page, kv, t);
+          const float fk = pow2i((int)p.c.ks[sc] - 127), fv = pow2i((int)p.c.vs[sc] - 127);
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            float f[4];
+            e4m3x4_f32(p.c.k[at + lane * E + j], f);
+            k[j] = f[0] * fk;
+            e4m3x4_f32(p.c.v[at + lane * E + j], f);
+            v[j] = f[0] * fv;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < E; ++j) {
+            k[j] = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.c.k + at)[lane * E + j] << 16);
+            v[j] = __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(p.c.v + at)[lane * E + j] << 16);
+          }
+        }
+      }
+      float d = 0.f;
+#pragma unroll
+      for (int j = 0; j < E; ++j) d += q[j] * k[j];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      const float mn = fmaxf(m, d), ref = mn == -INFINITY ? 0.f : mn;
+      const float a = ex2(m - ref), w = ex2(d - ref);
+      l = l * a + w;
+#pragma unroll
+      for (int j = 0; j < E; ++j) acc[j] = acc[j] * a + w * v[j];
+      m = mn;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (whole) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) p.out[row * p.o_row + head * p.o_head + lane * E + j] = (uint16_t)bf_pack(acc[j] * inv, 0.f);
+    } else {
+      const int64_t unit = ((int64_t)part * p.b.rows + row) * p.q_heads + head;
+#pragma unroll
+      for (int j = 0; j < E; ++j) p.part_o[unit * D + lane * E + j] = acc[j] * inv;
+      if (lane == 0) p.part_lse[unit] = l == 0.f ? -INFINITY : m + log2f(l);
+    }
+  }
+}
+
+}  // namespace cache
+}  // namespace cp

@@ -351,6 +351,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   if (!a || !a->q || !a->out || a->q_heads < 1 || a->window < 0) return CP_ERR_INVALID_ARG;
   if (a->q_heads % d.kv_heads) return CP_ERR_INVALID_ARG;
   if (a->q_heads / d.kv_heads > 64) return CP_ERR_UNSUPPORTED;
+  if ((int64_t)b.rows * (a->q_heads / d.kv_heads) >= (1 << 30)) return CP_ERR_UNSUPPORTED;   // rows are counted in 32 bits
   if (!(a->scale >= 0.f) || !std::isfinite(a->scale)) return CP_ERR_INVALID_ARG;
   p->q_head = a->q_head_stride ? a->q_head_stride : d.head_dim;
   p->o_head = a->out_head_stride ? a->out_head_stride : d.head_dim;
@@ -368,6 +369,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   p->scale_log2 = (float)(scale * 1.4426950408889634);
   p->causal = a->causal != 0;
   p->window = a->window;
+  p->a = plan_attend(b, d.kv_heads, a->q_heads, d.head_dim, d.dtype == CP_CACHE_E4M3, p->window);
   return CP_OK;
 }
 
@@ -393,7 +395,10 @@ int cp_cache_check(const cp_cache_desc* desc, const cp_batch* batch, const cp_ap
   AppendParams ap{};
   if (append && (st = check_append(d, b, append, &ap))) return st;
   AttendParams at{};
-  if (attend && (st = check_attend(d, b, attend, &at))) return st;
+  if (attend) {
+    if ((st = check_attend(d, b, attend, &at))) return st;
+    if (workspace_bytes) *workspace_bytes = attend_workspace(at.a, b, at.q_heads, d.head_dim);
+  }
   return CP_OK;
 }
 
@@ -429,7 +434,7 @@ int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out) {
     return CP_ERR_NOMEM;
   }
   c->view = view_of(d, static_cast<int32_t*>(status));
-  if (cudaMemset(status, 0, 16) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (prepare_attend() != cudaSuccess || cudaMemset(status, 0, 16) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cp_cache_destroy(c);
     return CP_ERR_CUDA;
   }
@@ -521,10 +526,14 @@ int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, v
   int st = check_batch(c->d, batch, &b);
   if (!st) st = check_attend(c->d, b, args, &p);
   if (st) return st;
-  (void)workspace;
-  (void)workspace_bytes;
+  const size_t need = attend_workspace(p.a, b, p.q_heads, c->d.head_dim);
+  if (need && (!workspace || workspace_bytes < need)) return CP_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return CP_ERR_UNSUPPORTED;
   DeviceGuard g(c->device);
   p.c = c->view;
+  const size_t units = (size_t)b.rows * p.q_heads * std::max(p.a.step_parts, p.a.chunk_parts);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + units * c->d.head_dim;
   return cuda_err(launch_attend(p, c->d.head_dim, c->d.dtype == CP_CACHE_E4M3, reinterpret_cast<cudaStream_t>(stream)));
 }
 

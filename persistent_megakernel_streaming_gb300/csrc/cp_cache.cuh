@@ -105,11 +105,29 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ------------------------------------------------------------------ attention
+// How a call is cut up, from the host's bounds alone (so that a captured call
+// keeps it): sequences of at most kStepRows rows a kv head go to the step
+// kernel, the others to the chunk kernel. An item (a sequence, or a tile of its
+// rows) whose visible positions are more than `chunk` is cut into parts of
+// that many, each a block's; a last kernel joins the parts.
+constexpr int kStepRows = 16;
+
+struct AttendPlan {
+  int use_step, use_chunk;
+  int step_chunk, step_parts;     // positions a part, most parts of an item
+  int chunk_chunk, chunk_parts;
+};
+AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, int window);
+size_t attend_workspace(const AttendPlan& a, const BatchView& b, int q_heads, int head_dim);
+
 struct AttendParams {
   CacheView c;
   BatchView b;
+  AttendPlan a;
   const uint16_t* q;
   uint16_t* out;
+  float* part_o;                          // [parts][rows][q_heads][D]: a part's softmax average of v
+  float* part_lse;                        // [parts][rows][q_heads]: log2 of its sum of exponentials
   int64_t q_row, q_head, o_row, o_head;   // element strides
   int group;                              // query heads per kv head
   int q_heads;
@@ -123,6 +141,26 @@ __device__ __forceinline__ void visible(const AttendParams& p, int pos, int len,
   *lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
 }
 
+// The positions some row of an item sees, from its first and last row's
+// positions; `base` is where its parts start (a multiple of 16, so that a
+// 16-position group never crosses a page).
+struct Range {
+  int lo, hi, base;
+};
+__device__ __forceinline__ Range item_range(const AttendParams& p, int pos_first, int pos_last, int len) {
+  Range r;
+  int d;
+  visible(p, pos_first, len, &r.lo, &d);
+  visible(p, pos_last, len, &d, &r.hi);
+  r.base = min(r.lo, max(r.hi, 0)) & ~15;
+  return r;
+}
+__device__ __forceinline__ int parts_of(const Range& r, int chunk) {
+  return r.hi > r.base ? (r.hi - r.base + chunk - 1) / chunk : 0;
+}
+
+// Once per device, with it current: the kernels' shared-memory sizes.
+cudaError_t prepare_attend();
 cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s);
 
 }  // namespace cache

@@ -104,6 +104,11 @@ def test_bad_attends_are_refused(kw, want):
     assert check(desc(), batch(), None, attend(**kw)) == want
 
 
+def test_more_rows_than_tiles_can_count_are_refused():
+    assert check(desc(kv_heads=1), batch(rows=1 << 26), None, attend(q_heads=16)) == UNSUPPORTED
+    assert check(desc(kv_heads=1), batch(rows=1 << 26), None, attend(q_heads=15)) == OK
+
+
 def test_append_and_attend_need_a_batch_and_a_cache(L):
     assert check(desc(), None, append()) == INVALID
     assert check(desc(), None, None, attend()) == INVALID

@@ -532,6 +532,21 @@ def test_two_captured_graphs_and_eager_calls_at_once():
             assert torch.equal(o, y)
 
 
+def test_a_workspace_of_the_callers():
+    w = World([9000], [1], 1, 64, 64, False).fill()
+    q, out = w.attend(2)
+    need = w.cache.workspace_bytes(w.batch, 2)
+    assert need > 0
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device="cuda")
+    got = torch.zeros_like(out)
+    w.cache.attend(w.batch, q.cuda(), got, workspace=ws[:need])
+    assert torch.equal(got, out) and (ws[need:] == 255).all()
+    with pytest.raises(cp.CPError):
+        w.cache.attend(w.batch, q.cuda(), got, workspace=ws[:need - 16])
+    with pytest.raises(cp.CPError):
+        w.cache.attend(w.batch, q.cuda(), got, workspace=ws[8:need + 8])
+
+
 def test_loose_bounds_change_nothing_but_rounding():
     w = World([700, 33], [1, 20], 2, 64, 16, False).fill()
     q, out = w.attend(4)
