@@ -29,6 +29,7 @@ SOURCES = [
     ("cp_plan.cpp", "cp_plan.cpp.o", []),
     ("cp_cache.cu", "cp_cache.cu.o", []),
     ("cp_attend.cu", "cp_attend.cu.o", []),
+    ("cp_attend_chunk.cu", "cp_attend_chunk.cu.o", []),
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -1,6 +1,7 @@
 // cp_attend.cu -- attention of a batch's new rows over the paged cache: the
 // plan of a call, the step kernel (up to 16 rows a kv head, bound by reading
-// the cache once) and the kernel that joins an item's parts.
+// the cache once) and the kernel that joins an item's parts. Sequences with
+// more rows go to cp_attend_chunk.cu.
 #include <algorithm>
 
 #include "cp_attend.cuh"
@@ -9,12 +10,14 @@ namespace cp {
 namespace cache {
 
 // ------------------------------------------------------------------ plan
-constexpr int kStepBlocks = 304;      // step blocks resident at once: two on each of 152 SMs
+constexpr int kSms = 152;
+constexpr int kStepBlocks = 2 * kSms; // step blocks resident at once
 constexpr int kMaxStepChunk = 4096;   // positions a step block holds page numbers for
 
 static int step_tile(int head_dim, bool e4m3) { return 4 * (e4m3 ? 32 : 16) * (128 / head_dim); }
 
-AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, int window) {
+AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, bool causal,
+                       int window) {
   AttendPlan a{};
   const int group = q_heads / kv_heads;
   a.use_step = group <= kStepRows;
@@ -30,6 +33,24 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
   chunk = std::min<int64_t>(std::max<int64_t>((chunk + tile - 1) / tile * tile, tile), kMaxStepChunk);
   a.step_chunk = (int)chunk;
   a.step_parts = a.use_step ? (int)std::max<int64_t>(1, (span + chunk - 1) / chunk) : 0;
+  if (a.use_chunk) {
+    // As many items as the rows make when every sequence has max_new of them; cut into the number of parts whose
+    // rounds on 152 SMs cost least, at two tiles of positions for a block's start and end.
+    const int64_t per = ((int64_t)b.max_new * group + kPairRows - 1) / kPairRows;
+    const int64_t blocks = std::max<int64_t>(1, (int64_t)b.rows / b.max_new) * per * kv_heads;
+    int64_t all = b.max_len;
+    // a window spans itself and the item's rows; not causal, the rows up to the last of the sequence
+    const int64_t ahead = causal ? std::min(b.max_new, (kPairRows + group - 1) / group + 1) : b.max_new;
+    if (window > 0) all = std::min<int64_t>(all, (int64_t)window + ahead + 15);
+    int64_t best = -1, parts = 1;
+    for (int64_t n = 1; n <= 32; ++n) {
+      const int64_t each = ((all + n - 1) / n + 127) / 128 * 128;
+      const int64_t cost = (blocks * n + kSms - 1) / kSms * (each + 256);
+      if (best < 0 || cost < best) best = cost, parts = n;
+    }
+    a.chunk_chunk = (int)(((all + parts - 1) / parts + 127) / 128 * 128);
+    a.chunk_parts = (int)((all + a.chunk_chunk - 1) / a.chunk_chunk);
+  }
   return a;
 }
 
@@ -476,8 +497,15 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   if (seq >= p.b.n) return;
   const Seq s = seq_of(p.b, seq, p.c.status);
   if (row < s.row0 || row >= s.row0 + s.n) return;
-  int parts = 0;
-  if (s.n * p.group <= kStepRows) parts = parts_of(item_range(p, s.first, s.first + s.n - 1, s.len), p.a.step_chunk);
+  const int nrows = s.n * p.group;
+  int parts;
+  if (p.a.use_step && nrows <= kStepRows) {
+    parts = parts_of(item_range(p, s.first, s.first + s.n - 1, s.len), p.a.step_chunk);
+  } else {
+    const int i0 = ((int)(row - s.row0) * p.group + head % p.group) / kPairRows * kPairRows;
+    const int i1 = min(i0 + kPairRows, nrows) - 1;
+    parts = parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len), p.a.chunk_chunk);
+  }
   if (parts <= 1) return;
   const int64_t n = (int64_t)p.b.rows * p.q_heads;
   float top = -INFINITY;
@@ -503,33 +531,16 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   else *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
-// Rows of sequences that the step kernel does not take, one warp each.
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(256) attend_rows_kernel(const __grid_constant__ AttendParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r = (int)(unit / p.q_heads), h = (int)(unit % p.q_heads);
-  if (r >= p.b.rows) return;
-  int seq = 0;
-  for (int i0 = 0; i0 < p.b.n; i0 += 32) {
-    const int i = i0 + lane;
-    seq += __popc(__ballot_sync(0xffffffffu, i < p.b.n && p.b.start[i + 1] <= r));
-  }
-  if (seq >= p.b.n) return;
-  const Seq s = seq_of(p.b, seq, p.c.status);
-  if (r < s.row0 || r >= s.row0 + s.n) return;
-  if (s.n * p.group <= kStepRows && p.a.use_step) return;
-  const int kv = h / p.group, i = (r - s.row0) * p.group + h % p.group;
-  plain_rows<D, E4M3>(p, s, seq, kv, i, i + 1, 0, s.len, 0, true, 0, 1);
-}
-
 template <int D, bool E4M3>
 cudaError_t launch(const AttendParams& p, cudaStream_t s) {
   if (p.a.use_step)
     attend_step_kernel<D, E4M3><<<dim3(p.a.step_parts, p.c.heads, p.b.n), kStepWarps * 32, kStepSmem, s>>>(p);
   const int64_t units = (int64_t)p.b.rows * p.q_heads;
   const unsigned grid = (unsigned)((units + 7) / 8);
-  if (p.a.use_chunk) attend_rows_kernel<D, E4M3><<<grid, 256, 0, s>>>(p);
+  if (p.a.use_chunk) {
+    const cudaError_t e = launch_attend_chunk(p, D, E4M3, s);
+    if (e != cudaSuccess) return e;
+  }
   if (std::max(p.a.step_parts, p.a.chunk_parts) > 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -556,7 +567,7 @@ cudaError_t prepare() {
 cudaError_t prepare_attend() {
   for (cudaError_t e : {prepare<64, false>(), prepare<64, true>(), prepare<128, false>(), prepare<128, true>()})
     if (e != cudaSuccess) return e;
-  return cudaSuccess;
+  return prepare_attend_chunk();
 }
 
 cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s) {

@@ -369,7 +369,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   p->scale_log2 = (float)(scale * 1.4426950408889634);
   p->causal = a->causal != 0;
   p->window = a->window;
-  p->a = plan_attend(b, d.kv_heads, a->q_heads, d.head_dim, d.dtype == CP_CACHE_E4M3, p->window);
+  p->a = plan_attend(b, d.kv_heads, a->q_heads, d.head_dim, d.dtype == CP_CACHE_E4M3, p->causal != 0, p->window);
   return CP_OK;
 }
 

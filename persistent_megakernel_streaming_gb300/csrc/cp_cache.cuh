@@ -112,12 +112,19 @@ __device__ __forceinline__ float ex2(float x) {
 // that many, each a block's; a last kernel joins the parts.
 constexpr int kStepRows = 16;
 
+constexpr int kPairRows = 256;    // rows (times query heads) that a chunk block takes
+
 struct AttendPlan {
   int use_step, use_chunk;
   int step_chunk, step_parts;     // positions a part, most parts of an item
   int chunk_chunk, chunk_parts;
 };
-AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, int window);
+AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, bool causal,
+                       int window);
+// An upper bound of the chunk kernel's items a kv head: whole pairs and one more a sequence.
+inline int64_t chunk_pairs(const BatchView& b, int group) {
+  return (int64_t)b.rows * group / kPairRows + (b.n < b.rows ? b.n : b.rows);
+}
 size_t attend_workspace(const AttendPlan& a, const BatchView& b, int q_heads, int head_dim);
 
 struct AttendParams {
@@ -161,6 +168,8 @@ __device__ __forceinline__ int parts_of(const Range& r, int chunk) {
 
 // Once per device, with it current: the kernels' shared-memory sizes.
 cudaError_t prepare_attend();
+cudaError_t prepare_attend_chunk();
+cudaError_t launch_attend_chunk(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s);
 cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s);
 
 }  // namespace cache

@@ -218,6 +218,47 @@ __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// Store 16 or 32 consecutive 32-bit columns of this warp's 32 TMEM lanes (wait with tm_wait_st).
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t taddr, const float* v) {
+  uint32_t r[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+  tm_st16(taddr, r);
+  tm_st16(taddr + 16, r + 16);
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs, fp32 accumulate. A holds two
+// consecutive elements of its row a 32-bit column, row i in lane i.
+__device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "setp.ne.b32 P, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// The same layout as an operand whose rows lie along K (tokens of V: 128-byte
+// rows of 64 columns, 8 rows an atom of 1024 B, the next 64 columns
+// `slab` bytes on): major along the columns.
+__device__ __forceinline__ uint64_t sdesc_sw128_cols(uint32_t addr, uint32_t slab) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(slab >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// Instruction descriptor of kind::f16 with M = 128, D fp32: A and B fp16 or
+// bf16, A K-major, B K-major or (`cols`) major along its columns.
+__device__ __forceinline__ uint32_t idesc_m128(int n, bool half, bool cols) {
+  const uint32_t f = half ? 0u : 1u;
+  return (1u << 4) | (f << 7) | (f << 10) | ((cols ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
 // Shared-memory matrix descriptor: K-major operand in the 128-byte swizzle
 // layout (rows of 128 B, 8-row atoms of 1024 B, atoms 1024 B apart).
 __device__ __forceinline__ uint64_t sdesc_sw128(uint32_t addr) {
