@@ -25,7 +25,7 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
   // the most positions an item spans: all, or a window and the rows behind it
   const int64_t rows = std::min(b.max_new, kStepRows / std::min(group, kStepRows));
   int64_t span = b.max_len;
-  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + rows + 15);
+  if (window > 0) span = std::min<int64_t>(span, (int64_t)window + rows + kStepAlign - 1);
   const int tile = step_tile(head_dim, e4m3);
   const int64_t items = (int64_t)b.n * kv_heads;
   const int64_t want = std::max<int64_t>(1, kStepBlocks * 8 / items);
@@ -41,7 +41,7 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
     int64_t all = b.max_len;
     // a window spans itself and the item's rows; not causal, the rows up to the last of the sequence
     const int64_t ahead = causal ? std::min(b.max_new, (kPairRows + group - 1) / group + 1) : b.max_new;
-    if (window > 0) all = std::min<int64_t>(all, (int64_t)window + ahead + 15);
+    if (window > 0) all = std::min<int64_t>(all, (int64_t)window + ahead + kChunkAlign - 1);
     int64_t best = -1, parts = 1;
     for (int64_t n = 1; n <= 32; ++n) {
       const int64_t each = ((all + n - 1) / n + 127) / 128 * 128;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
   const Seq s = seq_of(p.b, seq, p.c.status);
   const int nrows = s.n * p.group;
   if (s.n == 0 || nrows > kStepRows) return;
-  const Range range = item_range(p, s.first, s.first + s.n - 1, s.len);
+  const Range range = item_range(p, s.first, s.first + s.n - 1, s.len, kStepAlign);
   const int parts = parts_of(range, p.a.step_chunk);
   if (part >= max(parts, 1)) return;
   const int t_begin = range.base + part * p.a.step_chunk;
@@ -500,11 +500,11 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int nrows = s.n * p.group;
   int parts;
   if (p.a.use_step && nrows <= kStepRows) {
-    parts = parts_of(item_range(p, s.first, s.first + s.n - 1, s.len), p.a.step_chunk);
+    parts = parts_of(item_range(p, s.first, s.first + s.n - 1, s.len, kStepAlign), p.a.step_chunk);
   } else {
     const int i0 = ((int)(row - s.row0) * p.group + head % p.group) / kPairRows * kPairRows;
     const int i1 = min(i0 + kPairRows, nrows) - 1;
-    parts = parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len), p.a.chunk_chunk);
+    parts = parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len, kChunkAlign), p.a.chunk_chunk);
   }
   if (parts <= 1) return;
   const int64_t n = (int64_t)p.b.rows * p.q_heads;
@@ -532,13 +532,13 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 }
 
 template <int D, bool E4M3>
-cudaError_t launch(const AttendParams& p, cudaStream_t s) {
+cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   if (p.a.use_step)
     attend_step_kernel<D, E4M3><<<dim3(p.a.step_parts, p.c.heads, p.b.n), kStepWarps * 32, kStepSmem, s>>>(p);
   const int64_t units = (int64_t)p.b.rows * p.q_heads;
   const unsigned grid = (unsigned)((units + 7) / 8);
   if (p.a.use_chunk) {
-    const cudaError_t e = launch_attend_chunk(p, D, E4M3, s);
+    const cudaError_t e = launch_attend_chunk(p, maps, D, E4M3, s);
     if (e != cudaSuccess) return e;
   }
   if (std::max(p.a.step_parts, p.a.chunk_parts) > 1) {
@@ -570,9 +570,9 @@ cudaError_t prepare_attend() {
   return prepare_attend_chunk();
 }
 
-cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s) {
-  if (head_dim == 128) return e4m3 ? launch<128, true>(p, s) : launch<128, false>(p, s);
-  return e4m3 ? launch<64, true>(p, s) : launch<64, false>(p, s);
+cudaError_t launch_attend(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s) {
+  if (head_dim == 128) return e4m3 ? launch<128, true>(p, maps, s) : launch<128, false>(p, maps, s);
+  return e4m3 ? launch<64, true>(p, maps, s) : launch<64, false>(p, maps, s);
 }
 
 }  // namespace cache

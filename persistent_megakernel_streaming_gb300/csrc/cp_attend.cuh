@@ -52,7 +52,7 @@ __device__ __forceinline__ void store_lse(const AttendParams& p, int part, int64
 // masked values by zero, which is wrong where one is infinite or NaN; a block
 // that finds one next to a mask runs this instead.
 template <int D, bool E4M3>
-__device__ __noinline__ void plain_rows(const AttendParams& p, const Seq& s, int seq, int kv, int i0, int i1, int t_begin,
+__device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, int kv, int i0, int i1, int t_begin,
                                         int t_end, int part, bool whole, int warp, int warps) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;

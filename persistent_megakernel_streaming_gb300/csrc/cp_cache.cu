@@ -17,6 +17,7 @@ struct cp_cache {
   int device = 0;
   cp_cache_desc d{};
   CacheView view{};
+  CacheMaps maps{};
 };
 
 namespace {
@@ -273,7 +274,30 @@ int check_desc(const cp_cache_desc* in, cp_cache_desc* d) {
   const int per16 = e4m3 ? 16 : 8;
   if (d->token_stride % per16 || d->head_stride % per16 || d->page_stride % per16 || !aligned16(d->k) || !aligned16(d->v))
     return CP_ERR_UNSUPPORTED;
+  const int64_t most = ((int64_t)1 << 40) / (e4m3 ? 1 : 2);    // what a tensor map's strides reach
+  if (d->token_stride >= most || d->head_stride >= most || d->page_stride >= most) return CP_ERR_UNSUPPORTED;
   return CP_OK;
+}
+
+// The tensor map of K or V: 64 bf16 columns a box in the 128-byte swizzle that
+// the tensor core reads, or whole e4m3 rows as they lie; a page high.
+int make_map(const cp_cache_desc& d, void* base, CUtensorMap* map) {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult found;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+      found != cudaDriverEntryPointSuccess)
+    return CP_ERR_CUDA;
+  const bool e4m3 = d.dtype == CP_CACHE_E4M3;
+  const cuuint64_t es = e4m3 ? 1 : 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)d.head_dim, (cuuint64_t)d.page_size, (cuuint64_t)d.kv_heads, (cuuint64_t)d.pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)d.token_stride * es, (cuuint64_t)d.head_stride * es, (cuuint64_t)d.page_stride * es};
+  const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? d.head_dim : 64), (cuuint32_t)d.page_size, 1, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  const CUresult r = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)(
+      map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, steps,
+      CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? CP_OK : CP_ERR_UNSUPPORTED;
 }
 
 CacheView view_of(const cp_cache_desc& d, int32_t* status) {
@@ -428,6 +452,12 @@ int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out) {
   if (!c) return CP_ERR_NOMEM;
   c->device = device;
   c->d = d;
+  int mapped = make_map(d, d.k, &c->maps.k);
+  if (!mapped) mapped = make_map(d, d.v, &c->maps.v);
+  if (mapped) {
+    delete c;
+    return mapped;
+  }
   void* status = nullptr;
   if (cudaMalloc(&status, 16) != cudaSuccess) {
     delete c;
@@ -534,7 +564,7 @@ int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, v
   const size_t units = (size_t)b.rows * p.q_heads * std::max(p.a.step_parts, p.a.chunk_parts);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + units * c->d.head_dim;
-  return cuda_err(launch_attend(p, c->d.head_dim, c->d.dtype == CP_CACHE_E4M3, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_err(launch_attend(p, c->maps, c->d.head_dim, c->d.dtype == CP_CACHE_E4M3, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int64_t cp_test_slot(const cp_cache_desc* desc, const int32_t* table, int table_width, int pos, int head) {

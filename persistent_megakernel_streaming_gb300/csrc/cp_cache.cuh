@@ -2,6 +2,7 @@
 // batch's view on the device, the look-ups with their bounds checks, and the
 // element formats.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -113,6 +114,7 @@ __device__ __forceinline__ float ex2(float x) {
 constexpr int kStepRows = 16;
 
 constexpr int kPairRows = 256;    // rows (times query heads) that a chunk block takes
+constexpr int kStepAlign = 16, kChunkAlign = 128;   // where an item's parts may start
 
 struct AttendPlan {
   int use_step, use_chunk;
@@ -149,17 +151,18 @@ __device__ __forceinline__ void visible(const AttendParams& p, int pos, int len,
 }
 
 // The positions some row of an item sees, from its first and last row's
-// positions; `base` is where its parts start (a multiple of 16, so that a
-// 16-position group never crosses a page).
+// positions; `base` is where its parts start: a multiple of 16 for the step
+// kernel (16 positions never cross a page), of its 128-position tile for the
+// chunk kernel.
 struct Range {
   int lo, hi, base;
 };
-__device__ __forceinline__ Range item_range(const AttendParams& p, int pos_first, int pos_last, int len) {
+__device__ __forceinline__ Range item_range(const AttendParams& p, int pos_first, int pos_last, int len, int align) {
   Range r;
   int d;
   visible(p, pos_first, len, &r.lo, &d);
   visible(p, pos_last, len, &d, &r.hi);
-  r.base = min(r.lo, max(r.hi, 0)) & ~15;
+  r.base = min(r.lo, max(r.hi, 0)) & ~(align - 1);
   return r;
 }
 __device__ __forceinline__ int parts_of(const Range& r, int chunk) {
@@ -169,8 +172,13 @@ __device__ __forceinline__ int parts_of(const Range& r, int chunk) {
 // Once per device, with it current: the kernels' shared-memory sizes.
 cudaError_t prepare_attend();
 cudaError_t prepare_attend_chunk();
-cudaError_t launch_attend_chunk(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s);
-cudaError_t launch_attend(const AttendParams& p, int head_dim, bool e4m3, cudaStream_t s);
+// The chunk kernel reads pages through tensor maps of K and V (head_dim,
+// position in the page, head, page).
+struct CacheMaps {
+  CUtensorMap k, v;
+};
+cudaError_t launch_attend_chunk(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s);
+cudaError_t launch_attend(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s);
 
 }  // namespace cache
 }  // namespace cp
