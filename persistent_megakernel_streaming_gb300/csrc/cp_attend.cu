@@ -20,8 +20,10 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
                        int window) {
   AttendPlan a{};
   const int group = q_heads / kv_heads;
-  a.use_step = group <= kStepRows;
   a.use_chunk = (int64_t)b.max_new * group > kStepRows;
+  // where every sequence may have max_new rows the chunk kernel takes what few may turn out shorter: an empty
+  // launch of the step kernel costs 3 to 6 us
+  a.use_step = group <= kStepRows && (!a.use_chunk || (int64_t)b.n * b.max_new > b.rows);
   // the most positions an item spans: all, or a window and the rows behind it
   const int64_t rows = std::min(b.max_new, kStepRows / std::min(group, kStepRows));
   int64_t span = b.max_len;
@@ -34,19 +36,24 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
   a.step_chunk = (int)chunk;
   a.step_parts = a.use_step ? (int)std::max<int64_t>(1, (span + chunk - 1) / chunk) : 0;
   if (a.use_chunk) {
-    // As many items as the rows make when every sequence has max_new of them; cut into the number of parts whose
-    // rounds on 152 SMs cost least, at two tiles of positions for a block's start and end.
+    // As many items as the rows make when every sequence has max_new of them, cut into the number of parts that costs
+    // least on 152 SMs.
     const int64_t per = ((int64_t)b.max_new * group + kPairRows - 1) / kPairRows;
     const int64_t blocks = std::max<int64_t>(1, (int64_t)b.rows / b.max_new) * per * kv_heads;
     int64_t all = b.max_len;
     // a window spans itself and the item's rows; not causal, the rows up to the last of the sequence
     const int64_t ahead = causal ? std::min(b.max_new, (kPairRows + group - 1) / group + 1) : b.max_new;
     if (window > 0) all = std::min<int64_t>(all, (int64_t)window + ahead + kChunkAlign - 1);
-    int64_t best = -1, parts = 1;
+    // In nanoseconds: a tile of 128 positions 1500 (twice that in heads of 64 than the tensor core needs), a block's
+    // start and end 6000, and the parts' results written and read again at 5 TB/s.
+    double best = 0;
+    int64_t parts = 1;
+    const double tile_ns = head_dim == 128 ? 1500 : 1000;
+    const double join_ns = 2.0 * b.rows * q_heads * head_dim * 4 / 5000;
     for (int64_t n = 1; n <= 32; ++n) {
-      const int64_t each = ((all + n - 1) / n + 127) / 128 * 128;
-      const int64_t cost = (blocks * n + kSms - 1) / kSms * (each + 256);
-      if (best < 0 || cost < best) best = cost, parts = n;
+      const int64_t tiles = ((all + n - 1) / n + 127) / 128;
+      const double cost = (double)((blocks * n + kSms - 1) / kSms) * (tiles * tile_ns + 6000) + (n > 1 ? 3000 + n * join_ns : 0);
+      if (n == 1 || cost < best) best = cost, parts = n;
     }
     a.chunk_chunk = (int)(((all + parts - 1) / parts + 127) / 128 * 128);
     a.chunk_parts = (int)((all + a.chunk_chunk - 1) / a.chunk_chunk);
@@ -167,7 +174,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
   const int mask = (1 << p.c.page_shift) - 1;
 
   auto swz = [](int row, int unit) { return UPR == 4 ? unit ^ ((row >> 1) & 3) : unit ^ (row & 7); };
-  uint32_t sc_next[2] = {0, 0}, sc_cur[2] = {0, 0};   // scale bytes (key | value << 8) of the lane's positions
+  // scale bytes of the lane's positions (two in a tile of 64): of the tile two on, and of the next
+  uint8_t ks_next[2] = {0, 0}, vs_next[2] = {0, 0}, ks_cur[2] = {0, 0}, vs_cur[2] = {0, 0};
   // Tile i of this warp into its ring slot: rows outside [lo, t_end) or on no page are zeros.
   auto issue = [&](int i) {
     if (i < mine) {
@@ -193,15 +201,15 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
 #pragma unroll
         for (int x = 0; x < (TK + 31) / 32; ++x) {
           const int t = t0 + x * 32 + lane;
-          uint32_t b = 0;
+          ks_next[x] = vs_next[x] = 0;
           if (t >= range.lo && t < t_end) {
             const int pg = sh.pages[(t - t_begin) >> 4];
             if (pg >= 0) {
               const int64_t so = slot_scale(p.c, pg, kv, t);
-              b = p.c.ks[so] | (uint32_t)p.c.vs[so] << 8;
+              ks_next[x] = p.c.ks[so];
+              vs_next[x] = p.c.vs[so];
             }
           }
-          sc_next[x] = b;
         }
       }
     }
@@ -267,19 +275,25 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
 
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) {
-    if (E4M3) sc_cur[0] = sc_next[0], sc_cur[1] = sc_next[1];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) ks_cur[x] = ks_next[x], vs_cur[x] = vs_next[x];
     issue(i);
   }
   for (int i = 0; i < mine; ++i) {
     const int t0 = t_begin + (i * kStepWarps + warp) * TK;
     if (E4M3) {
       // this tile's scales to shared memory, where the lanes find the ones of their columns
-      const uint32_t now[2] = {sc_cur[0], sc_cur[1]};
-      sc_cur[0] = sc_next[0];
-      sc_cur[1] = sc_next[1];
+      int ek[2], ev[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        ek[x] = (int)ks_cur[x] - 127;
+        ev[x] = (int)vs_cur[x] - 127;
+        ks_cur[x] = ks_next[x];
+        vs_cur[x] = vs_next[x];
+      }
       int top = -1000;
 #pragma unroll
-      for (int x = 0; x < (TK + 31) / 32; ++x) top = max(top, (int)(now[x] >> 8) - 127);
+      for (int x = 0; x < (TK + 31) / 32; ++x) top = max(top, ev[x]);
       const int ref = max(ev_ref, __reduce_max_sync(0xffffffffu, top));
       if (ref != ev_ref) {
         const float f = pow2i(max(ev_ref - ref, -127));
@@ -289,8 +303,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
       }
 #pragma unroll
       for (int x = 0; x < (TK + 31) / 32; ++x) {
-        sh.scale_k[warp][x * 32 + lane] = pow2i((int)(now[x] & 255) - 127);
-        sh.scale_v[warp][x * 32 + lane] = pow2i(max((int)(now[x] >> 8) - 127 - ref, -127));
+        sh.scale_k[warp][x * 32 + lane] = pow2i(ek[x]);
+        sh.scale_v[warp][x * 32 + lane] = pow2i(max(ev[x] - ref, -127));
       }
     }
     cp_wait<kStages - 2>();
@@ -514,6 +528,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   constexpr int E = D / 32;
   float acc[E] = {}, sum = 0.f;
+#pragma unroll 8
   for (int i = 0; i < parts; ++i) {
     const float lse = p.part_lse[i * n + unit];
     const float w = lse == -INFINITY ? 0.f : ex2(lse - top);
@@ -542,16 +557,7 @@ cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s)
     if (e != cudaSuccess) return e;
   }
   if (std::max(p.a.step_parts, p.a.chunk_parts) > 1) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(256);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, attend_join_kernel<D>, p);
+    const cudaError_t e = launch_pdl(attend_join_kernel<D>, dim3(grid), 256, 0, s, p);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

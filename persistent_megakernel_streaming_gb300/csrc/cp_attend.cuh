@@ -10,6 +10,23 @@ namespace cache {
 using ptx::pdl_trigger;
 using ptx::pdl_wait;
 
+// A launch that may start before the kernel in front of it has ended (it waits
+// for that one where it needs to: pdl_wait).
+template <class K, class... A>
+cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Biased exponent of a bf16 pattern, 0 for infinities and NaN.
 __device__ __forceinline__ int finite_exp(uint32_t h) {
   const int e = (int)(h >> 7) & 255;

@@ -10,20 +10,23 @@
 // Warps 0-3 and 4-7: the softmax of tile 0 and tile 1, a thread a row. Warp
 // 12: one thread issues every MMA. Warp 13 brings pages in through tensor maps,
 // a lane a page. For each 128 positions S = Q K^T (128 x 128, fp32 in TMEM);
-// the softmax threads read their row of S twice (maximum, then weights: the
-// row does not fit their registers), write the weights as 16 bit over the S
-// they have read, and O += P V reads them from there. O stays in TMEM for the
-// whole pass; its reference maximum is only moved, and O rescaled, when a
-// row's maximum has risen by 2^kLazy over it, since the sum and the weights of
-// a part share the reference.
+// the softmax threads read their row of S in quarters, write the weights as 16
+// bit over the S they have read, and O += P V reads them from there. O stays in
+// TMEM for the whole pass. The reference of a row's weights is its first
+// tile's maximum; it is only moved, with all that it scales, when a later
+// score has risen by 2^kLazy over it, since the sum and the weights of a part
+// share the reference.
 //
 // bf16 pages land in the ring as the tensor core reads them. Tiles at the ends
 // of what the block's rows see, and tiles that only some of them see, pass
 // warps 8-11 first: values that nobody sees are zeroed (a page may hold
 // anything there), and values that some row must not see are looked over for
 // infinities and NaN. e4m3 pages land in a ring of their own and all pass
-// warps 8-11, which widen them to fp16 (exact) into the operand ring. Scales
-// and the handling of fp16's range are the step kernel's.
+// warps 8-11, which widen them to fp16 and multiply each row by its scale,
+// relative to the largest that the block has met and 2^kUp up: exact as long
+// as fp16 reaches, and what is lost below is 2^-25 of the largest row's
+// least bit. The power taken out of a tile's keys multiplies its scores, the
+// one of the values the result. Weights start at 2^kBias.
 #include "cp_attend.cuh"
 
 namespace cp {
@@ -45,7 +48,7 @@ template <int D, bool E4M3>
 struct Cfg {
   static constexpr int kOpBytes = kTile * D * 2;        // one operand tile
   static constexpr int kSlab = kTile * 128;             // 64 columns of it
-  static constexpr int kOps = D == 64 ? 8 : E4M3 ? 3 : 4;
+  static constexpr int kOps = D == 64 ? 8 : 4;
   static constexpr int kRawBytes = E4M3 ? kTile * D : 0;
   static constexpr int kRaws = E4M3 ? (D == 64 ? 4 : 2) : kOps;   // bf16: the operand ring itself
   static constexpr int kSmem = (2 + kOps) * kOpBytes + (E4M3 ? kRaws : 0) * kRawBytes + 1024;
@@ -54,14 +57,13 @@ struct Cfg {
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 
 struct ChunkShared {
-  uint64_t raw_full[8], raw_empty[8], op_full[8], op_empty[8];
+  uint64_t raw_full[8], raw_empty[8], op_full[8];
+  uint64_t done[4];   // rounds of the MMA warp
   uint64_t q_full, s_full[2], p_full[2], o_full;
   uint32_t tmem;
   int abort;       // a wait gave up
   int bad;         // a value that some row must not see is not finite
-  alignas(16) float fk[kScaleSlots][kTile];
-  alignas(16) float fv[kScaleSlots][kTile];
-  int vref[kScaleSlots];
+  int kref[kScaleSlots], vref[kScaleSlots];    // e4m3: exponents taken out of a tile's keys and values
 };
 
 // Bounded: after kWaitNs, or once another wait of the block gave up, false.
@@ -85,12 +87,27 @@ __device__ __forceinline__ bool wait_warp(ChunkShared& sh, uint32_t bar, uint32_
   return __all_sync(0xffffffffu, wait_bar(sh, bar, parity));
 }
 
+__device__ __forceinline__ uint32_t hf_mul(uint32_t x, uint32_t f) {
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f));
+  return *reinterpret_cast<const uint32_t*>(&y);
+}
+// Each lane that `need`s it waits for a barrier of its own.
+__device__ __forceinline__ bool wait_lanes(ChunkShared& sh, uint32_t bar, uint32_t parity, bool need) {
+  bool ok = !need || mb_try(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
+  if (!ok) ok = wait_bar(sh, bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ uint32_t hf_scale(uint32_t x, float f) {
+  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return hf_pack(y.x * f, y.y * f);
+}
 __device__ __forceinline__ uint64_t pack2(const uint32_t* x) { return pair_of(__uint_as_float(x[0]), __uint_as_float(x[1])); }
-__device__ __forceinline__ void unpack2(uint64_t y, uint32_t* x) {
-  float a, b;
-  split_pair(y, &a, &b);
-  x[0] = __float_as_uint(a);
-  x[1] = __float_as_uint(b);
+// Wait until the products that read operand load n are done: round i of the MMA warp reads K of tile i and V of
+// tile i - 1.
+__device__ __forceinline__ bool wait_done(ChunkShared& sh, int n) {
+  const int i = (n + 1) >> 1;
+  return wait_warp(sh, saddr(&sh.done[i & 3]), (i >> 2) & 1);
 }
 // Byte offset of 16-byte unit u (8 elements) of row r in an operand tile.
 __device__ __forceinline__ uint32_t op_at(int r, int u) {
@@ -108,14 +125,16 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
 
   // which sequence and which of its tile pairs: every warp counts the pairs, 32 sequences at a time
   int seq = -1, pair = 0;
+  Seq s{};
   {
     int before = 0;
     const int want = blockIdx.x / p.c.heads;
     for (int i0 = 0; i0 < p.b.n && seq < 0; i0 += 32) {
       int pairs = 0;
+      Seq one{};
       if (i0 + lane < p.b.n) {
-        const Seq s = seq_of(p.b, i0 + lane, p.c.status);
-        const int rows = s.n * p.group;
+        one = seq_of(p.b, i0 + lane, p.c.status);
+        const int rows = one.n * p.group;
         if (rows > kStepRows || !p.a.use_step) pairs = (rows + kPairRows - 1) / kPairRows;
       }
       int sum = pairs;
@@ -130,20 +149,30 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
         seq = i0 + at;
         const int end = __shfl_sync(0xffffffffu, before + sum, at);
         pair = end - 1 - want;            // the later rows of a sequence see more: they start first
+        s.row0 = __shfl_sync(0xffffffffu, one.row0, at);
+        s.n = __shfl_sync(0xffffffffu, one.n, at);
+        s.len = __shfl_sync(0xffffffffu, one.len, at);
+        s.first = __shfl_sync(0xffffffffu, one.first, at);
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
   }
-  if (seq < 0) return;
+  pdl_trigger();
+  if (seq < 0) {
+    pdl_wait();
+    return;
+  }
   const int kv = blockIdx.x % p.c.heads, part = blockIdx.y;
-  const Seq s = seq_of(p.b, seq, p.c.status);
   const int nrows = s.n * p.group;
   const int row0 = pair * kPairRows;
   const int rows_here = min(kPairRows, nrows - row0);
   auto pos_of = [&](int i) { return s.first + min(i, nrows - 1) / p.group; };
   const Range range = item_range(p, pos_of(row0), pos_of(row0 + rows_here - 1), s.len, kChunkAlign);
   const int parts = parts_of(range, p.a.chunk_chunk);
-  if (part >= max(parts, 1)) return;
+  if (part >= max(parts, 1)) {
+    pdl_wait();
+    return;
+  }
   const bool whole = parts <= 1;
   const int t_begin = range.base + part * p.a.chunk_chunk;
   const int t_end = min(t_begin + p.a.chunk_chunk, range.hi);
@@ -172,23 +201,18 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
   uint8_t* ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_s = saddr(ops), op_s = q_s + 2 * C::kOpBytes, raw_s = E4M3 ? op_s + NO * C::kOpBytes : op_s;
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < NR; ++i) {
-      mb_init(saddr(&sh.raw_full[i]), 1);
-      mb_init(saddr(&sh.raw_empty[i]), kHelpers / 32);
+  if (warp == kLoadWarp) {               // a lane a barrier
+    if (lane < 8) mb_init(saddr(&sh.raw_full[lane]), 1);
+    else if (lane < 16) mb_init(saddr(&sh.raw_empty[lane - 8]), kHelpers / 32);
+    else if (lane < 24) mb_init(saddr(&sh.op_full[lane - 16]), kHelpers);
+    else if (lane < 28) mb_init(saddr(&sh.done[lane - 24]), 1);
+    if (lane < 2) {
+      mb_init(saddr(&sh.s_full[lane]), 1);
+      mb_init(saddr(&sh.p_full[lane]), 4);
     }
-    for (int i = 0; i < NO; ++i) {
-      mb_init(saddr(&sh.op_full[i]), kHelpers);
-      mb_init(saddr(&sh.op_empty[i]), 1);
-    }
-    mb_init(saddr(&sh.q_full), 256);
-    for (int i = 0; i < 2; ++i) {
-      mb_init(saddr(&sh.s_full[i]), 1);
-      mb_init(saddr(&sh.p_full[i]), 128);
-    }
-    mb_init(saddr(&sh.o_full), 1);
-    sh.abort = 0;
-    sh.bad = 0;
+    if (lane == 2) mb_init(saddr(&sh.q_full), kPairRows);
+    if (lane == 3) mb_init(saddr(&sh.o_full), 1);
+    if (lane == 4) sh.abort = sh.bad = 0;
     mb_fence_init();
   }
   if (warp == kMmaWarp) {
@@ -209,42 +233,44 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
   float l = 0.f, m = -INFINITY;
   int vr = 0;
   constexpr float kBias = E4M3 ? 8.f : 0.f;
+  constexpr int kUp = 6;                                 // operands of e4m3 reach 448 * 2^kUp: inside fp16
   constexpr float kLazy = E4M3 ? 6.f : 8.f;              // weights reach 2^(kBias + kLazy): inside fp16
 
   if (warp < kHelper0) {
     // ---------------------------------------------------------------- softmax
-    float rs = p.scale_log2;
+    float row_scale = p.scale_log2;
     {
-      const uint32_t dst = q_s + i * C::kOpBytes;
-      const int r = (warp & 3) * 32 + lane;
-      const uint16_t* qp = p.q + out_row * p.q_row + (int64_t)head * p.q_head;
-      if (!E4M3) {
+      // the warp's 32 rows, a row's units side by side; e4m3's q in fp16 times a power of two of its row
+      constexpr int UPR = D / 8, RPI = 32 / UPR, N = 32 / RPI;
+      const int u = lane % UPR, base = (warp & 3) * 32;
+      uint4 x[N];
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u) {
-          const uint4 x = mine ? *reinterpret_cast<const uint4*>(qp + u * 8) : make_uint4(0, 0, 0, 0);
-          st_shared_v4u(dst + op_at(r, u), x);
-        }
-      } else {
-        uint4 x[D / 8];
-        int top = 0;
+      for (int k = 0; k < N; ++k) {
+        const int r = row0 + i * kTile + base + k * RPI + lane / UPR;
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (r < nrows)
+          x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.row0 + r / p.group) * p.q_row +
+                                                 (int64_t)(kv * p.group + r % p.group) * p.q_head + u * 8);
+      }
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u) {
-          x[u] = mine ? *reinterpret_cast<const uint4*>(qp + u * 8) : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      for (int k = 0; k < N; ++k) {
+        if (E4M3) {
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          int top = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) top = max(top, max(finite_exp(w[k] & 0xffffu), finite_exp(w[k] >> 16)));
-        }
-        const int e = min(max(top - 127, -100), 100);
-        const float inv = pow2i(-e);
-        rs = pow2i(e);
+          for (int q = 0; q < 4; ++q) top = max(top, max(finite_exp(w[q] & 0xffffu), finite_exp(w[q] >> 16)));
 #pragma unroll
-        for (int u = 0; u < D / 8; ++u) {
-          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          for (int o = UPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = min(max(top - 127, -100), 100);
+          const float inv = pow2i(-e);
           uint32_t y[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = hf_pack(bf_lo(w[k]) * inv, bf_hi(w[k]) * inv);
-          st_shared_v4u(dst + op_at(r, u), make_uint4(y[0], y[1], y[2], y[3]));
+          for (int q = 0; q < 4; ++q) y[q] = hf_pack(bf_lo(w[q]) * inv, bf_hi(w[q]) * inv);
+          x[k] = make_uint4(y[0], y[1], y[2], y[3]);
+          const int mine_e = __shfl_sync(0xffffffffu, e, (lane % RPI) * UPR);      // of row k * RPI + lane % RPI
+          if (lane / RPI == k) row_scale = p.scale_log2 * pow2i(mine_e);
         }
+        st_shared_v4u(q_s + i * C::kOpBytes + op_at(base + k * RPI + lane / UPR, u), x[k]);
       }
       fence_proxy_async_smem();
       mb_arrive(saddr(&sh.q_full));
@@ -255,83 +281,85 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     const uint32_t s_t = tmem + lanes + kTmemS + i * kTile, o_t = tmem + lanes + kTmemO + i * D;
     const int j0 = i ? jb[1] : jb[0], j1 = i ? je[1] : je[0];
     const int see_lo = i ? all_lo[1] : all_lo[0], see_hi = i ? all_hi[1] : all_hi[0];
-    const uint64_t rs2 = pair_of(rs, rs);
     uint64_t sum[2] = {0, 0};              // two pairs of partial sums
+    auto rescale = [&](float f) {          // of O; the products before this tile's are done
+      tm_wait_st();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float v[32];
+        tm_ld32(o_t + c, v);
+#pragma unroll
+        for (int x = 0; x < 32; ++x) v[x] *= f;
+        tm_st32(o_t + c, v);
+      }
+    };
     for (int j = j0; j < j1; ++j) {
       const int n = j - j0;
       const int t0 = t_begin + j * kTile;
       if (!wait_warp(sh, saddr(&sh.s_full[i]), n & 1)) break;
       if (E4M3 && !wait_warp(sh, saddr(&sh.op_full[(2 * j + 1) % NO]), ((2 * j + 1) / NO) & 1)) break;   // its scales
       tm_fence_after();
-      const float* fk = sh.fk[j % kScaleSlots];
-      const float* fv = sh.fv[j % kScaleSlots];
       const int vn = E4M3 ? sh.vref[j % kScaleSlots] : 0;
       const bool edge = t0 < see_lo || t0 + kTile > see_hi;
+      const float rs = E4M3 ? row_scale * pow2i(max(sh.kref[j % kScaleSlots] - kUp, -126)) : p.scale_log2;
+      const uint64_t rs2 = pair_of(rs, rs);
       uint32_t x0[32], x1[32];
-      // 32 scores in place, times their keys' scales, masked ones minus infinity
+      // 32 scores in place, masked ones minus infinity
       auto ready = [&](uint32_t* x, int c) {
-        if (E4M3) {
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            float4 f = *reinterpret_cast<const float4*>(fk + c + k);
-            unpack2(mul2(pack2(x + k), pair_of(f.x, f.y)), x + k);
-            unpack2(mul2(pack2(x + k + 2), pair_of(f.z, f.w)), x + k + 2);
-          }
-        }
         if (edge) {
 #pragma unroll
           for (int k = 0; k < 32; ++k)
             if (t0 + c + k < lo || t0 + c + k >= hi) x[k] = 0xff800000u;
         }
       };
-      auto top_of = [&](const uint32_t* x, float top) {
-        float a = top, b = __uint_as_float(x[0]);
+      auto top_of = [&](const uint32_t* x) {
+        float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
 #pragma unroll
-        for (int k = 1; k < 31; k += 2) {
+        for (int k = 2; k < 32; k += 2) {
           a = fmaxf(a, __uint_as_float(x[k]));
           b = fmaxf(b, __uint_as_float(x[k + 1]));
         }
-        return fmaxf(fmaxf(a, b), __uint_as_float(x[31]));
+        return fmaxf(a, b);
       };
-      float top = -INFINITY;
-      tm_ld32_start(s_t, x0);
-#pragma unroll
-      for (int c = 0; c < kTile; c += 64) {
-        tm_ld32_wait(x0);
-        tm_ld32_start(s_t + c + 32, x1);
-        ready(x0, c);
-        top = top_of(x0, top);
-        tm_ld32_wait(x1);
-        tm_ld32_start(s_t + (c + 64) % kTile, x0);       // the last one is the second pass's first
-        ready(x1, c + 32);
-        top = top_of(x1, top);
-      }
-      top *= rs;
-      if (__any_sync(0xffffffffu, top > m + kLazy || vn != vr)) {
-        const float mn = fmaxf(m, top);
-        float f = mn == m ? 1.f : ex2(m - mn);
-        const uint64_t f2 = pair_of(f, f);
-        sum[0] = mul2(sum[0], f2);
-        sum[1] = mul2(sum[1], f2);
-        m = mn;
-        if (E4M3) f *= pow2i(max(vr - vn, -127));
+      if (E4M3 && vn != vr) {              // a larger value scale: what is summed so far shrinks next to it
+        if (n > 0) rescale(pow2i(max(vr - vn, -127)));
         vr = vn;
-        if (n > 0) {
-          tm_ld32_wait(x0);
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float v[32];
-            tm_ld32(o_t + c, v);
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] *= f;
-            tm_st32(o_t + c, v);
-          }
-        }
       }
-      const float ref = (m == -INFINITY ? 0.f : m) - kBias;
-      const uint64_t ref2 = pair_of(-ref, -ref);
+      if (n == 0) {                        // the first tile sets the reference
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          tm_ld32_start(s_t + c, x0);
+          tm_ld32_wait(x0);
+          ready(x0, c);
+          top = fmaxf(top, top_of(x0));
+        }
+        m = top * rs;
+      }
+      // 32 weights and their sum; scores risen too far over the reference move it, with all that it scales
       auto weigh = [&](uint32_t* x, int c) {
         ready(x, c);
+        const float top = top_of(x) * rs;
+        if (__any_sync(0xffffffffu, top > m + kLazy)) {
+          const float mn = fmaxf(m, top);
+          const float f = mn == m ? 1.f : ex2(m - mn);
+          const uint64_t f2 = pair_of(f, f);
+          sum[0] = mul2(sum[0], f2);
+          sum[1] = mul2(sum[1], f2);
+          m = mn;
+          if (n > 0) rescale(f);
+          tm_wait_st();
+#pragma unroll 1
+          for (int d = 0; d < c / 2; d += 16) {          // this tile's weights so far
+            uint32_t w[16];
+            tm_ld16_raw(s_t + d, w);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = E4M3 ? hf_scale(w[k], f) : bf_pack(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
+            tm_st16(s_t + d, w);
+          }
+        }
+        const float ref = (m == -INFINITY ? 0.f : m) - kBias;
+        const uint64_t ref2 = pair_of(-ref, -ref);
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -340,20 +368,15 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
           split_pair(fma2(pack2(x + k + 2), rs2, ref2), y + 2, y + 3);
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = ex2(y[q]);
-          uint64_t a = pair_of(y[0], y[1]), b = pair_of(y[2], y[3]);
-          sum[0] = add2(sum[0], a);
-          sum[1] = add2(sum[1], b);
-          if (E4M3) {
-            const float4 f = *reinterpret_cast<const float4*>(fv + c + k);
-            split_pair(mul2(a, pair_of(f.x, f.y)), y, y + 1);
-            split_pair(mul2(b, pair_of(f.z, f.w)), y + 2, y + 3);
-          }
+          sum[0] = add2(sum[0], pair_of(y[0], y[1]));
+          sum[1] = add2(sum[1], pair_of(y[2], y[3]));
           w[k / 2] = E4M3 ? hf_pack(y[0], y[1]) : bf_pack(y[0], y[1]);
           w[k / 2 + 1] = E4M3 ? hf_pack(y[2], y[3]) : bf_pack(y[2], y[3]);
         }
         tm_st16(s_t + c / 2, w);
       };
-#pragma unroll
+      tm_ld32_start(s_t, x0);
+#pragma unroll 1
       for (int c = 0; c < kTile; c += 64) {
         tm_ld32_wait(x0);
         tm_ld32_start(s_t + c + 32, x1);
@@ -364,7 +387,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
       }
       tm_wait_st();
       tm_fence_before();
-      mb_arrive(saddr(&sh.p_full[i]));
+      __syncwarp();
+      if (lane == 0) mb_arrive(saddr(&sh.p_full[i]));
     }
     float y[4];
     split_pair(sum[0], y, y + 1);
@@ -396,74 +420,82 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
       constexpr int UPR = D / 16, RPI = kHelpers / UPR, N = kTile / RPI;
       const int u = tid % UPR, r0 = tid / UPR;
       const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
-      // each warp has the scale bytes (key | value << 8) of all of a tile: positions t0 + 32 h + lane
-      uint32_t scale[4];
-      auto load_scales = [&](int j) {
-        int pg = -1;
-        const int t8 = t_begin + j * kTile + (lane & 7) * 16;
-        if (j < ntiles && t8 < t_end) pg = page_of(table, p.b.width, p.c.pages, p.c.page_shift, t8);
+      // each warp has the scale bytes of all of a tile: positions t0 + 32 h + lane. Pages are asked for two tiles
+      // ahead and scales one, and nothing is done with them before their turn.
+      uint8_t key_scale[4], value_scale[4];
+      auto page_at = [&](int j) {
+        const int t = t_begin + j * kTile + (lane & 7) * 16;
+        return j < ntiles && t < t_end && (t >> p.c.page_shift) < p.b.width ? table[t >> p.c.page_shift] : -1;
+      };
+      auto load_scales = [&](int j, int pg) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const int t = t_begin + j * kTile + h * 32 + lane;
           const int page = __shfl_sync(0xffffffffu, pg, h * 2 + lane / 16);
-          scale[h] = 0;
-          if (page >= 0 && t >= range.lo && t < t_end) {
+          key_scale[h] = value_scale[h] = 0;
+          if ((uint32_t)page < (uint32_t)p.c.pages && j < ntiles && t >= range.lo && t < t_end) {
             const int64_t so = slot_scale(p.c, page, kv, t);
-            scale[h] = p.c.ks[so] | (uint32_t)p.c.vs[so] << 8;
+            key_scale[h] = p.c.ks[so];
+            value_scale[h] = p.c.vs[so];
           }
         }
       };
-      int vref = -127;
-      load_scales(0);
+      int pg = page_at(1);
+      load_scales(0, page_at(0));
+      int kref = -127, vref = -127;
       for (int n = 0; n < 2 * ntiles; ++n) {
         const int j = n >> 1, is_v = n & 1, t0 = t_begin + j * kTile;
         if (!wait_warp(sh, saddr(&sh.raw_full[n % NR]), (n / NR) & 1)) break;
-        if (n >= NO && !wait_warp(sh, saddr(&sh.op_empty[n % NO]), ((n / NO) & 1) ^ 1)) break;
+        if (n >= NO && !wait_done(sh, n - NO)) break;
         const uint32_t src = raw_s + (n % NR) * C::kRawBytes + u * 16, dst = op_s + (n % NO) * C::kOpBytes;
         const bool ends = is_v && (t0 < range.lo || t0 + kTile > t_end);
         const bool look = is_v && (t0 < pair_lo || t0 + kTile > pair_hi);
+        // every row by its scale next to the largest so far: a power of two, exact where fp16 reaches
+        int e4[4], top = -127;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          e4[h] = (int)(is_v ? value_scale[h] : key_scale[h]) - 127;
+          top = max(top, e4[h]);
+        }
+        int& ref = is_v ? vref : kref;
+        ref = max(ref, __reduce_max_sync(0xffffffffu, top));
+        if (tid == 0) (is_v ? sh.vref : sh.kref)[j % kScaleSlots] = ref;
         uint4 x[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
+        for (int k = 0; k < N; ++k)
           asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                        : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
                        : "r"(src + (r0 + k * RPI) * D)
                        : "memory");
-        }
-        __syncwarp();
-        if (lane == 0) mb_arrive(saddr(&sh.raw_empty[n % NR]));
+        if (look)
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int r = r0 + k * RPI;
+            if (ends && (t0 + r < range.lo || t0 + r >= t_end)) x[k] = make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) bad |= __vcmpeq4(w[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+          }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const int r = r0 + k * RPI;
-          if (ends && (t0 + r < range.lo || t0 + r >= t_end)) x[k] = make_uint4(0, 0, 0, 0);
+          const int e = max(__shfl_sync(0xffffffffu, e4[(k * RPI) / 32], r % 32) - ref + kUp, -25);
+          const uint32_t f = hf_pack(pow2i(e), pow2i(e));
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          if (look)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) bad |= __vcmpeq4(w[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
           uint32_t y[8];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            y[2 * q] = e4m3x2_f16x2(w[q] & 0xffffu);
-            y[2 * q + 1] = e4m3x2_f16x2(w[q] >> 16);
+            y[2 * q] = hf_mul(e4m3x2_f16x2(w[q] & 0xffffu), f);
+            y[2 * q + 1] = hf_mul(e4m3x2_f16x2(w[q] >> 16), f);
           }
           st_shared_v4u(dst + op_at(r, 2 * u), make_uint4(y[0], y[1], y[2], y[3]));
           st_shared_v4u(dst + op_at(r, 2 * u + 1), make_uint4(y[4], y[5], y[6], y[7]));
         }
-        const int slot = j % kScaleSlots, w4 = warp & 3;
-        if (!is_v) {
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            if (h == w4) sh.fk[slot][h * 32 + lane] = pow2i((int)(scale[h] & 255) - 127) * p.scale_log2;
-        } else {
-          int ev[4];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) ev[h] = (int)(scale[h] >> 8) - 127;
-          vref = max(vref, __reduce_max_sync(0xffffffffu, max(max(ev[0], ev[1]), max(ev[2], ev[3]))));
-          if (tid == 0) sh.vref[slot] = vref;
-#pragma unroll
-          for (int h = 0; h < 4; ++h)
-            if (h == w4) sh.fv[slot][h * 32 + lane] = pow2i(max(ev[h] - vref, -127));
-          load_scales(j + 1);
+        __syncwarp();
+        if (lane == 0) mb_arrive(saddr(&sh.raw_empty[n % NR]));
+        if (is_v) {
+          load_scales(j + 1, pg);
+          pg = page_at(j + 2);
         }
         fence_proxy_async_smem();
         mb_arrive(saddr(&sh.op_full[n % NO]));
@@ -488,9 +520,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     int pg = page_at(0);
     for (int n = 0; n < 2 * ntiles; ++n) {
       const int j = n >> 1, is_v = n & 1;
-      if (n >= NR &&
-          !wait_warp(sh, E4M3 ? saddr(&sh.raw_empty[n % NR]) : saddr(&sh.op_empty[n % NO]), ((n / NR) & 1) ^ 1))
-        break;
+      if (n >= NR && !(E4M3 ? wait_warp(sh, saddr(&sh.raw_empty[n % NR]), ((n / NR) & 1) ^ 1) : wait_done(sh, n - NR))) break;
       const uint32_t bar = saddr(&sh.raw_full[n % NR]);
       if (lane == 0) mb_expect(bar, E4M3 ? C::kRawBytes : C::kOpBytes);
       __syncwarp();
@@ -505,49 +535,74 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     }
     // what was asked for lands before the block may end, whatever ended the loop
     for (int n = max(0, 2 * ntiles - NR); n < 2 * ntiles; ++n) wait_warp(sh, saddr(&sh.raw_full[n % NR]), (n / NR) & 1);
-  } else if (warp == kMmaWarp && lane == 0) {
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
+    // The instructions between two products matter: about four queued ones cover them, and one takes nearly as long
+    // to issue as to run. The warp stays together and one lane issues, so that descriptors are uniform registers'.
+    const uint32_t lead = lane == 0;
     const uint32_t id_s = idesc_m128(kTile, E4M3, false), id_o = idesc_m128(D, E4M3, true);
-    bool ok = wait_bar(sh, saddr(&sh.q_full), 0);
-    for (int j = -1; ok && j < ntiles; ++j) {
-      const int nv = 2 * j + 1, nk = 2 * j + 2;       // V of tile j, K of tile j + 1
-      if (j >= 0) ok = wait_bar(sh, saddr(&sh.op_full[nv % NO]), (nv / NO) & 1);
-      bool k_here = j + 1 >= ntiles;
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const int tiles = __shfl_sync(0xffffffffu, ntiles, 0);
+    const int b0 = __shfl_sync(0xffffffffu, jb[0], 0), b1 = __shfl_sync(0xffffffffu, jb[1], 0);
+    const int e0 = __shfl_sync(0xffffffffu, je[0], 0), e1 = __shfl_sync(0xffffffffu, je[1], 0);
+    const uint32_t ops = __shfl_sync(0xffffffffu, op_s, 0), q0 = __shfl_sync(0xffffffffu, q_s, 0);
+    const uint64_t q_desc = sdesc_sw128(q0), k_desc = sdesc_sw128(ops), v_desc = sdesc_sw128_cols(ops, C::kSlab);
+    constexpr uint32_t kOpDesc = C::kOpBytes >> 4;
+    const uint32_t ops_full = saddr(sh.op_full), k_full = E4M3 ? ops_full : saddr(sh.raw_full);
+    const uint32_t s_full = saddr(sh.s_full), p_full = saddr(sh.p_full), done = saddr(sh.done);
+    auto scores = [&](int x, int slot) {
+      const uint64_t q = q_desc + x * kOpDesc, k0 = k_desc + slot * kOpDesc;
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (ok && j >= jb[x] && j < je[x]) {
-          ok = wait_bar(sh, saddr(&sh.p_full[x]), (j - jb[x]) & 1);
-          tm_fence_after();
-          if (ok) {
-            const uint32_t v = op_s + (nv % NO) * C::kOpBytes;
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              tm_mma_ts(tmem + kTmemO + x * D, tmem + kTmemS + x * kTile + k * 8, sdesc_sw128_cols(v + k * 2048, C::kSlab), id_o,
-                        j > jb[x] || k > 0);
-          }
-        }
-        if (ok && !k_here) {
-          ok = wait_bar(sh, E4M3 ? saddr(&sh.op_full[nk % NO]) : saddr(&sh.raw_full[nk % NO]), (nk / NO) & 1);
-          k_here = true;
-        }
-        if (ok && j + 1 >= jb[x] && j + 1 < je[x]) {
-          const uint32_t a = q_s + x * C::kOpBytes, b = op_s + (nk % NO) * C::kOpBytes;
-          tm_fence_after();
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint32_t at = (k / 4) * C::kSlab + (k % 4) * 32;
-            tm_mma(tmem + kTmemS + x * kTile, sdesc_sw128(a + at), sdesc_sw128(b + at), id_s, k > 0);
-          }
-          tm_commit(saddr(&sh.s_full[x]));
-        }
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = ((k / 4) * C::kSlab + (k % 4) * 32) >> 4;
+        tm_mma_lead(lead, tm + kTmemS + x * kTile, q + at, k0 + at, id_s, k > 0);
       }
+      tm_commit_lead(lead, s_full + 8 * x);
+    };
+    auto values = [&](int x, int slot, uint32_t more) {
+      const uint64_t v = v_desc + slot * kOpDesc;
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k)
+        tm_mma_ts_lead(lead, tm + kTmemO + x * D, tm + kTmemS + x * kTile + k * 8, v + k * (2048 >> 4), id_o, k ? 1u : more);
+    };
+    // slots of V of tile j and K of tile j + 1, the parity of their turn round the ring, and of the streams' turns
+    int sv = NO - 1, sk = 0;
+    uint32_t rv = 1, rk = 0, rp0 = 0, rp1 = 0;
+    bool ok = wait_warp(sh, saddr(&sh.q_full), 0);
+    for (int j = -1; ok && j < tiles; ++j) {
+      const bool v0 = j >= b0 && j < e0, v1 = j >= b1 && j < e1;                     // streams with values, and scores
+      const bool s0 = j + 1 >= b0 && j + 1 < e0, s1 = j + 1 >= b1 && j + 1 < e1;
+      // one wait for all that stream 0 needs, a lane a barrier
+      const uint32_t bar = lane == 0 ? ops_full + 8 * sv : lane == 1 ? k_full + 8 * sk : p_full;
+      const uint32_t par = lane == 0 ? rv : lane == 1 ? rk : rp0;
+      ok = wait_lanes(sh, bar, par, lane == 0 ? j >= 0 : lane == 1 ? j + 1 < tiles : lane == 2 && v0);
       if (!ok) break;
-      if (j >= 0) tm_commit(saddr(&sh.op_empty[nv % NO]));
-      if (j + 1 < ntiles) tm_commit(saddr(&sh.op_empty[nk % NO]));
+      tm_fence_after();
+      if (v0) {
+        values(0, sv, j > b0);
+        rp0 ^= 1;
+      }
+      if (s0) scores(0, sk);
+      if (v1) {
+        ok = wait_warp(sh, p_full + 8, rp1);
+        if (!ok) break;
+        tm_fence_after();
+        values(1, sv, j > b1);
+        rp1 ^= 1;
+      }
+      if (s1) scores(1, sk);
+      tm_commit_lead(lead, done + 8 * ((j + 1) & 3));
+      // loads alternate K, V: V of tile j + 1 follows K of tile j + 1
+      sv = sk + 1;
+      rv = rk;
+      if (sv == NO) sv = 0, rv ^= 1;
+      sk = sv + 1;
+      rk = rv;
+      if (sk == NO) sk = 0, rk ^= 1;
     }
-    tm_commit(saddr(&sh.o_full));
+    tm_commit_lead(lead, saddr(&sh.o_full));
     // after a wait that gave up, the products in flight still end before TMEM is given back
-    for (int x = 0; x < (1 << 20) && !mb_try(saddr(&sh.o_full), 0); ++x) {
+    for (int x = 0; x < (1 << 20) && !__all_sync(0xffffffffu, mb_try(saddr(&sh.o_full), 0)); ++x) {
     }
   }
   __syncwarp();
@@ -559,28 +614,36 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
   if (!failed && sh.bad) {
     plain_rows<D, E4M3>(p, s, seq, kv, row0, row0 + rows_here, t_begin, t_end, part, whole, warp, kThreadsC / 32);
   } else if (!failed && warp < kHelper0) {
+    // rows leave through the ring's memory, so that a row is written at once and not by its thread piece by piece
     const uint32_t o_t = tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + i * D;
     const bool any = i ? je[1] > jb[1] : je[0] > jb[0];
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const float e = E4M3 ? pow2i(min(max(vr, -126), 127)) : 1.f;
+    const float e = E4M3 ? pow2i(min(max(vr - kUp, -126), 127)) : 1.f;
+    constexpr int kPitch = D + 4;
+    static_assert(8 * 32 * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the eight warps' rows fit the operands' memory");
+    float* stage = reinterpret_cast<float*>(ops) + warp * 32 * kPitch;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float v[32];
       if (any) tm_ld32(o_t + c, v);
 #pragma unroll
-      for (int x = 0; x < 32; ++x) v[x] = any && inv != 0.f ? v[x] * inv * e : 0.f;
-      if (mine && whole) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + out_row * p.o_row + (int64_t)head * p.o_head + c);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          dst[x] = make_uint4(bf_pack(v[8 * x], v[8 * x + 1]), bf_pack(v[8 * x + 2], v[8 * x + 3]),
-                              bf_pack(v[8 * x + 4], v[8 * x + 5]), bf_pack(v[8 * x + 6], v[8 * x + 7]));
-      } else if (mine) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) store4<D>(p, part, false, out_row, head, c + 4 * x, v + 4 * x);
+      for (int x = 0; x < 32; x += 4) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (any && inv != 0.f) y = make_float4(v[x] * inv * e, v[x + 1] * inv * e, v[x + 2] * inv * e, v[x + 3] * inv * e);
+        *reinterpret_cast<float4*>(stage + lane * kPitch + c + x) = y;
       }
     }
     if (mine && !whole) store_lse(p, part, out_row, head, l == 0.f ? -INFINITY : m + log2f(l) - kBias);
+    __syncwarp();
+    constexpr int LPR = D / 4, RPI = 32 / LPR;
+    const int first = row0 + i * kTile + (warp & 3) * 32;
+#pragma unroll 4
+    for (int k = 0; k < 32 / RPI; ++k) {
+      const int r = k * RPI + lane / LPR, d = lane % LPR * 4;
+      if (first + r < nrows)
+        store4<D>(p, part, whole, s.row0 + (first + r) / p.group, kv * p.group + (first + r) % p.group, d,
+                  stage + r * kPitch + d);
+    }
     tm_fence_before();
   }
   __syncthreads();
@@ -588,6 +651,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     tm_fence_after();
     tm_dealloc(tmem, kTmemCols);
   }
+  pdl_wait();            // this grid's end stands for the step kernel's too
 }
 
 }  // namespace
@@ -606,8 +670,12 @@ cudaError_t prepare_attend_chunk() {
 template <int D, bool E4M3>
 static cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   const dim3 grid((unsigned)(p.c.heads * chunk_pairs(p.b, p.group)), p.a.chunk_parts);
-  attend_chunk_kernel<D, E4M3><<<grid, kThreadsC, Cfg<D, E4M3>::kSmem, s>>>(p, maps);
-  return cudaGetLastError();
+  if (!p.a.use_step) {
+    attend_chunk_kernel<D, E4M3><<<grid, kThreadsC, Cfg<D, E4M3>::kSmem, s>>>(p, maps);
+    return cudaGetLastError();
+  }
+  // behind the step kernel, whose results it does not need: it may fill the SMs that one leaves
+  return launch_pdl(attend_chunk_kernel<D, E4M3>, grid, kThreadsC, Cfg<D, E4M3>::kSmem, s, p, maps);
 }
 cudaError_t launch_attend_chunk(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s) {
   if (head_dim == 128) return e4m3 ? launch<128, true>(p, maps, s) : launch<128, false>(p, maps, s);

@@ -108,7 +108,7 @@ __device__ __forceinline__ float ex2(float x) {
 // ------------------------------------------------------------------ attention
 // How a call is cut up, from the host's bounds alone (so that a captured call
 // keeps it): sequences of at most kStepRows rows a kv head go to the step
-// kernel, the others to the chunk kernel. An item (a sequence, or a tile of its
+// kernel if it runs, the others to the chunk kernel. An item (a sequence, or a tile of its
 // rows) whose visible positions are more than `chunk` is cut into parts of
 // that many, each a block's; a last kernel joins the parts.
 constexpr int kStepRows = 16;

@@ -228,7 +228,14 @@ __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The same load without its wait, and the wait naming the registers so that
+__device__ __forceinline__ void tm_ld16_raw(uint32_t taddr, uint32_t* r) {
+  float v[16];
+  tm_ld16(taddr, v);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
+}
+
+// The 32-column load without its wait, and the wait naming the registers so that
 // nothing reads them before it (it waits for every load of the thread).
 __device__ __forceinline__ void tm_ld32_start(uint32_t taddr, uint32_t* r) {
   asm volatile(
@@ -292,14 +299,37 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const float* v) {
   tm_st16(taddr + 16, r + 16);
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// D[tmem] (+)= A[tmem] * B[smem desc], 16-bit inputs, fp32 accumulate. A holds two
-// consecutive elements of its row a 32-bit column, row i in lane i.
-__device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The products and their commit as one lane of a warp issues them (`lead` of
+// the others is 0), predicated inside the instruction's own block: the warp
+// stays together, so that addresses and descriptors stay in uniform registers.
+// A in shared memory, or in tensor memory: two consecutive elements of its row
+// a 32-bit column, row i in lane i.
+__device__ __forceinline__ void tm_mma_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred P;\n\t"
+      "{\n\t.reg .pred P, L;\n\t"
       "setp.ne.b32 P, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 L, %5, 0;\n\t"
+      "@L tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, P;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tm_mma_ts_lead(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred P, L;\n\t"
+      "setp.ne.b32 P, %4, 0;\n\t"
+      "setp.ne.b32 L, %5, 0;\n\t"
+      "@L tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tm_commit_lead(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred L;\n\t"
+      "setp.ne.b32 L, %1, 0;\n\t"
+      "@L tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
       : "memory");
 }
 
