@@ -7,22 +7,27 @@
 // 256 rows, and the two keep the tensor core busy in turn: while one tile's
 // softmax runs, the other's products do.
 //
-// Warps 0-3 and 4-7: the softmax of tile 0 and tile 1, a thread a row. Warp
-// 12: one thread issues every MMA. Warp 13 brings pages in through tensor maps,
-// a lane a page. For each 128 positions S = Q K^T (128 x 128, fp32 in TMEM);
-// the softmax threads read their row of S in quarters, write the weights as 16
-// bit over the S they have read, and O += P V reads them from there. O stays in
+// Warps 0-7 and 8-15: the softmax of tile 0 and tile 1, two threads a row with
+// 64 of a tile's 128 positions each (more warps at less work each: what one
+// tile's softmax takes is what the other tile's products have to cover). Warps
+// 20 and 21 issue the MMAs of tile 0 and tile 1: the tensor core stands still
+// while an issuer does anything else (measured: nothing of a gap between two
+// products of one warp is hidden, nearly all of it behind another warp's).
+// Warp 22 brings pages in through tensor maps, a lane a page. For each 128 positions S = Q K^T (128 x 128, fp32 in
+// TMEM); the softmax threads read their part of it twice (maximum, then
+// weights: it does not fit their registers), write the weights as 16 bit over
+// the S that they have read, and O += P V reads them from there. O stays in
 // TMEM for the whole pass. The reference of a row's weights is its first
-// tile's maximum; it is only moved, with all that it scales, when a later
-// score has risen by 2^kLazy over it, since the sum and the weights of a part
-// share the reference.
+// tile's maximum; it is only moved, and O rescaled, when a later score has
+// risen by 2^kLazy over it, since the sum and the weights of a part share the
+// reference.
 //
 // bf16 pages land in the ring as the tensor core reads them. Tiles at the ends
 // of what the block's rows see, and tiles that only some of them see, pass
-// warps 8-11 first: values that nobody sees are zeroed (a page may hold
+// warps 16-19 first: values that nobody sees are zeroed (a page may hold
 // anything there), and values that some row must not see are looked over for
 // infinities and NaN. e4m3 pages land in a ring of their own and all pass
-// warps 8-11, which widen them to fp16 and multiply each row by its scale,
+// warps 16-19, which widen them to fp16 and multiply each row by its scale,
 // relative to the largest that the block has met and 2^kUp up: exact as long
 // as fp16 reaches, and what is lost below is 2^-25 of the largest row's
 // least bit. The power taken out of a tile's keys multiplies its scores, the
@@ -36,10 +41,11 @@ namespace {
 using namespace ptx;
 
 constexpr int kTile = 128;             // rows of a tile, and positions of one
-constexpr int kThreadsC = 448;
-constexpr int kHelper0 = 8;            // first of four helper warps
+constexpr int kThreadsC = 704;
+constexpr int kSoftWarps = 16;         // softmax: eight a tile of rows
+constexpr int kHelper0 = 16;           // first of four helper warps
 constexpr int kHelpers = 128;
-constexpr int kMmaWarp = 12, kLoadWarp = 13;
+constexpr int kMmaWarp = 20, kLoadWarp = 21;
 constexpr int kScaleSlots = 8;         // tiles whose scales are held: more than the ring's
 constexpr long long kWaitNs = 2000000000ll;
 
@@ -51,7 +57,7 @@ struct Cfg {
   static constexpr int kOps = D == 64 ? 8 : 4;
   static constexpr int kRawBytes = E4M3 ? kTile * D : 0;
   static constexpr int kRaws = E4M3 ? (D == 64 ? 4 : 2) : kOps;   // bf16: the operand ring itself
-  static constexpr int kSmem = (2 + kOps) * kOpBytes + (E4M3 ? kRaws : 0) * kRawBytes + 1024;
+  static constexpr int kTiles = (2 + kOps) * kOpBytes + (E4M3 ? kRaws : 0) * kRawBytes;
 };
 // TMEM columns: the two tiles' scores (and weights), then their outputs
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
@@ -60,10 +66,22 @@ struct ChunkShared {
   uint64_t raw_full[8], raw_empty[8], op_full[8];
   uint64_t done[4];   // rounds of the MMA warp
   uint64_t q_full, s_full[2], p_full[2], o_full;
+  uint64_t turn[2];   // whose products come next
   uint32_t tmem;
   int abort;       // a wait gave up
   int bad;         // a value that some row must not see is not finite
   int kref[kScaleSlots], vref[kScaleSlots];    // e4m3: exponents taken out of a tile's keys and values
+  float row[2][kPairRows];     // what the two threads of a row tell each other; before that, [0]: e4m3's powers of
+                               // two taken out of the rows of q, times the scale
+};
+
+// Dynamic shared memory: the tiles from a 1024-byte boundary on, then the rest. Without static shared memory the
+// dynamic one starts on such a boundary; the largest size leaves 0.5 KB should it not.
+template <int D, bool E4M3>
+struct Smem {
+  static constexpr int kMost = 227 * 1024, kWant = Cfg<D, E4M3>::kTiles + (int)sizeof(ChunkShared) + 1024;
+  static_assert(Cfg<D, E4M3>::kTiles + (int)sizeof(ChunkShared) <= kMost, "tiles and barriers fit an SM");
+  static constexpr int kBytes = kWant < kMost ? kWant : kMost;
 };
 
 // Bounded: after kWaitNs, or once another wait of the block gave up, false.
@@ -91,16 +109,27 @@ __device__ __forceinline__ uint32_t hf_mul(uint32_t x, uint32_t f) {
   const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&f));
   return *reinterpret_cast<const uint32_t*>(&y);
 }
-// Each lane that `need`s it waits for a barrier of its own.
+// Each lane that `need`s it waits for a barrier of its own. Tests without pause at first: the tensor core stands still
+// meanwhile, and waking a suspended warp takes longer than most of these waits.
 __device__ __forceinline__ bool wait_lanes(ChunkShared& sh, uint32_t bar, uint32_t parity, bool need) {
-  bool ok = !need || mb_try(bar, parity);
-  if (__all_sync(0xffffffffu, ok)) return true;
+  bool ok = !need || mb_test(bar, parity);
+#pragma unroll 1
+  for (int i = 0; i < 4000 && !__all_sync(0xffffffffu, ok); ++i) ok = ok || mb_test(bar, parity);
   if (!ok) ok = wait_bar(sh, bar, parity);
   return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ uint32_t hf_scale(uint32_t x, float f) {
-  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
-  return hf_pack(y.x * f, y.y * f);
+// The two warps that share 32 rows: a barrier of their own, with the OR of a predicate.
+__device__ __forceinline__ bool pair_or(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 64, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)x), "r"(id)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ uint64_t pack2(const uint32_t* x) { return pair_of(__uint_as_float(x[0]), __uint_as_float(x[1])); }
 // Wait until the products that read operand load n are done: round i of the MMA warp reads K of tile i and V of
@@ -119,9 +148,35 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
                                                                     const __grid_constant__ CacheMaps maps) {
   using C = Cfg<D, E4M3>;
   constexpr int NO = C::kOps, NR = C::kRaws;
-  extern __shared__ uint8_t raw[];
-  __shared__ ChunkShared sh;
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t* ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  ChunkShared& sh = *reinterpret_cast<ChunkShared*>(ops + C::kTiles);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (ops + C::kTiles + sizeof(ChunkShared) > raw + Smem<D, E4M3>::kBytes) {
+    set_status(p.c.status, CP_ERR_UNSUPPORTED);
+    pdl_wait();
+    return;
+  }
+  if (warp == kLoadWarp) {               // a lane a barrier
+    if (lane < 8) mb_init(saddr(&sh.raw_full[lane]), 1);
+    else if (lane < 16) mb_init(saddr(&sh.raw_empty[lane - 8]), kHelpers / 32);
+    else if (lane < 24) mb_init(saddr(&sh.op_full[lane - 16]), kHelpers);
+    else if (lane < 28) mb_init(saddr(&sh.done[lane - 24]), 1);
+    if (lane < 2) {
+      mb_init(saddr(&sh.s_full[lane]), 1);
+      mb_init(saddr(&sh.p_full[lane]), 8);
+      mb_init(saddr(&sh.turn[lane]), 1);
+    }
+    if (lane == 2) mb_init(saddr(&sh.q_full), kSoftWarps * 32);
+    if (lane == 3) mb_init(saddr(&sh.o_full), 1);
+    if (lane == 4) sh.abort = sh.bad = 0;
+    mb_fence_init();
+  }
+  if (warp == kMmaWarp) {
+    tm_alloc(saddr(&sh.tmem), kTmemCols);
+    tm_relinquish();
+  }
 
   // which sequence and which of its tile pairs: every warp counts the pairs, 32 sequences at a time
   int seq = -1, pair = 0;
@@ -158,19 +213,32 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     }
   }
   pdl_trigger();
-  if (seq < 0) {
+  auto leave = [&] {                     // a block without work
+    if (warp == kMmaWarp) {
+      __syncwarp();
+      tm_dealloc(sh.tmem, kTmemCols);
+    }
     pdl_wait();
+  };
+  if (seq < 0) {
+    leave();
     return;
   }
   const int kv = blockIdx.x % p.c.heads, part = blockIdx.y;
   const int nrows = s.n * p.group;
   const int row0 = pair * kPairRows;
   const int rows_here = min(kPairRows, nrows - row0);
+  // row i of the pair is new row first_row + (first_head + i) / group, head (first_head + i) % group of the kv head; the
+  // quotient by a multiplication, exact for these sums below 320
+  const int first_row = row0 / p.group, first_head = row0 % p.group;
+  const uint32_t magic = (65535u + p.group) / p.group;
+  auto new_row = [&](int i) { return first_row + (int)(((uint32_t)(first_head + i) * magic) >> 16); };
+  auto head_of = [&](int i) { return first_head + i - (int)(((uint32_t)(first_head + i) * magic) >> 16) * p.group; };
   auto pos_of = [&](int i) { return s.first + min(i, nrows - 1) / p.group; };
   const Range range = item_range(p, pos_of(row0), pos_of(row0 + rows_here - 1), s.len, kChunkAlign);
   const int parts = parts_of(range, p.a.chunk_chunk);
   if (part >= max(parts, 1)) {
-    pdl_wait();
+    leave();
     return;
   }
   const bool whole = parts <= 1;
@@ -198,59 +266,39 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     }
   }
 
-  uint8_t* ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t q_s = saddr(ops), op_s = q_s + 2 * C::kOpBytes, raw_s = E4M3 ? op_s + NO * C::kOpBytes : op_s;
 
-  if (warp == kLoadWarp) {               // a lane a barrier
-    if (lane < 8) mb_init(saddr(&sh.raw_full[lane]), 1);
-    else if (lane < 16) mb_init(saddr(&sh.raw_empty[lane - 8]), kHelpers / 32);
-    else if (lane < 24) mb_init(saddr(&sh.op_full[lane - 16]), kHelpers);
-    else if (lane < 28) mb_init(saddr(&sh.done[lane - 24]), 1);
-    if (lane < 2) {
-      mb_init(saddr(&sh.s_full[lane]), 1);
-      mb_init(saddr(&sh.p_full[lane]), 4);
-    }
-    if (lane == 2) mb_init(saddr(&sh.q_full), kPairRows);
-    if (lane == 3) mb_init(saddr(&sh.o_full), 1);
-    if (lane == 4) sh.abort = sh.bad = 0;
-    mb_fence_init();
-  }
-  if (warp == kMmaWarp) {
-    tm_alloc(saddr(&sh.tmem), kTmemCols);
-    tm_relinquish();
-  }
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  // a softmax thread's row
-  const int i = warp >> 2;                               // stream (warps 0-7)
-  const int my = row0 + i * kTile + (warp & 3) * 32 + lane;
-  const bool mine = warp < kHelper0 && my < nrows;
-  const int64_t out_row = s.row0 + (mine ? my / p.group : 0);
-  const int head = kv * p.group + (mine ? my % p.group : 0);
+  // a softmax thread's row, and which half of a tile's positions (and later of its columns) is its
+  const int i = warp >> 3, half = (warp >> 2) & 1;       // stream (warps 0-15)
+  const int slot = (i * kTile + (warp & 3) * 32 + lane) & (kPairRows - 1);
+  const bool mine = warp < kSoftWarps && slot < rows_here;
+  const int pair_id = 1 + i * 4 + (warp & 3);            // the named barrier of the row's two warps
   float l = 0.f, m = -INFINITY;
   int vr = 0;
   constexpr float kBias = E4M3 ? 8.f : 0.f;
   constexpr int kUp = 6;                                 // operands of e4m3 reach 448 * 2^kUp: inside fp16
   constexpr float kLazy = E4M3 ? 6.f : 8.f;              // weights reach 2^(kBias + kLazy): inside fp16
+  constexpr int kHalf = kTile / 2;
 
-  if (warp < kHelper0) {
+  if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
-    float row_scale = p.scale_log2;
     {
-      // the warp's 32 rows, a row's units side by side; e4m3's q in fp16 times a power of two of its row
-      constexpr int UPR = D / 8, RPI = 32 / UPR, N = 32 / RPI;
-      const int u = lane % UPR, base = (warp & 3) * 32;
+      // 16 of the pair's 32 rows, a row's units side by side; e4m3's q in fp16 times a power of two of its row
+      constexpr int UPR = D / 8, RPI = 32 / UPR, N = 16 / RPI;
+      const int u = lane % UPR, base = (warp & 3) * 32 + half * 16 + lane / UPR;
       uint4 x[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const int r = row0 + i * kTile + base + k * RPI + lane / UPR;
+        const int r = i * kTile + base + k * RPI;
         x[k] = make_uint4(0, 0, 0, 0);
-        if (r < nrows)
-          x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.row0 + r / p.group) * p.q_row +
-                                                 (int64_t)(kv * p.group + r % p.group) * p.q_head + u * 8);
+        if (r < rows_here)
+          x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.row0 + new_row(r)) * p.q_row +
+                                                 (int64_t)(kv * p.group + head_of(r)) * p.q_head + u * 8);
       }
 #pragma unroll
       for (int k = 0; k < N; ++k) {
@@ -267,99 +315,93 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = hf_pack(bf_lo(w[q]) * inv, bf_hi(w[q]) * inv);
           x[k] = make_uint4(y[0], y[1], y[2], y[3]);
-          const int mine_e = __shfl_sync(0xffffffffu, e, (lane % RPI) * UPR);      // of row k * RPI + lane % RPI
-          if (lane / RPI == k) row_scale = p.scale_log2 * pow2i(mine_e);
+          if (u == 0) sh.row[0][i * kTile + base + k * RPI] = p.scale_log2 * pow2i(e);
         }
-        st_shared_v4u(q_s + i * C::kOpBytes + op_at(base + k * RPI + lane / UPR, u), x[k]);
+        st_shared_v4u(q_s + i * C::kOpBytes + op_at(base + k * RPI, u), x[k]);
       }
       fence_proxy_async_smem();
       mb_arrive(saddr(&sh.q_full));
+      if (E4M3) pair_or(pair_id, false);
     }
+    const float row_scale = E4M3 ? sh.row[0][slot] : p.scale_log2;
     int lo = 0, hi = 0;
-    if (mine) visible(p, s.first + my / p.group, s.len, &lo, &hi);
+    if (mine) visible(p, s.first + new_row(slot), s.len, &lo, &hi);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t s_t = tmem + lanes + kTmemS + i * kTile, o_t = tmem + lanes + kTmemO + i * D;
+    const uint32_t s_t = tmem + lanes + kTmemS + i * kTile + half * kHalf;
+    const uint32_t o_t = tmem + lanes + kTmemO + i * D + half * (D / 2);
     const int j0 = i ? jb[1] : jb[0], j1 = i ? je[1] : je[0];
     const int see_lo = i ? all_lo[1] : all_lo[0], see_hi = i ? all_hi[1] : all_hi[0];
     uint64_t sum[2] = {0, 0};              // two pairs of partial sums
-    auto rescale = [&](float f) {          // of O; the products before this tile's are done
-      tm_wait_st();
-#pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float v[32];
-        tm_ld32(o_t + c, v);
-#pragma unroll
-        for (int x = 0; x < 32; ++x) v[x] *= f;
-        tm_st32(o_t + c, v);
-      }
-    };
     for (int j = j0; j < j1; ++j) {
       const int n = j - j0;
       const int t0 = t_begin + j * kTile;
-      if (!wait_warp(sh, saddr(&sh.s_full[i]), n & 1)) break;
-      if (E4M3 && !wait_warp(sh, saddr(&sh.op_full[(2 * j + 1) % NO]), ((2 * j + 1) / NO) & 1)) break;   // its scales
+      bool ok = wait_warp(sh, saddr(&sh.s_full[i]), n & 1);
+      if (E4M3) ok = ok && wait_warp(sh, saddr(&sh.op_full[(2 * j + 1) % NO]), ((2 * j + 1) / NO) & 1);    // its scales
       tm_fence_after();
       const int vn = E4M3 ? sh.vref[j % kScaleSlots] : 0;
       const bool edge = t0 < see_lo || t0 + kTile > see_hi;
-      const float rs = E4M3 ? row_scale * pow2i(max(sh.kref[j % kScaleSlots] - kUp, -126)) : p.scale_log2;
-      const uint64_t rs2 = pair_of(rs, rs);
-      uint32_t x0[32], x1[32];
-      // 32 scores in place, masked ones minus infinity
+      const float rs = E4M3 ? row_scale * pow2i(max(sh.kref[j % kScaleSlots] - kUp, -126)) : row_scale;
+      // masked scores are minus infinity
       auto ready = [&](uint32_t* x, int c) {
         if (edge) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (t0 + c + k < lo || t0 + c + k >= hi) x[k] = 0xff800000u;
-        }
-      };
-      auto top_of = [&](const uint32_t* x) {
-        float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
-#pragma unroll
-        for (int k = 2; k < 32; k += 2) {
-          a = fmaxf(a, __uint_as_float(x[k]));
-          b = fmaxf(b, __uint_as_float(x[k + 1]));
-        }
-        return fmaxf(a, b);
-      };
-      if (E4M3 && vn != vr) {              // a larger value scale: what is summed so far shrinks next to it
-        if (n > 0) rescale(pow2i(max(vr - vn, -127)));
-        vr = vn;
-      }
-      if (n == 0) {                        // the first tile sets the reference
-        float top = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
-          tm_ld32_start(s_t + c, x0);
-          tm_ld32_wait(x0);
-          ready(x0, c);
-          top = fmaxf(top, top_of(x0));
-        }
-        m = top * rs;
-      }
-      // 32 weights and their sum; scores risen too far over the reference move it, with all that it scales
-      auto weigh = [&](uint32_t* x, int c) {
-        ready(x, c);
-        const float top = top_of(x) * rs;
-        if (__any_sync(0xffffffffu, top > m + kLazy)) {
-          const float mn = fmaxf(m, top);
-          const float f = mn == m ? 1.f : ex2(m - mn);
-          const uint64_t f2 = pair_of(f, f);
-          sum[0] = mul2(sum[0], f2);
-          sum[1] = mul2(sum[1], f2);
-          m = mn;
-          if (n > 0) rescale(f);
-          tm_wait_st();
-#pragma unroll 1
-          for (int d = 0; d < c / 2; d += 16) {          // this tile's weights so far
-            uint32_t w[16];
-            tm_ld16_raw(s_t + d, w);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = E4M3 ? hf_scale(w[k], f) : bf_pack(bf_lo(w[k]) * f, bf_hi(w[k]) * f);
-            tm_st16(s_t + d, w);
+          for (int k = 0; k < 32; ++k) {
+            const int t = t0 + half * kHalf + c + k;
+            if (t < lo || t >= hi) x[k] = 0xff800000u;
           }
         }
-        const float ref = (m == -INFINITY ? 0.f : m) - kBias;
-        const uint64_t ref2 = pair_of(-ref, -ref);
+      };
+      uint32_t x[32];
+      float top = -INFINITY;
+      if (ok) {
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+          tm_ld32_start(s_t + c, x);
+          tm_ld32_wait(x);
+          ready(x, c);
+          float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
+#pragma unroll
+          for (int k = 2; k < 32; k += 2) {
+            a = fmaxf(a, __uint_as_float(x[k]));
+            b = fmaxf(b, __uint_as_float(x[k + 1]));
+          }
+          top = fmaxf(top, fmaxf(a, b));
+        }
+        tm_ld32_start(s_t, x);             // the first of the second pass
+        top *= rs;
+      }
+      if (pair_or(pair_id, !ok || top > m + kLazy || vn != vr)) {
+        // move the reference, to what both threads of the row have seen (or end, if a wait gave up)
+        if (pair_or(pair_id, !ok)) break;
+        sh.row[half][slot] = top;
+        pair_or(pair_id, false);
+        const float mn = fmaxf(m, fmaxf(top, sh.row[half ^ 1][slot]));
+        float f = mn == m ? 1.f : ex2(m - mn);
+        const uint64_t f2 = pair_of(f, f);
+        sum[0] = mul2(sum[0], f2);
+        sum[1] = mul2(sum[1], f2);
+        m = mn;
+        if (E4M3) f *= pow2i(max(vr - vn, -127));          // a larger value scale
+        vr = vn;
+        if (n > 0) {
+          tm_ld32_wait(x);
+#pragma unroll 1
+          for (int c = 0; c < D / 2; c += 32) {
+            float v[32];
+            tm_ld32(o_t + c, v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) v[k] *= f;
+            tm_st32(o_t + c, v);
+          }
+          tm_ld32_start(s_t, x);
+        }
+      }
+      const float ref = (m == -INFINITY ? 0.f : m) - kBias;
+      const uint64_t rs2 = pair_of(rs, rs), ref2 = pair_of(-ref, -ref);
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 32) {
+        tm_ld32_wait(x);
+        ready(x, c);
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -373,17 +415,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
           w[k / 2] = E4M3 ? hf_pack(y[0], y[1]) : bf_pack(y[0], y[1]);
           w[k / 2 + 1] = E4M3 ? hf_pack(y[2], y[3]) : bf_pack(y[2], y[3]);
         }
+        if (c + 32 < kHalf) tm_ld32_start(s_t + c + 32, x);
         tm_st16(s_t + c / 2, w);
-      };
-      tm_ld32_start(s_t, x0);
-#pragma unroll 1
-      for (int c = 0; c < kTile; c += 64) {
-        tm_ld32_wait(x0);
-        tm_ld32_start(s_t + c + 32, x1);
-        weigh(x0, c);
-        tm_ld32_wait(x1);
-        if (c + 64 < kTile) tm_ld32_start(s_t + c + 64, x0);
-        weigh(x1, c + 32);
       }
       tm_wait_st();
       tm_fence_before();
@@ -394,6 +427,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
     split_pair(sum[0], y, y + 1);
     split_pair(sum[1], y + 2, y + 3);
     l = (y[0] + y[1]) + (y[2] + y[3]);
+    sh.row[half][slot] = l;                // met after the block's barrier
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- helpers
     const int tid = threadIdx.x - kHelper0 * 32;
@@ -563,7 +597,8 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
       const uint64_t v = v_desc + slot * kOpDesc;
 #pragma unroll
       for (int k = 0; k < kTile / 16; ++k)
-        tm_mma_ts_lead(lead, tm + kTmemO + x * D, tm + kTmemS + x * kTile + k * 8, v + k * (2048 >> 4), id_o, k ? 1u : more);
+        tm_mma_ts_lead(lead, tm + kTmemO + x * D, tm + kTmemS + x * kTile + (k / 4) * (kTile / 2) + (k % 4) * 8,
+                       v + k * (2048 >> 4), id_o, k ? 1u : more);
     };
     // slots of V of tile j and K of tile j + 1, the parity of their turn round the ring, and of the streams' turns
     int sv = NO - 1, sk = 0;
@@ -584,7 +619,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
       }
       if (s0) scores(0, sk);
       if (v1) {
-        ok = wait_warp(sh, p_full + 8, rp1);
+        ok = wait_lanes(sh, p_full + 8, rp1, lane == 0);
         if (!ok) break;
         tm_fence_after();
         values(1, sv, j > b1);
@@ -613,38 +648,39 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
   if (failed && threadIdx.x == 0) set_status(p.c.status, CP_ERR_TIMEOUT);
   if (!failed && sh.bad) {
     plain_rows<D, E4M3>(p, s, seq, kv, row0, row0 + rows_here, t_begin, t_end, part, whole, warp, kThreadsC / 32);
-  } else if (!failed && warp < kHelper0) {
-    // rows leave through the ring's memory, so that a row is written at once and not by its thread piece by piece
-    const uint32_t o_t = tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + i * D;
+  } else if (!failed && warp < kSoftWarps) {
+    // rows leave through the operands' memory, so that a row is written at once and not by its threads piece by piece
+    const uint32_t o_t = tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + i * D + half * (D / 2);
     const bool any = i ? je[1] > jb[1] : je[0] > jb[0];
+    l = sh.row[0][slot] + sh.row[1][slot];
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float e = E4M3 ? pow2i(min(max(vr - kUp, -126), 127)) : 1.f;
     constexpr int kPitch = D + 4;
-    static_assert(8 * 32 * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the eight warps' rows fit the operands' memory");
-    float* stage = reinterpret_cast<float*>(ops) + warp * 32 * kPitch;
+    static_assert(kPairRows * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the rows fit the operands' memory");
+    float* stage = reinterpret_cast<float*>(ops) + (i * kTile + (warp & 3) * 32) * kPitch;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
+    for (int c = 0; c < D / 2; c += 32) {
       float v[32];
       if (any) tm_ld32(o_t + c, v);
 #pragma unroll
       for (int x = 0; x < 32; x += 4) {
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
         if (any && inv != 0.f) y = make_float4(v[x] * inv * e, v[x + 1] * inv * e, v[x + 2] * inv * e, v[x + 3] * inv * e);
-        *reinterpret_cast<float4*>(stage + lane * kPitch + c + x) = y;
+        *reinterpret_cast<float4*>(stage + lane * kPitch + half * (D / 2) + c + x) = y;
       }
     }
-    if (mine && !whole) store_lse(p, part, out_row, head, l == 0.f ? -INFINITY : m + log2f(l) - kBias);
-    __syncwarp();
-    constexpr int LPR = D / 4, RPI = 32 / LPR;
-    const int first = row0 + i * kTile + (warp & 3) * 32;
-#pragma unroll 4
-    for (int k = 0; k < 32 / RPI; ++k) {
-      const int r = k * RPI + lane / LPR, d = lane % LPR * 4;
-      if (first + r < nrows)
-        store4<D>(p, part, whole, s.row0 + (first + r) / p.group, kv * p.group + (first + r) % p.group, d,
-                  stage + r * kPitch + d);
-    }
+    if (mine && !whole && half == 0)
+      store_lse(p, part, s.row0 + new_row(slot), kv * p.group + head_of(slot), l == 0.f ? -INFINITY : m + log2f(l) - kBias);
     tm_fence_before();
+    pair_or(pair_id, false);
+    constexpr int LPR = D / 4, RPI = 32 / LPR;
+    const int first = i * kTile + (warp & 3) * 32;
+#pragma unroll 8
+    for (int k = 0; k < 16 / RPI; ++k) {
+      const int r = half * 16 + k * RPI + lane / LPR, d = lane % LPR * 4;
+      if (first + r < rows_here)
+        store4<D>(p, part, whole, s.row0 + new_row(first + r), kv * p.group + head_of(first + r), d, stage + r * kPitch + d);
+    }
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -659,7 +695,7 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
 template <int D, bool E4M3>
 static cudaError_t prepare() {
   return cudaFuncSetAttribute(attend_chunk_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D, E4M3>::kSmem);
+                              Smem<D, E4M3>::kBytes);
 }
 cudaError_t prepare_attend_chunk() {
   for (cudaError_t e : {prepare<64, false>(), prepare<64, true>(), prepare<128, false>(), prepare<128, true>()})
@@ -671,11 +707,11 @@ template <int D, bool E4M3>
 static cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   const dim3 grid((unsigned)(p.c.heads * chunk_pairs(p.b, p.group)), p.a.chunk_parts);
   if (!p.a.use_step) {
-    attend_chunk_kernel<D, E4M3><<<grid, kThreadsC, Cfg<D, E4M3>::kSmem, s>>>(p, maps);
+    attend_chunk_kernel<D, E4M3><<<grid, kThreadsC, Smem<D, E4M3>::kBytes, s>>>(p, maps);
     return cudaGetLastError();
   }
   // behind the step kernel, whose results it does not need: it may fill the SMs that one leaves
-  return launch_pdl(attend_chunk_kernel<D, E4M3>, grid, kThreadsC, Cfg<D, E4M3>::kSmem, s, p, maps);
+  return launch_pdl(attend_chunk_kernel<D, E4M3>, grid, kThreadsC, Smem<D, E4M3>::kBytes, s, p, maps);
 }
 cudaError_t launch_attend_chunk(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s) {
   if (head_dim == 128) return e4m3 ? launch<128, true>(p, maps, s) : launch<128, false>(p, maps, s);
