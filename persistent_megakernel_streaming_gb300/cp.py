@@ -261,13 +261,6 @@ class Frame:
             pass
 
 
-def _bits(t, what: str, size: int):
-    """t, checked to hold `size`-byte elements (bf16 or their bit patterns; e4m3 or theirs)."""
-    if t.element_size() != size or t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what}: {size}-byte elements, the last axis contiguous")
-    return t
-
-
 def _stride(t, axis: int) -> int:
     """Elements between t's entries along `axis`; 0 (the C side's "contiguous") where there is one at most."""
     if t.shape[axis] <= 1:
@@ -293,9 +286,14 @@ class Batch:
         if length.dim() != 1 or start.dim() != 1 or pages.dim() != 2 or start.numel() != length.numel() + 1 or \
                 pages.shape[0] != length.numel():
             raise ValueError("start [n + 1], length [n] and pages [n][width]")
+        if not start.device == length.device == pages.device:
+            raise ValueError("start, length and pages on one device")
         self.start, self.length, self.pages, self.rows = start, length, pages, int(rows)
+        self.device_index = start.get_device()
+        self.plans = {}     # attend's workspace sizes by what they depend on
         self.desc = BatchDesc(length.numel(), int(rows), int(max_new), int(max_len), pages.shape[1],
                               _stride(pages, 0), _ptr(start), _ptr(length), _ptr(pages))
+        self.ref = C.byref(self.desc)
 
 
 class Cache:
@@ -312,8 +310,8 @@ class Cache:
             raise ValueError("k and v: [pages][kv_heads][page_size][head_dim] of the same strides, on one GPU")
         if size not in (1, 2) or (size == 1) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
             raise ValueError("bf16 pages without scales, or e4m3 pages with k_scale and v_scale")
-        _bits(k, "k", size)
-        _bits(v, "v", size)
+        if k.stride(3) != 1:
+            raise ValueError("k and v: the last axis contiguous")
         scale_strides = (0, 0, 0)
         if size == 1:
             for t in (k_scale, v_scale):
@@ -322,7 +320,8 @@ class Cache:
             scale_strides = [_stride(k_scale, i) for i in range(3)]
         self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.keep = (k, v, k_scale, v_scale)
-        self.device = k.device
+        self.device, self.device_index = k.device, k.get_device()
+        self.layout = (size, self.kv_heads, self.head_dim, self.page_size)
         self.desc = CacheDesc(int(size == 1), self.kv_heads, self.head_dim, self.page_size, self.pages, _ptr(k), _ptr(v),
                               *(_stride(k, i) for i in range(3)), _ptr(k_scale), _ptr(v_scale), *scale_strides)
         h = C.c_void_p()
@@ -332,68 +331,90 @@ class Cache:
     def append(self, batch: Batch, qkv, q_out=None, q_norm=None, k_norm=None, rms_eps: float = 1e-6,
                rope_base: float = 0.0, stream=None):
         """qkv [rows][(q_heads + 2 kv_heads) * head_dim] into the cache, its q into q_out [rows][q_heads][head_dim]."""
+        d = self.head_dim
         heads = 0 if q_out is None else q_out.shape[1]
-        self._rows(batch, _bits(qkv, "qkv", 2), (heads + 2 * self.kv_heads) * self.head_dim)
+        x, (row,) = self._rows(batch, qkv, "qkv", (heads + 2 * self.kv_heads) * d)
+        q, q_row = 0, 0
         if q_out is not None:
-            self._rows(batch, _bits(q_out, "q_out", 2), heads, self.head_dim)
-            if heads > 1 and q_out.stride(1) != self.head_dim:
+            q, (q_row, head) = self._rows(batch, q_out, "q_out", heads, d)
+            if head not in (0, d):
                 raise ValueError("q_out: contiguous heads")
-        for name, t in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if t is not None and (t.shape != (self.head_dim,) or t.device != self.device or _bits(t, name, 2) is None):
-                raise ValueError(f"{name}: [head_dim] on the cache's device")
-        a = AppendArgs(_ptr(qkv), _stride(qkv, 0), _ptr(q_out), 0 if q_out is None else _stride(q_out, 0), heads, _ptr(q_norm),
-                       _ptr(k_norm), float(rms_eps), float(rope_base))
-        _check(lib().cp_cache_append(self._h, C.byref(batch.desc), C.byref(a), self._stream(stream)), "cp_cache_append")
+        a = AppendArgs(x, row, q, q_row, heads, self._gain(q_norm), self._gain(k_norm), rms_eps, rope_base)
+        code = lib().cp_cache_append(self._h, batch.ref, C.byref(a), self._stream(stream))
+        if code:
+            raise CPError(code, "cp_cache_append")
 
     def read(self, batch: Batch, k_out=None, v_out=None, stream=None):
-        """The batch's rows' cached keys and values as bf16 [rows][kv_heads][head_dim]."""
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
+        """The batch's rows' cached keys and values as bf16 [rows][kv_heads][head_dim], contiguous."""
+        at = [0, 0]
+        for i, t in enumerate((k_out, v_out)):
             if t is not None:
-                self._rows(batch, _bits(t, name, 2), self.kv_heads, self.head_dim)
+                at[i], _ = self._rows(batch, t, "k_out, v_out", self.kv_heads, self.head_dim)
                 if not t.is_contiguous():
-                    raise ValueError(f"{name}: contiguous")
-        _check(lib().cp_cache_read(self._h, C.byref(batch.desc), _ptr(k_out), _ptr(v_out), self._stream(stream)),
-               "cp_cache_read")
+                    raise ValueError("k_out, v_out: contiguous")
+        code = lib().cp_cache_read(self._h, batch.ref, at[0], at[1], self._stream(stream))
+        if code:
+            raise CPError(code, "cp_cache_read")
 
     def attend(self, batch: Batch, q, out, scale: float = 0.0, causal: bool = True, window: int = 0, workspace=None,
                stream=None):
         """Attention of q [rows][q_heads][head_dim] over the cache into out (the same shape). Without a
         ``workspace`` (device bytes, see workspace_bytes) one is taken from torch's allocator for this call."""
-        for name, t in (("q", q), ("out", out)):
-            self._rows(batch, _bits(t, name, 2), q.shape[1], self.head_dim)
-        a = AttendArgs(_ptr(q), _ptr(out), _stride(q, 0), _stride(q, 1), _stride(out, 0), _stride(out, 1), q.shape[1], float(scale),
-                       int(causal), int(window))
-        need = C.c_size_t()
-        _check(lib().cp_cache_check(C.byref(self.desc), C.byref(batch.desc), None, C.byref(a), C.byref(need)),
-               "cp_cache_attend")
-        if workspace is None and need.value:
-            workspace = self._workspace(need.value, stream)
-        if workspace is not None and (workspace.device != self.device or not workspace.is_contiguous()):
-            raise ValueError("workspace: contiguous, on the cache's device")
-        size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib().cp_cache_attend(self._h, C.byref(batch.desc), C.byref(a), _ptr(workspace), size, self._stream(stream)),
-               "cp_cache_attend")
+        heads = q.shape[1]
+        x, (row, head) = self._rows(batch, q, "q", heads, self.head_dim)
+        y, (out_row, out_head) = self._rows(batch, out, "out", heads, self.head_dim)
+        a = AttendArgs(x, y, row, head, out_row, out_head, heads, scale, causal, window)
+        need = self._need(batch, heads, causal, window)
+        at, size = 0, 0
+        if workspace is not None:
+            if workspace.get_device() != self.device_index or not workspace.is_contiguous():
+                raise ValueError("workspace: contiguous, on the cache's device")
+            at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        elif need:
+            workspace = self._workspace(need, stream)
+            at, size = workspace.data_ptr(), need
+        code = lib().cp_cache_attend(self._h, batch.ref, C.byref(a), at, size, self._stream(stream))
+        if code:
+            raise CPError(code, "cp_cache_attend")
 
     def workspace_bytes(self, batch: Batch, q_heads: int, causal: bool = True, window: int = 0) -> int:
         """What ``attend`` needs for this batch, whatever its arrays hold."""
-        a = AttendArgs(16, 32, 0, 0, 0, 0, int(q_heads), 0.0, int(causal), int(window))
-        need = C.c_size_t()
-        _check(lib().cp_cache_check(C.byref(self.desc), C.byref(batch.desc), None, C.byref(a), C.byref(need)),
-               "cp_cache_check")
-        return need.value
+        return self._need(batch, int(q_heads), causal, window)
 
-    def _rows(self, batch, t, *shape):
-        if batch.start.device != self.device or batch.length.device != self.device or batch.pages.device != self.device:
-            raise ValueError("a batch on another device than the cache's")
-        if t.shape != (batch.rows, *shape):
-            raise ValueError(f"rows of shape {(batch.rows, *shape)} are wanted, got {tuple(t.shape)}")
-        if t.device != self.device:
-            raise ValueError("a tensor on another device than the cache's")
+    def _need(self, batch, heads, causal, window):
+        key = (self.layout, heads, bool(causal), window)
+        if key not in batch.plans:
+            a = AttendArgs(16, 32, 0, 0, 0, 0, heads, 0.0, causal, window)
+            need = C.c_size_t()
+            _check(lib().cp_cache_check(C.byref(self.desc), batch.ref, None, C.byref(a), C.byref(need)), "cp_cache_attend")
+            batch.plans[key] = need.value
+        return batch.plans[key]
+
+    def _rows(self, batch, t, what, *inner):
+        """Address of a row array and the strides of its axes but the last (0 where it has one entry at most)."""
+        shape, strides = tuple(t.shape), t.stride()
+        if shape != (batch.rows, *inner) or t.element_size() != 2 or strides[-1] != 1 and inner[-1] > 1:
+            raise ValueError(f"{what}: 16-bit elements [{', '.join(map(str, (batch.rows, *inner)))}], the last axis "
+                             f"contiguous; got {shape}, strides {strides}, {t.dtype}")
+        if t.get_device() != self.device_index or batch.device_index != self.device_index:
+            raise ValueError(f"{what}, or the batch: on another device than the cache's")
+        if shape[0] > 1 and strides[0] > 0 < strides[-2]:
+            return t.data_ptr(), strides[:-1]
+        if any(n > 1 and s <= 0 for n, s in zip(shape, strides)):
+            raise ValueError(f"{what}: entries that share memory (an expanded tensor)")
+        return t.data_ptr(), tuple(s if n > 1 else 0 for n, s in zip(shape[:-1], strides))
+
+    def _gain(self, t):
+        if t is None:
+            return 0
+        if tuple(t.shape) != (self.head_dim,) or t.element_size() != 2 or t.stride(0) != 1 or t.get_device() != self.device_index:
+            raise ValueError("q_norm, k_norm: bf16 [head_dim] on the cache's device")
+        return t.data_ptr()
 
     def _stream(self, stream) -> int:
         if stream is None:
             import torch
-            return int(torch.cuda.current_stream(self.device).cuda_stream)
+            return torch._C._cuda_getCurrentRawStream(self.device_index)
         return _stream(stream)
 
     def _workspace(self, size, stream):

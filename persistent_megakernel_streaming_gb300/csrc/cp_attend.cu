@@ -12,6 +12,7 @@ namespace cache {
 // ------------------------------------------------------------------ plan
 constexpr int kSms = 152;
 constexpr int kStepBlocks = 2 * kSms; // step blocks resident at once
+constexpr int kStepCluster = 8;       // blocks of a cluster that joins its parts itself
 constexpr int kMaxStepChunk = 4096;   // positions a step block holds page numbers for
 
 static int step_tile(int head_dim, bool e4m3) { return 4 * (e4m3 ? 32 : 16) * (128 / head_dim); }
@@ -33,6 +34,13 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
   const int64_t want = std::max<int64_t>(1, kStepBlocks * 8 / items);
   int64_t chunk = (span + want - 1) / want;
   chunk = std::min<int64_t>(std::max<int64_t>((chunk + tile - 1) / tile * tile, tile), kMaxStepChunk);
+  // A call whose blocks are all resident at once may join an item's parts within a cluster, through shared memory,
+  // and needs no second launch and no workspace: one sequence of 777 positions 18 -> 8.5 us a call. Longer
+  // ones need more parts than a cluster has blocks.
+  if (items * kStepCluster <= kStepBlocks && span <= kStepCluster * 512) {
+    chunk = std::max<int64_t>((span + kStepCluster - 1) / kStepCluster + tile - 1, tile) / tile * tile;
+    a.step_cluster = 1;
+  }
   a.step_chunk = (int)chunk;
   a.step_parts = a.use_step ? (int)std::max<int64_t>(1, (span + chunk - 1) / chunk) : 0;
   if (a.use_chunk) {
@@ -62,7 +70,7 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
 }
 
 size_t attend_workspace(const AttendPlan& a, const BatchView& b, int q_heads, int head_dim) {
-  const int parts = std::max(a.step_parts, a.chunk_parts);
+  const int parts = kept_parts(a);
   return parts > 1 ? (size_t)parts * b.rows * q_heads * (head_dim + 1) * sizeof(float) : 0;
 }
 
@@ -114,6 +122,46 @@ struct StepShared {
   uint16_t rows_pad[8];
 };
 
+// The parts of an item, weighed by their sums, by the cluster whose blocks have them: each takes a share of the
+// elements and reads the others' shared memory. Blocks without a part have left; the others leave together.
+constexpr int kAvgAt = 10240;           // floats into the ring: behind the warps' averages
+static_assert(kAvgAt >= kStepWarps * kStepRows * (128 + 4) && (kAvgAt + kStepRows * 129) * 4 <= kStepSmem, "the ring's plan");
+template <int D>
+__device__ __forceinline__ void join_cluster(const AttendParams& p, const Seq& s, int kv, int nrows, int parts, float* avg,
+                                             float* avg_lse) {
+  __syncwarp();
+  ptx::cluster_sync_all();
+  const uint32_t at = smem_u32(avg), at_lse = smem_u32(avg_lse);
+  for (int u = blockIdx.x * (kStepWarps * 32) + threadIdx.x; u < nrows * (D / 4); u += parts * (kStepWarps * 32)) {
+    const int r = u / (D / 4), d = u % (D / 4) * 4;
+    float lse[kStepCluster], top = -INFINITY;
+    float4 y[kStepCluster];
+#pragma unroll
+    for (int i = 0; i < kStepCluster; ++i) {
+      lse[i] = -INFINITY;
+      if (i < parts) {
+        lse[i] = ptx::ld_cluster(ptx::mapa(at_lse + r * 4, i));
+        y[i] = ptx::ld_cluster_v4(ptx::mapa(at + (r * D + d) * 4, i));
+      }
+      top = fmaxf(top, lse[i]);
+    }
+    float x[4] = {}, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kStepCluster; ++i)
+      if (i < parts) {
+        const float w = lse[i] == -INFINITY ? 0.f : ex2(lse[i] - top);
+        sum += w;
+        x[0] += w * y[i].x; x[1] += w * y[i].y; x[2] += w * y[i].z; x[3] += w * y[i].w;
+      }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] *= inv;
+    store4<D>(p, 0, true, s.row0 + r / p.group, kv * p.group + r % p.group, d, x);
+  }
+  __syncwarp();
+  ptx::cluster_sync_all();
+}
+
 // One block a (part, kv head, sequence); its four warps take the part's tiles
 // in turn, each with a running maximum, sum and product of its own and its own
 // ring of asynchronous copies, so that nothing in the loop waits for another
@@ -130,7 +178,7 @@ struct StepShared {
 // where the instruction wants two and two: the sum over the head does not
 // mind the order, so q is loaded in it, and the output columns come out
 // four neighbours a thread.
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool CLUSTER>
 __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const __grid_constant__ AttendParams p) {
   constexpr int TK = (E4M3 ? 32 : 16) * (128 / D);    // positions a tile
   constexpr int ES = E4M3 ? 1 : 2;
@@ -433,8 +481,12 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
   }
   cp_wait<0>();
   const bool whole = parts <= 1;
+  // a cluster's parts: each block's averages and log-sums, where the others read them
+  float* avg = reinterpret_cast<float*>(ring) + kAvgAt;
+  float* avg_lse = avg + kStepRows * 128;
   if (__syncthreads_or(bad)) {
-    plain_rows<D, E4M3>(p, s, seq, kv, 0, nrows, t_begin, t_end, part, whole, warp, kStepWarps);
+    plain_rows<D, E4M3>(p, s, seq, kv, 0, nrows, t_begin, t_end, part, whole, warp, kStepWarps, CLUSTER ? avg : nullptr, avg_lse);
+    if (CLUSTER && !whole) join_cluster<D>(p, s, kv, nrows, parts, avg, avg_lse);
     return;
   }
 
@@ -465,31 +517,38 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
   __syncthreads();
   constexpr int TPR = kStepWarps * 32 / kStepRows;    // threads a row
   const int r = threadIdx.x / TPR, d0 = threadIdx.x % TPR * 4;
-  if (r >= nrows) return;
-  float top = -INFINITY;
+  if (r < nrows) {
+    float top = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kStepWarps; ++w) top = fmaxf(top, sh.m[w][r]);
-  float fw[kStepWarps], sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kStepWarps; ++w) {
-    fw[w] = sh.m[w][r] == -INFINITY ? sh.l[w][r] : sh.l[w][r] * ex2(sh.m[w][r] - top);
-    sum += fw[w];
-  }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t row = s.row0 + r / p.group;
-  const int head = kv * p.group + r % p.group;
-#pragma unroll
-  for (int d = d0; d < D; d += TPR * 4) {
-    float x[4] = {};
+    for (int w = 0; w < kStepWarps; ++w) top = fmaxf(top, sh.m[w][r]);
+    float fw[kStepWarps], sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kStepWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring) + (w * kStepRows + r) * (D + 4) + d);
-      const float f = fw[w] * inv;
-      x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
+      fw[w] = sh.m[w][r] == -INFINITY ? sh.l[w][r] : sh.l[w][r] * ex2(sh.m[w][r] - top);
+      sum += fw[w];
     }
-    store4<D>(p, part, whole, row, head, d, x);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t row = s.row0 + r / p.group;
+    const int head = kv * p.group + r % p.group;
+#pragma unroll
+    for (int d = d0; d < D; d += TPR * 4) {
+      float x[4] = {};
+#pragma unroll
+      for (int w = 0; w < kStepWarps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(ring) + (w * kStepRows + r) * (D + 4) + d);
+        const float f = fw[w] * inv;
+        x[0] += y.x * f; x[1] += y.y * f; x[2] += y.z * f; x[3] += y.w * f;
+      }
+      if (CLUSTER && !whole) *reinterpret_cast<float4*>(avg + r * D + d) = make_float4(x[0], x[1], x[2], x[3]);
+      else store4<D>(p, part, whole, row, head, d, x);
+    }
+    const float lse = sum == 0.f ? -INFINITY : top + log2f(sum) - kBias;
+    if (!whole && d0 == 0) {
+      if (CLUSTER) avg_lse[r] = lse;
+      else store_lse(p, part, row, head, lse);
+    }
   }
-  if (!whole && d0 == 0) store_lse(p, part, row, head, sum == 0.f ? -INFINITY : top + log2f(sum) - kBias);
+  if (CLUSTER && !whole) join_cluster<D>(p, s, kv, nrows, parts, avg, avg_lse);
 }
 
 // ------------------------------------------------------------------ join
@@ -504,9 +563,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int head = (int)(unit % p.q_heads);
   if (row >= p.b.rows) return;
   int seq = 0;
+#pragma unroll 4
   for (int i0 = 0; i0 < p.b.n; i0 += 32) {
     const int i = i0 + lane;
-    seq += __popc(__ballot_sync(0xffffffffu, i < p.b.n && p.b.start[i + 1] <= row));
+    seq += __popc(__ballot_sync(0xffffffffu, i < p.b.n && p.b.start[min(i, p.b.n - 1) + 1] <= row));
   }
   if (seq >= p.b.n) return;
   const Seq s = seq_of(p.b, seq, p.c.status);
@@ -514,7 +574,7 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   const int nrows = s.n * p.group;
   int parts;
   if (p.a.use_step && nrows <= kStepRows) {
-    parts = parts_of(item_range(p, s.first, s.first + s.n - 1, s.len, kStepAlign), p.a.step_chunk);
+    parts = p.a.step_cluster ? 0 : parts_of(item_range(p, s.first, s.first + s.n - 1, s.len, kStepAlign), p.a.step_chunk);
   } else {
     const int i0 = ((int)(row - s.row0) * p.group + head % p.group) / kPairRows * kPairRows;
     const int i1 = min(i0 + kPairRows, nrows) - 1;
@@ -548,15 +608,22 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
 
 template <int D, bool E4M3>
 cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
-  if (p.a.use_step)
-    attend_step_kernel<D, E4M3><<<dim3(p.a.step_parts, p.c.heads, p.b.n), kStepWarps * 32, kStepSmem, s>>>(p);
+  if (p.a.use_step) {
+    const dim3 blocks(p.a.step_parts, p.c.heads, p.b.n);
+    if (p.a.step_cluster) {
+      const cudaError_t e = launch_cluster(attend_step_kernel<D, E4M3, true>, blocks, p.a.step_parts, kStepWarps * 32, kStepSmem, s, p);
+      if (e != cudaSuccess) return e;
+    } else {
+      attend_step_kernel<D, E4M3, false><<<blocks, kStepWarps * 32, kStepSmem, s>>>(p);
+    }
+  }
   const int64_t units = (int64_t)p.b.rows * p.q_heads;
   const unsigned grid = (unsigned)((units + 7) / 8);
   if (p.a.use_chunk) {
     const cudaError_t e = launch_attend_chunk(p, maps, D, E4M3, s);
     if (e != cudaSuccess) return e;
   }
-  if (std::max(p.a.step_parts, p.a.chunk_parts) > 1) {
+  if (kept_parts(p.a) > 1) {
     const cudaError_t e = launch_pdl(attend_join_kernel<D>, dim3(grid), 256, 0, s, p);
     if (e != cudaSuccess) return e;
   }
@@ -565,7 +632,8 @@ cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s)
 
 template <int D, bool E4M3>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(attend_step_kernel<D, E4M3>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
+  const cudaError_t e = cudaFuncSetAttribute(attend_step_kernel<D, E4M3, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(attend_step_kernel<D, E4M3, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
 }
 
 }  // namespace

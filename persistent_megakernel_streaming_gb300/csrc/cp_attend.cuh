@@ -27,6 +27,24 @@ cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A launch whose blocks along x are clusters of `cluster`.
+template <class K, class... A>
+cudaError_t launch_cluster(K kernel, dim3 grid, int cluster, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Biased exponent of a bf16 pattern, 0 for infinities and NaN.
 __device__ __forceinline__ int finite_exp(uint32_t h) {
   const int e = (int)(h >> 7) & 255;
@@ -70,7 +88,8 @@ __device__ __forceinline__ void store_lse(const AttendParams& p, int part, int64
 // that finds one next to a mask runs this instead.
 template <int D, bool E4M3>
 __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, int kv, int i0, int i1, int t_begin,
-                                        int t_end, int part, bool whole, int warp, int warps) {
+                                        int t_end, int part, bool whole, int warp, int warps, float* avg = nullptr,
+                                        float* avg_lse = nullptr) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
@@ -128,6 +147,10 @@ __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, i
     if (whole) {
 #pragma unroll
       for (int j = 0; j < E; ++j) p.out[row * p.o_row + head * p.o_head + lane * E + j] = (uint16_t)bf_pack(acc[j] * inv, 0.f);
+    } else if (avg) {                    // a block that joins its parts in shared memory
+#pragma unroll
+      for (int j = 0; j < E; ++j) avg[i * D + lane * E + j] = acc[j] * inv;
+      if (lane == 0) avg_lse[i] = l == 0.f ? -INFINITY : m + log2f(l);
     } else {
       const int64_t unit = ((int64_t)part * p.b.rows + row) * p.q_heads + head;
 #pragma unroll

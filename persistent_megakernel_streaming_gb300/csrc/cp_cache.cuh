@@ -119,10 +119,16 @@ constexpr int kStepAlign = 16, kChunkAlign = 128;   // where an item's parts may
 struct AttendPlan {
   int use_step, use_chunk;
   int step_chunk, step_parts;     // positions a part, most parts of an item
+  int step_cluster;               // the parts of a step item are one cluster's blocks, which join them
   int chunk_chunk, chunk_parts;
 };
 AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, bool causal,
                        int window);
+// Most parts of an item that go through the workspace.
+inline int kept_parts(const AttendPlan& a) {
+  const int step = a.step_cluster ? 0 : a.step_parts;
+  return step > a.chunk_parts ? step : a.chunk_parts;
+}
 // An upper bound of the chunk kernel's items a kv head: whole pairs and one more a sequence.
 inline int64_t chunk_pairs(const BatchView& b, int group) {
   return (int64_t)b.rows * group / kPairRows + (b.n < b.rows ? b.n : b.rows);

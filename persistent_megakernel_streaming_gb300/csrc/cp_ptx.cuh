@@ -103,6 +103,19 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t a, float x, float y, floa
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w)
                : "memory");
 }
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
 // Asynchronous store into (possibly another CTA's) shared memory that counts
 // its 16 bytes on the mbarrier `bar` (a shared::cluster address in the same CTA).
 __device__ __forceinline__ void st_async_v4(uint32_t a, float x, float y, float z, float w, uint32_t bar) {

@@ -284,6 +284,33 @@ def test_attend_long(e4m3, d, new):
 
 
 @pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("window", [0, 90])
+def test_attend_many_ragged_steps(e4m3, d, window):
+    """More items than are resident at once, cut into parts of which some sequences have many and some one."""
+    lengths = [1 + (i * 379) % 1500 for i in range(40)]
+    w = World(lengths, [1 + i % 3 for i in range(40)], 2, d, 32, e4m3, seed=8, pad=1).fill()
+    q, out = w.attend(4, window=window)
+    w.check(q, out, window=window)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+def test_attend_many_steps_ignore_what_is_masked(e4m3, d):
+    """As test_attend_ignores_what_is_masked, where the parts go through the workspace."""
+    lengths = [300 + i for i in range(40)]
+    w = World(lengths, [2] * 40, 1, d, 16, e4m3, seed=8).fill()
+    pool = [w.k.cpu().clone(), w.v.cpu().clone()]
+    for i, L in enumerate(lengths):         # the last position: the first of the two rows does not see it
+        for x in pool:
+            x[w.table[i, (L - 1) // 16], 0, (L - 1) % 16, 1] = 255 if e4m3 else -1
+    w.put(pool, [None if s is None else s.cpu() for s in (w.ks, w.vs)])
+    q, out = w.attend(2)
+    assert torch.isnan(out[1::2, :, 1]).all()
+    w.lengths, w.start, w.rows = [L - 1 for L in lengths], np.arange(41, dtype=np.int32), 40
+    w.kv = [(k[:-1], v[:-1]) for k, v in w.kv]
+    w.check(q[::2], out[::2])
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
 @pytest.mark.parametrize("new", [[1, 2], [70, 9]])
 def test_attend_sharp_and_scaled(e4m3, d, new):
     """Scores that grow along the sequence (the running maximum rises at every tile) and fall along it, sizes of
