@@ -14,8 +14,8 @@
 // while an issuer does anything else (measured: nothing of a gap between two
 // products of one warp is hidden, nearly all of it behind another warp's).
 // Warp 22 brings pages in through tensor maps, a lane a page. For each 128 positions S = Q K^T (128 x 128, fp32 in
-// TMEM); the softmax threads read their part of it twice (maximum, then
-// weights: it does not fit their registers), write the weights as 16 bit over
+// TMEM); the softmax threads read their part of it (over an e4m3 cache
+// twice: there it does not fit their registers), write the weights as 16 bit over
 // the S that they have read, and O += P V reads them from there. O stays in
 // TMEM for the whole pass. The reference of a row's weights is its first
 // tile's maximum; it is only moved, and O rescaled, when a later score has
@@ -24,10 +24,10 @@
 //
 // bf16 pages land in the ring as the tensor core reads them. Tiles at the ends
 // of what the block's rows see, and tiles that only some of them see, pass
-// warps 16-19 first: values that nobody sees are zeroed (a page may hold
+// the helpers first: values that nobody sees are zeroed (a page may hold
 // anything there), and values that some row must not see are looked over for
 // infinities and NaN. e4m3 pages land in a ring of their own and all pass
-// warps 16-19, which widen them to fp16 and multiply each row by its scale,
+// the helpers, which widen them to fp16 and multiply each row by its scale,
 // relative to the largest that the block has met and 2^kUp up: exact as long
 // as fp16 reaches, and what is lost below is 2^-25 of the largest row's
 // least bit. The power taken out of a tile's keys multiplies its scores, the
@@ -41,17 +41,18 @@ namespace {
 using namespace ptx;
 
 constexpr int kTile = 128;             // rows of a tile, and positions of one
-constexpr int kThreadsC = 704;
 constexpr int kSoftWarps = 16;         // softmax: eight a tile of rows
-constexpr int kHelper0 = 16;           // first of four helper warps
-constexpr int kHelpers = 128;
-constexpr int kMmaWarp = 20, kLoadWarp = 21;
+constexpr int kHelper0 = 16;           // first helper warp
 constexpr int kScaleSlots = 8;         // tiles whose scales are held: more than the ring's
 constexpr long long kWaitNs = 2000000000ll;
 
 // Loads are counted K of tile 0, V of tile 0, K of tile 1, ...; load n is in slot n % kOps.
 template <int D, bool E4M3>
 struct Cfg {
+  // four helper warps widen e4m3; bf16 needs few, and the softmax threads the registers
+  static constexpr int kHelpers = E4M3 ? 128 : 64;
+  static constexpr int kMmaWarp = kHelper0 + kHelpers / 32, kLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = (kLoadWarp + 1) * 32;
   static constexpr int kOpBytes = kTile * D * 2;        // one operand tile
   static constexpr int kSlab = kTile * 128;             // 64 columns of it
   static constexpr int kOps = D == 64 ? 8 : 4;
@@ -62,6 +63,13 @@ struct Cfg {
 // TMEM columns: the two tiles' scores (and weights), then their outputs
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 
+// What the end of a block needs, kept out of the registers meanwhile.
+struct Item {
+  Seq s;
+  int seq, kv, part, row0, rows_here, whole, t_begin, t_end, any[2], first_row, first_head;
+  uint32_t magic;
+};
+
 struct ChunkShared {
   uint64_t raw_full[8], raw_empty[8], op_full[8];
   uint64_t done[4];   // rounds of the MMA warp
@@ -71,6 +79,7 @@ struct ChunkShared {
   int abort;       // a wait gave up
   int bad;         // a value that some row must not see is not finite
   int kref[kScaleSlots], vref[kScaleSlots];    // e4m3: exponents taken out of a tile's keys and values
+  Item item;
   float row[2][kPairRows];     // what the two threads of a row tell each other; before that, [0]: e4m3's powers of
                                // two taken out of the rows of q, times the scale
 };
@@ -144,10 +153,10 @@ __device__ __forceinline__ uint32_t op_at(int r, int u) {
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid_constant__ AttendParams p,
+__global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel(const __grid_constant__ AttendParams p,
                                                                     const __grid_constant__ CacheMaps maps) {
   using C = Cfg<D, E4M3>;
-  constexpr int NO = C::kOps, NR = C::kRaws;
+  constexpr int NO = C::kOps, NR = C::kRaws, kHelpers = C::kHelpers, kMmaWarp = C::kMmaWarp, kLoadWarp = C::kLoadWarp;
   extern __shared__ __align__(1024) uint8_t raw[];
   uint8_t* ops = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   ChunkShared& sh = *reinterpret_cast<ChunkShared*>(ops + C::kTiles);
@@ -268,6 +277,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
 
   const uint32_t q_s = saddr(ops), op_s = q_s + 2 * C::kOpBytes, raw_s = E4M3 ? op_s + NO * C::kOpBytes : op_s;
 
+  // a softmax thread's part of q: 16 of its pair of warps' 32 rows, a row's units side by side; asked for here, so that
+  // it is there behind the barrier
+  constexpr int UPR = D / 8, RPI = 32 / UPR, N = 16 / RPI;
+  const int u = lane % UPR, base = (warp & 3) * 32 + ((warp >> 2) & 1) * 16 + lane / UPR;
+  uint4 x[N];
+  if (warp < kSoftWarps) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int r = (warp >> 3) * kTile + base + k * RPI;
+      x[k] = make_uint4(0, 0, 0, 0);
+      if (r < rows_here)
+        x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.row0 + new_row(r)) * p.q_row +
+                                               (int64_t)(kv * p.group + head_of(r)) * p.q_head + u * 8);
+    }
+  }
+  if (threadIdx.x == 0)
+    sh.item = {s, seq, kv, part, row0, rows_here, whole, t_begin, t_end, {je[0] > jb[0], je[1] > jb[1]}, first_row, first_head, magic};
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -288,21 +314,9 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
   if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
     {
-      // 16 of the pair's 32 rows, a row's units side by side; e4m3's q in fp16 times a power of two of its row
-      constexpr int UPR = D / 8, RPI = 32 / UPR, N = 16 / RPI;
-      const int u = lane % UPR, base = (warp & 3) * 32 + half * 16 + lane / UPR;
-      uint4 x[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) {
-        const int r = i * kTile + base + k * RPI;
-        x[k] = make_uint4(0, 0, 0, 0);
-        if (r < rows_here)
-          x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.row0 + new_row(r)) * p.q_row +
-                                                 (int64_t)(kv * p.group + head_of(r)) * p.q_head + u * 8);
-      }
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        if (E4M3) {
+        if (E4M3) {                        // in fp16, times a power of two of its row
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           int top = 0;
 #pragma unroll
@@ -351,23 +365,38 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
           }
         }
       };
-      uint32_t x[32];
+      auto top_of = [&](const uint32_t* x) {
+        float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
+#pragma unroll
+        for (int k = 2; k < 32; k += 2) {
+          a = fmaxf(a, __uint_as_float(x[k]));
+          b = fmaxf(b, __uint_as_float(x[k + 1]));
+        }
+        return fmaxf(a, b);
+      };
+      // bf16's threads have the registers to read their 64 scores once, e4m3's read them twice
+      constexpr bool kOnce = !E4M3;
+      uint32_t x[kOnce ? 64 : 32];
       float top = -INFINITY;
       if (ok) {
-#pragma unroll 1
-        for (int c = 0; c < kHalf; c += 32) {
-          tm_ld32_start(s_t + c, x);
+        if (kOnce) {
+          tm_ld32_start(s_t, x);
+          tm_ld32_start(s_t + 32, x + (kOnce ? 32 : 0));
           tm_ld32_wait(x);
-          ready(x, c);
-          float a = __uint_as_float(x[0]), b = __uint_as_float(x[1]);
-#pragma unroll
-          for (int k = 2; k < 32; k += 2) {
-            a = fmaxf(a, __uint_as_float(x[k]));
-            b = fmaxf(b, __uint_as_float(x[k + 1]));
+          tm_ld32_wait(x + (kOnce ? 32 : 0));
+          ready(x, 0);
+          ready(x + (kOnce ? 32 : 0), 32);
+          top = fmaxf(top_of(x), top_of(x + (kOnce ? 32 : 0)));
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < kHalf; c += 32) {
+            tm_ld32_start(s_t + c, x);
+            tm_ld32_wait(x);
+            ready(x, c);
+            top = fmaxf(top, top_of(x));
           }
-          top = fmaxf(top, fmaxf(a, b));
+          tm_ld32_start(s_t, x);           // the first of the second pass
         }
-        tm_ld32_start(s_t, x);             // the first of the second pass
         top *= rs;
       }
       if (pair_or(pair_id, !ok || top > m + kLazy || vn != vr)) {
@@ -384,24 +413,22 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
         if (E4M3) f *= pow2i(max(vr - vn, -127));          // a larger value scale
         vr = vn;
         if (n > 0) {
-          tm_ld32_wait(x);
+          if (!kOnce) tm_ld32_wait(x);
 #pragma unroll 1
-          for (int c = 0; c < D / 2; c += 32) {
-            float v[32];
-            tm_ld32(o_t + c, v);
+          for (int c = 0; c < D / 2; c += 16) {
+            float v[16];
+            uint32_t w[16];
+            tm_ld16(o_t + c, v);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) v[k] *= f;
-            tm_st32(o_t + c, v);
+            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(v[k] * f);
+            tm_st16(o_t + c, w);
           }
-          tm_ld32_start(s_t, x);
+          if (!kOnce) tm_ld32_start(s_t, x);
         }
       }
       const float ref = (m == -INFINITY ? 0.f : m) - kBias;
       const uint64_t rs2 = pair_of(rs, rs), ref2 = pair_of(-ref, -ref);
-#pragma unroll 1
-      for (int c = 0; c < kHalf; c += 32) {
-        tm_ld32_wait(x);
-        ready(x, c);
+      auto weigh = [&](uint32_t* x, int c) {
         uint32_t w[16];
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -415,8 +442,19 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
           w[k / 2] = E4M3 ? hf_pack(y[0], y[1]) : bf_pack(y[0], y[1]);
           w[k / 2 + 1] = E4M3 ? hf_pack(y[2], y[3]) : bf_pack(y[2], y[3]);
         }
-        if (c + 32 < kHalf) tm_ld32_start(s_t + c + 32, x);
+        if (!kOnce && c + 32 < kHalf) tm_ld32_start(s_t + c + 32, x);
         tm_st16(s_t + c / 2, w);
+      };
+      if (kOnce) {
+        weigh(x, 0);
+        weigh(x + (kOnce ? 32 : 0), 32);
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < kHalf; c += 32) {
+          tm_ld32_wait(x);
+          ready(x, c);
+          weigh(x, c);
+        }
       }
       tm_wait_st();
       tm_fence_before();
@@ -646,12 +684,23 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
 
   const bool failed = sh.abort != 0;
   if (failed && threadIdx.x == 0) set_status(p.c.status, CP_ERR_TIMEOUT);
+  const Item& it = sh.item;
   if (!failed && sh.bad) {
-    plain_rows<D, E4M3>(p, s, seq, kv, row0, row0 + rows_here, t_begin, t_end, part, whole, warp, kThreadsC / 32);
+    plain_rows<D, E4M3>(p, it.s, it.seq, it.kv, it.row0, it.row0 + it.rows_here, it.t_begin, it.t_end, it.part, it.whole, warp,
+                        C::kThreads / 32);
   } else if (!failed && warp < kSoftWarps) {
     // rows leave through the operands' memory, so that a row is written at once and not by its threads piece by piece
-    const uint32_t o_t = tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + i * D + half * (D / 2);
-    const bool any = i ? je[1] > jb[1] : je[0] > jb[0];
+    const int slot = threadIdx.x / 256 * kTile + (threadIdx.x & 127), half = (warp >> 2) & 1, i = warp >> 3;
+    const int pair_id = 1 + i * 4 + (warp & 3);
+    const uint32_t o_t = sh.tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + i * D + half * (D / 2);
+    const bool any = it.any[i];
+    const int group = p.group, first_row = it.first_row, first_head = it.first_head, head0 = it.kv * group;
+    const uint32_t magic = it.magic;
+    auto place = [&](int r, int64_t* row, int* head) {
+      const int q = (int)(((uint32_t)(first_head + r) * magic) >> 16);
+      *row = it.s.row0 + first_row + q;
+      *head = head0 + first_head + r - q * group;
+    };
     l = sh.row[0][slot] + sh.row[1][slot];
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float e = E4M3 ? pow2i(min(max(vr - kUp, -126), 127)) : 1.f;
@@ -669,23 +718,40 @@ __global__ void __launch_bounds__(kThreadsC, 1) attend_chunk_kernel(const __grid
         *reinterpret_cast<float4*>(stage + lane * kPitch + half * (D / 2) + c + x) = y;
       }
     }
-    if (mine && !whole && half == 0)
-      store_lse(p, part, s.row0 + new_row(slot), kv * p.group + head_of(slot), l == 0.f ? -INFINITY : m + log2f(l) - kBias);
+    int64_t row;
+    int head;
+    if (slot < it.rows_here && !it.whole && half == 0) {
+      place(slot, &row, &head);
+      store_lse(p, it.part, row, head, l == 0.f ? -INFINITY : m + log2f(l) - kBias);
+    }
     tm_fence_before();
     pair_or(pair_id, false);
+    // a row at a time (two of 64 columns), the next row's place by counting on
     constexpr int LPR = D / 4, RPI = 32 / LPR;
-    const int first = i * kTile + (warp & 3) * 32;
-#pragma unroll 8
-    for (int k = 0; k < 16 / RPI; ++k) {
-      const int r = half * 16 + k * RPI + lane / LPR, d = lane % LPR * 4;
-      if (first + r < rows_here)
-        store4<D>(p, part, whole, s.row0 + new_row(first + r), kv * p.group + head_of(first + r), d, stage + r * kPitch + d);
+    const int r0 = half * 16 + lane / LPR, d = lane % LPR * 4;
+    int left = it.rows_here - (i * kTile + (warp & 3) * 32 + r0);
+    place(i * kTile + (warp & 3) * 32 + r0, &row, &head);
+    head -= head0;
+    const float* src = stage + r0 * kPitch + d;
+    const int64_t o_row = p.o_row, o_head = p.o_head;
+    uint16_t* out = p.out + head0 * o_head + d;
+    float* part_o = p.part_o + ((int64_t)it.part * p.b.rows * p.q_heads + head0) * D + d;
+    const bool whole = it.whole;
+#pragma unroll 4
+    for (int k = 0; k < 16; k += RPI, left -= RPI, src += RPI * kPitch) {
+      if (left > 0) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        if (whole) *reinterpret_cast<uint2*>(out + row * o_row + head * o_head) = make_uint2(bf_pack(y.x, y.y), bf_pack(y.z, y.w));
+        else *reinterpret_cast<float4*>(part_o + (row * p.q_heads + head) * D) = y;
+      }
+      head += RPI;
+      for (; head >= group; head -= group) ++row;
     }
   }
   __syncthreads();
   if (warp == kMmaWarp) {
     tm_fence_after();
-    tm_dealloc(tmem, kTmemCols);
+    tm_dealloc(sh.tmem, kTmemCols);
   }
   pdl_wait();            // this grid's end stands for the step kernel's too
 }
@@ -707,11 +773,11 @@ template <int D, bool E4M3>
 static cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   const dim3 grid((unsigned)(p.c.heads * chunk_pairs(p.b, p.group)), p.a.chunk_parts);
   if (!p.a.use_step) {
-    attend_chunk_kernel<D, E4M3><<<grid, kThreadsC, Smem<D, E4M3>::kBytes, s>>>(p, maps);
+    attend_chunk_kernel<D, E4M3><<<grid, Cfg<D, E4M3>::kThreads, Smem<D, E4M3>::kBytes, s>>>(p, maps);
     return cudaGetLastError();
   }
   // behind the step kernel, whose results it does not need: it may fill the SMs that one leaves
-  return launch_pdl(attend_chunk_kernel<D, E4M3>, grid, kThreadsC, Smem<D, E4M3>::kBytes, s, p, maps);
+  return launch_pdl(attend_chunk_kernel<D, E4M3>, grid, Cfg<D, E4M3>::kThreads, Smem<D, E4M3>::kBytes, s, p, maps);
 }
 cudaError_t launch_attend_chunk(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s) {
   if (head_dim == 128) return e4m3 ? launch<128, true>(p, maps, s) : launch<128, false>(p, maps, s);
