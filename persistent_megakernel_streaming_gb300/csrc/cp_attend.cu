@@ -31,7 +31,9 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
   if (window > 0) span = std::min<int64_t>(span, (int64_t)window + rows + kStepAlign - 1);
   const int tile = step_tile(head_dim, e4m3);
   const int64_t items = (int64_t)b.n * kv_heads;
-  const int64_t want = std::max<int64_t>(1, kStepBlocks * 8 / items);
+  // two rounds of blocks if every sequence were the longest: 4, 8 and 16 rounds (a better balance, more starts and
+  // joins) measured up to 4, 2 and 6 % slower on ragged batches of 64 and 10 to 20 % on few long or equal sequences
+  const int64_t want = std::max<int64_t>(1, kStepBlocks * 2 / items);
   int64_t chunk = (span + want - 1) / want;
   chunk = std::min<int64_t>(std::max<int64_t>((chunk + tile - 1) / tile * tile, tile), kMaxStepChunk);
   // A call whose blocks are all resident at once may join an item's parts within a cluster, through shared memory,
@@ -41,6 +43,7 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
     chunk = std::max<int64_t>((span + kStepCluster - 1) / kStepCluster + tile - 1, tile) / tile * tile;
     a.step_cluster = 1;
   }
+  a.step_wide = rows * group > 8;
   a.step_chunk = (int)chunk;
   a.step_parts = a.use_step ? (int)std::max<int64_t>(1, (span + chunk - 1) / chunk) : 0;
   if (a.use_chunk) {
@@ -98,6 +101,12 @@ __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t* r) {
 __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+// The 8 x 8 matrix of 16-bit elements whose row i lanes 4i .. 4i+3 hold, transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
 }
 template <bool HALF>
 __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -165,25 +174,32 @@ __device__ __forceinline__ void join_cluster(const AttendParams& p, const Seq& s
 // One block a (part, kv head, sequence); its four warps take the part's tiles
 // in turn, each with a running maximum, sum and product of its own and its own
 // ring of asynchronous copies, so that nothing in the loop waits for another
-// warp; they are joined once at the end. The 16 rows of the matrix
-// instruction are the sequence's rows times the kv head's query heads.
+// warp; they are joined once at the end.
+//
+// The products are transposed, positions (and then columns of v) along the 16
+// rows of the matrix instruction and the sequence's rows times the kv head's
+// query heads along its columns: 8 of them, NT times. S^T = K q^T takes keys as
+// they lie, O^T = V^T P^T values transposed on their way out of shared memory;
+// S^T's layout is a transposition of 8 x 8 away from P^T's. (With the rows
+// along the 16, steps of two heads spent twice the instructions and registers
+// on rows that are not there: 64 sequences of 500 to 12001 e4m3
+// positions 151 us, now 137; 5.9 TB/s.)
 //
 // K and V go to shared memory as they lie (16-byte units exchanged within a
-// row so that ldmatrix meets no bank twice) and from there into mma fragments:
-// keys as they are, values transposed on the way. e4m3 is widened to fp16 in
+// row so that ldmatrix meets no bank twice). e4m3 is widened to fp16 in
 // registers (exact): q is fp16 times a power of two of its row, the key's
 // scale multiplies the score, the value's scale the weight, relative to the
 // largest seen (so that weight * scale stays in fp16's range; weights start
 // at 2^8 to use it). A 4-byte fragment of e4m3 is four neighbouring elements
 // where the instruction wants two and two: the sum over the head does not
-// mind the order, so q is loaded in it, and the output columns come out
-// four neighbours a thread.
-template <int D, bool E4M3, bool CLUSTER>
+// mind the order, so q is loaded in it, and two neighbouring columns of v
+// become rows 8 apart.
+template <int D, bool E4M3, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const __grid_constant__ AttendParams p) {
   constexpr int TK = (E4M3 ? 32 : 16) * (128 / D);    // positions a tile
   constexpr int ES = E4M3 ? 1 : 2;
   constexpr int UPR = D * ES / 16;                    // 16-byte units a row: 16, 8 or 4
-  constexpr int NT = TK / 8;                          // score tiles of 8 positions
+  constexpr int MT = TK / 16;                         // score tiles of 16 positions
   constexpr int KS = D / 16;                          // steps over the head
   constexpr int RPL = 32 / UPR;                       // rows that one copy of the warp covers
   extern __shared__ __align__(128) uint8_t ring[];
@@ -264,21 +280,24 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
     cp_commit();
   };
 
-  // q fragments, and for e4m3 the power of two taken out of each row
-  uint32_t qf[KS][4];
-  float qs[2] = {p.scale_log2, p.scale_log2};
+  // q fragments, and for e4m3 the power of two taken out of each row; this thread's columns of the scores are rows
+  // 8 n + 2 c and 8 n + 2 c + 1
+  uint32_t qf[KS][NT][2];
+  float qs[NT][2];
+  int lo[NT][2], hi[NT][2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = g + half * 8;
+  for (int n = 0; n < NT; ++n) {
+    const int r = n * 8 + g;
     const bool on = r < nrows;
     const uint16_t* qp = p.q + (int64_t)(s.row0 + (on ? r / p.group : 0)) * p.q_row +
                          (int64_t)(kv * p.group + (on ? r % p.group : 0)) * p.q_head;
     if (!E4M3) {
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        qf[k][half] = on ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 2 * c) : 0u;
-        qf[k][half + 2] = on ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8 + 2 * c) : 0u;
+        qf[k][n][0] = on ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 2 * c) : 0u;
+        qf[k][n][1] = on ? *reinterpret_cast<const uint32_t*>(qp + k * 16 + 8 + 2 * c) : 0u;
       }
+      qs[n][0] = qs[n][1] = p.scale_log2;
     } else {
       uint2 raw[KS];
       int top = 0;
@@ -296,28 +315,33 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = min(max(top - 127, -100), 100);
       const float inv = pow2i(-e);
-      qs[half] = p.scale_log2 * pow2i(e);
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
-        qf[k][half] = hf_pack(bf_lo(raw[k].x) * inv, bf_hi(raw[k].x) * inv);
-        qf[k][half + 2] = hf_pack(bf_lo(raw[k].y) * inv, bf_hi(raw[k].y) * inv);
+        qf[k][n][0] = hf_pack(bf_lo(raw[k].x) * inv, bf_hi(raw[k].x) * inv);
+        qf[k][n][1] = hf_pack(bf_lo(raw[k].y) * inv, bf_hi(raw[k].y) * inv);
       }
-    }
-  }
-  // the positions that this thread's two rows see
-  int lo[2], hi[2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = g + half * 8;
-    if (r < nrows) visible(p, s.first + r / p.group, s.len, &lo[half], &hi[half]);
-    else lo[half] = hi[half] = 0;
+      for (int j = 0; j < 2; ++j) qs[n][j] = p.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, (2 * c + j) * 4));
+    }
+    // the positions that the columns' rows see
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int row = n * 8 + 2 * c + j;
+      lo[n][j] = hi[n][j] = 0;
+      if (row < nrows) visible(p, s.first + row / p.group, s.len, &lo[n][j], &hi[n][j]);
+    }
   }
 
   constexpr float kBias = E4M3 ? 8.f : 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  float o[D / 8][4];
+  float m[NT][2], l[NT][2];
+  float o[D / 16][NT][4];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  for (int n = 0; n < NT; ++n) {
+    m[n][0] = m[n][1] = -INFINITY;
+    l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+  }
   int ev_ref = -1000;
   bool bad = false;
 
@@ -327,8 +351,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
     for (int x = 0; x < 2; ++x) ks_cur[x] = ks_next[x], vs_cur[x] = vs_next[x];
     issue(i);
   }
-  for (int i = 0; i < mine; ++i) {
-    const int t0 = t_begin + (i * kStepWarps + warp) * TK;
+  for (int it = 0; it < mine; ++it) {
+    const int t0 = t_begin + (it * kStepWarps + warp) * TK;
     if (E4M3) {
       // this tile's scales to shared memory, where the lanes find the ones of their columns
       int ek[2], ev[2];
@@ -346,7 +370,9 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
       if (ref != ev_ref) {
         const float f = pow2i(max(ev_ref - ref, -127));
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][0] *= f, o[n][1] *= f, o[n][2] *= f, o[n][3] *= f;
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[i][n][0] *= f, o[i][n][1] *= f, o[i][n][2] *= f, o[i][n][3] *= f;
         ev_ref = ref;
       }
 #pragma unroll
@@ -357,7 +383,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
     }
     cp_wait<kStages - 2>();
     __syncwarp();
-    const uint32_t tile = my_ring + (i % kStages) * kStageBytes;
+    const uint32_t tile = my_ring + (it % kStages) * kStageBytes;
     const uint32_t vtile = tile + kStageBytes / 2;
     const bool edge = t0 < lo_all || t0 + TK > hi_all;
     if (edge && nrows > p.group) {
@@ -367,117 +393,126 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
         bad |= any_nonfinite<E4M3>(vtile + row * (UPR * 16) + u * 16);
     }
     // scores
-    float sc[NT][4];
+    float sc[MT][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sc[i][n][0] = sc[i][n][1] = sc[i][n][2] = sc[i][n][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       if (!E4M3) {
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t b[4];
-          const int row = n * 8 + (lane >> 4) * 8 + (lane & 7), unit = k * 2 + ((lane >> 3) & 1);
-          ldsm4(tile + row * (UPR * 16) + swz(row, unit) * 16, b);
-          mma16816<false>(sc[n], qf[k], b[0], b[1]);
-          mma16816<false>(sc[n + 1], qf[k], b[2], b[3]);
+        for (int i = 0; i < MT; ++i) {
+          uint32_t a[4];
+          const int row = i * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), unit = k * 2 + (lane >> 4);
+          ldsm4(tile + row * (UPR * 16) + swz(row, unit) * 16, a);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<false>(sc[i][n], a, qf[k][n][0], qf[k][n][1]);
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < NT; n += 4) {
+        for (int i = 0; i < MT; i += 2) {
           uint32_t b[4];
-          const int row = n * 8 + lane;
+          const int row = i * 16 + lane;
           ldsm4(tile + row * (UPR * 16) + swz(row, k) * 16, b);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma16816<true>(sc[n + j], qf[k], e4m3x2_f16x2(b[j] & 0xffffu), e4m3x2_f16x2(b[j] >> 16));
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {e4m3x2_f16x2(b[2 * h] & 0xffffu), e4m3x2_f16x2(b[2 * h + 1] & 0xffffu),
+                                   e4m3x2_f16x2(b[2 * h] >> 16), e4m3x2_f16x2(b[2 * h + 1] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<true>(sc[i + h][n], a, qf[k][n][0], qf[k][n][1]);
+          }
         }
       }
     }
     // scale, mask, running maximum
-    float mx[2] = {m[0], m[1]};
+    float mx[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float2 fk = make_float2(1.f, 1.f);
-      if (E4M3) fk = *reinterpret_cast<const float2*>(&sh.scale_k[warp][n * 8 + 2 * c]);
+    for (int n = 0; n < NT; ++n) mx[n][0] = m[n][0], mx[n][1] = m[n][1];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sc[n][j] = sc[n][j] * qs[j >> 1] * (j & 1 ? fk.y : fk.x);
-        const int t = t0 + n * 8 + 2 * c + (j & 1);
-        if (edge && (t < lo[j >> 1] || t >= hi[j >> 1])) sc[n][j] = -INFINITY;
-        mx[j >> 1] = fmaxf(mx[j >> 1], sc[n][j]);
-      }
+    for (int i = 0; i < MT; ++i) {
+      float fk[2] = {1.f, 1.f};
+      if (E4M3) fk[0] = sh.scale_k[warp][i * 16 + g], fk[1] = sh.scale_k[warp][i * 16 + 8 + g];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sc[i][n][j] *= E4M3 ? qs[n][j & 1] * fk[j >> 1] : qs[n][j & 1];
+          const int t = t0 + i * 16 + (j >> 1) * 8 + g;
+          if (edge && (t < lo[n][j & 1] || t >= hi[n][j & 1])) sc[i][n][j] = -INFINITY;
+          mx[n][j & 1] = fmaxf(mx[n][j & 1], sc[i][n][j]);
+        }
     }
-    float ref[2];
+    float ref[NT][2];
     bool moved = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-      moved |= mx[h] > m[h];
-      ref[h] = (mx[h] == -INFINITY ? 0.f : mx[h]) - kBias;
-    }
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mx[n][j] = fmaxf(mx[n][j], __shfl_xor_sync(0xffffffffu, mx[n][j], x));
+        moved |= mx[n][j] > m[n][j];
+        ref[n][j] = (mx[n][j] == -INFINITY ? 0.f : mx[n][j]) - kBias;
+      }
     if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float f = mx[h] == m[h] ? 1.f : ex2(m[h] - mx[h]);
-        l[h] *= f;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
-        m[h] = mx[h];
-      }
-    }
-    // weights
-    uint32_t pf[NT][2];
+        for (int j = 0; j < 2; ++j) {
+          const float f = mx[n][j] == m[n][j] ? 1.f : ex2(m[n][j] - mx[n][j]);
+          l[n][j] *= f;
+          m[n][j] = mx[n][j];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        w[j] = ex2(sc[n][j] - ref[j >> 1]);
-        l[j >> 1] += w[j];
-      }
-      if (E4M3) {
-        const float2 fv = *reinterpret_cast<const float2*>(&sh.scale_v[warp][n * 8 + 2 * c]);
-        pf[n][0] = hf_pack(w[0] * fv.x, w[1] * fv.y);
-        pf[n][1] = hf_pack(w[2] * fv.x, w[3] * fv.y);
-      } else {
-        pf[n][0] = bf_pack(w[0], w[1]);
-        pf[n][1] = bf_pack(w[2], w[3]);
-      }
-    }
-    // weights times values
-#pragma unroll
-    for (int k = 0; k < TK / 16; k += E4M3 ? 2 : 1) {
-      if (!E4M3) {
-        const uint32_t a[4] = {pf[2 * k][0], pf[2 * k][1], pf[2 * k + 1][0], pf[2 * k + 1][1]};
-#pragma unroll
-        for (int n = 0; n < D / 8; n += 2) {
-          uint32_t b[4];
-          const int row = k * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), unit = n + (lane >> 4);
-          ldsm4t(vtile + row * (UPR * 16) + swz(row, unit) * 16, b);
-          mma16816<false>(o[n], a, b[0], b[1]);
-          mma16816<false>(o[n + 1], a, b[2], b[3]);
+          for (int i = 0; i < D / 16; ++i) o[i][n][j] *= f, o[i][n][2 + j] *= f;
         }
-      } else {
-        const uint32_t a0[4] = {pf[2 * k][0], pf[2 * k][1], pf[2 * k + 1][0], pf[2 * k + 1][1]};
-        const uint32_t a1[4] = {pf[2 * k + 2][0], pf[2 * k + 2][1], pf[2 * k + 3][0], pf[2 * k + 3][1]};
+    }
+    // weights, and from (position, row) to (row, position)
+    uint32_t pf[MT][NT][2];
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          uint32_t b[4];
-          const int row = k * 16 + lane;
-          ldsm4t(vtile + row * (UPR * 16) + swz(row, n) * 16, b);
+    for (int i = 0; i < MT; ++i) {
+      float fv[2] = {1.f, 1.f};
+      if (E4M3) fv[0] = sh.scale_v[warp][i * 16 + g], fv[1] = sh.scale_v[warp][i * 16 + 8 + g];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = ex2(sc[i][n][j] - ref[n][j & 1]);
+          l[n][j & 1] += w[j];
+        }
+        pf[i][n][0] = transposed(E4M3 ? hf_pack(w[0] * fv[0], w[1] * fv[0]) : bf_pack(w[0], w[1]));
+        pf[i][n][1] = transposed(E4M3 ? hf_pack(w[2] * fv[1], w[3] * fv[1]) : bf_pack(w[2], w[3]));
+      }
+    }
+    // values times weights
+#pragma unroll
+    for (int i = 0; i < MT; i += E4M3 ? 2 : 1) {
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        uint32_t b[4];
+        if (!E4M3) {
+          const int row = i * 16 + (lane >> 4) * 8 + (lane & 7), unit = d * 2 + ((lane >> 3) & 1);
+          ldsm4t(vtile + row * (UPR * 16) + swz(row, unit) * 16, b);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<false>(o[d][n], b, pf[i][n][0], pf[i][n][1]);
+        } else {
+          const int row = i * 16 + lane;
+          ldsm4t(vtile + row * (UPR * 16) + swz(row, d) * 16, b);
           // a register: two columns of position 2c, then of 2c + 1; split by column
 #pragma unroll
           for (int j = 0; j < 4; ++j) b[j] = __byte_perm(b[j], 0, 0x3120);
-          mma16816<true>(o[2 * n], a0, e4m3x2_f16x2(b[0] & 0xffffu), e4m3x2_f16x2(b[1] & 0xffffu));
-          mma16816<true>(o[2 * n + 1], a0, e4m3x2_f16x2(b[0] >> 16), e4m3x2_f16x2(b[1] >> 16));
-          mma16816<true>(o[2 * n], a1, e4m3x2_f16x2(b[2] & 0xffffu), e4m3x2_f16x2(b[3] & 0xffffu));
-          mma16816<true>(o[2 * n + 1], a1, e4m3x2_f16x2(b[2] >> 16), e4m3x2_f16x2(b[3] >> 16));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {e4m3x2_f16x2(b[2 * h] & 0xffffu), e4m3x2_f16x2(b[2 * h] >> 16),
+                                   e4m3x2_f16x2(b[2 * h + 1] & 0xffffu), e4m3x2_f16x2(b[2 * h + 1] >> 16)};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<true>(o[d][n], a, pf[(i + h) % MT][n][0], pf[(i + h) % MT][n][1]);
+          }
         }
       }
     }
     __syncwarp();
-    issue(i + kStages - 1);
+    issue(it + kStages - 1);
   }
   cp_wait<0>();
   const bool whole = parts <= 1;
@@ -492,28 +527,29 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
 
   // join the warps: each leaves its average and its sum, the block weighs them
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-    const int r = g + h * 8;
-    if (c == 0) {
-      sh.m[warp][r] = m[h];
-      sh.l[warp][r] = l[h];
-    }
-    const float f = l[h] == 0.f ? 0.f : 1.f / l[h];
-    const float e = E4M3 ? pow2i(min(max(ev_ref, -126), 127)) : 1.f;
-    float* dst = reinterpret_cast<float*>(ring) + (warp * kStepRows + r) * (D + 4);
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int n = 0; n < D / 8; n += 2) {
-      if (!E4M3) {
-        *reinterpret_cast<float2*>(dst + n * 8 + 2 * c) = make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
-        *reinterpret_cast<float2*>(dst + n * 8 + 8 + 2 * c) = make_float2(o[n + 1][2 * h] * f, o[n + 1][2 * h + 1] * f);
-      } else {
-        *reinterpret_cast<float4*>(dst + n * 8 + 4 * c) =
-            make_float4(o[n][2 * h] * f * e, o[n + 1][2 * h] * f * e, o[n][2 * h + 1] * f * e, o[n + 1][2 * h + 1] * f * e);
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[n][j] += __shfl_xor_sync(0xffffffffu, l[n][j], x);
+      const int r = n * 8 + 2 * c + j;
+      if (g == 0) {
+        sh.m[warp][r] = m[n][j];
+        sh.l[warp][r] = l[n][j];
+      }
+      const float f = l[n][j] == 0.f ? 0.f : 1.f / l[n][j];
+      const float e = E4M3 ? pow2i(min(max(ev_ref, -126), 127)) : 1.f;
+      float* dst = reinterpret_cast<float*>(ring) + (warp * kStepRows + r) * (D + 4);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        if (E4M3) {
+          *reinterpret_cast<float2*>(dst + i * 16 + 2 * g) = make_float2(o[i][n][j] * f * e, o[i][n][2 + j] * f * e);
+        } else {
+          dst[i * 16 + g] = o[i][n][j] * f;
+          dst[i * 16 + 8 + g] = o[i][n][2 + j] * f;
+        }
       }
     }
-  }
   __syncthreads();
   constexpr int TPR = kStepWarps * 32 / kStepRows;    // threads a row
   const int r = threadIdx.x / TPR, d0 = threadIdx.x % TPR * 4;
@@ -610,12 +646,17 @@ template <int D, bool E4M3>
 cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   if (p.a.use_step) {
     const dim3 blocks(p.a.step_parts, p.c.heads, p.b.n);
+    constexpr int threads = kStepWarps * 32;
+    cudaError_t e = cudaSuccess;
     if (p.a.step_cluster) {
-      const cudaError_t e = launch_cluster(attend_step_kernel<D, E4M3, true>, blocks, p.a.step_parts, kStepWarps * 32, kStepSmem, s, p);
-      if (e != cudaSuccess) return e;
+      e = p.a.step_wide ? launch_cluster(attend_step_kernel<D, E4M3, 2, true>, blocks, p.a.step_parts, threads, kStepSmem, s, p)
+                        : launch_cluster(attend_step_kernel<D, E4M3, 1, true>, blocks, p.a.step_parts, threads, kStepSmem, s, p);
+    } else if (p.a.step_wide) {
+      attend_step_kernel<D, E4M3, 2, false><<<blocks, threads, kStepSmem, s>>>(p);
     } else {
-      attend_step_kernel<D, E4M3, false><<<blocks, kStepWarps * 32, kStepSmem, s>>>(p);
+      attend_step_kernel<D, E4M3, 1, false><<<blocks, threads, kStepSmem, s>>>(p);
     }
+    if (e != cudaSuccess) return e;
   }
   const int64_t units = (int64_t)p.b.rows * p.q_heads;
   const unsigned grid = (unsigned)((units + 7) / 8);
@@ -632,8 +673,12 @@ cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s)
 
 template <int D, bool E4M3>
 cudaError_t prepare() {
-  const cudaError_t e = cudaFuncSetAttribute(attend_step_kernel<D, E4M3, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(attend_step_kernel<D, E4M3, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
+  for (const void* f : {(const void*)attend_step_kernel<D, E4M3, 1, false>, (const void*)attend_step_kernel<D, E4M3, 1, true>,
+                        (const void*)attend_step_kernel<D, E4M3, 2, false>, (const void*)attend_step_kernel<D, E4M3, 2, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kStepSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace

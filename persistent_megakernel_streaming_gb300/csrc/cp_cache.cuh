@@ -119,6 +119,7 @@ constexpr int kStepAlign = 16, kChunkAlign = 128;   // where an item's parts may
 struct AttendPlan {
   int use_step, use_chunk;
   int step_chunk, step_parts;     // positions a part, most parts of an item
+  int step_wide;                  // items of more than 8 rows
   int step_cluster;               // the parts of a step item are one cluster's blocks, which join them
   int chunk_chunk, chunk_parts;
 };
