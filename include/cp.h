@@ -374,6 +374,13 @@ typedef struct cp_cache_desc {
   uint8_t* k_scale;           /* device, CP_CACHE_E4M3 only (else NULL)      */
   uint8_t* v_scale;
   int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+  int64_t timeout_ns;         /* give up a wait inside cp_cache_attend after
+                                 this long (0 = default 2 s)                 */
+  int debug_stall;            /* testing: nonzero makes each block of
+                                 cp_cache_attend that brings pages in through
+                                 a ring (more than 16 rows a kv head) leave
+                                 out its first load, so that the waits for it
+                                 run out and set CP_ERR_TIMEOUT              */
 } cp_cache_desc;
 
 /* A ragged batch. Sequence i has the rows start[i] .. start[i+1]-1 of the
@@ -470,7 +477,8 @@ int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, 
  * in it between calls; calls that may overlap, captured ones included, need
  * workspaces of their own. q and out are 16-byte aligned, strides multiples
  * of 8 elements. Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA;
- * a wait inside the kernel that gives up sets the sticky CP_ERR_TIMEOUT. */
+ * a wait inside the kernel that gives up sets the sticky CP_ERR_TIMEOUT, and
+ * what that call leaves in out is not specified. */
 int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, void* workspace,
                     size_t workspace_bytes, cp_stream_t stream);
 

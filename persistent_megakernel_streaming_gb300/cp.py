@@ -73,7 +73,7 @@ class CacheDesc(C.Structure):
                 ("pages", C.c_int), ("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
                 ("head_stride", C.c_int64), ("token_stride", C.c_int64), ("k_scale", C.c_void_p),
                 ("v_scale", C.c_void_p), ("scale_page_stride", C.c_int64), ("scale_head_stride", C.c_int64),
-                ("scale_token_stride", C.c_int64)]
+                ("scale_token_stride", C.c_int64), ("timeout_ns", C.c_int64), ("debug_stall", C.c_int)]
 
 
 class BatchDesc(C.Structure):
@@ -303,7 +303,7 @@ class Cache:
     ``k_scale``, ``v_scale`` uint8 [pages][kv_heads][page_size]; both of the same strides. See include/cp.h for
     what the calls compute."""
 
-    def __init__(self, k, v, k_scale=None, v_scale=None):
+    def __init__(self, k, v, k_scale=None, v_scale=None, timeout_ns: int = 0, debug_stall: bool = False):
         size = k.element_size()
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.device != v.device or \
                 k.device.type != "cuda":
@@ -323,7 +323,8 @@ class Cache:
         self.device, self.device_index = k.device, k.get_device()
         self.layout = (size, self.kv_heads, self.head_dim, self.page_size)
         self.desc = CacheDesc(int(size == 1), self.kv_heads, self.head_dim, self.page_size, self.pages, _ptr(k), _ptr(v),
-                              *(_stride(k, i) for i in range(3)), _ptr(k_scale), _ptr(v_scale), *scale_strides)
+                              *(_stride(k, i) for i in range(3)), _ptr(k_scale), _ptr(v_scale), *scale_strides,
+                              timeout_ns, int(debug_stall))
         h = C.c_void_p()
         _check(lib().cp_cache_create(C.byref(self.desc), k.device.index, C.byref(h)), "cp_cache_create")
         self._h = h

@@ -44,7 +44,6 @@ constexpr int kTile = 128;             // rows of a tile, and positions of one
 constexpr int kSoftWarps = 16;         // softmax: eight a tile of rows
 constexpr int kHelper0 = 16;           // first helper warp
 constexpr int kScaleSlots = 8;         // tiles whose scales are held: more than the ring's
-constexpr long long kWaitNs = 2000000000ll;
 
 // Loads are counted K of tile 0, V of tile 0, K of tile 1, ...; load n is in slot n % kOps.
 template <int D, bool E4M3>
@@ -74,8 +73,8 @@ struct ChunkShared {
   uint64_t raw_full[8], raw_empty[8], op_full[8];
   uint64_t done[4];   // rounds of the MMA warp
   uint64_t q_full, s_full[2], p_full[2], o_full;
-  uint64_t turn[2];   // whose products come next
   uint32_t tmem;
+  long long timeout_ns;
   int abort;       // a wait gave up
   int bad;         // a value that some row must not see is not finite
   int kref[kScaleSlots], vref[kScaleSlots];    // e4m3: exponents taken out of a tile's keys and values
@@ -93,7 +92,7 @@ struct Smem {
   static constexpr int kBytes = kWant < kMost ? kWant : kMost;
 };
 
-// Bounded: after kWaitNs, or once another wait of the block gave up, false.
+// Bounded: after the cache's timeout, or once another wait of the block gave up, false.
 __device__ __forceinline__ bool wait_bar(ChunkShared& sh, uint32_t bar, uint32_t parity) {
   if (mb_try(bar, parity)) return true;
   const uint64_t t0 = gtime();
@@ -102,7 +101,7 @@ __device__ __forceinline__ bool wait_bar(ChunkShared& sh, uint32_t bar, uint32_t
     for (int i = 0; i < 64; ++i)
       if (mb_try(bar, parity)) return true;
     if (*(volatile int*)&sh.abort) return false;
-    if ((long long)(gtime() - t0) > kWaitNs) {
+    if ((long long)(gtime() - t0) > sh.timeout_ns) {
       *(volatile int*)&sh.abort = 1;
       return false;
     }
@@ -175,11 +174,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     if (lane < 2) {
       mb_init(saddr(&sh.s_full[lane]), 1);
       mb_init(saddr(&sh.p_full[lane]), 8);
-      mb_init(saddr(&sh.turn[lane]), 1);
     }
     if (lane == 2) mb_init(saddr(&sh.q_full), kSoftWarps * 32);
     if (lane == 3) mb_init(saddr(&sh.o_full), 1);
-    if (lane == 4) sh.abort = sh.bad = 0;
+    if (lane == 4) {
+      sh.abort = sh.bad = 0;
+      sh.timeout_ns = p.timeout_ns;
+    }
     mb_fence_init();
   }
   if (warp == kMmaWarp) {
@@ -589,11 +590,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       }
       return pg < 0 ? p.c.pages : pg;
     };
-    int pg = page_at(0);
+    int pg = page_at(0), asked = 0;
     for (int n = 0; n < 2 * ntiles; ++n) {
       const int j = n >> 1, is_v = n & 1;
       if (n >= NR && !(E4M3 ? wait_warp(sh, saddr(&sh.raw_empty[n % NR]), ((n / NR) & 1) ^ 1) : wait_done(sh, n - NR))) break;
       const uint32_t bar = saddr(&sh.raw_full[n % NR]);
+      asked = n + 1;
+      if (n == 0 && p.stall) continue;
       if (lane == 0) mb_expect(bar, E4M3 ? C::kRawBytes : C::kOpBytes);
       __syncwarp();
       if (lane < boxes) {
@@ -606,7 +609,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       if (is_v) pg = page_at(j + 1);
     }
     // what was asked for lands before the block may end, whatever ended the loop
-    for (int n = max(0, 2 * ntiles - NR); n < 2 * ntiles; ++n) wait_warp(sh, saddr(&sh.raw_full[n % NR]), (n / NR) & 1);
+    for (int n = max(p.stall ? 1 : 0, asked - NR); n < asked; ++n)
+      for (int k = 0; k < (1 << 20) && !__all_sync(0xffffffffu, mb_try(saddr(&sh.raw_full[n % NR]), (n / NR) & 1)); ++k) {
+      }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA
     // The instructions between two products matter: about four queued ones cover them, and one takes nearly as long

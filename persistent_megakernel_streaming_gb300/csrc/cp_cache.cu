@@ -42,9 +42,10 @@ struct Slot {
 __device__ __forceinline__ void find_slot(const CacheView& c, const BatchView& b, int r, Slot* out) {
   const int lane = threadIdx.x & 31;
   int seq = 0;
+#pragma unroll 8
   for (int i0 = 0; i0 < b.n; i0 += 32) {
     const int i = i0 + lane;
-    const bool before = i < b.n && b.start[i + 1] <= r;
+    const bool before = i < b.n && b.start[min(i, b.n - 1) + 1] <= r;
     seq += __popc(__ballot_sync(0xffffffffu, before));
   }
   if (lane) return;
@@ -324,6 +325,8 @@ int check_desc(const cp_cache_desc* in, cp_cache_desc* d) {
   if (!d->scale_token_stride) d->scale_token_stride = 1;
   if (!d->scale_head_stride) d->scale_head_stride = d->page_size;
   if (!d->scale_page_stride) d->scale_page_stride = (int64_t)d->kv_heads * d->page_size;
+  if (d->timeout_ns < 0) return CP_ERR_INVALID_ARG;
+  if (!d->timeout_ns) d->timeout_ns = 2000000000ll;
   if (d->token_stride < 0 || d->head_stride < 0 || d->page_stride < 0 || d->scale_token_stride < 0 ||
       d->scale_head_stride < 0 || d->scale_page_stride < 0)
     return CP_ERR_INVALID_ARG;
@@ -449,6 +452,8 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   p->scale_log2 = (float)(scale * 1.4426950408889634);
   p->causal = a->causal != 0;
   p->window = a->window;
+  p->timeout_ns = d.timeout_ns;
+  p->stall = d.debug_stall != 0;
   p->a = plan_attend(b, d.kv_heads, a->q_heads, d.head_dim, d.dtype == CP_CACHE_E4M3, p->causal != 0, p->window);
   return CP_OK;
 }

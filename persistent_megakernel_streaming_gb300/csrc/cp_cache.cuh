@@ -149,6 +149,8 @@ struct AttendParams {
   int q_heads;
   float scale_log2;                       // scale * log2(e)
   int causal, window;
+  int64_t timeout_ns;
+  int stall;                              // test: the first load is left out
 };
 
 // Positions [lo, hi) that the row at position `pos` sees.

@@ -63,7 +63,7 @@ def test_plain_arguments_are_accepted():
     (dict(page_size=8), UNSUPPORTED), (dict(page_size=48), UNSUPPORTED), (dict(page_size=256), UNSUPPORTED),
     (dict(pages=0), INVALID), (dict(dtype=1), INVALID), (dict(k_scale=P, v_scale=P), INVALID),
     (dict(dtype=1, k_scale=P), INVALID), (dict(k=P + 2), UNSUPPORTED), (dict(token_stride=132), UNSUPPORTED),
-    (dict(page_stride=-8), INVALID), (dict(page_stride=1 << 39), UNSUPPORTED), (dict(head_stride=1 << 40), UNSUPPORTED), (dict(dtype=1, k_scale=P, v_scale=P, token_stride=136), UNSUPPORTED)])
+    (dict(timeout_ns=-1), INVALID), (dict(page_stride=-8), INVALID), (dict(page_stride=1 << 39), UNSUPPORTED), (dict(head_stride=1 << 40), UNSUPPORTED), (dict(dtype=1, k_scale=P, v_scale=P, token_stride=136), UNSUPPORTED)])
 def test_bad_layouts_are_refused(kw, want):
     assert check(desc(**kw)) == want
     h = C.c_void_p()

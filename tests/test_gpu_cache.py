@@ -69,6 +69,9 @@ class World:
         self.ks = self.vs = None
         if e4m3:
             self.ks, self.vs = (torch.zeros((self.pages, hkv, page), dtype=torch.uint8, device=device) for _ in range(2))
+            if interleaved:
+                base = torch.zeros((self.pages, page, hkv, 2), dtype=torch.uint8, device=device)
+                self.ks, self.vs = (base[..., i].permute(0, 2, 1) for i in range(2))
         self.cache = cp.Cache(self.k, self.v, self.ks, self.vs)
         self.spread = spread
         self.batch_of = lambda **kw: cp.Batch(
@@ -593,6 +596,36 @@ def test_binding_refuses_wrong_rows_and_devices():
         w.cache.read(w.batch, None, None)
     with pytest.raises(ValueError):
         w.cache.append(w.batch, torch.zeros((4, 5 * 64), dtype=torch.bfloat16, device="cuda"), q[:, :2])
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+def test_a_wait_that_runs_out_is_reported(e4m3, d):
+    """The first load of every block is left out: the waits for it end, the call returns, the status says so, and the
+    device goes on."""
+    w = World([400, 300], [200, 9], 2, d, 32, e4m3).fill()
+    q, good = w.attend(4)
+    stalled = cp.Cache(w.k, w.v, w.ks, w.vs, timeout_ns=20_000_000, debug_stall=True)
+    out = torch.full_like(good, 7.0)
+    stalled.attend(w.batch, q.cuda(), out)
+    assert stalled.status() == cp.CP_ERR_TIMEOUT
+    stalled.clear_status()
+    assert stalled.status() == 0        # (what a call that timed out leaves in out is not specified)
+    assert torch.equal(w.attend(4, q=q)[1], good)
+
+
+def test_batches_of_many_sequences():
+    """More sequences than a warp looks at at once, most without rows."""
+    n = 700
+    new = [(3 if i % 50 == 7 else 40 if i % 300 == 11 else 0) for i in range(n)]
+    w = World([50 + i % 30 if new[i] else 0 for i in range(n)], new, 1, 64, 16, False, seed=6, pad=1).fill()
+    q, out = w.attend(2)
+    w.check(q, out)
+    k = torch.full((w.rows, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    w.cache.read(w.batch, k, None)
+    for i in range(n):
+        if new[i]:
+            np.testing.assert_array_equal(k[w.start[i]:w.start[i + 1]].double().cpu().numpy(),
+                                          w.kv[i][0][w.lengths[i] - new[i]:])
 
 
 # ------------------------------------------------------------ together, in front of a frame
