@@ -334,13 +334,13 @@ class Cache:
         """qkv [rows][(q_heads + 2 kv_heads) * head_dim] into the cache, its q into q_out [rows][q_heads][head_dim]."""
         d = self.head_dim
         heads = 0 if q_out is None else q_out.shape[1]
-        x, (row,) = self._rows(batch, qkv, "qkv", (heads + 2 * self.kv_heads) * d)
-        q, q_row = 0, 0
+        x, st = self._rows(batch, qkv, "qkv", (batch.rows, (heads + 2 * self.kv_heads) * d))
+        q, qs = 0, (0, 0)
         if q_out is not None:
-            q, (q_row, head) = self._rows(batch, q_out, "q_out", heads, d)
-            if head not in (0, d):
+            q, qs = self._rows(batch, q_out, "q_out", (batch.rows, heads, d))
+            if qs[1] not in (0, d):
                 raise ValueError("q_out: contiguous heads")
-        a = AppendArgs(x, row, q, q_row, heads, self._gain(q_norm), self._gain(k_norm), rms_eps, rope_base)
+        a = AppendArgs(x, st[0], q, qs[0], heads, self._gain(q_norm), self._gain(k_norm), rms_eps, rope_base)
         code = lib().cp_cache_append(self._h, batch.ref, C.byref(a), self._stream(stream))
         if code:
             raise CPError(code, "cp_cache_append")
@@ -350,7 +350,7 @@ class Cache:
         at = [0, 0]
         for i, t in enumerate((k_out, v_out)):
             if t is not None:
-                at[i], _ = self._rows(batch, t, "k_out, v_out", self.kv_heads, self.head_dim)
+                at[i], _ = self._rows(batch, t, "k_out, v_out", (batch.rows, self.kv_heads, self.head_dim))
                 if not t.is_contiguous():
                     raise ValueError("k_out, v_out: contiguous")
         code = lib().cp_cache_read(self._h, batch.ref, at[0], at[1], self._stream(stream))
@@ -362,9 +362,10 @@ class Cache:
         """Attention of q [rows][q_heads][head_dim] over the cache into out (the same shape). Without a
         ``workspace`` (device bytes, see workspace_bytes) one is taken from torch's allocator for this call."""
         heads = q.shape[1]
-        x, (row, head) = self._rows(batch, q, "q", heads, self.head_dim)
-        y, (out_row, out_head) = self._rows(batch, out, "out", heads, self.head_dim)
-        a = AttendArgs(x, y, row, head, out_row, out_head, heads, scale, causal, window)
+        shape = (batch.rows, heads, self.head_dim)
+        x, qs = self._rows(batch, q, "q", shape)
+        y, os_ = self._rows(batch, out, "out", shape)
+        a = AttendArgs(x, y, qs[0], qs[1], os_[0], os_[1], heads, scale, causal, window)
         need = self._need(batch, heads, causal, window)
         at, size = 0, 0
         if workspace is not None:
@@ -391,24 +392,24 @@ class Cache:
             batch.plans[key] = need.value
         return batch.plans[key]
 
-    def _rows(self, batch, t, what, *inner):
+    def _rows(self, batch, t, what, shape):
         """Address of a row array and the strides of its axes but the last (0 where it has one entry at most)."""
-        shape, strides = tuple(t.shape), t.stride()
-        if shape != (batch.rows, *inner) or t.element_size() != 2 or strides[-1] != 1 and inner[-1] > 1:
-            raise ValueError(f"{what}: 16-bit elements [{', '.join(map(str, (batch.rows, *inner)))}], the last axis "
-                             f"contiguous; got {shape}, strides {strides}, {t.dtype}")
+        strides = t.stride()
+        if t.shape != shape or t.element_size() != 2 or strides[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"{what}: 16-bit elements {list(shape)}, the last axis contiguous; got {list(t.shape)}, "
+                             f"strides {strides}, {t.dtype}")
         if t.get_device() != self.device_index or batch.device_index != self.device_index:
             raise ValueError(f"{what}, or the batch: on another device than the cache's")
         if shape[0] > 1 and strides[0] > 0 < strides[-2]:
-            return t.data_ptr(), strides[:-1]
+            return t.data_ptr(), strides
         if any(n > 1 and s <= 0 for n, s in zip(shape, strides)):
             raise ValueError(f"{what}: entries that share memory (an expanded tensor)")
-        return t.data_ptr(), tuple(s if n > 1 else 0 for n, s in zip(shape[:-1], strides))
+        return t.data_ptr(), tuple(s if n > 1 else 0 for n, s in zip(shape, strides))
 
     def _gain(self, t):
         if t is None:
             return 0
-        if tuple(t.shape) != (self.head_dim,) or t.element_size() != 2 or t.stride(0) != 1 or t.get_device() != self.device_index:
+        if t.shape != (self.head_dim,) or t.element_size() != 2 or t.stride(0) != 1 or t.get_device() != self.device_index:
             raise ValueError("q_norm, k_norm: bf16 [head_dim] on the cache's device")
         return t.data_ptr()
 
