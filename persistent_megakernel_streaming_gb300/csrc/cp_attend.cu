@@ -12,7 +12,7 @@ namespace cache {
 // ------------------------------------------------------------------ plan
 constexpr int kSms = 152;
 constexpr int kStepBlocks = 2 * kSms; // step blocks resident at once
-constexpr int kStepCluster = 8;       // blocks of a cluster that joins its parts itself
+constexpr int kStepCluster = kMostCluster;
 constexpr int kMaxStepChunk = 4096;   // positions a step block holds page numbers for
 
 static int step_tile(int head_dim, bool e4m3) { return 4 * (e4m3 ? 32 : 16) * (128 / head_dim); }
@@ -55,19 +55,23 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
     // a window spans itself and the item's rows; not causal, the rows up to the last of the sequence
     const int64_t ahead = causal ? std::min(b.max_new, (kPairRows + group - 1) / group + 1) : b.max_new;
     if (window > 0) all = std::min<int64_t>(all, (int64_t)window + ahead + kChunkAlign - 1);
-    // In nanoseconds: a tile of 128 positions 1500 (twice that in heads of 64 than the tensor core needs), a block's
-    // start and end 6000, and the parts' results written and read again at 5 TB/s.
+    // In nanoseconds: a tile of 128 positions 1700 (heads of 64: 1200), a block's start and end 9000, joining the parts
+    // of a cluster 2500, or through the workspace 3000 and the parts' results written and read again at 5 TB/s. Clusters
+    // only where all blocks are resident at once: their blocks start and leave together (a ragged batch in two rounds
+    // 169 us, in clusters 179).
     double best = 0;
     int64_t parts = 1;
-    const double tile_ns = head_dim == 128 ? 1500 : 1000;
+    const double tile_ns = head_dim == 128 ? 1700 : 1200;
     const double join_ns = 2.0 * b.rows * q_heads * head_dim * 4 / 5000;
     for (int64_t n = 1; n <= 32; ++n) {
       const int64_t tiles = ((all + n - 1) / n + 127) / 128;
-      const double cost = (double)((blocks * n + kSms - 1) / kSms) * (tiles * tile_ns + 6000) + (n > 1 ? 3000 + n * join_ns : 0);
+      const double cost = (double)((blocks * n + kSms - 1) / kSms) * (tiles * tile_ns + 9000) +
+                          (n == 1 ? 0 : n <= kMostCluster && blocks * n <= kSms ? 2500 : 3000 + n * join_ns);
       if (n == 1 || cost < best) best = cost, parts = n;
     }
     a.chunk_chunk = (int)(((all + parts - 1) / parts + 127) / 128 * 128);
     a.chunk_parts = (int)((all + a.chunk_chunk - 1) / a.chunk_chunk);
+    a.chunk_cluster = a.chunk_parts > 1 && a.chunk_parts <= kMostCluster && blocks * a.chunk_parts <= kSms;
   }
   return a;
 }
@@ -143,28 +147,8 @@ __device__ __forceinline__ void join_cluster(const AttendParams& p, const Seq& s
   const uint32_t at = smem_u32(avg), at_lse = smem_u32(avg_lse);
   for (int u = blockIdx.x * (kStepWarps * 32) + threadIdx.x; u < nrows * (D / 4); u += parts * (kStepWarps * 32)) {
     const int r = u / (D / 4), d = u % (D / 4) * 4;
-    float lse[kStepCluster], top = -INFINITY;
-    float4 y[kStepCluster];
-#pragma unroll
-    for (int i = 0; i < kStepCluster; ++i) {
-      lse[i] = -INFINITY;
-      if (i < parts) {
-        lse[i] = ptx::ld_cluster(ptx::mapa(at_lse + r * 4, i));
-        y[i] = ptx::ld_cluster_v4(ptx::mapa(at + (r * D + d) * 4, i));
-      }
-      top = fmaxf(top, lse[i]);
-    }
-    float x[4] = {}, sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < kStepCluster; ++i)
-      if (i < parts) {
-        const float w = lse[i] == -INFINITY ? 0.f : ex2(lse[i] - top);
-        sum += w;
-        x[0] += w * y[i].x; x[1] += w * y[i].y; x[2] += w * y[i].z; x[3] += w * y[i].w;
-      }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] *= inv;
+    float x[4];
+    join4(at + (r * D + d) * 4, at_lse + r * 4, parts, x);
     store4<D>(p, 0, true, s.row0 + r / p.group, kv * p.group + r % p.group, d, x);
   }
   __syncwarp();
@@ -614,7 +598,9 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
   } else {
     const int i0 = ((int)(row - s.row0) * p.group + head % p.group) / kPairRows * kPairRows;
     const int i1 = min(i0 + kPairRows, nrows) - 1;
-    parts = parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len, kChunkAlign), p.a.chunk_chunk);
+    parts = p.a.chunk_cluster
+                ? 0
+                : parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len, kChunkAlign), p.a.chunk_chunk);
   }
   if (parts <= 1) return;
   const int64_t n = (int64_t)p.b.rows * p.q_heads;
@@ -649,8 +635,8 @@ cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s)
     constexpr int threads = kStepWarps * 32;
     cudaError_t e = cudaSuccess;
     if (p.a.step_cluster) {
-      e = p.a.step_wide ? launch_cluster(attend_step_kernel<D, E4M3, 2, true>, blocks, p.a.step_parts, threads, kStepSmem, s, p)
-                        : launch_cluster(attend_step_kernel<D, E4M3, 1, true>, blocks, p.a.step_parts, threads, kStepSmem, s, p);
+      e = p.a.step_wide ? launch_as(attend_step_kernel<D, E4M3, 2, true>, blocks, p.a.step_parts, 1, false, threads, kStepSmem, s, p)
+                        : launch_as(attend_step_kernel<D, E4M3, 1, true>, blocks, p.a.step_parts, 1, false, threads, kStepSmem, s, p);
     } else if (p.a.step_wide) {
       attend_step_kernel<D, E4M3, 2, false><<<blocks, threads, kStepSmem, s>>>(p);
     } else {
@@ -665,7 +651,7 @@ cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s)
     if (e != cudaSuccess) return e;
   }
   if (kept_parts(p.a) > 1) {
-    const cudaError_t e = launch_pdl(attend_join_kernel<D>, dim3(grid), 256, 0, s, p);
+    const cudaError_t e = launch_as(attend_join_kernel<D>, dim3(grid), 1, 1, true, 256, 0, s, p);
     if (e != cudaSuccess) return e;
   }
   return cudaGetLastError();

@@ -10,38 +10,30 @@ namespace cache {
 using ptx::pdl_trigger;
 using ptx::pdl_wait;
 
-// A launch that may start before the kernel in front of it has ended (it waits
-// for that one where it needs to: pdl_wait).
+// A launch in clusters of cluster_x by cluster_y blocks, and, with `early`, one that may start before the kernel in
+// front of it has ended (it waits for that one where it needs to: pdl_wait).
 template <class K, class... A>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+cudaError_t launch_as(K kernel, dim3 grid, int cluster_x, int cluster_y, bool early, int threads, size_t smem, cudaStream_t s,
+                      const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  if (cluster_x * cluster_y > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = cluster_x;
+    attr[cfg.numAttrs].val.clusterDim.y = cluster_y;
+    attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (early) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// A launch whose blocks along x are clusters of `cluster`.
-template <class K, class... A>
-cudaError_t launch_cluster(K kernel, dim3 grid, int cluster, int threads, size_t smem, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cluster;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -89,7 +81,7 @@ __device__ __forceinline__ void store_lse(const AttendParams& p, int part, int64
 template <int D, bool E4M3>
 __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, int kv, int i0, int i1, int t_begin,
                                         int t_end, int part, bool whole, int warp, int warps, float* avg = nullptr,
-                                        float* avg_lse = nullptr) {
+                                        float* avg_lse = nullptr, int pitch = D) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
@@ -149,8 +141,8 @@ __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, i
       for (int j = 0; j < E; ++j) p.out[row * p.o_row + head * p.o_head + lane * E + j] = (uint16_t)bf_pack(acc[j] * inv, 0.f);
     } else if (avg) {                    // a block that joins its parts in shared memory
 #pragma unroll
-      for (int j = 0; j < E; ++j) avg[i * D + lane * E + j] = acc[j] * inv;
-      if (lane == 0) avg_lse[i] = l == 0.f ? -INFINITY : m + log2f(l);
+      for (int j = 0; j < E; ++j) avg[(i - i0) * pitch + lane * E + j] = acc[j] * inv;
+      if (lane == 0) avg_lse[i - i0] = l == 0.f ? -INFINITY : m + log2f(l);
     } else {
       const int64_t unit = ((int64_t)part * p.b.rows + row) * p.q_heads + head;
 #pragma unroll
@@ -158,6 +150,35 @@ __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, i
       if (lane == 0) p.part_lse[unit] = l == 0.f ? -INFINITY : m + log2f(l);
     }
   }
+}
+
+// Four neighbouring elements of a row of an item, weighed over its parts' blocks, which are a cluster: each holds its
+// averages at shared address `at` of the element and its log-sum of the row at `at_lse`.
+constexpr int kMostCluster = 8;
+__device__ __forceinline__ void join4(uint32_t at, uint32_t at_lse, int parts, float* x) {
+  float lse[kMostCluster], top = -INFINITY;
+  float4 y[kMostCluster];
+#pragma unroll
+  for (int i = 0; i < kMostCluster; ++i) {
+    lse[i] = -INFINITY;
+    if (i < parts) {
+      lse[i] = ptx::ld_cluster(ptx::mapa(at_lse, i));
+      y[i] = ptx::ld_cluster_v4(ptx::mapa(at, i));
+    }
+    top = fmaxf(top, lse[i]);
+  }
+  float sum = 0.f;
+  x[0] = x[1] = x[2] = x[3] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMostCluster; ++i)
+    if (i < parts) {
+      const float w = lse[i] == -INFINITY ? 0.f : ex2(lse[i] - top);
+      sum += w;
+      x[0] += w * y[i].x; x[1] += w * y[i].y; x[2] += w * y[i].z; x[3] += w * y[i].w;
+    }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] *= inv;
 }
 
 }  // namespace cache

@@ -65,7 +65,7 @@ constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 // What the end of a block needs, kept out of the registers meanwhile.
 struct Item {
   Seq s;
-  int seq, kv, part, row0, rows_here, whole, t_begin, t_end, any[2], first_row, first_head;
+  int seq, kv, part, parts, row0, rows_here, whole, t_begin, t_end, any[2], first_row, first_head;
   uint32_t magic;
 };
 
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     }
   }
   if (threadIdx.x == 0)
-    sh.item = {s, seq, kv, part, row0, rows_here, whole, t_begin, t_end, {je[0] > jb[0], je[1] > jb[1]}, first_row, first_head, magic};
+    sh.item = {s, seq, kv, part, parts, row0, rows_here, whole, t_begin, t_end, {je[0] > jb[0], je[1] > jb[1]}, first_row, first_head, magic};
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
@@ -339,8 +339,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       if (E4M3) pair_or(pair_id, false);
     }
     const float row_scale = E4M3 ? sh.row[0][slot] : p.scale_log2;
-    int lo = 0, hi = 0;
-    if (mine) visible(p, s.first + new_row(slot), s.len, &lo, &hi);
+    const int pos = mine ? s.first + new_row(slot) : -1;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_t = tmem + lanes + kTmemS + i * kTile + half * kHalf;
     const uint32_t o_t = tmem + lanes + kTmemO + i * D + half * (D / 2);
@@ -359,11 +358,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       // masked scores are minus infinity
       auto ready = [&](uint32_t* x, int c) {
         if (edge) {
+          int lo, hi;
+          visible(p, pos, sh.item.s.len, &lo, &hi);
+          lo -= t0 + half * kHalf + c;
+          hi -= t0 + half * kHalf + c;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int t = t0 + half * kHalf + c + k;
-            if (t < lo || t >= hi) x[k] = 0xff800000u;
-          }
+          for (int k = 0; k < 32; ++k)
+            if (k < lo || k >= hi) x[k] = 0xff800000u;
         }
       };
       auto top_of = [&](const uint32_t* x) {
@@ -430,21 +431,24 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       const float ref = (m == -INFINITY ? 0.f : m) - kBias;
       const uint64_t rs2 = pair_of(rs, rs), ref2 = pair_of(-ref, -ref);
       auto weigh = [&](uint32_t* x, int c) {
-        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          float y[4];
-          split_pair(fma2(pack2(x + k), rs2, ref2), y, y + 1);
-          split_pair(fma2(pack2(x + k + 2), rs2, ref2), y + 2, y + 3);
+        for (int h = 0; h < 32; h += 16) {
+          uint32_t w[8];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) y[q] = ex2(y[q]);
-          sum[0] = add2(sum[0], pair_of(y[0], y[1]));
-          sum[1] = add2(sum[1], pair_of(y[2], y[3]));
-          w[k / 2] = E4M3 ? hf_pack(y[0], y[1]) : bf_pack(y[0], y[1]);
-          w[k / 2 + 1] = E4M3 ? hf_pack(y[2], y[3]) : bf_pack(y[2], y[3]);
+          for (int k = 0; k < 16; k += 4) {
+            float y[4];
+            split_pair(fma2(pack2(x + h + k), rs2, ref2), y, y + 1);
+            split_pair(fma2(pack2(x + h + k + 2), rs2, ref2), y + 2, y + 3);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) y[q] = ex2(y[q]);
+            sum[0] = add2(sum[0], pair_of(y[0], y[1]));
+            sum[1] = add2(sum[1], pair_of(y[2], y[3]));
+            w[k / 2] = E4M3 ? hf_pack(y[0], y[1]) : bf_pack(y[0], y[1]);
+            w[k / 2 + 1] = E4M3 ? hf_pack(y[2], y[3]) : bf_pack(y[2], y[3]);
+          }
+          if (!kOnce && h == 16 && c + 32 < kHalf) tm_ld32_start(s_t + c + 32, x);
+          tm_st8(s_t + (c + h) / 2, w);
         }
-        if (!kOnce && c + 32 < kHalf) tm_ld32_start(s_t + c + 32, x);
-        tm_st16(s_t + c / 2, w);
       };
       if (kOnce) {
         weigh(x, 0);
@@ -690,9 +694,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
   const bool failed = sh.abort != 0;
   if (failed && threadIdx.x == 0) set_status(p.c.status, CP_ERR_TIMEOUT);
   const Item& it = sh.item;
+  constexpr int kPitch = D + 4;
+  static_assert(kPairRows * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the rows fit the operands' memory");
+  float* averages = reinterpret_cast<float*>(ops);
+  const bool cluster = p.a.chunk_cluster && !it.whole;       // the item's parts are a cluster's blocks
   if (!failed && sh.bad) {
     plain_rows<D, E4M3>(p, it.s, it.seq, it.kv, it.row0, it.row0 + it.rows_here, it.t_begin, it.t_end, it.part, it.whole, warp,
-                        C::kThreads / 32);
+                        C::kThreads / 32, cluster ? averages : nullptr, sh.row[0], kPitch);
   } else if (!failed && warp < kSoftWarps) {
     // rows leave through the operands' memory, so that a row is written at once and not by its threads piece by piece
     const int slot = threadIdx.x / 256 * kTile + (threadIdx.x & 127), half = (warp >> 2) & 1, i = warp >> 3;
@@ -709,9 +717,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     l = sh.row[0][slot] + sh.row[1][slot];
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float e = E4M3 ? pow2i(min(max(vr - kUp, -126), 127)) : 1.f;
-    constexpr int kPitch = D + 4;
-    static_assert(kPairRows * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the rows fit the operands' memory");
-    float* stage = reinterpret_cast<float*>(ops) + (i * kTile + (warp & 3) * 32) * kPitch;
+    float* stage = averages + (i * kTile + (warp & 3) * 32) * kPitch;
 #pragma unroll 1
     for (int c = 0; c < D / 2; c += 32) {
       float v[32];
@@ -723,14 +729,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
         *reinterpret_cast<float4*>(stage + lane * kPitch + half * (D / 2) + c + x) = y;
       }
     }
+    const float lse = l == 0.f ? -INFINITY : m + log2f(l) - kBias;
     int64_t row;
     int head;
-    if (slot < it.rows_here && !it.whole && half == 0) {
+    if (slot < it.rows_here && !it.whole && !cluster && half == 0) {
       place(slot, &row, &head);
-      store_lse(p, it.part, row, head, l == 0.f ? -INFINITY : m + log2f(l) - kBias);
+      store_lse(p, it.part, row, head, lse);
     }
     tm_fence_before();
     pair_or(pair_id, false);
+    if (cluster && half == 0) sh.row[0][slot] = lse;
     // a row at a time (two of 64 columns), the next row's place by counting on
     constexpr int LPR = D / 4, RPI = 32 / LPR;
     const int r0 = half * 16 + lane / LPR, d = lane % LPR * 4;
@@ -743,7 +751,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     float* part_o = p.part_o + ((int64_t)it.part * p.b.rows * p.q_heads + head0) * D + d;
     const bool whole = it.whole;
 #pragma unroll 4
-    for (int k = 0; k < 16; k += RPI, left -= RPI, src += RPI * kPitch) {
+    for (int k = cluster ? 16 : 0; k < 16; k += RPI, left -= RPI, src += RPI * kPitch) {
       if (left > 0) {
         const float4 y = *reinterpret_cast<const float4*>(src);
         if (whole) *reinterpret_cast<uint2*>(out + row * o_row + head * o_head) = make_uint2(bf_pack(y.x, y.y), bf_pack(y.z, y.w));
@@ -754,6 +762,21 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     }
   }
   __syncthreads();
+  if (cluster) {
+    // each of the item's blocks joins every n-th row, out of all blocks' shared memory; they leave together
+    cluster_sync_all();
+    constexpr int LPR = D / 4, RPI = 32 / LPR;
+    const int d = lane % LPR * 4;
+#pragma unroll 1
+    for (int r = it.part + it.parts * (warp * RPI + lane / LPR); r < it.rows_here; r += it.parts * (C::kThreads / 32) * RPI) {
+      float x[4];
+      join4(saddr(averages + r * kPitch + d), saddr(&sh.row[0][r]), it.parts, x);
+      const int q = (int)(((uint32_t)(it.first_head + r) * it.magic) >> 16);
+      store4<D>(p, 0, true, it.s.row0 + it.first_row + q, it.kv * p.group + it.first_head + r - q * p.group, d, x);
+    }
+    __syncwarp();
+    cluster_sync_all();
+  }
   if (warp == kMmaWarp) {
     tm_fence_after();
     tm_dealloc(sh.tmem, kTmemCols);
@@ -777,12 +800,9 @@ cudaError_t prepare_attend_chunk() {
 template <int D, bool E4M3>
 static cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   const dim3 grid((unsigned)(p.c.heads * chunk_pairs(p.b, p.group)), p.a.chunk_parts);
-  if (!p.a.use_step) {
-    attend_chunk_kernel<D, E4M3><<<grid, Cfg<D, E4M3>::kThreads, Smem<D, E4M3>::kBytes, s>>>(p, maps);
-    return cudaGetLastError();
-  }
-  // behind the step kernel, whose results it does not need: it may fill the SMs that one leaves
-  return launch_pdl(attend_chunk_kernel<D, E4M3>, grid, Cfg<D, E4M3>::kThreads, Smem<D, E4M3>::kBytes, s, p, maps);
+  // behind the step kernel, whose results it does not need, it may fill the SMs that one leaves
+  return launch_as(attend_chunk_kernel<D, E4M3>, grid, 1, p.a.chunk_cluster ? p.a.chunk_parts : 1, p.a.use_step != 0,
+                   Cfg<D, E4M3>::kThreads, Smem<D, E4M3>::kBytes, s, p, maps);
 }
 cudaError_t launch_attend_chunk(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s) {
   if (head_dim == 128) return e4m3 ? launch<128, true>(p, maps, s) : launch<128, false>(p, maps, s);

@@ -122,13 +122,15 @@ struct AttendPlan {
   int step_wide;                  // items of more than 8 rows
   int step_cluster;               // the parts of a step item are one cluster's blocks, which join them
   int chunk_chunk, chunk_parts;
+  int chunk_cluster;              // the same of a chunk item's
 };
 AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, bool causal,
                        int window);
 // Most parts of an item that go through the workspace.
 inline int kept_parts(const AttendPlan& a) {
   const int step = a.step_cluster ? 0 : a.step_parts;
-  return step > a.chunk_parts ? step : a.chunk_parts;
+  const int chunk = a.chunk_cluster ? 0 : a.chunk_parts;
+  return step > chunk ? step : chunk;
 }
 // An upper bound of the chunk kernel's items a kv head: whole pairs and one more a sequence.
 inline int64_t chunk_pairs(const BatchView& b, int group) {

@@ -371,6 +371,33 @@ def test_attend_ignores_what_is_masked(e4m3, d, new, window):
     assert (np.abs(got[~sees] - y[~sees]) <= tol[~sees]).all()
 
 
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("L,window", [(1500, 0), (1500, 700), (30011, 0)])
+def test_attend_chunk_parts_ignore_what_is_masked(e4m3, d, L, window):
+    """NaN in V at positions that some of a chunk's rows see, in a chunk whose positions are cut into parts (a few, that
+    a cluster joins, and many)."""
+    n = 50
+    w = World([L], [n], 1, d, 64, e4m3, seed=3).fill()
+    bad = [L - n + 20] + ([L - n - window + 30] if window else [])      # rows from 20 on; and rows up to 29
+    pool = [w.k.cpu().clone(), w.v.cpu().clone()]
+    for t in bad:
+        pool[1][w.table[0, t // 64], 0, t % 64, 3] = 255 if e4m3 else -1
+    w.put(pool, [None if s is None else s.cpu() for s in (w.ks, w.vs)])
+    q, out = w.attend(2, window=window)
+    got = out.double().cpu().numpy()
+    k, v = w.kv[0]
+    y, size, reach = ref.attend(q.double().numpy(), k, v, L - n, d ** -0.5, True, window)
+    rel = 2 * (d + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + (2.0 ** -11 if e4m3 else 2.0 ** -8) + L * 2.0 ** -24
+    tol = np.abs(y) * 2.0 ** -8 + size * rel * 1.01 + (2.0 ** -25 * L * np.abs(v).max() if e4m3 else 0)
+    rows = np.arange(n)
+    sees = rows >= 20
+    if window:
+        sees |= rows < 30
+    assert np.isnan(got[sees][..., 3]).all() and not np.isnan(got[~sees]).any()
+    other = np.arange(d) != 3
+    assert (np.abs(got - y) <= tol)[..., other].all() and (np.abs(got - y) <= tol)[~sees].all()
+
+
 @pytest.mark.parametrize("new", [[1], [40]])
 def test_attend_infinite_scores(new):
     """Keys of the type's lowest value: their scores are minus infinity or far below the others, never NaN."""
