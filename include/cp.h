@@ -445,7 +445,8 @@ typedef struct cp_cache cp_cache; /* opaque, owned by the library */
 /* Make a cache object for pages that the caller owns (device memory, kept
  * for the object's life; what they hold is not touched). Errors:
  * CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED (layout or device), CP_ERR_NOMEM,
- * CP_ERR_CUDA. The calls below run on the cache's device, whichever is
+ * CP_ERR_CUDA. It allocates and synchronises: not while a stream is being
+ * captured. The calls below run on the cache's device, whichever is
  * current. The object holds no scratch: calls on several streams may overlap
  * as far as their arrays, pages and workspaces do. */
 int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out);
@@ -456,7 +457,8 @@ int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out);
  * angle position * rope_base^(-2j/head_dim)), as in the frame's layer, in
  * fp32; q is rounded to q_out, k and v are rounded or quantised into the
  * row's place. One launch. qkv, q_out and the gains are 16-byte aligned,
- * strides multiples of 8 elements. */
+ * strides multiples of 8 elements. q_out may be qkv itself (q in its place,
+ * the same stride), and does not overlap it otherwise. */
 int cp_cache_append(cp_cache* c, const cp_batch* batch, const cp_append* args, cp_stream_t stream);
 
 /* The key and value cached at each of the batch's rows' positions, device
@@ -468,11 +470,12 @@ int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, 
 /* Attention of the batch's rows over their sequences' cached positions, the
  * rows' own among them (append them first): softmax over the visible
  * positions t of scale * q . k_t, times v_t; a row that sees none (no cached
- * position, or a negative position of its own) gives zeros. What a masked
+ * position, or, causal, a negative position of its own) gives zeros. What a masked
  * position holds does not matter, infinities and NaN included. Scores,
  * softmax statistics and sums are fp32; the weights are rounded to bfloat16
  * (fp16 over an e4m3 cache) for the product with v, and the result once to
- * bfloat16. Results are bit-identical run to run. `workspace`: device memory
+ * bfloat16. Results are bit-identical run to run. out may be q itself, with
+ * the same strides, and does not overlap it otherwise. `workspace`: device memory
  * of at least cp_cache_check's workspace_bytes, 16-byte aligned, nothing kept
  * in it between calls; calls that may overlap, captured ones included, need
  * workspaces of their own. q and out are 16-byte aligned, strides multiples

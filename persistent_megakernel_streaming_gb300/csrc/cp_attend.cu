@@ -88,6 +88,9 @@ constexpr int kStepWarps = 4;
 constexpr int kStages = 3;
 constexpr int kStageBytes = 8192;     // a warp's tile: K and V, 4 KB each
 constexpr int kGroups = kMaxStepChunk / 16;
+// e4m3: most powers of two between a value's scale and the largest. fp16 weights start at 2^8 and keep 11 bits down
+// to 2^-14: 2^12 down, those a thousandth of a row's largest still do.
+constexpr int kMostGap = 12;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
@@ -178,6 +181,11 @@ __device__ __forceinline__ void join_cluster(const AttendParams& p, const Seq& s
 // where the instruction wants two and two: the sum over the head does not
 // mind the order, so q is loaded in it, and two neighbouring columns of v
 // become rows 8 apart.
+//
+// bf16 is bound by HBM: 64 sequences of one row, 16/8 heads of 128, 311 to
+// 6000 positions 127 us a call, 6.5 TB/s, 96 % of the copy rate. e4m3 by the
+// instructions that widen it: the 64 sequences above 143 us a call, issue
+// slots 43 % and integer pipe 48 % busy, 85 % of the copy rate.
 template <int D, bool E4M3, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const __grid_constant__ AttendParams p) {
   constexpr int TK = (E4M3 ? 32 : 16) * (128 / D);    // positions a tile
@@ -337,6 +345,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
   }
   for (int it = 0; it < mine; ++it) {
     const int t0 = t_begin + (it * kStepWarps + warp) * TK;
+    bool far[2] = {false, false};
     if (E4M3) {
       // this tile's scales to shared memory, where the lanes find the ones of their columns
       int ek[2], ev[2];
@@ -352,6 +361,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
       for (int x = 0; x < (TK + 31) / 32; ++x) top = max(top, ev[x]);
       const int ref = max(ev_ref, __reduce_max_sync(0xffffffffu, top));
       if (ref != ev_ref) {
+        bad |= ev_ref > -127 && ref - ev_ref > kMostRise;
         const float f = pow2i(max(ev_ref - ref, -127));
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
@@ -363,6 +373,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
       for (int x = 0; x < (TK + 31) / 32; ++x) {
         sh.scale_k[warp][x * 32 + lane] = pow2i(ek[x]);
         sh.scale_v[warp][x * 32 + lane] = pow2i(max(ev[x] - ref, -127));
+        far[x] = ev[x] > -127 && ev[x] - ref < -kMostGap;      // a position's byte is never 0
       }
     }
     cp_wait<kStages - 2>();
@@ -375,6 +386,12 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
       const int u = lane % UPR, r0 = lane / UPR;
       for (int row = r0; row < TK; row += RPL)
         bad |= any_nonfinite<E4M3>(vtile + row * (UPR * 16) + u * 16);
+    }
+    if (E4M3 && __any_sync(0xffffffffu, far[0] || far[1])) {   // values of zeros have the least scale, and may be far
+#pragma unroll
+      for (int x = 0; x < (TK + 31) / 32; ++x)
+        for (int u = 0; far[x] && u < UPR; ++u)
+          bad |= any_nonzero(ptx::ld_shared_v4u(vtile + (x * 32 + lane) * (UPR * 16) + u * 16));
     }
     // scores
     float sc[MT][NT][4];
@@ -573,7 +590,8 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
 
 // ------------------------------------------------------------------ join
 // One warp a (row, query head) whose item was cut: the parts' averages weighed
-// by their sums. Bound by reading the parts once, small next to the cache.
+// by their sums. Bound by reading the parts once, small next to the cache
+// (largest where chunks are cut that fill no cluster: 16 us of a call of 170).
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();

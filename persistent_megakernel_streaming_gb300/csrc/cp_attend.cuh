@@ -46,8 +46,8 @@ __device__ __forceinline__ int finite_exp(uint32_t h) {
 // Whether 16 bytes of shared memory hold an element that is not finite.
 template <bool E4M3>
 __device__ __forceinline__ bool any_nonfinite(uint32_t addr) {
-  uint32_t w[4];
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+  const uint4 x = ptx::ld_shared_v4u(addr);
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -56,6 +56,13 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t addr) {
   }
   return bad;
 }
+
+// Whether 16 e4m3 bytes hold an element that is not zero.
+__device__ __forceinline__ bool any_nonzero(uint4 x) { return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0; }
+
+// Most powers of two by which the reference of an e4m3 cache's value scales may rise: fp32 outputs follow it with
+// their precision. Past it the rows that do not see the new value could lose theirs.
+constexpr int kMostRise = 110;
 
 // Four neighbouring elements of a row's result: the answer itself, rounded, or
 // a part's average in fp32.
@@ -77,7 +84,9 @@ __device__ __forceinline__ void store_lse(const AttendParams& p, int part, int64
 // row: lanes share the head's elements, walk the positions the row sees and
 // read no other, with a running maximum and sum. The matrix kernels multiply
 // masked values by zero, which is wrong where one is infinite or NaN; a block
-// that finds one next to a mask runs this instead.
+// that finds one next to a mask runs this instead. So does one over an e4m3
+// cache whose positions' scales lie further apart than the 16-bit operands
+// reach: a row may see only the small ones.
 template <int D, bool E4M3>
 __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, int kv, int i0, int i1, int t_begin,
                                         int t_end, int part, bool whole, int warp, int warps, float* avg = nullptr,

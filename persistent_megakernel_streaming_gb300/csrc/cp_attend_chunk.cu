@@ -9,14 +9,13 @@
 //
 // Warps 0-7 and 8-15: the softmax of tile 0 and tile 1, two threads a row with
 // 64 of a tile's 128 positions each (more warps at less work each: what one
-// tile's softmax takes is what the other tile's products have to cover). Warps
-// 20 and 21 issue the MMAs of tile 0 and tile 1: the tensor core stands still
-// while an issuer does anything else (measured: nothing of a gap between two
-// products of one warp is hidden, nearly all of it behind another warp's).
-// Warp 22 brings pages in through tensor maps, a lane a page. For each 128 positions S = Q K^T (128 x 128, fp32 in
-// TMEM); the softmax threads read their part of it (over an e4m3 cache
-// twice: there it does not fit their registers), write the weights as 16 bit over
-// the S that they have read, and O += P V reads them from there. O stays in
+// tile's softmax takes is what the other tile's products have to cover). Behind
+// them the helper warps, then the warp that issues every MMA, then the one that
+// brings pages in through tensor maps, a lane a page. For each 128 positions
+// S = Q K^T (128 x 128, fp32 in TMEM); the softmax threads read their part of
+// it (over an e4m3 cache twice: there it does not fit their registers), write
+// the weights as 16 bit over the S that they have read, and O += P V reads
+// them from there. O stays in
 // TMEM for the whole pass. The reference of a row's weights is its first
 // tile's maximum; it is only moved, and O rescaled, when a later score has
 // risen by 2^kLazy over it, since the sum and the weights of a part share the
@@ -28,10 +27,19 @@
 // anything there), and values that some row must not see are looked over for
 // infinities and NaN. e4m3 pages land in a ring of their own and all pass
 // the helpers, which widen them to fp16 and multiply each row by its scale,
-// relative to the largest that the block has met and 2^kUp up: exact as long
-// as fp16 reaches, and what is lost below is 2^-25 of the largest row's
-// least bit. The power taken out of a tile's keys multiplies its scores, the
+// relative to the largest that the block has met and 2^kUp up: exact as far
+// as fp16 reaches, to rows 2^21 smaller; a block that meets one further apart
+// computes its rows the plain way. The power taken out of a tile's keys multiplies its scores, the
 // one of the values the result. Weights start at 2^kBias.
+//
+// Bound by the chain from a tile's scores through its softmax to its second
+// product, and by the issuing warp: nothing of what it does between two groups
+// of products is hidden (each clock of it is one of the tensor core's). 512
+// rows of 16/8 heads of 128 behind 32256 positions, bf16: 135 us a call, 1010
+// TFLOP/s, the tensor pipe busy 52 %, 128 of 152 SMs; two prompts of 4096:
+// 154 us, 890 TFLOP/s, of which each block's start and end are 10 us. A second
+// issuing warp hides the gaps alone, but pulls the two softmaxes into step:
+// 186 us, with turns between the two 149.
 #include "cp_attend.cuh"
 
 namespace cp {
@@ -309,6 +317,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
   int vr = 0;
   constexpr float kBias = E4M3 ? 8.f : 0.f;
   constexpr int kUp = 6;                                 // operands of e4m3 reach 448 * 2^kUp: inside fp16
+  constexpr int kLeast = -15;                            // and the least, 2^-9, is still one of fp16's times this power
   constexpr float kLazy = E4M3 ? 6.f : 8.f;              // weights reach 2^(kBias + kLazy): inside fp16
   constexpr int kHalf = kTile / 2;
 
@@ -535,15 +544,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
           top = max(top, e4[h]);
         }
         int& ref = is_v ? vref : kref;
+        const int before = ref;
         ref = max(ref, __reduce_max_sync(0xffffffffu, top));
+        if (is_v) bad |= before > -127 && ref - before > kMostRise;
+        bool far = false;                                     // a position's byte is never 0
+#pragma unroll
+        for (int h = 0; h < 4; ++h) far |= e4[h] > -127 && e4[h] - ref + kUp < kLeast;
+        far = __any_sync(0xffffffffu, far);
         if (tid == 0) (is_v ? sh.vref : sh.kref)[j % kScaleSlots] = ref;
         uint4 x[N];
 #pragma unroll
-        for (int k = 0; k < N; ++k)
-          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                       : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
-                       : "r"(src + (r0 + k * RPI) * D)
-                       : "memory");
+        for (int k = 0; k < N; ++k) x[k] = ld_shared_v4u(src + (r0 + k * RPI) * D);
         if (look)
 #pragma unroll
           for (int k = 0; k < N; ++k) {
@@ -556,7 +567,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const int r = r0 + k * RPI;
-          const int e = max(__shfl_sync(0xffffffffu, e4[(k * RPI) / 32], r % 32) - ref + kUp, -25);
+          const int own = __shfl_sync(0xffffffffu, e4[(k * RPI) / 32], r % 32), e = max(own - ref + kUp, -25);
+          if (far) bad |= own > -127 && e < kLeast && any_nonzero(x[k]);
           const uint32_t f = hf_pack(pow2i(e), pow2i(e));
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           uint32_t y[8];

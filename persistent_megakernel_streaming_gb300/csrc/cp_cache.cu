@@ -105,7 +105,9 @@ struct AppendParams {
 // 64-bit float is needed. Each row's D/2 sines and cosines are made once; a
 // group of lanes stays with its row, keeps its four of them in registers, and
 // takes every n-th head, four loads in flight.
-// One read of qkv, one write of q and of the pages; arithmetic in pairs of fp32.
+// One read of qkv, one write of q and of the pages; arithmetic in pairs of fp32
+// (an element that lies within that arithmetic's error, some 2^-22, of the
+// middle between two e4m3 steps may take the other one: 4 in a million do).
 // Measured: 8191 rows of 16/8 heads of 128 into bf16 pages 31 us, 4.4 TB/s
 // (65 % of the copy rate: at 1.7 rounds of blocks the last round is short of
 // loads; half or twice the rows a block, 2 or 8 loads in flight and more
@@ -259,7 +261,9 @@ struct ReadParams {
 };
 
 // 16 cached bytes a lane: 8 bf16 copied, or 16 e4m3 widened to fp32, scaled by
-// the power of two and packed (exact: 4 significant bits). Bound by HBM.
+// the power of two and packed (exact: 4 significant bits). Bound by HBM: 12
+// sequences, 96000 rows of 8 heads of 128, e4m3: 96 us, 6.2 TB/s, 91 % of the
+// copy rate.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
   constexpr int kElems = E4M3 ? 16 : 8;
@@ -581,7 +585,7 @@ int cp_cache_append(cp_cache* c, const cp_batch* batch, const cp_append* args, c
   DeviceGuard g(c->device);
   p.c = c->view;
   p.rows_per_block = rows_per_block(b.rows);
-  const int grid = (b.rows + p.rows_per_block - 1) / p.rows_per_block;
+  const int grid = (b.rows - 1) / p.rows_per_block + 1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool e4m3 = c->d.dtype == CP_CACHE_E4M3;
   if (c->d.head_dim == 128) {
@@ -607,7 +611,7 @@ int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, 
   p.k_out = static_cast<uint16_t*>(k_out);
   p.v_out = static_cast<uint16_t*>(v_out);
   p.rows_per_block = rows_per_block(b.rows);
-  const int grid = (b.rows + p.rows_per_block - 1) / p.rows_per_block;
+  const int grid = (b.rows - 1) / p.rows_per_block + 1;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool e4m3 = c->d.dtype == CP_CACHE_E4M3;
   if (c->d.head_dim == 128) {

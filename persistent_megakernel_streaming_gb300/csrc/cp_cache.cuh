@@ -158,7 +158,7 @@ struct AttendParams {
 // Positions [lo, hi) that the row at position `pos` sees.
 __device__ __forceinline__ void visible(const AttendParams& p, int pos, int len, int* lo, int* hi) {
   *hi = p.causal ? min(pos + 1, len) : len;
-  *lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  *lo = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
 // The positions some row of an item sees, from its first and last row's

@@ -126,6 +126,11 @@ __device__ __forceinline__ void st_async_v4(uint32_t a, float x, float y, float 
 __device__ __forceinline__ void st_shared_v4(uint32_t a, float x, float y, float z, float w) {
   asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
+__device__ __forceinline__ uint4 ld_shared_v4u(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void st_shared_v4u(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
@@ -241,13 +246,6 @@ __device__ __forceinline__ void tm_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void tm_ld16_raw(uint32_t taddr, uint32_t* r) {
-  float v[16];
-  tm_ld16(taddr, v);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i]);
-}
-
 // The 32-column load without its wait, and the wait naming the registers so that
 // nothing reads them before it (it waits for every load of the thread).
 __device__ __forceinline__ void tm_ld32_start(uint32_t taddr, uint32_t* r) {
@@ -296,7 +294,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Store 16 or 32 consecutive 32-bit columns of this warp's 32 TMEM lanes (wait with tm_wait_st).
+// Store 16 or 8 consecutive 32-bit columns of this warp's 32 TMEM lanes (wait with tm_wait_st).
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -308,13 +306,6 @@ __device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
                "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
-}
-__device__ __forceinline__ void tm_st32(uint32_t taddr, const float* v) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
-  tm_st16(taddr, r);
-  tm_st16(taddr + 16, r + 16);
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // The products and their commit as one lane of a warp issues them (`lead` of

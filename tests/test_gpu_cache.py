@@ -398,6 +398,92 @@ def test_attend_chunk_parts_ignore_what_is_masked(e4m3, d, L, window):
     assert (np.abs(got - y) <= tol)[..., other].all() and (np.abs(got - y) <= tol)[~sees].all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [[2], [50]])
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+@pytest.mark.parametrize("gap,shift", [(10, 0), (20, 0), (40, 0), (100, 0), (115, -90)])
+def test_attend_rows_that_do_not_see_a_far_scale(d, new, window, which, gap, shift):
+    """One position's key or value 2^gap times the others (e4m3): rows that do not see it are as exact as if it were
+    not there. `shift` lowers all scales, so that a rise of the gap stays in range.
+
+    Beside the usual bound: weights are fp16 times the value's scale relative to the largest that the kernel keeps in
+    one reference, which is at most 2^12 above those of a row's own, so that one below 2^-14 is off by 2^-25 next to a
+    largest of 2^-12 at least (they start at 2^8): 2^-13 * L * max |v| over the positions the row sees, of which a
+    smaller gap keeps its part, 2^(gap - 25)."""
+    L = 200
+    w = World([L], new, 1, d, 16, True, seed=3).fill()
+    far = L - 1 if not window else L - new[0] - 10     # seen by the last row only; or by the first rows only
+    scales = [w.ks.cpu().int(), w.vs.cpu().int()]
+    kv = [x * 2.0 ** shift for x in w.kv[0]]
+    for i in range(2):
+        t = np.arange(L)
+        scales[i][w.table[0, t // 16], :, t % 16] += shift
+        if "kv"[i] in which:
+            scales[i][w.table[0, far // 16], :, far % 16] += gap
+    w.put([w.k.cpu(), w.v.cpu()], scales)
+    first = L - new[0]
+    q, out = w.attend(2, window=window)
+    got, rows = out.double().cpu().numpy(), 0
+    for r in range(new[0]):
+        lo, hi = max(0, first + r - window + 1) if window else 0, first + r + 1
+        if lo <= far < hi:
+            continue
+        rows += 1
+        k, v = (x[lo:hi] for x in kv)
+        y, size, reach = ref.attend(q.double().numpy()[r:r + 1], k, v, hi - lo - 1, d ** -0.5, True, 0)
+        rel = 2 * (d + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + 2.0 ** -11 + L * 2.0 ** -24
+        tol = np.abs(y) * 2.0 ** -8 + size * rel * 1.01 + 2.0 ** (min(gap, 12) - 25) * (hi - lo) * np.abs(v).max()
+        assert (np.abs(got[r:r + 1] - y) <= tol).all(), (r, np.abs(got[r:r + 1] - y).max(), tol.max())
+    assert rows == (new[0] - 1 if not window else max(0, new[0] - 10)) and w.cache.status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [[2], [50]])
+def test_attend_zeros_between_values(d, new):
+    """Keys and values of zeros have the least scale (e4m3), 2^-110, whatever the others'."""
+    L = 400
+    w = World([L], new, 1, d, 16, True, seed=6).fill()
+    t = np.arange(0, L, 3)
+    scales, pool = [w.ks.cpu().clone(), w.vs.cpu().clone()], [w.k.cpu().clone(), w.v.cpu().clone()]
+    for i in range(2):
+        scales[i][w.table[0, t // 16], :, t % 16] = 17
+        pool[i][w.table[0, t // 16], :, t % 16] = 0
+        w.kv[0][i][t] = 0
+    w.put(pool, scales)
+    q, out = w.attend(2)
+    w.check(q, out)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+def test_a_window_as_large_as_its_type(e4m3, d):
+    """...is none, also for rows in front of the first position."""
+    for new in ([1, 12], [40, 40]):
+        w = World([100, 10], new, 1, d, 16, e4m3, seed=6).fill()
+        for causal in (True, False):
+            q, out = w.attend(2, causal=causal, window=2 ** 31 - 1)
+            w.check(q, out, causal=causal)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("lengths,new", [([777], [1]), ([5000], [3]), ([900, 70, 3000], [300, 1, 40])])
+def test_in_place(e4m3, d, lengths, new):
+    """out in q's place, and q_out in qkv's."""
+    w = World(lengths, new, 2, d, 32, e4m3, seed=7).fill()
+    q, out = w.attend(4)
+    same = q.cuda()
+    w.cache.attend(w.batch, same, same)
+    assert torch.equal(same, out)
+    qkv = bf16(w.g.standard_normal((w.rows, 8 * d)))
+    gain = bf16(w.g.standard_normal(d)).cuda()
+    apart = torch.empty((w.rows, 4, d), dtype=torch.bfloat16, device="cuda")
+    w.cache.append(w.batch, qkv.cuda(), apart, gain, gain, rope_base=1e4)
+    same = qkv.cuda()
+    w.cache.append(w.batch, same, same[:, :4 * d].view(w.rows, 4, d), gain, gain, rope_base=1e4)
+    assert torch.equal(same[:, :4 * d].reshape(w.rows, 4, d), apart) and torch.equal(same[:, 4 * d:].cpu(), qkv[:, 4 * d:])
+    assert w.cache.status() == 0
+
+
 @pytest.mark.parametrize("new", [[1], [40]])
 def test_attend_infinite_scores(new):
     """Keys of the type's lowest value: their scores are minus infinity or far below the others, never NaN."""
