@@ -547,10 +547,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
         const int before = ref;
         ref = max(ref, __reduce_max_sync(0xffffffffu, top));
         if (is_v) bad |= before > -127 && ref - before > kMostRise;
-        bool far = false;                                     // a position's byte is never 0
-#pragma unroll
-        for (int h = 0; h < 4; ++h) far |= e4[h] > -127 && e4[h] - ref + kUp < kLeast;
-        far = __any_sync(0xffffffffu, far);
         if (tid == 0) (is_v ? sh.vref : sh.kref)[j % kScaleSlots] = ref;
         uint4 x[N];
 #pragma unroll
@@ -564,11 +560,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
 #pragma unroll
             for (int q = 0; q < 4; ++q) bad |= __vcmpeq4(w[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
           }
+        // scales further apart than fp16 reaches, but for values of zeros, which have the least; a position's byte is
+        // never 0
+        int low = 0;
+#pragma unroll
+        for (int h = 0; h < 4; ++h) low = min(low, e4[h] - ref + kUp - kLeast);
+        if (__any_sync(0xffffffffu, low < 0)) {
+#pragma unroll
+          for (int k = 0; k < N; ++k) {
+            const int own = __shfl_sync(0xffffffffu, e4[(k * RPI) / 32], (r0 + k * RPI) % 32);
+            bad |= own > -127 && own - ref + kUp < kLeast && any_nonzero(x[k]);
+          }
+        }
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const int r = r0 + k * RPI;
-          const int own = __shfl_sync(0xffffffffu, e4[(k * RPI) / 32], r % 32), e = max(own - ref + kUp, -25);
-          if (far) bad |= own > -127 && e < kLeast && any_nonzero(x[k]);
+          const int e = max(__shfl_sync(0xffffffffu, e4[(k * RPI) / 32], r % 32) - ref + kUp, -25);
           const uint32_t f = hf_pack(pow2i(e), pow2i(e));
           const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
           uint32_t y[8];
