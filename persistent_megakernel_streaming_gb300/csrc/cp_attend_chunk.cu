@@ -40,6 +40,8 @@
 // 154 us, 890 TFLOP/s, of which each block's start and end are 10 us. A second
 // issuing warp hides the gaps alone, but pulls the two softmaxes into step:
 // 186 us, with turns between the two 149.
+#include <type_traits>
+
 #include "cp_attend.cuh"
 
 namespace cp {
@@ -70,11 +72,15 @@ struct Cfg {
 // TMEM columns: the two tiles' scores (and weights), then their outputs
 constexpr uint32_t kTmemS = 0, kTmemO = 256, kTmemCols = 512;
 
-// What the end of a block needs, kept out of the registers meanwhile.
+// What the block computes: found by the load warp, and kept out of the others' registers.
 struct Item {
   Seq s;
-  int seq, kv, part, parts, row0, rows_here, whole, t_begin, t_end, any[2], first_row, first_head;
-  uint32_t magic;
+  int seq;                     // -1: nothing
+  int kv, part, parts, whole;
+  int row0, rows_here;         // the pair's rows
+  int first_row, first_head;   // row i of them is new row first_row + (first_head + i) / group, head (first_head + i) % group
+  int lo, t_begin, t_end, ntiles;       // first position that some row sees; the part's, and its tiles
+  int jb[2], je[2], all_lo[2], all_hi[2];   // tiles that tile i of rows takes part in, and the positions that all its rows see
 };
 
 struct ChunkShared {
@@ -174,16 +180,16 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     pdl_wait();
     return;
   }
-  if (warp == kLoadWarp) {               // a lane a barrier
+  if (warp == kHelper0) {                // a lane a barrier
     if (lane < 8) mb_init(saddr(&sh.raw_full[lane]), 1);
     else if (lane < 16) mb_init(saddr(&sh.raw_empty[lane - 8]), kHelpers / 32);
-    else if (lane < 24) mb_init(saddr(&sh.op_full[lane - 16]), kHelpers);
+    else if (lane < 24) mb_init(saddr(&sh.op_full[lane - 16]), kHelpers / 32);
     else if (lane < 28) mb_init(saddr(&sh.done[lane - 24]), 1);
     if (lane < 2) {
       mb_init(saddr(&sh.s_full[lane]), 1);
       mb_init(saddr(&sh.p_full[lane]), 8);
     }
-    if (lane == 2) mb_init(saddr(&sh.q_full), kSoftWarps * 32);
+    if (lane == 2) mb_init(saddr(&sh.q_full), kSoftWarps);
     if (lane == 3) mb_init(saddr(&sh.o_full), 1);
     if (lane == 4) {
       sh.abort = sh.bad = 0;
@@ -196,12 +202,13 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     tm_relinquish();
   }
 
-  // which sequence and which of its tile pairs: every warp counts the pairs, 32 sequences at a time
-  int seq = -1, pair = 0;
-  Seq s{};
-  {
+  // The load warp finds the block's item alone: every warp doing so took the issue slots for 2 to 3 us a block.
+  if (warp == kLoadWarp) {
+    // which sequence and which of its tile pairs: the pairs are counted 32 sequences at a time
+    int seq = -1, pair = 0;
+    Seq s{};
+    const int kv = blockIdx.x % p.c.heads, part = blockIdx.y, want = blockIdx.x / p.c.heads;
     int before = 0;
-    const int want = blockIdx.x / p.c.heads;
     for (int i0 = 0; i0 < p.b.n && seq < 0; i0 += 32) {
       int pairs = 0;
       Seq one{};
@@ -229,89 +236,64 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-  }
-  pdl_trigger();
-  auto leave = [&] {                     // a block without work
-    if (warp == kMmaWarp) {
-      __syncwarp();
-      tm_dealloc(sh.tmem, kTmemCols);
-    }
-    pdl_wait();
-  };
-  if (seq < 0) {
-    leave();
-    return;
-  }
-  const int kv = blockIdx.x % p.c.heads, part = blockIdx.y;
-  const int nrows = s.n * p.group;
-  const int row0 = pair * kPairRows;
-  const int rows_here = min(kPairRows, nrows - row0);
-  // row i of the pair is new row first_row + (first_head + i) / group, head (first_head + i) % group of the kv head; the
-  // quotient by a multiplication, exact for these sums below 320
-  const int first_row = row0 / p.group, first_head = row0 % p.group;
-  const uint32_t magic = (65535u + p.group) / p.group;
-  auto new_row = [&](int i) { return first_row + (int)(((uint32_t)(first_head + i) * magic) >> 16); };
-  auto head_of = [&](int i) { return first_head + i - (int)(((uint32_t)(first_head + i) * magic) >> 16) * p.group; };
-  auto pos_of = [&](int i) { return s.first + min(i, nrows - 1) / p.group; };
-  const Range range = item_range(p, pos_of(row0), pos_of(row0 + rows_here - 1), s.len, kChunkAlign);
-  const int parts = parts_of(range, p.a.chunk_chunk);
-  if (part >= max(parts, 1)) {
-    leave();
-    return;
-  }
-  const bool whole = parts <= 1;
-  const int t_begin = range.base + part * p.a.chunk_chunk;
-  const int t_end = min(t_begin + p.a.chunk_chunk, range.hi);
-  const int ntiles = t_end > t_begin ? (t_end - t_begin + kTile - 1) / kTile : 0;
-  // tiles that stream i (tile of rows i) takes part in, and the positions that all its rows see
-  int jb[2], je[2], all_lo[2], all_hi[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int f = row0 + i * kTile;
-    jb[i] = je[i] = 0;
-    all_lo[i] = all_hi[i] = 0;
-    if (f < nrows) {
-      const int first = pos_of(f), last = pos_of(f + kTile - 1);
+    Item& it = sh.item;
+    if (seq >= 0) {
+      const int nrows = s.n * p.group, row0 = pair * kPairRows, rows_here = min(kPairRows, nrows - row0);
+      const int first_row = row0 / p.group, first_head = row0 - first_row * p.group;
+      auto pos_of = [&](int i) { return s.first + first_row + (int)(((uint32_t)(first_head + min(i, rows_here - 1)) * p.magic) >> 16); };
+      // lane 0 for the pair, lanes 1 and 2 for its tiles of rows
+      const int f = lane == 2 ? kTile : 0;
+      const int first = pos_of(f), last = pos_of(lane == 1 ? kTile - 1 : kPairRows - 1);
       const Range r = item_range(p, first, last, s.len, kChunkAlign);
-      const int a = max(r.lo, t_begin), b = min(r.hi, t_end);
-      if (b > a) {
-        jb[i] = (a - t_begin) / kTile;
-        je[i] = (b - t_begin + kTile - 1) / kTile;
+      const Range range = {__shfl_sync(0xffffffffu, r.lo, 0), __shfl_sync(0xffffffffu, r.hi, 0), __shfl_sync(0xffffffffu, r.base, 0)};
+      const int parts = parts_of(range, p.a.chunk_chunk);
+      const int t_begin = range.base + part * p.a.chunk_chunk;
+      const int t_end = min(t_begin + p.a.chunk_chunk, range.hi);
+      if (part >= max(parts, 1)) seq = -1;
+      if (lane == 1 || lane == 2) {
+        const int x = lane - 1, a = max(r.lo, t_begin), b = min(r.hi, t_end);
+        const bool any = f < rows_here && b > a;
+        int d;
+        it.jb[x] = any ? (a - t_begin) / kTile : 0;
+        it.je[x] = any ? (b - t_begin + kTile - 1) / kTile : 0;
+        visible(p, last, s.len, &it.all_lo[x], &d);
+        visible(p, first, s.len, &d, &it.all_hi[x]);
       }
-      int d;
-      visible(p, last, s.len, &all_lo[i], &d);
-      visible(p, first, s.len, &d, &all_hi[i]);
+      if (lane == 0) {
+        it.s = s;
+        it.kv = kv;
+        it.part = part;
+        it.parts = parts;
+        it.whole = parts <= 1;
+        it.row0 = row0;
+        it.rows_here = rows_here;
+        it.first_row = first_row;
+        it.first_head = first_head;
+        it.lo = range.lo;
+        it.t_begin = t_begin;
+        it.t_end = t_end;
+        it.ntiles = t_end > t_begin ? (t_end - t_begin + kTile - 1) / kTile : 0;
+      }
     }
+    if (lane == 0) it.seq = seq;
   }
-
-  const uint32_t q_s = saddr(ops), op_s = q_s + 2 * C::kOpBytes, raw_s = E4M3 ? op_s + NO * C::kOpBytes : op_s;
-
-  // a softmax thread's part of q: 16 of its pair of warps' 32 rows, a row's units side by side; asked for here, so that
-  // it is there behind the barrier
-  constexpr int UPR = D / 8, RPI = 32 / UPR, N = 16 / RPI;
-  const int u = lane % UPR, base = (warp & 3) * 32 + ((warp >> 2) & 1) * 16 + lane / UPR;
-  uint4 x[N];
-  if (warp < kSoftWarps) {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int r = (warp >> 3) * kTile + base + k * RPI;
-      x[k] = make_uint4(0, 0, 0, 0);
-      if (r < rows_here)
-        x[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(s.row0 + new_row(r)) * p.q_row +
-                                               (int64_t)(kv * p.group + head_of(r)) * p.q_head + u * 8);
-    }
-  }
-  if (threadIdx.x == 0)
-    sh.item = {s, seq, kv, part, parts, row0, rows_here, whole, t_begin, t_end, {je[0] > jb[0], je[1] > jb[1]}, first_row, first_head, magic};
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
+  pdl_trigger();
+  const Item& it = sh.item;
+  if (it.seq < 0) {
+    if (warp == kMmaWarp) tm_dealloc(sh.tmem, kTmemCols);
+    pdl_wait();
+    return;
+  }
   const uint32_t tmem = sh.tmem;
+
+  const uint32_t q_s = saddr(ops), op_s = q_s + 2 * C::kOpBytes, raw_s = E4M3 ? op_s + NO * C::kOpBytes : op_s;
 
   // a softmax thread's row, and which half of a tile's positions (and later of its columns) is its
   const int i = warp >> 3, half = (warp >> 2) & 1;       // stream (warps 0-15)
   const int slot = (i * kTile + (warp & 3) * 32 + lane) & (kPairRows - 1);
-  const bool mine = warp < kSoftWarps && slot < rows_here;
   const int pair_id = 1 + i * 4 + (warp & 3);            // the named barrier of the row's two warps
   float l = 0.f, m = -INFINITY;
   int vr = 0;
@@ -323,7 +305,23 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
 
   if (warp < kSoftWarps) {
     // ---------------------------------------------------------------- softmax
+    // a row of the pair: its new row and its head; the quotient by a multiplication, exact for sums below 320
+    const int first_row = it.first_row, first_head = it.first_head, rows_here = it.rows_here;
+    auto new_row = [&](int r) { return first_row + (int)(((uint32_t)(first_head + r) * p.magic) >> 16); };
     {
+      // a thread's part of q: 16 of its pair of warps' 32 rows, a row's units side by side
+      constexpr int UPR = D / 8, RPI = 32 / UPR, N = 16 / RPI;
+      const int u = lane % UPR, base = (warp & 3) * 32 + half * 16 + lane / UPR;
+      const uint16_t* src = p.q + (int64_t)it.s.row0 * p.q_row + (int64_t)(it.kv * p.group) * p.q_head + u * 8;
+      uint4 x[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int r = i * kTile + base + k * RPI, n = new_row(r);
+        x[k] = make_uint4(0, 0, 0, 0);
+        if (r < rows_here)
+          x[k] = *reinterpret_cast<const uint4*>(src + (int64_t)n * p.q_row +
+                                                 (int64_t)(first_head + r - (n - first_row) * p.group) * p.q_head);
+      }
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         if (E4M3) {                        // in fp16, times a power of two of its row
@@ -344,16 +342,17 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
         st_shared_v4u(q_s + i * C::kOpBytes + op_at(base + k * RPI, u), x[k]);
       }
       fence_proxy_async_smem();
-      mb_arrive(saddr(&sh.q_full));
+      __syncwarp();
+      if (lane == 0) mb_arrive(saddr(&sh.q_full));
       if (E4M3) pair_or(pair_id, false);
     }
     const float row_scale = E4M3 ? sh.row[0][slot] : p.scale_log2;
-    const int pos = mine ? s.first + new_row(slot) : -1;
+    const int pos = slot < rows_here ? it.s.first + new_row(slot) : -1;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_t = tmem + lanes + kTmemS + i * kTile + half * kHalf;
     const uint32_t o_t = tmem + lanes + kTmemO + i * D + half * (D / 2);
-    const int j0 = i ? jb[1] : jb[0], j1 = i ? je[1] : je[0];
-    const int see_lo = i ? all_lo[1] : all_lo[0], see_hi = i ? all_hi[1] : all_hi[0];
+    const int j0 = it.jb[i], j1 = it.je[i], t_begin = it.t_begin;
+    const int see_lo = it.all_lo[i], see_hi = it.all_hi[i];
     uint64_t sum[2] = {0, 0};              // two pairs of partial sums
     for (int j = j0; j < j1; ++j) {
       const int n = j - j0;
@@ -368,7 +367,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       auto ready = [&](uint32_t* x, int c) {
         if (edge) {
           int lo, hi;
-          visible(p, pos, sh.item.s.len, &lo, &hi);
+          visible(p, pos, it.s.len, &lo, &hi);
           lo -= t0 + half * kHalf + c;
           hi -= t0 + half * kHalf + c;
 #pragma unroll
@@ -483,8 +482,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- helpers
     const int tid = threadIdx.x - kHelper0 * 32;
-    const int pair_lo = max(all_lo[0], all_lo[1]);
-    const int pair_hi = rows_here > kTile ? min(all_hi[0], all_hi[1]) : all_hi[0];
+    const int pair_lo = it.all_lo[1], pair_hi = it.all_hi[0];         // seen by the last row, and by the first
+    const int lo = it.lo, t_begin = it.t_begin, t_end = it.t_end, ntiles = it.ntiles;
     bool bad = false;
     if (!E4M3) {
       constexpr int UPR = D / 8, RPI = kHelpers / UPR;      // 16-byte units a row, rows an iteration
@@ -492,20 +491,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       for (int j = 0; j < ntiles; ++j) {
         const int n = 2 * j + 1, t0 = t_begin + j * kTile;
         if (!wait_warp(sh, saddr(&sh.raw_full[n % NO]), (n / NO) & 1)) break;
-        if (t0 < pair_lo || t0 + kTile > pair_hi) {         // also wherever a value is outside [range.lo, t_end)
+        if (t0 < pair_lo || t0 + kTile > pair_hi) {         // also wherever a value is outside [lo, t_end)
           for (int r = tid / UPR; r < kTile; r += RPI) {
             const uint32_t at = op_s + (n % NO) * C::kOpBytes + op_at(r, u);
-            if (t0 + r < range.lo || t0 + r >= t_end) st_shared_v4u(at, make_uint4(0, 0, 0, 0));
+            if (t0 + r < lo || t0 + r >= t_end) st_shared_v4u(at, make_uint4(0, 0, 0, 0));
             else bad |= any_nonfinite<false>(at);
           }
           fence_proxy_async_smem();
         }
-        mb_arrive(saddr(&sh.op_full[n % NO]));
+        __syncwarp();
+        if (lane == 0) mb_arrive(saddr(&sh.op_full[n % NO]));
       }
     } else {
       constexpr int UPR = D / 16, RPI = kHelpers / UPR, N = kTile / RPI;
       const int u = tid % UPR, r0 = tid / UPR;
-      const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
+      const int kv = it.kv;
+      const int32_t* table = p.b.table + (int64_t)it.seq * p.b.table_stride;
       // each warp has the scale bytes of all of a tile: positions t0 + 32 h + lane. Pages are asked for two tiles
       // ahead and scales one, and nothing is done with them before their turn.
       uint8_t key_scale[4], value_scale[4];
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
           const int t = t_begin + j * kTile + h * 32 + lane;
           const int page = __shfl_sync(0xffffffffu, pg, h * 2 + lane / 16);
           key_scale[h] = value_scale[h] = 0;
-          if ((uint32_t)page < (uint32_t)p.c.pages && j < ntiles && t >= range.lo && t < t_end) {
+          if ((uint32_t)page < (uint32_t)p.c.pages && j < ntiles && t >= lo && t < t_end) {
             const int64_t so = slot_scale(p.c, page, kv, t);
             key_scale[h] = p.c.ks[so];
             value_scale[h] = p.c.vs[so];
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
         if (!wait_warp(sh, saddr(&sh.raw_full[n % NR]), (n / NR) & 1)) break;
         if (n >= NO && !wait_done(sh, n - NO)) break;
         const uint32_t src = raw_s + (n % NR) * C::kRawBytes + u * 16, dst = op_s + (n % NO) * C::kOpBytes;
-        const bool ends = is_v && (t0 < range.lo || t0 + kTile > t_end);
+        const bool ends = is_v && (t0 < lo || t0 + kTile > t_end);
         const bool look = is_v && (t0 < pair_lo || t0 + kTile > pair_hi);
         // every row by its scale next to the largest so far: a power of two, exact where fp16 reaches
         int e4[4], top = -127;
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
 #pragma unroll
           for (int k = 0; k < N; ++k) {
             const int r = r0 + k * RPI;
-            if (ends && (t0 + r < range.lo || t0 + r >= t_end)) x[k] = make_uint4(0, 0, 0, 0);
+            if (ends && (t0 + r < lo || t0 + r >= t_end)) x[k] = make_uint4(0, 0, 0, 0);
             const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
 #pragma unroll
             for (int q = 0; q < 4; ++q) bad |= __vcmpeq4(w[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
@@ -594,20 +595,22 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
           pg = page_at(j + 2);
         }
         fence_proxy_async_smem();
-        mb_arrive(saddr(&sh.op_full[n % NO]));
+        __syncwarp();
+        if (lane == 0) mb_arrive(saddr(&sh.op_full[n % NO]));
       }
     }
     if (bad) *(volatile int*)&sh.bad = 1;
   } else if (warp == kLoadWarp) {
     // ---------------------------------------------------------------- loads
-    // lane i < 128 / page size: the tile's i-th page. What is outside [range.lo, t_end), on no page or on a bad one
+    // lane i < 128 / page size: the tile's i-th page. What is outside [lo, t_end), on no page or on a bad one
     // is asked for behind the pool's last page, which the tensor map returns as zeros.
-    const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
+    const int32_t* table = p.b.table + (int64_t)it.seq * p.b.table_stride;
+    const int lo = it.lo, t_begin = it.t_begin, t_end = it.t_end, ntiles = it.ntiles, kv = it.kv;
     const int size = 1 << p.c.page_shift, boxes = kTile >> p.c.page_shift;
     auto page_at = [&](int j) {
       const int t = t_begin + j * kTile + lane * size;
       int pg = -1;
-      if (j < ntiles && lane < boxes && t + size > range.lo && t < t_end) {
+      if (j < ntiles && lane < boxes && t + size > lo && t < t_end) {
         pg = page_of(table, p.b.width, p.c.pages, p.c.page_shift, t);
         if (pg < 0) set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
       }
@@ -620,6 +623,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       const uint32_t bar = saddr(&sh.raw_full[n % NR]);
       asked = n + 1;
       if (n == 0 && p.stall) continue;
+      // q goes first: when all blocks start at once, a ring's worth of K and V in front of it is 2 us
+      if (n == 1 && !wait_warp(sh, saddr(&sh.q_full), 0)) break;
       if (lane == 0) mb_expect(bar, E4M3 ? C::kRawBytes : C::kOpBytes);
       __syncwarp();
       if (lane < boxes) {
@@ -642,9 +647,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     const uint32_t lead = lane == 0;
     const uint32_t id_s = idesc_m128(kTile, E4M3, false), id_o = idesc_m128(D, E4M3, true);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-    const int tiles = __shfl_sync(0xffffffffu, ntiles, 0);
-    const int b0 = __shfl_sync(0xffffffffu, jb[0], 0), b1 = __shfl_sync(0xffffffffu, jb[1], 0);
-    const int e0 = __shfl_sync(0xffffffffu, je[0], 0), e1 = __shfl_sync(0xffffffffu, je[1], 0);
+    const int tiles = __shfl_sync(0xffffffffu, it.ntiles, 0);
+    const int b0 = __shfl_sync(0xffffffffu, it.jb[0], 0), b1 = __shfl_sync(0xffffffffu, it.jb[1], 0);
+    const int e0 = __shfl_sync(0xffffffffu, it.je[0], 0), e1 = __shfl_sync(0xffffffffu, it.je[1], 0);
     const uint32_t ops = __shfl_sync(0xffffffffu, op_s, 0), q0 = __shfl_sync(0xffffffffu, q_s, 0);
     const uint64_t q_desc = sdesc_sw128(q0), k_desc = sdesc_sw128(ops), v_desc = sdesc_sw128_cols(ops, C::kSlab);
     constexpr uint32_t kOpDesc = C::kOpBytes >> 4;
@@ -712,7 +717,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
 
   const bool failed = sh.abort != 0;
   if (failed && threadIdx.x == 0) set_status(p.c.status, CP_ERR_TIMEOUT);
-  const Item& it = sh.item;
   constexpr int kPitch = D + 4;
   static_assert(kPairRows * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the rows fit the operands' memory");
   float* averages = reinterpret_cast<float*>(ops);
@@ -725,9 +729,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     const int slot = threadIdx.x / 256 * kTile + (threadIdx.x & 127), half = (warp >> 2) & 1, i = warp >> 3;
     const int pair_id = 1 + i * 4 + (warp & 3);
     const uint32_t o_t = sh.tmem + ((uint32_t)(warp & 3) << 21) + kTmemO + i * D + half * (D / 2);
-    const bool any = it.any[i];
+    const bool any = it.je[i] > it.jb[i], whole = it.whole;
     const int group = p.group, first_row = it.first_row, first_head = it.first_head, head0 = it.kv * group;
-    const uint32_t magic = it.magic;
+    const uint32_t magic = p.magic;
     auto place = [&](int r, int64_t* row, int* head) {
       const int q = (int)(((uint32_t)(first_head + r) * magic) >> 16);
       *row = it.s.row0 + first_row + q;
@@ -737,47 +741,61 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const float e = E4M3 ? pow2i(min(max(vr - kUp, -126), 127)) : 1.f;
     float* stage = averages + (i * kTile + (warp & 3) * 32) * kPitch;
+    uint16_t* stage16 = reinterpret_cast<uint16_t*>(stage);
+    constexpr int kPitch16 = D + 8;
 #pragma unroll 1
     for (int c = 0; c < D / 2; c += 32) {
       float v[32];
       if (any) tm_ld32(o_t + c, v);
 #pragma unroll
-      for (int x = 0; x < 32; x += 4) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (any && inv != 0.f) y = make_float4(v[x] * inv * e, v[x + 1] * inv * e, v[x + 2] * inv * e, v[x + 3] * inv * e);
-        *reinterpret_cast<float4*>(stage + lane * kPitch + half * (D / 2) + c + x) = y;
+      for (int x = 0; x < 32; ++x) v[x] = any && inv != 0.f ? v[x] * inv * e : 0.f;
+      if (whole) {
+#pragma unroll
+        for (int x = 0; x < 32; x += 8)
+          *reinterpret_cast<uint4*>(stage16 + lane * kPitch16 + half * (D / 2) + c + x) =
+              make_uint4(bf_pack(v[x], v[x + 1]), bf_pack(v[x + 2], v[x + 3]), bf_pack(v[x + 4], v[x + 5]), bf_pack(v[x + 6], v[x + 7]));
+      } else {
+#pragma unroll
+        for (int x = 0; x < 32; x += 4)
+          *reinterpret_cast<float4*>(stage + lane * kPitch + half * (D / 2) + c + x) = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
       }
     }
     const float lse = l == 0.f ? -INFINITY : m + log2f(l) - kBias;
     int64_t row;
     int head;
-    if (slot < it.rows_here && !it.whole && !cluster && half == 0) {
+    if (slot < it.rows_here && !whole && !cluster && half == 0) {
       place(slot, &row, &head);
       store_lse(p, it.part, row, head, lse);
     }
     tm_fence_before();
     pair_or(pair_id, false);
     if (cluster && half == 0) sh.row[0][slot] = lse;
-    // a row at a time (two of 64 columns), the next row's place by counting on
-    constexpr int LPR = D / 4, RPI = 32 / LPR;
-    const int r0 = half * 16 + lane / LPR, d = lane % LPR * 4;
-    int left = it.rows_here - (i * kTile + (warp & 3) * 32 + r0);
-    place(i * kTile + (warp & 3) * 32 + r0, &row, &head);
-    head -= head0;
-    const float* src = stage + r0 * kPitch + d;
-    const int64_t o_row = p.o_row, o_head = p.o_head;
-    uint16_t* out = p.out + head0 * o_head + d;
-    float* part_o = p.part_o + ((int64_t)it.part * p.b.rows * p.q_heads + head0) * D + d;
-    const bool whole = it.whole;
+    // 16 of the rows a warp, their elements side by side, 16 bytes a lane; the next row's place by counting on
+    const int rows0 = i * kTile + (warp & 3) * 32 + half * 16;
+    auto rows_out = [&](auto per, auto store) {
+      constexpr int LPR = D / decltype(per)::value, RPI = 32 / LPR;
+      const int r0 = lane / LPR, d = lane % LPR * decltype(per)::value;
+      int left = it.rows_here - (rows0 + r0);
+      place(rows0 + r0, &row, &head);
+      head -= head0;
 #pragma unroll 4
-    for (int k = cluster ? 16 : 0; k < 16; k += RPI, left -= RPI, src += RPI * kPitch) {
-      if (left > 0) {
-        const float4 y = *reinterpret_cast<const float4*>(src);
-        if (whole) *reinterpret_cast<uint2*>(out + row * o_row + head * o_head) = make_uint2(bf_pack(y.x, y.y), bf_pack(y.z, y.w));
-        else *reinterpret_cast<float4*>(part_o + (row * p.q_heads + head) * D) = y;
+      for (int k = 0; k < 16; k += RPI, left -= RPI) {
+        if (left > 0) store(half * 16 + r0 + k, d);
+        head += RPI;
+        for (; head >= group; head -= group) ++row;
       }
-      head += RPI;
-      for (; head >= group; head -= group) ++row;
+    };
+    if (whole) {
+      const int64_t o_row = p.o_row, o_head = p.o_head;
+      uint16_t* out = p.out + head0 * o_head;
+      rows_out(std::integral_constant<int, 8>(), [&](int r, int d) {
+        *reinterpret_cast<uint4*>(out + row * o_row + head * o_head + d) = *reinterpret_cast<const uint4*>(stage16 + r * kPitch16 + d);
+      });
+    } else if (!cluster) {
+      float* part_o = p.part_o + ((int64_t)it.part * p.b.rows * p.q_heads + head0) * D;
+      rows_out(std::integral_constant<int, 4>(), [&](int r, int d) {
+        *reinterpret_cast<float4*>(part_o + (row * p.q_heads + head) * D + d) = *reinterpret_cast<const float4*>(stage + r * kPitch + d);
+      });
     }
   }
   __syncthreads();
@@ -790,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     for (int r = it.part + it.parts * (warp * RPI + lane / LPR); r < it.rows_here; r += it.parts * (C::kThreads / 32) * RPI) {
       float x[4];
       join4(saddr(averages + r * kPitch + d), saddr(&sh.row[0][r]), it.parts, x);
-      const int q = (int)(((uint32_t)(it.first_head + r) * it.magic) >> 16);
+      const int q = (int)(((uint32_t)(it.first_head + r) * p.magic) >> 16);
       store4<D>(p, 0, true, it.s.row0 + it.first_row + q, it.kv * p.group + it.first_head + r - q * p.group, d, x);
     }
     __syncwarp();

@@ -460,6 +460,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   p->out = static_cast<uint16_t*>(a->out);
   p->q_heads = a->q_heads;
   p->group = a->q_heads / d.kv_heads;
+  p->magic = (65535u + p->group) / p->group;
   const double scale = a->scale > 0.f ? (double)a->scale : 1.0 / std::sqrt((double)d.head_dim);
   p->scale_log2 = (float)(scale * 1.4426950408889634);
   p->causal = a->causal != 0;

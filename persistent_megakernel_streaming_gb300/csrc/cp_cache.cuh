@@ -148,6 +148,7 @@ struct AttendParams {
   float* part_lse;                        // [parts][rows][q_heads]: log2 of its sum of exponentials
   int64_t q_row, q_head, o_row, o_head;   // element strides
   int group;                              // query heads per kv head
+  uint32_t magic;                         // x / group is x * magic >> 16, for x below 320
   int q_heads;
   float scale_log2;                       // scale * log2(e)
   int causal, window;
