@@ -177,7 +177,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
 
   if (ops + C::kTiles + sizeof(ChunkShared) > raw + Smem<D, E4M3>::kBytes) {
     set_status(p.c.status, CP_ERR_UNSUPPORTED);
-    pdl_wait();
     return;
   }
   if (warp == kHelper0) {                // a lane a barrier
@@ -284,7 +283,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
   const Item& it = sh.item;
   if (it.seq < 0) {
     if (warp == kMmaWarp) tm_dealloc(sh.tmem, kTmemCols);
-    pdl_wait();
     return;
   }
   const uint32_t tmem = sh.tmem;
@@ -818,7 +816,6 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     tm_fence_after();
     tm_dealloc(sh.tmem, kTmemCols);
   }
-  pdl_wait();            // this grid's end stands for the step kernel's too
 }
 
 }  // namespace
@@ -837,8 +834,7 @@ cudaError_t prepare_attend_chunk() {
 template <int D, bool E4M3>
 static cudaError_t launch(const AttendParams& p, const CacheMaps& maps, cudaStream_t s) {
   const dim3 grid((unsigned)(p.c.heads * chunk_pairs(p.b, p.group)), p.a.chunk_parts);
-  // behind the step kernel, whose results it does not need, it may fill the SMs that one leaves
-  return launch_as(attend_chunk_kernel<D, E4M3>, grid, 1, p.a.chunk_cluster ? p.a.chunk_parts : 1, p.a.use_step != 0,
+  return launch_as(attend_chunk_kernel<D, E4M3>, grid, 1, p.a.chunk_cluster ? p.a.chunk_parts : 1, false,
                    Cfg<D, E4M3>::kThreads, Smem<D, E4M3>::kBytes, s, p, maps);
 }
 cudaError_t launch_attend_chunk(const AttendParams& p, const CacheMaps& maps, int head_dim, bool e4m3, cudaStream_t s) {
