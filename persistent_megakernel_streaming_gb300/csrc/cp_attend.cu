@@ -10,7 +10,6 @@ namespace cp {
 namespace cache {
 
 // ------------------------------------------------------------------ plan
-constexpr int kSms = 152;
 constexpr int kStepBlocks = 2 * kSms; // step blocks resident at once
 constexpr int kStepCluster = kMostCluster;
 constexpr int kMaxStepChunk = 4096;   // positions a step block holds page numbers for
@@ -55,22 +54,22 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
     // a window spans itself and the item's rows; not causal, the rows up to the last of the sequence
     const int64_t ahead = causal ? std::min(b.max_new, (kPairRows + group - 1) / group + 1) : b.max_new;
     if (window > 0) all = std::min<int64_t>(all, (int64_t)window + ahead + kChunkAlign - 1);
-    // In nanoseconds: a tile of 128 positions 1700 (heads of 64: 1200), a block's start and end 9000, joining the parts
-    // of a cluster 2500, or through the workspace 3000 and the parts' results written and read again at 5 TB/s. Clusters
+    // In nanoseconds: rounds of blocks (chunk_rounds_ns), joining the parts of a cluster 2500, or through the workspace 3000 and the parts' results written and read again at 5 TB/s. Clusters
     // only where all blocks are resident at once: their blocks start and leave together (a ragged batch in two rounds
     // 169 us, in clusters 179).
     double best = 0;
     int64_t parts = 1;
-    const double tile_ns = head_dim == 128 ? 1700 : 1200;
     const double join_ns = 2.0 * b.rows * q_heads * head_dim * 4 / 5000;
     for (int64_t n = 1; n <= 32; ++n) {
-      const int64_t tiles = ((all + n - 1) / n + 127) / 128;
-      const double cost = (double)((blocks * n + kSms - 1) / kSms) * (tiles * tile_ns + 9000) +
+      const double cost = chunk_rounds_ns(blocks * n, (int)(((all + n - 1) / n + 127) / 128), head_dim) +
                           (n == 1 ? 0 : n <= kMostCluster && blocks * n <= kSms ? 2500 : 3000 + n * join_ns);
       if (n == 1 || cost < best) best = cost, parts = n;
     }
     a.chunk_chunk = (int)(((all + parts - 1) / parts + 127) / 128 * 128);
     a.chunk_parts = (int)((all + a.chunk_chunk - 1) / a.chunk_chunk);
+    a.chunk_span = (int)all;
+    // a batch in more than one round, of items that one round holds: ragged, they may leave one of longer parts
+    a.chunk_coarser = b.n > 1 && a.chunk_parts > 1 && blocks * a.chunk_parts > kSms && blocks <= kSms;
     a.chunk_cluster = a.chunk_parts > 1 && a.chunk_parts <= kMostCluster && blocks * a.chunk_parts <= kSms;
   }
   return a;
@@ -78,7 +77,7 @@ AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_d
 
 size_t attend_workspace(const AttendPlan& a, const BatchView& b, int q_heads, int head_dim) {
   const int parts = kept_parts(a);
-  return parts > 1 ? (size_t)parts * b.rows * q_heads * (head_dim + 1) * sizeof(float) : 0;
+  return parts > 1 ? (size_t)parts * b.rows * q_heads * (head_dim + 1) * sizeof(float) + 16 : 0;
 }
 
 namespace {
@@ -599,7 +598,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
 // ------------------------------------------------------------------ join
 // One warp a (row, query head) whose item was cut: the parts' averages weighed
 // by their sums. Bound by reading the parts once, small next to the cache
-// (largest where chunks are cut that fill no cluster: 16 us of a call of 170).
+// (largest where chunks are cut that fill no cluster: 16 us of a call of 139).
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();
@@ -626,7 +625,8 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant_
     const int i1 = min(i0 + kPairRows, nrows) - 1;
     parts = p.a.chunk_cluster
                 ? 0
-                : parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len, kChunkAlign), p.a.chunk_chunk);
+                : parts_of(item_range(p, s.first + i0 / p.group, s.first + i1 / p.group, s.len, kChunkAlign),
+                           p.a.chunk_coarser ? *p.coarser : p.a.chunk_chunk);
   }
   if (parts <= 1) return;
   const int64_t n = (int64_t)p.b.rows * p.q_heads;

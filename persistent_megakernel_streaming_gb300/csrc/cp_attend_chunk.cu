@@ -35,9 +35,9 @@
 // Bound by the chain from a tile's scores through its softmax to its second
 // product, and by the issuing warp: nothing of what it does between two groups
 // of products is hidden (each clock of it is one of the tensor core's). 512
-// rows of 16/8 heads of 128 behind 32256 positions, bf16: 135 us a call, 1010
+// rows of 16/8 heads of 128 behind 32256 positions, bf16: 133 us a call, 1020
 // TFLOP/s, the tensor pipe busy 52 %, 128 of 152 SMs; two prompts of 4096:
-// 154 us, 890 TFLOP/s, of which each block's start and end are 10 us. A second
+// 150 us, 919 TFLOP/s, of which each block's start and end are 9 us. A second
 // issuing warp hides the gaps alone, but pulls the two softmaxes into step:
 // 186 us, with turns between the two 149.
 #include <type_traits>
@@ -165,6 +165,40 @@ __device__ __forceinline__ uint32_t op_at(int r, int u) {
   return (uint32_t)((u >> 3) * (kTile * 128) + r * 128 + (((u & 7) ^ (r & 7)) << 4));
 }
 
+// Positions a part, by a whole warp: the plan's, made for sequences that all have the longest one's length and for more
+// than one round of blocks, or longer ones if at the sequences' own lengths those are one round that costs less. Every
+// block comes to the same. (16 sequences of 700 to 9000 e4m3 positions, four of them with 301 new rows: 150 us a call
+// in the plan's parts, 140 in these. Choosing among several rounds too measured up to 7 % slower and 5 % faster.)
+template <int D>
+__device__ __forceinline__ int chosen_chunk(const AttendParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int n = min(lane + 1, p.a.chunk_parts);
+  const uint32_t tiles = ((p.a.chunk_span + n - 1) / n + kTile - 1) / kTile, magic = 0xffffffffu / tiles + 1;
+  uint32_t blocks = 0, all = 0;
+  for (int i0 = 0; i0 < p.b.n; i0 += 32) {
+    uint32_t pairs = 0, len = 0;
+    if (i0 + lane < p.b.n) {
+      const Seq s = seq_of(p.b, i0 + lane, p.c.status);
+      const int rows = s.n * p.group;
+      if (rows > kStepRows || !p.a.use_step) pairs = (rows + kPairRows - 1) / kPairRows * p.c.heads;
+      len = (min(s.len, p.a.chunk_span) + kTile - 1) / kTile;
+    }
+    for (uint32_t left = __ballot_sync(0xffffffffu, pairs > 0); left; left &= left - 1) {
+      const int at = __ffs(left) - 1;
+      const uint32_t items = __shfl_sync(0xffffffffu, pairs, at), of_one = __shfl_sync(0xffffffffu, len, at);
+      blocks += items * (tiles == 1 ? of_one : __umulhi(of_one + tiles - 1, magic));
+      all += items * of_one;
+    }
+  }
+  // a round costs its longest block; several, of uneven blocks that follow one another closely, all work and half a block
+  const float block = chunk_rounds_ns(1, tiles, D);
+  const float even = ((float)all * (D == 128 ? kTileNs128 : kTileNs64) + (float)blocks * kBlockNs) * (1.f / kSms) + 0.5f * block;
+  const float plan = __shfl_sync(0xffffffffu, even, 31);       // lane 31 has the plan's
+  const uint32_t fits = __ballot_sync(0xffffffffu, blocks <= kSms && block < plan);
+  const int chosen = __shfl_sync(0xffffffffu, (int)tiles, fits ? 31 - __clz(fits) : 31);
+  return fits ? chosen * kTile : p.a.chunk_chunk;
+}
+
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel(const __grid_constant__ AttendParams p,
                                                                     const __grid_constant__ CacheMaps maps) {
@@ -245,9 +279,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       const int first = pos_of(f), last = pos_of(lane == 1 ? kTile - 1 : kPairRows - 1);
       const Range r = item_range(p, first, last, s.len, kChunkAlign);
       const Range range = {__shfl_sync(0xffffffffu, r.lo, 0), __shfl_sync(0xffffffffu, r.hi, 0), __shfl_sync(0xffffffffu, r.base, 0)};
-      const int parts = parts_of(range, p.a.chunk_chunk);
-      const int t_begin = range.base + part * p.a.chunk_chunk;
-      const int t_end = min(t_begin + p.a.chunk_chunk, range.hi);
+      const int chunk = p.a.chunk_coarser ? chosen_chunk<D>(p) : p.a.chunk_chunk;
+      const int parts = parts_of(range, chunk);
+      const int t_begin = range.base + part * chunk;
+      const int t_end = min(t_begin + chunk, range.hi);
       if (part >= max(parts, 1)) seq = -1;
       if (lane == 1 || lane == 2) {
         const int x = lane - 1, a = max(r.lo, t_begin), b = min(r.hi, t_end);
@@ -259,6 +294,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
         visible(p, first, s.len, &d, &it.all_hi[x]);
       }
       if (lane == 0) {
+        if (p.a.chunk_coarser) *p.coarser = chunk;
         it.s = s;
         it.kv = kv;
         it.part = part;

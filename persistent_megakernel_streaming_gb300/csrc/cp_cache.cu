@@ -641,6 +641,7 @@ int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, v
   const size_t units = (size_t)b.rows * p.q_heads * kept_parts(p.a);
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + units * c->d.head_dim;
+  p.coarser = reinterpret_cast<int*>(p.part_lse + units);
   return cuda_err(launch_attend(p, c->maps, c->d.head_dim, c->d.dtype == CP_CACHE_E4M3, reinterpret_cast<cudaStream_t>(stream)));
 }
 

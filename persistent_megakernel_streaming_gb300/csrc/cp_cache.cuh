@@ -112,6 +112,7 @@ __device__ __forceinline__ float ex2(float x) {
 // rows) whose visible positions are more than `chunk` is cut into parts of
 // that many, each a block's; a last kernel joins the parts.
 constexpr int kStepRows = 16;
+constexpr int kSms = 152;
 
 constexpr int kPairRows = 256;    // rows (times query heads) that a chunk block takes
 constexpr int kStepAlign = 16, kChunkAlign = 128;   // where an item's parts may start
@@ -123,7 +124,14 @@ struct AttendPlan {
   int step_cluster;               // the parts of a step item are one cluster's blocks, which join them
   int chunk_chunk, chunk_parts;
   int chunk_cluster;              // the same of a chunk item's
+  int chunk_span;                 // positions that the parts were made for
+  int chunk_coarser;              // the kernel looks at the lengths and may take fewer, longer parts
 };
+// Nanoseconds of a chunk call: a tile of 128 positions 1700 (heads of 64: 1200), a block's start and end 9000.
+constexpr int kTileNs128 = 1700, kTileNs64 = 1200, kBlockNs = 9000;
+__host__ __device__ __forceinline__ float chunk_rounds_ns(int64_t blocks, int tiles, int head_dim) {
+  return (float)((blocks + kSms - 1) / kSms) * (float)(tiles * (head_dim == 128 ? kTileNs128 : kTileNs64) + kBlockNs);
+}
 AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, bool causal,
                        int window);
 // Most parts of an item that go through the workspace.
@@ -146,6 +154,7 @@ struct AttendParams {
   uint16_t* out;
   float* part_o;                          // [parts][rows][q_heads][D]: a part's softmax average of v
   float* part_lse;                        // [parts][rows][q_heads]: log2 of its sum of exponentials
+  int* coarser;                           // the chunk kernel's own choice of positions a part
   int64_t q_row, q_head, o_row, o_head;   // element strides
   int group;                              // query heads per kv head
   uint32_t magic;                         // x / group is x * magic >> 16, for x below 320

@@ -286,6 +286,16 @@ def test_attend_long(e4m3, d, new):
     w.check(q, out, window=9000)
 
 
+@pytest.mark.parametrize("e4m3,d", [(False, 64), (True, 128)])
+@pytest.mark.parametrize("lengths,new", [([6000, 1500], [17, 17]), ([6000, 5900], [17, 17]), ([6000, 700, 40], [18, 17, 1]),
+                                         ([6000, 300, 6000], [0, 20, 0])])
+def test_attend_chunks_of_uneven_lengths(e4m3, d, lengths, new):
+    """80 items or so in the plan's parts, and in fewer and longer ones where the lengths leave few blocks."""
+    w = World(lengths, new, 40, d, 32, e4m3, seed=11, pad=1).fill()
+    q, out = w.attend(40)
+    w.check(q, out)
+
+
 @pytest.mark.parametrize("e4m3,d", FORMATS)
 @pytest.mark.parametrize("window", [0, 90])
 def test_attend_many_ragged_steps(e4m3, d, window):
