@@ -23,9 +23,9 @@ struct cp_cache {
 
 namespace {
 
-constexpr int kAppendThreads = 256;
-constexpr int kReadThreads = 256;
-constexpr int kMaxRowsPerBlock = 8;    // one warp finds one row's sequence
+constexpr int kAppendThreads = 128;
+constexpr int kReadThreads = 128;
+constexpr int kMaxRowsPerBlock = 4;    // one warp finds one row's sequence
 
 // ------------------------------------------------------------------ rows
 // Where a row goes: its sequence's table entry resolved to byte offsets.
@@ -108,11 +108,12 @@ struct AppendParams {
 // One read of qkv, one write of q and of the pages; arithmetic in pairs of fp32
 // (an element that lies within that arithmetic's error, some 2^-22, of the
 // middle between two e4m3 steps may take the other one: 4 in a million do).
-// Measured: 8191 rows of 16/8 heads of 128 into bf16 pages 31 us, 4.4 TB/s
-// (65 % of the copy rate: at 1.7 rounds of blocks the last round is short of
-// loads; half or twice the rows a block, 2 or 8 loads in flight and more
-// resident blocks at fewer registers each measured 3 to 25 % slower); e4m3
-// pages, 16/16 heads, 9018 rows 47 us.
+// Measured: 8191 rows of 16/8 heads of 128 into bf16 pages 31 us a call, 4.3
+// TB/s (63 % of the copy rate: the last round of blocks is short of loads.
+// Blocks of 256 threads and 8 rows 33 us, of 512 36, of 64 and 2 rows 31; 2 or
+// 8 loads in flight and more resident blocks at fewer registers 1 to 25 %
+// slower; the first loads ahead of the look-up no faster); e4m3 pages, 16/16
+// heads, 9018 rows written and read back 73 us.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8;
@@ -262,7 +263,7 @@ struct ReadParams {
 
 // 16 cached bytes a lane: 8 bf16 copied, or 16 e4m3 widened to fp32, scaled by
 // the power of two and packed (exact: 4 significant bits). Bound by HBM: 12
-// sequences, 96000 rows of 8 heads of 128, e4m3: 96 us, 6.2 TB/s, 91 % of the
+// sequences, 96000 rows of 8 heads of 128, e4m3: 95 us, 6.2 TB/s, 92 % of the
 // copy rate.
 template <int D, bool E4M3>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p) {
@@ -473,7 +474,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
 
 int cuda_err(cudaError_t e) { return e == cudaSuccess ? CP_OK : CP_ERR_CUDA; }
 
-// Rows per block, a power of two: one until every SM has two blocks, then up to eight, which share the look-ups.
+// Rows per block, a power of two: one until every SM has two blocks, then up to four, which share the look-ups.
 int rows_per_block(int rows) {
   int n = 1;
   while (n < kMaxRowsPerBlock && rows >= 304 * 2 * n) n *= 2;
