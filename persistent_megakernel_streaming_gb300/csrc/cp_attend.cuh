@@ -2,7 +2,7 @@
 // next to masked non-finite values, and how a part's result is stored.
 #pragma once
 #include "cp_cache.cuh"
-#include "cp_ptx.cuh"
+#include "cp_cache_ptx.cuh"
 
 namespace cp {
 namespace cache {

@@ -9,7 +9,7 @@
 
 #include "cp.h"
 #include "cp_cache.cuh"
-#include "cp_ptx.cuh"
+#include "cp_cache_ptx.cuh"
 
 using namespace cp;
 using namespace cp::cache;
