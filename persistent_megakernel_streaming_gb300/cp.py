@@ -304,10 +304,16 @@ class Cache:
     what the calls compute."""
 
     def __init__(self, k, v, k_scale=None, v_scale=None, timeout_ns: int = 0, debug_stall: bool = False):
+        import torch
+        self.kinds = (torch.bfloat16, torch.int16)      # other 16-bit types would be read as bf16
         size = k.element_size()
         if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.device != v.device or \
                 k.device.type != "cuda":
             raise ValueError("k and v: [pages][kv_heads][page_size][head_dim] of the same strides, on one GPU")
+        if size == 2 and (k.dtype not in self.kinds or v.dtype not in self.kinds):
+            raise ValueError("k and v: bf16 (or its bits as int16), or e4m3")
+        if size == 1 and (k.dtype not in (torch.uint8, torch.float8_e4m3fn) or v.dtype != k.dtype):
+            raise ValueError("k and v: e4m3 (or its bits as uint8), or bf16")
         if size not in (1, 2) or (size == 1) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
             raise ValueError("bf16 pages without scales, or e4m3 pages with k_scale and v_scale")
         if k.stride(3) != 1:
@@ -395,8 +401,8 @@ class Cache:
     def _rows(self, batch, t, what, shape):
         """Address of a row array and the strides of its axes but the last (0 where it has one entry at most)."""
         strides = t.stride()
-        if t.shape != shape or t.element_size() != 2 or strides[-1] != 1 and shape[-1] > 1:
-            raise ValueError(f"{what}: 16-bit elements {list(shape)}, the last axis contiguous; got {list(t.shape)}, "
+        if t.shape != shape or t.dtype not in self.kinds or strides[-1] != 1 and shape[-1] > 1:
+            raise ValueError(f"{what}: bf16 (or int16) {list(shape)}, the last axis contiguous; got {list(t.shape)}, "
                              f"strides {strides}, {t.dtype}")
         if t.get_device() != self.device_index or batch.device_index != self.device_index:
             raise ValueError(f"{what}, or the batch: on another device than the cache's")
@@ -409,7 +415,7 @@ class Cache:
     def _gain(self, t):
         if t is None:
             return 0
-        if t.shape != (self.head_dim,) or t.element_size() != 2 or t.stride(0) != 1 or t.get_device() != self.device_index:
+        if t.shape != (self.head_dim,) or t.dtype not in self.kinds or t.stride(0) != 1 or t.get_device() != self.device_index:
             raise ValueError("q_norm, k_norm: bf16 [head_dim] on the cache's device")
         return t.data_ptr()
 

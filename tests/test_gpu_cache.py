@@ -721,6 +721,23 @@ def test_binding_refuses_wrong_rows_and_devices():
         w.cache.append(w.batch, torch.zeros((4, 5 * 64), dtype=torch.bfloat16, device="cuda"), q[:, :2])
 
 
+def test_binding_refuses_other_types_of_the_same_size():
+    w = World([20], [3], 1, 64).fill()
+    q = torch.zeros((3, 2, 64), dtype=torch.float16, device="cuda")
+    out, qkv = torch.zeros_like(q, dtype=torch.bfloat16), torch.zeros((3, 4 * 64), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: w.cache.attend(w.batch, q, out), lambda: w.cache.attend(w.batch, out, q),
+                 lambda: w.cache.append(w.batch, qkv.half(), out), lambda: w.cache.append(w.batch, qkv, q),
+                 lambda: w.cache.append(w.batch, qkv, out, q_norm=q[0, 0]), lambda: w.cache.read(w.batch, q[:, :1]),
+                 lambda: cp.Cache(w.k.view(torch.float16), w.v.view(torch.float16)),
+                 lambda: cp.Cache(w.k.view(torch.uint8), w.v.view(torch.uint8).view(torch.float8_e5m2),
+                                  torch.zeros(w.k.shape[:3], dtype=torch.uint8, device="cuda"),
+                                  torch.zeros(w.k.shape[:3], dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
+    w.cache.attend(w.batch, out.view(torch.int16), out)
+    assert w.cache.status() == 0
+
+
 @pytest.mark.parametrize("e4m3,d", FORMATS)
 def test_a_wait_that_runs_out_is_reported(e4m3, d):
     """The first load of every block is left out: the waits for it end, the call returns, the status says so, and the
