@@ -659,6 +659,32 @@ def test_captured_step_follows_lengths_tables_and_rows():
     assert cache.status() == 0
 
 
+@pytest.mark.parametrize("e4m3,d", [(False, 64), (True, 128)])
+def test_captured_chunks_and_steps_follow_the_lengths(e4m3, d):
+    """A call of every kernel, read by the next one in the graph, replayed at lengths that are cut up differently."""
+    w = World([6000, 5900, 700], [17, 17, 1], 40, d, 32, e4m3, seed=12).fill()
+    q = bf16(w.g.standard_normal((w.rows, 40, d))).cuda()
+    outs = [torch.zeros((w.rows, 40, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    w.cache.attend(w.batch, q, outs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        w.cache.attend(w.batch, q, outs[0])
+        outs[1].copy_(outs[0])
+    for lengths in ([6000, 1500, 700], [6000, 5900, 1], [40, 30, 700], [900, 5900, 20], [6000, 5900, 700]):
+        w.batch.length.copy_(torch.tensor(lengths, dtype=torch.int32))
+        for x in outs:
+            x.zero_()
+        graph.replay()
+        got = outs[1].clone()
+        w.lengths, kv = lengths, w.kv
+        w.kv = [(k[:L], v[:L]) for (k, v), L in zip(kv, lengths)]
+        w.check(q, got)
+        w.kv = kv
+        outs[0].zero_()
+        w.cache.attend(w.batch, q, outs[0])
+        assert torch.equal(outs[0], got)
+
+
 def test_two_captured_graphs_and_eager_calls_at_once():
     """Each call's workspace is its own: two graphs replayed together on two streams, with eager calls between."""
     w = World([6000, 4000], [1, 40], 2, 64, 32, False, seed=2).fill()
