@@ -512,6 +512,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     split_pair(sum[0], y, y + 1);
     split_pair(sum[1], y + 2, y + 3);
     l = (y[0] + y[1]) + (y[2] + y[3]);
+    // the row's other thread may still be to read this slot: the last move's maximum, or, without a tile, q's scale
+    pair_or(pair_id, false);
     sh.row[half][slot] = l;                // met after the block's barrier
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- helpers
