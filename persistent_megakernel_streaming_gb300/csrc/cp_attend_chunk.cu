@@ -657,10 +657,10 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       const int j = n >> 1, is_v = n & 1;
       if (n >= NR && !(E4M3 ? wait_warp(sh, saddr(&sh.raw_empty[n % NR]), ((n / NR) & 1) ^ 1) : wait_done(sh, n - NR))) break;
       const uint32_t bar = saddr(&sh.raw_full[n % NR]);
-      asked = n + 1;
-      if (n == 0 && p.stall) continue;
       // q goes first: when all blocks start at once, a ring's worth of K and V in front of it is 2 us
       if (n == 1 && !wait_warp(sh, saddr(&sh.q_full), 0)) break;
+      asked = n + 1;                       // behind the last wait: what is counted here is on its way
+      if (n == 0 && p.stall) continue;
       if (lane == 0) mb_expect(bar, E4M3 ? C::kRawBytes : C::kOpBytes);
       __syncwarp();
       if (lane < boxes) {

@@ -1,6 +1,8 @@
 """The paged cache at the ends of its ranges: few tiles, zeros, rows and scales of wide range, bounds far above what a call
 holds. The world, the reference and the derivation of the tolerances are test_gpu_cache's; the comparison here takes
 NaN for wrong."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -36,3 +38,24 @@ def test_streams_of_one_tile(e4m3, d, L, n):
         again = torch.full_like(out, 7.0)
         w.cache.attend(w.batch, q, again)
         assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+def test_a_timeout_that_any_wait_may_meet(e4m3, d):
+    """Whichever wait gives up first, a block only waits for what it has asked for and the call ends."""
+    w = World([4000, 900, 300], [300, 200, 9], 2, d, 32, e4m3, seed=24).fill()
+    q, good = w.attend(4)
+    torch.cuda.synchronize()
+    hasty = cp.Cache(w.k, w.v, w.ks, w.vs, timeout_ns=1)
+    out, q = torch.full_like(good, 7.0), q.cuda()
+    for _ in range(20):
+        t0 = time.monotonic()
+        hasty.attend(w.batch, q, out)
+        status = hasty.status()
+        assert status in (cp.CP_OK, cp.CP_ERR_TIMEOUT) and time.monotonic() - t0 < 1.0
+        if status == cp.CP_OK:
+            assert torch.equal(out, good)
+        hasty.clear_status()
+    again = torch.full_like(good, 7.0)
+    w.cache.attend(w.batch, q, again)
+    assert torch.equal(again, good) and w.cache.status() == cp.CP_OK
