@@ -40,6 +40,7 @@
 // 150 us, 919 TFLOP/s, of which each block's start and end are 9 us. A second
 // issuing warp hides the gaps alone, but pulls the two softmaxes into step:
 // 186 us, with turns between the two 149.
+#include <cfloat>
 #include <type_traits>
 
 #include "cp_attend.cuh"
@@ -396,7 +397,9 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       tm_fence_after();
       const int vn = E4M3 ? sh.vref[j % kScaleSlots] : 0;
       const bool edge = t0 < see_lo || t0 + kTile > see_hi;
-      const float rs = E4M3 ? row_scale * pow2i(max(sh.kref[j % kScaleSlots] - kUp, -126)) : row_scale;
+      // never zero, which would make NaN of masked scores: a row of zeros over keys of zeros has 2^-219. At the least
+      // normal float the others stay below 2^-100
+      const float rs = E4M3 ? fmaxf(row_scale * pow2i(max(sh.kref[j % kScaleSlots] - kUp, -126)), FLT_MIN) : row_scale;
       // masked scores are minus infinity
       auto ready = [&](uint32_t* x, int c) {
         if (edge) {

@@ -59,3 +59,38 @@ def test_a_timeout_that_any_wait_may_meet(e4m3, d):
     again = torch.full_like(good, 7.0)
     w.cache.attend(w.batch, q, again)
     assert torch.equal(again, good) and w.cache.status() == cp.CP_OK
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 33), (False, 100)])
+@pytest.mark.parametrize("lengths,new", [([40, 300], [40, 300]), ([1000, 77], [40, 9]), ([130, 3], [1, 2]),
+                                         ([10, 600], [60, 300]), ([9000], [40])])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -40])
+def test_zero_queries_over_zero_keys(e4m3, d, causal, window, lengths, new, size):
+    """...give the mean of the visible values: a tile whose last positions are masked, rows that see nothing, one part
+    and several."""
+    w = World(lengths, new, 2, d, 32, e4m3, seed=22, pad=1).fill()
+    w.kv = [(k * 0, v) for k, v in w.kv]
+    pool, scale = w.k.cpu().clone(), None if w.ks is None else w.ks.cpu().clone()
+    for i, L in enumerate(lengths):
+        t = np.arange(L)
+        pool[w.table[i, t // 32], :, t % 32] = 0
+        if e4m3:
+            scale[w.table[i, t // 32], :, t % 32] = 17          # 2^-110, as rows of zeros are appended
+    w.put([pool, w.v.cpu()], [scale, None if w.vs is None else w.vs.cpu()])
+    q, out = w.attend(4, causal=causal, window=window, q=bf16(np.full((w.rows, 4, d), size)))
+    w.check(q, out, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+def test_a_batch_of_zeros_through_append_and_attend(e4m3, d):
+    """What a warm-up does: zeros through the norm, the rotation and the cache."""
+    w = World([60, 200], [60, 33], 2, d, 16, e4m3, seed=25).fill()
+    gain, zeros = torch.ones(d, dtype=torch.bfloat16, device="cuda"), torch.zeros((w.rows, 8 * d), dtype=torch.bfloat16, device="cuda")
+    q = torch.full((w.rows, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    w.cache.append(w.batch, zeros, q, gain, gain, rope_base=1e4)
+    for i, (L, n) in enumerate(zip(w.lengths, w.new)):
+        for x in w.kv[i]:
+            x[L - n:] = 0
+    q, out = w.attend(4, q=q)
+    w.check(q, out)
