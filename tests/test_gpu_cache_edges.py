@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import test_gpu_cache as base
+from oracle import cache as ref
 from persistent_megakernel_streaming_gb300 import build, cp
 from test_gpu_cache import FORMATS, bf16
 
@@ -94,3 +95,91 @@ def test_a_batch_of_zeros_through_append_and_attend(e4m3, d):
             x[L - n:] = 0
     q, out = w.attend(4, q=q)
     w.check(q, out)
+
+
+# test_gpu_cache's own cases, whose comparison lets NaN pass, with this one
+@pytest.fixture
+def strict(monkeypatch):
+    monkeypatch.setattr(base, "World", World)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("shape", range(len(base.SHAPES)))
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 33), (False, 100), (True, 1)])
+def test_attend_is_finite(strict, e4m3, d, shape, causal, window):
+    base.test_attend(e4m3, d, shape, causal, window)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+def test_long_ragged_and_sharp_are_finite(strict, e4m3, d):
+    for new in ([1], [40]):
+        base.test_attend_long(e4m3, d, new)
+    for window in (0, 90):
+        base.test_attend_many_ragged_steps(e4m3, d, window)
+    for new in ([1, 2], [70, 9]):
+        base.test_attend_sharp_and_scaled(e4m3, d, new)
+    base.test_attend_many_steps_ignore_what_is_masked(e4m3, d)
+    base.test_a_window_as_large_as_its_type(e4m3, d)
+    base.test_attend_strided_rows_and_repeatable(e4m3, d)
+
+
+@pytest.mark.parametrize("e4m3,d", [(False, 64), (True, 128)])
+def test_uneven_captured_and_loose_are_finite(strict, e4m3, d):
+    for lengths, new in (([6000, 1500], [17, 17]), ([6000, 5900], [17, 17]), ([6000, 700, 40], [18, 17, 1]),
+                         ([6000, 300, 6000], [0, 20, 0])):
+        base.test_attend_chunks_of_uneven_lengths(e4m3, d, lengths, new)
+    base.test_captured_chunks_and_steps_follow_the_lengths(e4m3, d)
+    if e4m3:
+        for n in ([2], [50]):
+            base.test_attend_zeros_between_values(d, n)
+    else:
+        base.test_loose_bounds_change_nothing_but_rounding()
+        base.test_batches_of_many_sequences()
+
+
+# ------------------------------------------------------------ the lower end of a window, rows apart
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("L,n,window", [(200, 2, 20), (200, 5, 20), (900, 3, 300), (200, 50, 20), (40, 2, 16), (1500, 2, 1)])
+def test_rows_ignore_what_left_their_window(e4m3, d, L, n, window):
+    """NaN and infinity in K and V of the first position that the first row sees: the others are as if it were not there."""
+    w = World([L], [n], 1, d, 16, e4m3, seed=3).fill()
+    bad = L - n - window + 1
+    pool = [w.k.cpu().clone(), w.v.cpu().clone()]
+    for x in pool:
+        x[w.table[0, bad // 16], 0, bad % 16, 3] = 255 if e4m3 else 0x7f80
+        x[w.table[0, bad // 16], 0, bad % 16, 5] = 255 if e4m3 else -1
+    w.put(pool, [None if s is None else s.cpu() for s in (w.ks, w.vs)])
+    q, out = w.attend(2, window=window)
+    assert torch.isnan(out[0, :, 5]).all()
+    k, v = w.kv[0]
+    got = out.double().cpu().numpy()[1:]
+    y, size, reach = ref.attend(q.double().numpy()[1:], k, v, L - n + 1, d ** -0.5, True, window)
+    rel = 2 * (d + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + (2.0 ** -11 if e4m3 else 2.0 ** -8) + L * 2.0 ** -24
+    tol = np.abs(y) * 2.0 ** -8 + size * rel * 1.01 + (2.0 ** -25 * L * np.abs(v).max() if e4m3 else 0)
+    assert len(got) == n - 1 and (np.abs(got - y) <= tol).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [2, 4])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+@pytest.mark.parametrize("gap,shift", [(10, 0), (20, 0), (40, 0), (100, 0), (115, -90)])
+def test_a_far_scale_that_left_the_window(d, n, which, gap, shift):
+    """As test_gpu_cache's test_attend_rows_that_do_not_see_a_far_scale, with its bound, for the first position that the
+    first of a few rows sees."""
+    L, window = 200, 20
+    w = World([L], [n], 1, d, 16, True, seed=3).fill()
+    far = L - n - window + 1
+    scales = [w.ks.cpu().int(), w.vs.cpu().int()]
+    k, v = (x * 2.0 ** shift for x in w.kv[0])
+    t = np.arange(L)
+    for i in range(2):
+        scales[i][w.table[0, t // 16], :, t % 16] += shift
+        if "kv"[i] in which:
+            scales[i][w.table[0, far // 16], :, far % 16] += gap
+    w.put([w.k.cpu(), w.v.cpu()], scales)
+    q, out = w.attend(2, window=window)
+    got = out.double().cpu().numpy()[1:]
+    y, size, reach = ref.attend(q.double().numpy()[1:], k, v, L - n + 1, d ** -0.5, True, window)
+    rel = 2 * (d + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + 2.0 ** -11 + window * 2.0 ** -24
+    tol = np.abs(y) * 2.0 ** -8 + size * rel * 1.01 + 2.0 ** (min(gap, 12) - 25) * window * np.abs(v[far + 1:]).max()
+    assert len(got) == n - 1 and (np.abs(got - y) <= tol).all() and w.cache.status() == 0
