@@ -474,7 +474,11 @@ int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, 
  * position holds does not matter, infinities and NaN included. Scores,
  * softmax statistics and sums are fp32; the weights are rounded to bfloat16
  * (fp16 over an e4m3 cache) for the product with v, and the result once to
- * bfloat16. Results are bit-identical run to run. out may be q itself, with
+ * bfloat16. Over an e4m3 cache q enters its product in fp16, times a power of
+ * two a row: elements 2^-17 or more of the row's largest keep all their bits,
+ * and where the others could move a score by more than 2^-12 (a weight by
+ * 2^-12 of itself) the rows concerned are computed from q as it is, more
+ * slowly. Results are bit-identical run to run. out may be q itself, with
  * the same strides, and does not overlap it otherwise. `workspace`: device memory
  * of at least cp_cache_check's workspace_bytes, 16-byte aligned, nothing kept
  * in it between calls; calls that may overlap, captured ones included, need

@@ -275,6 +275,7 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
   uint32_t qf[KS][NT][2];
   float qs[NT][2];
   int lo[NT][2], hi[NT][2];
+  float lost = 0.f;                 // the most that a row's fp16 left of q out, times its scale (kMostLost)
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int r = n * 8 + g;
@@ -303,13 +304,23 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = min(max(top - 127, -100), 100);
+      const int e = min(max(top - 127, -126), 126);
       const float inv = pow2i(-e);
+      bool small = false;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         qf[k][n][0] = hf_pack(bf_lo(raw[k].x) * inv, bf_hi(raw[k].x) * inv);
         qf[k][n][1] = hf_pack(bf_lo(raw[k].y) * inv, bf_hi(raw[k].y) * inv);
+        small |= any_small<2>(qf[k][n]);
       }
+      float out = 0.f;
+      if (__any_sync(0xffffffffu, small && on)) {
+#pragma unroll
+        for (int k = 0; k < KS; ++k) out += left_out(raw[k].x, inv, qf[k][n][0]) + left_out(raw[k].y, inv, qf[k][n][1]);
+        out += __shfl_xor_sync(0xffffffffu, out, 1);
+        out += __shfl_xor_sync(0xffffffffu, out, 2);
+      }
+      lost = fmaxf(lost, p.scale_log2 * pow2i(e) * fmaxf(out, kLeastLost));
 #pragma unroll
       for (int j = 0; j < 2; ++j) qs[n][j] = p.scale_log2 * pow2i(__shfl_sync(0xffffffffu, e, (2 * c + j) * 4));
     }
@@ -332,7 +343,7 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
   }
-  int ev_ref = -1000;
+  int ev_ref = -1000, ek_top = -126;
   bool bad = false;
 
 #pragma unroll
@@ -350,6 +361,7 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         ek[x] = (int)ks_cur[x] - 127;
+        ek_top = max(ek_top, ek[x]);
         ev[x] = (int)vs_cur[x] - 127;
         ks_cur[x] = ks_next[x];
         vs_cur[x] = vs_next[x];
@@ -514,6 +526,7 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
     issue(it + kStages - 1);
   }
   cp_wait<0>();
+  if (E4M3 && mine > 0) bad |= lost * (448.f * pow2i(__reduce_max_sync(0xffffffffu, ek_top))) > kMostLost;
   const bool whole = parts <= 1;
   // a cluster's parts: each block's averages and log-sums, where the others read them
   float* avg = reinterpret_cast<float*>(ring) + kAvgAt;

@@ -60,6 +60,28 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t addr) {
 // Whether 16 e4m3 bytes hold an element that is not zero.
 __device__ __forceinline__ bool any_nonzero(uint4 x) { return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0; }
 
+// Over an e4m3 cache q enters the products in fp16, each row under a power of two that puts its largest element into
+// [1, 4). Elements below 2^-14 lose bits there. What a row has lost, times the scale of its scores and the largest key
+// that it may meet (448 times the largest scale), bounds the error of a score (in powers of two); a block where that
+// passes kMostLost computes its rows the plain way, from q as it is. kLeastLost stands in for a row that lost nothing, so
+// that the same bound finds scores whose scale comes near the end of fp32.
+constexpr float kMostLost = 0x1p-12f, kLeastLost = 0x1p-121f;
+
+// Whether fp16 pairs hold an element below fp16's normal range.
+template <int N>
+__device__ __forceinline__ bool any_small(const uint32_t* y) {
+  __half2 m = __habs2(*reinterpret_cast<const __half2*>(y));
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = __hmin2(m, __habs2(*reinterpret_cast<const __half2*>(y + i)));
+  const uint32_t x = *reinterpret_cast<const uint32_t*>(&m);
+  return !(x & 0x7c00u) || !(x & 0x7c000000u);
+}
+// What the fp16 pair y keeps not of the bf16 pair w times f (nothing of infinities and NaN).
+__device__ __forceinline__ float left_out(uint32_t w, float f, uint32_t y) {
+  const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&y));
+  return fmaxf(fabsf(bf_lo(w) * f - h.x), 0.f) + fmaxf(fabsf(bf_hi(w) * f - h.y), 0.f);
+}
+
 // Most powers of two by which the reference of an e4m3 cache's value scales may rise: fp32 outputs follow it with
 // their precision. Past it the rows that do not see the new value could lose theirs.
 constexpr int kMostRise = 110;

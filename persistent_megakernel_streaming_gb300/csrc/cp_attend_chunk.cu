@@ -92,6 +92,7 @@ struct ChunkShared {
   long long timeout_ns;
   int abort;       // a wait gave up
   int bad;         // a value that some row must not see is not finite
+  int lost;        // e4m3: bits of the largest product of a row's scale and what fp16 left of its q out (kMostLost)
   int kref[kScaleSlots], vref[kScaleSlots];    // e4m3: exponents taken out of a tile's keys and values
   Item item;
   float row[2][kPairRows];     // what the two threads of a row tell each other; before that, [0]: e4m3's powers of
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
     if (lane == 2) mb_init(saddr(&sh.q_full), kSoftWarps);
     if (lane == 3) mb_init(saddr(&sh.o_full), 1);
     if (lane == 4) {
-      sh.abort = sh.bad = 0;
+      sh.abort = sh.bad = sh.lost = 0;
       sh.timeout_ns = p.timeout_ns;
     }
     mb_fence_init();
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       const int u = lane % UPR, base = (warp & 3) * 32 + half * 16 + lane / UPR;
       const uint16_t* src = p.q + (int64_t)it.s.row0 * p.q_row + (int64_t)(it.kv * p.group) * p.q_head + u * 8;
       uint4 x[N];
+      float lost = 0.f;
 #pragma unroll
       for (int k = 0; k < N; ++k) {
         const int r = i * kTile + base + k * RPI, n = new_row(r);
@@ -366,20 +368,33 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
           for (int q = 0; q < 4; ++q) top = max(top, max(finite_exp(w[q] & 0xffffu), finite_exp(w[q] >> 16)));
 #pragma unroll
           for (int o = UPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = min(max(top - 127, -100), 100);
+          const int e = min(max(top - 127, -126), 126);
           const float inv = pow2i(-e);
           uint32_t y[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) y[q] = hf_pack(bf_lo(w[q]) * inv, bf_hi(w[q]) * inv);
           x[k] = make_uint4(y[0], y[1], y[2], y[3]);
-          if (u == 0) sh.row[0][i * kTile + base + k * RPI] = p.scale_log2 * pow2i(e);
+          const float scale = p.scale_log2 * pow2i(e);
+          if (u == 0) sh.row[0][i * kTile + base + k * RPI] = scale;
+          float out = 0.f;
+          if (__any_sync(0xffffffffu, any_small<4>(y))) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) out += left_out(w[q], inv, y[q]);
+#pragma unroll
+            for (int o = UPR / 2; o; o >>= 1) out += __shfl_xor_sync(0xffffffffu, out, o);
+          }
+          lost = fmaxf(lost, scale * fmaxf(out, kLeastLost));
         }
         st_shared_v4u(q_s + i * C::kOpBytes + op_at(base + k * RPI, u), x[k]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mb_arrive(saddr(&sh.q_full));
-      if (E4M3) pair_or(pair_id, false);
+      if (E4M3) {
+        const int most = __reduce_max_sync(0xffffffffu, __float_as_int(lost));    // not negative: ordered as integers
+        if (lane == 0) atomicMax(&sh.lost, most);
+        pair_or(pair_id, false);
+      }
     }
     const float row_scale = E4M3 ? sh.row[0][slot] : p.scale_log2;
     const int pos = slot < rows_here ? it.s.first + new_row(slot) : -1;
@@ -755,12 +770,15 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
   tm_fence_after();
 
   const bool failed = sh.abort != 0;
+  // rows of q that fp16 could not hold, next to the largest keys that the block met
+  const bool far_q = E4M3 && !failed && it.ntiles > 0 &&
+                     __int_as_float(sh.lost) * (448.f * pow2i(max(sh.kref[(it.ntiles - 1) % kScaleSlots], -126))) > kMostLost;
   if (failed && threadIdx.x == 0) set_status(p.c.status, CP_ERR_TIMEOUT);
   constexpr int kPitch = D + 4;
   static_assert(kPairRows * kPitch * 4 <= (2 + NO) * C::kOpBytes, "the rows fit the operands' memory");
   float* averages = reinterpret_cast<float*>(ops);
   const bool cluster = p.a.chunk_cluster && !it.whole;       // the item's parts are a cluster's blocks
-  if (!failed && sh.bad) {
+  if (!failed && (sh.bad || far_q)) {
     plain_rows<D, E4M3>(p, it.s, it.seq, it.kv, it.row0, it.row0 + it.rows_here, it.t_begin, it.t_end, it.part, it.whole, warp,
                         C::kThreads / 32, cluster ? averages : nullptr, sh.row[0], kPitch);
   } else if (!failed && warp < kSoftWarps) {

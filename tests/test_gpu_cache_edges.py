@@ -183,3 +183,67 @@ def test_a_far_scale_that_left_the_window(d, n, which, gap, shift):
     rel = 2 * (d + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + 2.0 ** -11 + window * 2.0 ** -24
     tol = np.abs(y) * 2.0 ** -8 + size * rel * 1.01 + 2.0 ** (min(gap, 12) - 25) * window * np.abs(v[far + 1:]).max()
     assert len(got) == n - 1 and (np.abs(got - y) <= tol).all() and w.cache.status() == 0
+
+
+# ------------------------------------------------------------ queries of wide range
+def channels(w, up):
+    """World of one sequence, whose keys' channel c is 2^up[c] times what it would be (as the cache holds it)."""
+    inner, calls = w.g.standard_normal, []
+
+    class Wide:
+        def standard_normal(self, shp):
+            calls.append(1)
+            x = inner(shp)
+            return x * np.exp2(up) if len(calls) == 1 else x * 0 if len(calls) == 2 else x
+
+    w.g = Wide()
+    return w.fill()
+
+
+def compare(w, q, out, window=0):
+    """test_gpu_cache's bound, and the 2^-12 that a score over e4m3 may be off for its q in fp16: twice (the weight and
+    the sum) ln 2 times that, below 2^-11."""
+    (k, v), (L,), (n,) = w.kv[0], w.lengths, w.new
+    y, size, reach = ref.attend(q.double().cpu().numpy(), k, v, L - n, w.d ** -0.5, True, window)
+    rel = 2 * (w.d + 8) * 2.0 ** -24 * reach[..., None] + 2.0 ** -21 + (2.0 ** -10 if w.e4m3 else 2.0 ** -8) + L * 2.0 ** -24
+    tol = np.abs(y) * 2.0 ** -8 + size * rel * 1.01 + (2.0 ** -25 * L * np.abs(v).max() if w.e4m3 else 0)
+    bad = ~(np.abs(out.double().cpu().numpy() - y) <= tol)
+    assert not bad.any() and w.cache.status() == 0, np.argwhere(bad)[:4]
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("L,n", [(300, 2), (300, 40), (6000, 1), (6000, 50), (700, 700)])
+@pytest.mark.parametrize("width", [8, 12, 16, 18, 24, 40])
+def test_queries_of_wide_range(e4m3, d, L, n, width):
+    """Channels whose keys are up to 2^width larger and whose queries are as much smaller: each counts alike in a score."""
+    up = np.linspace(0, width, d)
+    w = channels(World([L], [n], 2, d, 32, e4m3, seed=26), up)
+    q, out = w.attend(4, q=bf16(w.g.standard_normal((n, 4, d)) * np.exp2(-up)))
+    compare(w, q, out)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("shift", [-110, -60, 60, 100])
+def test_queries_of_any_size(e4m3, d, n, shift):
+    """All of q 2^shift times as large, and the keys as much smaller (but for what the least scale leaves of them)."""
+    w = channels(World([300], [n], 2, d, 32, e4m3, seed=27), np.full(d, -float(shift)))
+    q, out = w.attend(4, q=bf16(w.g.standard_normal((n, 4, d)) * 2.0 ** shift))
+    compare(w, q, out)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("n", [1, 2, 40])
+@pytest.mark.parametrize("top", [0, 19, 120])
+def test_a_channel_of_q_that_no_key_has(e4m3, d, n, top):
+    """One element of q far above the others meets keys of zero there: the score is the others'."""
+    up = np.full(d, 20.0 if top < 100 else 0.0)
+    w = channels(World([300], [n], 2, d, 32, e4m3, seed=28), up)
+    w.kv[0][0][..., 5] = 0
+    t, pool = np.arange(300), w.k.cpu().clone()
+    pool[w.table[0, t // 32], :, t % 32, 5] = 0
+    w.put([pool, w.v.cpu()], [None if s is None else s.cpu() for s in (w.ks, w.vs)])
+    q = w.g.standard_normal((n, 4, d)) * np.exp2(-up)
+    q[..., 5] = 2.0 ** top
+    q, out = w.attend(4, q=bf16(q))
+    compare(w, q, out)
