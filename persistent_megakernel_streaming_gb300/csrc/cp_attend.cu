@@ -206,14 +206,14 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
   const int parts = parts_of(range, p.a.step_chunk);
   if (part >= max(parts, 1)) return;
   const int t_begin = range.base + part * p.a.step_chunk;
-  const int t_end = min(t_begin + p.a.step_chunk, range.hi);
+  const int t_end = t_begin + min(p.a.step_chunk, range.hi - t_begin);    // positions end near those of 32 bits
   // every row sees [lo_all, hi_all) of the item; outside it a tile is masked by row
   int lo_all, hi_all, unused;
   visible(p, s.first + s.n - 1, s.len, &lo_all, &unused);
   visible(p, s.first, s.len, &unused, &hi_all);
 
   const int32_t* table = p.b.table + (int64_t)seq * p.b.table_stride;
-  for (int i = threadIdx.x; t_begin + i * 16 < t_end; i += kStepWarps * 32) {
+  for (int i = threadIdx.x; i * 16 < t_end - t_begin; i += kStepWarps * 32) {
     const int pg = page_of(table, p.b.width, p.c.pages, p.c.page_shift, t_begin + i * 16);
     if (pg < 0) set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
     sh.pages[i] = pg;

@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
       const Range range = {__shfl_sync(0xffffffffu, r.lo, 0), __shfl_sync(0xffffffffu, r.hi, 0), __shfl_sync(0xffffffffu, r.base, 0)};
       const int chunk = p.a.chunk_coarser ? chosen_chunk<D>(p) : p.a.chunk_chunk;
       const int parts = parts_of(range, chunk);
-      const int t_begin = range.base + part * chunk;
-      const int t_end = min(t_begin + chunk, range.hi);
+      const int t_begin = range.base + (part < parts ? part * chunk : 0);
+      const int t_end = t_begin + min(chunk, range.hi - t_begin);
       if (part >= max(parts, 1)) seq = -1;
       if (lane == 1 || lane == 2) {
         const int x = lane - 1, a = max(r.lo, t_begin), b = min(r.hi, t_end);

@@ -130,7 +130,7 @@ struct AttendPlan {
 // Nanoseconds of a chunk call: a tile of 128 positions 1700 (heads of 64: 1200), a block's start and end 9000.
 constexpr int kTileNs128 = 1700, kTileNs64 = 1200, kBlockNs = 9000;
 __host__ __device__ __forceinline__ float chunk_rounds_ns(int64_t blocks, int tiles, int head_dim) {
-  return (float)((blocks + kSms - 1) / kSms) * (float)(tiles * (head_dim == 128 ? kTileNs128 : kTileNs64) + kBlockNs);
+  return (float)((blocks + kSms - 1) / kSms) * (float)((int64_t)tiles * (head_dim == 128 ? kTileNs128 : kTileNs64) + kBlockNs);
 }
 AttendPlan plan_attend(const BatchView& b, int kv_heads, int q_heads, int head_dim, bool e4m3, bool causal,
                        int window);
@@ -187,7 +187,7 @@ __device__ __forceinline__ Range item_range(const AttendParams& p, int pos_first
   return r;
 }
 __device__ __forceinline__ int parts_of(const Range& r, int chunk) {
-  return r.hi > r.base ? (r.hi - r.base + chunk - 1) / chunk : 0;
+  return r.hi > r.base ? (r.hi - r.base - 1) / chunk + 1 : 0;     // a part may be nearly as long as positions reach
 }
 
 // Once per device, with it current: the kernels' shared-memory sizes.

@@ -247,3 +247,19 @@ def test_a_channel_of_q_that_no_key_has(e4m3, d, n, top):
     q[..., 5] = 2.0 ** top
     q, out = w.attend(4, q=bf16(q))
     compare(w, q, out)
+
+
+# ------------------------------------------------------------ bounds far above what a call holds
+@pytest.mark.parametrize("e4m3,d", [(False, 64), (True, 128)])
+@pytest.mark.parametrize("lengths,new,group,hkv", [([777], [1], 2, 1), ([1000, 40], [2, 1], 1, 1), ([500], [300], 2, 2),
+                                                   ([2432], [2432], 2, 8)])
+def test_a_table_that_holds_as_many_positions_as_there_are(e4m3, d, lengths, new, group, hkv):
+    """max_len as large as it may be: what a call cuts up is the bound, what it computes the lengths."""
+    w = World(lengths, new, hkv, d, 128, e4m3, seed=29).fill()
+    wide = torch.full((len(lengths), 1 << 24), -7, dtype=torch.int32, device="cuda")
+    wide[:, :w.table.shape[1]] = torch.from_numpy(w.table).cuda()
+    loose = cp.Batch(w.batch.start, w.batch.length, wide, w.rows, max_new=max(new))
+    q, out = w.attend(group * hkv, batch=loose)
+    w.check(q, out)
+    q, out = w.attend(group * hkv, batch=loose, window=200)
+    w.check(q, out, window=200)
