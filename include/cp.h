@@ -352,8 +352,9 @@ enum cp_cache_dtype {
                            byte e + 127. Each element is rounded once, to the
                            nearest, ties to even; a power of two costs a float
                            format no precision, and every element is a
-                           bfloat16 exactly. An infinity or NaN is kept as
-                           NaN */
+                           bfloat16 exactly: one of 1.9375 * 2^127 or more,
+                           whose nearest is 2^128, is kept as 1.875 * 2^127.
+                           An infinity or NaN is kept as NaN */
 };
 
 /* Layout of a cache. Pages are [pages][kv_heads][page_size][head_dim], with

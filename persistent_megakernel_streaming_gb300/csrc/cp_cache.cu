@@ -82,6 +82,9 @@ __device__ __forceinline__ uint32_t e4m3x4(const float* x, float f) {
   return a | (uint32_t)b << 16;
 }
 
+// Bits of 1.9375 * 2^127: from here on the nearest e4m3 step is 2^128, past fp32 and bf16.
+constexpr int kRoundsPast = 0x7f780000;
+
 struct AppendParams {
   CacheView c;
   BatchView b;
@@ -225,15 +228,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           top = max(top, max(__float_as_int(x[i]) & 0x7fffffff, __float_as_int(y[i]) & 0x7fffffff));
-        if (top >= 0x7f800000) {                              // infinities are kept as NaN, and set no scale
+        if (top >= kRoundsPast) {
+          // infinities are kept as NaN, and set no scale; what would round to 2^128 is kept as the step below
           top = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int a = __float_as_int(x[i]) & 0x7fffffff, b = __float_as_int(y[i]) & 0x7fffffff;
-            if (a >= 0x7f800000) x[i] = __int_as_float(0x7fc00000);
-            else top = max(top, a);
-            if (b >= 0x7f800000) y[i] = __int_as_float(0x7fc00000);
-            else top = max(top, b);
+          for (int i = 0; i < 8; ++i) {
+            float& z = i < 4 ? x[i] : y[i - 4];
+            const bool no = (__float_as_int(z) & 0x7fffffff) >= 0x7f800000;
+            z = no ? __int_as_float(0x7fc00000) : fminf(fmaxf(z, -0x1.ep127f), 0x1.ep127f);
+            top = max(top, no ? 0 : __float_as_int(z) & 0x7fffffff);
           }
         }
 #pragma unroll

@@ -263,3 +263,48 @@ def test_a_table_that_holds_as_many_positions_as_there_are(e4m3, d, lengths, new
     w.check(q, out)
     q, out = w.attend(group * hkv, batch=loose, window=200)
     w.check(q, out, window=200)
+
+
+# ------------------------------------------------------------ the largest elements
+LOWEST = -3.3895313892515355e38         # of bf16
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_the_largest_elements_stay_finite_in_e4m3(d):
+    w = World([40], [40], 2, d, 16, True, seed=30)
+    x = w.g.standard_normal((40, 4 * d))
+    x[0], x[1, 3], x[2, d + 5] = LOWEST, -LOWEST, LOWEST
+    x[3, ::2], x[4, ::7], x[5, 2] = 2.0 ** 127 * 1.9375, -(2.0 ** 127) * 1.9296875, 2.0 ** 127 * 1.875
+    x[6, 1], x[6, 2], x[6, 3] = LOWEST, np.inf, np.nan
+    qkv = bf16(x)
+    w.cache.append(w.batch, qkv.cuda())
+    k, v = (torch.empty((40, 2, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w.cache.read(w.batch, k, v)
+    want = qkv.double().numpy().reshape(40, 4, d)
+    most = 2.0 ** 127 * 1.875                                   # the largest step below 2^128
+    byte, e = ref.quantise(np.where(np.isfinite(want), np.clip(want, -most, most), want))
+    want = ref.dequantise(byte, e)
+    np.testing.assert_array_equal(k.double().cpu().numpy(), want[:, :2])
+    np.testing.assert_array_equal(v.double().cpu().numpy(), want[:, 2:])
+    assert not torch.isinf(k).any() and not torch.isinf(v).any() and w.cache.status() == 0
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("n", [1, 40])
+def test_keys_of_the_lowest_value_weigh_nothing(e4m3, d, n):
+    """...to queries above zero: scores below all others, or minus infinity, through append and attend."""
+    L = 100
+    w = World([L], [L], 1, d, 16, e4m3, seed=31)
+    x = w.g.standard_normal((L, 2 * d))
+    low = np.arange(0, 60, 3)
+    x[low, :d] = LOWEST
+    w.cache.append(w.batch, bf16(x).cuda())
+    k, v = (torch.empty((L, 1, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w.cache.read(w.batch, k, v)
+    keep = np.setdiff1d(np.arange(L), low)
+    w.start, w.new, w.rows = np.array([0, n], np.int32), [n], n
+    w.batch = w.batch_of(max_new=n)
+    q, out = w.attend(2, q=bf16(np.abs(w.g.standard_normal((n, 2, d))) + 0.1))
+    k, v = k.double().cpu().numpy()[keep], v.double().cpu().numpy()[keep]
+    w.lengths, w.kv = [len(keep)], [(k, v)]             # the rows are the last positions, none of them low
+    compare(w, q, out)
