@@ -270,6 +270,19 @@ def _stride(t, axis: int) -> int:
     return t.stride(axis)
 
 
+def _int32(x, what: str) -> int:
+    """x as the C side's int; ctypes would keep its low 32 bits and say nothing."""
+    if not -2 ** 31 <= int(x) < 2 ** 31:
+        raise ValueError(f"{what}: {x} is past 32 bits")
+    return int(x)
+
+
+def _not_lost(x: float, what: str):
+    """x is not one that fp32 turns into zero, which the C side takes for "none given"."""
+    if 0 < abs(x) < 2.0 ** -149:
+        raise ValueError(f"{what}: {x} is zero in fp32")
+
+
 class Batch:
     """A ragged batch (cp_batch): row ``start[i] + j`` of the calls' row arrays is sequence i's new row j.
 
@@ -288,11 +301,11 @@ class Batch:
             raise ValueError("start [n + 1], length [n] and pages [n][width]")
         if not start.device == length.device == pages.device:
             raise ValueError("start, length and pages on one device")
-        self.start, self.length, self.pages, self.rows = start, length, pages, int(rows)
+        self.start, self.length, self.pages, self.rows = start, length, pages, _int32(rows, "rows")
         self.device_index = start.get_device()
         self.plans = {}     # attend's workspace sizes by what they depend on
-        self.desc = BatchDesc(length.numel(), int(rows), int(max_new), int(max_len), pages.shape[1],
-                              _stride(pages, 0), _ptr(start), _ptr(length), _ptr(pages))
+        self.desc = BatchDesc(_int32(length.numel(), "sequences"), self.rows, _int32(max_new, "max_new"),
+                              _int32(max_len, "max_len"), _int32(pages.shape[1], "width"), _stride(pages, 0), _ptr(start), _ptr(length), _ptr(pages))
         self.ref = C.byref(self.desc)
 
 
@@ -324,7 +337,7 @@ class Cache:
                 if t.element_size() != 1 or t.shape != k.shape[:3] or t.stride() != k_scale.stride() or t.device != k.device:
                     raise ValueError("scales: uint8 [pages][kv_heads][page_size] of the same strides")
             scale_strides = [_stride(k_scale, i) for i in range(3)]
-        self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.pages, self.kv_heads, self.page_size, self.head_dim = (_int32(n, "k and v") for n in k.shape)
         self.keep = (k, v, k_scale, v_scale)
         self.device, self.device_index = k.device, k.get_device()
         self.layout = (size, self.kv_heads, self.head_dim, self.page_size)
@@ -346,6 +359,7 @@ class Cache:
             q, qs = self._rows(batch, q_out, "q_out", (batch.rows, heads, d))
             if qs[1] not in (0, d):
                 raise ValueError("q_out: contiguous heads")
+        _not_lost(rope_base, "rope_base")
         a = AppendArgs(x, st[0], q, qs[0], heads, self._gain(q_norm), self._gain(k_norm), rms_eps, rope_base)
         code = lib().cp_cache_append(self._h, batch.ref, C.byref(a), self._stream(stream))
         if code:
@@ -371,8 +385,9 @@ class Cache:
         shape = (batch.rows, heads, self.head_dim)
         x, qs = self._rows(batch, q, "q", shape)
         y, os_ = self._rows(batch, out, "out", shape)
-        a = AttendArgs(x, y, qs[0], qs[1], os_[0], os_[1], heads, scale, causal, window)
+        _not_lost(scale, "scale")
         need = self._need(batch, heads, causal, window)
+        a = AttendArgs(x, y, qs[0], qs[1], os_[0], os_[1], heads, scale, causal, window)
         at, size = 0, 0
         if workspace is not None:
             if workspace.get_device() != self.device_index or not workspace.is_contiguous():
@@ -392,6 +407,7 @@ class Cache:
     def _need(self, batch, heads, causal, window):
         key = (self.layout, heads, bool(causal), window)
         if key not in batch.plans:
+            _int32(window, "window")
             a = AttendArgs(16, 32, 0, 0, 0, 0, heads, 0.0, causal, window)
             need = C.c_size_t()
             _check(lib().cp_cache_check(C.byref(self.desc), batch.ref, None, C.byref(a), C.byref(need)), "cp_cache_attend")

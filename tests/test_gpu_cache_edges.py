@@ -308,3 +308,18 @@ def test_keys_of_the_lowest_value_weigh_nothing(e4m3, d, n):
     k, v = k.double().cpu().numpy()[keep], v.double().cpu().numpy()[keep]
     w.lengths, w.kv = [len(keep)], [(k, v)]             # the rows are the last positions, none of them low
     compare(w, q, out)
+
+
+# ------------------------------------------------------------ what the binding refuses
+def test_binding_refuses_what_its_types_would_change():
+    """A window past 32 bits would lose its upper bits, a scale or a base below fp32 would be "none given"."""
+    w = World([40], [2], 1, 64).fill()
+    q, out = w.attend(2)
+    q = q.cuda()
+    qkv = torch.zeros((2, 4 * 64), dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: w.cache.attend(w.batch, q, out, window=2 ** 32 + 7), lambda: w.cache.attend(w.batch, q, out, window=2 ** 31),
+                 lambda: w.cache.workspace_bytes(w.batch, 2, window=2 ** 32), lambda: w.cache.attend(w.batch, q, out, scale=1e-50),
+                 lambda: w.cache.append(w.batch, qkv, out, rope_base=1e-50)):
+        with pytest.raises(ValueError):
+            call()
+    w.check(q, out)
