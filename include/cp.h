@@ -359,7 +359,8 @@ enum cp_cache_dtype {
 
 /* Layout of a cache. Pages are [pages][kv_heads][page_size][head_dim], with
  * the same strides for keys and values; strides count elements, 0 means
- * contiguous. Scales are [pages][kv_heads][page_size] bytes. Limits
+ * contiguous, in any order of the axes as long as no two entries overlap
+ * (CP_ERR_INVALID_ARG). Scales are [pages][kv_heads][page_size] bytes. Limits
  * (CP_ERR_UNSUPPORTED outside): head_dim 64 or 128, page_size 16, 32, 64 or
  * 128, 1 <= kv_heads <= 128, k and v aligned to 16 bytes and the strides
  * multiples of 16 bytes. */
@@ -431,7 +432,7 @@ typedef struct cp_attend {
   const void* q;              /* device bf16 [rows][q_heads][head_dim]       */
   void* out;                  /* device bf16, the same shape                 */
   int64_t q_stride, q_head_stride;      /* elements; 0: contiguous           */
-  int64_t out_stride, out_head_stride;
+  int64_t out_stride, out_head_stride;  /* no two heads' outputs overlap      */
   int q_heads;                /* a multiple of kv_heads, up to 64 times; q
                                  head h reads kv head h / (q_heads/kv_heads) */
   float scale;                /* of the scores, > 0 (0: head_dim^-1/2)       */

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "cp.h"
@@ -318,6 +319,27 @@ struct DeviceGuard {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether the entries of a strided array, `row` elements each, lie apart: from the smallest stride up, each passes
+// all that the ones below it span.
+struct Axis {
+  int64_t n, stride;
+};
+bool lie_apart(int64_t row, std::initializer_list<Axis> axes) {
+  Axis a[3];
+  int m = 0;
+  for (const Axis& x : axes)
+    if (x.n > 1) a[m++] = x;
+  std::sort(a, a + m, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  for (int i = 0; i < m; ++i) {
+    if (a[i].stride < row) return false;
+    if (i + 1 < m) {                                   // row + (n - 1) * stride, which may pass 64 bits, within the next stride
+      if ((a[i + 1].stride - row) / a[i].stride < a[i].n - 1) return false;
+      row += (a[i].n - 1) * a[i].stride;
+    }
+  }
+  return true;
+}
+
 int check_desc(const cp_cache_desc* in, cp_cache_desc* d) {
   if (!in || !in->k || !in->v) return CP_ERR_INVALID_ARG;
   *d = *in;
@@ -344,6 +366,10 @@ int check_desc(const cp_cache_desc* in, cp_cache_desc* d) {
     return CP_ERR_UNSUPPORTED;
   const int64_t most = ((int64_t)1 << 40) / (e4m3 ? 1 : 2);    // what a tensor map's strides reach
   if (d->token_stride >= most || d->head_stride >= most || d->page_stride >= most) return CP_ERR_UNSUPPORTED;
+  if (!lie_apart(d->head_dim, {{d->page_size, d->token_stride}, {d->kv_heads, d->head_stride}, {d->pages, d->page_stride}}))
+    return CP_ERR_INVALID_ARG;
+  if (e4m3 && !lie_apart(1, {{d->page_size, d->scale_token_stride}, {d->kv_heads, d->scale_head_stride}, {d->pages, d->scale_page_stride}}))
+    return CP_ERR_INVALID_ARG;
   return CP_OK;
 }
 
@@ -459,6 +485,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   if (p->q_head < 0 || p->o_head < 0 || p->q_row < 0 || p->o_row < 0) return CP_ERR_INVALID_ARG;
   if (p->q_head % 8 || p->o_head % 8 || p->q_row % 8 || p->o_row % 8 || !aligned16(a->q) || !aligned16(a->out))
     return CP_ERR_UNSUPPORTED;
+  if (!lie_apart(d.head_dim, {{b.rows, p->o_row}, {a->q_heads, p->o_head}})) return CP_ERR_INVALID_ARG;
   p->b = b;
   p->q = static_cast<const uint16_t*>(a->q);
   p->out = static_cast<uint16_t*>(a->out);

@@ -36,3 +36,33 @@ def test_binding_refuses_numbers_past_32_bits(kw):
     with pytest.raises(ValueError):
         cp.Batch(i, i[:2], torch.zeros(2, 4, dtype=torch.int32), **kw)
     assert cp.Batch(i, i[:2], torch.zeros(2, 4, dtype=torch.int32), 5, 2, 64).desc.max_length == 64
+
+
+@pytest.mark.parametrize("kw", [dict(token_stride=64), dict(token_stride=120), dict(head_stride=128), dict(head_stride=63 * 128),
+                                dict(page_stride=7 * 64 * 128), dict(page_stride=8 * 64 * 128 - 8), dict(token_stride=8 * 128),
+                                dict(token_stride=8 * 128, head_stride=120), dict(page_stride=8),
+                                dict(dtype=1, k_scale=P, v_scale=P, scale_token_stride=8),
+                                dict(dtype=1, k_scale=P, v_scale=P, scale_page_stride=64)])
+def test_pages_that_overlap_are_refused(kw):
+    assert cp.lib().cp_cache_check(C.byref(desc(**kw)), None, None, None, None) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(token_stride=8 * 128, head_stride=128), dict(token_stride=200, head_stride=63 * 200 + 128, page_stride=8 * 12728),
+                                dict(page_stride=128, head_stride=100 * 128, token_stride=8 * 100 * 128),     # pages innermost
+                                dict(pages=1, page_stride=8), dict(kv_heads=1, head_stride=8),
+                                dict(pages=(1 << 31) - 1, page_stride=1 << 38),
+                                dict(pages=1 << 20, page_stride=128, head_stride=1 << 38, kv_heads=2, token_stride=1 << 30),
+                                dict(dtype=1, k_scale=P, v_scale=P, scale_token_stride=16, scale_head_stride=2, scale_page_stride=1024)])
+def test_pages_of_any_order_are_accepted(kw):
+    assert cp.lib().cp_cache_check(C.byref(desc(**kw)), None, None, None, None) == 0
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(out_stride=2040), 1), (dict(out_head_stride=120), 1), (dict(out_head_stride=64), 1), (dict(out_stride=128), 1),
+    (dict(out_stride=64, out_head_stride=7 * 128), 1), (dict(out_stride=128, out_head_stride=7 * 128), 0),
+    (dict(out_stride=4096, out_head_stride=256), 0), (dict(q_stride=8, q_head_stride=8), 0)])
+def test_outputs_that_overlap_are_refused(kw, want):
+    """7 rows of 16 heads of 128; what is only read may overlap."""
+    assert cp.lib().cp_cache_check(C.byref(desc()), C.byref(batch()), None, C.byref(attend(**kw)), None) == want
+    assert cp.lib().cp_cache_check(C.byref(desc()), C.byref(batch(rows=1, max_new=1)), None,
+                                   C.byref(attend(out_stride=8)), None) == 0
