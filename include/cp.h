@@ -399,8 +399,10 @@ typedef struct cp_cache_desc {
  * array's bounds: a start that descends or passes rows, more new rows than
  * max_new, a length outside 0 .. max_length, a page outside the pool and a
  * row of cp_cache_append or cp_cache_read at a negative position set the
- * cache's sticky CP_ERR_DEVICE_BOUNDS; bad starts and lengths are clamped, a
- * bad page reads as zeros and is not written. */
+ * cache's sticky CP_ERR_DEVICE_BOUNDS; bad starts and lengths are clamped, and
+ * of a position on a bad page cp_cache_attend takes key and value as zeros,
+ * cp_cache_append writes nothing to the pages, and cp_cache_read leaves the
+ * row's outputs as they were. */
 typedef struct cp_batch {
   int sequences;              /* 1 .. 65535                                  */
   int rows;                   /* rows of the row arrays, >= 1                */
@@ -457,8 +459,9 @@ int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out);
  * over the head (x * (mean(x^2) + eps)^(-1/2) * gain, if a gain is given) and
  * rotated by the row's position (rotate-half, pairs (j, j + head_dim/2),
  * angle position * rope_base^(-2j/head_dim)), as in the frame's layer, in
- * fp32; q is rounded to q_out, k and v are rounded or quantised into the
- * row's place. One launch. qkv, q_out and the gains are 16-byte aligned,
+ * fp32 (a head whose sum of squares passes fp32's range comes out as zeros);
+ * q is rounded to q_out, k and v are rounded or quantised into the row's
+ * place. One launch. qkv, q_out and the gains are 16-byte aligned,
  * strides multiples of 8 elements. q_out may be qkv itself (q in its place,
  * the same stride), and does not overlap it otherwise. */
 int cp_cache_append(cp_cache* c, const cp_batch* batch, const cp_append* args, cp_stream_t stream);

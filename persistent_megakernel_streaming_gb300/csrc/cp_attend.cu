@@ -168,8 +168,8 @@ __device__ __forceinline__ void join_cluster(const AttendParams& p, const Seq& s
 // they lie, O^T = V^T P^T values transposed on their way out of shared memory;
 // S^T's layout is a transposition of 8 x 8 away from P^T's. (With the rows
 // along the 16, steps of two heads spent twice the instructions and registers
-// on rows that are not there: 64 sequences of 500 to 12001 e4m3
-// positions 151 us, now 137; 5.9 TB/s.)
+// on rows that are not there: 64 sequences of 500 to 12001 e4m3 positions
+// 151 us, now 140, the kernel alone; 5.8 TB/s.)
 //
 // K and V go to shared memory as they lie (16-byte units exchanged within a
 // row so that ldmatrix meets no bank twice). e4m3 is widened to fp16 in
@@ -183,8 +183,9 @@ __device__ __forceinline__ void join_cluster(const AttendParams& p, const Seq& s
 //
 // bf16 is bound by HBM: 64 sequences of one row, 16/8 heads of 128, 311 to
 // 6000 positions 127 us a call, 6.5 TB/s, 96 % of the copy rate. e4m3 by the
-// instructions that widen it: the 64 sequences above 143 us a call, issue
-// slots 43 % and integer pipe 48 % busy, 85 % of the copy rate.
+// chain of conversions in front of each product, at 7.6 warps an SM: the 64
+// sequences above 143 us a call, 85 % of the copy rate, with issue slots 44 %
+// and the integer pipe 48 % busy (twice bf16's: widening is most of it).
 template <int D, bool E4M3, int NT, bool CLUSTER>
 __device__ __forceinline__ void step_block(const AttendParams& p) {
   constexpr int TK = (E4M3 ? 32 : 16) * (128 / D);    // positions a tile
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(kStepWarps * 32, 2) attend_step_kernel(const _
 // ------------------------------------------------------------------ join
 // One warp a (row, query head) whose item was cut: the parts' averages weighed
 // by their sums. Bound by reading the parts once, small next to the cache
-// (largest where chunks are cut that fill no cluster: 16 us of a call of 139).
+// (largest where chunks are cut that fill no cluster: 11 us of a call of 141).
 template <int D>
 __global__ void __launch_bounds__(256) attend_join_kernel(const __grid_constant__ AttendParams p) {
   pdl_wait();

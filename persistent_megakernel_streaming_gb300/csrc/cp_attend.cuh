@@ -108,7 +108,10 @@ __device__ __forceinline__ void store_lse(const AttendParams& p, int part, int64
 // masked values by zero, which is wrong where one is infinite or NaN; a block
 // that finds one next to a mask runs this instead. So does one over an e4m3
 // cache whose positions' scales lie further apart than the 16-bit operands
-// reach: a row may see only the small ones.
+// reach (a row may see only the small ones), or whose q is wider than fp16.
+// Right and slow: 512 rows over 32768 bf16 positions 60 ms a call instead of
+// 0.135 where one NaN stands behind the diagonal, 64 single rows over e4m3
+// with one value 2^20 above the others 6.6 ms instead of 0.14.
 template <int D, bool E4M3>
 __device__ __noinline__ void plain_rows(const AttendParams& p, Seq s, int seq, int kv, int i0, int i1, int t_begin,
                                         int t_end, int part, bool whole, int warp, int warps, float* avg = nullptr,

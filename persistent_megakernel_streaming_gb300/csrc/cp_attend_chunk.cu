@@ -35,9 +35,9 @@
 // Bound by the chain from a tile's scores through its softmax to its second
 // product, and by the issuing warp: nothing of what it does between two groups
 // of products is hidden (each clock of it is one of the tensor core's). 512
-// rows of 16/8 heads of 128 behind 32256 positions, bf16: 133 us a call, 1020
-// TFLOP/s, the tensor pipe busy 52 %, 128 of 152 SMs; two prompts of 4096:
-// 150 us, 919 TFLOP/s, of which each block's start and end are 9 us. A second
+// rows of 16/8 heads of 128 behind 32256 positions, bf16: 135 us a call, 1010
+// TFLOP/s, the tensor pipe busy 51 %, 128 of 152 SMs; two prompts of 4096:
+// 150 us, 917 TFLOP/s, of which each block's start and end are 9 us. A second
 // issuing warp hides the gaps alone, but pulls the two softmaxes into step:
 // 186 us, with turns between the two 149.
 #include <cfloat>
@@ -170,7 +170,7 @@ __device__ __forceinline__ uint32_t op_at(int r, int u) {
 // Positions a part, by a whole warp: the plan's, made for sequences that all have the longest one's length and for more
 // than one round of blocks, or longer ones if at the sequences' own lengths those are one round that costs less. Every
 // block comes to the same. (16 sequences of 700 to 9000 e4m3 positions, four of them with 301 new rows: 150 us a call
-// in the plan's parts, 140 in these. Choosing among several rounds too measured up to 7 % slower and 5 % faster.)
+// in the plan's parts, 141 in these. Choosing among several rounds too measured up to 7 % slower and 5 % faster.)
 template <int D>
 __device__ __forceinline__ int chosen_chunk(const AttendParams& p) {
   const int lane = threadIdx.x & 31;
