@@ -305,7 +305,7 @@ __device__ __forceinline__ void step_block(const AttendParams& p) {
       }
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = min(max(top - 127, -126), 126);
+      const int e = min(max(top - 127, kLeastExp), 126);
       const float inv = pow2i(-e);
       bool small = false;
 #pragma unroll

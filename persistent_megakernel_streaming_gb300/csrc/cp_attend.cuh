@@ -61,11 +61,13 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t addr) {
 __device__ __forceinline__ bool any_nonzero(uint4 x) { return ((x.x | x.y | x.z | x.w) & 0x7f7f7f7fu) != 0; }
 
 // Over an e4m3 cache q enters the products in fp16, each row under a power of two that puts its largest element into
-// [1, 4). Elements below 2^-14 lose bits there. What a row has lost, times the scale of its scores and the largest key
-// that it may meet (448 times the largest scale), bounds the error of a score (in powers of two); a block where that
-// passes kMostLost computes its rows the plain way, from q as it is. kLeastLost stands in for a row that lost nothing, so
-// that the same bound finds scores whose scale comes near the end of fp32.
+// [1, 4), but for rows of less than 2^kLeastExp. Elements below 2^-14 lose bits there. What a row has lost, times the
+// scale of its scores and the largest key that it may meet (448 times the largest scale), bounds the error of a score (in
+// powers of two); a block where that passes kMostLost computes its rows the plain way, from q as it is. kLeastLost
+// stands in for a row that lost nothing, so that the same bound finds scores whose scale comes near the end of fp32.
+// (Looking costs 16 sequences of 1 or 301 rows 1.3 % of their 141 us, 64 single rows 0.2 % of 143.)
 constexpr float kMostLost = 0x1p-12f, kLeastLost = 0x1p-121f;
+constexpr int kLeastExp = -100;    // of a row's power of two, which times the scale of the scores stays a normal float
 
 // Whether fp16 pairs hold an element below fp16's normal range.
 template <int N>

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<D, E4M3>::kThreads, 1) attend_chunk_kernel
           for (int q = 0; q < 4; ++q) top = max(top, max(finite_exp(w[q] & 0xffffu), finite_exp(w[q] >> 16)));
 #pragma unroll
           for (int o = UPR / 2; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = min(max(top - 127, -126), 126);
+          const int e = min(max(top - 127, kLeastExp), 126);
           const float inv = pow2i(-e);
           uint32_t y[4];
 #pragma unroll

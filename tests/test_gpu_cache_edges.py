@@ -224,7 +224,7 @@ def test_queries_of_wide_range(e4m3, d, L, n, width):
 
 @pytest.mark.parametrize("e4m3,d", FORMATS)
 @pytest.mark.parametrize("n", [2, 40])
-@pytest.mark.parametrize("shift", [-110, -60, 60, 100])
+@pytest.mark.parametrize("shift", [-110, -99, -60, 60, 100])
 def test_queries_of_any_size(e4m3, d, n, shift):
     """All of q 2^shift times as large, and the keys as much smaller (but for what the least scale leaves of them)."""
     w = channels(World([300], [n], 2, d, 32, e4m3, seed=27), np.full(d, -float(shift)))
