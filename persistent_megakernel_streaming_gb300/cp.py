@@ -289,7 +289,14 @@ class Batch:
     ``start`` int32 [sequences + 1], ``length`` int32 [sequences] (cached positions, the new rows' own included),
     ``pages`` int32 [sequences][width]; device tensors, read when a call runs on the device. ``rows`` is the row
     arrays' length, ``max_new`` and ``max_len`` bound the new rows and the length of any sequence (0: no bound
-    but the arrays' own)."""
+    but the arrays' own). What a batch was made of stays: new lengths or pages are written into the tensors, other
+    tensors or bounds are another batch."""
+
+    def __setattr__(self, name, value):
+        # the C side keeps the addresses and the bounds that the checks were made for
+        if self.__dict__.get(name, value) is not value:        # (batch.length += 1 sets what is there)
+            raise AttributeError(f"{name}: fixed when the batch is made")
+        super().__setattr__(name, value)
 
     def __init__(self, start, length, pages, rows: int, max_new: int = 0, max_len: int = 0):
         import torch

@@ -66,3 +66,15 @@ def test_outputs_that_overlap_are_refused(kw, want):
     assert cp.lib().cp_cache_check(C.byref(desc()), C.byref(batch()), None, C.byref(attend(**kw)), None) == want
     assert cp.lib().cp_cache_check(C.byref(desc()), C.byref(batch(rows=1, max_new=1)), None,
                                    C.byref(attend(out_stride=8)), None) == 0
+
+
+def test_a_batch_stays_what_it_was_made_of():
+    """The C side has the tensors' addresses: one that took another's place would not be read, and the old one freed."""
+    i, table = torch.zeros(3, dtype=torch.int32), torch.zeros(2, 4, dtype=torch.int32)
+    b = cp.Batch(i, i[:2], table, 5, 2, 64)
+    for name, value in (("start", i.clone()), ("length", i[:2].clone()), ("pages", table.clone()), ("rows", 3), ("desc", None)):
+        with pytest.raises(AttributeError):
+            setattr(b, name, value)
+    assert b.rows == 5 and b.start is i and b.pages is table
+    b.length += 1               # in place, and what stood there again
+    assert i.tolist() == [1, 1, 0]
