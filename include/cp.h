@@ -437,7 +437,8 @@ typedef struct cp_attend {
   int64_t out_stride, out_head_stride;  /* no two heads' outputs overlap      */
   int q_heads;                /* a multiple of kv_heads, up to 64 times; q
                                  head h reads kv head h / (q_heads/kv_heads) */
-  float scale;                /* of the scores, > 0 (0: head_dim^-1/2)       */
+  float scale;                /* of the scores, > 0 (0: head_dim^-1/2), below
+                                 2.3e38: times log2(e) it is an fp32 number  */
   int causal;                 /* nonzero: a row sees positions up to its own;
                                  zero: all length[i] positions               */
   int window;                 /* > 0: only positions after its own position

@@ -495,6 +495,7 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   p->magic = (65535u + p->group) / p->group;
   const double scale = a->scale > 0.f ? (double)a->scale : 1.0 / std::sqrt((double)d.head_dim);
   p->scale_log2 = (float)(scale * 1.4426950408889634);
+  if (!std::isfinite(p->scale_log2)) return CP_ERR_INVALID_ARG;
   p->causal = a->causal != 0;
   p->window = a->window;
   p->timeout_ns = d.timeout_ns;

@@ -78,3 +78,9 @@ def test_a_batch_stays_what_it_was_made_of():
     assert b.rows == 5 and b.start is i and b.pages is table
     b.length += 1               # in place, and what stood there again
     assert i.tolist() == [1, 1, 0]
+
+
+@pytest.mark.parametrize("scale,want", [(2.3e38, 0), (2.4e38, 1), (3.4e38, 1), (1e-45, 0)])
+def test_scales_next_to_the_ends_of_fp32(scale, want):
+    """The kernels multiply by scale * log2(e): as an infinity it would make NaN of a score of zero."""
+    assert cp.lib().cp_cache_check(C.byref(desc()), C.byref(batch()), None, C.byref(attend(scale=scale)), None) == want

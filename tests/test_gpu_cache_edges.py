@@ -323,3 +323,13 @@ def test_binding_refuses_what_its_types_would_change():
         with pytest.raises(ValueError):
             call()
     w.check(q, out)
+
+
+@pytest.mark.parametrize("e4m3,d", FORMATS)
+@pytest.mark.parametrize("scale", [1e-44, 1e-30])
+def test_scales_next_to_zero(e4m3, d, scale):
+    """...make every visible position count alike; masked ones stay out."""
+    w = World([300, 70], [40, 2], 2, d, 32, e4m3, seed=33).fill()
+    for window in (0, 33):
+        q, out = w.attend(4, scale=scale, window=window)
+        w.check(q, out, scale=scale, window=window)
