@@ -495,6 +495,15 @@ int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, 
 int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, void* workspace,
                     size_t workspace_bytes, cp_stream_t stream);
 
+/* Copy whole pages of the cache, keys, values and scales: for i < *count, page
+ * moves[i][0] to page moves[i][1]. `moves` is device int32 [capacity][2] and
+ * `count` device int32 [1], as cp_pages_grow and cp_pages_compact write them;
+ * a count below 1 copies nothing. The pages copied to are distinct, and none
+ * is copied from. A count past capacity (the moves there are made) and a page
+ * outside the pool (that move is left out) set the sticky
+ * CP_ERR_DEVICE_BOUNDS; a page onto itself is left as it is. One launch. */
+int cp_cache_copy(cp_cache* c, const int32_t* moves, int capacity, const int32_t* count, cp_stream_t stream);
+
 /* Synchronise the device and return the cache's sticky device status (CP_OK,
  * CP_ERR_DEVICE_BOUNDS or CP_ERR_TIMEOUT; CP_ERR_CUDA if the synchronisation
  * fails); reset it. Calls on a cache whose status is set still run. */
@@ -511,6 +520,216 @@ void cp_cache_destroy(cp_cache* c);
  * and attend's heads and mask, not on what the arrays hold. */
 int cp_cache_check(const cp_cache_desc* desc, const cp_batch* batch, const cp_append* append,
                    const cp_attend* attend, size_t* workspace_bytes);
+
+/* ============================================================ pages of a cache
+ * Which pages hold what: page tables and lengths of many sequences over one
+ * pool of pages, with a count of the table entries that name each page, so
+ * that sequences share the pages of a common prefix. Caches of the same page
+ * count and size (a model's layers) share one such state; what a call wants
+ * moved inside the pages it leaves in `moves`, for cp_cache_copy of each. The
+ * arrays are the caller's, on the device, and are read and written there when
+ * a call runs, so that calls can be captured; tables and lengths are those of
+ * cp_batch. */
+typedef struct cp_pages_desc {
+  int pages;                  /* pages in the pool, 1 .. 2^30                 */
+  int page_size;              /* positions per page: 16, 32, 64 or 128       */
+  int sequences;              /* 1 .. 65535                                  */
+  int table_width;            /* entries per sequence in page_table          */
+  int64_t table_stride;       /* entries from one sequence to the next (0:
+                                 table_width)                                */
+  int32_t* refs;              /* device [pages]: table entries (and other
+                                 holders, if the caller adds them) that name
+                                 a page; 0: the page is free                 */
+  int32_t* page_table;        /* device [sequences][table_stride]            */
+  int32_t* length;            /* device [sequences]: positions held, in the
+                                 first ceil(length / page_size) entries; no
+                                 other entry is read                         */
+} cp_pages_desc;
+
+typedef struct cp_pages cp_pages; /* opaque, owned by the library */
+
+/* Make an object for such a state (the arrays are kept for its life; what
+ * they hold is not touched). It holds scratch memory: its calls are made in
+ * one stream's order, captured ones included. Errors: CP_ERR_INVALID_ARG,
+ * CP_ERR_UNSUPPORTED (limits or device), CP_ERR_NOMEM, CP_ERR_CUDA. It
+ * allocates and synchronises: not while a stream is being captured.
+ * The calls check what the arrays hold without leaving their bounds: a
+ * length below 0 or past the table (taken as 0), a sequence or page out of
+ * range, and a count that does not cover its entries set the sticky
+ * CP_ERR_DEVICE_BOUNDS, and what is concerned is left out. */
+int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out);
+
+/* For each of n pairs, sequence dst[i], which holds nothing, becomes a copy of
+ * sequence src[i] that shares its pages (device int32 [n] each; several may
+ * copy one sequence). A pair whose dst holds something, stands twice or is
+ * itself copied from in this call is left out (CP_ERR_DEVICE_BOUNDS). */
+int cp_pages_fork(cp_pages* p, const int32_t* src, const int32_t* dst, int n, cp_stream_t stream);
+
+/* Make room for add[i] more positions (device int32 [sequences], 0 or more)
+ * and add them to the lengths. Free pages are taken in ascending order, for
+ * one sequence after the other. A sequence that grows into a page that it
+ * shares gets a page of its own instead, to which moves[] copies what is
+ * there; of the sequences that share one and grow in the same call, the last
+ * keeps it if no other holds it. Then cp_cache_copy moves them, in front of what
+ * writes the new positions. `moves`: device int32 [capacity][2], capacity at
+ * least `sequences`; the moves stand in the sequences' order and *count is
+ * their number. If the pool has too few free pages nothing at all is changed,
+ * and *count is minus the number that it lacks. A sequence that would grow
+ * past its table, or by a negative number, is left out
+ * (CP_ERR_DEVICE_BOUNDS). */
+int cp_pages_grow(cp_pages* p, const int32_t* add, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream);
+
+/* Cut each sequence to at most keep[i] positions (device int32 [sequences];
+ * 0 ends it, one no less than its length leaves it as it is, a negative one
+ * too, with CP_ERR_DEVICE_BOUNDS), and take its hold off the pages past them:
+ * one that nobody holds is free. Entries given up become -1. */
+int cp_pages_trim(cp_pages* p, const int32_t* keep, cp_stream_t stream);
+
+/* Move the held pages to the pool's front: with n of them, those from page n
+ * on move, in ascending order, to the free pages below n, in ascending order.
+ * moves[] says so for cp_cache_copy (`moves`: device int32 [capacity][2],
+ * capacity at least pages / 2; *count their number), counts and tables are
+ * rewritten. All pages from n on are then free. */
+int cp_pages_compact(cp_pages* p, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream);
+
+/* Synchronise the device and return the sticky device status (CP_OK,
+ * CP_ERR_DEVICE_BOUNDS; CP_ERR_CUDA if the synchronisation fails); reset it. */
+int cp_pages_status(cp_pages* p);
+int cp_pages_clear_status(cp_pages* p);
+
+/* Release the object (synchronises its device), not the arrays. */
+void cp_pages_destroy(cp_pages* p);
+
+/* Host only: the status that cp_pages_create returns for this description on
+ * a GPU. */
+int cp_pages_check(const cp_pages_desc* desc);
+
+/* ============================================================ projections
+ * A projection of few rows whose weights are kept in 4 bits: the layers in
+ * front of the frame read all their weights for the rows of one step. Weight
+ * (n, k) is the bfloat16 nearest to (q[n][k] - zero) * scale, with a scale,
+ * and a zero point, for each row n and `group` consecutive k. */
+enum cp_out_dtype { CP_OUT_BF16 = 0, CP_OUT_F32 = 1 };
+
+/* Limits (CP_ERR_UNSUPPORTED outside): group 32, 64 or 128; width at most
+ * 2^20, features at most 2^24. */
+typedef struct cp_linear_desc {
+  int features;               /* rows of the weights                          */
+  int width;                  /* inputs, a multiple of group                  */
+  int group;
+  int gated;                  /* nonzero: the first half of the rows is a gate
+                                 projection's, the second an up projection's
+                                 (features is even), and a result is
+                                 silu(gate) * up, features / 2 of them        */
+  const void* q;              /* device [features][width / 2] bytes, two
+                                 weights each: the even k in the low half     */
+  const void* scale;          /* device bf16 [features][width / group]       */
+  const void* zero;           /* device bytes [features][width / group], each
+                                 0 .. 15; NULL: 8                             */
+} cp_linear_desc;
+
+typedef struct cp_linear_args {
+  const void* x;              /* device bf16 [rows][width]                    */
+  int64_t x_stride;           /* elements from row to row (0: contiguous)     */
+  int rows;                   /* 1 .. 65535                                   */
+  int out_dtype;              /* enum cp_out_dtype                            */
+  void* out;                  /* device [rows][features, or half of them]     */
+  int64_t out_stride;
+  const void* add;            /* device, as out: added to the result before
+                                 it is rounded; NULL: nothing                 */
+  int64_t add_stride;
+} cp_linear_args;
+
+typedef struct cp_linear cp_linear; /* opaque, owned by the library */
+
+/* Lay the weights out for the kernels, in memory that the object owns (about
+ * what the arrays take; these may be freed on return). Errors:
+ * CP_ERR_INVALID_ARG (a zero point above 15, too), CP_ERR_UNSUPPORTED (limits
+ * or device), CP_ERR_NOMEM, CP_ERR_CUDA. It allocates and synchronises: not
+ * while a stream is being captured. The object holds no scratch: calls on
+ * several streams may overlap. */
+int cp_linear_create(const cp_linear_desc* desc, int device, cp_linear** out);
+
+/* out[r] = sum over k of x[r][k] * weight[n][k], or silu(gate) * up of two
+ * such sums, plus add[r]: exact products, sums and the rest in fp32, rounded
+ * once to out's type. A row's result does not depend on the other rows' values. Bit-identical
+ * run to run. One launch. x is 16-byte aligned, x_stride a multiple of 8; rows
+ * of out lie apart. out may be add itself, with the same stride, and overlaps
+ * neither it nor x otherwise. */
+int cp_linear_apply(cp_linear* l, const cp_linear_args* args, cp_stream_t stream);
+
+/* The weights as the numbers that they stand for, device bf16
+ * [features][width], 16-byte aligned or not. */
+int cp_linear_unpack(cp_linear* l, void* out, cp_stream_t stream);
+
+/* Release the object (synchronises its device). */
+void cp_linear_destroy(cp_linear* l);
+
+/* Host only: the status that the calls return for these arguments on a GPU.
+ * args may be NULL. */
+int cp_linear_check(const cp_linear_desc* desc, const cp_linear_args* args);
+
+/* ============================================================ drafted tokens
+ * Verification of drafted tokens: a draft proposed tokens for some sequences,
+ * one pass of the target gave logits behind each of them, and as many are
+ * taken as leaves the target's own distribution unchanged, with one token more
+ * from the target. Sequence i has the rows start[i] .. start[i+1]-1: row r's
+ * logits are for the token that draft[r] proposes, and those of the sequence's
+ * last row for the token behind its drafted ones (one row: nothing was
+ * drafted, the call is a plain draw; none: accepted is 0 and token -1). */
+enum cp_logits_dtype { CP_LOGITS_F32 = 0, CP_LOGITS_BF16 = 1 };
+
+typedef struct cp_verify_args {
+  int sequences;              /* 1 .. 65535                                   */
+  int rows;                   /* rows of the row arrays, 1 .. 2^20            */
+  int vocab;                  /* 1 .. 2^24, and rows * vocab up to 2^43       */
+  int dtype;                  /* enum cp_logits_dtype                         */
+  const int32_t* start;       /* device [sequences + 1]                       */
+  const void* logits;         /* device [rows][vocab]: the target's           */
+  int64_t logits_stride;      /* elements from row to row (0: contiguous)     */
+  const void* draft_logits;   /* the draft's, of the same type and shape, or
+                                 NULL: each drafted token was certain         */
+  int64_t draft_stride;
+  const int32_t* draft;       /* device [rows]; not read for last rows        */
+  const float* temperature;   /* device [sequences]; <= 0 (or NaN): greedy    */
+  const float* u_accept;      /* device [rows], uniform in [0, 1); not read
+                                 for last rows                                */
+  const float* u_token;       /* device [sequences], uniform in [0, 1)        */
+  int32_t* accepted;          /* device [sequences]: drafted tokens taken     */
+  int32_t* token;             /* device [sequences]: the token behind them    */
+  float* prob;                /* device [rows] or NULL: the target's
+                                 probability of each drafted token (at
+                                 temperature 1 where greedy); last rows' are
+                                 left as they are                             */
+} cp_verify_args;
+
+/* With p = softmax(logits / temperature) and q that of the draft's logits (1
+ * for the drafted token if there are none), drafted token d of a row is taken
+ * if u_accept * q[d] < p[d] and those before it were. The token behind those
+ * taken is drawn from max(p - q, 0) of the first refused row (scaled to sum
+ * 1), or from p of the last one: the least v whose cumulated weight passes
+ * u_token times the sum. Greedy sequences take d if it is the target's
+ * largest logit (the lowest index of equal ones), and then that token.
+ * A logit is times the fp32 1 / temperature; probabilities are fp32 numbers
+ * and each row's sums more exact than 2^-40, so that the token drawn is the
+ * same wherever they are computed so. A NaN or -infinite logit has no
+ * probability, +infinite ones share it all. A drafted token outside the
+ * vocabulary is not taken. A row without any probability (all its logits
+ * masked) takes no token; if one is to be drawn there the token is -1. Should
+ * the roundings of p and q leave a refused row no weight, p is drawn from.
+ * Uniforms outside [0, 1) count as its nearer end. Where
+ * start descends or passes rows, every accepted and token is -1.
+ * Rows behind the last sequence belong to nobody. Results are bit-identical
+ * run to run. `workspace`: device memory of at least cp_verify_check's
+ * workspace_bytes, 16-byte aligned, nothing kept in it between calls; calls
+ * that may overlap, captured ones included, need workspaces of their own.
+ * Errors: CP_ERR_INVALID_ARG, CP_ERR_UNSUPPORTED, CP_ERR_CUDA. */
+int cp_verify(const cp_verify_args* args, int device, void* workspace, size_t workspace_bytes, cp_stream_t stream);
+
+/* Host only: the status that cp_verify returns for these arguments on a GPU,
+ * and the workspace that it needs (may be NULL), which depends on sequences,
+ * rows and vocab alone. */
+int cp_verify_check(const cp_verify_args* args, size_t* workspace_bytes);
 
 /* ------------------------------------------------------------ host checks */
 /* Build the static schedule for `shape` with `grid` CTAs in clusters of

@@ -30,6 +30,9 @@ SOURCES = [
     ("cp_cache.cu", "cp_cache.cu.o", []),
     ("cp_attend.cu", "cp_attend.cu.o", []),
     ("cp_attend_chunk.cu", "cp_attend_chunk.cu.o", []),
+    ("cp_pages.cu", "cp_pages.cu.o", []),
+    ("cp_linear.cu", "cp_linear.cu.o", []),
+    ("cp_verify.cu", "cp_verify.cu.o", []),
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

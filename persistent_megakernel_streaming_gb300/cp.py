@@ -25,7 +25,11 @@ EXPORTS = ["cp_create", "cp_frame", "cp_frame_split", "cp_debug_logits", "cp_deb
            "cp_clear_status", "cp_get_info", "cp_trace", "cp_destroy", "cp_strerror",
            "cp_plan_check", "cp_test_philox", "cp_test_draw", "cp_frame_static",
            "cp_cache_create", "cp_cache_append", "cp_cache_read", "cp_cache_attend", "cp_cache_status",
-           "cp_cache_clear_status", "cp_cache_destroy", "cp_cache_check", "cp_test_slot"]
+           "cp_cache_clear_status", "cp_cache_destroy", "cp_cache_check", "cp_test_slot", "cp_cache_copy",
+           "cp_pages_create", "cp_pages_fork", "cp_pages_grow", "cp_pages_trim", "cp_pages_compact", "cp_pages_status",
+           "cp_pages_clear_status", "cp_pages_destroy", "cp_pages_check",
+           "cp_linear_create", "cp_linear_apply", "cp_linear_unpack", "cp_linear_destroy", "cp_linear_check",
+           "cp_verify", "cp_verify_check"]
 
 
 class Shape(C.Structure):
@@ -94,6 +98,28 @@ class AttendArgs(C.Structure):
                 ("causal", C.c_int), ("window", C.c_int)]
 
 
+class PagesDesc(C.Structure):
+    _fields_ = [("pages", C.c_int), ("page_size", C.c_int), ("sequences", C.c_int), ("table_width", C.c_int),
+                ("table_stride", C.c_int64), ("refs", C.c_void_p), ("page_table", C.c_void_p), ("length", C.c_void_p)]
+
+
+class LinearDesc(C.Structure):
+    _fields_ = [("features", C.c_int), ("width", C.c_int), ("group", C.c_int), ("gated", C.c_int), ("q", C.c_void_p),
+                ("scale", C.c_void_p), ("zero", C.c_void_p)]
+
+
+class LinearArgs(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_stride", C.c_int64), ("rows", C.c_int), ("out_dtype", C.c_int), ("out", C.c_void_p),
+                ("out_stride", C.c_int64), ("add", C.c_void_p), ("add_stride", C.c_int64)]
+
+
+class VerifyArgs(C.Structure):
+    _fields_ = [("sequences", C.c_int), ("rows", C.c_int), ("vocab", C.c_int), ("dtype", C.c_int), ("start", C.c_void_p),
+                ("logits", C.c_void_p), ("logits_stride", C.c_int64), ("draft_logits", C.c_void_p), ("draft_stride", C.c_int64),
+                ("draft", C.c_void_p), ("temperature", C.c_void_p), ("u_accept", C.c_void_p), ("u_token", C.c_void_p),
+                ("accepted", C.c_void_p), ("token", C.c_void_p), ("prob", C.c_void_p)]
+
+
 class CPError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -138,6 +164,25 @@ def lib() -> C.CDLL:
         L.cp_cache_destroy.restype = None
         L.cp_cache_check.argtypes = [C.POINTER(CacheDesc), C.POINTER(BatchDesc), C.POINTER(AppendArgs),
                                      C.POINTER(AttendArgs), C.POINTER(C.c_size_t)]
+        L.cp_cache_copy.argtypes = [vp, vp, i, vp, st]
+        L.cp_pages_create.argtypes = [C.POINTER(PagesDesc), i, C.POINTER(vp)]
+        L.cp_pages_fork.argtypes = [vp, vp, vp, i, st]
+        L.cp_pages_grow.argtypes = [vp, vp, vp, i, vp, st]
+        L.cp_pages_trim.argtypes = [vp, vp, st]
+        L.cp_pages_compact.argtypes = [vp, vp, i, vp, st]
+        L.cp_pages_status.argtypes = [vp]
+        L.cp_pages_clear_status.argtypes = [vp]
+        L.cp_pages_destroy.argtypes = [vp]
+        L.cp_pages_destroy.restype = None
+        L.cp_pages_check.argtypes = [C.POINTER(PagesDesc)]
+        L.cp_linear_create.argtypes = [C.POINTER(LinearDesc), i, C.POINTER(vp)]
+        L.cp_linear_apply.argtypes = [vp, C.POINTER(LinearArgs), st]
+        L.cp_linear_unpack.argtypes = [vp, vp, st]
+        L.cp_linear_destroy.argtypes = [vp]
+        L.cp_linear_destroy.restype = None
+        L.cp_linear_check.argtypes = [C.POINTER(LinearDesc), C.POINTER(LinearArgs)]
+        L.cp_verify.argtypes = [C.POINTER(VerifyArgs), i, vp, C.c_size_t, st]
+        L.cp_verify_check.argtypes = [C.POINTER(VerifyArgs), C.POINTER(C.c_size_t)]
         L.cp_test_slot.argtypes = [C.POINTER(CacheDesc), C.POINTER(C.c_int32), i, i, i]
         L.cp_test_slot.restype = C.c_int64
         _lib = L
@@ -283,6 +328,32 @@ def _not_lost(x: float, what: str):
         raise ValueError(f"{what}: {x} is zero in fp32")
 
 
+def _stream_on(index: int, stream) -> int:
+    """The raw stream: torch's current one of that device, if none is given."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(index)
+    return _stream(stream)
+
+
+def _workspace(device, size: int, stream):
+    """Device bytes, allocated on the stream that uses them, so that the allocator hands them on in that stream's order."""
+    import torch
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
+def _array(t, what: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous device array of that type, shape and device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{what}: {dtype} {list(shape)}, contiguous, on cuda:{index}; got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
 class Batch:
     """A ragged batch (cp_batch): row ``start[i] + j`` of the calls' row arrays is sequence i's new row j.
 
@@ -384,6 +455,14 @@ class Cache:
         if code:
             raise CPError(code, "cp_cache_read")
 
+    def copy(self, moves, count, stream=None):
+        """Whole pages, keys, values and scales, from moves[i][0] to moves[i][1] for i below count[0]: int32 [capacity][2]
+        and [1], as Pages.grow and Pages.compact write them."""
+        a, capacity, n = _moves(moves, count, self.device_index)
+        code = lib().cp_cache_copy(self._h, a, capacity, n, self._stream(stream))
+        if code:
+            raise CPError(code, "cp_cache_copy")
+
     def attend(self, batch: Batch, q, out, scale: float = 0.0, causal: bool = True, window: int = 0, workspace=None,
                stream=None):
         """Attention of q [rows][q_heads][head_dim] over the cache into out (the same shape). Without a
@@ -443,20 +522,10 @@ class Cache:
         return t.data_ptr()
 
     def _stream(self, stream) -> int:
-        if stream is None:
-            import torch
-            return torch._C._cuda_getCurrentRawStream(self.device_index)
-        return _stream(stream)
+        return _stream_on(self.device_index, stream)
 
     def _workspace(self, size, stream):
-        # allocated on the stream that uses it, so that the allocator hands it on in that stream's order
-        import torch
-        if stream is None:
-            return torch.empty(size, dtype=torch.uint8, device=self.device)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(size, dtype=torch.uint8, device=self.device)
+        return _workspace(self.device, size, stream)
 
     def status(self) -> int:
         return lib().cp_cache_status(self._h)
@@ -474,6 +543,224 @@ class Cache:
             self.close()
         except Exception:
             pass
+
+
+def _moves(moves, count, index: int):
+    import torch
+    if moves.dtype != torch.int32 or moves.dim() != 2 or moves.shape[1] != 2 or not moves.is_contiguous() or \
+            moves.get_device() != index:
+        raise ValueError(f"moves: int32 [capacity][2], contiguous, on cuda:{index}")
+    return moves.data_ptr(), _int32(moves.shape[0], "moves"), _array(count, "count", torch.int32, (1,), index)
+
+
+class Pages:
+    """Which pages of a cache, or of several of the same page count and size, hold what (cp_pages_create).
+
+    ``refs`` int32 [pages]: how many table entries name a page (0: free). ``table`` int32 [sequences][width] and
+    ``length`` int32 [sequences]: as a Batch's pages and length. Device tensors that the calls read and write; what
+    the calls want moved inside the pages stands in ``moves`` (int32 [capacity][2]) and ``count`` (int32 [1]), for
+    Cache.copy of each cache."""
+
+    def __init__(self, refs, table, length, page_size: int):
+        import torch
+        for name, t, dims in (("refs", refs, 1), ("table", table, 2), ("length", length, 1)):
+            if t.dtype != torch.int32 or t.dim() != dims or t.device.type != "cuda" or t.device != refs.device or \
+                    t.shape[-1] > 1 and t.stride(-1) != 1:
+                raise ValueError(f"{name}: int32, {dims} axes, contiguous, on one GPU")
+        if table.shape[0] != length.shape[0]:
+            raise ValueError("table [sequences][width] and length [sequences]")
+        self.keep = (refs, table, length)
+        self.device_index = refs.get_device()
+        self.sequences, self.pages = length.shape[0], refs.shape[0]
+        self.desc = PagesDesc(_int32(refs.shape[0], "refs"), _int32(page_size, "page_size"), _int32(length.shape[0], "length"),
+                              _int32(table.shape[1], "table"), _stride(table, 0), _ptr(refs), _ptr(table), _ptr(length))
+        h = C.c_void_p()
+        _check(lib().cp_pages_create(C.byref(self.desc), self.device_index, C.byref(h)), "cp_pages_create")
+        self._h = h
+
+    def fork(self, src, dst, stream=None):
+        """Sequences dst[i], which hold nothing, become copies of src[i] that share its pages (int32 [n] each)."""
+        import torch
+        n = dst.numel()
+        code = lib().cp_pages_fork(self._h, _array(src, "src", torch.int32, (n,), self.device_index),
+                                   _array(dst, "dst", torch.int32, (n,), self.device_index), n, _stream_on(self.device_index, stream))
+        if code:
+            raise CPError(code, "cp_pages_fork")
+
+    def grow(self, add, moves, count, stream=None):
+        """Room for add[i] (int32 [sequences]) more positions each; count[0] below 0: the pool lacks that many pages, and
+        nothing was changed."""
+        import torch
+        m, capacity, n = _moves(moves, count, self.device_index)
+        code = lib().cp_pages_grow(self._h, _array(add, "add", torch.int32, (self.sequences,), self.device_index), m, capacity, n,
+                                   _stream_on(self.device_index, stream))
+        if code:
+            raise CPError(code, "cp_pages_grow")
+
+    def trim(self, keep, stream=None):
+        """Each sequence cut to at most keep[i] (int32 [sequences]) positions, pages past them given up."""
+        import torch
+        code = lib().cp_pages_trim(self._h, _array(keep, "keep", torch.int32, (self.sequences,), self.device_index),
+                                   _stream_on(self.device_index, stream))
+        if code:
+            raise CPError(code, "cp_pages_trim")
+
+    def compact(self, moves, count, stream=None):
+        """The held pages moved to the pool's front."""
+        m, capacity, n = _moves(moves, count, self.device_index)
+        code = lib().cp_pages_compact(self._h, m, capacity, n, _stream_on(self.device_index, stream))
+        if code:
+            raise CPError(code, "cp_pages_compact")
+
+    def status(self) -> int:
+        return lib().cp_pages_status(self._h)
+
+    def clear_status(self):
+        _check(lib().cp_pages_clear_status(self._h), "cp_pages_clear_status")
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().cp_pages_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Linear:
+    """A projection with 4-bit weights (cp_linear_create), laid out once into memory of its own.
+
+    ``q`` uint8 [features][width / 2], two weights a byte, the even input in the low half; ``scale`` bf16
+    [features][width / group] and ``zero`` uint8 of the same shape (None: 8). ``gated``: the first half of the rows is a
+    gate projection's, the second an up projection's."""
+
+    def __init__(self, q, scale, zero=None, gated: bool = False):
+        import torch
+        if q.dtype != torch.uint8 or q.dim() != 2 or scale.dim() != 2 or scale.dtype not in (torch.bfloat16, torch.int16) or \
+                q.device.type != "cuda":
+            raise ValueError("q: uint8 [features][width / 2], scale: bf16 [features][width / group], on a GPU")
+        n, half = q.shape
+        index = q.get_device()
+        if scale.shape[0] != n or not scale.shape[1] or 2 * half % scale.shape[1]:
+            raise ValueError("q [features][width / 2] and scale [features][width / group]")
+        _array(q, "q", torch.uint8, (n, half), index)
+        _array(scale, "scale", scale.dtype, scale.shape, index)
+        if zero is not None:
+            _array(zero, "zero", torch.uint8, scale.shape, index)
+        self.features, self.width, self.group, self.gated = n, 2 * half, 2 * half // scale.shape[1], bool(gated)
+        self.outs = n // 2 if gated else n
+        self.device_index = index
+        self.desc = LinearDesc(_int32(n, "features"), _int32(self.width, "width"), self.group, int(self.gated), _ptr(q), _ptr(scale),
+                               _ptr(zero))
+        self.dtypes = {torch.bfloat16: 0, torch.float32: 1}
+        self.x_dtypes = (torch.bfloat16, torch.int16)
+        h = C.c_void_p()
+        _check(lib().cp_linear_create(C.byref(self.desc), index, C.byref(h)), "cp_linear_create")
+        self._h = h
+
+    def apply(self, x, out, add=None, stream=None):
+        """x bf16 [rows][width] into out [rows][features, or half of them if gated], bf16 or fp32; ``add`` of out's type is
+        added before the result is rounded."""
+        rows = x.shape[0]
+        if x.dtype not in self.x_dtypes or x.shape != (rows, self.width) or x.get_device() != self.device_index:
+            raise ValueError(f"x: bf16 [rows][{self.width}] on the weights' device")
+        kind = self.dtypes.get(out.dtype)
+        if kind is None or out.get_device() != self.device_index:
+            raise ValueError("out: bf16 or fp32 on the weights' device")
+        a = LinearArgs(x.data_ptr(), self._row(x, "x"), rows, kind, out.data_ptr(), self._row(out, "out", rows))
+        if add is not None:
+            if add.dtype != out.dtype or add.get_device() != self.device_index:
+                raise ValueError("add: of out's type and device")
+            a.add, a.add_stride = add.data_ptr(), self._row(add, "add", rows)
+        code = lib().cp_linear_apply(self._h, C.byref(a), _stream_on(self.device_index, stream))
+        if code:
+            raise CPError(code, "cp_linear_apply")
+
+    def _row(self, t, what, rows=None):
+        """The stride of t's rows."""
+        if rows is not None and t.shape != (rows, self.outs):
+            raise ValueError(f"{what}: [{rows}][{self.outs}]; got {list(t.shape)}")
+        if t.shape[1] > 1 and t.stride(1) != 1:
+            raise ValueError(f"{what}: the last axis contiguous")
+        return _stride(t, 0)
+
+    def unpack(self, out, stream=None):
+        """The weights as the bf16 numbers that they stand for, into out [features][width]."""
+        if out.dtype not in self.x_dtypes:
+            raise ValueError("out: bf16")
+        a = _array(out, "out", out.dtype, (self.features, self.width), self.device_index)
+        code = lib().cp_linear_unpack(self._h, a, _stream_on(self.device_index, stream))
+        if code:
+            raise CPError(code, "cp_linear_unpack")
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().cp_linear_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_verify_needs: dict = {}
+
+
+def verify_workspace_bytes(sequences: int, rows: int, vocab: int) -> int:
+    """What ``verify`` needs, whatever its arrays hold."""
+    key = (sequences, rows, vocab)
+    need = _verify_needs.get(key)
+    if need is None:
+        a = VerifyArgs(_int32(sequences, "sequences"), _int32(rows, "rows"), _int32(vocab, "vocab"), 0, 16, 16, 0, None, 0, 16, 16, 16,
+                       16, 16, 16, None)
+        n = C.c_size_t()
+        _check(lib().cp_verify_check(C.byref(a), C.byref(n)), "cp_verify")
+        if len(_verify_needs) > 4096:
+            _verify_needs.clear()
+        need = _verify_needs[key] = n.value
+    return need
+
+
+def verify(logits, draft, start, u_accept, u_token, temperature, accepted, token, prob=None, draft_logits=None, workspace=None,
+           stream=None):
+    """Verification of drafted tokens (cp_verify): how many of each sequence's are taken, and the token behind them.
+
+    ``logits`` bf16 or fp32 [rows][vocab], the target's, and ``draft_logits`` the draft's (None: its tokens were certain);
+    ``draft`` int32, ``u_accept`` and ``prob`` fp32 [rows]; ``start`` int32 [sequences + 1]; ``u_token`` and ``temperature`` fp32,
+    ``accepted`` and ``token`` int32 [sequences]. Without a ``workspace`` (device bytes, see verify_workspace_bytes) one
+    is taken from torch's allocator for this call."""
+    import torch
+    index = logits.get_device()
+    if logits.dim() != 2 or index < 0 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: bf16 or fp32 [rows][vocab] on a GPU")
+    rows, vocab = logits.shape
+    n = accepted.numel()
+    strides = [0, 0]
+    for k, t in enumerate((logits, draft_logits)):
+        if t is not None:
+            if t.dtype != logits.dtype or t.shape != logits.shape or t.get_device() != index or vocab > 1 and t.stride(1) != 1:
+                raise ValueError("logits, draft_logits: of one type, shape and device, the last axis contiguous")
+            strides[k] = _stride(t, 0)
+    need = verify_workspace_bytes(n, rows, vocab)
+    f32, i32 = torch.float32, torch.int32
+    a = VerifyArgs(n, rows, vocab, int(logits.dtype == torch.bfloat16), _array(start, "start", i32, (n + 1,), index), logits.data_ptr(),
+                   strides[0], _ptr(draft_logits) or None, strides[1], _array(draft, "draft", i32, (rows,), index),
+                   _array(temperature, "temperature", f32, (n,), index), _array(u_accept, "u_accept", f32, (rows,), index),
+                   _array(u_token, "u_token", f32, (n,), index), _array(accepted, "accepted", i32, (n,), index),
+                   _array(token, "token", i32, (n,), index), None if prob is None else _array(prob, "prob", f32, (rows,), index))
+    if workspace is None:
+        workspace = _workspace(logits.device, need, stream)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace: contiguous, on the logits' device")
+    code = lib().cp_verify(C.byref(a), index, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           _stream_on(index, stream))
+    if code:
+        raise CPError(code, "cp_verify")
 
 
 def test_philox(ctr, key, use_curand: bool, out, stream=None):

@@ -3,39 +3,13 @@
 #pragma once
 #include "cp_cache.cuh"
 #include "cp_cache_ptx.cuh"
+#include "cp_call.h"
 
 namespace cp {
 namespace cache {
 
 using ptx::pdl_trigger;
 using ptx::pdl_wait;
-
-// A launch in clusters of cluster_x by cluster_y blocks, and, with `early`, one that may start before the kernel in
-// front of it has ended (it waits for that one where it needs to: pdl_wait).
-template <class K, class... A>
-cudaError_t launch_as(K kernel, dim3 grid, int cluster_x, int cluster_y, bool early, int threads, size_t smem, cudaStream_t s,
-                      const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  if (cluster_x * cluster_y > 1) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
-    attr[cfg.numAttrs].val.clusterDim.x = cluster_x;
-    attr[cfg.numAttrs].val.clusterDim.y = cluster_y;
-    attr[cfg.numAttrs].val.clusterDim.z = 1;
-    ++cfg.numAttrs;
-  }
-  if (early) {
-    attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
-    ++cfg.numAttrs;
-  }
-  cfg.attrs = attr;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 
 // Biased exponent of a bf16 pattern, 0 for infinities and NaN.
 __device__ __forceinline__ int finite_exp(uint32_t h) {

@@ -11,6 +11,7 @@
 #include "cp.h"
 #include "cp_cache.cuh"
 #include "cp_cache_ptx.cuh"
+#include "cp_call.h"
 
 using namespace cp;
 using namespace cp::cache;
@@ -305,42 +306,65 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   }
 }
 
-// ------------------------------------------------------------------ checks
-struct DeviceGuard {
-  int prev = -1;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) prev = -1;
-    if (prev == dev) prev = -1;
-    else cudaSetDevice(dev);
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
+// ------------------------------------------------------------------ copies of pages
+struct CopyParams {
+  CacheView c;
+  const int32_t* moves;
+  const int32_t* count;
+  int capacity;
+  int lane_shift;      // 16-byte units a position: a power of two
+  int units;           // of a page, keys and values
+  int pieces;          // blocks' shares of a page
+  int scale_vec;       // positions' scales lie side by side, on 16-byte boundaries
 };
+constexpr int kCopyThreads = 256, kCopyUnits = 4 * kCopyThreads;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-// Whether the entries of a strided array, `row` elements each, lie apart: from the smallest stride up, each passes
-// all that the ones below it span.
-struct Axis {
-  int64_t n, stride;
-};
-bool lie_apart(int64_t row, std::initializer_list<Axis> axes) {
-  Axis a[3];
-  int m = 0;
-  for (const Axis& x : axes)
-    if (x.n > 1) a[m++] = x;
-  std::sort(a, a + m, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
-  for (int i = 0; i < m; ++i) {
-    if (a[i].stride < row) return false;
-    if (i + 1 < m) {                                   // row + (n - 1) * stride, which may pass 64 bits, within the next stride
-      if ((a[i + 1].stride - row) / a[i].stride < a[i].n - 1) return false;
-      row += (a[i].n - 1) * a[i].stride;
+// A block takes pieces of 16 KB: four 16-byte loads a thread in flight, then the stores. Bound by HBM.
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+  int n = *p.count;
+  if (n > p.capacity) {
+    n = p.capacity;
+    if (threadIdx.x == 0) set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
+  }
+  const int place_shift = p.lane_shift + p.c.page_shift, half = p.units >> 1;
+  for (int64_t piece = blockIdx.x; piece < (int64_t)n * p.pieces; piece += gridDim.x) {
+    const int move = (int)(piece / p.pieces), part = (int)(piece - (int64_t)move * p.pieces);
+    const int from = p.moves[2 * (int64_t)move], to = p.moves[2 * (int64_t)move + 1];
+    if ((uint32_t)from >= (uint32_t)p.c.pages || (uint32_t)to >= (uint32_t)p.c.pages) {
+      if (threadIdx.x == 0) set_status(p.c.status, CP_ERR_DEVICE_BOUNDS);
+      continue;
+    }
+    if (from == to) continue;
+    const int64_t there = (int64_t)(to - from) * p.c.page_b;
+    uint4 x[4];
+    uint8_t* at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int u = part * kCopyUnits + k * kCopyThreads + threadIdx.x;
+      const int is_v = u >= half, w = is_v ? u - half : u;
+      const int head = w >> place_shift, place = (w >> p.lane_shift) & ((1 << p.c.page_shift) - 1), l = w & ((1 << p.lane_shift) - 1);
+      at[k] = u < p.units ? (is_v ? p.c.v : p.c.k) + (int64_t)from * p.c.page_b + head * p.c.head_b + place * p.c.tok_b + l * 16 : nullptr;
+      if (at[k]) x[k] = *reinterpret_cast<const uint4*>(at[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (at[k]) *reinterpret_cast<uint4*>(at[k] + there) = x[k];
+    if (!p.c.ks || part) continue;
+    // the page's scales: the first block's
+    const int scales = p.c.heads << p.c.page_shift;
+    const int64_t s_from = (int64_t)from * p.c.sc_page, s_there = (int64_t)(to - from) * p.c.sc_page;
+    const int step = p.scale_vec ? 16 : 1;
+    for (int i = threadIdx.x * step; i < 2 * scales; i += kCopyThreads * step) {
+      const int is_v = i >= scales, w = is_v ? i - scales : i;
+      const int head = w >> p.c.page_shift, place = w & ((1 << p.c.page_shift) - 1);
+      uint8_t* a = (is_v ? p.c.vs : p.c.ks) + s_from + head * p.c.sc_head + place * p.c.sc_tok;
+      if (p.scale_vec) *reinterpret_cast<uint4*>(a + s_there) = *reinterpret_cast<const uint4*>(a);
+      else a[s_there] = *a;
     }
   }
-  return true;
 }
 
+// ------------------------------------------------------------------ checks
 int check_desc(const cp_cache_desc* in, cp_cache_desc* d) {
   if (!in || !in->k || !in->v) return CP_ERR_INVALID_ARG;
   *d = *in;
@@ -504,8 +528,6 @@ int check_attend(const cp_cache_desc& d, const BatchView& b, const cp_attend* a,
   return CP_OK;
 }
 
-int cuda_err(cudaError_t e) { return e == cudaSuccess ? CP_OK : CP_ERR_CUDA; }
-
 // Rows per block, a power of two: one until every SM has two blocks, then up to four, which share the look-ups.
 int rows_per_block(int rows) {
   int n = 1;
@@ -542,22 +564,11 @@ int cp_cache_create(const cp_cache_desc* desc, int device, cp_cache** out) {
   cp_cache_desc d;
   const int st = check_desc(desc, &d);
   if (st) return st;
-  int ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess || device < 0 || device >= ndev) return CP_ERR_UNSUPPORTED;
+  const int dev = check_device(device);
+  if (dev) return dev;
   DeviceGuard guard(device);
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess)
-    return CP_ERR_CUDA;
-  if (major != 10 || minor != 3) return CP_ERR_UNSUPPORTED;
-  for (const void* ptr : {(const void*)d.k, (const void*)d.v, (const void*)d.k_scale, (const void*)d.v_scale}) {
-    cudaPointerAttributes a{};
-    if (!ptr) continue;
-    if (cudaPointerGetAttributes(&a, ptr) != cudaSuccess || a.type != cudaMemoryTypeDevice || a.device != device) {
-      cudaGetLastError();
-      return CP_ERR_INVALID_ARG;
-    }
-  }
+  for (const void* ptr : {(const void*)d.k, (const void*)d.v, (const void*)d.k_scale, (const void*)d.v_scale})
+    if (ptr && !on_device(ptr, device)) return CP_ERR_INVALID_ARG;
   cp_cache* c = new (std::nothrow) cp_cache();
   if (!c) return CP_ERR_NOMEM;
   c->device = device;
@@ -655,6 +666,25 @@ int cp_cache_read(cp_cache* c, const cp_batch* batch, void* k_out, void* v_out, 
     if (e4m3) read_kernel<64, true><<<grid, kReadThreads, 0, s>>>(p);
     else read_kernel<64, false><<<grid, kReadThreads, 0, s>>>(p);
   }
+  return cuda_err(cudaGetLastError());
+}
+
+int cp_cache_copy(cp_cache* c, const int32_t* moves, int capacity, const int32_t* count, cp_stream_t stream) {
+  if (!c || !moves || !count || capacity < 1) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(c->device);
+  CopyParams p{};
+  p.c = c->view;
+  p.moves = moves;
+  p.count = count;
+  p.capacity = capacity;
+  const int unit = c->d.head_dim * (c->d.dtype == CP_CACHE_E4M3 ? 1 : 2) / 16;
+  while (1 << p.lane_shift < unit) ++p.lane_shift;
+  p.units = 2 * c->d.kv_heads * c->d.page_size * unit;
+  p.pieces = (p.units - 1) / kCopyUnits + 1;
+  const bool aligned = aligned16(p.c.ks) && aligned16(p.c.vs) && p.c.sc_head % 16 == 0 && p.c.sc_page % 16 == 0;
+  p.scale_vec = p.c.sc_tok == 1 && aligned;
+  const int64_t grid = std::min<int64_t>((int64_t)capacity * p.pieces, kSms * 8);
+  copy_kernel<<<(unsigned)grid, kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
   return cuda_err(cudaGetLastError());
 }
 

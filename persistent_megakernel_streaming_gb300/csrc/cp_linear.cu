@@ -1,0 +1,325 @@
+// cp_linear.cu -- projections of few rows with 4-bit weights: the C ABI (checks,
+// layout of the weights, launches) and the kernel for up to 16 rows.
+#include <cuda_runtime.h>
+
+#include <new>
+
+#include "cp.h"
+#include "cp_call.h"
+#include "cp_linear.cuh"
+
+using namespace cp;
+using namespace cp::linear;
+
+struct cp_linear {
+  int device = 0;
+  Weights w{};
+  void* memory = nullptr;
+};
+
+namespace {
+
+// ------------------------------------------------------------------ layout
+struct PackParams {
+  Weights w;
+  const uint8_t* q;
+  const uint16_t* scale;
+  const uint8_t* zero;
+  uint4* w_out;
+  uint32_t* scale_out;
+  uint16_t* zero_out;
+  int* bad;
+};
+
+__global__ void pack_kernel(const PackParams p) {
+  const Weights& w = p.w;
+  const int64_t lanes = (int64_t)w.tiles * w.blocks * 32, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < lanes; i += step) {
+    const int lane = (int)(i & 31), g = lane >> 2, c = lane & 3;
+    const int64_t rest = i >> 5;
+    const int b = (int)(rest % w.blocks), t = (int)(rest / w.blocks);
+    uint32_t out[4];
+    for (int j = 0; j < 4; ++j) {
+      out[j] = 0;
+      for (int a = 0; a < 4; ++a) {
+        const int row = row_of(w, t, g + (a & 1) * 8), k = b * kBlockK + 16 * c + 4 * j + (a >> 1) * 2;
+        if (row < 0 || k >= w.width) continue;
+        const uint32_t two = p.q[(int64_t)row * (w.width / 2) + k / 2];
+        out[j] |= (two & 15) << (4 * a) | (two >> 4) << (16 + 4 * a);
+      }
+    }
+    p.w_out[i] = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+  const int64_t metas = (int64_t)w.tiles * w.groups * 8;
+  const int held = w.width >> w.group_shift;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < metas; i += step) {
+    const int g = (int)(i & 7);
+    const int64_t rest = i >> 3;
+    const int grp = (int)(rest % w.groups), t = (int)(rest / w.groups);
+    uint32_t s = 0, z = 0;
+    for (int h = 0; h < 2; ++h) {
+      const int row = row_of(w, t, g + 8 * h);
+      if (row < 0 || grp >= held) continue;        // rows and inputs that are not there weigh nothing
+      const int64_t at = (int64_t)row * held + grp;
+      s |= (uint32_t)p.scale[at] << (16 * h);
+      if (p.zero) {
+        z |= (uint32_t)p.zero[at] << (8 * h);
+        if (p.zero[at] > 15) *p.bad = 1;
+      }
+    }
+    p.scale_out[i] = s;
+    if (p.zero) p.zero_out[i] = (uint16_t)z;
+  }
+}
+
+__global__ void unpack_kernel(const Weights w, uint16_t* out) {
+  const int64_t lanes = (int64_t)w.tiles * w.blocks * 32, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < lanes; i += step) {
+    const int lane = (int)(i & 31), g = lane >> 2, c = lane & 3;
+    const int64_t rest = i >> 5;
+    const int b = (int)(rest % w.blocks), t = (int)(rest / w.blocks);
+    const int64_t at = ((int64_t)t * w.groups + ((b * kBlockK + 16 * c) >> w.group_shift)) * 8 + g;
+    const Meta m = meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero);
+    const uint4 v = w.w[i];
+    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+    for (int j = 0; j < 4; ++j) {
+      uint32_t a[4];
+      widen(words[j], m, a);
+      for (int x = 0; x < 4; ++x) {
+        const int row = row_of(w, t, g + (x & 1) * 8), k = b * kBlockK + 16 * c + 4 * j + (x >> 1) * 2;
+        if (row < 0 || k >= w.width) continue;
+        out[(int64_t)row * w.width + k] = (uint16_t)a[x];
+        out[(int64_t)row * w.width + k + 1] = (uint16_t)(a[x] >> 16);
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------ few rows
+constexpr int kWarps = 8;
+
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <class T>
+__device__ __forceinline__ float load_out(const void* p, int64_t i);
+template <>
+__device__ __forceinline__ float load_out<float>(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+template <>
+__device__ __forceinline__ float load_out<__nv_bfloat16>(const void* p, int64_t i) {
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+// NT tiles of 8 rows of x; a block has two tiles of the weights, of a gated projection the gate's and the same of up,
+// its warps every eighth block of inputs.
+template <class T, int NT>
+__global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_constant__ ApplyParams p) {
+  __shared__ float part[kWarps][2 * kTileRows][8 * NT + 1];
+  const Weights& w = p.w;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int t0 = blockIdx.x * 2, row0 = blockIdx.y * 8 * NT;
+  float acc[2][NT][4] = {};
+  for (int b = warp; b < w.blocks; b += kWarps) {
+    uint4 x[NT][2];
+    const int k = b * kBlockK + 16 * c;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
+      const int r = row0 + n * 8 + g;
+      if (r < p.rows && k < w.width) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)r * p.x_row + k);
+        x[n][0] = src[0];
+        x[n][1] = src[1];
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint4 v = w.w[((int64_t)(t0 + t) * w.blocks + b) * 32 + lane];
+      const int64_t at = ((int64_t)(t0 + t) * w.groups + (k >> w.group_shift)) * 8 + g;
+      const Meta m = meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero);
+      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t a[4];
+        widen(words[j], m, a);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 y = x[n][j >> 1];
+          if (j & 1) mma(acc[t][n], a, y.z, y.w);
+          else mma(acc[t][n], a, y.x, y.y);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[warp][t * kTileRows + g + (i >> 1) * 8][n * 8 + 2 * c + (i & 1)] = acc[t][n][i];
+  __syncthreads();
+  const int per = w.gated ? kTileRows : 2 * kTileRows;
+  for (int i = threadIdx.x; i < per * 8 * NT; i += kWarps * 32) {
+    const int f = i % per, r = i / per;
+    const int n = blockIdx.x * per + f;
+    if (n >= w.outs || row0 + r >= p.rows) continue;
+    float y = 0.f, u = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) y += part[k][f][r];
+    if (w.gated) {
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k) u += part[k][kTileRows + f][r];
+      y = silu(y) * u;
+    }
+    if (p.add) y += load_out<T>(p.add, (row0 + r) * p.add_row + n);
+    store_out(static_cast<T*>(p.out) + (row0 + r) * p.out_row + n, y);
+  }
+}
+
+template <class T>
+cudaError_t launch_apply(const ApplyParams& p, cudaStream_t s) {
+  if (p.rows <= 8) {
+    few_rows_kernel<T, 1><<<dim3(p.w.tiles / 2, 1), kWarps * 32, 0, s>>>(p);
+  } else {
+    few_rows_kernel<T, 2><<<dim3(p.w.tiles / 2, (p.rows + 15) / 16), kWarps * 32, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ checks
+int check_desc(const cp_linear_desc* d, Weights* w) {
+  if (!d || !d->q || !d->scale || d->features < 1 || d->width < 1 || d->group < 1) return CP_ERR_INVALID_ARG;
+  if (d->group != 32 && d->group != 64 && d->group != 128) return CP_ERR_UNSUPPORTED;
+  if (d->width % d->group || (d->gated && d->features % 2)) return CP_ERR_INVALID_ARG;
+  if (d->width > 1 << 20 || d->features > 1 << 24) return CP_ERR_UNSUPPORTED;
+  w->features = d->features;
+  w->width = d->width;
+  w->group_shift = d->group == 32 ? 5 : d->group == 64 ? 6 : 7;
+  w->gated = d->gated != 0;
+  w->outs = d->gated ? d->features / 2 : d->features;
+  const int tiles = (w->outs + kTileRows - 1) / kTileRows * (d->gated ? 2 : 1);
+  w->tiles = (tiles + kPadTiles - 1) / kPadTiles * kPadTiles;
+  w->blocks = (d->width + kBlockK - 1) / kBlockK;
+  w->groups = (w->blocks * kBlockK + d->group - 1) / d->group;
+  return CP_OK;
+}
+
+int check_args(const Weights& w, const cp_linear_args* a, ApplyParams* p) {
+  if (!a || !a->x || !a->out || a->rows < 1) return CP_ERR_INVALID_ARG;
+  if (a->out_dtype != CP_OUT_BF16 && a->out_dtype != CP_OUT_F32) return CP_ERR_INVALID_ARG;
+  if (a->rows > 65535) return CP_ERR_UNSUPPORTED;
+  p->w = w;
+  p->x = static_cast<const uint16_t*>(a->x);
+  p->out = a->out;
+  p->add = a->add;
+  p->rows = a->rows;
+  p->x_row = a->x_stride ? a->x_stride : w.width;
+  p->out_row = a->out_stride ? a->out_stride : w.outs;
+  p->add_row = a->add_stride ? a->add_stride : w.outs;
+  if (p->x_row < 0 || p->out_row < 0 || p->add_row < 0) return CP_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 40;
+  if (p->x_row > most || p->out_row > most || p->add_row > most) return CP_ERR_UNSUPPORTED;
+  if (p->x_row % 8 || !aligned16(a->x)) return CP_ERR_UNSUPPORTED;
+  const uintptr_t es = a->out_dtype == CP_OUT_BF16 ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(a->out) % es || reinterpret_cast<uintptr_t>(a->add) % es) return CP_ERR_UNSUPPORTED;
+  if (!lie_apart(w.outs, {{a->rows, p->out_row}})) return CP_ERR_INVALID_ARG;
+  return CP_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+extern "C" {
+
+int cp_linear_check(const cp_linear_desc* desc, const cp_linear_args* args) {
+  Weights w{};
+  const int st = check_desc(desc, &w);
+  if (st || !args) return st;
+  ApplyParams p{};
+  return check_args(w, args, &p);
+}
+
+int cp_linear_create(const cp_linear_desc* desc, int device, cp_linear** out) {
+  if (!out) return CP_ERR_INVALID_ARG;
+  *out = nullptr;
+  PackParams p{};
+  Weights& w = p.w;
+  int st = check_desc(desc, &w);
+  if (st) return st;
+  if ((st = check_device(device))) return st;
+  DeviceGuard guard(device);
+  for (const void* ptr : {desc->q, desc->scale, desc->zero})
+    if (ptr && !on_device(ptr, device)) return CP_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(desc->scale) % 2) return CP_ERR_UNSUPPORTED;
+  cp_linear* l = new (std::nothrow) cp_linear();
+  if (!l) return CP_ERR_NOMEM;
+  l->device = device;
+  const size_t w_bytes = up256((size_t)w.tiles * w.blocks * 512), metas = (size_t)w.tiles * w.groups * 8;
+  const size_t zero_bytes = desc->zero ? up256(metas * 2) : 0;
+  if (cudaMalloc(&l->memory, w_bytes + up256(metas * 4) + zero_bytes + 256) != cudaSuccess) {
+    cudaGetLastError();
+    delete l;
+    return CP_ERR_NOMEM;
+  }
+  uint8_t* at = static_cast<uint8_t*>(l->memory);
+  p.w_out = reinterpret_cast<uint4*>(at);
+  p.scale_out = reinterpret_cast<uint32_t*>(at + w_bytes);
+  p.zero_out = desc->zero ? reinterpret_cast<uint16_t*>(at + w_bytes + up256(metas * 4)) : nullptr;
+  p.bad = reinterpret_cast<int*>(at + w_bytes + up256(metas * 4) + zero_bytes);
+  p.q = static_cast<const uint8_t*>(desc->q);
+  p.scale = static_cast<const uint16_t*>(desc->scale);
+  p.zero = static_cast<const uint8_t*>(desc->zero);
+  w.w = p.w_out;
+  w.scale = p.scale_out;
+  w.zero = p.zero_out;
+  l->w = w;
+  int bad = 0;
+  // what the caller's streams still write into the arrays is waited for
+  bool ok = cudaDeviceSynchronize() == cudaSuccess && cudaMemset(p.bad, 0, 4) == cudaSuccess;
+  if (ok) {
+    pack_kernel<<<1216, 256>>>(p);
+    ok = cudaGetLastError() == cudaSuccess && cudaMemcpy(&bad, p.bad, 4, cudaMemcpyDeviceToHost) == cudaSuccess;
+  }
+  if (!ok || bad) {
+    cp_linear_destroy(l);
+    return bad ? CP_ERR_INVALID_ARG : CP_ERR_CUDA;
+  }
+  *out = l;
+  return CP_OK;
+}
+
+void cp_linear_destroy(cp_linear* l) {
+  if (!l) return;
+  {
+    DeviceGuard g(l->device);
+    cudaDeviceSynchronize();
+    cudaFree(l->memory);
+  }
+  delete l;
+}
+
+int cp_linear_apply(cp_linear* l, const cp_linear_args* args, cp_stream_t stream) {
+  if (!l) return CP_ERR_INVALID_ARG;
+  ApplyParams p{};
+  const int st = check_args(l->w, args, &p);
+  if (st) return st;
+  DeviceGuard g(l->device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_err(args->out_dtype == CP_OUT_BF16 ? launch_apply<__nv_bfloat16>(p, s) : launch_apply<float>(p, s));
+}
+
+int cp_linear_unpack(cp_linear* l, void* out, cp_stream_t stream) {
+  if (!l || !out) return CP_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(out) % 2) return CP_ERR_UNSUPPORTED;
+  DeviceGuard g(l->device);
+  unpack_kernel<<<1216, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(l->w, static_cast<uint16_t*>(out));
+  return cuda_err(cudaGetLastError());
+}
+
+}  // extern "C"

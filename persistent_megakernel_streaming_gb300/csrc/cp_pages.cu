@@ -1,0 +1,496 @@
+// cp_pages.cu -- which pages of a cache hold what: the C ABI (checks and
+// launches) and the kernels that fork, grow, trim and compact sequences.
+//
+// All of it is whole numbers in an order that the calls define, so the results
+// do not depend on how blocks are scheduled: counts are only added to, and
+// whatever has an order (which free page goes to whom) comes from prefix sums.
+#include <cuda_runtime.h>
+
+#include <new>
+
+#include "cp.h"
+#include "cp_call.h"
+#include "cp_ptx.cuh"
+
+using namespace cp;
+
+namespace {
+
+// What a sequence grows by.
+struct Plan {
+  int len;           // new length, or -1: it stays as it is
+  int had, want;     // pages
+  int last;          // a shared page that it grows into, or -1
+  int copies;        // whether it takes a page of its own for that
+  int base, move;    // its first new page's place in the list, its place among the moves
+};
+
+struct PagesView {
+  int32_t* refs;
+  int32_t* table;
+  int32_t* length;
+  int64_t stride;
+  int pages, sequences, width, shift;   // page size 1 << shift
+  int32_t* status;
+  // scratch
+  int32_t* list;     // [pages] free pages in order
+  int32_t* map;      // [pages] where a page moves, or -1 (from page *live on)
+  int32_t* tail;     // [pages] sequences that grow into a shared page; zeros between calls
+  int32_t* keeper;   // [pages] the last of them, plus one; zeros between calls
+  Plan* plan;        // [sequences]
+  int64_t* sums;     // [4][kMostBlocks]
+  int32_t* live;     // [1] pages that hold something
+};
+
+constexpr int kMostBlocks = 8;
+constexpr int64_t kLow = ((int64_t)1 << 40) - 1;   // two counts in one sum
+
+}  // namespace
+
+struct cp_pages {
+  int device = 0;
+  PagesView view{};
+  void* memory = nullptr;
+};
+
+namespace {
+
+__device__ __forceinline__ void set_status(const PagesView& v) { atomicCAS(v.status, 0, (int)CP_ERR_DEVICE_BOUNDS); }
+
+// Positions of a sequence; ones that its table cannot hold count as none.
+__device__ __forceinline__ int length_of(const PagesView& v, int i) {
+  const int l = v.length[i];
+  if (l >= 0 && ((int64_t)l + (1 << v.shift) - 1) >> v.shift <= v.width) return l;
+  set_status(v);
+  return 0;
+}
+__device__ __forceinline__ int pages_for(const PagesView& v, int64_t length) {
+  return (int)((length + (1 << v.shift) - 1) >> v.shift);
+}
+__device__ __forceinline__ bool in_pool(const PagesView& v, int page) { return (uint32_t)page < (uint32_t)v.pages; }
+
+// ------------------------------------------------------------------ fork
+// A block a pair. Whether pairs get in each other's way is looked up among all of them by every block: no order
+// between blocks is needed then.
+__global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int32_t* src, const int32_t* dst, int n) {
+  const int pair = blockIdx.x, s = src[pair], d = dst[pair];
+  bool bad = (uint32_t)s >= (uint32_t)v.sequences || (uint32_t)d >= (uint32_t)v.sequences;
+  for (int i = threadIdx.x; i < n; i += 256) bad |= (i != pair && dst[i] == d) || src[i] == d;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(v);
+    return;
+  }
+  const int len = length_of(v, s), held = pages_for(v, len);
+  if (v.length[d] != 0) {                // the same for all threads: nobody writes it before the barrier
+    if (threadIdx.x == 0) set_status(v);
+    return;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) v.length[d] = len;
+  const int32_t* from = v.table + s * v.stride;
+  int32_t* to = v.table + d * v.stride;
+  for (int i = threadIdx.x; i < held; i += 256) {
+    const int page = from[i];
+    to[i] = page;
+    if (in_pool(v, page)) atomicAdd(v.refs + page, 1);
+    else set_status(v);
+  }
+}
+
+// ------------------------------------------------------------------ trim
+__global__ void __launch_bounds__(128) trim_kernel(const PagesView v, const int32_t* keep) {
+  const int i = blockIdx.x;
+  const int len = length_of(v, i);
+  int want = keep[i];
+  if (want < 0) {
+    set_status(v);
+    return;
+  }
+  if (want >= len) return;
+  __syncthreads();                       // every thread has read the length
+  const int held = pages_for(v, len);
+  if (threadIdx.x == 0) v.length[i] = want;
+  int32_t* row = v.table + i * v.stride;
+  for (int k = pages_for(v, want) + threadIdx.x; k < held; k += 128) {
+    const int page = row[k];
+    row[k] = -1;
+    if (!in_pool(v, page)) {
+      set_status(v);
+    } else if (atomicSub(v.refs + page, 1) <= 0) {
+      atomicAdd(v.refs + page, 1);       // nobody held it
+      set_status(v);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ one cluster
+// Growing and compacting need prefix sums over all sequences and all pages: one cluster of up to 8 blocks does them, a
+// contiguous share of both to each block, and meets at cluster barriers, which order its memory accesses too.
+constexpr int kThreads = 1024;
+
+// Exclusive prefix of x over the block's threads; *sum: of all. Synchronises.
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* sum) {
+  __shared__ int64_t warps[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  __syncthreads();
+  if (lane == 31) warps[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t w = warps[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += up;
+    }
+    warps[lane] = w;
+  }
+  __syncthreads();
+  *sum = warps[31];
+  return inc - x + (warp ? warps[warp - 1] : 0);
+}
+// The block's share of n things, in steps of 4.
+struct Share {
+  int begin, end;
+};
+__device__ __forceinline__ Share share_of(int n) {
+  const int64_t each = (((int64_t)n + gridDim.x - 1) / gridDim.x + 3) & ~3ll;
+  return {(int)min((int64_t)n, each * blockIdx.x), (int)min((int64_t)n, each * (blockIdx.x + 1))};
+}
+// The sums of the blocks before this one, and of all, of what each has left in row `row`.
+__device__ __forceinline__ int64_t before_me(const PagesView& v, int row, int64_t* all) {
+  int64_t mine = 0, sum = 0;
+  for (int k = 0; k < (int)gridDim.x; ++k) {
+    const int64_t x = __ldcg(v.sums + row * kMostBlocks + k);
+    if (k < (int)blockIdx.x) mine += x;
+    sum += x;
+  }
+  *all = sum;
+  return mine;
+}
+// Which of pages p .. p + 3 below `end` satisfy a predicate of (page, count): a bit each.
+template <class F>
+__device__ __forceinline__ uint32_t four(const PagesView& v, int p, int end, F f) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (p + k < end && f(p + k, v.refs[p + k])) bits |= 1u << k;
+  return bits;
+}
+template <class F>
+__device__ __forceinline__ int64_t count_pages(const PagesView& v, Share pages, F f) {
+  int64_t n = 0, sum;
+  for (int p = pages.begin + threadIdx.x * 4; p < pages.end; p += kThreads * 4) n += __popc(four(v, p, pages.end, f));
+  block_scan(n, &sum);
+  return sum;
+}
+// For each such page of the share in ascending order, act(its rank, counted from `rank` on, page).
+template <class F, class A>
+__device__ __forceinline__ void each_page(const PagesView& v, Share pages, int64_t rank, F f, A act) {
+  for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads * 4) {
+    const int p = p0 + threadIdx.x * 4;
+    const uint32_t bits = four(v, p, pages.end, f);
+    int64_t sum, at = rank + block_scan(__popc(bits), &sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (bits >> k & 1) act(at++, p + k);
+    rank += sum;
+  }
+}
+
+// ------------------------------------------------------------------ grow
+__device__ __forceinline__ Plan ask_of(const PagesView& v, const int32_t* add, int i) {
+  Plan a{};
+  const int len = length_of(v, i), more = add[i];
+  a.len = a.last = -1;
+  a.had = a.want = pages_for(v, len);
+  if (more == 0 || v.length[i] != len) return a;
+  const int64_t to = (int64_t)len + more;
+  if (more < 0 || to > INT32_MAX || (to + (1 << v.shift) - 1) >> v.shift > v.width) {
+    set_status(v);
+    return a;
+  }
+  if (len & ((1 << v.shift) - 1)) {
+    const int page = v.table[i * v.stride + a.had - 1];
+    if (!in_pool(v, page)) {
+      set_status(v);
+      return a;
+    }
+    const int refs = v.refs[page];
+    if (refs < 1) {
+      set_status(v);
+      return a;
+    }
+    if (refs > 1) a.last = page;
+  }
+  a.len = (int)to;
+  a.want = pages_for(v, to);
+  return a;
+}
+
+__global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const int32_t* add, int32_t* moves, int32_t* count) {
+  const Share pages = share_of(v.pages), seqs = share_of(v.sequences);
+  const int tid = threadIdx.x;
+  auto is_free = [](int, int refs) { return refs == 0; };
+  for (int i = seqs.begin + tid; i < seqs.end; i += kThreads) {
+    const Plan a = ask_of(v, add, i);
+    v.plan[i] = a;
+    if (a.last >= 0) {
+      atomicAdd(v.tail + a.last, 1);
+      atomicMax(v.keeper + a.last, i + 1);
+    }
+  }
+  const int64_t free_here = count_pages(v, pages, is_free);
+  if (tid == 0) v.sums[blockIdx.x] = free_here;
+  ptx::cluster_sync_all();
+  // all that grow into a shared page take one of their own, but the last of them if nobody else holds it
+  int64_t fresh_here = 0, moved_here = 0;
+  for (int i0 = seqs.begin; i0 < seqs.end; i0 += kThreads) {
+    const int i = i0 + tid;
+    Plan a{};
+    if (i < seqs.end) {
+      a = v.plan[i];
+      if (a.last >= 0) a.copies = !(__ldcg(v.tail + a.last) >= v.refs[a.last] && __ldcg(v.keeper + a.last) == i + 1);
+    }
+    int64_t sum;
+    const int64_t fresh = a.want - a.had + a.copies;
+    const int64_t at = block_scan((int64_t)a.copies << 40 | fresh, &sum);
+    if (i < seqs.end) {
+      v.plan[i].copies = a.copies;
+      v.plan[i].base = (int)min(fresh_here + (at & kLow), (int64_t)INT32_MAX);
+      v.plan[i].move = (int)(moved_here + (at >> 40));
+    }
+    fresh_here += sum & kLow;
+    moved_here += sum >> 40;
+  }
+  if (tid == 0) {
+    v.sums[kMostBlocks + blockIdx.x] = fresh_here;
+    v.sums[2 * kMostBlocks + blockIdx.x] = moved_here;
+  }
+  ptx::cluster_sync_all();
+  int64_t free_all, fresh_all, moved_all;
+  const int64_t free0 = before_me(v, 0, &free_all), fresh0 = before_me(v, 1, &fresh_all), moved0 = before_me(v, 2, &moved_all);
+  const bool enough = free_all >= fresh_all;
+  if (blockIdx.x == 0 && tid == 0) *count = enough ? (int)moved_all : -(int)min(fresh_all - free_all, (int64_t)INT32_MAX);
+  if (enough && free0 < fresh_all)
+    each_page(v, pages, free0, is_free, [&](int64_t at, int page) {
+      if (at < fresh_all) v.list[at] = page;
+    });
+  ptx::cluster_sync_all();
+  // a warp a sequence
+  const int lane = tid & 31;
+  for (int i = seqs.begin + (tid >> 5); i < seqs.end; i += kThreads / 32) {
+    const Plan a = v.plan[i];
+    if (a.last >= 0 && lane == 0) v.tail[a.last] = v.keeper[a.last] = 0;
+    if (!enough || a.len < 0) continue;
+    const int64_t base = fresh0 + a.base;
+    int32_t* row = v.table + i * v.stride;
+    if (lane == 0) {
+      v.length[i] = a.len;
+      if (a.copies) {
+        const int page = __ldcg(v.list + base);
+        const int64_t m = moved0 + a.move;
+        moves[2 * m] = a.last;
+        moves[2 * m + 1] = page;
+        row[a.had - 1] = page;
+        v.refs[page] = 1;
+        atomicSub(v.refs + a.last, 1);
+      }
+    }
+    for (int k = lane; k < a.want - a.had; k += 32) {
+      const int page = __ldcg(v.list + base + a.copies + k);
+      row[a.had + k] = page;
+      v.refs[page] = 1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ compact
+__global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, int32_t* moves, int32_t* count) {
+  const Share pages = share_of(v.pages);
+  const int tid = threadIdx.x;
+  const int64_t live_here = count_pages(v, pages, [](int, int refs) { return refs != 0; });
+  if (tid == 0) v.sums[blockIdx.x] = live_here;
+  ptx::cluster_sync_all();
+  int64_t all, holes, moving;
+  before_me(v, 0, &all);
+  const int n = (int)all;
+  auto is_hole = [n](int p, int refs) { return p < n && refs == 0; };
+  auto moves_on = [n](int p, int refs) { return p >= n && refs != 0; };
+  const int64_t holes_here = count_pages(v, pages, is_hole), moving_here = count_pages(v, pages, moves_on);
+  if (tid == 0) {
+    v.sums[kMostBlocks + blockIdx.x] = holes_here;
+    v.sums[2 * kMostBlocks + blockIdx.x] = moving_here;
+  }
+  ptx::cluster_sync_all();
+  const int64_t hole0 = before_me(v, 1, &holes), moving0 = before_me(v, 2, &moving);
+  each_page(v, pages, hole0, is_hole, [&](int64_t at, int page) { v.list[at] = page; });
+  for (int p = max(pages.begin, n) + tid; p < pages.end; p += kThreads) v.map[p] = -1;
+  if (blockIdx.x == 0 && tid == 0) {
+    *count = (int)moving;
+    *v.live = n;
+  }
+  ptx::cluster_sync_all();
+  each_page(v, pages, moving0, moves_on, [&](int64_t at, int page) {
+    const int to = __ldcg(v.list + at);
+    moves[2 * at] = page;
+    moves[2 * at + 1] = to;
+    v.map[page] = to;
+    v.refs[to] = v.refs[page];
+    v.refs[page] = 0;
+  });
+}
+
+// The tables, after it: a block a sequence.
+__global__ void __launch_bounds__(128) remap_kernel(const PagesView v) {
+  const int i = blockIdx.x, held = pages_for(v, length_of(v, i)), n = *v.live;
+  int32_t* row = v.table + i * v.stride;
+  for (int k = threadIdx.x; k < held; k += 128) {
+    const int page = row[k];
+    if (in_pool(v, page) && page < n) continue;
+    const int to = in_pool(v, page) ? v.map[page] : -1;
+    if (to >= 0) row[k] = to;
+    else set_status(v);
+  }
+}
+
+// ------------------------------------------------------------------ checks
+int check_desc(const cp_pages_desc* d, PagesView* v) {
+  if (!d || !d->refs || !d->page_table || !d->length) return CP_ERR_INVALID_ARG;
+  if (d->pages < 1 || d->page_size < 1 || d->sequences < 1 || d->table_width < 1 || d->table_stride < 0) return CP_ERR_INVALID_ARG;
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return CP_ERR_UNSUPPORTED;
+  if (d->pages > 1 << 30 || d->sequences > 65535) return CP_ERR_UNSUPPORTED;
+  if (d->table_stride && d->sequences > 1 && d->table_stride < d->table_width) return CP_ERR_INVALID_ARG;
+  v->refs = d->refs;
+  v->table = d->page_table;
+  v->length = d->length;
+  v->stride = d->table_stride ? d->table_stride : d->table_width;
+  v->pages = d->pages;
+  v->sequences = d->sequences;
+  v->width = d->table_width;
+  v->shift = d->page_size == 16 ? 4 : d->page_size == 32 ? 5 : d->page_size == 64 ? 6 : 7;
+  return CP_OK;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Blocks of the one cluster.
+int blocks_for(const PagesView& v) {
+  int n = 1;
+  while (n < kMostBlocks && (v.pages > n * 4 * kThreads || v.sequences > n * kThreads)) n *= 2;
+  return n;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cp_pages_check(const cp_pages_desc* desc) {
+  PagesView v{};
+  return check_desc(desc, &v);
+}
+
+int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out) {
+  if (!out) return CP_ERR_INVALID_ARG;
+  *out = nullptr;
+  PagesView v{};
+  int st = check_desc(desc, &v);
+  if (st) return st;
+  if ((st = check_device(device))) return st;
+  DeviceGuard guard(device);
+  for (const void* ptr : {v.refs, v.table, v.length})
+    if (!on_device(ptr, device)) return CP_ERR_INVALID_ARG;
+  cp_pages* p = new (std::nothrow) cp_pages();
+  if (!p) return CP_ERR_NOMEM;
+  p->device = device;
+  const size_t each = up256((size_t)v.pages * 4), plans = up256((size_t)v.sequences * sizeof(Plan));
+  const size_t bytes = 4 * each + plans + 512;
+  if (cudaMalloc(&p->memory, bytes) != cudaSuccess) {
+    cudaGetLastError();
+    delete p;
+    return CP_ERR_NOMEM;
+  }
+  uint8_t* at = static_cast<uint8_t*>(p->memory);
+  v.list = reinterpret_cast<int32_t*>(at);
+  v.map = reinterpret_cast<int32_t*>(at + each);
+  v.tail = reinterpret_cast<int32_t*>(at + 2 * each);
+  v.keeper = reinterpret_cast<int32_t*>(at + 3 * each);
+  v.plan = reinterpret_cast<Plan*>(at + 4 * each);
+  v.sums = reinterpret_cast<int64_t*>(at + 4 * each + plans);
+  v.live = reinterpret_cast<int32_t*>(at + 4 * each + plans + 256);
+  v.status = v.live + 1;
+  p->view = v;
+  if (cudaMemset(p->memory, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    cp_pages_destroy(p);
+    return CP_ERR_CUDA;
+  }
+  *out = p;
+  return CP_OK;
+}
+
+void cp_pages_destroy(cp_pages* p) {
+  if (!p) return;
+  {
+    DeviceGuard g(p->device);
+    cudaDeviceSynchronize();
+    cudaFree(p->memory);
+  }
+  delete p;
+}
+
+int cp_pages_status(cp_pages* p) {
+  if (!p) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(p->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return CP_ERR_CUDA;
+  int32_t v = 0;
+  if (cudaMemcpy(&v, p->view.status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return CP_ERR_CUDA;
+  return v;
+}
+
+int cp_pages_clear_status(cp_pages* p) {
+  if (!p) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(p->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return CP_ERR_CUDA;
+  if (cudaMemset(p->view.status, 0, 4) != cudaSuccess) return CP_ERR_CUDA;
+  return cuda_err(cudaDeviceSynchronize());
+}
+
+int cp_pages_fork(cp_pages* p, const int32_t* src, const int32_t* dst, int n, cp_stream_t stream) {
+  if (!p || !src || !dst || n < 1 || n > p->view.sequences) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(p->device);
+  fork_kernel<<<n, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p->view, src, dst, n);
+  return cuda_err(cudaGetLastError());
+}
+
+int cp_pages_trim(cp_pages* p, const int32_t* keep, cp_stream_t stream) {
+  if (!p || !keep) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(p->device);
+  trim_kernel<<<p->view.sequences, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p->view, keep);
+  return cuda_err(cudaGetLastError());
+}
+
+int cp_pages_grow(cp_pages* p, const int32_t* add, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream) {
+  if (!p || !add || !moves || !count || capacity < p->view.sequences) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(p->device);
+  const int n = blocks_for(p->view);
+  return cuda_err(launch_as(grow_kernel, dim3(n), n, 1, false, kThreads, 0, reinterpret_cast<cudaStream_t>(stream), p->view, add,
+                            moves, count));
+}
+
+int cp_pages_compact(cp_pages* p, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream) {
+  if (!p || !moves || !count || capacity < p->view.pages / 2) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(p->device);
+  const int n = blocks_for(p->view);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_as(compact_kernel, dim3(n), n, 1, false, kThreads, 0, s, p->view, moves, count);
+  if (e != cudaSuccess) return CP_ERR_CUDA;
+  remap_kernel<<<p->view.sequences, 128, 0, s>>>(p->view);
+  return cuda_err(cudaGetLastError());
+}
+
+}  // extern "C"
