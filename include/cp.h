@@ -711,8 +711,8 @@ typedef struct cp_verify_args {
  * u_token times the sum. Greedy sequences take d if it is the target's
  * largest logit (the lowest index of equal ones), and then that token.
  * A logit is times the fp32 1 / temperature; probabilities are fp32 numbers
- * and each row's sums more exact than 2^-40, so that the token drawn is the
- * same wherever they are computed so. A NaN or -infinite logit has no
+ * and each row's sums are kept in twice fp32's bits, so that the token drawn is
+ * the one that 64-bit sums of the same numbers give. A NaN or -infinite logit has no
  * probability, +infinite ones share it all. A drafted token outside the
  * vocabulary is not taken. A row without any probability (all its logits
  * masked) takes no token; if one is to be drawn there the token is -1. Should

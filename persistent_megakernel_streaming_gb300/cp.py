@@ -349,7 +349,7 @@ def _workspace(device, size: int, stream):
 
 def _array(t, what: str, dtype, shape, index: int) -> int:
     """Address of a contiguous device array of that type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{what}: {dtype} {list(shape)}, contiguous, on cuda:{index}; got {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -709,6 +709,7 @@ class Linear:
 
 
 _verify_needs: dict = {}
+_verify_dtypes: dict = {}
 
 
 def verify_workspace_bytes(sequences: int, rows: int, vocab: int) -> int:
@@ -735,30 +736,37 @@ def verify(logits, draft, start, u_accept, u_token, temperature, accepted, token
     ``accepted`` and ``token`` int32 [sequences]. Without a ``workspace`` (device bytes, see verify_workspace_bytes) one
     is taken from torch's allocator for this call."""
     import torch
-    index = logits.get_device()
-    if logits.dim() != 2 or index < 0 or logits.dtype not in (torch.float32, torch.bfloat16):
+    if not _verify_dtypes:
+        _verify_dtypes.update({torch.float32: 0, torch.bfloat16: 1})
+    f32, i32, index = torch.float32, torch.int32, logits.get_device()
+    dtype, shape = logits.dtype, logits.shape
+    kind = _verify_dtypes.get(dtype)
+    if kind is None or index < 0 or len(shape) != 2:
         raise ValueError("logits: bf16 or fp32 [rows][vocab] on a GPU")
-    rows, vocab = logits.shape
-    n = accepted.numel()
-    strides = [0, 0]
-    for k, t in enumerate((logits, draft_logits)):
-        if t is not None:
-            if t.dtype != logits.dtype or t.shape != logits.shape or t.get_device() != index or vocab > 1 and t.stride(1) != 1:
-                raise ValueError("logits, draft_logits: of one type, shape and device, the last axis contiguous")
-            strides[k] = _stride(t, 0)
-    need = verify_workspace_bytes(n, rows, vocab)
-    f32, i32 = torch.float32, torch.int32
-    a = VerifyArgs(n, rows, vocab, int(logits.dtype == torch.bfloat16), _array(start, "start", i32, (n + 1,), index), logits.data_ptr(),
-                   strides[0], _ptr(draft_logits) or None, strides[1], _array(draft, "draft", i32, (rows,), index),
-                   _array(temperature, "temperature", f32, (n,), index), _array(u_accept, "u_accept", f32, (rows,), index),
-                   _array(u_token, "u_token", f32, (n,), index), _array(accepted, "accepted", i32, (n,), index),
-                   _array(token, "token", i32, (n,), index), None if prob is None else _array(prob, "prob", f32, (rows,), index))
+    rows, vocab = shape
+    by_row, by_seq = (rows,), (accepted.numel(),)
+    stride, draft_at, draft_stride = _stride(logits, 0), None, 0
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("logits: the last axis contiguous")
+    if draft_logits is not None:
+        if draft_logits.dtype is not dtype or draft_logits.shape != shape or draft_logits.get_device() != index or \
+                vocab > 1 and draft_logits.stride(1) != 1:
+            raise ValueError("draft_logits: of the logits' type, shape and device, the last axis contiguous")
+        draft_at, draft_stride = draft_logits.data_ptr(), _stride(draft_logits, 0)
+    n = by_seq[0]
+    need = _verify_needs.get((n, rows, vocab)) or verify_workspace_bytes(n, rows, vocab)
+    a = VerifyArgs(n, rows, vocab, kind, _array(start, "start", i32, (n + 1,), index), logits.data_ptr(), stride, draft_at, draft_stride,
+                   _array(draft, "draft", i32, by_row, index), _array(temperature, "temperature", f32, by_seq, index),
+                   _array(u_accept, "u_accept", f32, by_row, index), _array(u_token, "u_token", f32, by_seq, index),
+                   _array(accepted, "accepted", i32, by_seq, index), _array(token, "token", i32, by_seq, index),
+                   None if prob is None else _array(prob, "prob", f32, by_row, index))
     if workspace is None:
-        workspace = _workspace(logits.device, need, stream)
+        workspace, size = _workspace(logits.device, need, stream), need
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace: contiguous, on the logits' device")
-    code = lib().cp_verify(C.byref(a), index, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           _stream_on(index, stream))
+    else:
+        size = workspace.numel() * workspace.element_size()
+    code = lib().cp_verify(C.byref(a), index, workspace.data_ptr(), size, _stream_on(index, stream))
     if code:
         raise CPError(code, "cp_verify")
 

@@ -1,17 +1,20 @@
 // cp_verify.cu -- verification of drafted tokens against the target's logits.
 //
 // Two launches. The first reads every logit once and leaves the maximum and the
-// sum of exponentials of each piece of a row. The second, for each sequence,
-// joins them, settles which drafted tokens are taken, and draws the token
-// behind them from one row: there it sums again, so exactly that the draw
-// does not depend on the order of the sums (below).
+// sum of exponentials of each piece of a row. The second, a cluster for each
+// sequence, joins them, settles which drafted tokens are taken, and draws the
+// token behind them from one row: there it sums again, in 64-bit fixed point,
+// so that the draw does not depend on the order of the sums.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
+#include <cstring>
 
 #include "cp.h"
 #include "cp_call.h"
+#include "cp_ptx.cuh"
 
 using namespace cp;
 
@@ -23,9 +26,11 @@ struct Piece {
   int arg, pad;
 };
 
-constexpr int kPiece = 8192;           // logits of a row that a block takes
-constexpr int kStatThreads = 256;
-constexpr int kTokenThreads = 1024;
+constexpr int kStatThreads = 256, kPer = 32;
+constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block takes
+constexpr int kTokenThreads = 512, kTokenWarps = kTokenThreads / 32;
+constexpr int kRowsKept = 32;                    // rows of a sequence whose pieces are joined once
+constexpr int kMostCluster = 16;
 
 struct VerifyParams {
   const int32_t* start;
@@ -41,40 +46,53 @@ struct VerifyParams {
   float* prob;
   Piece* pieces;                       // [2][rows][splits]: the target's, the draft's
   int n, rows, vocab, splits;
+  int cluster, chunk;                  // blocks a sequence, logits a block
+  int z_bits;                          // of the fixed point of their sums
 };
 
 // Scaled logits are finite: NaN and -infinity become the lowest number, whose exponential next to any other is 0; a
 // row whose largest is that has no probabilities.
 constexpr float kLowest = -FLT_MAX;
+constexpr float kLog2e = 1.44269504f;
 __device__ __forceinline__ float scaled(float l, float by) { return fminf(fmaxf(__fmul_rn(l, by), kLowest), FLT_MAX); }
 __device__ __forceinline__ float scale_of(float temperature) {
   return temperature > 0.f ? fminf(__fdiv_rn(1.f, temperature), FLT_MAX) : 1.f;
 }
 __device__ __forceinline__ float exp_from(float x, float m) { return expf(__fsub_rn(x, m)); }
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// One piece out of the warp's: the largest first, so that each lane's sum is scaled once.
+__device__ __forceinline__ Piece join_warp(const Piece& a) {
+  Piece r;
+  r.m = warp_max(a.m);
+  r.s = warp_sum(a.s * expf(a.m - r.m));
+  r.arg = __reduce_min_sync(0xffffffffu, a.m == r.m ? a.arg : INT32_MAX);
+  r.pad = 0;
+  return r;
+}
 
 __device__ __forceinline__ float value(const float* p) { return *p; }
 __device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// Eight logits (16-byte aligned), and calls of f(x, index) for all of [begin, end) of a row, in steps of the calling
-// group's `threads`: eight at a time where they are aligned.
-__device__ __forceinline__ void load8(const float* p, float* x) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* x) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-
-__device__ __forceinline__ void join(float* m, float* s, float m2, float s2) {
-  const float top = fmaxf(*m, m2);
-  *s = *s * expf(*m - top) + s2 * expf(m2 - top);
-  *m = top;
+__device__ __forceinline__ void join(Piece* a, const Piece& b) {
+  if (b.m > a->m || (b.m == a->m && b.arg < a->arg)) a->arg = b.arg;
+  const float top = fmaxf(a->m, b.m);
+  a->s = a->s * expf(a->m - top) + b.s * expf(b.m - top);
+  a->m = top;
 }
 
 // The sequence that row r belongs to, by one warp; n: none.
@@ -90,13 +108,52 @@ __device__ __forceinline__ int sequence_of(const VerifyParams& p, int r) {
   return seq;
 }
 
+// A thread's logits of a piece, in registers: 16 bytes at a time from a 16-byte boundary on, so that `skew` elements
+// in front of the row may belong to the first; what is not the row's is minus infinity.
 template <class T>
-__global__ void __launch_bounds__(kStatThreads) stats_kernel(const __grid_constant__ VerifyParams p) {
+struct Loads {
+  static constexpr int kVec = 16 / sizeof(T), kVecs = kPer / kVec;
+  uint4 raw[kVecs];
+  __device__ __forceinline__ static int index(int part, int skew, int v) {
+    return part * kPiece + (v * kStatThreads + (int)threadIdx.x) * kVec - skew;
+  }
+  __device__ __forceinline__ void load(const T* row, int vocab, int part, int skew) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = index(part, skew, v);
+      raw[v] = sizeof(T) == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
+                              : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+      if (i >= 0 && i + kVec <= vocab) {
+        raw[v] = *reinterpret_cast<const uint4*>(row + i);
+      } else if (i + kVec > 0 && i < vocab) {
+        T x[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) x[k] = i + k >= 0 && i + k < vocab ? row[i + k] : T(-INFINITY);
+        memcpy(&raw[v], x, 16);
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int v, int k) const {
+    const uint32_t w[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
+    if (sizeof(T) == 4) return __uint_as_float(w[k & 3]);
+    return __uint_as_float(k & 1 ? w[(k >> 1) & 3] & 0xffff0000u : w[(k >> 1) & 3] << 16);
+  }
+};
+
+// Bound by HBM. A thread holds its 32 logits, so that their maximum comes first and nothing is rescaled; an exponential
+// is one multiplication, one fused one, and ex2. Where NaN or infinities spoil that, the piece is done again with
+// clamped logits.
+template <class T>
+__global__ void __launch_bounds__(kStatThreads, 4) stats_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ int own;
-  __shared__ float ms[8], ss[8];
-  __shared__ int as[8];
+  __shared__ Piece warps[kStatThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.x / p.splits, part = blockIdx.x % p.splits, is_draft = blockIdx.y;
+  const T* row = is_draft ? static_cast<const T*>(p.draft_logits) + r * p.draft_row : static_cast<const T*>(p.logits) + r * p.row;
+  const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  ptx::pdl_trigger();
+  Loads<T> x;
+  if (!is_draft) x.load(row, p.vocab, part, skew);                 // on their way while the row's sequence is looked up
   if (warp == 0) {
     const int seq = sequence_of(p, r);
     if (lane == 0) own = seq;
@@ -106,95 +163,83 @@ __global__ void __launch_bounds__(kStatThreads) stats_kernel(const __grid_consta
   if (seq >= p.n || p.start[seq] > r) return;                      // nobody's
   const float heat = p.temperature[seq];
   const bool greedy = !(heat > 0.f);
-  if (is_draft && (greedy || r == p.start[seq + 1] - 1)) return;   // not asked for
+  if (is_draft) {
+    if (greedy || r == p.start[seq + 1] - 1) return;               // not asked for
+    x.load(row, p.vocab, part, skew);
+  }
   const float by = scale_of(heat);
-  const T* row = is_draft ? static_cast<const T*>(p.draft_logits) + r * p.draft_row : static_cast<const T*>(p.logits) + r * p.row;
-  const int begin = part * kPiece, end = min(begin + kPiece, p.vocab);
-  float m = kLowest, s = 0.f;
-  int arg = INT32_MAX;
-  // what lies in front of a 16-byte boundary, eight at a time behind it, and the rest
-  const int skew = (int)((reinterpret_cast<uintptr_t>(row + begin) & 15) / sizeof(T));
-  const int head = min(begin + (skew ? (int)(16 / sizeof(T)) - skew : 0), end), body = head + (end - head) / 8 * 8;
-  for (int i = head + threadIdx.x * 8; i < body; i += kStatThreads * 8) {
-    float x[8];
-    load8(row + i, x);
-    float top = kLowest;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[k] = scaled(x[k], by);
-      top = fmaxf(top, x[k]);
-    }
-    if (top > m || i == head + (int)threadIdx.x * 8) {
-      if (greedy && (top > m || arg == INT32_MAX)) {
-#pragma unroll
-        for (int k = 7; k >= 0; --k) arg = x[k] == top ? i + k : arg;
-      }
-      s *= expf(m - top);
-      m = top;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s += exp_from(x[k], m);
-  }
-  for (int i = threadIdx.x < (unsigned)(head - begin) ? begin + (int)threadIdx.x : body + (int)threadIdx.x - (head - begin); i < end;
-       i = i < head ? end : i + kStatThreads) {
-    const float x = scaled(value(row + i), by);
-    if (greedy && (x > m || (x == m && i < arg))) arg = i;
-    join(&m, &s, x, 1.f);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    const int a2 = __shfl_xor_sync(0xffffffffu, arg, o);
-    if (m2 > m || (m2 == m && a2 < arg)) arg = a2;
-    // the same sum in both lanes: the larger lane's second
-    const bool up = lane & o;
-    float m1 = up ? m2 : m, s1 = up ? s2 : s;
-    join(&m1, &s1, up ? m : m2, up ? s : s2);
-    m = m1;
-    s = s1;
-  }
-  if (lane == 0) {
-    ms[warp] = m;
-    ss[warp] = s;
-    as[warp] = arg;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int k = 1; k < kStatThreads / 32; ++k) {
-      if (ms[k] > m || (ms[k] == m && as[k] < arg)) arg = as[k];
-      join(&m, &s, ms[k], ss[k]);
-    }
-    p.pieces[((int64_t)is_draft * p.rows + r) * p.splits + part] = {m, s, arg, 0};
-  }
-}
-
-// The whole row's, by one warp.
-__device__ __forceinline__ Piece row_stats(const VerifyParams& p, int is_draft, int r) {
-  const int lane = threadIdx.x & 31;
-  const Piece* at = p.pieces + ((int64_t)is_draft * p.rows + r) * p.splits;
   Piece a = {kLowest, 0.f, INT32_MAX, 0};
-  for (int k = lane; k < p.splits; k += 32) {
-    const Piece b = at[k];
-    if (b.m > a.m || (b.m == a.m && b.arg < a.arg)) a.arg = b.arg;
-    join(&a.m, &a.s, b.m, b.s);
-  }
+  constexpr int V = Loads<T>::kVecs, K = Loads<T>::kVec;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    Piece b;
-    b.m = __shfl_xor_sync(0xffffffffu, a.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, a.s, o);
-    b.arg = __shfl_xor_sync(0xffffffffu, a.arg, o);
-    if (b.m > a.m || (b.m == a.m && b.arg < a.arg)) a.arg = b.arg;
-    const bool up = lane & o;
-    float m1 = up ? b.m : a.m, s1 = up ? b.s : a.s;
-    join(&m1, &s1, up ? a.m : b.m, up ? a.s : b.s);
-    a.m = m1;
-    a.s = s1;
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < K; ++k) a.m = fmaxf(a.m, __fmul_rn(x.get(v, k), by));
+  a.m = warp_max(a.m);
+  const float ref = -__fmul_rn(a.m, kLog2e);
+  float s[4] = {};
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k & 3] += ex2(__fmaf_rn(__fmul_rn(x.get(v, k), by), kLog2e, ref));
+  a.s = (s[0] + s[1]) + (s[2] + s[3]);
+  if (__any_sync(0xffffffffu, !(a.s <= FLT_MAX)) || a.m == INFINITY) {
+    a.m = kLowest;
+    a.s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = 0; k < K; ++k) a.m = fmaxf(a.m, scaled(x.get(v, k), by));
+    a.m = warp_max(a.m);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = 0; k < K; ++k) a.s += exp_from(scaled(x.get(v, k), by), a.m);
   }
-  return a;
+  if (greedy) {
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v)
+#pragma unroll
+      for (int k = K - 1; k >= 0; --k)
+        if (scaled(x.get(v, k), by) == a.m) a.arg = Loads<T>::index(part, skew, v) + k;
+    a.arg = __reduce_min_sync(0xffffffffu, a.arg);
+  }
+  a.s = warp_sum(a.s);
+  if (lane == 0) warps[warp] = a;
+  __syncthreads();
+  if (warp == 0) {
+    a = {kLowest, 0.f, INT32_MAX, 0};
+    if (lane < kStatThreads / 32) a = warps[lane];
+    a = join_warp(a);
+    if (lane == 0) p.pieces[((int64_t)is_draft * p.rows + r) * p.splits + part] = a;
+  }
 }
 
-// A sum of fp32 numbers with its rounding errors kept: twice fp32's bits.
+// The whole row's, by one warp; the first of its pieces may have been loaded.
+__device__ __forceinline__ Piece piece_of(const VerifyParams& p, int is_draft, int r, int k) {
+  if (k >= p.splits) return {kLowest, 0.f, INT32_MAX, 0};
+  const int4 x = reinterpret_cast<const int4*>(p.pieces)[((int64_t)is_draft * p.rows + r) * p.splits + k];
+  return {__int_as_float(x.x), __int_as_float(x.y), x.z, 0};
+}
+__device__ __forceinline__ Piece row_stats(const VerifyParams& p, int is_draft, int r, Piece first) {
+  for (int k = (threadIdx.x & 31) + 32; k < p.splits; k += 32) join(&first, piece_of(p, is_draft, r, k));
+  return join_warp(first);
+}
+__device__ __forceinline__ Piece row_stats(const VerifyParams& p, int is_draft, int r) {
+  return row_stats(p, is_draft, r, piece_of(p, is_draft, r, threadIdx.x & 31));
+}
+
+// A thread's sum of fp32 numbers keeps what rounding loses (the exact error of a sum, Knuth): twice fp32's bits, in the
+// thread's own order. From there on sums are whole numbers of 64-bit fixed point, so that any order gives the same:
+// exponentials are at most 1, as many as the vocabulary has, and in units of 2^-z_bits cannot pass 2^63; weights sum to
+// 1 and a few roundings, in units of 2^-62. FP64, and conversions to 64-bit whole numbers, run at 1/64 of fp32's rate:
+// the draw over 2048 logits took 65 us with the one and 14 with the other.
+typedef unsigned long long fixed;
+constexpr int kWeightBits = 62;
+__device__ __forceinline__ fixed to_fixed(float x, int bits) {       // x not negative; cut off below a unit
+  const int b = __float_as_int(x), s = (b >> 23) - 150 + bits;
+  const fixed m = (b & 0x7fffff) | 0x800000;
+  return s >= 0 ? m << s : s > -24 ? m >> -s : 0;
+}
 struct Sum {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float x) {
@@ -202,153 +247,316 @@ struct Sum {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(x, z)));
     hi = t;
   }
-  __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+  __device__ __forceinline__ fixed value(int bits) const {
+    const fixed l = to_fixed(fabsf(lo), bits);
+    return to_fixed(hi, bits) + (lo < 0.f ? 0 - l : l);
+  }
 };
-
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ fixed warp_total(fixed x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+__device__ __forceinline__ fixed warp_prefix(fixed x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const fixed y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+// 2^bits / x to fp32's rounding, x not 0.
+__device__ __forceinline__ float inverse(fixed x, int bits) {
+  const int lead = __clzll((long long)x);
+  const fixed y = x << lead;                                         // [1, 2) as 1.63 bits: 24 of them and the next 32
+  const float hi = (float)(uint32_t)(y >> 40) * 0x1p-23f, lo = (float)(uint32_t)(y >> 8) * 0x1p-55f;
+  const float r = __frcp_rn(hi);
+  return __fmul_rn(__fmaf_rn(r, __fmaf_rn(-lo, r, __fmaf_rn(-hi, r, 1.f)), r), __int_as_float((127 + bits - 63 + lead) << 23));
+}
+// The whole part of u x, u in [0, 1): u's bits times x, shifted.
+__device__ __forceinline__ fixed times(float u, fixed x) {
+  const int bits = __float_as_int(u), e = bits >> 23;
+  const fixed m = e ? (bits & 0x7fffff) | 0x800000 : bits & 0x7fffff;
+  const int down = 150 - max(e, 1);                                  // u = m 2^-down, 24 <= down
+  const fixed lo = m * x, hi = __umul64hi(m, x);
+  return down < 64 ? hi << (64 - down) | lo >> down : down < 128 ? hi >> (down - 64) : 0;
+}
 
+struct TokenShared {
+  int first;                            // the first refused row, or the last
+  Piece rows[2][kRowsKept];             // the target's and the draft's rows
+  int draft[kRowsKept];
+  fixed part[2][kTokenWarps];           // each warp's sums
+  fixed z[2][kMostCluster];             // each block's sums of exponentials
+  fixed w[2][kMostCluster];             // each block's sum of weights, by turn
+  float rz[2];                          // 1 over all of them
+};
+
+// One value to the same place of all of the cluster's blocks.
+__device__ __forceinline__ void tell(fixed* slot, int cluster, fixed x) {
+  if (threadIdx.x < (unsigned)cluster) {
+    const uint32_t at = ptx::mapa(ptx::saddr(slot), threadIdx.x);
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
+  }
+  __syncwarp();
+}
+
+// A row's share of a block: its logits from `src` on, `skew` elements past a 16-byte boundary.
 template <class T>
-__global__ void __launch_bounds__(kTokenThreads) token_kernel(const __grid_constant__ VerifyParams p) {
-  constexpr int kWarps = kTokenThreads / 32;
-  __shared__ int first;                // the first refused row, or the last
-  __shared__ int found;
-  __shared__ double sums[2][kWarps];
-  const int seq = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+struct Part {
+  static constexpr int K = 16 / sizeof(T);
+  const T* src;
+  int size, skew;
+  float m;
+  __device__ __forceinline__ Part(const T* s, int n, float top)
+      : src(s), size(n), skew((int)((reinterpret_cast<uintptr_t>(s) & 15) / sizeof(T))), m(top) {}
+  // the v-th 16 bytes; minus infinity for what is not its
+  __device__ __forceinline__ uint4 load(int v) const {
+    const int i = v * K - skew;
+    if (i >= 0 && i + K <= size) return *reinterpret_cast<const uint4*>(src + i);
+    uint4 raw = sizeof(T) == 4 ? make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u)
+                               : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+    if (i + K > 0 && i < size) {
+      T x[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) x[k] = i + k >= 0 && i + k < size ? src[i + k] : T(-INFINITY);
+      memcpy(&raw, x, 16);
+    }
+    return raw;
+  }
+  // their exponentials: added to z and, if KEEP, left at kept[skew + i]. 0 for what is not there: m is above the lowest
+  template <bool KEEP>
+  __device__ __forceinline__ void take(int v, const uint4& raw, float by, Sum* z, float* kept) const {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    float e[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float l = sizeof(T) == 4 ? __uint_as_float(w[k & 3]) : __uint_as_float(k & 1 ? w[(k >> 1) & 3] & 0xffff0000u : w[(k >> 1) & 3] << 16);
+      e[k] = exp_from(scaled(l, by), m);
+      z[k & 1].add(e[k]);
+    }
+    if (KEEP && v * K < size + skew)
+#pragma unroll
+      for (int k = 0; k < K; k += 4) *reinterpret_cast<float4*>(kept + v * K + k) = make_float4(e[k], e[k + 1], e[k + 2], e[k + 3]);
+  }
+};
+
+// What a block's chunk of exponentials takes in shared memory: room for the skew at the front and the last load's end.
+__host__ __device__ __forceinline__ int kept_floats(int chunk) { return (chunk + 16 + 3) & ~3; }
+
+template <class T, bool KEEP>
+__global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_constant__ VerifyParams p) {
+  extern __shared__ __align__(16) float kept[];       // exponentials of the block's chunk of the target's, and of the draft's
+  __shared__ TokenShared sh;
+  const int rank = blockIdx.x % p.cluster, seq = blockIdx.x / p.cluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // its memory may be written
   const int r0 = p.start[seq], r1 = p.start[seq + 1];
+  const float heat = p.temperature[seq], by = scale_of(heat), u_token = p.u_token[seq];
+  const bool greedy = !(heat > 0.f);
   // a start out of order leaves in doubt whose rows are whose, for every sequence
   bool out_of_order = false;
   for (int i = threadIdx.x; i < p.n; i += kTokenThreads) {
     const int b = p.start[i], e = p.start[i + 1];
     out_of_order |= b < 0 || e < b || e > p.rows;
   }
+  if (threadIdx.x == 0) sh.first = r1 - 1;
   const bool bad = __syncthreads_or(out_of_order);
+  const T* logits = static_cast<const T*>(p.logits);
+  const T* drafts = greedy ? nullptr : static_cast<const T*>(p.draft_logits);
+  bool waited = false;
+  for (int r = r0 + warp; r < r1 && !bad; r += kTokenWarps) {        // every block of the cluster does the same
+    const bool last = r == r1 - 1;
+    const int d = last ? -1 : p.draft[r];
+    const bool in = (uint32_t)d < (uint32_t)p.vocab;
+    const float u = last ? 0.f : fminf(fmaxf(p.u_accept[r], 0.f), 0x1.fffffep-1f);
+    const float xp = in ? scaled(value(logits + r * p.row + d), by) : 0.f;
+    const float xq = in && drafts ? scaled(value(drafts + r * p.draft_row + d), by) : 0.f;
+    if (!waited) ptx::pdl_wait();                                    // the sums, in front of which all but them is read
+    waited = true;
+    Piece a = piece_of(p, 0, r, lane), b = {kLowest, 0.f, 0, 0};
+    if (drafts && !last) b = piece_of(p, 1, r, lane);
+    a = row_stats(p, 0, r, a);
+    if (drafts && !last) b = row_stats(p, 1, r, b);
+    const float pd = in && a.m > kLowest ? exp_from(xp, a.m) / a.s : 0.f;
+    const float qd = !drafts ? 1.f : in && b.m > kLowest ? exp_from(xq, b.m) / b.s : 0.f;
+    // u q < p of fp32 numbers, exactly: the product's rounding is a number of its own
+    const float uq = __fmul_rn(u, qd);
+    const bool less = uq < pd || (uq == pd && __fmaf_rn(u, qd, -uq) < 0.f);
+    const bool yes = greedy ? a.m > kLowest && d == a.arg : less;
+    if (lane == 0) {
+      if (r - r0 < kRowsKept) {
+        sh.rows[0][r - r0] = a;
+        sh.rows[1][r - r0] = b;
+        sh.draft[r - r0] = d;
+      }
+      if (!last && p.prob && rank == 0) p.prob[r] = pd;
+      if (!last && !yes) atomicMin(&sh.first, r);
+    }
+  }
+  __syncwarp();
+  if (!waited) ptx::pdl_wait();
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (bad || r0 == r1) {
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && rank == 0) {
       p.accepted[seq] = bad ? -1 : 0;
       p.token[seq] = -1;
     }
     return;
   }
-  const float heat = p.temperature[seq], by = scale_of(heat);
-  const bool greedy = !(heat > 0.f);
-  if (threadIdx.x == 0) {
-    first = r1 - 1;
-    found = INT32_MAX;
-  }
   __syncthreads();
-  const T* logits = static_cast<const T*>(p.logits);
-  const T* drafts = static_cast<const T*>(p.draft_logits);
-  for (int r = r0 + warp; r < r1 - 1; r += kWarps) {
-    const int d = p.draft[r];
-    const bool in = (uint32_t)d < (uint32_t)p.vocab;
-    const Piece a = row_stats(p, 0, r);
-    const float pd = in && a.m > kLowest ? exp_from(scaled(value(logits + r * p.row + d), by), a.m) / a.s : 0.f;
-    float qd = 1.f;
-    if (drafts && !greedy) {
-      const Piece b = row_stats(p, 1, r);
-      qd = in && b.m > kLowest ? exp_from(scaled(value(drafts + r * p.draft_row + d), by), b.m) / b.s : 0.f;
-    }
-    const double u = fminf(fmaxf(p.u_accept[r], 0.f), 0x1.fffffep-1f);
-    const bool yes = greedy ? a.m > kLowest && d == a.arg : u * (double)qd < (double)pd;
-    if (lane == 0) {
-      if (p.prob) p.prob[r] = pd;
-      if (!yes) atomicMin(&first, r);
-    }
+  const int r = sh.first;
+  const bool refused = r < r1 - 1, both = refused && drafts;
+  Piece a, b = {kLowest, 0.f, 0, 0};
+  int d;
+  if (r - r0 < kRowsKept) {
+    a = sh.rows[0][r - r0];
+    if (both) b = sh.rows[1][r - r0];
+    d = sh.draft[r - r0];
+  } else {
+    a = row_stats(p, 0, r);
+    if (both) b = row_stats(p, 1, r);
+    d = refused ? p.draft[r] : -1;
   }
-  __syncthreads();
-  const int r = first;
-  const bool refused = r < r1 - 1;
-  if (threadIdx.x == 0) p.accepted[seq] = r - r0;
-  const Piece a = row_stats(p, 0, r);
-  if (greedy || !(a.m > kLowest)) {
-    if (threadIdx.x == 0) p.token[seq] = a.m > kLowest ? a.arg : -1;
-    return;
+  if (threadIdx.x == 0 && rank == 0) {
+    p.accepted[seq] = r - r0;
+    if (greedy || !(a.m > kLowest)) p.token[seq] = a.m > kLowest ? a.arg : -1;
   }
-  const bool both = refused && drafts;
-  const float qm = both ? row_stats(p, 1, r).m : 0.f;
-  const int out = refused && !drafts ? p.draft[r] : -1;              // a certain draft's token, taken out
-  const T* row = logits + r * p.row;
-  const T* draft_row = both ? drafts + r * p.draft_row : nullptr;
-  // sums of both rows' exponentials
-  Sum zp, zq;
-  for (int i = threadIdx.x; i < p.vocab; i += kTokenThreads) {
-    zp.add(exp_from(scaled(value(row + i), by), a.m));
-    if (both) zq.add(exp_from(scaled(value(draft_row + i), by), qm));
-  }
-  const double z0 = warp_sum(zp.value()), z1 = warp_sum(zq.value());
-  if (lane == 0) {
-    sums[0][warp] = z0;
-    sums[1][warp] = z1;
-  }
-  __syncthreads();
-  double tp = 0., tq = 0.;
-  for (int k = 0; k < kWarps; ++k) {
-    tp += sums[0][k];
-    tq += sums[1][k];
-  }
-  const float rp = (float)(1. / tp), rq = both && qm > kLowest ? (float)(1. / tq) : 0.f;
-  auto weight = [&](int i, bool residual) {
-    const float x = __fmul_rn(exp_from(scaled(value(row + i), by), a.m), rp);
-    if (!residual) return x;
-    if (both) return fmaxf(__fsub_rn(x, __fmul_rn(exp_from(scaled(value(draft_row + i), by), qm), rq)), 0.f);
-    return i == out ? 0.f : x;
-  };
-  // each warp a stretch of the vocabulary
-  const int each = (p.vocab + kWarps - 1) / kWarps, begin = min(warp * each, p.vocab), end = min(begin + each, p.vocab);
-  bool residual = true;
-  double total = 0.;
-  for (int turn = 0; turn < 2; ++turn) {
-    Sum w;
-    for (int i = begin + lane; i < end; i += 32) w.add(weight(i, residual));
-    const double mine = warp_sum(w.value());
-    __syncthreads();
-    if (lane == 0) sums[0][warp] = mine;
-    __syncthreads();
-    total = 0.;
-    for (int k = 0; k < kWarps; ++k) total += sums[0][k];
-    if (total > 0.) break;
-    residual = false;
-  }
-  const double want = fminf(fmaxf(p.u_token[seq], 0.f), 0x1.fffffep-1f) * total;
-  double before = 0.;
-  int my = -1;                                                       // the stretch that the draw falls into
-  for (int k = 0; k < kWarps; ++k) {
-    if (sums[0][k] > 0.) {
-      my = k;
-      if (before + sums[0][k] > want) break;
-    }
-    before += sums[0][k];
-  }
-  if (my != warp) return;
-  before = 0.;
-  for (int k = 0; k < my; ++k) before += sums[0][k];
-  int last = 0;                                                      // rounding may put the draw behind all of them
-  for (int i0 = begin; i0 < end; i0 += 32) {
-    const int i = i0 + lane;
-    const float w = i < end ? weight(i, residual) : 0.f;
-    double c = w;
+  if (greedy || !(a.m > kLowest)) return;                            // the whole cluster
+  const bool with_q = b.m > kLowest;
+  const int begin = min(rank * p.chunk, p.vocab), size = min(p.chunk, p.vocab - begin);
+  const T* row = logits + r * p.row + begin;
+  const T* draft_row = with_q ? drafts + r * p.draft_row + begin : row;
+  const Part<T> of_p(row, size, a.m), of_q(draft_row, with_q ? size : 0, b.m);
+  float* const put_q = kept + kept_floats(p.chunk);
+  const float* kept_p = kept + of_p.skew;
+  const float* kept_q = with_q ? put_q + of_q.skew : kept_p;
+  // sums of both rows' exponentials; two of each, whose steps do not wait for one another
+  Sum sum_p[2], sum_q[2];
+  constexpr int U = sizeof(T) == 4 ? 4 : 2;
+  for (int v0 = threadIdx.x; v0 * Part<T>::K < size + max(of_p.skew, of_q.skew); v0 += U * kTokenThreads) {
+    uint4 x[U], y[U];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const double up = __shfl_up_sync(0xffffffffu, c, o);
-      if (lane >= o) c += up;
-    }
-    c += before;
-    const uint32_t some = __ballot_sync(0xffffffffu, w > 0.f), hit = __ballot_sync(0xffffffffu, w > 0.f && c > want);
-    if (some) last = i0 + 31 - __clz(some);
-    if (hit) {
-      last = i0 + __ffs(hit) - 1;
-      break;
-    }
-    before = __shfl_sync(0xffffffffu, c, 31);
+    for (int u = 0; u < U; ++u) x[u] = of_p.load(v0 + u * kTokenThreads);
+    if (with_q)
+#pragma unroll
+      for (int u = 0; u < U; ++u) y[u] = of_q.load(v0 + u * kTokenThreads);
+#pragma unroll
+    for (int u = 0; u < U; ++u) of_p.template take<KEEP>(v0 + u * kTokenThreads, x[u], by, sum_p, kept);
+    if (with_q)
+#pragma unroll
+      for (int u = 0; u < U; ++u) of_q.template take<KEEP>(v0 + u * kTokenThreads, y[u], by, sum_q, put_q);
   }
-  if (lane == 0) p.token[seq] = last;
+  fixed zp = sum_p[0].value(p.z_bits) + sum_p[1].value(p.z_bits), zq = 0;
+  if (with_q) zq = warp_total(sum_q[0].value(p.z_bits) + sum_q[1].value(p.z_bits));
+  zp = warp_total(zp);
+  if (lane == 0) {
+    sh.part[0][warp] = zp;
+    sh.part[1][warp] = zq;
+  }
+  __syncthreads();
+  // over the block, and over the cluster: one warp's work
+  auto of_block = [&](const fixed* parts) { return warp_total(lane < kTokenWarps ? parts[lane] : 0); };
+  auto of_cluster = [&](const fixed* slots) { return warp_total(lane < p.cluster ? slots[lane] : 0); };
+  if (warp == 0) {
+    tell(&sh.z[0][rank], p.cluster, of_block(sh.part[0]));
+    if (with_q) tell(&sh.z[1][rank], p.cluster, of_block(sh.part[1]));
+  }
+  // the token that a certain draft proposed weighs nothing where it was refused; its exponential is kept aside
+  const int out = refused && !drafts && (uint32_t)(d - begin) < (uint32_t)size ? d - begin : -1;
+  float aside = 0.f;
+  if (KEEP && out >= 0 && threadIdx.x == 0) {
+    aside = kept_p[out];
+    kept[of_p.skew + out] = 0.f;
+  }
+  __syncwarp();
+  ptx::cluster_sync_all();
+  if (warp < 2) {
+    const fixed z = of_cluster(sh.z[warp]);
+    if (lane == 0) sh.rz[warp] = warp == 0 || with_q ? inverse(z, p.z_bits) : 0.f;
+  }
+  __syncthreads();
+  const float rp = sh.rz[0];
+  float rq = sh.rz[1];                                               // 0 without a draft's logits: p - 0 p is p
+  bool residual = true;
+  auto weight = [&](int i) {
+    float x, y;
+    if (KEEP) {
+      x = kept_p[i];
+      y = kept_q[i];
+    } else {
+      x = residual && i == out ? 0.f : exp_from(scaled(value(row + i), by), a.m);
+      y = with_q ? exp_from(scaled(value(draft_row + i), by), b.m) : 0.f;
+    }
+    return fmaxf(__fsub_rn(__fmul_rn(x, rp), __fmul_rn(y, rq)), 0.f);
+  };
+  // each warp a stretch of the block's logits, of whole 32s
+  const int each = ((size + kTokenWarps - 1) / kTokenWarps + 31) & ~31, w0 = min(warp * each, size), w1 = min(w0 + each, size);
+  fixed total = 0;
+  int turn = 0;
+  for (;; ++turn) {
+    Sum sum;
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) sum.add(weight(i));
+    const fixed w = warp_total(sum.value(kWeightBits));
+    if (lane == 0) sh.part[turn][warp] = w;
+    __syncthreads();
+    if (warp == 0) tell(&sh.w[turn][rank], p.cluster, of_block(sh.part[turn]));
+    __syncwarp();
+    ptx::cluster_sync_all();
+    total = 0;
+    for (int k = 0; k < p.cluster; ++k) total |= sh.w[turn][k];      // whether there is any
+    if (total || turn) break;                                        // the same in every block
+    // roundings left nothing: from p itself
+    residual = false;
+    rq = 0.f;
+    if (KEEP && out >= 0 && threadIdx.x == 0) kept[of_p.skew + out] = aside;
+    __syncthreads();
+  }
+  if (warp) return;                                                  // nobody reads another block's memory from here on
+  const fixed want = times(fminf(fmaxf(u_token, 0.f), 0x1.fffffep-1f), of_cluster(sh.w[turn]));
+  // the block, the warp's stretch, 32 logits of it, the logit: each time the first whose end passes that. A stretch's
+  // sum and its parts' may differ in the last bits that threads kept: should none of them pass, the last that weighs
+  // anything is it
+  auto first_above = [&](fixed x, fixed* before) {
+    const fixed end = *before + warp_prefix(x);
+    const uint32_t some = __ballot_sync(0xffffffffu, x != 0), hit = __ballot_sync(0xffffffffu, end > want) & some;
+    const int at = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : 0;
+    *before = __shfl_sync(0xffffffffu, end - x, at);
+    return at;
+  };
+  fixed before = 0;
+  if (first_above(lane < p.cluster ? sh.w[turn][lane] : 0, &before) != rank) return;
+  const int stretch = first_above(lane < kTokenWarps ? sh.part[turn][lane] : 0, &before);
+  const int s0 = min(stretch * each, size), s1 = min(s0 + each, size);
+  int at = s0;
+  int run = 1;                                                       // a power of two
+  while (run < 32 && run * 32 < s1 - s0) run *= 2;
+  for (int t0 = s0; t0 < s1; t0 += 32 * run) {
+    // lane l: the sum of the l-th run, read so that the lanes' banks differ
+    Sum sum;
+#pragma unroll 4
+    for (int k = 0; k < run; ++k) {
+      const int i = t0 + lane * run + ((k + lane) & (run - 1));
+      if (i < s1) sum.add(weight(i));
+    }
+    const fixed x = sum.value(kWeightBits), all = warp_total(x);
+    if (all) {
+      fixed base = before;
+      const int i0 = t0 + first_above(x, &base) * run, i = i0 + lane;
+      at = i0 + first_above(lane < run && i < s1 ? to_fixed(weight(i), kWeightBits) : 0, &base);
+    }
+    before += all;
+    if (before > want) break;
+  }
+  if (lane == 0) p.token[seq] = begin + at;
 }
 
 // ------------------------------------------------------------------ checks
+constexpr int kResident = 2 * 152;
+constexpr size_t kMostKept = 100 * 1024;       // bytes of exponentials in a block's shared memory: two blocks an SM
+size_t kept_bytes(const VerifyParams& p) { return (size_t)kept_floats(p.chunk) * (p.draft_logits ? 8 : 4); }
+
 int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   if (!a || !a->start || !a->logits || !a->draft || !a->temperature || !a->u_accept || !a->u_token || !a->accepted || !a->token)
     return CP_ERR_INVALID_ARG;
@@ -375,8 +583,16 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   p->n = a->sequences;
   p->rows = a->rows;
   p->vocab = a->vocab;
-  p->splits = (a->vocab + kPiece - 1) / kPiece;
-  if ((int64_t)p->rows * p->splits > 1 << 30) return CP_ERR_UNSUPPORTED;   // blocks
+  p->cluster = 1;
+  p->splits = (a->vocab + (int)(16 / es) - 1 + kPiece - 1) / kPiece;        // wherever a row starts within 16 bytes
+  // blocks a sequence: more while there is work for them and room for all at once, or until a block's share can be kept
+  auto cut = [&] { p->chunk = (p->vocab + p->cluster - 1) / p->cluster; };
+  for (cut(); p->cluster < kMostCluster &&
+              ((p->chunk > 2048 && (int64_t)p->n * p->cluster * 2 <= kResident) || kept_bytes(*p) > kMostKept);
+       cut())
+    p->cluster *= 2;
+  p->z_bits = 62;
+  while (((int64_t)1 << (63 - p->z_bits)) < p->vocab) --p->z_bits;
   *workspace = (size_t)2 * p->rows * p->splits * sizeof(Piece);
   return CP_OK;
 }
@@ -384,8 +600,30 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
 template <class T>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
   stats_kernel<T><<<dim3((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1), kStatThreads, 0, s>>>(p);
-  token_kernel<T><<<p.n, kTokenThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const bool keep = kept_bytes(p) <= kMostKept;
+  const dim3 grid((unsigned)(p.n * p.cluster));
+  return keep ? launch_as(token_kernel<T, true>, grid, p.cluster, 1, true, kTokenThreads, kept_bytes(p), s, p)
+              : launch_as(token_kernel<T, false>, grid, p.cluster, 1, true, kTokenThreads, 0, s, p);
+}
+
+template <class T, bool KEEP>
+bool allow() {
+  return cudaFuncSetAttribute(token_kernel<T, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? (int)kMostKept : 0) == cudaSuccess &&
+         cudaFuncSetAttribute(token_kernel<T, KEEP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+}
+
+// Once per device: whether it is one that the kernels run on, and their shared memory.
+int prepare(int device) {
+  static std::atomic<int> done[64];
+  if (device >= 0 && device < 64 && done[device].load(std::memory_order_acquire)) return CP_OK;
+  const int st = check_device(device);
+  if (st) return st;
+  DeviceGuard g(device);
+  if (!allow<float, true>() || !allow<float, false>() || !allow<__nv_bfloat16, true>() || !allow<__nv_bfloat16, false>()) return CP_ERR_CUDA;
+  if (device < 64) done[device].store(1, std::memory_order_release);
+  return CP_OK;
 }
 
 }  // namespace
@@ -408,7 +646,7 @@ int cp_verify(const cp_verify_args* args, int device, void* workspace, size_t wo
   if (st) return st;
   if (!workspace || workspace_bytes < need) return CP_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return CP_ERR_UNSUPPORTED;
-  const int dev = check_device(device);
+  const int dev = prepare(device);
   if (dev) return dev;
   DeviceGuard g(device);
   p.pieces = static_cast<Piece*>(workspace);

@@ -98,6 +98,9 @@ def test_long_drafts_and_large_vocabularies():
     check(make([40, 100, 0], 400, seed=6, sharp=1.0))
     check(make([2, 1], 151000, seed=7))
     check(make([1], 300001, seed=8, with_draft=False))
+    for dtype in (torch.float32, torch.bfloat16):                   # more than the blocks' shared memory keeps
+        check(make([1, 0, 2], 400003, dtype, seed=22))
+        check(make([1, 2], 900001, dtype, seed=23, with_draft=False, temperature=2.0))
 
 
 def test_the_same_draw_wherever_it_is_computed():
