@@ -585,6 +585,7 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   p->vocab = a->vocab;
   p->cluster = 1;
   p->splits = (a->vocab + (int)(16 / es) - 1 + kPiece - 1) / kPiece;        // wherever a row starts within 16 bytes
+  if ((int64_t)p->rows * p->splits > 1 << 30) return CP_ERR_UNSUPPORTED;             // blocks
   // blocks a sequence: more while there is work for them and room for all at once, or until a block's share can be kept
   auto cut = [&] { p->chunk = (p->vocab + p->cluster - 1) / p->cluster; };
   for (cut(); p->cluster < kMostCluster &&
