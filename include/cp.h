@@ -626,6 +626,13 @@ typedef struct cp_linear_desc {
   const void* scale;          /* device bf16 [features][width / group]       */
   const void* zero;           /* device bytes [features][width / group], each
                                  0 .. 15; NULL: 8                             */
+  int64_t timeout_ns;         /* give up a wait inside cp_linear_apply after
+                                 this long (0 = default 2 s)                  */
+  int debug_stall;            /* testing: nonzero makes each block of
+                                 cp_linear_apply that brings x in through a
+                                 ring (more than 16 rows) leave out its first
+                                 load, so that the waits for it run out and
+                                 set CP_ERR_TIMEOUT                           */
 } cp_linear_desc;
 
 typedef struct cp_linear_args {
@@ -661,6 +668,12 @@ int cp_linear_apply(cp_linear* l, const cp_linear_args* args, cp_stream_t stream
 /* The weights as the numbers that they stand for, device bf16
  * [features][width], 16-byte aligned or not. */
 int cp_linear_unpack(cp_linear* l, void* out, cp_stream_t stream);
+
+/* Synchronise the device and return the sticky device status (CP_OK, or
+ * CP_ERR_TIMEOUT: a wait inside a kernel gave up, and what that call left in
+ * out is not specified; CP_ERR_CUDA if the synchronisation fails); reset it. */
+int cp_linear_status(cp_linear* l);
+int cp_linear_clear_status(cp_linear* l);
 
 /* Release the object (synchronises its device). */
 void cp_linear_destroy(cp_linear* l);

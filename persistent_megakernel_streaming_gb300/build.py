@@ -32,6 +32,7 @@ SOURCES = [
     ("cp_attend_chunk.cu", "cp_attend_chunk.cu.o", []),
     ("cp_pages.cu", "cp_pages.cu.o", []),
     ("cp_linear.cu", "cp_linear.cu.o", []),
+    ("cp_linear_rows.cu", "cp_linear_rows.cu.o", []),
     ("cp_verify.cu", "cp_verify.cu.o", []),
 ]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -28,7 +28,7 @@ EXPORTS = ["cp_create", "cp_frame", "cp_frame_split", "cp_debug_logits", "cp_deb
            "cp_cache_clear_status", "cp_cache_destroy", "cp_cache_check", "cp_test_slot", "cp_cache_copy",
            "cp_pages_create", "cp_pages_fork", "cp_pages_grow", "cp_pages_trim", "cp_pages_compact", "cp_pages_status",
            "cp_pages_clear_status", "cp_pages_destroy", "cp_pages_check",
-           "cp_linear_create", "cp_linear_apply", "cp_linear_unpack", "cp_linear_destroy", "cp_linear_check",
+           "cp_linear_create", "cp_linear_apply", "cp_linear_status", "cp_linear_clear_status", "cp_linear_unpack", "cp_linear_destroy", "cp_linear_check",
            "cp_verify", "cp_verify_check"]
 
 
@@ -105,7 +105,7 @@ class PagesDesc(C.Structure):
 
 class LinearDesc(C.Structure):
     _fields_ = [("features", C.c_int), ("width", C.c_int), ("group", C.c_int), ("gated", C.c_int), ("q", C.c_void_p),
-                ("scale", C.c_void_p), ("zero", C.c_void_p)]
+                ("scale", C.c_void_p), ("zero", C.c_void_p), ("timeout_ns", C.c_int64), ("debug_stall", C.c_int)]
 
 
 class LinearArgs(C.Structure):
@@ -178,6 +178,8 @@ def lib() -> C.CDLL:
         L.cp_linear_create.argtypes = [C.POINTER(LinearDesc), i, C.POINTER(vp)]
         L.cp_linear_apply.argtypes = [vp, C.POINTER(LinearArgs), st]
         L.cp_linear_unpack.argtypes = [vp, vp, st]
+        L.cp_linear_status.argtypes = [vp]
+        L.cp_linear_clear_status.argtypes = [vp]
         L.cp_linear_destroy.argtypes = [vp]
         L.cp_linear_destroy.restype = None
         L.cp_linear_check.argtypes = [C.POINTER(LinearDesc), C.POINTER(LinearArgs)]
@@ -637,7 +639,7 @@ class Linear:
     [features][width / group] and ``zero`` uint8 of the same shape (None: 8). ``gated``: the first half of the rows is a
     gate projection's, the second an up projection's."""
 
-    def __init__(self, q, scale, zero=None, gated: bool = False):
+    def __init__(self, q, scale, zero=None, gated: bool = False, timeout_ns: int = 0, debug_stall: bool = False):
         import torch
         if q.dtype != torch.uint8 or q.dim() != 2 or scale.dim() != 2 or scale.dtype not in (torch.bfloat16, torch.int16) or \
                 q.device.type != "cuda":
@@ -654,7 +656,7 @@ class Linear:
         self.outs = n // 2 if gated else n
         self.device_index = index
         self.desc = LinearDesc(_int32(n, "features"), _int32(self.width, "width"), self.group, int(self.gated), _ptr(q), _ptr(scale),
-                               _ptr(zero))
+                               _ptr(zero) or None, timeout_ns, int(debug_stall))
         self.dtypes = {torch.bfloat16: 0, torch.float32: 1}
         self.x_dtypes = (torch.bfloat16, torch.int16)
         h = C.c_void_p()
@@ -695,6 +697,12 @@ class Linear:
         code = lib().cp_linear_unpack(self._h, a, _stream_on(self.device_index, stream))
         if code:
             raise CPError(code, "cp_linear_unpack")
+
+    def status(self) -> int:
+        return lib().cp_linear_status(self._h)
+
+    def clear_status(self):
+        _check(lib().cp_linear_clear_status(self._h), "cp_linear_clear_status")
 
     def close(self):
         if getattr(self, "_h", None):

@@ -1,5 +1,5 @@
-// cp_linear.cu -- projections of few rows with 4-bit weights: the C ABI (checks,
-// layout of the weights, launches) and the kernel for up to 16 rows.
+// cp_linear.cu -- projections with 4-bit weights: the C ABI (checks, layout of
+// the weights, launches) and the kernel for up to 16 rows.
 #include <cuda_runtime.h>
 
 #include <new>
@@ -14,6 +14,9 @@ using namespace cp::linear;
 struct cp_linear {
   int device = 0;
   Weights w{};
+  int32_t* status = nullptr;
+  long long timeout_ns = 0;
+  int stall = 0;
   void* memory = nullptr;
 };
 
@@ -42,7 +45,7 @@ __global__ void pack_kernel(const PackParams p) {
     for (int j = 0; j < 4; ++j) {
       out[j] = 0;
       for (int a = 0; a < 4; ++a) {
-        const int row = row_of(w, t, g + (a & 1) * 8), k = b * kBlockK + 16 * c + 4 * j + (a >> 1) * 2;
+        const int row = row_of(w, t, g + (a & 1) * 8), k = b * kBlockK + 16 * j + 4 * c + (a >> 1) * 2;
         if (row < 0 || k >= w.width) continue;
         const uint32_t two = p.q[(int64_t)row * (w.width / 2) + k / 2];
         out[j] |= (two & 15) << (4 * a) | (two >> 4) << (16 + 4 * a);
@@ -78,15 +81,14 @@ __global__ void unpack_kernel(const Weights w, uint16_t* out) {
     const int lane = (int)(i & 31), g = lane >> 2, c = lane & 3;
     const int64_t rest = i >> 5;
     const int b = (int)(rest % w.blocks), t = (int)(rest / w.blocks);
-    const int64_t at = ((int64_t)t * w.groups + ((b * kBlockK + 16 * c) >> w.group_shift)) * 8 + g;
-    const Meta m = meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero);
     const uint4 v = w.w[i];
     const uint32_t words[4] = {v.x, v.y, v.z, v.w};
     for (int j = 0; j < 4; ++j) {
       uint32_t a[4];
-      widen(words[j], m, a);
+      const int64_t at = meta_at(w, t, b * kBlockK + 16 * j, g);
+      widen(words[j], meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero), a);
       for (int x = 0; x < 4; ++x) {
-        const int row = row_of(w, t, g + (x & 1) * 8), k = b * kBlockK + 16 * c + 4 * j + (x >> 1) * 2;
+        const int row = row_of(w, t, g + (x & 1) * 8), k = b * kBlockK + 16 * j + 4 * c + (x >> 1) * 2;
         if (row < 0 || k >= w.width) continue;
         out[(int64_t)row * w.width + k] = (uint16_t)a[x];
         out[(int64_t)row * w.width + k + 1] = (uint16_t)(a[x] >> 16);
@@ -104,17 +106,6 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <class T>
-__device__ __forceinline__ float load_out(const void* p, int64_t i);
-template <>
-__device__ __forceinline__ float load_out<float>(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
-template <>
-__device__ __forceinline__ float load_out<__nv_bfloat16>(const void* p, int64_t i) {
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 // NT tiles of 8 rows of x; a block has two tiles of the weights, of a gated projection the gate's and the same of up,
 // its warps every eighth block of inputs.
 template <class T, int NT>
@@ -125,33 +116,30 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
   const int t0 = blockIdx.x * 2, row0 = blockIdx.y * 8 * NT;
   float acc[2][NT][4] = {};
   for (int b = warp; b < w.blocks; b += kWarps) {
-    uint4 x[NT][2];
-    const int k = b * kBlockK + 16 * c;
+    uint2 x[NT][4];
+    const int k = b * kBlockK;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      x[n][0] = x[n][1] = make_uint4(0, 0, 0, 0);
       const int r = row0 + n * 8 + g;
-      if (r < p.rows && k < w.width) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.x + (int64_t)r * p.x_row + k);
-        x[n][0] = src[0];
-        x[n][1] = src[1];
-      }
+      const uint16_t* src = p.x + (int64_t)r * p.x_row + k + 4 * c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[n][j] = r < p.rows && k + 16 * j < w.width ? *reinterpret_cast<const uint2*>(src + 16 * j) : make_uint2(0, 0);
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       const uint4 v = w.w[((int64_t)(t0 + t) * w.blocks + b) * 32 + lane];
-      const int64_t at = ((int64_t)(t0 + t) * w.groups + (k >> w.group_shift)) * 8 + g;
-      const Meta m = meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero);
       const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t a[4];
-        widen(words[j], m, a);
+      for (int h = 0; h < 2; ++h) {                // groups of 32 have two in a block
+        const int64_t at = meta_at(w, t0 + t, k + 32 * h, g);
+        const Meta m = meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 y = x[n][j >> 1];
-          if (j & 1) mma(acc[t][n], a, y.z, y.w);
-          else mma(acc[t][n], a, y.x, y.y);
+        for (int j = 2 * h; j < 2 * h + 2; ++j) {
+          uint32_t a[4];
+          widen(words[j], m, a);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma(acc[t][n], a, x[n][j].x, x[n][j].y);
         }
       }
     }
@@ -182,20 +170,19 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
 }
 
 template <class T>
-cudaError_t launch_apply(const ApplyParams& p, cudaStream_t s) {
-  if (p.rows <= 8) {
-    few_rows_kernel<T, 1><<<dim3(p.w.tiles / 2, 1), kWarps * 32, 0, s>>>(p);
-  } else {
-    few_rows_kernel<T, 2><<<dim3(p.w.tiles / 2, (p.rows + 15) / 16), kWarps * 32, 0, s>>>(p);
-  }
+cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
+  if (p.rows <= 8) few_rows_kernel<T, 1><<<dim3(p.w.tiles / 2, 1), kWarps * 32, 0, s>>>(p);
+  else few_rows_kernel<T, 2><<<dim3(p.w.tiles / 2, (p.rows + 15) / 16), kWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
+
+constexpr int kFewRows = 16;
 
 // ------------------------------------------------------------------ checks
 int check_desc(const cp_linear_desc* d, Weights* w) {
   if (!d || !d->q || !d->scale || d->features < 1 || d->width < 1 || d->group < 1) return CP_ERR_INVALID_ARG;
   if (d->group != 32 && d->group != 64 && d->group != 128) return CP_ERR_UNSUPPORTED;
-  if (d->width % d->group || (d->gated && d->features % 2)) return CP_ERR_INVALID_ARG;
+  if (d->width % d->group || (d->gated && d->features % 2) || d->timeout_ns < 0) return CP_ERR_INVALID_ARG;
   if (d->width > 1 << 20 || d->features > 1 << 24) return CP_ERR_UNSUPPORTED;
   w->features = d->features;
   w->width = d->width;
@@ -222,8 +209,8 @@ int check_args(const Weights& w, const cp_linear_args* a, ApplyParams* p) {
   p->out_row = a->out_stride ? a->out_stride : w.outs;
   p->add_row = a->add_stride ? a->add_stride : w.outs;
   if (p->x_row < 0 || p->out_row < 0 || p->add_row < 0) return CP_ERR_INVALID_ARG;
-  const int64_t most = (int64_t)1 << 40;
-  if (p->x_row > most || p->out_row > most || p->add_row > most) return CP_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 39;                       // what a tensor map's strides reach
+  if (p->x_row >= most || p->out_row > most || p->add_row > most) return CP_ERR_UNSUPPORTED;
   if (p->x_row % 8 || !aligned16(a->x)) return CP_ERR_UNSUPPORTED;
   const uintptr_t es = a->out_dtype == CP_OUT_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(a->out) % es || reinterpret_cast<uintptr_t>(a->add) % es) return CP_ERR_UNSUPPORTED;
@@ -279,9 +266,12 @@ int cp_linear_create(const cp_linear_desc* desc, int device, cp_linear** out) {
   w.scale = p.scale_out;
   w.zero = p.zero_out;
   l->w = w;
+  l->status = p.bad + 1;
+  l->timeout_ns = desc->timeout_ns ? desc->timeout_ns : 2000000000ll;
+  l->stall = desc->debug_stall;
   int bad = 0;
   // what the caller's streams still write into the arrays is waited for
-  bool ok = cudaDeviceSynchronize() == cudaSuccess && cudaMemset(p.bad, 0, 4) == cudaSuccess;
+  bool ok = cudaDeviceSynchronize() == cudaSuccess && cudaMemset(p.bad, 0, 8) == cudaSuccess && prepare_many_rows() == cudaSuccess;
   if (ok) {
     pack_kernel<<<1216, 256>>>(p);
     ok = cudaGetLastError() == cudaSuccess && cudaMemcpy(&bad, p.bad, 4, cudaMemcpyDeviceToHost) == cudaSuccess;
@@ -309,9 +299,31 @@ int cp_linear_apply(cp_linear* l, const cp_linear_args* args, cp_stream_t stream
   ApplyParams p{};
   const int st = check_args(l->w, args, &p);
   if (st) return st;
+  p.status = l->status;
+  p.timeout_ns = l->timeout_ns;
+  p.stall = l->stall;
   DeviceGuard g(l->device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_err(args->out_dtype == CP_OUT_BF16 ? launch_apply<__nv_bfloat16>(p, s) : launch_apply<float>(p, s));
+  const bool f32 = args->out_dtype == CP_OUT_F32;
+  if (p.rows > kFewRows) return cuda_err(launch_many_rows(p, f32, s));
+  return cuda_err(f32 ? launch_few_rows<float>(p, s) : launch_few_rows<__nv_bfloat16>(p, s));
+}
+
+int cp_linear_status(cp_linear* l) {
+  if (!l) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(l->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return CP_ERR_CUDA;
+  int32_t v = 0;
+  if (cudaMemcpy(&v, l->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return CP_ERR_CUDA;
+  return v;
+}
+
+int cp_linear_clear_status(cp_linear* l) {
+  if (!l) return CP_ERR_INVALID_ARG;
+  DeviceGuard g(l->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return CP_ERR_CUDA;
+  if (cudaMemset(l->status, 0, 4) != cudaSuccess) return CP_ERR_CUDA;
+  return cuda_err(cudaDeviceSynchronize());
 }
 
 int cp_linear_unpack(cp_linear* l, void* out, cp_stream_t stream) {

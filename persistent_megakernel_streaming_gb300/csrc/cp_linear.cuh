@@ -2,15 +2,15 @@
 // arithmetic that the kernels share.
 //
 // Rows of the weights are taken 16 at a time (a tile), inputs 64 at a time (a
-// block). Lane 4 g + c of a warp holds rows g and g + 8 of a tile and inputs
-// 16 c .. 16 c + 15 of a block, one 16-byte word a block: 32-bit word j has
-// inputs 16 c + 4 j .. + 3, nibbles 0 to 3 the even ones of (row g: 0, row
-// g + 8: 0, row g: 2, row g + 8: 2), nibbles 4 to 7 the odd ones behind them.
-// A word thus becomes, by four masks and shifts, the four registers of an A
-// fragment of a 16 x 8 x 16 product whose inputs stand in an order of their
-// own (a sum over k does not mind), while the lane's part of x is 32
-// consecutive bytes. The tensor memory's 16-row stores have the same lanes, so
-// that the kernel for many rows reads the same words.
+// block). Lane 4 g + c of a warp holds rows g and g + 8 of a tile, one 16-byte
+// word a block: its 32-bit word j has inputs 16 j + 4 c .. + 3, nibbles 0 to 3
+// the even ones of (row g: 0, row g + 8: 0, row g: 2, row g + 8: 2), nibbles 4
+// to 7 the odd ones behind them. By four masks and shifts a word becomes the
+// four registers of an A fragment of a 16 x 8 x 16 product (whose inputs stand
+// in an order of their own: a sum over k does not mind, and a lane's part of x
+// is 8 consecutive bytes); and the tensor memory's stores of 16 rows by 256
+// bits want just these lanes and inputs, in their own order, so that x comes
+// as it lies there. Both kernels thus read the same words.
 //
 // A gated projection's tiles alternate: 16 rows of the gate, the same of up.
 #pragma once
@@ -38,6 +38,9 @@ struct Weights {
 
 struct ApplyParams {
   Weights w;
+  int32_t* status;           // sticky
+  long long timeout_ns;
+  int stall;                 // test: the first load is left out
   const uint16_t* x;
   int64_t x_row, out_row, add_row;
   void* out;
@@ -90,8 +93,28 @@ __device__ __forceinline__ void widen(uint32_t w, const Meta& m, uint32_t* a) {
     a[i] = bf2_mul(bf2_sub((w >> (4 * i) & 0x000f000fu) | 0x43004300u, m.z[i & 1]), m.s[i & 1]);
 }
 
+// The place of a lane's scales and zero points: of tile t, input k.
+__device__ __forceinline__ int64_t meta_at(const Weights& w, int t, int k, int g) {
+  return ((int64_t)t * w.groups + (k >> w.group_shift)) * 8 + g;
+}
+
+template <class T>
+__device__ __forceinline__ float load_out(const void* p, int64_t i);
+template <>
+__device__ __forceinline__ float load_out<float>(const void* p, int64_t i) { return static_cast<const float*>(p)[i]; }
+template <>
+__device__ __forceinline__ float load_out<__nv_bfloat16>(const void* p, int64_t i) {
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+__device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
 // Exact to fp32's rounding: the type of the result may be fp32.
 __device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+
+// Many rows: cp_linear_rows.cu. Once per device, with it current: its shared memory.
+cudaError_t prepare_many_rows();
+cudaError_t launch_many_rows(const ApplyParams& p, bool f32, cudaStream_t s);
 
 }  // namespace linear
 }  // namespace cp

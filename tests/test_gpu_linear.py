@@ -182,6 +182,19 @@ def test_streams_graphs_and_repeats():
         assert torch.equal(out.float(), 2 * want.float())
 
 
+def test_a_wait_that_runs_out_is_reported():
+    q, scale, z, x = make(256, 512, 64, False, 12, 40)
+    lin = cp.Linear(torch.from_numpy(q).cuda(), scale.cuda(), timeout_ns=50_000_000, debug_stall=True)
+    out = torch.zeros((40, 256), dtype=torch.float32, device="cuda")
+    lin.apply(x.cuda(), out)
+    assert lin.status() == cp.CP_ERR_TIMEOUT
+    lin.clear_status()
+    assert lin.status() == 0
+    lin.apply(x.cuda()[:9], out[:9])               # few rows come through no ring
+    assert lin.status() == 0
+    check(out[:9], *ref.apply(wide(x[:9]), ref.weights(q, wide(scale)), False), torch.float32)
+
+
 def test_refusals_on_the_gpu():
     q, scale, z, x = make(64, 128, 64, True, 0)
     lin = linear(q, scale, z)

@@ -37,7 +37,7 @@ def linear_check(d=None, a=None):
     (dict(q=None), INVALID), (dict(scale=None), INVALID), (dict(features=0), INVALID), (dict(width=0), INVALID),
     (dict(width=250), INVALID), (dict(group=0), INVALID), (dict(group=16), UNSUPPORTED), (dict(group=256), UNSUPPORTED),
     (dict(features=101, gated=1), INVALID), (dict(features=(1 << 24) + 1), UNSUPPORTED), (dict(width=(1 << 20) + 64), UNSUPPORTED),
-    (dict(width=-64), INVALID)])
+    (dict(width=-64), INVALID), (dict(timeout_ns=-1), INVALID), (dict(timeout_ns=5), OK)])
 def test_weights(d, want, L):
     assert linear_check(d) == want
     h = C.c_void_p()
@@ -51,7 +51,7 @@ def test_weights(d, want, L):
     (dict(out_dtype=2), INVALID), (dict(out_dtype=-1), INVALID), (dict(x=P + 8), UNSUPPORTED), (dict(x_stride=260), UNSUPPORTED),
     (dict(x_stride=-256), INVALID), (dict(out_stride=99), INVALID), (dict(out=P + 1), UNSUPPORTED),
     (dict(out_dtype=1, out=P + 2), UNSUPPORTED), (dict(add=P + 1), UNSUPPORTED), (dict(add=P, add_stride=-1), INVALID),
-    (dict(x_stride=1 << 41), UNSUPPORTED), (dict(out_stride=1 << 41), UNSUPPORTED)])
+    (dict(x_stride=1 << 39), UNSUPPORTED), (dict(x_stride=(1 << 39) - 8), OK), (dict(out_stride=1 << 41), UNSUPPORTED)])
 def test_applications(a, want):
     assert linear_check({}, a) == want
 
@@ -60,6 +60,7 @@ def test_null_objects_are_refused(L):
     assert L.cp_linear_check(None, None) == INVALID
     assert L.cp_linear_apply(None, C.byref(of(cp.LinearArgs, ARGS, {})), None) == INVALID
     assert L.cp_linear_unpack(None, P, None) == INVALID
+    assert L.cp_linear_status(None) == INVALID and L.cp_linear_clear_status(None) == INVALID
     assert L.cp_pages_check(None) == INVALID
     assert L.cp_pages_fork(None, P, P, 1, None) == INVALID and L.cp_pages_grow(None, P, P, 9, P, None) == INVALID
     assert L.cp_pages_trim(None, P, None) == INVALID and L.cp_pages_compact(None, P, 9, P, None) == INVALID
