@@ -651,8 +651,8 @@ typedef struct cp_linear cp_linear; /* opaque, owned by the library */
 
 /* Lay the weights out for the kernels, in memory that the object owns (about
  * what the arrays take; these may be freed on return). Errors:
- * CP_ERR_INVALID_ARG (a zero point above 15, too), CP_ERR_UNSUPPORTED (limits
- * or device), CP_ERR_NOMEM, CP_ERR_CUDA. It allocates and synchronises: not
+ * CP_ERR_INVALID_ARG (a zero point above 15, too), CP_ERR_UNSUPPORTED (limits,
+ * a finite scale of 2^122 or more, or the device), CP_ERR_NOMEM, CP_ERR_CUDA. It allocates and synchronises: not
  * while a stream is being captured. The object holds no scratch: calls on
  * several streams may overlap. */
 int cp_linear_create(const cp_linear_desc* desc, int device, cp_linear** out);

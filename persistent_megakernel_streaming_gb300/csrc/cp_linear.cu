@@ -28,67 +28,71 @@ struct PackParams {
   const uint8_t* q;
   const uint16_t* scale;
   const uint8_t* zero;
-  uint4* w_out;
-  uint32_t* scale_out;
-  uint16_t* zero_out;
+  uint8_t* out;
   int* bad;
 };
 
+// A thread a lane's word; lanes 0 .. 7 of a tile write its scales and zero points too.
 __global__ void pack_kernel(const PackParams p) {
   const Weights& w = p.w;
-  const int64_t lanes = (int64_t)w.tiles * w.blocks * 32, step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < lanes; i += step) {
+  const int64_t words = (int64_t)w.tiles * w.per_piece * 2 * 32, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < words; i += step) {
     const int lane = (int)(i & 31), g = lane >> 2, c = lane & 3;
     const int64_t rest = i >> 5;
-    const int b = (int)(rest % w.blocks), t = (int)(rest / w.blocks);
+    const int t = (int)(rest % w.tiles), k0 = (int)(rest / w.tiles) * kBlockK;
+    uint8_t* record = p.out + record_at(w, t, k0);
     uint32_t out[4];
     for (int j = 0; j < 4; ++j) {
       out[j] = 0;
       for (int a = 0; a < 4; ++a) {
-        const int row = row_of(w, t, g + (a & 1) * 8), k = b * kBlockK + 16 * j + 4 * c + (a >> 1) * 2;
+        const int row = row_of(w, t, g + (a & 1) * 8), k = k0 + 16 * j + 4 * c + (a >> 1) * 2;
         if (row < 0 || k >= w.width) continue;
         const uint32_t two = p.q[(int64_t)row * (w.width / 2) + k / 2];
         out[j] |= (two & 15) << (4 * a) | (two >> 4) << (16 + 4 * a);
       }
     }
-    p.w_out[i] = make_uint4(out[0], out[1], out[2], out[3]);
-  }
-  const int64_t metas = (int64_t)w.tiles * w.groups * 8;
-  const int held = w.width >> w.group_shift;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < metas; i += step) {
-    const int g = (int)(i & 7);
-    const int64_t rest = i >> 3;
-    const int grp = (int)(rest % w.groups), t = (int)(rest / w.groups);
-    uint32_t s = 0, z = 0;
-    for (int h = 0; h < 2; ++h) {
-      const int row = row_of(w, t, g + 8 * h);
-      if (row < 0 || grp >= held) continue;        // rows and inputs that are not there weigh nothing
-      const int64_t at = (int64_t)row * held + grp;
-      s |= (uint32_t)p.scale[at] << (16 * h);
-      if (p.zero) {
-        z |= (uint32_t)p.zero[at] << (8 * h);
-        if (p.zero[at] > 15) *p.bad = 1;
+    *reinterpret_cast<uint4*>(record + word_in(t, k0, lane)) = make_uint4(out[0], out[1], out[2], out[3]);
+    if (lane >= 8) continue;
+    for (int k = k0; k < k0 + kBlockK; k += 32) {              // a group of more is written by each of its blocks, alike
+      uint32_t s = 0, z = 0;
+      for (int h = 0; h < 2; ++h) {
+        const int row = row_of(w, t, lane + 8 * h);
+        if (row < 0 || k >= w.width) continue;               // rows and inputs that are not there weigh nothing
+        const int64_t at = (int64_t)row * (w.width >> w.group_shift) + (k >> w.group_shift);
+        const uint32_t up = __bfloat16_as_ushort(__float2bfloat16_rn(64.f * __uint_as_float((uint32_t)p.scale[at] << 16)));
+        if ((up & 0x7fff) == 0x7f80 && (p.scale[at] & 0x7fff) != 0x7f80) atomicOr(p.bad, 2);
+        s |= up << (16 * h);
+        if (p.zero) {
+          z |= (uint32_t)p.zero[at] << (8 * h);
+          if (p.zero[at] > 15) atomicOr(p.bad, 1);
+        }
       }
+      *reinterpret_cast<uint32_t*>(record + scale_in(w, t, k, lane)) = s;
+      if (p.zero) *reinterpret_cast<uint16_t*>(record + zero_in(w, t, k, lane)) = (uint16_t)z;
     }
-    p.scale_out[i] = s;
-    if (p.zero) p.zero_out[i] = (uint16_t)z;
   }
 }
 
+// A lane's scales and zero points of a record.
+__device__ __forceinline__ Meta load_meta(const Weights& w, const uint8_t* record, int t, int k, int g) {
+  const uint32_t s = *reinterpret_cast<const uint32_t*>(record + scale_in(w, t, k, g));
+  return meta_of(s, w.zero ? *reinterpret_cast<const uint16_t*>(record + zero_in(w, t, k, g)) : kNoZero);
+}
+
 __global__ void unpack_kernel(const Weights w, uint16_t* out) {
-  const int64_t lanes = (int64_t)w.tiles * w.blocks * 32, step = (int64_t)gridDim.x * blockDim.x;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < lanes; i += step) {
+  const int64_t words = (int64_t)w.tiles * w.per_piece * 2 * 32, step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < words; i += step) {
     const int lane = (int)(i & 31), g = lane >> 2, c = lane & 3;
     const int64_t rest = i >> 5;
-    const int b = (int)(rest % w.blocks), t = (int)(rest / w.blocks);
-    const uint4 v = w.w[i];
-    const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+    const int t = (int)(rest % w.tiles), k0 = (int)(rest / w.tiles) * kBlockK;
+    const uint8_t* record = w.records + record_at(w, t, k0);
+    const uint4 v = *reinterpret_cast<const uint4*>(record + word_in(t, k0, lane));
+    const uint32_t of[4] = {v.x, v.y, v.z, v.w};
     for (int j = 0; j < 4; ++j) {
       uint32_t a[4];
-      const int64_t at = meta_at(w, t, b * kBlockK + 16 * j, g);
-      widen(words[j], meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero), a);
+      widen(of[j], load_meta(w, record, t, k0 + 16 * j, g), a);
       for (int x = 0; x < 4; ++x) {
-        const int row = row_of(w, t, g + (x & 1) * 8), k = b * kBlockK + 16 * j + 4 * c + (x >> 1) * 2;
+        const int row = row_of(w, t, g + (x & 1) * 8), k = k0 + 16 * j + 4 * c + (x >> 1) * 2;
         if (row < 0 || k >= w.width) continue;
         out[(int64_t)row * w.width + k] = (uint16_t)a[x];
         out[(int64_t)row * w.width + k + 1] = (uint16_t)(a[x] >> 16);
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int t0 = blockIdx.x * 2, row0 = blockIdx.y * 8 * NT;
   float acc[2][NT][4] = {};
-  for (int b = warp; b < w.blocks; b += kWarps) {
+  for (int b = warp; b * kBlockK < w.width; b += kWarps) {
     uint2 x[NT][4];
     const int k = b * kBlockK;
 #pragma unroll
@@ -128,12 +132,12 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
     }
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const uint4 v = w.w[((int64_t)(t0 + t) * w.blocks + b) * 32 + lane];
+      const uint8_t* record = w.records + record_at(w, t0 + t, k);
+      const uint4 v = *reinterpret_cast<const uint4*>(record + word_in(t0 + t, k, lane));
       const uint32_t words[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {                // groups of 32 have two in a block
-        const int64_t at = meta_at(w, t0 + t, k + 32 * h, g);
-        const Meta m = meta_of(w.scale[at], w.zero ? w.zero[at] : kNoZero);
+        const Meta m = load_meta(w, record, t0 + t, k + 32 * h, g);
 #pragma unroll
         for (int j = 2 * h; j < 2 * h + 2; ++j) {
           uint32_t a[4];
@@ -191,8 +195,10 @@ int check_desc(const cp_linear_desc* d, Weights* w) {
   w->outs = d->gated ? d->features / 2 : d->features;
   const int tiles = (w->outs + kTileRows - 1) / kTileRows * (d->gated ? 2 : 1);
   w->tiles = (tiles + kPadTiles - 1) / kPadTiles * kPadTiles;
-  w->blocks = (d->width + kBlockK - 1) / kBlockK;
-  w->groups = (w->blocks * kBlockK + d->group - 1) / d->group;
+  w->zero = d->zero != nullptr;
+  w->per_piece = (d->width + kRecordK - 1) / kRecordK;
+  w->groups = kRecordK / d->group;
+  w->bytes = kRecordWords + w->groups * (kRecordScales + (w->zero ? kRecordZeros : 0));
   return CP_OK;
 }
 
@@ -215,10 +221,10 @@ int check_args(const Weights& w, const cp_linear_args* a, ApplyParams* p) {
   const uintptr_t es = a->out_dtype == CP_OUT_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(a->out) % es || reinterpret_cast<uintptr_t>(a->add) % es) return CP_ERR_UNSUPPORTED;
   if (!lie_apart(w.outs, {{a->rows, p->out_row}})) return CP_ERR_INVALID_ARG;
+  const auto four = [es](const void* at, int64_t row) { return reinterpret_cast<uintptr_t>(at) % (4 * es) == 0 && row % 4 == 0; };
+  p->by_four = four(a->out, p->out_row) && (!a->add || four(a->add, p->add_row));
   return CP_OK;
 }
-
-size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
@@ -247,24 +253,18 @@ int cp_linear_create(const cp_linear_desc* desc, int device, cp_linear** out) {
   cp_linear* l = new (std::nothrow) cp_linear();
   if (!l) return CP_ERR_NOMEM;
   l->device = device;
-  const size_t w_bytes = up256((size_t)w.tiles * w.blocks * 512), metas = (size_t)w.tiles * w.groups * 8;
-  const size_t zero_bytes = desc->zero ? up256(metas * 2) : 0;
-  if (cudaMalloc(&l->memory, w_bytes + up256(metas * 4) + zero_bytes + 256) != cudaSuccess) {
+  const size_t bytes = (size_t)(w.tiles / kPadTiles) * w.per_piece * w.bytes;
+  if (cudaMalloc(&l->memory, bytes + 256) != cudaSuccess) {          // records are multiples of 128 bytes
     cudaGetLastError();
     delete l;
     return CP_ERR_NOMEM;
   }
-  uint8_t* at = static_cast<uint8_t*>(l->memory);
-  p.w_out = reinterpret_cast<uint4*>(at);
-  p.scale_out = reinterpret_cast<uint32_t*>(at + w_bytes);
-  p.zero_out = desc->zero ? reinterpret_cast<uint16_t*>(at + w_bytes + up256(metas * 4)) : nullptr;
-  p.bad = reinterpret_cast<int*>(at + w_bytes + up256(metas * 4) + zero_bytes);
+  p.out = static_cast<uint8_t*>(l->memory);
+  p.bad = reinterpret_cast<int*>(p.out + bytes);
   p.q = static_cast<const uint8_t*>(desc->q);
   p.scale = static_cast<const uint16_t*>(desc->scale);
   p.zero = static_cast<const uint8_t*>(desc->zero);
-  w.w = p.w_out;
-  w.scale = p.scale_out;
-  w.zero = p.zero_out;
+  w.records = p.out;
   l->w = w;
   l->status = p.bad + 1;
   l->timeout_ns = desc->timeout_ns ? desc->timeout_ns : 2000000000ll;
@@ -278,7 +278,7 @@ int cp_linear_create(const cp_linear_desc* desc, int device, cp_linear** out) {
   }
   if (!ok || bad) {
     cp_linear_destroy(l);
-    return bad ? CP_ERR_INVALID_ARG : CP_ERR_CUDA;
+    return bad & 1 ? CP_ERR_INVALID_ARG : bad ? CP_ERR_UNSUPPORTED : CP_ERR_CUDA;
   }
   *out = l;
   return CP_OK;

@@ -4,15 +4,20 @@
 // A block takes up to FT times 128 rows of the weights (features), up to 256
 // rows of x, and a share of the inputs; a cluster's blocks have the same
 // features and rows and different inputs, and join their sums through
-// distributed shared memory. For each 64 inputs and 128 features the weights
-// are the A operand, widened to bf16 in registers and put into tensor memory
-// (D[feature][row of x] += A[feature][64] B[row of x][64]); x is the B operand,
-// brought in by tensor-map copies as it lies.
+// distributed shared memory. For each record (128 features by 128 inputs) the
+// weights are the A operand, widened to bf16 in registers and put into tensor
+// memory (D[feature][row of x] += A[feature][128] B[row of x][128]); x is the B
+// operand, brought in by tensor-map copies as it lies.
 //
-// Warps 0-7 widen: warp w has the 32 features of TMEM lanes 32 (w % 4), and
-// every second piece of weights (128 features by 64 inputs), which it loads
-// kAhead pieces ahead into registers; at the end they write the results. Warp
-// 8 issues the products, warp 9 the copies of x.
+// One lane brings the records into a ring in shared memory, one x; the others
+// widen: warp w has the 32 features of TMEM lanes 32 (w % 4) of every
+// kGroups-th record; at the end they write the results. The records' products
+// go in turn to two or four streams, each with an issuing lane and sums of its
+// own: what a lane does between two records' products (waits, commits) takes
+// about as long as they do, and with one lane nothing covers it (64 rows, 16384
+// to 8192: 32 us). (Weights loaded ahead into the widening warps' own registers: a
+// warp's outstanding loads share few scoreboards, and waiting for the oldest
+// waits for the newest.)
 #include <cuda.h>
 
 #include "cp_cache_ptx.cuh"
@@ -24,33 +29,52 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kWidenWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
-constexpr int kAhead = 4;
-constexpr int kMostRows = 256;          // of x, a block
-constexpr int kMostStages = 8;
-constexpr int kSlots = 4;               // pieces of weights in tensor memory: columns 384 ..
-constexpr uint32_t kTmemA = 384, kTmemCols = 512;
+constexpr int kGroups = 4;               // of four widening warps
+constexpr int kMostStreams = 4;
+constexpr int kWidenWarps = 4 * kGroups, kMmaWarp = kWidenWarps, kWeightWarp = kMmaWarp + kMostStreams, kXWarp = kWeightWarp + 1;
+constexpr int kThreads = (kXWarp + 1) * 32;
+constexpr int kMostRows = 192;           // of x, a block
+constexpr int kMostStages = 8;           // of x's ring: 128 inputs each
+constexpr int kUnits = 8;                // records in the weights' ring, a power of two
+constexpr int kMostSlots = 4;            // widened records in tensor memory, 64 columns each: the last 128 or 256 columns
+constexpr uint32_t kTmemCols = 512;
 constexpr int kMostCluster = 8;
-constexpr int kSmem = 200 * 1024;       // x's ring, and at the end the sums that the cluster joins
+constexpr int kRing = kUnits * kMostRecord;
+constexpr int kSmem = 216 * 1024;        // both rings, and at the end the sums that the cluster joins
 
 struct Plan {
-  int ft;             // 128-feature pieces a block
+  int ft;             // 128-feature pieces a block: 1, or up to as many as streams, which it divides
+  int streams;        // 2 or 4: records' products by turns; stream s has the sums of piece s % ft
   int cluster;        // shares of the inputs
   int n;              // rows of x a block, a multiple of 16
   int chunks;         // blocks along the rows
-  int stages;
+  int stages;         // of x's ring
+  int slots;          // 2 or 4
+};
+
+// A place in a ring and the parity of its turn round it, by counting: a quotient takes one warp 100 to 200 clocks, and
+// with several of them for each unit the issuing warps were what the kernel waited for (64 rows, 16384 to 8192: 100 us).
+struct Turn {
+  int at = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next(int n, int by = 1) {      // by up to n
+    at += by;
+    if (at >= n) {
+      at -= n;
+      parity ^= 1;
+    }
+  }
 };
 
 struct RowsShared {
-  uint64_t a_full[kSlots], a_empty[kSlots], b_full[kMostStages], b_empty[kMostStages], d_full;
+  uint64_t w_full[kUnits], w_empty[kUnits], a_full[kMostSlots], a_empty[kMostSlots], b_full[kMostStages], b_empty[kMostStages], d_full;
   uint32_t tmem;
   long long timeout_ns;
   int abort;          // a wait gave up
 };
 
 // Bounded: after the timeout, or once another wait of the block gave up, false.
-__device__ __forceinline__ bool wait_bar(RowsShared& sh, uint32_t bar, uint32_t parity) {
-  if (mb_try(bar, parity)) return true;
+__device__ __noinline__ bool wait_long(RowsShared& sh, uint32_t bar, uint32_t parity) {
   const uint64_t t0 = gtime();
   for (;;) {
 #pragma unroll 1
@@ -62,6 +86,9 @@ __device__ __forceinline__ bool wait_bar(RowsShared& sh, uint32_t bar, uint32_t 
       return false;
     }
   }
+}
+__device__ __forceinline__ bool wait_bar(RowsShared& sh, uint32_t bar, uint32_t parity) {
+  return mb_try(bar, parity) || wait_long(sh, bar, parity);
 }
 __device__ __forceinline__ bool wait_warp(RowsShared& sh, uint32_t bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_bar(sh, bar, parity));
@@ -82,36 +109,69 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int c
       : "memory");
 }
 
-// A lane's part of a piece: two tiles' words, and their scales and zero points (of both halves of the 64 inputs).
-struct Piece {
-  uint4 w[2];
-  uint32_t s[2][2];
-  uint32_t z[2][2];
-};
+// One lane of the warp, always the same. Behind this the compiler knows that one lane is left, and keeps what the
+// products and copies are given in uniform registers, if it comes from uniform values: a product every 28 clocks (32
+// rows of x; 42 for 64, 90 for 160). Behind `lane == 0`, or predicated in a warp that stays together, it took 100 to
+// 130 whatever the rows, and the whole kernel 76 us instead of what stands above.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one)
+      :
+      : "memory");
+  return one != 0;
+}
+// A in tensor memory, B in shared memory.
+__device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t"
+      "setp.ne.b32 P, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, P;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
 
-template <class T>
+template <class T, bool ZERO>
 __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_constant__ ApplyParams p, const __grid_constant__ Plan plan,
                                                                 const __grid_constant__ CUtensorMap map) {
   extern __shared__ __align__(1024) uint8_t raw[];
   __shared__ RowsShared sh;
-  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   const Weights& w = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = plan.cluster, rank = blockIdx.x % S, piece0 = blockIdx.x / S * plan.ft;
-  const int ft = min(plan.ft, w.tiles / 8 - piece0), n = plan.n;
+  const int ft = plan.ft, n = plan.n;
   const int row0 = blockIdx.y * n;
-  const int b0 = (int)((int64_t)w.blocks * rank / S), b1 = (int)((int64_t)w.blocks * (rank + 1) / S);
-  const uint32_t stage_bytes = (uint32_t)n * 128;
+  const int b0 = (int)((int64_t)w.per_piece * rank / S), b1 = (int)((int64_t)w.per_piece * (rank + 1) / S);   // records
+  const uint32_t stage_bytes = (uint32_t)n * 256;    // two halves of 64 inputs
+  const uint32_t x_ring = (saddr(raw) + 1023) & ~1023u, w_ring = x_ring + plan.stages * stage_bytes;
+  const int slots = plan.slots;
+  const uint32_t tmem_a = kTmemCols - slots * 64;
 
-  if (warp == kLoadWarp) {
-    if (lane < kSlots) {
-      mb_init(saddr(&sh.a_full[lane]), 4);
-      mb_init(saddr(&sh.a_empty[lane]), 1);
-    } else if (lane < kSlots + kMostStages) {
-      mb_init(saddr(&sh.b_full[lane - kSlots]), 1);
-      mb_init(saddr(&sh.b_empty[lane - kSlots]), 1);
+  if (warp == kWeightWarp) {
+    if (lane < kUnits) {
+      mb_init(saddr(&sh.w_full[lane]), 1);
+      mb_init(saddr(&sh.w_empty[lane]), 4);
+    } else if (lane < kUnits + kMostSlots) {
+      mb_init(saddr(&sh.a_full[lane - kUnits]), 4);
+      mb_init(saddr(&sh.a_empty[lane - kUnits]), 1);
+    } else if (lane < kUnits + kMostSlots + kMostStages) {
+      mb_init(saddr(&sh.b_full[lane - kUnits - kMostSlots]), 1);
+      mb_init(saddr(&sh.b_empty[lane - kUnits - kMostSlots]), ft);
     } else if (lane == 31) {
-      mb_init(saddr(&sh.d_full), 1);
+      mb_init(saddr(&sh.d_full), plan.streams);
       sh.abort = 0;
       sh.timeout_ns = p.timeout_ns;
     }
@@ -124,110 +184,132 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   tm_fence_before();
   __syncthreads();
   tm_fence_after();
-  const uint32_t tmem = sh.tmem;
+  constexpr uint32_t tmem = 0;             // all of it is the block's: it starts at its first column
   const int units = (b1 - b0) * ft;
 
   if (warp < kWidenWarps) {
     // ---------------------------------------------------------------- widen
     const int quarter = warp & 3, g = lane >> 2;
-    const bool zeros = w.zero != nullptr;
-    Piece ahead[kAhead];
-    // piece u: block b0 + u / ft, features piece0 + u % ft
-    auto load = [&](int u, Piece& x) {
-      if (u >= units) return;
-      const int b = b0 + u / ft, t = (piece0 + u % ft) * 8 + quarter * 2;
+    const int slot_shift = slots == 4 ? 2 : 1, group_shift = w.group_shift;
+    const uint32_t zeros = kRecordWords + w.groups * kRecordScales;
+    // a group for each slot at most: each then waits for its own last unit's products, and a turn's parity says which
+    const int groups = min(kGroups, slots);
+    for (int u = (warp >> 2) < groups ? warp >> 2 : units; u < units; u += groups) {
+      const int unit = u & (kUnits - 1), slot = u & (slots - 1);
+      if (!wait_warp(sh, saddr(&sh.w_full[unit]), (uint32_t)(u / kUnits) & 1)) break;
+      const uint32_t at = w_ring + unit * kMostRecord, own = quarter * 16 + g;
+      const uint32_t to = tmem + ((uint32_t)(quarter * 32) << 16) + tmem_a + slot * 64;
+      bool ok = true;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x.w[i] = w.w[((int64_t)(t + i) * w.blocks + b) * 32 + lane];
+      for (int sub = 0; sub < 2; ++sub) {
+        uint32_t r[2][16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int64_t at = meta_at(w, t + i, b * kBlockK + 32 * h, g);
-          x.s[i][h] = w.scale[at];
-          x.z[i][h] = zeros ? w.zero[at] : kNoZero;
+        for (int i = 0; i < 2; ++i) {
+          const uint4 words = ld_shared_v4u(at + sub * 4096 + (quarter * 2 + i) * 512 + lane * 16);
+          const uint32_t v[4] = {words.x, words.y, words.z, words.w};
+          Meta m;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j == 0 || (j == 2 && group_shift == 5)) {
+              const int grp = (sub * 64 + j * 16) >> group_shift;
+              const uint32_t s = ld_shared_u32(at + kRecordWords + grp * kRecordScales + (own + i * 8) * 4);
+              m = meta_of(s, ZERO ? ld_shared_u16(at + zeros + grp * kRecordZeros + (own + i * 8) * 2) : kNoZero);
+            }
+            uint32_t a[4];
+            widen(v[j], m, a);
+            r[i][4 * j] = a[0];
+            r[i][4 * j + 1] = a[2];
+            r[i][4 * j + 2] = a[1];
+            r[i][4 * j + 3] = a[3];
+          }
         }
-      }
-    };
-    auto put = [&](int u, const Piece& x) {
-      const int slot = u % kSlots;
-      if (u >= kSlots && !wait_warp(sh, saddr(&sh.a_empty[slot]), (u / kSlots - 1) & 1)) return false;
-      tm_fence_after();
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t words[4] = {x.w[i].x, x.w[i].y, x.w[i].z, x.w[i].w};
-        uint32_t r[16];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a[4];
-          widen(words[j], meta_of(x.s[i][j >> 1], x.z[i][j >> 1]), a);
-          r[4 * j] = a[0];
-          r[4 * j + 1] = a[2];
-          r[4 * j + 2] = a[1];
-          r[4 * j + 3] = a[3];
+        // the first half is widened while the products out of the slot's last unit still run
+        if (sub == 0) {
+          ok = wait_warp(sh, saddr(&sh.a_empty[slot]), ((uint32_t)(u >> slot_shift) & 1) ^ 1);     // at first: free
+          if (!ok) break;
+          tm_fence_after();
         }
-        tm_st_16x256b_x4(tmem + ((uint32_t)(quarter * 32 + i * 16) << 16) + kTmemA + slot * 32, r);
+        tm_st_16x256b_x4(to + sub * 32, r[0]);
+        tm_st_16x256b_x4(to + (16 << 16) + sub * 32, r[1]);
       }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mb_arrive(saddr(&sh.w_empty[unit]));
       tm_wait_st();
       tm_fence_before();
       __syncwarp();
       if (lane == 0) mb_arrive(saddr(&sh.a_full[slot]));
-      return true;
-    };
-    const int first = warp >> 2;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) load(first + 2 * k, ahead[k]);
-    bool ok = true;
-    for (int u = first; u < units && ok; u += 2 * kAhead) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int at = u + 2 * k;
-        if (at < units && ok) {
-          ok = put(at, ahead[k]);
-          load(at + 2 * kAhead, ahead[k]);
+    }
+  } else if (warp == kWeightWarp) {
+    // ---------------------------------------------------------------- weights
+    if (elect_one()) {
+      // a last group of fewer pieces has its last one again: nothing else is to know of it but the results
+      const int last = w.tiles / 8 - 1 - piece0;
+      const uint8_t* from = w.records + record_at(w, piece0 * 8, b0 * kRecordK);
+      const int64_t next_piece = (int64_t)w.per_piece * w.bytes;
+      int asked = 0, f = 0;
+      Turn unit;
+      for (; asked < units; ++asked) {
+        if (!wait_bar(sh, saddr(&sh.w_empty[unit.at]), unit.parity ^ 1)) break;
+        const uint32_t bar = saddr(&sh.w_full[unit.at]);
+        mb_expect(bar, w.bytes);
+        bulk_g2s(w_ring + unit.at * kMostRecord, from + min(f, last) * next_piece, w.bytes, bar);
+        unit.next(kUnits);
+        if (++f == ft) {
+          f = 0;
+          from += w.bytes;
         }
       }
+      // what was asked for lands before the block may end, whatever ended the loop
+      for (int u = max(0, asked - kUnits); u < asked; ++u)
+        for (int k = 0; k < (1 << 20) && !mb_try(saddr(&sh.w_full[u & (kUnits - 1)]), (uint32_t)(u / kUnits) & 1); ++k) {
+        }
     }
-  } else if (warp == kLoadWarp) {
+  } else if (warp == kXWarp) {
     // ---------------------------------------------------------------- x
-    int asked = 0;
-    for (int i = 0; i < b1 - b0; ++i) {
-      const int stage = i % plan.stages;
-      if (i >= plan.stages && !wait_warp(sh, saddr(&sh.b_empty[stage]), (i / plan.stages - 1) & 1)) break;
-      asked = i + 1;
-      if (i == 0 && p.stall) continue;
-      if (lane == 0) {
-        mb_expect(saddr(&sh.b_full[stage]), stage_bytes);
-        tma_load_2d(saddr(ring) + stage * stage_bytes, &map, (b0 + i) * kBlockK, row0, saddr(&sh.b_full[stage]));
+    if (elect_one()) {
+      Turn stage;
+      int asked = 0;
+      for (; asked < b1 - b0; ++asked) {
+        const uint32_t bar = saddr(&sh.b_full[stage.at]), at = x_ring + stage.at * stage_bytes;
+        if (!wait_bar(sh, saddr(&sh.b_empty[stage.at]), stage.parity ^ 1)) break;
+        if (asked > 0 || !p.stall) {
+          mb_expect(bar, stage_bytes);
+          tma_load_2d(at, &map, (b0 + asked) * kRecordK, row0, bar);
+          tma_load_2d(at + stage_bytes / 2, &map, (b0 + asked) * kRecordK + kBlockK, row0, bar);
+        }
+        stage.next(plan.stages);
       }
-      __syncwarp();
+      // what was asked for lands before the block may end, whatever ended the loop
+      for (int i = max(p.stall ? 1 : 0, asked - plan.stages); i < asked; ++i)
+        for (int k = 0; k < (1 << 20) && !mb_try(saddr(&sh.b_full[i % plan.stages]), (i / plan.stages) & 1); ++k) {
+        }
     }
-    // what was asked for lands before the block may end, whatever ended the loop
-    for (int i = max(p.stall ? 1 : 0, asked - plan.stages); i < asked; ++i)
-      for (int k = 0; k < (1 << 20) && !__all_sync(0xffffffffu, mb_try(saddr(&sh.b_full[i % plan.stages]), (i / plan.stages) & 1)); ++k) {
-      }
-  } else {
+  } else if (warp - kMmaWarp < plan.streams) {
     // ---------------------------------------------------------------- products
-    const uint32_t lead = lane == 0, id = idesc_bf16_m128(n);
-    const uint64_t b_desc = sdesc_sw128(saddr(ring));
-    bool ok = true;
-    for (int i = 0; i < b1 - b0 && ok; ++i) {
-      const int stage = i % plan.stages;
-      ok = wait_warp(sh, saddr(&sh.b_full[stage]), (i / plan.stages) & 1);
-      const uint64_t b = b_desc + (uint64_t)(stage * (stage_bytes >> 4));
-      for (int f = 0; f < ft && ok; ++f) {
-        const int u = i * ft + f, slot = u % kSlots;
-        ok = wait_warp(sh, saddr(&sh.a_full[slot]), (u / kSlots) & 1);
-        if (!ok) break;
+    if (elect_one()) {
+      const int own = warp - kMmaWarp, streams = plan.streams, step = streams / ft;
+      const uint32_t id = idesc_bf16_m128(n), stage_desc = stage_bytes >> 4, d = tmem + own * n;
+      const uint64_t b_desc = sdesc_sw128(x_ring);
+      Turn stage, slot;
+      stage.next(plan.stages, own / ft);
+      slot.at = own;
+      for (int i = own / ft; i < b1 - b0; i += step) {
+        if (!wait_bar(sh, saddr(&sh.b_full[stage.at]), stage.parity) || !wait_bar(sh, saddr(&sh.a_full[slot.at]), slot.parity)) break;
         tm_fence_after();
+        const uint64_t x0 = b_desc + stage.at * stage_desc, x1 = x0 + stage_desc / 2;
+        const uint32_t a = tmem + tmem_a + slot.at * 64;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tm_mma_ts_lead(lead, tmem + f * n, tmem + kTmemA + slot * 32 + k * 8, b + 2 * k, id, i > 0 || k > 0);
-        tm_commit_lead(lead, saddr(&sh.a_empty[slot]));
+        for (int k = 0; k < 8; ++k) tm_mma_ts(d, a + k * 8, (k < 4 ? x0 : x1) + 2 * (k & 3), id, i >= step || k > 0);
+        tm_commit(saddr(&sh.a_empty[slot.at]));
+        tm_commit(saddr(&sh.b_empty[stage.at]));
+        slot.next(slots, streams);
+        stage.next(plan.stages, step);
       }
-      if (ok) tm_commit_lead(lead, saddr(&sh.b_empty[stage]));
-    }
-    tm_commit_lead(lead, saddr(&sh.d_full));
-    // the products in flight end before anything is read or given back, even after a wait that gave up
-    for (int k = 0; k < (1 << 20) && !__all_sync(0xffffffffu, mb_try(saddr(&sh.d_full), 0)); ++k) {
+      tm_commit(saddr(&sh.d_full));
+      // the products in flight end before anything is read or given back, even after a wait that gave up
+      for (int k = 0; k < (1 << 20) && !mb_try(saddr(&sh.d_full), 0); ++k) {
+      }
     }
   }
   __syncwarp();
@@ -237,25 +319,20 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   if (failed && threadIdx.x == 0) atomicCAS(p.status, 0, (int)CP_ERR_TIMEOUT);
 
   // Results. Feature i of a piece is in TMEM lane i, row r of x in column r.
-  const int rows_here = min(n, p.rows - row0);
-  T* out = static_cast<T*>(p.out);
-  auto finish = [&](int r, int feature, float y) {
-    if (p.add) y += load_out<T>(p.add, (int64_t)(row0 + r) * p.add_row + feature);
-    store_out(out + (int64_t)(row0 + r) * p.out_row + feature, y);
-  };
-  float* sums = reinterpret_cast<float*>(ring);            // [row][features of the block]
+  const int rows_here = min(n, p.rows - row0), here = min(ft, w.tiles / 8 - piece0);
+  float* sums = reinterpret_cast<float*>(raw + (x_ring - saddr(raw)));      // [row][features of the block]
   const int wide = plan.ft * 128;
   if (warp < kWidenWarps && !failed) {
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, part = warp >> 2;
     const uint32_t lanes = (uint32_t)quarter << 21;
-    for (int f = 0; f < ft; ++f) {
-      for (int c = half * 16; c < n; c += 32) {
-        float v[16];
-        if (b1 > b0) {
-          tm_ld16(tmem + lanes + f * n + c, v);
-        } else {
+    for (int f = 0; f < here; ++f) {
+      for (int c = part * 16; c < n; c += 16 * kGroups) {
+        float v[16] = {};
+        for (int s = f; s < plan.streams && s / ft < b1 - b0; s += ft) {       // its streams that had any products
+          float x[16];
+          tm_ld16(tmem + lanes + s * n + c, x);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) v[x] = 0.f;
+          for (int k = 0; k < 16; ++k) v[k] += x[k];
         }
         if (S > 1) {
 #pragma unroll
@@ -265,13 +342,16 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const float up = __shfl_xor_sync(0xffffffffu, v[x], 16);
-            if (lane < 16 && feature < w.outs && c + x < rows_here) finish(c + x, feature, silu(v[x]) * up);
+            if (lane < 16 && feature < w.outs && c + x < rows_here) {
+              float y = silu(v[x]) * up;
+              finish<T>(p, row0 + c + x, feature, 1, &y);
+            }
           }
         } else {
           const int feature = (piece0 + f) * 128 + quarter * 32 + lane;
 #pragma unroll
           for (int x = 0; x < 16; ++x)
-            if (feature < w.outs && c + x < rows_here) finish(c + x, feature, v[x]);
+            if (feature < w.outs && c + x < rows_here) finish<T>(p, row0 + c + x, feature, 1, v + x);
         }
       }
     }
@@ -280,23 +360,34 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   if (S > 1) {
     __syncwarp();
     cluster_sync_all();
-    // each of the cluster's blocks takes every S-th row, and adds up in the blocks' order
-    const int per = w.gated ? wide / 2 : wide;
+    // each of the cluster's blocks takes every S-th row, four features a thread, and adds up in the blocks' order; all
+    // loads from other blocks' memory are under way before the first is waited for
+    const int fours = (w.gated ? here * 64 : here * 128) / 4, items = (rows_here - rank + S - 1) / S * fours;
     if (!failed)
-      for (int r = rank; r < rows_here; r += S)
-        for (int i = threadIdx.x; i < per; i += kThreads) {
-          const int at = w.gated ? (i >> 4) * 32 + (i & 15) : i;
-          const uint32_t mine = saddr(sums + r * wide + at);
-          float y = 0.f, up = 0.f;
-          for (int k = 0; k < S; ++k) {
-            const uint32_t from = mapa(mine, k);
-            y += ld_cluster(from);
-            if (w.gated) up += ld_cluster(from + 64);
+      for (int i = threadIdx.x; i < items; i += kThreads) {
+        const int r = rank + i / fours * S, f = i % fours * 4;
+        const int at = w.gated ? (f >> 4) * 32 + (f & 15) : f;
+        const uint32_t mine = saddr(sums + r * wide + at);
+        float4 v[kMostCluster], u[kMostCluster];
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k)
+          if (k < S) {
+            v[k] = ld_cluster_v4(mapa(mine, k));
+            if (w.gated) u[k] = ld_cluster_v4(mapa(mine, k) + 64);
           }
-          if (w.gated) y = silu(y) * up;
-          const int feature = piece0 * (w.gated ? 64 : 128) + i;
-          if (feature < w.outs && i < ft * (w.gated ? 64 : 128)) finish(r, feature, y);
-        }
+        float y[4] = {}, up[4] = {};
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k)
+          if (k < S) {
+            y[0] += v[k].x; y[1] += v[k].y; y[2] += v[k].z; y[3] += v[k].w;
+            if (w.gated) up[0] += u[k].x, up[1] += u[k].y, up[2] += u[k].z, up[3] += u[k].w;
+          }
+        if (w.gated)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[k] = silu(y[k]) * up[k];
+        const int feature = piece0 * (w.gated ? 64 : 128) + f;
+        if (feature < w.outs) finish<T>(p, row0 + r, feature, min(4, w.outs - feature), y);
+      }
     __syncwarp();
     cluster_sync_all();
   } else {
@@ -318,25 +409,32 @@ Plan make_plan(const ApplyParams& p) {
   const int pieces = p.w.tiles / 8;
   a.ft = 1;
   a.cluster = 1;
-  while (a.cluster < kMostCluster && pieces * a.chunks * a.cluster * 2 <= 152 && p.w.blocks >= a.cluster * 4) a.cluster *= 2;
-  a.stages = kSmem / (a.n * 128);
+  while (a.cluster < kMostCluster && pieces * a.chunks * a.cluster * 2 <= 152 && p.w.per_piece >= a.cluster * 2) a.cluster *= 2;
+  a.streams = a.n <= 64 ? 4 : 2;
+  a.stages = (kSmem - kRing) / (a.n * 256);
   if (a.stages > kMostStages) a.stages = kMostStages;
+  a.slots = a.streams * a.n <= 256 ? 4 : 2;
   return a;
 }
 
 template <class T>
 cudaError_t launch(const ApplyParams& p, const Plan& a, const CUtensorMap& map, cudaStream_t s) {
   const int groups = (p.w.tiles / 8 + a.ft - 1) / a.ft;
-  return launch_as(many_rows_kernel<T>, dim3((unsigned)(groups * a.cluster), (unsigned)a.chunks), a.cluster, 1, false, kThreads,
-                   kSmem + 1024, s, p, a, map);
+  const dim3 grid((unsigned)(groups * a.cluster), (unsigned)a.chunks);
+  return p.w.zero ? launch_as(many_rows_kernel<T, true>, grid, a.cluster, 1, false, kThreads, kSmem + 1024, s, p, a, map)
+                  : launch_as(many_rows_kernel<T, false>, grid, a.cluster, 1, false, kThreads, kSmem + 1024, s, p, a, map);
 }
 
 }  // namespace
 
+template <class T, bool ZERO>
+static cudaError_t prepare() {
+  return cudaFuncSetAttribute(many_rows_kernel<T, ZERO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem + 1024);
+}
 cudaError_t prepare_many_rows() {
-  cudaError_t e = cudaFuncSetAttribute(many_rows_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem + 1024);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(many_rows_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem + 1024);
+  for (cudaError_t e : {prepare<float, false>(), prepare<float, true>(), prepare<__nv_bfloat16, false>(), prepare<__nv_bfloat16, true>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
 }
 
 cudaError_t launch_many_rows(const ApplyParams& p, bool f32, cudaStream_t s) {

@@ -99,6 +99,8 @@ def test_the_plain_sum_exactly():
 def test_unpack(zero, gated):
     for n, k, group in ((2, 32, 32), (250, 448, 64), (130, 128, 128)):
         q, scale, z, _ = make(n, k, group, zero, n, spread=4.0)
+        scale[-1] = -scale[-1]
+        scale[0] = 2.0 ** -126 * 1.5                  # the least exponent of a normal number
         out = torch.zeros((n, k), dtype=torch.bfloat16, device="cuda")
         linear(q, scale, z, gated).unpack(out)
         np.testing.assert_array_equal(wide(out), ref.weights(q, wide(scale), z))
@@ -141,7 +143,7 @@ def test_rows_do_not_touch_one_another():
 
 
 def test_extreme_scales():
-    """Results from 2^-100 to infinity; a scale of zero; a weight that its scale turns into infinity."""
+    """Results from 2^-100 to 2^100; scales of zero, infinity, NaN, the largest taken and the least refused."""
     for rows in (2, 70):
         q, _, _, x = make(64, 128, 128, False, 9, rows)
         s = np.zeros((64, 1), np.float32)
@@ -154,10 +156,18 @@ def test_extreme_scales():
         y, off = ref.apply(wide(x), ref.weights(q, wide(scale)), False)
         check(out, y, off, torch.float32)
         assert (out[:, 5] == 0).all()
-    s[7] = 2.0 ** 127
+    s[7], s[9] = np.inf, np.nan
+    s[11] = -2.0 ** 121                            # the largest exponent that is taken
     lin = linear(q, torch.from_numpy(s).to(torch.bfloat16), None)
     lin.apply(x.cuda(), out)
-    assert not out[:, 7].isfinite().any() and out[:, 8].isfinite().all()
+    assert not out[:, [7, 9]].isfinite().any() and out[:, [8, 10]].isfinite().all()
+    w = torch.zeros((64, 128), dtype=torch.bfloat16, device="cuda")
+    lin.unpack(w)
+    np.testing.assert_array_equal(wide(w)[11], (ref.nibbles(q)[11] - 8) * -2.0 ** 121)
+    s[7] = 2.0 ** 122
+    with pytest.raises(cp.CPError) as e:
+        linear(q, torch.from_numpy(s).to(torch.bfloat16), None)
+    assert e.value.code == 2
 
 
 def test_streams_graphs_and_repeats():
