@@ -7,6 +7,7 @@
 #include "cp.h"
 #include "cp_call.h"
 #include "cp_linear.cuh"
+#include "cp_ptx.cuh"
 
 using namespace cp;
 using namespace cp::linear;
@@ -118,6 +119,8 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
   const Weights& w = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int t0 = blockIdx.x * 2, row0 = blockIdx.y * 8 * NT;
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
   float acc[2][NT][4] = {};
   for (int b = warp; b * kBlockK < w.width; b += kWarps) {
     uint2 x[NT][4];
@@ -175,9 +178,9 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_cons
 
 template <class T>
 cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
-  if (p.rows <= 8) few_rows_kernel<T, 1><<<dim3(p.w.tiles / 2, 1), kWarps * 32, 0, s>>>(p);
-  else few_rows_kernel<T, 2><<<dim3(p.w.tiles / 2, (p.rows + 15) / 16), kWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  const dim3 grid(p.w.tiles / 2, p.rows <= 8 ? 1 : (p.rows + 15) / 16);
+  return p.rows <= 8 ? launch_as(few_rows_kernel<T, 1>, grid, 1, 1, true, kWarps * 32, 0, s, p)
+                     : launch_as(few_rows_kernel<T, 2>, grid, 1, 1, true, kWarps * 32, 0, s, p);
 }
 
 constexpr int kFewRows = 16;

@@ -145,8 +145,17 @@ __device__ __forceinline__ void store_four(__nv_bfloat16* p, const float* v) {
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Exact to fp32's rounding: the type of the result may be fp32.
-__device__ __forceinline__ float silu(float x) { return x / (1.f + expf(-x)); }
+// x / (1 + exp(-x)) to a few of fp32's half steps (the result may be fp32): the rounding of the exponent's product with
+// log2(e) is put back as a factor, and the quotient is one approximate reciprocal.
+__device__ __forceinline__ float silu(float x) {
+  const float y = fminf(fmaxf(-x, -200.f), 200.f);           // past these the exponential is 0 or infinite
+  const float t = __fmul_rn(y, 1.44269502f), rest = __fmaf_rn(y, 1.92596303e-8f, __fmaf_rn(y, 1.44269502f, -t));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  e = __fmul_rn(e, __fmaf_rn(rest, 0.693147182f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return x * r;
+}
 
 // Results of one row from `feature` on, `n` of them (up to four): the residual added, rounded, written.
 template <class T>

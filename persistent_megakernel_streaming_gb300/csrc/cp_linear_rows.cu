@@ -38,7 +38,7 @@ constexpr int kMostStages = 8;           // of x's ring: 128 inputs each
 constexpr int kUnits = 8;                // records in the weights' ring, a power of two
 constexpr int kMostSlots = 4;            // widened records in tensor memory, 64 columns each: the last 128 or 256 columns
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMostCluster = 8;
+constexpr int kMostCluster = 4;          // of 8, whose blocks have an SM each, few fit: 16 to 30 us where 4 take 6 to 10
 constexpr int kRing = kUnits * kMostRecord;
 constexpr int kSmem = 216 * 1024;        // both rings, and at the end the sums that the cluster joins
 
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
     }
     mb_fence_init();
   }
+  pdl_trigger();
   if (warp == kMmaWarp) {
     tm_alloc(saddr(&sh.tmem), kTmemCols);
     tm_relinquish();
@@ -270,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
     if (elect_one()) {
       Turn stage;
       int asked = 0;
+      pdl_wait();                          // x may be what the kernel in front writes; the weights are nobody's
       for (; asked < b1 - b0; ++asked) {
         const uint32_t bar = saddr(&sh.b_full[stage.at]), at = x_ring + stage.at * stage_bytes;
         if (!wait_bar(sh, saddr(&sh.b_empty[stage.at]), stage.parity ^ 1)) break;
@@ -318,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   const bool failed = sh.abort != 0;
   if (failed && threadIdx.x == 0) atomicCAS(p.status, 0, (int)CP_ERR_TIMEOUT);
 
+  pdl_wait();                              // what reads out or writes add in front of this is done
   // Results. Feature i of a piece is in TMEM lane i, row r of x in column r.
   const int rows_here = min(n, p.rows - row0), here = min(ft, w.tiles / 8 - piece0);
   float* sums = reinterpret_cast<float*>(raw + (x_ring - saddr(raw)));      // [row][features of the block]
@@ -338,14 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
 #pragma unroll
           for (int x = 0; x < 16; ++x) sums[(c + x) * wide + f * 128 + quarter * 32 + lane] = v[x];
         } else if (w.gated) {
-          const int feature = (piece0 + f) * 64 + quarter * 16 + (lane & 15);
+          // lanes 0 .. 15 have the gates, the others up of the same features: of two rows, each half takes one
+          const int feature = (piece0 + f) * 64 + quarter * 16 + (lane & 15), odd = lane >> 4;
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float up = __shfl_xor_sync(0xffffffffu, v[x], 16);
-            if (lane < 16 && feature < w.outs && c + x < rows_here) {
-              float y = silu(v[x]) * up;
-              finish<T>(p, row0 + c + x, feature, 1, &y);
-            }
+          for (int x = 0; x < 16; x += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[x] : v[x + 1], 16);
+            float y = silu(odd ? other : v[x]) * (odd ? v[x + 1] : other);
+            if (feature < w.outs && c + x + odd < rows_here) finish<T>(p, row0 + c + x + odd, feature, 1, &y);
           }
         } else {
           const int feature = (piece0 + f) * 128 + quarter * 32 + lane;
@@ -401,28 +403,50 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
 
 int up_to(int a, int b) { return (a + b - 1) / b * b; }
 
+// How a call is cut up: what costs least by a model of the measured times, in microseconds. A round of blocks takes
+// kRoundUs to start and end; a record's products 8 times (12 + n / 2) clocks on the tensor core, and no less than what
+// widening and the hand-overs take; joining moves a block's sums through distributed shared memory at 12 bytes a clock.
+// Clusters leave SMs over. (64 rows, 16384 to 8192: two shares of the inputs and one piece a block 27 us, no shares 41,
+// four pieces in four shares 43; 320 rows, 2048 to 2 x 6144: three chunks of 112 rows and two pieces a block 25, two of
+// 160 35, five of 64 33.)
+constexpr double kRoundUs = 5, kRecordUs = 0.256, kClocksUs = 1900;
+int blocks_at_once(int cluster) { return cluster == 1 ? 152 : cluster == 2 ? 148 : 144; }
+
 Plan make_plan(const ApplyParams& p) {
-  Plan a{};
-  a.chunks = (p.rows + kMostRows - 1) / kMostRows;
-  a.n = up_to((p.rows + a.chunks - 1) / a.chunks, 16);
-  a.chunks = (p.rows + a.n - 1) / a.n;
-  const int pieces = p.w.tiles / 8;
-  a.ft = 1;
-  a.cluster = 1;
-  while (a.cluster < kMostCluster && pieces * a.chunks * a.cluster * 2 <= 152 && p.w.per_piece >= a.cluster * 2) a.cluster *= 2;
-  a.streams = a.n <= 64 ? 4 : 2;
-  a.stages = (kSmem - kRing) / (a.n * 256);
-  if (a.stages > kMostStages) a.stages = kMostStages;
-  a.slots = a.streams * a.n <= 256 ? 4 : 2;
-  return a;
+  Plan best{};
+  double least = 1e30;
+  const int pieces = p.w.tiles / 8, fewest = (p.rows + kMostRows - 1) / kMostRows;
+  for (int chunks = fewest; chunks <= fewest + 3; ++chunks) {
+    Plan a{};
+    a.n = up_to((p.rows + chunks - 1) / chunks, 16);
+    a.chunks = (p.rows + a.n - 1) / a.n;
+    a.streams = a.n <= 64 ? 4 : 2;
+    a.stages = (kSmem - kRing) / (a.n * 256);
+    if (a.stages > kMostStages) a.stages = kMostStages;
+    a.slots = a.streams * a.n <= 256 ? 4 : 2;
+    const double record = 8 * (12 + 0.5 * a.n) / kClocksUs;
+    for (a.ft = 1; a.ft <= a.streams; a.ft *= 2)
+      for (a.cluster = 1; a.cluster <= kMostCluster && a.cluster <= p.w.per_piece; a.cluster *= 2) {
+        const int64_t blocks = (int64_t)((pieces + a.ft - 1) / a.ft) * a.cluster * a.chunks;
+        const int64_t rounds = (blocks + blocks_at_once(a.cluster) - 1) / blocks_at_once(a.cluster);
+        const int units = (p.w.per_piece + a.cluster - 1) / a.cluster * a.ft;
+        const double join = a.cluster == 1 ? 0 : 1 + a.n * a.ft * 512. * (a.cluster - 1) / a.cluster / 12 / kClocksUs;
+        const double us = rounds * (kRoundUs + units * (record > kRecordUs ? record : kRecordUs) + join);
+        if (us < least) {
+          least = us;
+          best = a;
+        }
+      }
+  }
+  return best;
 }
 
 template <class T>
 cudaError_t launch(const ApplyParams& p, const Plan& a, const CUtensorMap& map, cudaStream_t s) {
   const int groups = (p.w.tiles / 8 + a.ft - 1) / a.ft;
   const dim3 grid((unsigned)(groups * a.cluster), (unsigned)a.chunks);
-  return p.w.zero ? launch_as(many_rows_kernel<T, true>, grid, a.cluster, 1, false, kThreads, kSmem + 1024, s, p, a, map)
-                  : launch_as(many_rows_kernel<T, false>, grid, a.cluster, 1, false, kThreads, kSmem + 1024, s, p, a, map);
+  return p.w.zero ? launch_as(many_rows_kernel<T, true>, grid, a.cluster, 1, true, kThreads, kSmem + 1024, s, p, a, map)
+                  : launch_as(many_rows_kernel<T, false>, grid, a.cluster, 1, true, kThreads, kSmem + 1024, s, p, a, map);
 }
 
 }  // namespace
