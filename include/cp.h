@@ -630,7 +630,8 @@ typedef struct cp_linear_desc {
                                  this long (0 = default 2 s)                  */
   int debug_stall;            /* testing: nonzero makes each block of
                                  cp_linear_apply that brings x in through a
-                                 ring (more than 16 rows) leave out its first
+                                 ring (more than 16 rows, or fewer of large
+                                 weights) leave out its first
                                  load, so that the waits for it run out and
                                  set CP_ERR_TIMEOUT                           */
 } cp_linear_desc;

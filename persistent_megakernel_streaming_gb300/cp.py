@@ -330,17 +330,27 @@ def _not_lost(x: float, what: str):
         raise ValueError(f"{what}: {x} is zero in fp32")
 
 
+_torch = None        # torch, once there are tensors to look at: an import statement costs a call 0.2 us
+
+
+def _with_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _stream_on(index: int, stream) -> int:
     """The raw stream: torch's current one of that device, if none is given."""
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(index)
+        return (_torch or _with_torch())._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
 def _workspace(device, size: int, stream):
     """Device bytes, allocated on the stream that uses them, so that the allocator hands them on in that stream's order."""
-    import torch
+    torch = _torch or _with_torch()
     if stream is None:
         return torch.empty(size, dtype=torch.uint8, device=device)
     if not hasattr(stream, "cuda_stream"):
@@ -548,11 +558,10 @@ class Cache:
 
 
 def _moves(moves, count, index: int):
-    import torch
-    if moves.dtype != torch.int32 or moves.dim() != 2 or moves.shape[1] != 2 or not moves.is_contiguous() or \
-            moves.get_device() != index:
+    i32, shape = (_torch or _with_torch()).int32, moves.shape
+    if moves.dtype is not i32 or len(shape) != 2 or shape[1] != 2 or not moves.is_contiguous() or moves.get_device() != index:
         raise ValueError(f"moves: int32 [capacity][2], contiguous, on cuda:{index}")
-    return moves.data_ptr(), _int32(moves.shape[0], "moves"), _array(count, "count", torch.int32, (1,), index)
+    return moves.data_ptr(), _int32(shape[0], "moves"), _array(count, "count", i32, (1,), index)
 
 
 class Pages:
@@ -574,6 +583,8 @@ class Pages:
         self.keep = (refs, table, length)
         self.device_index = refs.get_device()
         self.sequences, self.pages = length.shape[0], refs.shape[0]
+        self.i32, self.each = torch.int32, (length.shape[0],)
+        _with_torch()
         self.desc = PagesDesc(_int32(refs.shape[0], "refs"), _int32(page_size, "page_size"), _int32(length.shape[0], "length"),
                               _int32(table.shape[1], "table"), _stride(table, 0), _ptr(refs), _ptr(table), _ptr(length))
         h = C.c_void_p()
@@ -582,27 +593,24 @@ class Pages:
 
     def fork(self, src, dst, stream=None):
         """Sequences dst[i], which hold nothing, become copies of src[i] that share its pages (int32 [n] each)."""
-        import torch
-        n = dst.numel()
-        code = lib().cp_pages_fork(self._h, _array(src, "src", torch.int32, (n,), self.device_index),
-                                   _array(dst, "dst", torch.int32, (n,), self.device_index), n, _stream_on(self.device_index, stream))
+        shape, index = (dst.numel(),), self.device_index
+        code = lib().cp_pages_fork(self._h, _array(src, "src", self.i32, shape, index), _array(dst, "dst", self.i32, shape, index),
+                                   shape[0], _stream_on(index, stream))
         if code:
             raise CPError(code, "cp_pages_fork")
 
     def grow(self, add, moves, count, stream=None):
         """Room for add[i] (int32 [sequences]) more positions each; count[0] below 0: the pool lacks that many pages, and
         nothing was changed."""
-        import torch
         m, capacity, n = _moves(moves, count, self.device_index)
-        code = lib().cp_pages_grow(self._h, _array(add, "add", torch.int32, (self.sequences,), self.device_index), m, capacity, n,
+        code = lib().cp_pages_grow(self._h, _array(add, "add", self.i32, self.each, self.device_index), m, capacity, n,
                                    _stream_on(self.device_index, stream))
         if code:
             raise CPError(code, "cp_pages_grow")
 
     def trim(self, keep, stream=None):
         """Each sequence cut to at most keep[i] (int32 [sequences]) positions, pages past them given up."""
-        import torch
-        code = lib().cp_pages_trim(self._h, _array(keep, "keep", torch.int32, (self.sequences,), self.device_index),
+        code = lib().cp_pages_trim(self._h, _array(keep, "keep", self.i32, self.each, self.device_index),
                                    _stream_on(self.device_index, stream))
         if code:
             raise CPError(code, "cp_pages_trim")
@@ -666,28 +674,35 @@ class Linear:
     def apply(self, x, out, add=None, stream=None):
         """x bf16 [rows][width] into out [rows][features, or half of them if gated], bf16 or fp32; ``add`` of out's type is
         added before the result is rounded."""
-        rows = x.shape[0]
-        if x.dtype not in self.x_dtypes or x.shape != (rows, self.width) or x.get_device() != self.device_index:
+        index, shape, out_dtype = self.device_index, x.shape, out.dtype
+        rows = shape[0]
+        if x.dtype not in self.x_dtypes or shape != (rows, self.width) or x.get_device() != index:
             raise ValueError(f"x: bf16 [rows][{self.width}] on the weights' device")
-        kind = self.dtypes.get(out.dtype)
-        if kind is None or out.get_device() != self.device_index:
+        kind = self.dtypes.get(out_dtype)
+        if kind is None or out.get_device() != index:
             raise ValueError("out: bf16 or fp32 on the weights' device")
-        a = LinearArgs(x.data_ptr(), self._row(x, "x"), rows, kind, out.data_ptr(), self._row(out, "out", rows))
+        shape = (rows, self.outs)
+        a = LinearArgs(x.data_ptr(), self._row(x, "x", x.shape), rows, kind, out.data_ptr(), self._row(out, "out", shape))
         if add is not None:
-            if add.dtype != out.dtype or add.get_device() != self.device_index:
+            if add.dtype is not out_dtype or add.get_device() != index:
                 raise ValueError("add: of out's type and device")
-            a.add, a.add_stride = add.data_ptr(), self._row(add, "add", rows)
-        code = lib().cp_linear_apply(self._h, C.byref(a), _stream_on(self.device_index, stream))
+            a.add, a.add_stride = add.data_ptr(), self._row(add, "add", shape)
+        code = lib().cp_linear_apply(self._h, C.byref(a), _stream_on(index, stream))
         if code:
             raise CPError(code, "cp_linear_apply")
 
-    def _row(self, t, what, rows=None):
-        """The stride of t's rows."""
-        if rows is not None and t.shape != (rows, self.outs):
-            raise ValueError(f"{what}: [{rows}][{self.outs}]; got {list(t.shape)}")
-        if t.shape[1] > 1 and t.stride(1) != 1:
+    def _row(self, t, what, shape):
+        """The stride of t's rows (0 for a single one)."""
+        if t.shape != shape:
+            raise ValueError(f"{what}: {list(shape)}; got {list(t.shape)}")
+        row, one = t.stride()
+        if one != 1 and shape[1] > 1:
             raise ValueError(f"{what}: the last axis contiguous")
-        return _stride(t, 0)
+        if shape[0] <= 1:
+            return 0
+        if row <= 0:
+            raise ValueError(f"{what}: rows that share memory (an expanded tensor)")
+        return row
 
     def unpack(self, out, stream=None):
         """The weights as the bf16 numbers that they stand for, into out [features][width]."""
@@ -717,7 +732,6 @@ class Linear:
 
 
 _verify_needs: dict = {}
-_verify_dtypes: dict = {}
 
 
 def verify_workspace_bytes(sequences: int, rows: int, vocab: int) -> int:
@@ -743,27 +757,26 @@ def verify(logits, draft, start, u_accept, u_token, temperature, accepted, token
     ``draft`` int32, ``u_accept`` and ``prob`` fp32 [rows]; ``start`` int32 [sequences + 1]; ``u_token`` and ``temperature`` fp32,
     ``accepted`` and ``token`` int32 [sequences]. Without a ``workspace`` (device bytes, see verify_workspace_bytes) one
     is taken from torch's allocator for this call."""
-    import torch
-    if not _verify_dtypes:
-        _verify_dtypes.update({torch.float32: 0, torch.bfloat16: 1})
+    torch = _torch or _with_torch()
     f32, i32, index = torch.float32, torch.int32, logits.get_device()
     dtype, shape = logits.dtype, logits.shape
-    kind = _verify_dtypes.get(dtype)
-    if kind is None or index < 0 or len(shape) != 2:
+    if dtype is not f32 and dtype is not torch.bfloat16 or index < 0 or len(shape) != 2:
         raise ValueError("logits: bf16 or fp32 [rows][vocab] on a GPU")
     rows, vocab = shape
     by_row, by_seq = (rows,), (accepted.numel(),)
-    stride, draft_at, draft_stride = _stride(logits, 0), None, 0
-    if vocab > 1 and logits.stride(1) != 1:
-        raise ValueError("logits: the last axis contiguous")
-    if draft_logits is not None:
-        if draft_logits.dtype is not dtype or draft_logits.shape != shape or draft_logits.get_device() != index or \
-                vocab > 1 and draft_logits.stride(1) != 1:
-            raise ValueError("draft_logits: of the logits' type, shape and device, the last axis contiguous")
-        draft_at, draft_stride = draft_logits.data_ptr(), _stride(draft_logits, 0)
+    strides = [0, 0]
+    for k, t in enumerate((logits, draft_logits)):
+        if t is not None:
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+                raise ValueError("draft_logits: of the logits' type, shape and device")
+            row, one = t.stride()
+            if vocab > 1 and one != 1 or rows > 1 and row <= 0:
+                raise ValueError("logits, draft_logits: the last axis contiguous, rows that share no memory")
+            strides[k] = row if rows > 1 else 0
     n = by_seq[0]
     need = _verify_needs.get((n, rows, vocab)) or verify_workspace_bytes(n, rows, vocab)
-    a = VerifyArgs(n, rows, vocab, kind, _array(start, "start", i32, (n + 1,), index), logits.data_ptr(), stride, draft_at, draft_stride,
+    a = VerifyArgs(n, rows, vocab, int(dtype is not f32), _array(start, "start", i32, (n + 1,), index), logits.data_ptr(), strides[0],
+                   None if draft_logits is None else draft_logits.data_ptr(), strides[1],
                    _array(draft, "draft", i32, by_row, index), _array(temperature, "temperature", f32, by_seq, index),
                    _array(u_accept, "u_accept", f32, by_row, index), _array(u_token, "u_token", f32, by_seq, index),
                    _array(accepted, "accepted", i32, by_seq, index), _array(token, "token", i32, by_seq, index),

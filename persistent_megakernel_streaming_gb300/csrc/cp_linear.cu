@@ -1,5 +1,5 @@
 // cp_linear.cu -- projections with 4-bit weights: the C ABI (checks, layout of
-// the weights, launches) and the kernel for up to 16 rows.
+// the weights, launches) and the kernel for few rows.
 #include <cuda_runtime.h>
 
 #include <new>
@@ -77,7 +77,7 @@ __global__ void pack_kernel(const PackParams p) {
 // A lane's scales and zero points of a record.
 __device__ __forceinline__ Meta load_meta(const Weights& w, const uint8_t* record, int t, int k, int g) {
   const uint32_t s = *reinterpret_cast<const uint32_t*>(record + scale_in(w, t, k, g));
-  return meta_of(s, w.zero ? *reinterpret_cast<const uint16_t*>(record + zero_in(w, t, k, g)) : kNoZero);
+  return w.zero ? meta_of<true>(s, *reinterpret_cast<const uint16_t*>(record + zero_in(w, t, k, g))) : meta_of<false>(s, 0);
 }
 
 __global__ void unpack_kernel(const Weights w, uint16_t* out) {
@@ -103,87 +103,135 @@ __global__ void unpack_kernel(const Weights w, uint16_t* out) {
 }
 
 // ------------------------------------------------------------------ few rows
-constexpr int kWarps = 8;
-
 __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// NT tiles of 8 rows of x; a block has two tiles of the weights, of a gated projection the gate's and the same of up,
-// its warps every eighth block of inputs.
-template <class T, int NT>
-__global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(const __grid_constant__ ApplyParams p) {
-  __shared__ float part[kWarps][2 * kTileRows][8 * NT + 1];
+// NT tiles of 8 rows of x; a block has TILES tiles of the weights (of a gated projection the gate's and the same of up),
+// its WARPS warps every so manieth record, U records at a time, whose loads are all under way before the first is used;
+// the first of them before the kernel in front has ended, since nobody writes weights. GROUPS of scales a record.
+template <int NT, int WARPS, int TILES, int U, int GROUPS, bool ZERO>
+__global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_constant__ ApplyParams p) {
+  __shared__ float part[WARPS][TILES * kTileRows][8 * NT + 1];
   const Weights& w = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int t0 = blockIdx.x * 2, row0 = blockIdx.y * 8 * NT;
+  const int t0 = blockIdx.x * TILES, row0 = blockIdx.y * 8 * NT;
+  const int rows_here = min(8 * NT, p.rows - row0);
+  const uint8_t* words = w.records + record_at(w, t0, 0) + word_in(t0, 0, lane);
+  const uint8_t* scales = w.records + record_at(w, t0, 0) + scale_in(w, t0, 0, g);
+  const uint8_t* zeros = w.records + record_at(w, t0, 0) + zero_in(w, t0, 0, g);
+  const uint16_t* x_row = p.x + (int64_t)(row0 + g) * p.x_row + 4 * c;
   ptx::pdl_trigger();
-  ptx::pdl_wait();
-  float acc[2][NT][4] = {};
-  for (int b = warp; b * kBlockK < w.width; b += kWarps) {
-    uint2 x[NT][4];
-    const int k = b * kBlockK;
+  float acc[TILES][NT][4] = {};
+  for (int first = warp; first < w.per_piece; first += WARPS * U) {
+    uint4 word[U][TILES][2];
+    uint32_t scale[U][TILES][GROUPS], zero[U][TILES][GROUPS];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = row0 + n * 8 + g;
-      const uint16_t* src = p.x + (int64_t)r * p.x_row + k + 4 * c;
+    for (int u = 0; u < U; ++u) {
+      const int64_t at = (int64_t)min(first + u * WARPS, w.per_piece - 1) * w.bytes;   // past the last: it again, and its x as zeros
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[n][j] = r < p.rows && k + 16 * j < w.width ? *reinterpret_cast<const uint2*>(src + 16 * j) : make_uint2(0, 0);
+      for (int t = 0; t < TILES; ++t) {
+        word[u][t][0] = *reinterpret_cast<const uint4*>(words + at + t * 512);
+        word[u][t][1] = *reinterpret_cast<const uint4*>(words + at + t * 512 + 4096);
+#pragma unroll
+        for (int i = 0; i < GROUPS; ++i) {
+          scale[u][t][i] = *reinterpret_cast<const uint32_t*>(scales + at + t * 32 + i * kRecordScales);
+          zero[u][t][i] = ZERO ? *reinterpret_cast<const uint16_t*>(zeros + at + t * 16 + i * kRecordZeros) : 0;
+        }
+      }
     }
+    if (first == warp) ptx::pdl_wait();
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint8_t* record = w.records + record_at(w, t0 + t, k);
-      const uint4 v = *reinterpret_cast<const uint4*>(record + word_in(t0 + t, k, lane));
-      const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+    for (int u = 0; u < U; ++u) {
+      const int k = (first + u * WARPS) * kRecordK;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {                // groups of 32 have two in a block
-        const Meta m = load_meta(w, record, t0 + t, k + 32 * h, g);
+      for (int h = 0; h < 2; ++h) {
+        uint2 x[NT][4];
 #pragma unroll
-        for (int j = 2 * h; j < 2 * h + 2; ++j) {
-          uint32_t a[4];
-          widen(words[j], m, a);
+        for (int n = 0; n < NT; ++n) {
+          const uint16_t* src = x_row + (int64_t)n * 8 * p.x_row + k + h * kBlockK;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma(acc[t][n], a, x[n][j].x, x[n][j].y);
+          for (int j = 0; j < 4; ++j)
+            x[n][j] = n * 8 + g < rows_here && k + h * kBlockK + 16 * j < w.width ? *reinterpret_cast<const uint2*>(src + 16 * j) : make_uint2(0, 0);
+        }
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+          const uint4 v = word[u][t][h];
+          const uint32_t four[4] = {v.x, v.y, v.z, v.w};
+          Meta m;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            constexpr int kSteps = 8 / GROUPS;       // of 16 inputs, a group
+            if ((h * 4 + j) % kSteps == 0 || j == 0) m = meta_of<ZERO>(scale[u][t][(h * 4 + j) / kSteps], zero[u][t][(h * 4 + j) / kSteps]);
+            uint32_t a[4];
+            widen(four[j], m, a);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma(acc[t][n], a, x[n][j].x, x[n][j].y);
+          }
         }
       }
     }
   }
+  ptx::pdl_wait();                                   // a warp without records has not waited yet
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < TILES; ++t)
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) part[warp][t * kTileRows + g + (i >> 1) * 8][n * 8 + 2 * c + (i & 1)] = acc[t][n][i];
   __syncthreads();
-  const int per = w.gated ? kTileRows : 2 * kTileRows;
-  for (int i = threadIdx.x; i < per * 8 * NT; i += kWarps * 32) {
-    const int f = i % per, r = i / per;
+  constexpr int kAll = TILES * kTileRows;
+  const int per = w.gated ? kTileRows : kAll;
+  for (int i = threadIdx.x; i < per * rows_here; i += WARPS * 32) {
+    const int f = w.gated ? i & (kTileRows - 1) : i & (kAll - 1), r = w.gated ? i / kTileRows : i / kAll;
     const int n = blockIdx.x * per + f;
-    if (n >= w.outs || row0 + r >= p.rows) continue;
-    float y = 0.f, u = 0.f;
+    if (n >= w.outs) continue;
+    float y = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) y += part[k][f][r];
-    if (w.gated) {
+    for (int k = 0; k < WARPS; ++k) y += part[k][f][r];
+    if (TILES == 2 && w.gated) {
+      float up = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) u += part[k][kTileRows + f][r];
-      y = silu(y) * u;
+      for (int k = 0; k < WARPS; ++k) up += part[k][(TILES - 1) * kTileRows + f][r];
+      y = silu(y) * up;
     }
-    if (p.add) y += load_out<T>(p.add, (row0 + r) * p.add_row + n);
-    store_out(static_cast<T*>(p.out) + (row0 + r) * p.out_row + n, y);
+    if (p.f32) finish<float>(p, row0 + r, n, 1, &y);
+    else finish<__nv_bfloat16>(p, row0 + r, n, 1, &y);
   }
 }
 
-template <class T>
+template <int NT, int WARPS, int TILES, int U, int GROUPS>
+cudaError_t launch_few(const ApplyParams& p, cudaStream_t s) {
+  const dim3 grid(p.w.tiles / TILES, (p.rows + 8 * NT - 1) / (8 * NT));
+  return p.w.zero ? launch_as(few_rows_kernel<NT, WARPS, TILES, U, GROUPS, true>, grid, 1, 1, true, WARPS * 32, 0, s, p)
+                  : launch_as(few_rows_kernel<NT, WARPS, TILES, U, GROUPS, false>, grid, 1, 1, true, WARPS * 32, 0, s, p);
+}
+template <int NT, int WARPS, int TILES, int U>
+cudaError_t launch_few(const ApplyParams& p, cudaStream_t s) {
+  return p.w.groups == 1 ? launch_few<NT, WARPS, TILES, U, 1>(p, s)
+                         : p.w.groups == 2 ? launch_few<NT, WARPS, TILES, U, 2>(p, s) : launch_few<NT, WARPS, TILES, U, 4>(p, s);
+}
+// Few blocks take many warps each, which end sooner; many blocks fewer warps, so that more blocks share an SM and some
+// load while others join their sums. (1 row, 2048 to 4096, 128 blocks: 2.5 us with 16 warps, 3.5 with 8; 8 rows, 8192
+// to 8192, 256: 10.8 and 17.3; 1 row, 8192 to 28672, 896: 26.9 and 26.3; 3 rows, 2048 to 50001, 1563: 16.3 and 14.3.)
+constexpr int kManyBlocks = 512;
+
 cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
-  const dim3 grid(p.w.tiles / 2, p.rows <= 8 ? 1 : (p.rows + 15) / 16);
-  return p.rows <= 8 ? launch_as(few_rows_kernel<T, 1>, grid, 1, 1, true, kWarps * 32, 0, s, p)
-                     : launch_as(few_rows_kernel<T, 2>, grid, 1, 1, true, kWarps * 32, 0, s, p);
+  if (p.rows > 8) return launch_few<2, 16, 2, 1>(p, s);
+  return p.w.tiles / 2 <= kManyBlocks ? launch_few<1, 16, 2, 1>(p, s) : launch_few<1, 8, 2, 1>(p, s);
 }
 
-constexpr int kFewRows = 16;
+// Nine to sixteen rows: two fragments a word, and no tensor memory to fill, win while the weights are few. (Records of
+// 4 MB: 3.3 to 3.7 us here, 5.8 to 6.1 in the other kernel; of 6 MB 6.6 and 8.1; of 13 MB 8.7 to 9.5 and 8.6; of 34 MB 18
+// to 20 and 14.)
+constexpr int kFewRows = 8, kSomeRows = 16;
+constexpr int64_t kSomeBytes = 8 << 20;
+bool takes_few(const ApplyParams& p) {
+  return p.rows <= kFewRows || (p.rows <= kSomeRows && (int64_t)(p.w.tiles / kPadTiles) * p.w.per_piece * p.w.bytes <= kSomeBytes);
+}
+
 
 // ------------------------------------------------------------------ checks
 int check_desc(const cp_linear_desc* d, Weights* w) {
@@ -214,6 +262,7 @@ int check_args(const Weights& w, const cp_linear_args* a, ApplyParams* p) {
   p->out = a->out;
   p->add = a->add;
   p->rows = a->rows;
+  p->f32 = a->out_dtype == CP_OUT_F32;
   p->x_row = a->x_stride ? a->x_stride : w.width;
   p->out_row = a->out_stride ? a->out_stride : w.outs;
   p->add_row = a->add_stride ? a->add_stride : w.outs;
@@ -307,9 +356,7 @@ int cp_linear_apply(cp_linear* l, const cp_linear_args* args, cp_stream_t stream
   p.stall = l->stall;
   DeviceGuard g(l->device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const bool f32 = args->out_dtype == CP_OUT_F32;
-  if (p.rows > kFewRows) return cuda_err(launch_many_rows(p, f32, s));
-  return cuda_err(f32 ? launch_few_rows<float>(p, s) : launch_few_rows<__nv_bfloat16>(p, s));
+  return cuda_err(takes_few(p) ? launch_few_rows(p, s) : launch_many_rows(p, s));
 }
 
 int cp_linear_status(cp_linear* l) {

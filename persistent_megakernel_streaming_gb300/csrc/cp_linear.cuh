@@ -54,6 +54,7 @@ struct ApplyParams {
   void* out;
   const void* add;
   int rows;
+  int f32;                   // out's type: fp32, or bf16
   int by_four;               // rows of out and add start where four results can be written at once
 };
 
@@ -84,13 +85,14 @@ struct Meta {
   uint32_t z[2];   // minus the zero points, over 64
 };
 constexpr uint32_t kUp127 = 0x7f007f00u, kUp123 = 0x7d007d00u, kDown127 = 0xff00ff00u;    // bf16 2^127, 2^123, -2^127
-constexpr uint32_t kNoZero = 0x0808u;
+constexpr uint32_t kEight = 0xbe00be00u;     // -8 / 64: where there are no zero points
+template <bool ZERO>
 __device__ __forceinline__ Meta meta_of(uint32_t scale, uint32_t zero) {
   Meta m;
   m.s[0] = __byte_perm(scale, 0, 0x1010);
   m.s[1] = __byte_perm(scale, 0, 0x3232);
-  m.z[0] = bf2_mul(__byte_perm(zero, 0, 0x4040), kDown127);
-  m.z[1] = bf2_mul(__byte_perm(zero, 0, 0x4141), kDown127);
+  m.z[0] = ZERO ? bf2_mul(__byte_perm(zero, 0, 0x4040), kDown127) : kEight;
+  m.z[1] = ZERO ? bf2_mul(__byte_perm(zero, 0, 0x4141), kDown127) : kEight;
   return m;
 }
 
@@ -179,7 +181,7 @@ __device__ __forceinline__ void finish(const ApplyParams& p, int row, int featur
 
 // Many rows: cp_linear_rows.cu. Once per device, with it current: its shared memory.
 cudaError_t prepare_many_rows();
-cudaError_t launch_many_rows(const ApplyParams& p, bool f32, cudaStream_t s);
+cudaError_t launch_many_rows(const ApplyParams& p, cudaStream_t s);
 
 }  // namespace linear
 }  // namespace cp

@@ -1,5 +1,5 @@
-// cp_linear_rows.cu -- projections of more than 16 rows with 4-bit weights, on
-// tcgen05.
+// cp_linear_rows.cu -- projections of more than 8 or 16 rows with 4-bit weights,
+// on tcgen05.
 //
 // A block takes up to FT times 128 rows of the weights (features), up to 256
 // rows of x, and a share of the inputs; a cluster's blocks have the same
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
             if (j == 0 || (j == 2 && group_shift == 5)) {
               const int grp = (sub * 64 + j * 16) >> group_shift;
               const uint32_t s = ld_shared_u32(at + kRecordWords + grp * kRecordScales + (own + i * 8) * 4);
-              m = meta_of(s, ZERO ? ld_shared_u16(at + zeros + grp * kRecordZeros + (own + i * 8) * 2) : kNoZero);
+              m = meta_of<ZERO>(s, ZERO ? ld_shared_u16(at + zeros + grp * kRecordZeros + (own + i * 8) * 2) : 0);
             }
             uint32_t a[4];
             widen(v[j], m, a);
@@ -461,7 +461,7 @@ cudaError_t prepare_many_rows() {
   return cudaSuccess;
 }
 
-cudaError_t launch_many_rows(const ApplyParams& p, bool f32, cudaStream_t s) {
+cudaError_t launch_many_rows(const ApplyParams& p, cudaStream_t s) {
   static const auto encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -481,7 +481,7 @@ cudaError_t launch_many_rows(const ApplyParams& p, bool f32, cudaStream_t s) {
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  return f32 ? launch<float>(p, a, map, s) : launch<__nv_bfloat16>(p, a, map, s);
+  return p.f32 ? launch<float>(p, a, map, s) : launch<__nv_bfloat16>(p, a, map, s);
 }
 
 }  // namespace linear
