@@ -774,20 +774,24 @@ def verify(logits, draft, start, u_accept, u_token, temperature, accepted, token
                 raise ValueError("logits, draft_logits: the last axis contiguous, rows that share no memory")
             strides[k] = row if rows > 1 else 0
     n = by_seq[0]
-    need = _verify_needs.get((n, rows, vocab)) or verify_workspace_bytes(n, rows, vocab)
+    need = _verify_needs.get((n, rows, vocab))
+    if need is None:
+        need = verify_workspace_bytes(n, rows, vocab)
     a = VerifyArgs(n, rows, vocab, int(dtype is not f32), _array(start, "start", i32, (n + 1,), index), logits.data_ptr(), strides[0],
                    None if draft_logits is None else draft_logits.data_ptr(), strides[1],
                    _array(draft, "draft", i32, by_row, index), _array(temperature, "temperature", f32, by_seq, index),
                    _array(u_accept, "u_accept", f32, by_row, index), _array(u_token, "u_token", f32, by_seq, index),
                    _array(accepted, "accepted", i32, by_seq, index), _array(token, "token", i32, by_seq, index),
                    None if prob is None else _array(prob, "prob", f32, by_row, index))
-    if workspace is None:
-        workspace, size = _workspace(logits.device, need, stream), need
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError("workspace: contiguous, on the logits' device")
-    else:
-        size = workspace.numel() * workspace.element_size()
-    code = lib().cp_verify(C.byref(a), index, workspace.data_ptr(), size, _stream_on(index, stream))
+    at, size = 0, 0
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace: contiguous, on the logits' device")
+        at, size = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif need:
+        workspace = _workspace(logits.device, need, stream)
+        at, size = workspace.data_ptr(), need
+    code = lib().cp_verify(C.byref(a), index, at, size, _stream_on(index, stream))
     if code:
         raise CPError(code, "cp_verify")
 

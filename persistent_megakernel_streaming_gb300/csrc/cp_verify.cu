@@ -4,7 +4,8 @@
 // sum of exponentials of each piece of a row. The second, a cluster for each
 // sequence, joins them, settles which drafted tokens are taken, and draws the
 // token behind them from one row: there it sums again, in 64-bit fixed point,
-// so that the draw does not depend on the order of the sums.
+// so that the draw does not depend on the order of the sums. Over a small
+// vocabulary the second reads the rows itself, and is the only one.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,6 +32,7 @@ constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block
 constexpr int kTokenThreads = 512, kTokenWarps = kTokenThreads / 32;
 constexpr int kRowsKept = 32;                    // rows of a sequence whose pieces are joined once
 constexpr int kMostCluster = 16;
+constexpr int kDirect = 4096;                    // vocabularies up to which the second launch reads the rows itself
 
 struct VerifyParams {
   const int32_t* start;
@@ -48,6 +50,7 @@ struct VerifyParams {
   int n, rows, vocab, splits;
   int cluster, chunk;                  // blocks a sequence, logits a block
   int z_bits;                          // of the fixed point of their sums
+  int direct;                          // one launch: the vocabulary is small
 };
 
 // Scaled logits are finite: NaN and -infinity become the lowest number, whose exponential next to any other is 0; a
@@ -288,6 +291,7 @@ struct TokenShared {
   Piece rows[2][kRowsKept];             // the target's and the draft's rows
   int draft[kRowsKept];
   fixed part[2][kTokenWarps];           // each warp's sums
+  Piece pair[kTokenWarps / 2];          // what one warp of a pair found out about the draft
   fixed z[2][kMostCluster];             // each block's sums of exponentials
   fixed w[2][kMostCluster];             // each block's sum of weights, by turn
   float rz[2];                          // 1 over all of them
@@ -345,7 +349,40 @@ struct Part {
 // What a block's chunk of exponentials takes in shared memory: room for the skew at the front and the last load's end.
 __host__ __device__ __forceinline__ int kept_floats(int chunk) { return (chunk + 16 + 3) & ~3; }
 
-template <class T, bool KEEP>
+// A whole row's maximum and sum by one warp, for vocabularies of up to kDirect: twice over it, the second time out of L1.
+template <class T>
+__device__ __forceinline__ Piece direct_stats(const T* row, int vocab, float by, bool greedy) {
+  const int lane = threadIdx.x & 31;
+  Piece a = {kLowest, 0.f, INT32_MAX, 0};
+#pragma unroll 16
+  for (int i = lane; i < vocab; i += 32) a.m = fmaxf(a.m, __fmul_rn(value(row + i), by));
+  a.m = warp_max(a.m);
+  const float ref = -__fmul_rn(a.m, kLog2e);
+#pragma unroll 16
+  for (int i = lane; i < vocab; i += 32) a.s += ex2(__fmaf_rn(__fmul_rn(value(row + i), by), kLog2e, ref));
+  if (__any_sync(0xffffffffu, !(a.s <= FLT_MAX)) || a.m == INFINITY) {     // NaN or infinities: clamped logits
+    a.m = kLowest;
+    a.s = 0.f;
+    for (int i = lane; i < vocab; i += 32) a.m = fmaxf(a.m, scaled(value(row + i), by));
+    a.m = warp_max(a.m);
+    for (int i = lane; i < vocab; i += 32) a.s += exp_from(scaled(value(row + i), by), a.m);
+  }
+  if (greedy) {
+    for (int i = lane; i < vocab; i += 32)
+      if (scaled(value(row + i), by) == a.m) {
+        a.arg = i;
+        break;
+      }
+    a.arg = __reduce_min_sync(0xffffffffu, a.arg);
+  }
+  a.s = warp_sum(a.s);
+  return a;
+}
+
+// The two warps that share a row: a barrier of their own.
+__device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
+template <class T, bool KEEP, bool DIRECT>
 __global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(16) float kept[];       // exponentials of the block's chunk of the target's, and of the draft's
   __shared__ TokenShared sh;
@@ -365,19 +402,37 @@ __global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_co
   const T* logits = static_cast<const T*>(p.logits);
   const T* drafts = greedy ? nullptr : static_cast<const T*>(p.draft_logits);
   bool waited = false;
-  for (int r = r0 + warp; r < r1 && !bad; r += kTokenWarps) {        // every block of the cluster does the same
+  // every block of the cluster does the same: a warp a row, or, where the rows are read here, one for the target's and one
+  // for the draft's
+  constexpr int kRowWarps = DIRECT ? 2 : 1;
+  for (int r = r0 + warp / kRowWarps; r < r1 && !bad; r += kTokenWarps / kRowWarps) {
     const bool last = r == r1 - 1;
     const int d = last ? -1 : p.draft[r];
     const bool in = (uint32_t)d < (uint32_t)p.vocab;
     const float u = last ? 0.f : fminf(fmaxf(p.u_accept[r], 0.f), 0x1.fffffep-1f);
     const float xp = in ? scaled(value(logits + r * p.row + d), by) : 0.f;
     const float xq = in && drafts ? scaled(value(drafts + r * p.draft_row + d), by) : 0.f;
-    if (!waited) ptx::pdl_wait();                                    // the sums, in front of which all but them is read
-    waited = true;
-    Piece a = piece_of(p, 0, r, lane), b = {kLowest, 0.f, 0, 0};
-    if (drafts && !last) b = piece_of(p, 1, r, lane);
-    a = row_stats(p, 0, r, a);
-    if (drafts && !last) b = row_stats(p, 1, r, b);
+    Piece a, b = {kLowest, 0.f, 0, 0};
+    if (DIRECT) {
+      const bool of_draft = warp & 1;
+      if (of_draft) {
+        if (drafts && !last) b = direct_stats(drafts + r * p.draft_row, p.vocab, by, false);
+        if (lane == 0) sh.pair[warp / 2] = b;
+      } else {
+        a = direct_stats(logits + r * p.row, p.vocab, by, greedy);
+      }
+      pair_sync(1 + warp / 2);
+      if (!of_draft) b = sh.pair[warp / 2];
+      pair_sync(1 + warp / 2);
+      if (of_draft) continue;
+    } else {
+      if (!waited) ptx::pdl_wait();                                  // the sums, in front of which all but them is read
+      waited = true;
+      a = piece_of(p, 0, r, lane);
+      if (drafts && !last) b = piece_of(p, 1, r, lane);
+      a = row_stats(p, 0, r, a);
+      if (drafts && !last) b = row_stats(p, 1, r, b);
+    }
     const float pd = in && a.m > kLowest ? exp_from(xp, a.m) / a.s : 0.f;
     const float qd = !drafts ? 1.f : in && b.m > kLowest ? exp_from(xq, b.m) / b.s : 0.f;
     // u q < p of fp32 numbers, exactly: the product's rounding is a number of its own
@@ -395,7 +450,7 @@ __global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_co
     }
   }
   __syncwarp();
-  if (!waited) ptx::pdl_wait();
+  if (!DIRECT && !waited) ptx::pdl_wait();
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (bad || r0 == r1) {
     if (threadIdx.x == 0 && rank == 0) {
@@ -414,8 +469,8 @@ __global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_co
     if (both) b = sh.rows[1][r - r0];
     d = sh.draft[r - r0];
   } else {
-    a = row_stats(p, 0, r);
-    if (both) b = row_stats(p, 1, r);
+    a = DIRECT ? direct_stats(logits + r * p.row, p.vocab, by, greedy) : row_stats(p, 0, r);
+    if (both) b = DIRECT ? direct_stats(drafts + r * p.draft_row, p.vocab, by, false) : row_stats(p, 1, r);
     d = refused ? p.draft[r] : -1;
   }
   if (threadIdx.x == 0 && rank == 0) {
@@ -594,25 +649,29 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
     p->cluster *= 2;
   p->z_bits = 62;
   while (((int64_t)1 << (63 - p->z_bits)) < p->vocab) --p->z_bits;
-  *workspace = (size_t)2 * p->rows * p->splits * sizeof(Piece);
+  p->direct = p->vocab <= kDirect;
+  *workspace = p->direct ? 0 : (size_t)2 * p->rows * p->splits * sizeof(Piece);
   return CP_OK;
 }
 
+template <class T, bool KEEP, bool DIRECT>
+cudaError_t launch_token(const VerifyParams& p, cudaStream_t s) {
+  return launch_as(token_kernel<T, KEEP, DIRECT>, dim3((unsigned)(p.n * p.cluster)), p.cluster, 1, !DIRECT, kTokenThreads,
+                   KEEP ? kept_bytes(p) : 0, s, p);
+}
 template <class T>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
+  if (p.direct) return launch_token<T, true, true>(p, s);
   stats_kernel<T><<<dim3((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1), kStatThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const bool keep = kept_bytes(p) <= kMostKept;
-  const dim3 grid((unsigned)(p.n * p.cluster));
-  return keep ? launch_as(token_kernel<T, true>, grid, p.cluster, 1, true, kTokenThreads, kept_bytes(p), s, p)
-              : launch_as(token_kernel<T, false>, grid, p.cluster, 1, true, kTokenThreads, 0, s, p);
+  return kept_bytes(p) <= kMostKept ? launch_token<T, true, false>(p, s) : launch_token<T, false, false>(p, s);
 }
 
-template <class T, bool KEEP>
+template <class T, bool KEEP, bool DIRECT>
 bool allow() {
-  return cudaFuncSetAttribute(token_kernel<T, KEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? (int)kMostKept : 0) == cudaSuccess &&
-         cudaFuncSetAttribute(token_kernel<T, KEEP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  return cudaFuncSetAttribute(token_kernel<T, KEEP, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? (int)kMostKept : 0) == cudaSuccess &&
+         cudaFuncSetAttribute(token_kernel<T, KEEP, DIRECT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
 }
 
 // Once per device: whether it is one that the kernels run on, and their shared memory.
@@ -622,7 +681,9 @@ int prepare(int device) {
   const int st = check_device(device);
   if (st) return st;
   DeviceGuard g(device);
-  if (!allow<float, true>() || !allow<float, false>() || !allow<__nv_bfloat16, true>() || !allow<__nv_bfloat16, false>()) return CP_ERR_CUDA;
+  if (!allow<float, true, true>() || !allow<float, true, false>() || !allow<float, false, false>() || !allow<__nv_bfloat16, true, true>() ||
+      !allow<__nv_bfloat16, true, false>() || !allow<__nv_bfloat16, false, false>())
+    return CP_ERR_CUDA;
   if (device < 64) done[device].store(1, std::memory_order_release);
   return CP_OK;
 }
@@ -645,7 +706,7 @@ int cp_verify(const cp_verify_args* args, int device, void* workspace, size_t wo
   size_t need = 0;
   const int st = check(args, &p, &need);
   if (st) return st;
-  if (!workspace || workspace_bytes < need) return CP_ERR_INVALID_ARG;
+  if (need && (!workspace || workspace_bytes < need)) return CP_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return CP_ERR_UNSUPPORTED;
   const int dev = prepare(device);
   if (dev) return dev;

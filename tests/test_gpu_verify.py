@@ -292,7 +292,7 @@ def test_the_distribution_of_what_comes_out():
 
 
 def test_refusals():
-    b = make([1], 10)
+    b = make([1], 5000)
     args = [b["logits"].cuda(), b["draft"].cuda(), torch.from_numpy(b["start"]).cuda(), b["u_accept"].cuda(), b["u_token"].cuda(),
             b["temperature"].cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")]
     cp.verify(*args)
@@ -305,7 +305,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         cp.verify(*args, draft_logits=args[0].bfloat16())
     with pytest.raises(ValueError):
-        cp.verify(*args, draft_logits=args[0][:1].expand(2, 10))
+        cp.verify(*args, draft_logits=args[0][:1].expand(2, 5000))
     with pytest.raises(cp.CPError):
         cp.verify(*args, workspace=torch.zeros(15, dtype=torch.uint8, device="cuda"))
     with pytest.raises(cp.CPError):

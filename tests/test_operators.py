@@ -88,11 +88,11 @@ def test_pools(d, want, L):
         assert L.cp_pages_create(C.byref(desc), 0, C.byref(h)) == want and not h.value
 
 
-VERIFY = dict(sequences=3, rows=9, vocab=1000, start=P, logits=P, draft=P, temperature=P, u_accept=P, u_token=P, accepted=P, token=P)
+VERIFY = dict(sequences=3, rows=9, vocab=10000, start=P, logits=P, draft=P, temperature=P, u_accept=P, u_token=P, accepted=P, token=P)
 
 
 @pytest.mark.parametrize("a,want", [
-    ({}, OK), (dict(dtype=1, draft_logits=P, prob=P, logits_stride=1001, draft_stride=1), OK), (dict(start=None), INVALID),
+    ({}, OK), (dict(dtype=1, draft_logits=P, prob=P, logits_stride=10001, draft_stride=1), OK), (dict(start=None), INVALID),
     (dict(logits=None), INVALID), (dict(draft=None), INVALID), (dict(temperature=None), INVALID), (dict(u_accept=None), INVALID),
     (dict(u_token=None), INVALID), (dict(accepted=None), INVALID), (dict(token=None), INVALID), (dict(sequences=0), INVALID),
     (dict(sequences=65536), UNSUPPORTED), (dict(rows=0), INVALID), (dict(rows=(1 << 20) + 1), UNSUPPORTED), (dict(vocab=0), INVALID),
@@ -112,9 +112,14 @@ def test_verifications(a, want, L):
         assert L.cp_verify(C.byref(args), 0, P + 8, 1 << 30, None) == UNSUPPORTED
 
 
+def test_a_small_vocabulary_needs_no_workspace(L):
+    need = C.c_size_t(7)
+    assert L.cp_verify_check(C.byref(of(cp.VerifyArgs, VERIFY, dict(vocab=2048))), C.byref(need)) == OK and need.value == 0
+
+
 def test_the_workspace_depends_on_sizes_alone():
     assert cp.verify_workspace_bytes(3, 9, 1000) == cp.verify_workspace_bytes(3, 9, 1000)
-    assert cp.verify_workspace_bytes(3, 18, 100000) > cp.verify_workspace_bytes(3, 9, 100000)
+    assert cp.verify_workspace_bytes(3, 18, 100000) > cp.verify_workspace_bytes(3, 9, 100000) > 0
 
 
 def test_binding_refuses_tensors_that_are_not_on_a_gpu():
