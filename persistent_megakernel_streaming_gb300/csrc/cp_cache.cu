@@ -321,6 +321,8 @@ constexpr int kCopyThreads = 256, kCopyUnits = 4 * kCopyThreads;
 
 // A block takes pieces of 16 KB: four 16-byte loads a thread in flight, then the stores. Bound by HBM.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
   int n = *p.count;
   if (n > p.capacity) {
     n = p.capacity;
@@ -684,8 +686,7 @@ int cp_cache_copy(cp_cache* c, const int32_t* moves, int capacity, const int32_t
   const bool aligned = aligned16(p.c.ks) && aligned16(p.c.vs) && p.c.sc_head % 16 == 0 && p.c.sc_page % 16 == 0;
   p.scale_vec = p.c.sc_tok == 1 && aligned;
   const int64_t grid = std::min<int64_t>((int64_t)capacity * p.pieces, kSms * 8);
-  copy_kernel<<<(unsigned)grid, kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  return cuda_err(cudaGetLastError());
+  return cuda_err(launch_as(copy_kernel, dim3((unsigned)grid), 1, 1, true, kCopyThreads, 0, reinterpret_cast<cudaStream_t>(stream), p));
 }
 
 int cp_cache_attend(cp_cache* c, const cp_batch* batch, const cp_attend* args, void* workspace, size_t workspace_bytes,

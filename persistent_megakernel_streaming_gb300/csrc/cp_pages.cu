@@ -38,7 +38,6 @@ struct PagesView {
   int32_t* tail;     // [pages] sequences that grow into a shared page; zeros between calls
   int32_t* keeper;   // [pages] the last of them, plus one; zeros between calls
   Plan* plan;        // [sequences]
-  int64_t* sums;     // [4][kMostBlocks]
   int32_t* live;     // [1] pages that hold something
 };
 
@@ -73,6 +72,8 @@ __device__ __forceinline__ bool in_pool(const PagesView& v, int page) { return (
 // A block a pair. Whether pairs get in each other's way is looked up among all of them by every block: no order
 // between blocks is needed then.
 __global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int32_t* src, const int32_t* dst, int n) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
   const int pair = blockIdx.x, s = src[pair], d = dst[pair];
   bool bad = (uint32_t)s >= (uint32_t)v.sequences || (uint32_t)d >= (uint32_t)v.sequences;
   for (int i = threadIdx.x; i < n; i += 256) bad |= (i != pair && dst[i] == d) || src[i] == d;
@@ -87,8 +88,8 @@ __global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int3
   }
   __syncthreads();
   if (threadIdx.x == 0) v.length[d] = len;
-  const int32_t* from = v.table + s * v.stride;
-  int32_t* to = v.table + d * v.stride;
+  const int32_t* from = v.table + (int64_t)s * v.stride;
+  int32_t* to = v.table + (int64_t)d * v.stride;
   for (int i = threadIdx.x; i < held; i += 256) {
     const int page = from[i];
     to[i] = page;
@@ -99,9 +100,10 @@ __global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int3
 
 // ------------------------------------------------------------------ trim
 __global__ void __launch_bounds__(128) trim_kernel(const PagesView v, const int32_t* keep) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
   const int i = blockIdx.x;
-  const int len = length_of(v, i);
-  int want = keep[i];
+  const int want = keep[i], len = length_of(v, i);
   if (want < 0) {
     set_status(v);
     return;
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(128) trim_kernel(const PagesView v, const int3
   __syncthreads();                       // every thread has read the length
   const int held = pages_for(v, len);
   if (threadIdx.x == 0) v.length[i] = want;
-  int32_t* row = v.table + i * v.stride;
+  int32_t* row = v.table + (int64_t)i * v.stride;
   for (int k = pages_for(v, want) + threadIdx.x; k < held; k += 128) {
     const int page = row[k];
     row[k] = -1;
@@ -125,7 +127,9 @@ __global__ void __launch_bounds__(128) trim_kernel(const PagesView v, const int3
 
 // ------------------------------------------------------------------ one cluster
 // Growing and compacting need prefix sums over all sequences and all pages: one cluster of up to 8 blocks does them, a
-// contiguous share of both to each block, and meets at cluster barriers, which order its memory accesses too.
+// contiguous share of both to each block, and meets at cluster barriers, which order its memory accesses too. What bounds
+// them is the chain of loads, scans and barriers: a thread that has one sequence, or four pages, keeps what it knows of
+// them in registers from one to the next.
 constexpr int kThreads = 1024;
 
 // Exclusive prefix of x over the block's threads; *sum: of all. Synchronises.
@@ -162,17 +166,35 @@ __device__ __forceinline__ Share share_of(int n) {
   const int64_t each = (((int64_t)n + gridDim.x - 1) / gridDim.x + 3) & ~3ll;
   return {(int)min((int64_t)n, each * blockIdx.x), (int)min((int64_t)n, each * (blockIdx.x + 1))};
 }
-// The sums of the blocks before this one, and of all, of what each has left in row `row`.
-__device__ __forceinline__ int64_t before_me(const PagesView& v, int row, int64_t* all) {
+// One value of each block told to all of the cluster, for after its next barrier.
+struct Told {
+  int64_t of[kMostBlocks];
+};
+__device__ __forceinline__ void tell(Told& t, int64_t x) {            // one warp, all lanes
+  if (threadIdx.x < gridDim.x) {
+    const uint32_t at = ptx::mapa(ptx::saddr(&t.of[blockIdx.x]), threadIdx.x);
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
+  }
+  __syncwarp();
+}
+// The sum of the blocks' before this one, and of all.
+__device__ __forceinline__ int64_t before_me(const Told& t, int64_t* all) {
   int64_t mine = 0, sum = 0;
   for (int k = 0; k < (int)gridDim.x; ++k) {
-    const int64_t x = __ldcg(v.sums + row * kMostBlocks + k);
-    if (k < (int)blockIdx.x) mine += x;
-    sum += x;
+    if (k < (int)blockIdx.x) mine += t.of[k];
+    sum += t.of[k];
   }
   *all = sum;
   return mine;
 }
+// Every block's memory is there to be written, from the wait on.
+__device__ __forceinline__ void arrive_early() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_early() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+__device__ __forceinline__ void meet() {
+  __syncwarp();
+  ptx::cluster_sync_all();
+}
+
 // Which of pages p .. p + 3 below `end` satisfy a predicate of (page, count): a bit each.
 template <class F>
 __device__ __forceinline__ uint32_t four(const PagesView& v, int p, int end, F f) {
@@ -216,7 +238,7 @@ __device__ __forceinline__ Plan ask_of(const PagesView& v, const int32_t* add, i
     return a;
   }
   if (len & ((1 << v.shift) - 1)) {
-    const int page = v.table[i * v.stride + a.had - 1];
+    const int page = v.table[(int64_t)i * v.stride + a.had - 1];
     if (!in_pool(v, page)) {
       set_status(v);
       return a;
@@ -233,64 +255,87 @@ __device__ __forceinline__ Plan ask_of(const PagesView& v, const int32_t* add, i
   return a;
 }
 
+// ONE: no thread has more than one sequence, or more than four pages.
+template <bool ONE>
 __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const int32_t* add, int32_t* moves, int32_t* count) {
+  __shared__ Told free_told, fresh_told, moved_told;
   const Share pages = share_of(v.pages), seqs = share_of(v.sequences);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, my_page = pages.begin + tid * 4, my_seq = seqs.begin + tid;
   auto is_free = [](int, int refs) { return refs == 0; };
-  for (int i = seqs.begin + tid; i < seqs.end; i += kThreads) {
-    const Plan a = ask_of(v, add, i);
-    v.plan[i] = a;
-    if (a.last >= 0) {
-      atomicAdd(v.tail + a.last, 1);
-      atomicMax(v.keeper + a.last, i + 1);
+  arrive_early();
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
+  const uint32_t bits = ONE ? four(v, my_page, pages.end, is_free) : 0;
+  Plan own{};
+  for (int i = my_seq; i < seqs.end; i += kThreads) {
+    own = ask_of(v, add, i);
+    if (!ONE) v.plan[i] = own;
+    if (own.last >= 0) {
+      atomicAdd(v.tail + own.last, 1);
+      atomicMax(v.keeper + own.last, i + 1);
     }
   }
-  const int64_t free_here = count_pages(v, pages, is_free);
-  if (tid == 0) v.sums[blockIdx.x] = free_here;
-  ptx::cluster_sync_all();
+  int64_t free_here, my_free = 0;
+  if (ONE) my_free = block_scan(__popc(bits), &free_here);
+  else free_here = count_pages(v, pages, is_free);
+  wait_early();
+  if (tid < 32) tell(free_told, free_here);
+  meet();
   // all that grow into a shared page take one of their own, but the last of them if nobody else holds it
   int64_t fresh_here = 0, moved_here = 0;
-  for (int i0 = seqs.begin; i0 < seqs.end; i0 += kThreads) {
+  for (int i0 = seqs.begin; i0 < seqs.end || ONE; i0 += kThreads) {
     const int i = i0 + tid;
-    Plan a{};
-    if (i < seqs.end) {
-      a = v.plan[i];
-      if (a.last >= 0) a.copies = !(__ldcg(v.tail + a.last) >= v.refs[a.last] && __ldcg(v.keeper + a.last) == i + 1);
-    }
+    Plan a = own;
+    if (!ONE && i < seqs.end) a = v.plan[i];
+    if (i >= seqs.end) a = Plan{-1, 0, 0, -1, 0, 0, 0};
+    if (a.last >= 0) a.copies = !(__ldcg(v.tail + a.last) >= v.refs[a.last] && __ldcg(v.keeper + a.last) == i + 1);
     int64_t sum;
     const int64_t fresh = a.want - a.had + a.copies;
     const int64_t at = block_scan((int64_t)a.copies << 40 | fresh, &sum);
-    if (i < seqs.end) {
-      v.plan[i].copies = a.copies;
-      v.plan[i].base = (int)min(fresh_here + (at & kLow), (int64_t)INT32_MAX);
-      v.plan[i].move = (int)(moved_here + (at >> 40));
-    }
+    a.base = (int)min(fresh_here + (at & kLow), (int64_t)INT32_MAX);
+    a.move = (int)(moved_here + (at >> 40));
+    if (ONE) own = a;
+    else if (i < seqs.end) v.plan[i] = a;
     fresh_here += sum & kLow;
     moved_here += sum >> 40;
+    if (ONE) break;
   }
-  if (tid == 0) {
-    v.sums[kMostBlocks + blockIdx.x] = fresh_here;
-    v.sums[2 * kMostBlocks + blockIdx.x] = moved_here;
+  if (tid < 32) {
+    tell(fresh_told, fresh_here);
+    tell(moved_told, moved_here);
   }
-  ptx::cluster_sync_all();
+  meet();
   int64_t free_all, fresh_all, moved_all;
-  const int64_t free0 = before_me(v, 0, &free_all), fresh0 = before_me(v, 1, &fresh_all), moved0 = before_me(v, 2, &moved_all);
+  const int64_t free0 = before_me(free_told, &free_all), fresh0 = before_me(fresh_told, &fresh_all), moved0 = before_me(moved_told, &moved_all);
   const bool enough = free_all >= fresh_all;
   if (blockIdx.x == 0 && tid == 0) *count = enough ? (int)moved_all : -(int)min(fresh_all - free_all, (int64_t)INT32_MAX);
-  if (enough && free0 < fresh_all)
-    each_page(v, pages, free0, is_free, [&](int64_t at, int page) {
+  if (enough && free0 < fresh_all) {
+    auto take = [&](int64_t at, int page) {
       if (at < fresh_all) v.list[at] = page;
-    });
-  ptx::cluster_sync_all();
-  // a warp a sequence
+    };
+    if (ONE) {
+      int64_t at = free0 + my_free;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (bits >> k & 1) take(at++, my_page + k);
+    } else {
+      each_page(v, pages, free0, is_free, take);
+    }
+  }
+  meet();
+  // what a sequence has is changed by its own thread, or, of many pages, by its warp
   const int lane = tid & 31;
-  for (int i = seqs.begin + (tid >> 5); i < seqs.end; i += kThreads / 32) {
-    const Plan a = v.plan[i];
-    if (a.last >= 0 && lane == 0) v.tail[a.last] = v.keeper[a.last] = 0;
-    if (!enough || a.len < 0) continue;
+  for (int i0 = seqs.begin + (tid & ~31); i0 < seqs.end; i0 += kThreads) {
+    const int i = i0 + lane;
+    Plan a = own;
+    if (!ONE && i < seqs.end) a = v.plan[i];
+    if (i >= seqs.end) a = Plan{-1, 0, 0, -1, 0, 0, 0};
+    if (a.last >= 0) v.tail[a.last] = v.keeper[a.last] = 0;
+    const bool grows = enough && a.len >= 0;
     const int64_t base = fresh0 + a.base;
-    int32_t* row = v.table + i * v.stride;
-    if (lane == 0) {
+    int32_t* row = v.table + (int64_t)i * v.stride;
+    const int more = grows ? a.want - a.had : 0;
+    if (grows) {
       v.length[i] = a.len;
       if (a.copies) {
         const int page = __ldcg(v.list + base);
@@ -301,62 +346,138 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const
         v.refs[page] = 1;
         atomicSub(v.refs + a.last, 1);
       }
+      if (more <= 2)
+        for (int k = 0; k < more; ++k) {
+          const int page = __ldcg(v.list + base + a.copies + k);
+          row[a.had + k] = page;
+          v.refs[page] = 1;
+        }
     }
-    for (int k = lane; k < a.want - a.had; k += 32) {
-      const int page = __ldcg(v.list + base + a.copies + k);
-      row[a.had + k] = page;
-      v.refs[page] = 1;
+    for (uint32_t many = __ballot_sync(0xffffffffu, more > 2); many; many &= many - 1) {
+      const int from = __ffs(many) - 1, n = __shfl_sync(0xffffffffu, more, from), had = __shfl_sync(0xffffffffu, a.had, from);
+      const int64_t at = __shfl_sync(0xffffffffu, base + a.copies, from);
+      int32_t* to = v.table + (int64_t)(i0 + from) * v.stride + had;
+      for (int k = lane; k < n; k += 32) {
+        const int page = __ldcg(v.list + at + k);
+        to[k] = page;
+        v.refs[page] = 1;
+      }
     }
   }
 }
 
 // ------------------------------------------------------------------ compact
-__global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, int32_t* moves, int32_t* count) {
-  const Share pages = share_of(v.pages);
-  const int tid = threadIdx.x;
-  const int64_t live_here = count_pages(v, pages, [](int, int refs) { return refs != 0; });
-  if (tid == 0) v.sums[blockIdx.x] = live_here;
-  ptx::cluster_sync_all();
-  int64_t all, holes, moving;
-  before_me(v, 0, &all);
-  const int n = (int)all;
-  auto is_hole = [n](int p, int refs) { return p < n && refs == 0; };
-  auto moves_on = [n](int p, int refs) { return p >= n && refs != 0; };
-  const int64_t holes_here = count_pages(v, pages, is_hole), moving_here = count_pages(v, pages, moves_on);
-  if (tid == 0) {
-    v.sums[kMostBlocks + blockIdx.x] = holes_here;
-    v.sums[2 * kMostBlocks + blockIdx.x] = moving_here;
-  }
-  ptx::cluster_sync_all();
-  const int64_t hole0 = before_me(v, 1, &holes), moving0 = before_me(v, 2, &moving);
-  each_page(v, pages, hole0, is_hole, [&](int64_t at, int page) { v.list[at] = page; });
-  for (int p = max(pages.begin, n) + tid; p < pages.end; p += kThreads) v.map[p] = -1;
-  if (blockIdx.x == 0 && tid == 0) {
-    *count = (int)moving;
-    *v.live = n;
-  }
-  ptx::cluster_sync_all();
-  each_page(v, pages, moving0, moves_on, [&](int64_t at, int page) {
-    const int to = __ldcg(v.list + at);
-    moves[2 * at] = page;
-    moves[2 * at + 1] = to;
-    v.map[page] = to;
-    v.refs[to] = v.refs[page];
-    v.refs[page] = 0;
-  });
-}
-
-// The tables, after it: a block a sequence.
-__global__ void __launch_bounds__(128) remap_kernel(const PagesView v) {
-  const int i = blockIdx.x, held = pages_for(v, length_of(v, i)), n = *v.live;
-  int32_t* row = v.table + i * v.stride;
-  for (int k = threadIdx.x; k < held; k += 128) {
+// A sequence's entries, by `threads` threads of which this is the t-th: where the pages from n on went.
+__device__ __forceinline__ void remap(const PagesView& v, int i, int n, int t, int threads) {
+  const int held = pages_for(v, length_of(v, i));
+  int32_t* row = v.table + (int64_t)i * v.stride;
+  for (int k = t; k < held; k += threads) {
     const int page = row[k];
     if (in_pool(v, page) && page < n) continue;
-    const int to = in_pool(v, page) ? v.map[page] : -1;
+    const int to = in_pool(v, page) ? __ldcg(v.map + page) : -1;
     if (to >= 0) row[k] = to;
     else set_status(v);
   }
+}
+
+// With n pages held, P(p) of them below page p: the free page p < n is the (p - P(p))-th hole, and the held page p >= n the
+// (P(p) - P(n))-th that moves. One prefix sum settles both.
+template <bool ONE>
+__global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, int32_t* moves, int32_t* count, int tables) {
+  __shared__ Told live_told, below_told;
+  __shared__ int64_t below_n;              // P(n), where this block's share has page n
+  const Share pages = share_of(v.pages);
+  const int tid = threadIdx.x, my_page = pages.begin + tid * 4;
+  auto is_live = [](int, int refs) { return refs != 0; };
+  arrive_early();
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
+  if (tid == 0) below_n = 0;
+  const uint32_t bits = ONE ? four(v, my_page, pages.end, is_live) : 0;
+  int64_t live_here, my_live = 0;
+  if (ONE) my_live = block_scan(__popc(bits), &live_here);
+  else live_here = count_pages(v, pages, is_live);
+  wait_early();
+  if (tid < 32) tell(live_told, live_here);
+  meet();
+  int64_t all;
+  const int64_t live0 = before_me(live_told, &all);
+  const int n = (int)all;
+  // holes to the list; what P(n) is, from the block that knows
+  auto holes = [&](uint32_t b, int p, int64_t before) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int page = p + k;
+      if (page >= pages.end) break;
+      if (page == n) below_n = before;
+      if (b >> k & 1) ++before;
+      else if (page < n) v.list[page - before] = page;
+      if (page >= n) v.map[page] = -1;
+    }
+  };
+  if (ONE) {
+    holes(bits, my_page, live0 + my_live);
+  } else {
+    int64_t rank = live0;
+    for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads * 4) {
+      const uint32_t b = four(v, p0 + tid * 4, pages.end, is_live);
+      int64_t sum;
+      const int64_t at = rank + block_scan(__popc(b), &sum);
+      holes(b, p0 + tid * 4, at);
+      rank += sum;
+    }
+  }
+  __syncthreads();
+  if (tid < 32) tell(below_told, below_n);
+  meet();
+  int64_t below;
+  before_me(below_told, &below);
+  if (n == v.pages) below = n;             // nothing lies behind
+  if (blockIdx.x == 0 && tid == 0) {
+    *count = n - (int)below;
+    *v.live = n;
+  }
+  auto move_on = [&](uint32_t b, int p, int64_t before) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int page = p + k;
+      if (!(b >> k & 1)) continue;
+      if (page >= n) {
+        const int64_t at = before - below;
+        const int to = __ldcg(v.list + at);
+        moves[2 * at] = page;
+        moves[2 * at + 1] = to;
+        v.map[page] = to;
+        v.refs[to] = v.refs[page];
+        v.refs[page] = 0;
+      }
+      ++before;
+    }
+  };
+  if (ONE) {
+    move_on(bits, my_page, live0 + my_live);
+  } else {
+    int64_t rank = live0;
+    for (int p0 = pages.begin; p0 < pages.end; p0 += kThreads * 4) {
+      // what other blocks write below n is not looked at: pages from n on alone move, and change in their own turn alone
+      const int p = p0 + tid * 4;
+      const uint32_t b = four(v, p, pages.end, [n](int page, int refs) { return page >= n && refs != 0; });
+      int64_t sum, at = block_scan(__popc(b), &sum);
+      if (p0 == pages.begin) rank = max(below, live0);
+      move_on(b, p, rank + at);
+      rank += sum;
+    }
+  }
+  if (!tables) return;
+  meet();
+  for (int i = blockIdx.x * (kThreads / 32) + (tid >> 5); i < v.sequences; i += gridDim.x * (kThreads / 32)) remap(v, i, n, tid & 31, 32);
+}
+
+// The tables, where they are too large for the one cluster: a block a sequence.
+__global__ void __launch_bounds__(128) remap_kernel(const PagesView v) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
+  remap(v, blockIdx.x, *v.live, threadIdx.x, 128);
 }
 
 // ------------------------------------------------------------------ checks
@@ -386,6 +507,13 @@ int blocks_for(const PagesView& v) {
   return n;
 }
 
+// Whether no thread of the cluster gets more than a sequence and four pages (shares are rounded up to four).
+bool one_each(const PagesView& v, int blocks) {
+  const auto share = [blocks](int n) { return ((n + blocks - 1) / blocks + 3) & ~3; };
+  return share(v.pages) <= 4 * kThreads && share(v.sequences) <= kThreads;
+}
+constexpr int64_t kFewEntries = 1 << 17;        // of the tables: the cluster that compacts rewrites them itself
+
 }  // namespace
 
 extern "C" {
@@ -409,7 +537,7 @@ int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out) {
   if (!p) return CP_ERR_NOMEM;
   p->device = device;
   const size_t each = up256((size_t)v.pages * 4), plans = up256((size_t)v.sequences * sizeof(Plan));
-  const size_t bytes = 4 * each + plans + 512;
+  const size_t bytes = 4 * each + plans + 256;
   if (cudaMalloc(&p->memory, bytes) != cudaSuccess) {
     cudaGetLastError();
     delete p;
@@ -421,8 +549,7 @@ int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out) {
   v.tail = reinterpret_cast<int32_t*>(at + 2 * each);
   v.keeper = reinterpret_cast<int32_t*>(at + 3 * each);
   v.plan = reinterpret_cast<Plan*>(at + 4 * each);
-  v.sums = reinterpret_cast<int64_t*>(at + 4 * each + plans);
-  v.live = reinterpret_cast<int32_t*>(at + 4 * each + plans + 256);
+  v.live = reinterpret_cast<int32_t*>(at + 4 * each + plans);
   v.status = v.live + 1;
   p->view = v;
   if (cudaMemset(p->memory, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
@@ -463,23 +590,21 @@ int cp_pages_clear_status(cp_pages* p) {
 int cp_pages_fork(cp_pages* p, const int32_t* src, const int32_t* dst, int n, cp_stream_t stream) {
   if (!p || !src || !dst || n < 1 || n > p->view.sequences) return CP_ERR_INVALID_ARG;
   DeviceGuard g(p->device);
-  fork_kernel<<<n, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p->view, src, dst, n);
-  return cuda_err(cudaGetLastError());
+  return cuda_err(launch_as(fork_kernel, dim3(n), 1, 1, true, 256, 0, reinterpret_cast<cudaStream_t>(stream), p->view, src, dst, n));
 }
 
 int cp_pages_trim(cp_pages* p, const int32_t* keep, cp_stream_t stream) {
   if (!p || !keep) return CP_ERR_INVALID_ARG;
   DeviceGuard g(p->device);
-  trim_kernel<<<p->view.sequences, 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p->view, keep);
-  return cuda_err(cudaGetLastError());
+  return cuda_err(launch_as(trim_kernel, dim3(p->view.sequences), 1, 1, true, 128, 0, reinterpret_cast<cudaStream_t>(stream), p->view, keep));
 }
 
 int cp_pages_grow(cp_pages* p, const int32_t* add, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream) {
   if (!p || !add || !moves || !count || capacity < p->view.sequences) return CP_ERR_INVALID_ARG;
   DeviceGuard g(p->device);
   const int n = blocks_for(p->view);
-  return cuda_err(launch_as(grow_kernel, dim3(n), n, 1, false, kThreads, 0, reinterpret_cast<cudaStream_t>(stream), p->view, add,
-                            moves, count));
+  return cuda_err(launch_as(one_each(p->view, n) ? grow_kernel<true> : grow_kernel<false>, dim3(n), n, 1, true, kThreads, 0,
+                            reinterpret_cast<cudaStream_t>(stream), p->view, add, moves, count));
 }
 
 int cp_pages_compact(cp_pages* p, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream) {
@@ -487,10 +612,11 @@ int cp_pages_compact(cp_pages* p, int32_t* moves, int capacity, int32_t* count, 
   DeviceGuard g(p->device);
   const int n = blocks_for(p->view);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_as(compact_kernel, dim3(n), n, 1, false, kThreads, 0, s, p->view, moves, count);
-  if (e != cudaSuccess) return CP_ERR_CUDA;
-  remap_kernel<<<p->view.sequences, 128, 0, s>>>(p->view);
-  return cuda_err(cudaGetLastError());
+  const int tables = (int64_t)p->view.sequences * p->view.width <= kFewEntries;
+  cudaError_t e = launch_as(one_each(p->view, n) ? compact_kernel<true> : compact_kernel<false>, dim3(n), n, 1, true, kThreads, 0, s,
+                            p->view, moves, count, tables);
+  if (e == cudaSuccess && !tables) e = launch_as(remap_kernel, dim3(p->view.sequences), 1, 1, true, 128, 0, s, p->view);
+  return cuda_err(e);
 }
 
 }  // extern "C"
