@@ -319,7 +319,9 @@ struct CopyParams {
 };
 constexpr int kCopyThreads = 256, kCopyUnits = 4 * kCopyThreads;
 
-// A block takes pieces of 16 KB: four 16-byte loads a thread in flight, then the stores. Bound by HBM.
+// A block takes pieces of 16 KB: four 16-byte loads a thread in flight, then the stores. Both leave L2 first, so that the
+// tables and counts of the calls around this one stay there (200 sequences branched in two, e4m3: 28 -> 25 us for the
+// four calls). Bound by HBM: 3940 pages of 262 KB 158 us, 6.5 TB/s.
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
   ptx::pdl_trigger();
   ptx::pdl_wait();
@@ -346,11 +348,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
       const int is_v = u >= half, w = is_v ? u - half : u;
       const int head = w >> place_shift, place = (w >> p.lane_shift) & ((1 << p.c.page_shift) - 1), l = w & ((1 << p.lane_shift) - 1);
       at[k] = u < p.units ? (is_v ? p.c.v : p.c.k) + (int64_t)from * p.c.page_b + head * p.c.head_b + place * p.c.tok_b + l * 16 : nullptr;
-      if (at[k]) x[k] = *reinterpret_cast<const uint4*>(at[k]);
+      if (at[k]) x[k] = __ldcs(reinterpret_cast<const uint4*>(at[k]));
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (at[k]) *reinterpret_cast<uint4*>(at[k] + there) = x[k];
+      if (at[k]) __stcs(reinterpret_cast<uint4*>(at[k] + there), x[k]);
     if (!p.c.ks || part) continue;
     // the page's scales: the first block's
     const int scales = p.c.heads << p.c.page_shift;
