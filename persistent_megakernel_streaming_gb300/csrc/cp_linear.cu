@@ -122,7 +122,10 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
   const uint8_t* words = w.records + record_at(w, t0, 0) + word_in(t0, 0, lane);
   const uint8_t* scales = w.records + record_at(w, t0, 0) + scale_in(w, t0, 0, g);
   const uint8_t* zeros = w.records + record_at(w, t0, 0) + zero_in(w, t0, 0, g);
-  const uint16_t* x_row = p.x + (int64_t)(row0 + g) * p.x_row + 4 * c;
+  // a lane without a row of x takes the last again: its columns of the products are left out
+  const uint16_t* x_row[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) x_row[n] = p.x + (int64_t)(row0 + min(n * 8 + g, rows_here - 1)) * p.x_row + 4 * c;
   ptx::pdl_trigger();
   float acc[TILES][NT][4] = {};
   for (int first = warp; first < w.per_piece; first += WARPS * U) {
@@ -149,12 +152,18 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint2 x[NT][4];
+        const int k0 = k + h * kBlockK;
+        if (k0 + kBlockK <= w.width) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint16_t* src = x_row + (int64_t)n * 8 * p.x_row + k + h * kBlockK;
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            x[n][j] = n * 8 + g < rows_here && k + h * kBlockK + 16 * j < w.width ? *reinterpret_cast<const uint2*>(src + 16 * j) : make_uint2(0, 0);
+            for (int j = 0; j < 4; ++j) x[n][j] = *reinterpret_cast<const uint2*>(x_row[n] + k0 + 16 * j);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              x[n][j] = k0 + 16 * j < w.width ? *reinterpret_cast<const uint2*>(x_row[n] + k0 + 16 * j) : make_uint2(0, 0);
         }
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
@@ -183,18 +192,19 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
       for (int i = 0; i < 4; ++i) part[warp][t * kTileRows + g + (i >> 1) * 8][n * 8 + 2 * c + (i & 1)] = acc[t][n][i];
   __syncthreads();
   constexpr int kAll = TILES * kTileRows;
-  const int per = w.gated ? kTileRows : kAll;
+  const int per = w.gated ? kAll / 2 : kAll;
   for (int i = threadIdx.x; i < per * rows_here; i += WARPS * 32) {
-    const int f = w.gated ? i & (kTileRows - 1) : i & (kAll - 1), r = w.gated ? i / kTileRows : i / kAll;
+    const int f = i & (per - 1), r = i / per;        // per is a power of two
     const int n = blockIdx.x * per + f;
     if (n >= w.outs) continue;
+    const int at = w.gated ? (f >> 4) * 32 + (f & 15) : f;
     float y = 0.f;
 #pragma unroll
-    for (int k = 0; k < WARPS; ++k) y += part[k][f][r];
-    if (TILES == 2 && w.gated) {
+    for (int k = 0; k < WARPS; ++k) y += part[k][at][r];
+    if (TILES > 1 && w.gated) {
       float up = 0.f;
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) up += part[k][(TILES - 1) * kTileRows + f][r];
+      for (int k = 0; k < WARPS; ++k) up += part[k][(at + kTileRows) & (kAll - 1)][r];
       y = silu(y) * up;
     }
     if (p.f32) finish<float>(p, row0 + r, n, 1, &y);
@@ -213,21 +223,25 @@ cudaError_t launch_few(const ApplyParams& p, cudaStream_t s) {
   return p.w.groups == 1 ? launch_few<NT, WARPS, TILES, U, 1>(p, s)
                          : p.w.groups == 2 ? launch_few<NT, WARPS, TILES, U, 2>(p, s) : launch_few<NT, WARPS, TILES, U, 4>(p, s);
 }
-// Few blocks take many warps each, which end sooner; many blocks fewer warps, so that more blocks share an SM and some
-// load while others join their sums. (1 row, 2048 to 4096, 128 blocks: 2.5 us with 16 warps, 3.5 with 8; 8 rows, 8192
-// to 8192, 256: 10.8 and 17.3; 1 row, 8192 to 28672, 896: 26.9 and 26.3; 3 rows, 2048 to 50001, 1563: 16.3 and 14.3.)
-constexpr int kManyBlocks = 512;
-
-cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
-  if (p.rows > 8) return launch_few<2, 16, 2, 1>(p, s);
-  return p.w.tiles / 2 <= kManyBlocks ? launch_few<1, 16, 2, 1>(p, s) : launch_few<1, 8, 2, 1>(p, s);
-}
-
 // Nine to sixteen rows: two fragments a word, and no tensor memory to fill, win while the weights are few. (Records of
 // 4 MB: 3.3 to 3.7 us here, 5.8 to 6.1 in the other kernel; of 6 MB 6.6 and 8.1; of 13 MB 8.7 to 9.5 and 8.6; of 34 MB 18
 // to 20 and 14.)
 constexpr int kFewRows = 8, kSomeRows = 16;
 constexpr int64_t kSomeBytes = 8 << 20;
+// Up to 8 rows: as many warps a block as leaves one round of blocks, for the more of them the sooner a block ends; where
+// there are many rounds, more of the weights a block, so that x is read less often. Measured, us (16 warps and 1 tile; 16
+// and 2; 8, 2 and two records at a time; 8 and 4): 1 row, 2048 to 4096 2.4, 3.1, 3.6, 3.8; 4 rows, 6144 to 2048 4.5, 6.0,
+// 5.7, 8.1; 8 rows, 8192 to 8192 15.5, 10.3, 14.4, 21.9; 5 rows, 2048 to 2 x 6144 gated -, 5.1, 4.4, 7; 1 row, 8192 to
+// 28672 34.1, 26.6, 26.2, 24.3; 3 rows, 2048 to 50001 21.2, 16.4, 15.2, 13.8.
+cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
+  if (p.rows > kFewRows) return launch_few<2, 16, 2, 1>(p, s);
+  const int pairs = p.w.tiles / 2;                   // blocks of two tiles; an SM holds 2 of 16 warps, 3 of 8
+  if (pairs * 2 <= 304 && !p.w.gated) return launch_few<1, 16, 1, 1>(p, s);
+  if (pairs <= 304) return launch_few<1, 16, 2, 1>(p, s);
+  if (pairs <= 456) return launch_few<1, 8, 2, 2>(p, s);
+  return launch_few<1, 8, 4, 1>(p, s);
+}
+
 bool takes_few(const ApplyParams& p) {
   return p.rows <= kFewRows || (p.rows <= kSomeRows && (int64_t)(p.w.tiles / kPadTiles) * p.w.per_piece * p.w.bytes <= kSomeBytes);
 }
