@@ -29,7 +29,9 @@ struct Piece {
 
 constexpr int kStatThreads = 256, kPer = 32;
 constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block takes
-constexpr int kTokenThreads = 512, kTokenWarps = kTokenThreads / 32;
+// Three blocks an SM: the draw waits (for loads, barriers, other blocks) more than it computes. With 512 threads a block and
+// two an SM 48 sequences over 131075 took 51 us behind the sums, with these 40.
+constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
 constexpr int kRowsKept = 32;                    // rows of a sequence whose pieces are joined once
 constexpr int kMostCluster = 16;
 constexpr int kDirect = 4096;                    // vocabularies up to which the second launch reads the rows itself
@@ -383,11 +385,15 @@ __device__ __forceinline__ Piece direct_stats(const T* row, int vocab, float by,
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 
 template <class T, bool KEEP, bool DIRECT>
-__global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(16) float kept[];       // exponentials of the block's chunk of the target's, and of the draft's
   __shared__ TokenShared sh;
   const int rank = blockIdx.x % p.cluster, seq = blockIdx.x / p.cluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // its memory may be written
+  if (DIRECT) {
+    ptx::pdl_trigger();
+    ptx::pdl_wait();
+  }
   const int r0 = p.start[seq], r1 = p.start[seq + 1];
   const float heat = p.temperature[seq], by = scale_of(heat), u_token = p.u_token[seq];
   const bool greedy = !(heat > 0.f);
@@ -608,8 +614,8 @@ __global__ void __launch_bounds__(kTokenThreads, 2) token_kernel(const __grid_co
 }
 
 // ------------------------------------------------------------------ checks
-constexpr int kResident = 2 * 152;
-constexpr size_t kMostKept = 100 * 1024;       // bytes of exponentials in a block's shared memory: two blocks an SM
+constexpr int kResident = 3 * 152;
+constexpr size_t kMostKept = 72 * 1024;        // bytes of exponentials in a block's shared memory: three blocks an SM
 size_t kept_bytes(const VerifyParams& p) { return (size_t)kept_floats(p.chunk) * (p.draft_logits ? 8 : 4); }
 
 int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
@@ -656,7 +662,7 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
 
 template <class T, bool KEEP, bool DIRECT>
 cudaError_t launch_token(const VerifyParams& p, cudaStream_t s) {
-  return launch_as(token_kernel<T, KEEP, DIRECT>, dim3((unsigned)(p.n * p.cluster)), p.cluster, 1, !DIRECT, kTokenThreads,
+  return launch_as(token_kernel<T, KEEP, DIRECT>, dim3((unsigned)(p.n * p.cluster)), p.cluster, 1, true, kTokenThreads,
                    KEEP ? kept_bytes(p) : 0, s, p);
 }
 template <class T>
