@@ -638,7 +638,8 @@ typedef struct cp_linear_desc {
 
 typedef struct cp_linear_args {
   const void* x;              /* device bf16 [rows][width]                    */
-  int64_t x_stride;           /* elements from row to row (0: contiguous)     */
+  int64_t x_stride;           /* elements from row to row (0: contiguous), no
+                                 less than width                              */
   int rows;                   /* 1 .. 65535                                   */
   int out_dtype;              /* enum cp_out_dtype                            */
   void* out;                  /* device [rows][features, or half of them]     */

@@ -129,11 +129,12 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
   ptx::pdl_trigger();
   float acc[TILES][NT][4] = {};
   for (int first = warp; first < w.per_piece; first += WARPS * U) {
+    const int here = (w.per_piece - first + WARPS - 1) / WARPS;          // records left to this warp
     uint4 word[U][TILES][2];
     uint32_t scale[U][TILES][GROUPS], zero[U][TILES][GROUPS];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at = (int64_t)min(first + u * WARPS, w.per_piece - 1) * w.bytes;   // past the last: it again, and its x as zeros
+      const int64_t at = (int64_t)(first + (u < here ? u * WARPS : 0)) * w.bytes;       // past the last: loaded, and left out
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         word[u][t][0] = *reinterpret_cast<const uint4*>(words + at + t * 512);
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
     if (first == warp) ptx::pdl_wait();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (u >= here) break;
       const int k = (first + u * WARPS) * kRecordK;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -280,7 +282,7 @@ int check_args(const Weights& w, const cp_linear_args* a, ApplyParams* p) {
   p->x_row = a->x_stride ? a->x_stride : w.width;
   p->out_row = a->out_stride ? a->out_stride : w.outs;
   p->add_row = a->add_stride ? a->add_stride : w.outs;
-  if (p->x_row < 0 || p->out_row < 0 || p->add_row < 0) return CP_ERR_INVALID_ARG;
+  if (p->x_row < 0 || p->out_row < 0 || p->add_row < 0 || (a->rows > 1 && p->x_row < w.width)) return CP_ERR_INVALID_ARG;
   const int64_t most = (int64_t)1 << 39;                       // what a tensor map's strides reach
   if (p->x_row >= most || p->out_row > most || p->add_row > most) return CP_ERR_UNSUPPORTED;
   if (p->x_row % 8 || !aligned16(a->x)) return CP_ERR_UNSUPPORTED;

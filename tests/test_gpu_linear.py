@@ -156,6 +156,17 @@ def test_extreme_scales():
         y, off = ref.apply(wide(x), ref.weights(q, wide(scale)), False)
         check(out, y, off, torch.float32)
         assert (out[:, 5] == 0).all()
+    # an infinite weight and no other: the result is infinite, whatever the block's share of the inputs
+    one = np.full((512, 64), 0x88, np.uint8)
+    one[3, 5] = 0x98
+    big = np.full((512, 1), 1.0, np.float32)
+    big[3] = np.inf
+    zeros = torch.full((512, 1), 8, dtype=torch.uint8)
+    for n in (64, 512):
+        y = torch.empty((2, n), dtype=torch.float32, device="cuda")
+        lin = cp.Linear(torch.from_numpy(one[:n]).cuda(), torch.from_numpy(big[:n]).to(torch.bfloat16).cuda(), zeros[:n].cuda())
+        lin.apply(torch.ones((2, 128), dtype=torch.bfloat16, device="cuda"), y)
+        assert y[:, 3].isnan().all() and (y[:, :3] == 0).all() and (y[:, 4:] == 0).all()      # 0 times infinity is in there
     s[7], s[9] = np.inf, np.nan
     s[11] = -2.0 ** 121                            # the largest exponent that is taken
     lin = linear(q, torch.from_numpy(s).to(torch.bfloat16), None)
@@ -190,6 +201,37 @@ def test_streams_graphs_and_repeats():
             graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.float(), 2 * want.float())
+
+
+def test_captured_behind_two_streams_and_a_copy():
+    """A captured call behind a copy, and behind kernels of two streams that met."""
+    for rows in (2, 60):
+        q, scale, z, x = make(256, 512, 64, True, 13, rows)
+        lin = linear(q, scale, z)
+        a, b, out = (torch.zeros((rows, 512), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+        out = torch.zeros((rows, 256), dtype=torch.float32, device="cuda")
+        want = torch.zeros_like(out)
+        src = x.cuda()
+        lin.apply(src, want)
+        main, side = torch.cuda.Stream(), torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=main):
+            a.copy_(src)
+            lin.apply(a, out)
+            out.zero_()
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                b.copy_(src)
+                b.add_(0)
+            a.zero_()
+            main.wait_stream(side)
+            lin.apply(b, out)
+            lin.apply(b, out, add=out)
+        for _ in range(3):
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want + want)
 
 
 def test_a_wait_that_runs_out_is_reported():

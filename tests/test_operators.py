@@ -49,7 +49,7 @@ def test_weights(d, want, L):
     ({}, OK), (dict(add=2 * P), OK), (dict(out_dtype=1, x_stride=264, out_stride=101, add=P + 4, add_stride=100), OK),
     (dict(rows=65535), OK), (dict(x=None), INVALID), (dict(out=None), INVALID), (dict(rows=0), INVALID), (dict(rows=65536), UNSUPPORTED),
     (dict(out_dtype=2), INVALID), (dict(out_dtype=-1), INVALID), (dict(x=P + 8), UNSUPPORTED), (dict(x_stride=260), UNSUPPORTED),
-    (dict(x_stride=-256), INVALID), (dict(out_stride=99), INVALID), (dict(out=P + 1), UNSUPPORTED),
+    (dict(x_stride=-256), INVALID), (dict(x_stride=248), INVALID), (dict(x_stride=8, rows=1), OK), (dict(out_stride=99), INVALID), (dict(out=P + 1), UNSUPPORTED),
     (dict(out_dtype=1, out=P + 2), UNSUPPORTED), (dict(add=P + 1), UNSUPPORTED), (dict(add=P, add_stride=-1), INVALID),
     (dict(x_stride=1 << 39), UNSUPPORTED), (dict(x_stride=(1 << 39) - 8), OK), (dict(out_stride=1 << 41), UNSUPPORTED)])
 def test_applications(a, want):
