@@ -103,14 +103,14 @@ __device__ __forceinline__ void join(Piece* a, const Piece& b) {
 // The sequence that row r belongs to, by one warp; n: none.
 __device__ __forceinline__ int sequence_of(const VerifyParams& p, int r) {
   const int lane = threadIdx.x & 31;
-  int seq = 0;
-#pragma unroll 8
-  for (int i0 = 0; i0 < p.n; i0 += 32) {
-    const int i = i0 + lane;
-    const bool before = i < p.n && p.start[min(i, p.n - 1) + 1] <= r;
-    seq += __popc(__ballot_sync(0xffffffffu, before));
+  int lo = 0, len = p.n;                 // of the sequences from lo on, `len`, those that end at or before r are counted
+  while (len > 32) {
+    const int step = (len + 31) / 32, i = lo + (lane + 1) * step;
+    const int full = __popc(__ballot_sync(0xffffffffu, i <= lo + len && p.start[min(i, p.n)] <= r));
+    lo += full * step;
+    len = min(step, len - full * step);
   }
-  return seq;
+  return lo + __popc(__ballot_sync(0xffffffffu, lane < len && p.start[min(lo + lane, p.n - 1) + 1] <= r));
 }
 
 // A thread's logits of a piece, in registers: 16 bytes at a time from a 16-byte boundary on, so that `skew` elements

@@ -94,6 +94,25 @@ def test_mixed_temperatures_and_many_sequences():
     assert accepted.max() >= 4 and (accepted == 0).any()
 
 
+def test_as_many_sequences_as_a_call_takes():
+    """Every sequence's rows are found among 65535, ragged, with empty ones among them."""
+    g = np.random.default_rng(3)
+    for vocab in (3, 4100):
+        n = 65535 if vocab == 3 else 5000
+        drafted = g.integers(0, 3, n)
+        b = make([0], vocab, seed=24, temperature=0.0)
+        start = np.concatenate([[0], np.cumsum(drafted)]).astype(np.int32)            # 0, 1 or 2 rows
+        rows = int(start[-1])
+        best = g.integers(0, vocab, rows)
+        x = torch.zeros(rows, vocab, device="cuda")
+        x[torch.arange(rows), torch.from_numpy(best).cuda()] = 1.0
+        b.update(start=start, logits=x, draft_logits=None, draft=torch.from_numpy(best.astype(np.int32)), u_accept=torch.zeros(rows),
+                 u_token=torch.zeros(n), temperature=torch.zeros(n))
+        accepted, token, _ = run(b)
+        np.testing.assert_array_equal(accepted, np.maximum(drafted - 1, 0))
+        np.testing.assert_array_equal(token, np.where(drafted > 0, best[np.minimum(start[1:] - 1, rows - 1)], -1))
+
+
 def test_long_drafts_and_large_vocabularies():
     check(make([40, 100, 0], 400, seed=6, sharp=1.0))
     check(make([2, 1], 151000, seed=7))
