@@ -117,15 +117,14 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
   __shared__ float part[WARPS][TILES * kTileRows][8 * NT + 1];
   const Weights& w = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int t0 = blockIdx.x * TILES, row0 = blockIdx.y * 8 * NT;
-  const int rows_here = min(8 * NT, p.rows - row0);
+  const int t0 = blockIdx.x * TILES;
   const uint8_t* words = w.records + record_at(w, t0, 0) + word_in(t0, 0, lane);
   const uint8_t* scales = w.records + record_at(w, t0, 0) + scale_in(w, t0, 0, g);
   const uint8_t* zeros = w.records + record_at(w, t0, 0) + zero_in(w, t0, 0, g);
   // a lane without a row of x takes the last again: its columns of the products are left out
   const uint16_t* x_row[NT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) x_row[n] = p.x + (int64_t)(row0 + min(n * 8 + g, rows_here - 1)) * p.x_row + 4 * c;
+  for (int n = 0; n < NT; ++n) x_row[n] = p.x + (int64_t)min(n * 8 + g, p.rows - 1) * p.x_row + 4 * c;
   ptx::pdl_trigger();
   float acc[TILES][NT][4] = {};
   for (int first = warp; first < w.per_piece; first += WARPS * U) {
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
   __syncthreads();
   constexpr int kAll = TILES * kTileRows;
   const int per = w.gated ? kAll / 2 : kAll;
-  for (int i = threadIdx.x; i < per * rows_here; i += WARPS * 32) {
+  for (int i = threadIdx.x; i < per * p.rows; i += WARPS * 32) {
     const int f = i & (per - 1), r = i / per;        // per is a power of two
     const int n = blockIdx.x * per + f;
     if (n >= w.outs) continue;
@@ -209,14 +208,14 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
       for (int k = 0; k < WARPS; ++k) up += part[k][(at + kTileRows) & (kAll - 1)][r];
       y = silu(y) * up;
     }
-    if (p.f32) finish<float>(p, row0 + r, n, 1, &y);
-    else finish<__nv_bfloat16>(p, row0 + r, n, 1, &y);
+    if (p.f32) finish<float>(p, r, n, 1, &y);
+    else finish<__nv_bfloat16>(p, r, n, 1, &y);
   }
 }
 
 template <int NT, int WARPS, int TILES, int U, int GROUPS>
 cudaError_t launch_few(const ApplyParams& p, cudaStream_t s) {
-  const dim3 grid(p.w.tiles / TILES, (p.rows + 8 * NT - 1) / (8 * NT));
+  const dim3 grid(p.w.tiles / TILES);
   return p.w.zero ? launch_as(few_rows_kernel<NT, WARPS, TILES, U, GROUPS, true>, grid, 1, 1, true, WARPS * 32, 0, s, p)
                   : launch_as(few_rows_kernel<NT, WARPS, TILES, U, GROUPS, false>, grid, 1, 1, true, WARPS * 32, 0, s, p);
 }
@@ -247,7 +246,6 @@ cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
 bool takes_few(const ApplyParams& p) {
   return p.rows <= kFewRows || (p.rows <= kSomeRows && (int64_t)(p.w.tiles / kPadTiles) * p.w.per_piece * p.w.bytes <= kSomeBytes);
 }
-
 
 // ------------------------------------------------------------------ checks
 int check_desc(const cp_linear_desc* d, Weights* w) {

@@ -645,7 +645,8 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   p->rows = a->rows;
   p->vocab = a->vocab;
   p->cluster = 1;
-  p->splits = (a->vocab + (int)(16 / es) - 1 + kPiece - 1) / kPiece;        // wherever a row starts within 16 bytes
+  const auto splits = [a](int es) { return (a->vocab + 16 / es - 1 + kPiece - 1) / kPiece; };   // wherever a row starts within 16 bytes
+  p->splits = splits((int)es);
   if ((int64_t)p->rows * p->splits > 1 << 30) return CP_ERR_UNSUPPORTED;             // blocks
   // blocks a sequence: more while there is work for them and room for all at once, or until a block's share can be kept
   auto cut = [&] { p->chunk = (p->vocab + p->cluster - 1) / p->cluster; };
@@ -656,7 +657,7 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   p->z_bits = 62;
   while (((int64_t)1 << (63 - p->z_bits)) < p->vocab) --p->z_bits;
   p->direct = p->vocab <= kDirect;
-  *workspace = p->direct ? 0 : (size_t)2 * p->rows * p->splits * sizeof(Piece);
+  *workspace = p->direct ? 0 : (size_t)2 * p->rows * splits(2) * sizeof(Piece);       // the same for both types
   return CP_OK;
 }
 

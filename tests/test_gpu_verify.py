@@ -94,6 +94,13 @@ def test_mixed_temperatures_and_many_sequences():
     assert accepted.max() >= 4 and (accepted == 0).any()
 
 
+@pytest.mark.parametrize("vocab", [8185, 8187, 8189, 16381])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_that_end_just_before_a_piece_does(vocab, dtype):
+    check(make([3, 0, 2], vocab, dtype, seed=vocab))
+    check(make([2, 1], vocab, dtype, seed=vocab, pad=3))
+
+
 def test_as_many_sequences_as_a_call_takes():
     """Every sequence's rows are found among 65535, ragged, with empty ones among them."""
     g = np.random.default_rng(3)

@@ -117,6 +117,17 @@ def test_a_small_vocabulary_needs_no_workspace(L):
     assert L.cp_verify_check(C.byref(of(cp.VerifyArgs, VERIFY, dict(vocab=2048))), C.byref(need)) == OK and need.value == 0
 
 
+@pytest.mark.parametrize("vocab", [4097, 8184, 8185, 8186, 8187, 8188, 8189, 8190, 16380, 16381, 32000, 1 << 24])
+def test_the_workspace_is_the_same_for_both_types(L, vocab):
+    a = of(cp.VerifyArgs, VERIFY, dict(vocab=vocab))
+    sizes = []
+    for a.dtype in (0, 1):
+        n = C.c_size_t()
+        assert L.cp_verify_check(C.byref(a), C.byref(n)) == OK
+        sizes.append(n.value)
+    assert sizes == [cp.verify_workspace_bytes(a.sequences, a.rows, vocab)] * 2
+
+
 def test_the_workspace_depends_on_sizes_alone():
     assert cp.verify_workspace_bytes(3, 9, 1000) == cp.verify_workspace_bytes(3, 9, 1000)
     assert cp.verify_workspace_bytes(3, 18, 100000) > cp.verify_workspace_bytes(3, 9, 100000) > 0
