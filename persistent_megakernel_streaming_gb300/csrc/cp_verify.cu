@@ -6,6 +6,9 @@
 // token behind them from one row: there it sums again, in 64-bit fixed point,
 // so that the draw does not depend on the order of the sums. Over a small
 // vocabulary the second reads the rows itself, and is the only one.
+//
+// Of 48 sequences of 7 drafted tokens over 131075 fp32 logits (378 MB) the
+// first takes 62 us (6.1 TB/s), the second 39 behind it.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,11 +33,17 @@ struct Piece {
 constexpr int kStatThreads = 256, kPer = 32;
 constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block takes
 // Three blocks an SM: the draw waits (for loads, barriers, other blocks) more than it computes. With 512 threads a block and
-// two an SM 48 sequences over 131075 took 51 us behind the sums, with these 40.
-constexpr int kTokenThreads = 256, kTokenWarps = kTokenThreads / 32;
+// two an SM 48 sequences over 131075 took 51 us behind the sums, with these 40. Reading small rows itself, it takes 512
+// for up to as many sequences as SMs: us with 512 and 256 for 1 sequence of 4 drafted tokens over 4096 9.9 and 12.2, for
+// 152 of 5 over 2048 9.4 and 10.4, for 256 of 5 over 2048 18.9 and 15.7.
+constexpr int kTokenThreads = 256, kWideThreads = 512;
+constexpr int kWideMost = 152;
 constexpr int kRowsKept = 32;                    // rows of a sequence whose pieces are joined once
 constexpr int kMostCluster = 16;
-constexpr int kDirect = 4096;                    // vocabularies up to which the second launch reads the rows itself
+// Vocabularies up to which the second launch reads the rows itself, us with one launch and with two: 1 sequence of 4 drafted
+// tokens over 2048 9.2 and 10.4, over 4096 9.9 and 10.4, over 8192 13.9 and 11.4; 64 of 3 over 4096 10.5 and 14.4, over 8192
+// 14.7 and 18.5; 1000 of 3 over 4096 43 and 60.
+constexpr int kDirect = 4096;
 
 struct VerifyParams {
   const int32_t* start;
@@ -145,7 +154,7 @@ struct Loads {
   }
 };
 
-// Bound by HBM. A thread holds its 32 logits, so that their maximum comes first and nothing is rescaled; an exponential
+// Bound by HBM (6.1 TB/s). A thread holds its 32 logits, so that their maximum comes first and nothing is rescaled; an exponential
 // is one multiplication, one fused one, and ex2. Where NaN or infinities spoil that, the piece is done again with
 // clamped logits.
 template <class T>
@@ -257,10 +266,12 @@ struct Sum {
     return to_fixed(hi, bits) + (lo < 0.f ? 0 - l : l);
   }
 };
+// The warp's sum (modulo 2^64), by 32-bit reductions of parts that leave room for 32 of them: 27, 27 and 10 bits.
 __device__ __forceinline__ fixed warp_total(fixed x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+  const uint32_t part = (1u << 27) - 1;
+  const uint32_t a = __reduce_add_sync(0xffffffffu, (uint32_t)x & part), b = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 27) & part),
+                 c = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 54));
+  return a + ((fixed)b << 27) + ((fixed)c << 54);
 }
 __device__ __forceinline__ fixed warp_prefix(fixed x) {
   const int lane = threadIdx.x & 31;
@@ -288,12 +299,13 @@ __device__ __forceinline__ fixed times(float u, fixed x) {
   return down < 64 ? hi << (64 - down) | lo >> down : down < 128 ? hi >> (down - 64) : 0;
 }
 
+template <int WARPS>
 struct TokenShared {
   int first;                            // the first refused row, or the last
   Piece rows[2][kRowsKept];             // the target's and the draft's rows
   int draft[kRowsKept];
-  fixed part[2][kTokenWarps];           // each warp's sums
-  Piece pair[kTokenWarps / 2];          // what one warp of a pair found out about the draft
+  fixed part[2][WARPS];           // each warp's sums
+  Piece pair[WARPS / 2];          // what one warp of a pair found out about the draft
   fixed z[2][kMostCluster];             // each block's sums of exponentials
   fixed w[2][kMostCluster];             // each block's sum of weights, by turn
   float rz[2];                          // 1 over all of them
@@ -317,6 +329,11 @@ struct Part {
   float m;
   __device__ __forceinline__ Part(const T* s, int n, float top)
       : src(s), size(n), skew((int)((reinterpret_cast<uintptr_t>(s) & 15) / sizeof(T))), m(top) {}
+  __device__ __forceinline__ static float get(const uint4& raw, int k) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    if (sizeof(T) == 4) return __uint_as_float(w[k & 3]);
+    return __uint_as_float(k & 1 ? w[(k >> 1) & 3] & 0xffff0000u : w[(k >> 1) & 3] << 16);
+  }
   // the v-th 16 bytes; minus infinity for what is not its
   __device__ __forceinline__ uint4 load(int v) const {
     const int i = v * K - skew;
@@ -334,12 +351,10 @@ struct Part {
   // their exponentials: added to z and, if KEEP, left at kept[skew + i]. 0 for what is not there: m is above the lowest
   template <bool KEEP>
   __device__ __forceinline__ void take(int v, const uint4& raw, float by, Sum* z, float* kept) const {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     float e[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const float l = sizeof(T) == 4 ? __uint_as_float(w[k & 3]) : __uint_as_float(k & 1 ? w[(k >> 1) & 3] & 0xffff0000u : w[(k >> 1) & 3] << 16);
-      e[k] = exp_from(scaled(l, by), m);
+      e[k] = exp_from(scaled(get(raw, k), by), m);
       z[k & 1].add(e[k]);
     }
     if (KEEP && v * K < size + skew)
@@ -355,13 +370,23 @@ __host__ __device__ __forceinline__ int kept_floats(int chunk) { return (chunk +
 template <class T>
 __device__ __forceinline__ Piece direct_stats(const T* row, int vocab, float by, bool greedy) {
   const int lane = threadIdx.x & 31;
+  // each of a lane's logits, with its place, 32 loads under way at once; minus infinity behind the row
+  auto each = [&](auto f) {
+    for (int i0 = 0; i0 < vocab; i0 += 32 * 32) {
+      float x[32];
+#pragma unroll
+      for (int u = 0; u < 32; ++u) x[u] = i0 + lane + 32 * u < vocab ? value(row + i0 + lane + 32 * u) : -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) f(x[u], i0 + lane + 32 * u);
+    }
+  };
   Piece a = {kLowest, 0.f, INT32_MAX, 0};
-#pragma unroll 16
-  for (int i = lane; i < vocab; i += 32) a.m = fmaxf(a.m, __fmul_rn(value(row + i), by));
+  each([&](float l, int) { a.m = fmaxf(a.m, __fmul_rn(l, by)); });
   a.m = warp_max(a.m);
   const float ref = -__fmul_rn(a.m, kLog2e);
-#pragma unroll 16
-  for (int i = lane; i < vocab; i += 32) a.s += ex2(__fmaf_rn(__fmul_rn(value(row + i), by), kLog2e, ref));
+  float s[2] = {};
+  each([&](float l, int i) { s[i >> 5 & 1] += ex2(__fmaf_rn(__fmul_rn(l, by), kLog2e, ref)); });
+  a.s = s[0] + s[1];
   if (__any_sync(0xffffffffu, !(a.s <= FLT_MAX)) || a.m == INFINITY) {     // NaN or infinities: clamped logits
     a.m = kLowest;
     a.s = 0.f;
@@ -370,11 +395,9 @@ __device__ __forceinline__ Piece direct_stats(const T* row, int vocab, float by,
     for (int i = lane; i < vocab; i += 32) a.s += exp_from(scaled(value(row + i), by), a.m);
   }
   if (greedy) {
-    for (int i = lane; i < vocab; i += 32)
-      if (scaled(value(row + i), by) == a.m) {
-        a.arg = i;
-        break;
-      }
+    each([&](float l, int i) {
+      if (i < a.arg && scaled(l, by) == a.m) a.arg = i;
+    });
     a.arg = __reduce_min_sync(0xffffffffu, a.arg);
   }
   a.s = warp_sum(a.s);
@@ -384,13 +407,21 @@ __device__ __forceinline__ Piece direct_stats(const T* row, int vocab, float by,
 // The two warps that share a row: a barrier of their own.
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 
-template <class T, bool KEEP, bool DIRECT>
-__global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_constant__ VerifyParams p) {
+// What a sequence's blocks do. The first passes are short, so this is a chain of loads, sums over a warp, a block and a
+// cluster, and barriers: 6 to 10 us from launch to launch for a few sequences, whatever the vocabulary up to 4096, and 11 us a
+// round of blocks over large ones. KEEP: the exponentials of the block's logits stay in shared memory between the sum
+// of them and the weights (n = 64 over 32000: 18.6 us, without 37.9); DIRECT: as many threads, and the rows' sums are
+// made here.
+template <class T, bool KEEP, int DIRECT>
+__global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWideThreads ? 1 : 3) token_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(16) float kept[];       // exponentials of the block's chunk of the target's, and of the draft's
-  __shared__ TokenShared sh;
-  const int rank = blockIdx.x % p.cluster, seq = blockIdx.x / p.cluster, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // its memory may be written
-  if (DIRECT) {
+  constexpr int kThreads = DIRECT ? DIRECT : kTokenThreads, kWarps = kThreads / 32;
+  __shared__ TokenShared<kWarps> sh;
+  const int cluster = DIRECT ? 1 : p.cluster, rank = DIRECT ? 0 : blockIdx.x % p.cluster, seq = DIRECT ? blockIdx.x : blockIdx.x / p.cluster;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!DIRECT) {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // its memory may be written
+  } else {
     ptx::pdl_trigger();
     ptx::pdl_wait();
   }
@@ -399,7 +430,7 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
   const bool greedy = !(heat > 0.f);
   // a start out of order leaves in doubt whose rows are whose, for every sequence
   bool out_of_order = false;
-  for (int i = threadIdx.x; i < p.n; i += kTokenThreads) {
+  for (int i = threadIdx.x; i < p.n; i += kThreads) {
     const int b = p.start[i], e = p.start[i + 1];
     out_of_order |= b < 0 || e < b || e > p.rows;
   }
@@ -411,13 +442,11 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
   // every block of the cluster does the same: a warp a row, or, where the rows are read here, one for the target's and one
   // for the draft's
   constexpr int kRowWarps = DIRECT ? 2 : 1;
-  for (int r = r0 + warp / kRowWarps; r < r1 && !bad; r += kTokenWarps / kRowWarps) {
+  for (int r = r0 + warp / kRowWarps; r < r1 && !bad; r += kWarps / kRowWarps) {
     const bool last = r == r1 - 1;
     const int d = last ? -1 : p.draft[r];
     const bool in = (uint32_t)d < (uint32_t)p.vocab;
     const float u = last ? 0.f : fminf(fmaxf(p.u_accept[r], 0.f), 0x1.fffffep-1f);
-    const float xp = in ? scaled(value(logits + r * p.row + d), by) : 0.f;
-    const float xq = in && drafts ? scaled(value(drafts + r * p.draft_row + d), by) : 0.f;
     Piece a, b = {kLowest, 0.f, 0, 0};
     if (DIRECT) {
       const bool of_draft = warp & 1;
@@ -439,6 +468,8 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
       a = row_stats(p, 0, r, a);
       if (drafts && !last) b = row_stats(p, 1, r, b);
     }
+    const float xp = in ? scaled(value(logits + r * p.row + d), by) : 0.f;
+    const float xq = in && drafts ? scaled(value(drafts + r * p.draft_row + d), by) : 0.f;
     const float pd = in && a.m > kLowest ? exp_from(xp, a.m) / a.s : 0.f;
     const float qd = !drafts ? 1.f : in && b.m > kLowest ? exp_from(xq, b.m) / b.s : 0.f;
     // u q < p of fp32 numbers, exactly: the product's rounding is a number of its own
@@ -457,7 +488,7 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
   }
   __syncwarp();
   if (!DIRECT && !waited) ptx::pdl_wait();
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (!DIRECT) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (bad || r0 == r1) {
     if (threadIdx.x == 0 && rank == 0) {
       p.accepted[seq] = bad ? -1 : 0;
@@ -495,18 +526,18 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
   // sums of both rows' exponentials; two of each, whose steps do not wait for one another
   Sum sum_p[2], sum_q[2];
   constexpr int U = sizeof(T) == 4 ? 4 : 2;
-  for (int v0 = threadIdx.x; v0 * Part<T>::K < size + max(of_p.skew, of_q.skew); v0 += U * kTokenThreads) {
+  for (int v0 = threadIdx.x; v0 * Part<T>::K < size + max(of_p.skew, of_q.skew); v0 += U * kThreads) {
     uint4 x[U], y[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) x[u] = of_p.load(v0 + u * kTokenThreads);
+    for (int u = 0; u < U; ++u) x[u] = of_p.load(v0 + u * kThreads);
     if (with_q)
 #pragma unroll
-      for (int u = 0; u < U; ++u) y[u] = of_q.load(v0 + u * kTokenThreads);
+      for (int u = 0; u < U; ++u) y[u] = of_q.load(v0 + u * kThreads);
 #pragma unroll
-    for (int u = 0; u < U; ++u) of_p.template take<KEEP>(v0 + u * kTokenThreads, x[u], by, sum_p, kept);
+    for (int u = 0; u < U; ++u) of_p.template take<KEEP>(v0 + u * kThreads, x[u], by, sum_p, kept);
     if (with_q)
 #pragma unroll
-      for (int u = 0; u < U; ++u) of_q.template take<KEEP>(v0 + u * kTokenThreads, y[u], by, sum_q, put_q);
+      for (int u = 0; u < U; ++u) of_q.template take<KEEP>(v0 + u * kThreads, y[u], by, sum_q, put_q);
   }
   fixed zp = sum_p[0].value(p.z_bits) + sum_p[1].value(p.z_bits), zq = 0;
   if (with_q) zq = warp_total(sum_q[0].value(p.z_bits) + sum_q[1].value(p.z_bits));
@@ -517,11 +548,20 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
   }
   __syncthreads();
   // over the block, and over the cluster: one warp's work
-  auto of_block = [&](const fixed* parts) { return warp_total(lane < kTokenWarps ? parts[lane] : 0); };
-  auto of_cluster = [&](const fixed* slots) { return warp_total(lane < p.cluster ? slots[lane] : 0); };
+  auto of_block = [&](const fixed* parts) { return warp_total(lane < kWarps ? parts[lane] : 0); };
+  auto of_cluster = [&](const fixed* slots) { return DIRECT ? slots[0] : warp_total(lane < cluster ? slots[lane] : 0); };
+  auto to_all = [&](fixed* slots, fixed x) {
+    if (!DIRECT) tell(slots + rank, cluster, x);
+    else if (lane == 0) slots[0] = x;
+  };
+  auto meet = [] {
+    __syncwarp();
+    if (DIRECT) __syncthreads();
+    else ptx::cluster_sync_all();
+  };
   if (warp == 0) {
-    tell(&sh.z[0][rank], p.cluster, of_block(sh.part[0]));
-    if (with_q) tell(&sh.z[1][rank], p.cluster, of_block(sh.part[1]));
+    to_all(sh.z[0], of_block(sh.part[0]));
+    if (with_q) to_all(sh.z[1], of_block(sh.part[1]));
   }
   // the token that a certain draft proposed weighs nothing where it was refused; its exponential is kept aside
   const int out = refused && !drafts && (uint32_t)(d - begin) < (uint32_t)size ? d - begin : -1;
@@ -530,8 +570,7 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
     aside = kept_p[out];
     kept[of_p.skew + out] = 0.f;
   }
-  __syncwarp();
-  ptx::cluster_sync_all();
+  meet();
   if (warp < 2) {
     const fixed z = of_cluster(sh.z[warp]);
     if (lane == 0) sh.rz[warp] = warp == 0 || with_q ? inverse(z, p.z_bits) : 0.f;
@@ -552,7 +591,7 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
     return fmaxf(__fsub_rn(__fmul_rn(x, rp), __fmul_rn(y, rq)), 0.f);
   };
   // each warp a stretch of the block's logits, of whole 32s
-  const int each = ((size + kTokenWarps - 1) / kTokenWarps + 31) & ~31, w0 = min(warp * each, size), w1 = min(w0 + each, size);
+  const int each = ((size + kWarps - 1) / kWarps + 31) & ~31, w0 = min(warp * each, size), w1 = min(w0 + each, size);
   fixed total = 0;
   int turn = 0;
   for (;; ++turn) {
@@ -562,11 +601,10 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
     const fixed w = warp_total(sum.value(kWeightBits));
     if (lane == 0) sh.part[turn][warp] = w;
     __syncthreads();
-    if (warp == 0) tell(&sh.w[turn][rank], p.cluster, of_block(sh.part[turn]));
-    __syncwarp();
-    ptx::cluster_sync_all();
+    if (warp == 0) to_all(sh.w[turn], of_block(sh.part[turn]));
+    meet();
     total = 0;
-    for (int k = 0; k < p.cluster; ++k) total |= sh.w[turn][k];      // whether there is any
+    for (int k = 0; k < cluster; ++k) total |= sh.w[turn][k];      // whether there is any
     if (total || turn) break;                                        // the same in every block
     // roundings left nothing: from p itself
     residual = false;
@@ -587,8 +625,8 @@ __global__ void __launch_bounds__(kTokenThreads, 3) token_kernel(const __grid_co
     return at;
   };
   fixed before = 0;
-  if (first_above(lane < p.cluster ? sh.w[turn][lane] : 0, &before) != rank) return;
-  const int stretch = first_above(lane < kTokenWarps ? sh.part[turn][lane] : 0, &before);
+  if (!DIRECT && first_above(lane < cluster ? sh.w[turn][lane] : 0, &before) != rank) return;
+  const int stretch = first_above(lane < kWarps ? sh.part[turn][lane] : 0, &before);
   const int s0 = min(stretch * each, size), s1 = min(s0 + each, size);
   int at = s0;
   int run = 1;                                                       // a power of two
@@ -648,34 +686,35 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   const auto splits = [a](int es) { return (a->vocab + 16 / es - 1 + kPiece - 1) / kPiece; };   // wherever a row starts within 16 bytes
   p->splits = splits((int)es);
   if ((int64_t)p->rows * p->splits > 1 << 30) return CP_ERR_UNSUPPORTED;             // blocks
+  p->direct = p->vocab <= kDirect;
   // blocks a sequence: more while there is work for them and room for all at once, or until a block's share can be kept
+  // (16 blocks and 8, us: 16 sequences over 131075 29 and 49, 1 14 and 27; room for twice as many: 64 over 32000 18.6 -> 22.6)
   auto cut = [&] { p->chunk = (p->vocab + p->cluster - 1) / p->cluster; };
-  for (cut(); p->cluster < kMostCluster &&
+  for (cut(); !p->direct && p->cluster < kMostCluster &&
               ((p->chunk > 2048 && (int64_t)p->n * p->cluster * 2 <= kResident) || kept_bytes(*p) > kMostKept);
        cut())
     p->cluster *= 2;
   p->z_bits = 62;
   while (((int64_t)1 << (63 - p->z_bits)) < p->vocab) --p->z_bits;
-  p->direct = p->vocab <= kDirect;
   *workspace = p->direct ? 0 : (size_t)2 * p->rows * splits(2) * sizeof(Piece);       // the same for both types
   return CP_OK;
 }
 
-template <class T, bool KEEP, bool DIRECT>
+template <class T, bool KEEP, int DIRECT>
 cudaError_t launch_token(const VerifyParams& p, cudaStream_t s) {
-  return launch_as(token_kernel<T, KEEP, DIRECT>, dim3((unsigned)(p.n * p.cluster)), p.cluster, 1, true, kTokenThreads,
+  return launch_as(token_kernel<T, KEEP, DIRECT>, dim3((unsigned)(p.n * p.cluster)), p.cluster, 1, true, DIRECT ? DIRECT : kTokenThreads,
                    KEEP ? kept_bytes(p) : 0, s, p);
 }
 template <class T>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
-  if (p.direct) return launch_token<T, true, true>(p, s);
+  if (p.direct) return p.n <= kWideMost ? launch_token<T, true, kWideThreads>(p, s) : launch_token<T, true, kTokenThreads>(p, s);
   stats_kernel<T><<<dim3((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1), kStatThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return kept_bytes(p) <= kMostKept ? launch_token<T, true, false>(p, s) : launch_token<T, false, false>(p, s);
+  return kept_bytes(p) <= kMostKept ? launch_token<T, true, 0>(p, s) : launch_token<T, false, 0>(p, s);
 }
 
-template <class T, bool KEEP, bool DIRECT>
+template <class T, bool KEEP, int DIRECT>
 bool allow() {
   return cudaFuncSetAttribute(token_kernel<T, KEEP, DIRECT>, cudaFuncAttributeMaxDynamicSharedMemorySize, KEEP ? (int)kMostKept : 0) == cudaSuccess &&
          cudaFuncSetAttribute(token_kernel<T, KEEP, DIRECT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
@@ -688,8 +727,11 @@ int prepare(int device) {
   const int st = check_device(device);
   if (st) return st;
   DeviceGuard g(device);
-  if (!allow<float, true, true>() || !allow<float, true, false>() || !allow<float, false, false>() || !allow<__nv_bfloat16, true, true>() ||
-      !allow<__nv_bfloat16, true, false>() || !allow<__nv_bfloat16, false, false>())
+  const auto all = [](auto t) {
+    using T = decltype(t);
+    return allow<T, true, kWideThreads>() && allow<T, true, kTokenThreads>() && allow<T, true, 0>() && allow<T, false, 0>();
+  };
+  if (!all(0.f) || !all(__nv_bfloat16()))
     return CP_ERR_CUDA;
   if (device < 64) done[device].store(1, std::memory_order_release);
   return CP_OK;
