@@ -112,8 +112,16 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
 // NT tiles of 8 rows of x; a block has TILES tiles of the weights (of a gated projection the gate's and the same of up),
 // its WARPS warps every so manieth record, U records at a time, whose loads are all under way before the first is used;
 // the first of them before the kernel in front has ended, since nobody writes weights. GROUPS of scales a record.
+// Bound by the chain of loads, widening (some 20 instructions a word of 8 weights) and products of a block, and by how many
+// blocks an SM holds: three of 8 warps, even where registers spill for it (us with that bound and without: 3 rows, 2048 to
+// 50001 13.6 and 15.5; 1 row, 8192 to 28672 in groups of 64 26.1 and 29.0; 2 rows, 6144 to 12288 in groups of 32 12.6 and
+// 16.6), but for 4 tiles with zero points of small groups (16.9 becomes 20.3); two of 16 with 2 tiles; with 1 the compiler
+// does better unbound (2.4 and 2.6).
+template <int NT, int WARPS, int TILES, int GROUPS, bool ZERO>
+constexpr int kBlocksAnSm = NT > 1 || TILES == 1 ? 0 : WARPS == 16 ? 2 : TILES == 4 && ZERO && GROUPS > 1 ? 2 : 3;
+
 template <int NT, int WARPS, int TILES, int U, int GROUPS, bool ZERO>
-__global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_constant__ ApplyParams p) {
+__global__ void __launch_bounds__(WARPS * 32, kBlocksAnSm<NT, WARPS, TILES, GROUPS, ZERO>) few_rows_kernel(const __grid_constant__ ApplyParams p) {
   __shared__ float part[WARPS][TILES * kTileRows][8 * NT + 1];
   const Weights& w = p.w;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -128,19 +136,18 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
   ptx::pdl_trigger();
   float acc[TILES][NT][4] = {};
   for (int first = warp; first < w.per_piece; first += WARPS * U) {
-    const int here = (w.per_piece - first + WARPS - 1) / WARPS;          // records left to this warp
     uint4 word[U][TILES][2];
     uint32_t scale[U][TILES][GROUPS], zero[U][TILES][GROUPS];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at = (int64_t)(first + (u < here ? u * WARPS : 0)) * w.bytes;       // past the last: loaded, and left out
+      const int64_t at = (int64_t)min(first + u * WARPS, w.per_piece - 1) * w.bytes;   // past the last: it again, its scales and x as zeros
 #pragma unroll
       for (int t = 0; t < TILES; ++t) {
         word[u][t][0] = *reinterpret_cast<const uint4*>(words + at + t * 512);
         word[u][t][1] = *reinterpret_cast<const uint4*>(words + at + t * 512 + 4096);
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
-          scale[u][t][i] = *reinterpret_cast<const uint32_t*>(scales + at + t * 32 + i * kRecordScales);
+          scale[u][t][i] = u > 0 && first + u * WARPS >= w.per_piece ? 0 : *reinterpret_cast<const uint32_t*>(scales + at + t * 32 + i * kRecordScales);
           zero[u][t][i] = ZERO ? *reinterpret_cast<const uint16_t*>(zeros + at + t * 16 + i * kRecordZeros) : 0;
         }
       }
@@ -148,7 +155,6 @@ __global__ void __launch_bounds__(WARPS * 32) few_rows_kernel(const __grid_const
     if (first == warp) ptx::pdl_wait();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (u >= here) break;
       const int k = (first + u * WARPS) * kRecordK;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
