@@ -146,6 +146,31 @@ def test_many_pages_and_sequences(pages, sequences):
     b.compact()
 
 
+@pytest.mark.parametrize("sequences,pages,width", [(1, 64, 60), (33, 4096, 130), (80, 4097, 60), (129, 20000, 200), (1030, 33000, 40),
+                                                   (8300, 70000, 9), (300, 40000, 130)])
+def test_many_pages_at_once(sequences, pages, width):
+    """Sequences that take up to `width` pages in one call, some none, some one or two, over shared pages too; half of them
+    end, and the others move."""
+    g = np.random.default_rng(sequences)
+    b = empty(pages, sequences, width, stride=width + 3)
+    some = g.random(sequences)
+    add = np.where(some < 0.3, 0, np.where(some < 0.5, g.integers(1, 33, sequences), g.integers(1, 16 * width - 60, sequences)))
+    add = np.where(g.random(sequences) < 0.05, 16 * (width - 4), add)
+    while (-(-add // 16)).sum() > pages * 3 // 4:
+        add = add // 2
+    b.grow(add)
+    empty_ones = np.flatnonzero(add == 0)
+    n = len(empty_ones) // 2
+    if n:
+        b.fork(g.choice(np.flatnonzero(add > 0), n), empty_ones[:n])
+    b.grow(np.where(b.plain.length > 0, g.integers(0, 58, sequences), 0))
+    b.trim(np.where(g.random(sequences) < 0.5, 0, b.plain.length))
+    b.compact()
+    b.grow(np.where(b.plain.length == 0, np.minimum(g.integers(0, 200, sequences), 16 * width - 40), 3))
+    b.trim(np.zeros(sequences))
+    b.compact()
+
+
 def test_what_the_arrays_hold_is_checked():
     """Bad lengths, pages, counts and sequences: nothing is touched but the status."""
     def fresh():
