@@ -139,6 +139,23 @@ __device__ __forceinline__ void tm_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// 16 columns from each of two addresses, under way together: v[0 .. 15], v[16 .. 31]. (The first load's registers are not
+// the second's address.)
+__device__ __forceinline__ void tm_ld16_two(uint32_t a, uint32_t b, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=&r"(r[0]), "=&r"(r[1]), "=&r"(r[2]), "=&r"(r[3]), "=&r"(r[4]), "=&r"(r[5]), "=&r"(r[6]), "=&r"(r[7]), "=&r"(r[8]), "=&r"(r[9]),
+        "=&r"(r[10]), "=&r"(r[11]), "=&r"(r[12]), "=&r"(r[13]), "=&r"(r[14]), "=&r"(r[15]), "=&r"(r[16]), "=&r"(r[17]), "=&r"(r[18]),
+        "=&r"(r[19]), "=&r"(r[20]), "=&r"(r[21]), "=&r"(r[22]), "=&r"(r[23]), "=&r"(r[24]), "=&r"(r[25]), "=&r"(r[26]), "=&r"(r[27]),
+        "=&r"(r[28]), "=&r"(r[29]), "=&r"(r[30]), "=&r"(r[31])
+      : "r"(a), "r"(b)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ uint32_t ld_shared_u32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -334,32 +351,33 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   if (warp < kWidenWarps && !failed) {
     const int quarter = warp & 3, part = warp >> 2;
     const uint32_t lanes = (uint32_t)quarter << 21;
-    for (int f = 0; f < here; ++f) {
-      for (int c = part * 16; c < n; c += 16 * kGroups) {
-        float v[16] = {};
-        for (int s = f; s < plan.streams && s / ft < b1 - b0; s += ft) {       // its streams that had any products
-          float x[16];
-          tm_ld16(tmem + lanes + s * n + c, x);
+    const int turns = b1 - b0;                        // stream s had products if there are more than s / ft
+    auto put = [&](int f, int c, const float* v) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] += x[k];
+      for (int x = 0; x < 16; ++x) sums[(c + x) * wide + f * 128 + quarter * 32 + lane] = v[x];
+    };
+    for (int c = part * 16; c < n; c += 16 * kGroups) {
+      float v[32], x[32];
+      if (ft == 1) {                                  // two streams' sums of the piece at a time
+        tm_ld16_two(tmem + lanes + c, tmem + lanes + n + c, v);
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] += turns > 1 ? v[16 + k] : 0.f;
+        if (plan.streams > 2 && turns > 2) {
+          tm_ld16_two(tmem + lanes + 2 * n + c, tmem + lanes + 3 * n + c, x);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) v[k] += turns > 3 ? x[k] + x[16 + k] : x[k];
         }
-        if (S > 1) {
+        put(0, c, v);
+      } else {                                        // two pieces'
+        for (int f = 0; f < here; f += 2) {
+          tm_ld16_two(tmem + lanes + f * n + c, tmem + lanes + (f + 1) * n + c, v);
+          if (plan.streams > ft && turns > 1) {
+            tm_ld16_two(tmem + lanes + (f + ft) * n + c, tmem + lanes + (f + ft + 1) * n + c, x);
 #pragma unroll
-          for (int x = 0; x < 16; ++x) sums[(c + x) * wide + f * 128 + quarter * 32 + lane] = v[x];
-        } else if (w.gated) {
-          // lanes 0 .. 15 have the gates, the others up of the same features: of two rows, each half takes one
-          const int feature = (piece0 + f) * 64 + quarter * 16 + (lane & 15), odd = lane >> 4;
-#pragma unroll
-          for (int x = 0; x < 16; x += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, odd ? v[x] : v[x + 1], 16);
-            float y = silu(odd ? other : v[x]) * (odd ? v[x + 1] : other);
-            if (feature < w.outs && c + x + odd < rows_here) finish<T>(p, row0 + c + x + odd, feature, 1, &y);
+            for (int k = 0; k < 32; ++k) v[k] += x[k];
           }
-        } else {
-          const int feature = (piece0 + f) * 128 + quarter * 32 + lane;
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            if (feature < w.outs && c + x < rows_here) finish<T>(p, row0 + c + x, feature, 1, v + x);
+          put(f, c, v);
+          if (f + 1 < here) put(f + 1, c, v + 16);
         }
       }
     }
@@ -368,38 +386,46 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   if (S > 1) {
     __syncwarp();
     cluster_sync_all();
-    // each of the cluster's blocks takes every S-th row, four features a thread, and adds up in the blocks' order; all
-    // loads from other blocks' memory are under way before the first is waited for
-    const int fours = (w.gated ? here * 64 : here * 128) / 4, items = (rows_here - rank + S - 1) / S * fours;
-    if (!failed)
-      for (int i = threadIdx.x; i < items; i += kThreads) {
-        const int r = rank + i / fours * S, f = i % fours * 4;
-        const int at = w.gated ? (f >> 4) * 32 + (f & 15) : f;
-        const uint32_t mine = saddr(sums + r * wide + at);
-        float4 v[kMostCluster], u[kMostCluster];
-#pragma unroll
-        for (int k = 0; k < kMostCluster; ++k)
-          if (k < S) {
-            v[k] = ld_cluster_v4(mapa(mine, k));
-            if (w.gated) u[k] = ld_cluster_v4(mapa(mine, k) + 64);
-          }
-        float y[4] = {}, up[4] = {};
-#pragma unroll
-        for (int k = 0; k < kMostCluster; ++k)
-          if (k < S) {
-            y[0] += v[k].x; y[1] += v[k].y; y[2] += v[k].z; y[3] += v[k].w;
-            if (w.gated) up[0] += u[k].x, up[1] += u[k].y, up[2] += u[k].z, up[3] += u[k].w;
-          }
-        if (w.gated)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) y[k] = silu(y[k]) * up[k];
-        const int feature = piece0 * (w.gated ? 64 : 128) + f;
-        if (feature < w.outs) finish<T>(p, row0 + r, feature, min(4, w.outs - feature), y);
-      }
-    __syncwarp();
-    cluster_sync_all();
   } else {
     __syncthreads();
+  }
+  // each of the cluster's blocks takes every S-th row, four features a thread, and adds up in the blocks' order; all loads
+  // from other blocks' memory are under way before the first is waited for. (Straight out of tensor memory, an element a
+  // thread at a time, results took 5 us of 320 rows, 2048 to 2 x 6144, this way XX.)
+  const int lg = 31 - __clz(plan.ft) + (w.gated ? 4 : 5), items = (rows_here - rank + S - 1) / S << lg;
+  if (!failed)
+    for (int i = threadIdx.x; i < items; i += kThreads) {
+      const int r = rank + (i >> lg) * S, f = (i & ((1 << lg) - 1)) * 4;
+      const int feature = piece0 * (w.gated ? 64 : 128) + f;
+      if (feature >= w.outs) continue;                                         // a last group of fewer pieces, too
+      const float* own = sums + r * wide + (w.gated ? (f >> 4) * 32 + (f & 15) : f);
+      float4 v[kMostCluster], u[kMostCluster];
+      if (S == 1) {
+        v[0] = *reinterpret_cast<const float4*>(own);
+        if (w.gated) u[0] = *reinterpret_cast<const float4*>(own + kTileRows);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k)
+          if (k < S) {
+            v[k] = ld_cluster_v4(mapa(saddr(own), k));
+            if (w.gated) u[k] = ld_cluster_v4(mapa(saddr(own + kTileRows), k));
+          }
+      }
+      float y[4] = {}, up[4] = {};
+#pragma unroll
+      for (int k = 0; k < kMostCluster; ++k)
+        if (k < S) {
+          y[0] += v[k].x; y[1] += v[k].y; y[2] += v[k].z; y[3] += v[k].w;
+          if (w.gated) up[0] += u[k].x, up[1] += u[k].y, up[2] += u[k].z, up[3] += u[k].w;
+        }
+      if (w.gated)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = silu(y[k]) * up[k];
+      finish<T>(p, row0 + r, feature, min(4, w.outs - feature), y);
+    }
+  if (S > 1) {
+    __syncwarp();
+    cluster_sync_all();
   }
   if (warp == kMmaWarp) {
     tm_fence_after();
