@@ -238,14 +238,16 @@ constexpr int64_t kSomeBytes = 8 << 20;
 // Up to 8 rows: as many warps a block as leaves one round of blocks, for the more of them the sooner a block ends; where
 // there are many rounds, more of the weights a block, so that x is read less often. Measured, us (16 warps and 1 tile; 16
 // and 2; 8, 2 and two records at a time; 8 and 4): 1 row, 2048 to 4096 2.4, 3.1, 3.6, 3.8; 4 rows, 6144 to 2048 4.5, 6.0,
-// 5.7, 8.1; 8 rows, 8192 to 8192 15.5, 10.3, 14.4, 21.9; 5 rows, 2048 to 2 x 6144 gated -, 5.1, 4.4, 7; 1 row, 8192 to
-// 28672 34.1, 26.6, 26.2, 24.3; 3 rows, 2048 to 50001 21.2, 16.4, 15.2, 13.8.
+// 5.7, 8.1; 8 rows, 8192 to 8192 15.5, 10.3, 14.4, 21.9; 5 rows, 2048 to 2 x 6144 gated -, 5.1, 4.4, 7; 5 rows, 1024
+// to 12288 (a record for each of 8 warps) -, 4.0, 4.4, -; 3 rows, 4096 to 16384 -, 10.6, 12.8, 12.8, to 20480 -, 13.3, 13.7,
+// 13.1; 1 row, 8192 to 28672 34.1, 26.6, 26.2, 24.3; 3 rows, 2048 to 50001 21.2, 16.4, 15.2, 13.8.
 cudaError_t launch_few_rows(const ApplyParams& p, cudaStream_t s) {
   if (p.rows > kFewRows) return launch_few<2, 16, 2, 1>(p, s);
   const int pairs = p.w.tiles / 2;                   // blocks of two tiles; an SM holds 2 of 16 warps, 3 of 8
   if (pairs * 2 <= 304 && !p.w.gated) return launch_few<1, 16, 1, 1>(p, s);
   if (pairs <= 304) return launch_few<1, 16, 2, 1>(p, s);
-  if (pairs <= 456) return launch_few<1, 8, 2, 2>(p, s);
+  if (pairs <= 456 && p.w.per_piece > 8) return launch_few<1, 8, 2, 2>(p, s);
+  if (pairs <= 608) return launch_few<1, 16, 2, 1>(p, s);        // two rounds
   return launch_few<1, 8, 4, 1>(p, s);
 }
 

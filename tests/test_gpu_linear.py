@@ -76,6 +76,25 @@ def test_widths(k, group, rows):
     compare(rows, 80, k, group, True, False, False, torch.float32, seed=k)
 
 
+@pytest.mark.parametrize("n,k", [(2400, 384), (4870, 384), (9700, 640), (9800, 1000 - 40), (14500, 1152), (14500, 640), (14700, 640),
+                                 (19450, 384), (19500, 384), (30000, 256)])
+@pytest.mark.parametrize("group,zero,gated", [(128, False, False), (32, True, True), (64, True, False), (64, False, True)])
+def test_numbers_of_blocks(n, k, group, zero, gated):
+    """Few rows, over as many features as make each number of warps, tiles and records a block."""
+    k = k // group * group
+    compare(5, n, k, group, zero, gated, True, torch.bfloat16, seed=n)
+    compare(8, n, k, group, zero, gated, False, torch.float32, seed=n + 1)
+
+
+@pytest.mark.parametrize("rows,n,k", [(17, 20000, 256), (40, 33000, 128), (64, 66000, 128), (30, 130, 4096), (100, 12000, 256),
+                                      (190, 20000, 128), (192, 300, 2048), (350, 9000, 384), (64, 8200, 512), (200, 2049, 1024)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_plans(rows, n, k, gated):
+    """Many rows, over what makes one, two and four pieces a block, clusters of one to four, and each number of rows a block."""
+    compare(rows, n // 2 * 2, k, 128, False, gated, True, torch.bfloat16, seed=n)
+    compare(rows, n // 2 * 2, k, 32, True, gated, False, torch.float32, seed=n + 1)
+
+
 def test_larger_layers():
     compare(1, 4096, 2048, 128, False, False, False, torch.bfloat16)
     compare(64, 4098, 2048, 64, True, True, True, torch.bfloat16)
