@@ -19,11 +19,11 @@
 // warp's outstanding loads share few scoreboards, and waiting for the oldest
 // waits for the newest.)
 //
-// A call costs 4.7 us and 0.26 a record of a block (n of 64; a block with 64 of
-// them 24 us for 64 rows, 16384 to 8192, on 128 SMs: 2.9 TB/s of weights, 707
-// TFLOP/s). A record of 64 rows is 336 clocks of the tensor core, 375 of
-// issuing what widens it, and measured 490: both, and the hand-overs between
-// them, which take 380 even where nothing is widened.
+// A call costs 4.2 us (64 rows) to 7 (112 rows of 256 features a block) and
+// 0.225 a record of a block (64 of them, 64 rows, 16384 to 8192: 23.7 us on 128
+// SMs, 3.1 TB/s, 725 TFLOP/s). A record of 64 rows is 336 clocks of the tensor
+// core, 375 of issuing what widens it, and measured 430: both, and the hand-overs
+// between them, which take 380 even where nothing is widened.
 #include <cuda.h>
 
 #include "cp_cache_ptx.cuh"
@@ -439,9 +439,9 @@ int up_to(int a, int b) { return (a + b - 1) / b * b; }
 // How a call is cut up: what costs least by a model of the measured times, in microseconds. A round of blocks takes
 // kRoundUs to start and end; a record's products 8 times (12 + n / 2) clocks on the tensor core, and no less than what
 // widening and the hand-overs take; joining moves a block's sums through distributed shared memory at 12 bytes a clock.
-// Clusters leave SMs over. (64 rows, 16384 to 8192: one piece and two shares of the inputs a block 23.2 us, two pieces and
-// four shares 23.5, one piece and no shares 37.6, and four 30.5; 320 rows, 2048 to 2 x 6144: three chunks of 112 rows and two
-// pieces a block 16.9, one piece 21.6, two chunks of 160 rows 24.4, five of 64 27.3.)
+// Clusters leave SMs over. (64 rows, 16384 to 8192: one piece and two shares of the inputs a block 22.7 us, two pieces and
+// four shares 22.9, one piece and no shares 36.5, and four 29.7; 320 rows, 2048 to 2 x 6144: three chunks of 112 rows and two
+// pieces a block 15.0, one piece 19.8, two chunks of 160 rows 21.7, five of 64 25.3.)
 constexpr double kRoundUs = 5, kRecordUs = 0.256, kClocksUs = 1900;
 int blocks_at_once(int cluster) { return cluster == 1 ? 152 : cluster == 2 ? 148 : 144; }
 
