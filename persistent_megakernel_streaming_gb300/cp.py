@@ -674,15 +674,18 @@ class Linear:
     def apply(self, x, out, add=None, stream=None):
         """x bf16 [rows][width] into out [rows][features, or half of them if gated], bf16 or fp32; ``add`` of out's type is
         added before the result is rounded."""
-        index, shape, out_dtype = self.device_index, x.shape, out.dtype
-        rows = shape[0]
-        if x.dtype not in self.x_dtypes or shape != (rows, self.width) or x.get_device() != index:
+        index, rows, out_dtype = self.device_index, x.shape[0], out.dtype
+        shape = (rows, self.width)
+        if x.dtype not in self.x_dtypes or x.shape != shape or x.get_device() != index:
             raise ValueError(f"x: bf16 [rows][{self.width}] on the weights' device")
         kind = self.dtypes.get(out_dtype)
         if kind is None or out.get_device() != index:
             raise ValueError("out: bf16 or fp32 on the weights' device")
+        x_row = 0 if x.is_contiguous() else self._row(x, "x", shape)
         shape = (rows, self.outs)
-        a = LinearArgs(x.data_ptr(), self._row(x, "x", x.shape), rows, kind, out.data_ptr(), self._row(out, "out", shape))
+        if out.shape != shape:
+            raise ValueError(f"out: {list(shape)}; got {list(out.shape)}")
+        a = LinearArgs(x.data_ptr(), x_row, rows, kind, out.data_ptr(), 0 if out.is_contiguous() else self._row(out, "out", shape))
         if add is not None:
             if add.dtype is not out_dtype or add.get_device() != index:
                 raise ValueError("add: of out's type and device")
