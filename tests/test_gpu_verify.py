@@ -150,6 +150,32 @@ def test_the_same_draw_wherever_it_is_computed():
     assert refused.any() and not refused.all()
 
 
+@pytest.mark.parametrize("sequences", [3, 152, 153, 310])
+@pytest.mark.parametrize("vocab", [517, 4095, 4096, 4097])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_small_vocabularies_of_few_and_many_sequences(sequences, vocab, dtype):
+    """On both sides of where the rows' sums are made elsewhere, and of where blocks are smaller; rows that start anywhere."""
+    g = np.random.default_rng(sequences + vocab)
+    drafted = [int(x) for x in g.integers(0, 5, sequences)]
+    b = make(drafted, vocab, dtype, seed=vocab, sharp=2.0)
+    b["temperature"] = torch.from_numpy(np.where(g.random(sequences) < 0.2, 0.0, g.uniform(0.3, 1.4, sequences)).astype(np.float32))
+
+    def odd(t):
+        t = t.cuda()
+        w = torch.full((t.shape[0], t.shape[1] + 5), 9e3, dtype=t.dtype, device="cuda")
+        w[:, 3:-2] = t
+        return w[:, 3:-2]
+
+    usual = run(b)
+    check(b, usual)
+    # where a row starts within 16 bytes decides which logits a thread sums, and a sum of other fp32 partial sums is another
+    # rounding of the same number: 4097 logits, 0.0952981561 for 0.0952981487, one step of 2^-27
+    check(b, run(b, move=odd))
+    few = dict(b, start=b["start"][: 3], temperature=b["temperature"][: 2], u_token=b["u_token"][: 2])
+    for got, want in zip(run(few)[:2], usual):
+        np.testing.assert_array_equal(got, want[:2])                        # however many sequences there are
+
+
 def test_a_draft_equal_to_the_target_is_always_taken():
     for vocab in (50, 3001, 20000):
         b = make([6] * 20, vocab, seed=10)
