@@ -30,7 +30,7 @@ struct Piece {
   int arg, pad;
 };
 
-constexpr int kStatThreads = 256, kPer = 32;
+constexpr int kStatThreads = 128, kPer = 32;
 constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block takes; the last up to 16 bytes a thread more
 // Three blocks an SM: the draw waits (for loads, barriers, other blocks) more than it computes. With 512 threads a block and
 // two an SM 48 sequences over 131075 took 51 us behind the sums, with these 40. Reading small rows itself, it takes 512
@@ -158,11 +158,12 @@ struct Loads {
   }
 };
 
-// Bound by HBM (6.1 TB/s). A thread holds its 32 logits, so that their maximum comes first and nothing is rescaled; an exponential
-// is one multiplication, one fused one, and ex2. Where NaN or infinities spoil that, the piece is done again with
-// clamped logits.
+// Bound by HBM. A thread holds its 32 logits, so that their maximum comes first and nothing is rescaled; an exponential
+// is one multiplication, one fused one, and ex2. Where NaN or infinities spoil that, the piece is done again with clamped
+// logits. Eight blocks of 128 threads an SM: us a call of 48 sequences of 7 over 131075 92.5, four of 256 94.5, two of 512
+// 96.0; three of 256, where no register spills, 103; half as many logits a thread 98.9.
 template <class T>
-__global__ void __launch_bounds__(kStatThreads, 4) stats_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kStatThreads, 8) stats_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ int own;
   __shared__ Piece warps[kStatThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -94,7 +94,7 @@ def test_mixed_temperatures_and_many_sequences():
     assert accepted.max() >= 4 and (accepted == 0).any()
 
 
-@pytest.mark.parametrize("vocab", [8185, 8187, 8189, 9212, 9213, 9214, 9216, 9217, 10232, 10233, 10234, 10240, 10241, 16381, 17405, 17406])
+@pytest.mark.parametrize("vocab", [4601, 4605, 4606, 5113, 5114, 8185, 8187, 8189, 8701, 8702, 8704, 9212, 9213, 9214, 9216, 9217, 10232, 10233, 10234, 10240, 10241, 16381, 17405, 17406])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_rows_that_end_about_where_a_piece_does(vocab, dtype):
     check(make([3, 0, 2], vocab, dtype, seed=vocab))

@@ -117,7 +117,7 @@ def test_a_small_vocabulary_needs_no_workspace(L):
     assert L.cp_verify_check(C.byref(of(cp.VerifyArgs, VERIFY, dict(vocab=2048))), C.byref(need)) == OK and need.value == 0
 
 
-@pytest.mark.parametrize("vocab", [4097, 8184, 8185, 8186, 8187, 8188, 8189, 8190, 16380, 16381, 32000, 1 << 24])
+@pytest.mark.parametrize("vocab", [4097, 4603, 4604, 4605, 4606, 5113, 5114, 8184, 8185, 8186, 8187, 8188, 8189, 8190, 16380, 16381, 32000, 1 << 24])
 def test_the_workspace_is_the_same_for_both_types(L, vocab):
     a = of(cp.VerifyArgs, VERIFY, dict(vocab=vocab))
     sizes = []
