@@ -39,7 +39,7 @@ constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block
 constexpr int kTokenThreads = 256, kWideThreads = 512;
 constexpr int kWideMost = 152;
 constexpr int kRowsKept = 32;                    // rows of a sequence whose pieces are joined once
-constexpr int kMostCluster = 16;
+constexpr int kMostCluster = 16, kMostSums = kMostCluster * kTokenThreads / 32;
 // Vocabularies up to which the second launch reads the rows itself, us with one launch and with two: 1 sequence of 4 drafted
 // tokens over 2048 9.2 and 10.4, over 4096 9.9 and 10.4, over 8192 13.9 and 11.4; 64 of 3 over 4096 10.5 and 14.4, over 8192
 // 14.7 and 18.5; 1000 of 3 over 4096 43 and 60.
@@ -304,20 +304,18 @@ struct TokenShared {
   int first;                            // the first refused row, or the last
   Piece rows[2][kRowsKept];             // the target's and the draft's rows
   int draft[kRowsKept];
-  fixed part[2][WARPS];           // each warp's sums
-  Piece pair[WARPS / 2];          // what one warp of a pair found out about the draft
-  fixed z[2][kMostCluster];             // each block's sums of exponentials
-  fixed w[2][kMostCluster];             // each block's sum of weights, by turn
-  float rz[2];                          // 1 over all of them
+  Piece pair[WARPS / 2];                // what one warp of a pair found out about the draft
+  fixed z[2][kMostSums];                // each of the cluster's warps' sums of exponentials
+  fixed w[2][kMostSums];                // and of weights, by turn
 };
 
-// One value to the same place of all of the cluster's blocks.
+// One value of a warp to the same place of all of the cluster's blocks.
 __device__ __forceinline__ void tell(fixed* slot, int cluster, fixed x) {
-  if (threadIdx.x < (unsigned)cluster) {
-    const uint32_t at = ptx::mapa(ptx::saddr(slot), threadIdx.x);
+  const int lane = threadIdx.x & 31;
+  if (lane < cluster) {
+    const uint32_t at = ptx::mapa(ptx::saddr(slot), lane);
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
   }
-  __syncwarp();
 }
 
 // A row's share of a block: its logits from `src` on, `skew` elements past a 16-byte boundary.
@@ -523,6 +521,25 @@ __global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWi
   float* const put_q = kept + kept_floats(p.chunk);
   const float* kept_p = kept + of_p.skew;
   const float* kept_q = with_q ? put_q + of_q.skew : kept_p;
+  // each warp's sums go to all blocks, and each warp adds them all up for itself: one barrier a sum
+  const int sums = cluster * kWarps, own = rank * kWarps + warp;
+  auto to_all = [&](fixed* slots, fixed x) {
+    if (!DIRECT) tell(slots + own, cluster, x);
+    else if (lane == 0) slots[own] = x;
+  };
+  auto meet = [] {
+    __syncwarp();
+    if (DIRECT) __syncthreads();
+    else ptx::cluster_sync_all();
+  };
+  auto sum_below = [&](const fixed* slots, int n) {
+    fixed x = 0;
+    for (int k = lane; k < n; k += 32) x += slots[k];
+    return warp_total(x);
+  };
+  // the token that a certain draft proposed weighs nothing where it was refused; its exponential is kept aside
+  const int out = refused && !drafts && (uint32_t)(d - begin) < (uint32_t)size ? d - begin : -1;
+  float aside = -1.f;
   // sums of both rows' exponentials; two of each, whose steps do not wait for one another
   Sum sum_p[2], sum_q[2];
   constexpr int U = sizeof(T) == 4 ? 4 : 2;
@@ -534,50 +551,22 @@ __global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWi
 #pragma unroll
       for (int u = 0; u < U; ++u) y[u] = of_q.load(v0 + u * kThreads);
 #pragma unroll
-    for (int u = 0; u < U; ++u) of_p.template take<KEEP>(v0 + u * kThreads, x[u], by, sum_p, kept);
+    for (int u = 0; u < U; ++u) {
+      of_p.template take<KEEP>(v0 + u * kThreads, x[u], by, sum_p, kept);
+      if (KEEP && out >= 0 && (out + of_p.skew) / Part<T>::K == v0 + u * kThreads) {
+        aside = kept[out + of_p.skew];
+        kept[out + of_p.skew] = 0.f;
+      }
+    }
     if (with_q)
 #pragma unroll
       for (int u = 0; u < U; ++u) of_q.template take<KEEP>(v0 + u * kThreads, y[u], by, sum_q, put_q);
   }
-  fixed zp = sum_p[0].value(p.z_bits) + sum_p[1].value(p.z_bits), zq = 0;
-  if (with_q) zq = warp_total(sum_q[0].value(p.z_bits) + sum_q[1].value(p.z_bits));
-  zp = warp_total(zp);
-  if (lane == 0) {
-    sh.part[0][warp] = zp;
-    sh.part[1][warp] = zq;
-  }
-  __syncthreads();
-  // over the block, and over the cluster: one warp's work
-  auto of_block = [&](const fixed* parts) { return warp_total(lane < kWarps ? parts[lane] : 0); };
-  auto of_cluster = [&](const fixed* slots) { return DIRECT ? slots[0] : warp_total(lane < cluster ? slots[lane] : 0); };
-  auto to_all = [&](fixed* slots, fixed x) {
-    if (!DIRECT) tell(slots + rank, cluster, x);
-    else if (lane == 0) slots[0] = x;
-  };
-  auto meet = [] {
-    __syncwarp();
-    if (DIRECT) __syncthreads();
-    else ptx::cluster_sync_all();
-  };
-  if (warp == 0) {
-    to_all(sh.z[0], of_block(sh.part[0]));
-    if (with_q) to_all(sh.z[1], of_block(sh.part[1]));
-  }
-  // the token that a certain draft proposed weighs nothing where it was refused; its exponential is kept aside
-  const int out = refused && !drafts && (uint32_t)(d - begin) < (uint32_t)size ? d - begin : -1;
-  float aside = 0.f;
-  if (KEEP && out >= 0 && threadIdx.x == 0) {
-    aside = kept_p[out];
-    kept[of_p.skew + out] = 0.f;
-  }
+  to_all(sh.z[0], warp_total(sum_p[0].value(p.z_bits) + sum_p[1].value(p.z_bits)));
+  if (with_q) to_all(sh.z[1], warp_total(sum_q[0].value(p.z_bits) + sum_q[1].value(p.z_bits)));
   meet();
-  if (warp < 2) {
-    const fixed z = of_cluster(sh.z[warp]);
-    if (lane == 0) sh.rz[warp] = warp == 0 || with_q ? inverse(z, p.z_bits) : 0.f;
-  }
-  __syncthreads();
-  const float rp = sh.rz[0];
-  float rq = sh.rz[1];                                               // 0 without a draft's logits: p - 0 p is p
+  const float rp = inverse(sum_below(sh.z[0], sums), p.z_bits);
+  float rq = with_q ? inverse(sum_below(sh.z[1], sums), p.z_bits) : 0.f;      // 0 without a draft's logits: p - 0 p is p
   bool residual = true;
   auto weight = [&](int i) {
     float x, y;
@@ -590,70 +579,53 @@ __global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWi
     }
     return fmaxf(__fsub_rn(__fmul_rn(x, rp), __fmul_rn(y, rq)), 0.f);
   };
-  // each warp a stretch of the block's logits, of whole 32s
-  const int each = ((size + kWarps - 1) / kWarps + 31) & ~31, w0 = min(warp * each, size), w1 = min(w0 + each, size);
-  fixed total = 0;
+  // each thread a run of the block's logits, an odd number, so that a warp's lanes read from different banks
+  const int run = (size + kThreads - 1) / kThreads | 1, begin_run = min((int)threadIdx.x * run, size), end_run = min(begin_run + run, size);
+  fixed x, total;
   int turn = 0;
   for (;; ++turn) {
     Sum sum;
 #pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) sum.add(weight(i));
-    const fixed w = warp_total(sum.value(kWeightBits));
-    if (lane == 0) sh.part[turn][warp] = w;
-    __syncthreads();
-    if (warp == 0) to_all(sh.w[turn], of_block(sh.part[turn]));
+    for (int i = begin_run; i < end_run; ++i) sum.add(weight(i));
+    x = sum.value(kWeightBits);
+    to_all(sh.w[turn], warp_total(x));
     meet();
-    total = 0;
-    for (int k = 0; k < cluster; ++k) total |= sh.w[turn][k];      // whether there is any
+    total = sum_below(sh.w[turn], sums);
     if (total || turn) break;                                        // the same in every block
     // roundings left nothing: from p itself
     residual = false;
     rq = 0.f;
-    if (KEEP && out >= 0 && threadIdx.x == 0) kept[of_p.skew + out] = aside;
+    if (KEEP && aside >= 0.f) kept[out + of_p.skew] = aside;
     __syncthreads();
   }
-  if (warp) return;                                                  // nobody reads another block's memory from here on
-  const fixed want = times(fminf(fmaxf(u_token, 0.f), 0x1.fffffep-1f), of_cluster(sh.w[turn]));
-  // the block, the warp's stretch, 32 logits of it, the logit: each time the first whose end passes that. A stretch's
-  // sum and its parts' may differ in the last bits that threads kept: should none of them pass, the last that weighs
-  // anything is it
-  auto first_above = [&](fixed x, fixed* before) {
-    const fixed end = *before + warp_prefix(x);
-    const uint32_t some = __ballot_sync(0xffffffffu, x != 0), hit = __ballot_sync(0xffffffffu, end > want) & some;
-    const int at = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : 0;
-    *before = __shfl_sync(0xffffffffu, end - x, at);
+  // nobody reads another block's memory from here on. The warp, its thread, the thread's logit: each time the first whose
+  // end passes `want`. A thread's sum and its logits' may differ in the last bits that it kept: should none of them pass,
+  // the last that weighs anything is it
+  const fixed want = times(fminf(fmaxf(u_token, 0.f), 0x1.fffffep-1f), total);
+  fixed before = sum_below(sh.w[turn], own);
+  if (want < before || want - before >= sh.w[turn][own]) return;
+  auto first_above = [&](fixed y, bool* passed) {
+    const fixed end = before + warp_prefix(y);
+    const uint32_t some = __ballot_sync(0xffffffffu, y != 0), hit = __ballot_sync(0xffffffffu, end > want) & some;
+    const int at = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
+    *passed = hit != 0;
+    before = __shfl_sync(0xffffffffu, hit ? end - y : end, hit ? at : 31);
     return at;
   };
-  fixed before = 0;
-  if (!DIRECT && first_above(lane < cluster ? sh.w[turn][lane] : 0, &before) != rank) return;
-  const int stretch = first_above(lane < kWarps ? sh.part[turn][lane] : 0, &before);
-  const int s0 = min(stretch * each, size), s1 = min(s0 + each, size);
-  int at = s0;
-  int run = 1;                                                       // a power of two
-  while (run < 32 && run * 32 < s1 - s0) run *= 2;
-  for (int t0 = s0; t0 < s1; t0 += 32 * run) {
-    // lane l: the sum of the l-th run, read so that the lanes' banks differ
-    Sum sum;
-#pragma unroll 4
-    for (int k = 0; k < run; ++k) {
-      const int i = t0 + lane * run + ((k + lane) & (run - 1));
-      if (i < s1) sum.add(weight(i));
-    }
-    const fixed x = sum.value(kWeightBits), all = warp_total(x);
-    if (all) {
-      fixed base = before;
-      const int i0 = t0 + first_above(x, &base) * run, i = i0 + lane;
-      at = i0 + first_above(lane < run && i < s1 ? to_fixed(weight(i), kWeightBits) : 0, &base);
-    }
-    before += all;
-    if (before > want) break;
+  bool passed;
+  const int from = max(first_above(x, &passed), 0), i0 = (warp * 32 + from) * run, i1 = min(i0 + run, size);
+  int token = i0;
+  for (int t = i0; t < i1; t += 32) {
+    const int at = first_above(t + lane < i1 ? to_fixed(weight(t + lane), kWeightBits) : 0, &passed);
+    if (at >= 0) token = t + at;
+    if (passed) break;
   }
-  if (lane == 0) p.token[seq] = begin + at;
+  if (lane == 0) p.token[seq] = begin + token;
 }
 
 // ------------------------------------------------------------------ checks
 constexpr int kResident = 3 * 152;
-constexpr size_t kMostKept = 72 * 1024;        // bytes of exponentials in a block's shared memory: three blocks an SM
+constexpr size_t kMostKept = 69 * 1024;        // bytes of exponentials in a block's shared memory: three blocks an SM
 size_t kept_bytes(const VerifyParams& p) { return (size_t)kept_floats(p.chunk) * (p.draft_logits ? 8 : 4); }
 
 int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
