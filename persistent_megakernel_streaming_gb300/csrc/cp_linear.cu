@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(WARPS * 32, kBlocksAnSm<NT, WARPS, TILES, GROU
         word[u][t][1] = *reinterpret_cast<const uint4*>(words + at + t * 512 + 4096);
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
-          scale[u][t][i] = u > 0 && first + u * WARPS >= w.per_piece ? 0 : *reinterpret_cast<const uint32_t*>(scales + at + t * 32 + i * kRecordScales);
+          const bool past = u > 0 && first + u * WARPS >= w.per_piece;
+          scale[u][t][i] = past ? 0 : *reinterpret_cast<const uint32_t*>(scales + at + t * 32 + i * kRecordScales);
           zero[u][t][i] = ZERO ? *reinterpret_cast<const uint16_t*>(zeros + at + t * 16 + i * kRecordZeros) : 0;
         }
       }

@@ -69,8 +69,8 @@ __device__ __forceinline__ int pages_for(const PagesView& v, int64_t length) {
 __device__ __forceinline__ bool in_pool(const PagesView& v, int page) { return (uint32_t)page < (uint32_t)v.pages; }
 
 // ------------------------------------------------------------------ fork
-// A block a pair; some 3 us whatever it copies: a launch and three loads that wait for one another. Whether pairs get in each other's way is looked up among all of them by every block: no order
-// between blocks is needed then.
+// A block a pair; some 3 us whatever it copies: a launch and three loads that wait for one another. Whether pairs get in
+// each other's way is looked up among all of them by every block: no order between blocks is needed then.
 __global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int32_t* src, const int32_t* dst, int n) {
   ptx::pdl_trigger();
   ptx::pdl_wait();

@@ -8,7 +8,8 @@
 // vocabulary the second reads the rows itself, and is the only one.
 //
 // Of 48 sequences of 7 drafted tokens over 131075 fp32 logits (378 MB) the
-// first takes 62 us (6.1 TB/s), the second 39 behind it.
+// first takes 59 us (6.4 TB/s), the second 34 to 38 behind it: 8 to settle what
+// is taken, 12 for the exponentials, 4 to add them up, 6 for the weights.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,15 +35,16 @@ constexpr int kStatThreads = 128, kPer = 32;
 constexpr int kPiece = kStatThreads * kPer;      // logits of a row that a block takes; the last up to 16 bytes a thread more
 // Three blocks an SM: the draw waits (for loads, barriers, other blocks) more than it computes. With 512 threads a block and
 // two an SM 48 sequences over 131075 took 51 us behind the sums, with these 40. Reading small rows itself, it takes 512
-// for up to as many sequences as SMs: us with 512 and 256 for 1 sequence of 4 drafted tokens over 4096 9.9 and 12.2, for
-// 152 of 5 over 2048 9.4 and 10.4, for 256 of 5 over 2048 18.9 and 15.7.
+// for up to as many sequences as SMs whose rows 256 would read in two turns (two warps a row): us with 512 and 256 for 1
+// sequence of 4 drafted tokens over 4096 9.0 and 10.7, for 152 of 5 over 2048 9.0 and 9.7, for 64 of 3 over 4096 9.9 and 9.3,
+// for 256 of 5 over 2048 18.9 and 15.7.
 constexpr int kTokenThreads = 256, kWideThreads = 512;
 constexpr int kWideMost = 152;
 constexpr int kRowsKept = 32;                    // rows of a sequence whose pieces are joined once
 constexpr int kMostCluster = 16, kMostSums = kMostCluster * kTokenThreads / 32;
 // Vocabularies up to which the second launch reads the rows itself, us with one launch and with two: 1 sequence of 4 drafted
-// tokens over 2048 9.2 and 10.4, over 4096 9.9 and 10.4, over 8192 13.9 and 11.4; 64 of 3 over 4096 10.5 and 14.4, over 8192
-// 14.7 and 18.5; 1000 of 3 over 4096 43 and 60.
+// tokens over 2048 8.3 and 10.2, over 4096 9.0 and 10.2, over 8192 12.5 and 10.2; 64 of 3 over 4096 9.9 and 14.3, over 8192
+// 13.9 and 14.4; 256 of 5 over 4096 20.0 and 19.9; 1000 of 3 over 4096 40 and 44.
 constexpr int kDirect = 4096;
 
 struct VerifyParams {
@@ -406,16 +408,18 @@ __device__ __forceinline__ Piece direct_stats(const T* row, int vocab, float by,
 __device__ __forceinline__ void pair_sync(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
 
 // What a sequence's blocks do. The first passes are short, so this is a chain of loads, sums over a warp, a block and a
-// cluster, and barriers: 6 to 10 us from launch to launch for a few sequences, whatever the vocabulary up to 4096, and 11 us a
-// round of blocks over large ones. KEEP: the exponentials of the block's logits stay in shared memory between the sum
-// of them and the weights (n = 64 over 32000: 18.6 us, without 37.9); DIRECT: as many threads, and the rows' sums are
-// made here.
+// cluster, and barriers: 6 to 10 us from launch to launch for a few sequences over up to 4096, some 2 us each for the
+// exponentials, their sum and the weights over 32000. KEEP: the exponentials of the block's logits stay in shared memory
+// between the sum of them and the weights (64 sequences over 32000: 18.6 us, without 37.9); DIRECT: as many threads, and
+// the rows' sums are made here.
 template <class T, bool KEEP, int DIRECT>
-__global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWideThreads ? 1 : 3) token_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWideThreads ? 1 : 3)
+    token_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ __align__(16) float kept[];       // exponentials of the block's chunk of the target's, and of the draft's
   constexpr int kThreads = DIRECT ? DIRECT : kTokenThreads, kWarps = kThreads / 32;
   __shared__ TokenShared<kWarps> sh;
-  const int cluster = DIRECT ? 1 : p.cluster, rank = DIRECT ? 0 : blockIdx.x % p.cluster, seq = DIRECT ? blockIdx.x : blockIdx.x / p.cluster;
+  const int cluster = DIRECT ? 1 : p.cluster, rank = DIRECT ? 0 : blockIdx.x % p.cluster;
+  const int seq = DIRECT ? blockIdx.x : blockIdx.x / p.cluster;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (!DIRECT) {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // its memory may be written
@@ -662,7 +666,7 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   if ((int64_t)p->rows * p->splits > 1 << 30) return CP_ERR_UNSUPPORTED;             // blocks
   p->direct = p->vocab <= kDirect;
   // blocks a sequence: more while there is work for them and room for all at once, or until a block's share can be kept
-  // (16 blocks and 8, us: 16 sequences over 131075 29 and 49, 1 14 and 27; room for twice as many: 64 over 32000 18.6 -> 22.6)
+  // (16 blocks and 8, us: 16 sequences over 131075 26 and 35, 1 12 and 21; room for twice as many: 64 over 32000 16.6 -> 21.8)
   auto cut = [&] { p->chunk = (p->vocab + p->cluster - 1) / p->cluster; };
   for (cut(); !p->direct && p->cluster < kMostCluster &&
               ((p->chunk > 2048 && (int64_t)p->n * p->cluster * 2 <= kResident) || kept_bytes(*p) > kMostKept);
@@ -681,7 +685,8 @@ cudaError_t launch_token(const VerifyParams& p, cudaStream_t s) {
 }
 template <class T>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
-  if (p.direct) return p.n <= kWideMost ? launch_token<T, true, kWideThreads>(p, s) : launch_token<T, true, kTokenThreads>(p, s);
+  const bool wide = p.n <= kWideMost && p.rows > 4 * p.n;
+  if (p.direct) return wide ? launch_token<T, true, kWideThreads>(p, s) : launch_token<T, true, kTokenThreads>(p, s);
   stats_kernel<T><<<dim3((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1), kStatThreads, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
