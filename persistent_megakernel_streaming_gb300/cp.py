@@ -766,26 +766,33 @@ def verify(logits, draft, start, u_accept, u_token, temperature, accepted, token
     if dtype is not f32 and dtype is not torch.bfloat16 or index < 0 or len(shape) != 2:
         raise ValueError("logits: bf16 or fp32 [rows][vocab] on a GPU")
     rows, vocab = shape
-    by_row, by_seq = (rows,), (accepted.numel(),)
-    strides = [0, 0]
-    for k, t in enumerate((logits, draft_logits)):
-        if t is not None:
-            if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
-                raise ValueError("draft_logits: of the logits' type, shape and device")
-            row, one = t.stride()
-            if vocab > 1 and one != 1 or rows > 1 and row <= 0:
-                raise ValueError("logits, draft_logits: the last axis contiguous, rows that share no memory")
-            strides[k] = row if rows > 1 else 0
-    n = by_seq[0]
+    n = accepted.numel()
+    by_row, by_seq = (rows,), (n,)
+    # one expression: a call for each array takes the host longer than a small batch takes the GPU
+    if not (start.dtype is i32 and draft.dtype is i32 and accepted.dtype is i32 and token.dtype is i32 and temperature.dtype is f32 and
+            u_accept.dtype is f32 and u_token.dtype is f32 and start.shape == (n + 1,) and draft.shape == by_row and
+            u_accept.shape == by_row and temperature.shape == by_seq and u_token.shape == by_seq and accepted.shape == by_seq and
+            token.shape == by_seq and start.get_device() == index and draft.get_device() == index and
+            u_accept.get_device() == index and temperature.get_device() == index and u_token.get_device() == index and
+            accepted.get_device() == index and token.get_device() == index and start.is_contiguous() and draft.is_contiguous() and
+            u_accept.is_contiguous() and temperature.is_contiguous() and u_token.is_contiguous() and accepted.is_contiguous() and
+            token.is_contiguous()):
+        for t, what, kind, each in ((start, "start", i32, (n + 1,)), (draft, "draft", i32, by_row), (u_accept, "u_accept", f32, by_row),
+                                    (temperature, "temperature", f32, by_seq), (u_token, "u_token", f32, by_seq),
+                                    (accepted, "accepted", i32, by_seq), (token, "token", i32, by_seq)):
+            _array(t, what, kind, each, index)                # which of them it is
+    row = 0 if logits.is_contiguous() else _logits_row(logits)
+    draft_at, draft_row = None, 0
+    if draft_logits is not None:
+        if draft_logits.dtype is not dtype or draft_logits.shape != shape or draft_logits.get_device() != index:
+            raise ValueError("draft_logits: of the logits' type, shape and device")
+        draft_at, draft_row = draft_logits.data_ptr(), 0 if draft_logits.is_contiguous() else _logits_row(draft_logits)
     need = _verify_needs.get((n, rows, vocab))
     if need is None:
         need = verify_workspace_bytes(n, rows, vocab)
-    a = VerifyArgs(n, rows, vocab, int(dtype is not f32), _array(start, "start", i32, (n + 1,), index), logits.data_ptr(), strides[0],
-                   None if draft_logits is None else draft_logits.data_ptr(), strides[1],
-                   _array(draft, "draft", i32, by_row, index), _array(temperature, "temperature", f32, by_seq, index),
-                   _array(u_accept, "u_accept", f32, by_row, index), _array(u_token, "u_token", f32, by_seq, index),
-                   _array(accepted, "accepted", i32, by_seq, index), _array(token, "token", i32, by_seq, index),
-                   None if prob is None else _array(prob, "prob", f32, by_row, index))
+    a = VerifyArgs(n, rows, vocab, 0 if dtype is f32 else 1, start.data_ptr(), logits.data_ptr(), row, draft_at, draft_row,
+                   draft.data_ptr(), temperature.data_ptr(), u_accept.data_ptr(), u_token.data_ptr(), accepted.data_ptr(),
+                   token.data_ptr(), None if prob is None else _array(prob, "prob", f32, by_row, index))
     at, size = 0, 0
     if workspace is not None:
         if workspace.get_device() != index or not workspace.is_contiguous():
@@ -797,6 +804,14 @@ def verify(logits, draft, start, u_accept, u_token, temperature, accepted, token
     code = lib().cp_verify(C.byref(a), index, at, size, _stream_on(index, stream))
     if code:
         raise CPError(code, "cp_verify")
+
+
+def _logits_row(t) -> int:
+    """Elements from row to row; 0 for a single one."""
+    row, one = t.stride()
+    if t.shape[1] > 1 and one != 1 or t.shape[0] > 1 and row <= 0:
+        raise ValueError("logits, draft_logits: the last axis contiguous, rows that share no memory")
+    return row if t.shape[0] > 1 else 0
 
 
 def test_philox(ctr, key, use_curand: bool, out, stream=None):
