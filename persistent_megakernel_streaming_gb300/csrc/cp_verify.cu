@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(kStatThreads, 8) stats_kernel(const __grid_con
   const int r = blockIdx.x / p.splits, part = blockIdx.x % p.splits, is_draft = blockIdx.y;
   const T* row = is_draft ? static_cast<const T*>(p.draft_logits) + r * p.draft_row : static_cast<const T*>(p.logits) + r * p.row;
   const int skew = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
+  // only then may the next launch start: it reads what lies in front of this one before it waits for this one
+  ptx::pdl_wait();
   ptx::pdl_trigger();
   Loads<T> x;
   if (!is_draft) x.load(row, p.vocab, part, p.splits, skew);                 // on their way while the row's sequence is looked up
@@ -690,8 +692,8 @@ template <class T>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
   const bool wide = p.n <= kWideMost && p.rows > 4 * p.n;
   if (p.direct) return wide ? launch_token<T, true, kWideThreads>(p, s) : launch_token<T, true, kTokenThreads>(p, s);
-  stats_kernel<T><<<dim3((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1), kStatThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const dim3 grid((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1);
+  const cudaError_t e = launch_as(stats_kernel<T>, grid, 1, 1, true, kStatThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   return kept_bytes(p) <= kMostKept ? launch_token<T, true, 0>(p, s) : launch_token<T, false, 0>(p, s);
 }
