@@ -166,7 +166,6 @@ struct Loads {
 // 96.0; three of 256, where no register spills, 103; half as many logits a thread 98.9.
 template <class T>
 __global__ void __launch_bounds__(kStatThreads, 8) stats_kernel(const __grid_constant__ VerifyParams p) {
-  __shared__ int own;
   __shared__ Piece warps[kStatThreads / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.x / p.splits, part = blockIdx.x % p.splits, is_draft = blockIdx.y;
@@ -177,12 +176,7 @@ __global__ void __launch_bounds__(kStatThreads, 8) stats_kernel(const __grid_con
   ptx::pdl_trigger();
   Loads<T> x;
   if (!is_draft) x.load(row, p.vocab, part, p.splits, skew);                 // on their way while the row's sequence is looked up
-  if (warp == 0) {
-    const int seq = sequence_of(p, r);
-    if (lane == 0) own = seq;
-  }
-  __syncthreads();
-  const int seq = own;
+  const int seq = sequence_of(p, r);                               // each warp for itself: no barrier
   if (seq >= p.n || p.start[seq] > r) return;                      // nobody's
   const float heat = p.temperature[seq];
   const bool greedy = !(heat > 0.f);
