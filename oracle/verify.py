@@ -71,3 +71,13 @@ def verify(start, logits, draft, u_accept, u_token, temperature, draft_logits=No
             one["token"] = int(np.flatnonzero(c > one["target"])[0]) if (c > one["target"]).any() else int(np.flatnonzero(w)[-1])
         out.append(one)
     return out, prob
+
+
+def probabilities(row, temperature):
+    """Probabilities in 64 bits of the fp32 products that the call defines, and those products; temperature > 0."""
+    with np.errstate(over="ignore"):
+        by = min(np.float32(1) / np.float32(temperature), np.float32(-LOWEST))
+        x = np.asarray(row, np.float32) * by
+    x = np.where(np.isnan(x), LOWEST, np.clip(x.astype(np.float64), LOWEST, -LOWEST))
+    e = np.exp(x - x.max())
+    return e / e.sum(), x
