@@ -725,9 +725,14 @@ typedef struct cp_verify_args {
  * 1), or from p of the last one: the least v whose cumulated weight passes
  * u_token times the sum. Greedy sequences take d if it is the target's
  * largest logit (the lowest index of equal ones), and then that token.
- * A logit is times the fp32 1 / temperature; probabilities are fp32 numbers
- * and each row's sums are kept in twice fp32's bits, so that the token drawn is
- * the one that 64-bit sums of the same numbers give. A NaN or -infinite logit has no
+ * A logit is times the fp32 1 / temperature, probabilities are fp32 numbers.
+ * What drafted tokens are taken by (p[d], q[d], prob) has sums in fp32: next to
+ * softmax of those products it is off by at most some 120 + 6 ln(vocab) of
+ * fp32's half steps, and one more for each unit of the product below the row's
+ * largest. A token that has all of the probability has 1, two that share it
+ * 1/2. The row that the token is drawn from is summed again in twice fp32's
+ * bits, so that the token is the one that 64-bit sums of the same weights give.
+ * A product that is NaN, -infinite or fp32's lowest number has no
  * probability, +infinite ones share it all. A drafted token outside the
  * vocabulary is not taken. A row without any probability (all its logits
  * masked) takes no token; if one is to be drawn there the token is -1. Should

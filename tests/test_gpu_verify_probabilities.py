@@ -150,3 +150,15 @@ def test_certain_and_tied_tokens(vocab, dtype):
             assert prob[[0, 1, 2]].tolist() == [1.0] * 3 and prob[[4, 6]].tolist() == [0.5] * 2
             assert accepted.tolist() == [3, 0, 1]
             assert token.tolist() == [7, vocab - 2, vocab - 2]   # the last: of the row behind, 0.6 of two halves
+
+
+@pytest.mark.parametrize("vocab", [64, 8192])
+def test_rows_of_the_lowest_number(vocab):
+    """fp32's lowest has no probability, whatever else there is; bf16's is a number like another."""
+    for dtype, temperature, weighs in ((torch.float32, 1.0, False), (torch.float32, 0.5, False), (torch.float32, 2.0, True),
+                                       (torch.bfloat16, 1.0, True), (torch.bfloat16, 0.5, False)):
+        x = torch.full((3, vocab), torch.finfo(dtype).min, dtype=dtype)
+        accepted, token, prob = run(x, [3, 0, 0], [0, 2, 3], [0.0, 0, 0], [0.5, 0.5], [temperature] * 2)
+        assert accepted.tolist() == [int(weighs), 0]
+        assert token.tolist() == ([vocab // 2] * 2 if weighs else [-1] * 2)
+        assert prob[0] == (1 / vocab if weighs else 0)
