@@ -555,7 +555,8 @@ typedef struct cp_pages cp_pages; /* opaque, owned by the library */
  * allocates and synchronises: not while a stream is being captured.
  * The calls check what the arrays hold without leaving their bounds: a
  * length below 0 or past the table (taken as 0), a sequence or page out of
- * range, and a count that does not cover its entries set the sticky
+ * range, and a count below the entries that a call finds to name its page (in
+ * cp_pages_grow: below the sequences that grow into it) set the sticky
  * CP_ERR_DEVICE_BOUNDS, and what is concerned is left out. */
 int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out);
 
@@ -575,8 +576,8 @@ int cp_pages_fork(cp_pages* p, const int32_t* src, const int32_t* dst, int n, cp
  * least `sequences`; the moves stand in the sequences' order and *count is
  * their number. If the pool has too few free pages nothing at all is changed,
  * and *count is minus the number that it lacks. A sequence that would grow
- * past its table, or by a negative number, is left out
- * (CP_ERR_DEVICE_BOUNDS). */
+ * past its table, or by a negative number, is left out, and so are all that
+ * grow into a page whose count is less than they are (CP_ERR_DEVICE_BOUNDS). */
 int cp_pages_grow(cp_pages* p, const int32_t* add, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream);
 
 /* Cut each sequence to at most keep[i] positions (device int32 [sequences];

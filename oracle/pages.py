@@ -71,14 +71,16 @@ class Pool:
                 if not self.ok(page) or self.refs[page] < 1:
                     self.bad = True
                     continue
-                if self.refs[page] > 1:
-                    last = int(page)
-                    sharers.setdefault(last, []).append(i)
+                last = int(page)
+                sharers.setdefault(last, []).append(i)
             grows.append((i, length, int(length + more), last))
+        short = {p for p, who in sharers.items() if len(who) > self.refs[p]}
+        self.bad |= len(short) > 0
+        grows = [g for g in grows if g[3] not in short]
         free = [p for p in range(len(self.refs)) if self.refs[p] == 0]
         plan, need = [], 0
         for i, length, to, last in grows:
-            stays = last >= 0 and len(sharers[last]) >= self.refs[last] and sharers[last][-1] == i
+            stays = last >= 0 and len(sharers[last]) == self.refs[last] and sharers[last][-1] == i
             copies = last >= 0 and not stays
             plan.append((i, length, to, last, copies))
             need += self.held(to) - self.held(length) + copies

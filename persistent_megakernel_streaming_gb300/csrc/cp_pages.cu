@@ -20,8 +20,8 @@ namespace {
 struct Plan {
   int len;           // new length, or -1: it stays as it is
   int had, want;     // pages
-  int last;          // a shared page that it grows into, or -1
-  int copies;        // whether it takes a page of its own for that
+  int last;          // the partly filled page that it grows into, or -1
+  int copies;        // whether it takes a page of its own for that: others hold it too
   int base, move;    // its first new page's place in the list, its place among the moves
 };
 
@@ -35,7 +35,7 @@ struct PagesView {
   // scratch
   int32_t* list;     // [pages] free pages in order
   int32_t* map;      // [pages] where a page moves, or -1 (from page *live on)
-  int32_t* tail;     // [pages] sequences that grow into a shared page; zeros between calls
+  int32_t* tail;     // [pages] sequences that grow into a partly filled page; zeros between calls
   int32_t* keeper;   // [pages] the last of them, plus one; zeros between calls
   Plan* plan;        // [sequences]
   int32_t* live;     // [1] pages that hold something
@@ -244,12 +244,11 @@ __device__ __forceinline__ Plan ask_of(const PagesView& v, const int32_t* add, i
       set_status(v);
       return a;
     }
-    const int refs = v.refs[page];
-    if (refs < 1) {
+    if (v.refs[page] < 1) {
       set_status(v);
       return a;
     }
-    if (refs > 1) a.last = page;
+    a.last = page;
   }
   a.len = (int)to;
   a.want = pages_for(v, to);
@@ -292,14 +291,24 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const
   wait_early();
   if (tid < 32) tell(free_told, free_here);
   meet();
-  // all that grow into a shared page take one of their own, but the last of them if nobody else holds it
+  // all that grow into a shared page take one of their own, but the last of them if nobody else holds it; none of them
+  // grows if the page's count is less than they are
   int64_t fresh_here = 0, moved_here = 0;
   for (int i0 = seqs.begin; i0 < seqs.end || ONE; i0 += kThreads) {
     const int i = i0 + tid;
     Plan a = own;
     if (!ONE && i < seqs.end) a = v.plan[i];
     if (i >= seqs.end) a = Plan{-1, 0, 0, -1, 0, 0, 0};
-    if (a.last >= 0) a.copies = !(__ldcg(v.tail + a.last) >= v.refs[a.last] && __ldcg(v.keeper + a.last) == i + 1);
+    if (a.last >= 0) {
+      const int sharers = __ldcg(v.tail + a.last), keeper = __ldcg(v.keeper + a.last), refs = v.refs[a.last];
+      if (sharers > refs) {
+        set_status(v);
+        a.len = -1;
+        a.want = a.had;
+      } else {
+        a.copies = !(sharers == refs && keeper == i + 1);
+      }
+    }
     int64_t sum;
     if (a.want - a.had > 2) many = 1;
     const int64_t fresh = a.want - a.had + a.copies;
