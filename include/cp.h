@@ -556,14 +556,15 @@ typedef struct cp_pages cp_pages; /* opaque, owned by the library */
  * The calls check what the arrays hold without leaving their bounds: a
  * length below 0 or past the table (taken as 0), a sequence or page out of
  * range, and a count below the entries that a call finds to name its page (in
- * cp_pages_grow: below the sequences that grow into it) set the sticky
+ * cp_pages_grow: below the sequences that grow into it; elsewhere: below 1) set the sticky
  * CP_ERR_DEVICE_BOUNDS, and what is concerned is left out. */
 int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out);
 
 /* For each of n pairs, sequence dst[i], which holds nothing, becomes a copy of
  * sequence src[i] that shares its pages (device int32 [n] each; several may
  * copy one sequence). A pair whose dst holds something, stands twice or is
- * itself copied from in this call is left out (CP_ERR_DEVICE_BOUNDS). */
+ * itself copied from in this call, or whose src names a page with a count
+ * below 1, is left out (CP_ERR_DEVICE_BOUNDS). */
 int cp_pages_fork(cp_pages* p, const int32_t* src, const int32_t* dst, int n, cp_stream_t stream);
 
 /* Make room for add[i] more positions (device int32 [sequences], 0 or more)

@@ -31,6 +31,9 @@ class Pool:
                 self.bad = True
                 continue
             length = self.len_of(s)
+            if any(self.ok(page) and self.refs[page] < 1 for page in self.table[s, : self.held(length)]):
+                self.bad = True
+                continue
             self.length[d] = length
             for k in range(self.held(length)):
                 page = self.table[s, k]

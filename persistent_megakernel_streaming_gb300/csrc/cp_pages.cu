@@ -82,14 +82,18 @@ __global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int3
     return;
   }
   const int len = length_of(v, s), held = pages_for(v, len);
-  if (v.length[d] != 0) {                // the same for all threads: nobody writes it before the barrier
+  const int32_t* from = v.table + (int64_t)s * v.stride;
+  int32_t* to = v.table + (int64_t)d * v.stride;
+  bool left_out = v.length[d] != 0;      // nobody writes it before the barrier
+  for (int i = threadIdx.x; i < held; i += 256) {
+    const int page = from[i];
+    left_out |= in_pool(v, page) && v.refs[page] < 1;    // nobody's: no call of this kernel makes it somebody's
+  }
+  if (__syncthreads_or(left_out)) {
     if (threadIdx.x == 0) set_status(v);
     return;
   }
-  __syncthreads();
   if (threadIdx.x == 0) v.length[d] = len;
-  const int32_t* from = v.table + (int64_t)s * v.stride;
-  int32_t* to = v.table + (int64_t)d * v.stride;
   for (int i = threadIdx.x; i < held; i += 256) {
     const int page = from[i];
     to[i] = page;

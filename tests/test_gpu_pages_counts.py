@@ -45,3 +45,17 @@ def test_a_short_count_in_a_full_pool():
     b = Both([2, 1], [[0, -1], [0, -1], [0, -1], [1, -1]], [3, 3, 3, 16], 16)
     b.grow([20, 20, 20, 0])
     assert b.plain.bad and int(b.count) == 0
+
+
+@pytest.mark.parametrize("count", [0, -1, -2 ** 31])
+@pytest.mark.parametrize("place", [0, 1, 299])
+def test_a_forked_page_that_nobody_holds(count, place):
+    """Those that copy its sequence are left out, however many; another pair of the call stands."""
+    refs, table = np.zeros(700, np.int64), np.full((8, 300), -1)
+    table[0], table[1], table[2, :2] = np.arange(300), np.arange(300, 600), [600, 601]
+    refs[:602] = 1
+    refs[table[0, place]] = count
+    b = Both(refs, table, [4800, 4799, 17, 0, 0, 0, 0, 0], 16)
+    b.fork([0, 1, 0, 2], [3, 5, 4, 7])
+    assert b.plain.bad and b.plain.length.tolist() == [4800, 4799, 17, 0, 0, 4799, 0, 17]
+    assert b.plain.refs[table[0, place]] == count
