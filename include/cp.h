@@ -591,7 +591,8 @@ int cp_pages_trim(cp_pages* p, const int32_t* keep, cp_stream_t stream);
  * on move, in ascending order, to the free pages below n, in ascending order.
  * moves[] says so for cp_cache_copy (`moves`: device int32 [capacity][2],
  * capacity at least pages / 2; *count their number), counts and tables are
- * rewritten. All pages from n on are then free. */
+ * rewritten. All pages from n on are then free. An entry that names a page
+ * whose count was 0 is left as it is (CP_ERR_DEVICE_BOUNDS). */
 int cp_pages_compact(cp_pages* p, int32_t* moves, int capacity, int32_t* count, cp_stream_t stream);
 
 /* Synchronise the device and return the sticky device status (CP_OK,

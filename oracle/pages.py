@@ -114,7 +114,7 @@ class Pool:
         for i in range(len(self.length)):
             for k in range(self.held(self.len_of(i))):
                 page = int(self.table[i, k])
-                if not self.ok(page) or page >= n and page not in to:
+                if not self.ok(page) or page in holes or page >= n and page not in to:
                     self.bad = True
                 elif page >= n:
                     self.table[i, k] = to[page]

@@ -34,11 +34,10 @@ struct PagesView {
   int32_t* status;
   // scratch
   int32_t* list;     // [pages] free pages in order
-  int32_t* map;      // [pages] where a page moves, or -1 (from page *live on)
+  int32_t* map;      // [pages] where a page is after a compaction; -1: nobody held it
   int32_t* tail;     // [pages] sequences that grow into a partly filled page; zeros between calls
   int32_t* keeper;   // [pages] the last of them, plus one; zeros between calls
   Plan* plan;        // [sequences]
-  int32_t* live;     // [1] pages that hold something
 };
 
 constexpr int kMostBlocks = 8;
@@ -411,16 +410,15 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const
 }
 
 // ------------------------------------------------------------------ compact
-// A sequence's entries, by `threads` threads of which this is the t-th: where the pages from n on went.
-__device__ __forceinline__ void remap(const PagesView& v, int i, int n, int t, int threads) {
+// A sequence's entries, by `threads` threads of which this is the t-th: where the pages are now. One that names a page that
+// nobody held stays as it is: what has moved there is not its.
+__device__ __forceinline__ void remap(const PagesView& v, int i, int t, int threads) {
   const int held = pages_for(v, length_of(v, i));
   int32_t* row = v.table + (int64_t)i * v.stride;
   for (int k = t; k < held; k += threads) {
-    const int page = row[k];
-    if (in_pool(v, page) && page < n) continue;
-    const int to = in_pool(v, page) ? __ldcg(v.map + page) : -1;
-    if (to >= 0) row[k] = to;
-    else set_status(v);
+    const int page = row[k], to = in_pool(v, page) ? __ldcg(v.map + page) : -1;
+    if (to < 0) set_status(v);
+    else if (to != page) row[k] = to;
   }
 }
 
@@ -454,9 +452,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, in
       const int page = p + k;
       if (page >= pages.end) break;
       if (page == n) below_n = before;
-      if (b >> k & 1) ++before;
-      else if (page < n) v.list[page - before] = page;
-      if (page >= n) v.map[page] = -1;
+      const bool live = b >> k & 1;
+      if (!live && page < n) v.list[page - before] = page;
+      before += live;
+      v.map[page] = live && page < n ? page : -1;
     }
   };
   if (ONE) {
@@ -477,10 +476,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, in
   int64_t below;
   before_me(below_told, &below);
   if (n == v.pages) below = n;             // nothing lies behind
-  if (blockIdx.x == 0 && tid == 0) {
-    *count = n - (int)below;
-    *v.live = n;
-  }
+  if (blockIdx.x == 0 && tid == 0) *count = n - (int)below;
   auto move_on = [&](uint32_t b, int p, int64_t before) {
     // loads first: those of four pages do not wait for one another
     int64_t at[4];
@@ -519,14 +515,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, in
   }
   if (!tables) return;
   meet();
-  for (int i = blockIdx.x * (kThreads / 32) + (tid >> 5); i < v.sequences; i += gridDim.x * (kThreads / 32)) remap(v, i, n, tid & 31, 32);
+  for (int i = blockIdx.x * (kThreads / 32) + (tid >> 5); i < v.sequences; i += gridDim.x * (kThreads / 32)) remap(v, i, tid & 31, 32);
 }
 
 // The tables, where they are too large for the one cluster: a block a sequence.
 __global__ void __launch_bounds__(128) remap_kernel(const PagesView v) {
   ptx::pdl_trigger();
   ptx::pdl_wait();
-  remap(v, blockIdx.x, *v.live, threadIdx.x, 128);
+  remap(v, blockIdx.x, threadIdx.x, 128);
 }
 
 // ------------------------------------------------------------------ checks
@@ -601,8 +597,7 @@ int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out) {
   v.tail = reinterpret_cast<int32_t*>(at + 2 * each);
   v.keeper = reinterpret_cast<int32_t*>(at + 3 * each);
   v.plan = reinterpret_cast<Plan*>(at + 4 * each);
-  v.live = reinterpret_cast<int32_t*>(at + 4 * each + plans);
-  v.status = v.live + 1;
+  v.status = reinterpret_cast<int32_t*>(at + 4 * each + plans);
   p->view = v;
   if (cudaMemset(p->memory, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cp_pages_destroy(p);

@@ -59,3 +59,30 @@ def test_a_forked_page_that_nobody_holds(count, place):
     b.fork([0, 1, 0, 2], [3, 5, 4, 7])
     assert b.plain.bad and b.plain.length.tolist() == [4800, 4799, 17, 0, 0, 4799, 0, 17]
     assert b.plain.refs[table[0, place]] == count
+
+
+@pytest.mark.parametrize("pages,sequences,width", [(40, 3, 8), (5000, 900, 30), (33000, 400, 30)])
+@pytest.mark.parametrize("above", [False, True])
+def test_a_compaction_over_pages_that_nobody_holds(pages, sequences, width, above):
+    """Entries that name them, below the number held or above, stay as they are; all others follow their pages."""
+    g = np.random.default_rng(pages)
+    table, length, refs = np.full((sequences, width), -1), np.zeros(sequences, np.int64), np.zeros(pages, np.int64)
+    order, at = g.permutation(pages), 0
+    for i in range(sequences):
+        k = int(g.integers(1, width + 1))
+        if at + k > pages * 2 // 3:
+            break
+        table[i, :k], length[i] = order[at:at + k], 16 * k
+        at += k
+    refs[order[:at]] = 1
+    short = max(2, at // 50)
+    named = order[:at]
+    named = (named[named >= at - short] if above else named[named < at - short])[:short]
+    refs[named] = 0
+    b = Both(refs, table, length, 16)
+    moves = b.compact()
+    assert b.plain.bad and moves and len(named) == short
+    b.pool.clear_status()
+    b.plain.bad = False
+    stays = np.isin(table, named)
+    np.testing.assert_array_equal(b.plain.table[stays], table[stays])
