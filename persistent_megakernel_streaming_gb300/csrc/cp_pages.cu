@@ -38,6 +38,8 @@ struct PagesView {
   int32_t* tail;     // [pages] sequences that grow into a partly filled page; zeros between calls
   int32_t* keeper;   // [pages] the last of them, plus one; zeros between calls
   Plan* plan;        // [sequences]
+  int32_t* marks;    // [sequences] pairs of a fork that name a sequence; zeros between calls
+  int32_t* clash;    // [sequences] whether a pair of the fork gets in another's way
 };
 
 constexpr int kMostBlocks = 8;
@@ -66,40 +68,6 @@ __device__ __forceinline__ int pages_for(const PagesView& v, int64_t length) {
   return (int)((length + (1 << v.shift) - 1) >> v.shift);
 }
 __device__ __forceinline__ bool in_pool(const PagesView& v, int page) { return (uint32_t)page < (uint32_t)v.pages; }
-
-// ------------------------------------------------------------------ fork
-// A block a pair; some 3 us whatever it copies: a launch and three loads that wait for one another. Whether pairs get in
-// each other's way is looked up among all of them by every block: no order between blocks is needed then.
-__global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int32_t* src, const int32_t* dst, int n) {
-  ptx::pdl_trigger();
-  ptx::pdl_wait();
-  const int pair = blockIdx.x, s = src[pair], d = dst[pair];
-  bool bad = (uint32_t)s >= (uint32_t)v.sequences || (uint32_t)d >= (uint32_t)v.sequences;
-  for (int i = threadIdx.x; i < n; i += 256) bad |= (i != pair && dst[i] == d) || src[i] == d;
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) set_status(v);
-    return;
-  }
-  const int len = length_of(v, s), held = pages_for(v, len);
-  const int32_t* from = v.table + (int64_t)s * v.stride;
-  int32_t* to = v.table + (int64_t)d * v.stride;
-  bool left_out = v.length[d] != 0;      // nobody writes it before the barrier
-  for (int i = threadIdx.x; i < held; i += 256) {
-    const int page = from[i];
-    left_out |= in_pool(v, page) && v.refs[page] < 1;    // nobody's: no call of this kernel makes it somebody's
-  }
-  if (__syncthreads_or(left_out)) {
-    if (threadIdx.x == 0) set_status(v);
-    return;
-  }
-  if (threadIdx.x == 0) v.length[d] = len;
-  for (int i = threadIdx.x; i < held; i += 256) {
-    const int page = from[i];
-    to[i] = page;
-    if (in_pool(v, page)) atomicAdd(v.refs + page, 1);
-    else set_status(v);
-  }
-}
 
 // ------------------------------------------------------------------ trim
 // A block a sequence, bound by the launch: 1 us behind another kernel for up to 1000 sequences, 8.6 for 8192.
@@ -226,6 +194,67 @@ __device__ __forceinline__ void each_page(const PagesView& v, Share pages, int64
     for (int k = 0; k < 4; ++k)
       if (bits >> k & 1) act(at++, p + k);
     rank += sum;
+  }
+}
+
+// ------------------------------------------------------------------ fork
+// Whether pairs get in each other's way, for more of them than each looks through for itself: a sequence that one pair
+// copies to, and no other pair names. Marks are counted, read and cleared by one cluster.
+constexpr int kCopied = 1 << 20;         // more than there are pairs
+__global__ void __launch_bounds__(kThreads) clash_kernel(const PagesView v, const int32_t* src, const int32_t* dst, int n) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
+  const int first = blockIdx.x * kThreads + threadIdx.x, step = gridDim.x * kThreads;
+  auto is_one = [&](int s) { return (uint32_t)s < (uint32_t)v.sequences; };
+  for (int i = first; i < n; i += step) {
+    const int s = src[i], d = dst[i];
+    if (is_one(s)) atomicOr(v.marks + s, kCopied);
+    if (is_one(d)) atomicAdd(v.marks + d, 1);
+  }
+  meet();
+  for (int i = first; i < n; i += step) v.clash[i] = !is_one(dst[i]) || __ldcg(v.marks + dst[i]) != 1;
+  meet();
+  for (int i = first; i < n; i += step) {
+    if (is_one(src[i])) v.marks[src[i]] = 0;
+    if (is_one(dst[i])) v.marks[dst[i]] = 0;
+  }
+}
+
+// A block a pair; some 3 us up to a hundred pairs whatever they copy: a launch and four loads that wait for one another.
+// OWN: whether pairs get in each other's way is looked up among all of them by every block, so that no order between blocks
+// is needed; otherwise the kernel in front says so.
+template <bool OWN>
+__global__ void __launch_bounds__(256) fork_kernel(const PagesView v, const int32_t* src, const int32_t* dst, int n) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
+  const int pair = blockIdx.x, s = src[pair], d = dst[pair];
+  bool bad = (uint32_t)s >= (uint32_t)v.sequences || (uint32_t)d >= (uint32_t)v.sequences;
+  if (OWN)
+    for (int i = threadIdx.x; i < n; i += 256) bad |= (i != pair && dst[i] == d) || src[i] == d;
+  else
+    bad |= v.clash[pair] != 0;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) set_status(v);
+    return;
+  }
+  const int len = length_of(v, s), held = pages_for(v, len);
+  const int32_t* from = v.table + (int64_t)s * v.stride;
+  int32_t* to = v.table + (int64_t)d * v.stride;
+  bool left_out = v.length[d] != 0;      // nobody writes it before the barrier
+  for (int i = threadIdx.x; i < held; i += 256) {
+    const int page = from[i];
+    left_out |= in_pool(v, page) && v.refs[page] < 1;    // nobody's: no call of this kernel makes it somebody's
+  }
+  if (__syncthreads_or(left_out)) {
+    if (threadIdx.x == 0) set_status(v);
+    return;
+  }
+  if (threadIdx.x == 0) v.length[d] = len;
+  for (int i = threadIdx.x; i < held; i += 256) {
+    const int page = from[i];
+    to[i] = page;
+    if (in_pool(v, page)) atomicAdd(v.refs + page, 1);
+    else set_status(v);
   }
 }
 
@@ -558,6 +587,9 @@ bool one_each(const PagesView& v, int blocks) {
   const auto share = [blocks](int n) { return ((n + blocks - 1) / blocks + 3) & ~3; };
   return share(v.pages) <= 4 * kThreads && share(v.sequences) <= kThreads;
 }
+// Pairs up to which each block of a fork looks through all of them itself, us of a fork and a trim behind it that way and
+// with marks: 1024 10.4 and 11.5, 1536 12.9 and 13.2, 2048 16.9 and 14.3, 8192 69 and 35, 32000 1153 and 119.
+constexpr int kOwnPairs = 1536;
 // Table entries up to which the cluster that compacts rewrites them itself, us that way and with a launch of their own: 64
 // entries 3.2 and 3.5, 4096 4.4 and 4.6, 32768 10.0 and 9.0, 262144 32.7 and 27.4.
 constexpr int64_t kFewEntries = 1 << 13;
@@ -585,7 +617,8 @@ int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out) {
   if (!p) return CP_ERR_NOMEM;
   p->device = device;
   const size_t each = up256((size_t)v.pages * 4), plans = up256((size_t)v.sequences * sizeof(Plan));
-  const size_t bytes = 4 * each + plans + 256;
+  const size_t marks = up256((size_t)v.sequences * 4);
+  const size_t bytes = 4 * each + plans + 2 * marks + 256;
   if (cudaMalloc(&p->memory, bytes) != cudaSuccess) {
     cudaGetLastError();
     delete p;
@@ -597,7 +630,9 @@ int cp_pages_create(const cp_pages_desc* desc, int device, cp_pages** out) {
   v.tail = reinterpret_cast<int32_t*>(at + 2 * each);
   v.keeper = reinterpret_cast<int32_t*>(at + 3 * each);
   v.plan = reinterpret_cast<Plan*>(at + 4 * each);
-  v.status = reinterpret_cast<int32_t*>(at + 4 * each + plans);
+  v.marks = reinterpret_cast<int32_t*>(at + 4 * each + plans);
+  v.clash = reinterpret_cast<int32_t*>(at + 4 * each + plans + marks);
+  v.status = reinterpret_cast<int32_t*>(at + 4 * each + plans + 2 * marks);
   p->view = v;
   if (cudaMemset(p->memory, 0, bytes) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cp_pages_destroy(p);
@@ -637,7 +672,10 @@ int cp_pages_clear_status(cp_pages* p) {
 int cp_pages_fork(cp_pages* p, const int32_t* src, const int32_t* dst, int n, cp_stream_t stream) {
   if (!p || !src || !dst || n < 1 || n > p->view.sequences) return CP_ERR_INVALID_ARG;
   DeviceGuard g(p->device);
-  return cuda_err(launch_as(fork_kernel, dim3(n), 1, 1, true, 256, 0, reinterpret_cast<cudaStream_t>(stream), p->view, src, dst, n));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (n <= kOwnPairs) return cuda_err(launch_as(fork_kernel<true>, dim3(n), 1, 1, true, 256, 0, s, p->view, src, dst, n));
+  const cudaError_t e = launch_as(clash_kernel, dim3(kMostBlocks), kMostBlocks, 1, true, kThreads, 0, s, p->view, src, dst, n);
+  return cuda_err(e == cudaSuccess ? launch_as(fork_kernel<false>, dim3(n), 1, 1, true, 256, 0, s, p->view, src, dst, n) : e);
 }
 
 int cp_pages_trim(cp_pages* p, const int32_t* keep, cp_stream_t stream) {

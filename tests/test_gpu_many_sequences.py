@@ -1,0 +1,74 @@
+"""Calls over as many sequences as there may be: what gets in whose way is found, and the work grows with their number, not
+with its square."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+from persistent_megakernel_streaming_gb300 import cp
+from test_gpu_pages import Both
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(a):
+    return torch.from_numpy(np.asarray(a, np.int32)).cuda()
+
+
+def fastest(f, repeats=7):
+    """Microseconds of the fastest of some calls."""
+    f()
+    best = np.inf
+    for _ in range(repeats):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        f()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+@pytest.mark.parametrize("pairs", [1535, 1536, 1537, 2500])
+def test_forks_that_get_in_each_others_way(pairs):
+    """Destinations named twice, copied from, out of range, held, and sources out of range, among many good pairs; then the
+    same again: nothing is left behind of the first call."""
+    g = np.random.default_rng(pairs)
+    n = 2 * pairs + 40
+    table, length, refs = np.full((n, 2), -1), np.zeros(n, np.int64), np.zeros(n, np.int64)
+    held = g.permutation(n)[: pairs // 2]
+    table[held, 0], length[held], refs[held] = held, g.integers(1, 17, len(held)), 1
+    free = np.setdiff1d(np.arange(n), held)
+    b = Both(refs, table, length, 16)
+    for _ in range(2):
+        src, dst = g.choice(held, pairs), g.permutation(free)[:pairs]
+        at = g.permutation(pairs)
+        dst[at[:40]] = dst[at[40:80]]                       # twice
+        dst[at[80:100]] = src[at[100:120]]                  # copied from by another, and held
+        src[at[120:140]] = dst[at[140:160]]                 # copied to by another
+        src[at[160]] = dst[at[160]]
+        src[at[161:165]], dst[at[165:169]] = [-1, n, 2 ** 31 - 1, -2 ** 31], [-1, n, 2 ** 31 - 1, -2 ** 31]
+        b.fork(src, dst)
+        assert b.plain.bad
+        b.pool.clear_status()
+        b.plain.bad = False
+        b.trim(np.where(np.isin(np.arange(n), held), 99, 0))
+    src, dst = g.choice(held, pairs), g.permutation(free)[:pairs]
+    b.fork(src, dst)
+    assert not b.plain.bad
+
+
+def test_the_time_of_a_fork_is_linear():
+    times = []
+    for n in (4000, 32000):
+        refs, table, length = np.zeros(2 * n), np.full((2 * n, 2), -1), np.zeros(2 * n)
+        refs[:n], table[:n, 0], length[:n] = 1, np.arange(n), 5
+        pool = cp.Pages(*(i32(a) for a in (refs, table, length)), 16)
+        src, dst, keep = i32(np.arange(n)), i32(np.arange(n) + n), i32(length)
+
+        def call():
+            pool.fork(src, dst)
+            pool.trim(keep)
+
+        times.append(fastest(call))
+        assert pool.status() == 0
+    assert times[1] < 16 * times[0], times                  # 8 times the pairs; 26 times as long with the square of them
