@@ -750,8 +750,8 @@ typedef struct cp_verify_args {
 int cp_verify(const cp_verify_args* args, int device, void* workspace, size_t workspace_bytes, cp_stream_t stream);
 
 /* Host only: the status that cp_verify returns for these arguments on a GPU,
- * and the workspace that it needs (may be NULL; none over a small vocabulary),
- * which depends on sequences, rows and vocab alone. */
+ * and the workspace that it needs (may be NULL; none for up to 2048 sequences
+ * over a small vocabulary), which depends on sequences, rows and vocab alone. */
 int cp_verify_check(const cp_verify_args* args, size_t* workspace_bytes);
 
 /* ------------------------------------------------------------ host checks */

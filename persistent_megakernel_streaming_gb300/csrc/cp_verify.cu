@@ -5,7 +5,8 @@
 // sequence, joins them, settles which drafted tokens are taken, and draws the
 // token behind them from one row: there it sums again, in 64-bit fixed point,
 // so that the draw does not depend on the order of the sums. Over a small
-// vocabulary the second reads the rows itself, and is the only one.
+// vocabulary the second reads the rows itself, and is the only one (but for a
+// look through the starts of many sequences).
 //
 // Of 48 sequences of 7 drafted tokens over 131075 fp32 logits (378 MB) the
 // first takes 59 us (6.4 TB/s), the second 34 to 38 behind it: 8 to settle what
@@ -47,6 +48,15 @@ constexpr int kMostCluster = 16, kMostSums = kMostCluster * kTokenThreads / 32;
 // 13.9 and 14.4; 256 of 5 over 4096 20.0 and 19.9; 1000 of 3 over 4096 40 and 44.
 constexpr int kDirect = 4096;
 
+// A start out of order leaves in doubt whose rows are whose, for every sequence. It is looked through once, by up to so many
+// blocks, a word for each of their four warps.
+constexpr int kOrderBlocks = 32;
+constexpr size_t kOrderBytes = kOrderBlocks * sizeof(int4);
+// Sequences up to which each block of a draw in one launch looks through start itself, us a call that way and with a launch in
+// front that does: plain draws over 2048 logits, 512 11.5 and 12.1, 2048 31.3 and 30.7, 8192 134 and 113, 65535 2323 and 954;
+// over 4, 2048 22.6 and 22.7, 65535 1978 and 608.
+constexpr int kOwnOrder = 2048;
+
 struct VerifyParams {
   const int32_t* start;
   const void* logits;
@@ -59,11 +69,13 @@ struct VerifyParams {
   int32_t* accepted;
   int32_t* token;
   float* prob;
+  int4* order;                         // [checks]: not 0 where a warp found start out of order
   Piece* pieces;                       // [2][rows][splits]: the target's, the draft's
   int n, rows, vocab, splits;
   int cluster, chunk;                  // blocks a sequence, logits a block
   int z_bits;                          // of the fixed point of their sums
   int direct;                          // one launch: the vocabulary is small
+  int checks;                          // blocks that look through start; 0: each block of the draw does
 };
 
 // Scaled logits are finite: NaN and -infinity become the lowest number, whose exponential next to any other is 0; a
@@ -127,6 +139,26 @@ __device__ __forceinline__ int sequence_of(const VerifyParams& p, int r) {
   return lo + __popc(__ballot_sync(0xffffffffu, lane < len && p.start[min(lo + lane, p.n - 1) + 1] <= r));
 }
 
+// Whether sequence i's rows are not some of the call's, in order.
+__device__ __forceinline__ bool out_of_order(const VerifyParams& p, int i) {
+  const int b = p.start[i], e = p.start[i + 1];
+  return b < 0 || e < b || e > p.rows;
+}
+// Block b's share of them.
+__device__ __forceinline__ void check_order(const VerifyParams& p, int b) {
+  bool bad = false;
+#pragma unroll 4
+  for (int i = b * kStatThreads + threadIdx.x; i < p.n; i += p.checks * kStatThreads) bad |= out_of_order(p, i);
+  bad = __any_sync(0xffffffffu, bad);
+  if ((threadIdx.x & 31) == 0) reinterpret_cast<int*>(p.order + b)[threadIdx.x >> 5] = bad;
+}
+// Where no other launch can see to it.
+__global__ void __launch_bounds__(kStatThreads) order_kernel(const __grid_constant__ VerifyParams p) {
+  ptx::pdl_trigger();
+  ptx::pdl_wait();
+  check_order(p, blockIdx.x);
+}
+
 // A thread's logits of a piece, in registers: 16 bytes at a time from a 16-byte boundary on, so that `skew` elements
 // in front of the row may belong to the first; what is not the row's is minus infinity. Few of them are wanted again, so
 // that they leave L2 first (48 sequences of 7 over 131075: 100.5 -> 96.2 us a call).
@@ -179,6 +211,7 @@ __global__ void __launch_bounds__(kStatThreads, 8) stats_kernel(const __grid_con
   ptx::pdl_trigger();
   Loads<T> x;
   if (!is_draft) x.load(row, p.vocab, part, p.splits, skew);                 // on their way while the row's sequence is looked up
+  if (!is_draft && blockIdx.x < p.checks) check_order(p, blockIdx.x);
   const int seq = sequence_of(p, r);                               // each warp for itself: no barrier
   if (seq >= p.n || p.start[seq] > r) return;                      // nobody's
   const float heat = p.temperature[seq];
@@ -432,17 +465,31 @@ __global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWi
   const int r0 = p.start[seq], r1 = p.start[seq + 1];
   const float heat = p.temperature[seq], by = scale_of(heat), u_token = p.u_token[seq];
   const bool greedy = !(heat > 0.f);
-  // a start out of order leaves in doubt whose rows are whose, for every sequence
-  bool out_of_order = false;
-  for (int i = threadIdx.x; i < p.n; i += kThreads) {
-    const int b = p.start[i], e = p.start[i + 1];
-    out_of_order |= b < 0 || e < b || e > p.rows;
+  int4 order = {};
+  bool bad = false;
+  if (DIRECT) {
+    if (p.checks) {
+      if (lane < p.checks) order = p.order[lane];
+    } else {
+      for (int i = threadIdx.x; i < p.n; i += kThreads) bad |= out_of_order(p, i);
+    }
+    bad |= (order.x | order.y | order.z | order.w) != 0;
+  } else {
+    bad = out_of_order(p, seq);                                      // the others' are known behind the launch in front
   }
   if (threadIdx.x == 0) sh.first = r1 - 1;
-  const bool bad = __syncthreads_or(out_of_order);
+  bad = __syncthreads_or(bad);
   const T* logits = static_cast<const T*>(p.logits);
   const T* drafts = greedy ? nullptr : static_cast<const T*>(p.draft_logits);
   bool waited = false;
+  auto wait = [&] {                                                  // for the sums, in front of which all but them is read
+    if (!waited) {
+      ptx::pdl_wait();
+      if (lane < p.checks) order = p.order[lane];
+    }
+    waited = true;
+  };
+  auto disorder = [&] { return __any_sync(0xffffffffu, (order.x | order.y | order.z | order.w) != 0) != 0; };
   // every block of the cluster does the same: a warp a row, or, where the rows are read here, one for the target's and one
   // for the draft's
   constexpr int kRowWarps = DIRECT ? 2 : 1;
@@ -463,12 +510,12 @@ __global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWi
       pair_sync(1 + warp / 2);
       if (of_draft) continue;
     } else {
-      if (!waited) ptx::pdl_wait();                                  // the sums, in front of which all but them is read
-      waited = true;
+      wait();
       a = piece_of(p, 0, r, lane);
       if (drafts && !last) b = piece_of(p, 1, r, lane);
       a = row_stats(p, 0, r, a);
       if (drafts && !last) b = row_stats(p, 1, r, b);
+      bad = disorder();
     }
     const float xp = in ? scaled(value(logits + r * p.row + d), by) : 0.f;
     const float xq = in && drafts ? scaled(value(drafts + r * p.draft_row + d), by) : 0.f;
@@ -484,12 +531,13 @@ __global__ void __launch_bounds__(DIRECT ? DIRECT : kTokenThreads, DIRECT == kWi
         sh.rows[1][r - r0] = b;
         sh.draft[r - r0] = d;
       }
-      if (!last && p.prob && rank == 0) p.prob[r] = pd;
+      if (!last && p.prob && rank == 0 && !bad) p.prob[r] = pd;
       if (!last && !yes) atomicMin(&sh.first, r);
     }
   }
   __syncwarp();
-  if (!DIRECT && !waited) ptx::pdl_wait();
+  if (!DIRECT) wait();
+  if (!DIRECT) bad |= disorder();
   if (!DIRECT) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
   if (bad || r0 == r1) {
     if (threadIdx.x == 0 && rank == 0) {
@@ -674,7 +722,10 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
     p->cluster *= 2;
   p->z_bits = 62;
   while (((int64_t)1 << (63 - p->z_bits)) < p->vocab) --p->z_bits;
-  *workspace = p->direct ? 0 : (size_t)2 * p->rows * std::max(splits(2), splits(4)) * sizeof(Piece);       // the same for both types
+  p->checks = p->direct && p->n <= kOwnOrder ? 0 : std::min(kOrderBlocks, (p->n + kStatThreads - 1) / kStatThreads);
+  if (!p->direct) p->checks = (int)std::min<int64_t>(p->checks, (int64_t)p->rows * p->splits);
+  *workspace = (p->checks ? kOrderBytes : 0) +
+               (p->direct ? 0 : (size_t)2 * p->rows * std::max(splits(2), splits(4)) * sizeof(Piece));        // the same for both types
   return CP_OK;
 }
 
@@ -686,7 +737,13 @@ cudaError_t launch_token(const VerifyParams& p, cudaStream_t s) {
 template <class T>
 cudaError_t launch(const VerifyParams& p, cudaStream_t s) {
   const bool wide = p.n <= kWideMost && p.rows > 4 * p.n;
-  if (p.direct) return wide ? launch_token<T, true, kWideThreads>(p, s) : launch_token<T, true, kTokenThreads>(p, s);
+  if (p.direct) {
+    if (p.checks) {
+      const cudaError_t e = launch_as(order_kernel, dim3((unsigned)p.checks), 1, 1, true, kStatThreads, 0, s, p);
+      if (e != cudaSuccess) return e;
+    }
+    return wide ? launch_token<T, true, kWideThreads>(p, s) : launch_token<T, true, kTokenThreads>(p, s);
+  }
   const dim3 grid((unsigned)(p.rows * p.splits), p.draft_logits ? 2 : 1);
   const cudaError_t e = launch_as(stats_kernel<T>, grid, 1, 1, true, kStatThreads, 0, s, p);
   if (e != cudaSuccess) return e;
@@ -739,7 +796,8 @@ int cp_verify(const cp_verify_args* args, int device, void* workspace, size_t wo
   const int dev = prepare(device);
   if (dev) return dev;
   DeviceGuard g(device);
-  p.pieces = static_cast<Piece*>(workspace);
+  p.order = static_cast<int4*>(workspace);
+  p.pieces = reinterpret_cast<Piece*>(static_cast<uint8_t*>(workspace) + kOrderBytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return cuda_err(args->dtype == CP_LOGITS_BF16 ? launch<__nv_bfloat16>(p, s) : launch<float>(p, s));
 }

@@ -72,3 +72,66 @@ def test_the_time_of_a_fork_is_linear():
         times.append(fastest(call))
         assert pool.status() == 0
     assert times[1] < 16 * times[0], times                  # 8 times the pairs; 26 times as long with the square of them
+
+
+def draws(n, vocab, dtype=torch.float32, **kw):
+    """A batch of plain draws, and what a call on it leaves."""
+    x = torch.zeros(n, vocab, dtype=dtype, device="cuda")
+    x[:, 1] = 60.0                                          # the token
+    z, f = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.full((n,), 0.5, device="cuda")
+    accepted, token, prob = torch.full_like(z, -7), torch.full_like(z, -7), torch.full_like(f, -7.0)
+
+    def call(start):
+        cp.verify(x, z, start, f, f, f, accepted, token, prob=prob, **kw)
+        return accepted, token, prob
+
+    return call
+
+
+@pytest.mark.parametrize("n", [1, 127, 128, 129, 2047, 2048, 2049, 4097, 65535])
+@pytest.mark.parametrize("vocab", [3, 4100])
+def test_one_start_out_of_order(n, vocab):
+    """Wherever it is; the next call, in order again, finds nothing of it."""
+    n = min(n, 5000) if vocab > 3 else n
+    call, good = draws(n, vocab), np.arange(n + 1)
+    for i in sorted({0, 1, n // 3, n - 128, n - 2, n - 1, n} & set(range(n + 1))):
+        for wrong in (-1, good[i] - 2, n + 1, 2 ** 31 - 1, -2 ** 31):
+            start = good.copy()
+            start[i] = wrong
+            if (np.diff(start) >= 0).all() and start[0] >= 0 and start[-1] <= n:
+                continue
+            accepted, token, prob = call(i32(start))
+            assert (accepted == -1).all() and (token == -1).all() and (prob == -7).all(), (i, wrong)
+        accepted, token, prob = call(i32(good))
+        assert (accepted == 0).all() and (token == 1).all() and (prob == -7).all()
+
+
+@pytest.mark.parametrize("vocab", [4, 4100])
+def test_the_time_of_a_verification_is_linear(vocab):
+    times = []
+    for n in (8000, 64000):
+        call, start = draws(n, vocab, torch.bfloat16), i32(np.arange(n + 1))
+        times.append(fastest(lambda: call(start)))
+    assert times[1] < 12 * times[0], times                  # 8 times the sequences; 16 to 20 times as long with the square of them
+
+
+def test_captured_calls_over_many_sequences():
+    """Two graphs with workspaces of their own, in turn, and one replayed behind a start out of order."""
+    n = 3000
+    good, bad = i32(np.arange(n + 1)), i32(np.arange(n + 1)[::-1])
+    start = good.clone()
+    graphs = []
+    for _ in range(2):
+        call = draws(n, 50, workspace=torch.full((cp.verify_workspace_bytes(n, n, 50),), 255, dtype=torch.uint8, device="cuda"))
+        out = call(start)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call(start)
+        graphs.append((graph, out, call))                   # the graph reads what the call holds
+    for k, which in enumerate((good, bad, good, good, bad, bad, good)):
+        start.copy_(which)
+        graph, (accepted, token, _), _ = graphs[k % 2]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (token == (1 if which is good else -1)).all() and (accepted == (0 if which is good else -1)).all()
