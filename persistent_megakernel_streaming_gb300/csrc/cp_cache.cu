@@ -416,10 +416,12 @@ int make_map(const cp_cache_desc& d, void* base, CUtensorMap* map) {
   const cuuint64_t strides[3] = {(cuuint64_t)d.token_stride * es, (cuuint64_t)d.head_stride * es, (cuuint64_t)d.page_stride * es};
   const cuuint32_t box[4] = {(cuuint32_t)(e4m3 ? d.head_dim : 64), (cuuint32_t)d.page_size, 1, 1};
   const cuuint32_t steps[4] = {1, 1, 1, 1};
-  const CUresult r = reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)(
-      map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, steps,
-      CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = in_context([&] {
+    return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(fn)(
+        map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims, strides, box, steps,
+        CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
   return r == CUDA_SUCCESS ? CP_OK : CP_ERR_UNSUPPORTED;
 }
 

@@ -1,6 +1,7 @@
 // cp_call.h -- what the host sides of the calls on caller-owned arrays share:
 // the current device kept, checks of addresses and strides, error codes.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -47,6 +48,16 @@ inline bool lie_apart(int64_t row, std::initializer_list<Axis> axes) {
 }
 
 inline int cuda_err(cudaError_t e) { return e == cudaSuccess ? CP_OK : CP_ERR_CUDA; }
+
+// A function of the driver's, which makes no context of its own: where a thread's first use of CUDA finds none, that of the
+// current device is made the thread's, and the function called again.
+template <class F>
+CUresult in_context(F call) {
+  CUresult r = call();
+  int device = 0;
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess) r = call();
+  return r;
+}
 
 // CP_OK on an sm_103 device.
 inline int check_device(int device) {

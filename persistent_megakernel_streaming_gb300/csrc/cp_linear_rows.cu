@@ -510,10 +510,12 @@ cudaError_t launch_many_rows(const ApplyParams& p, cudaStream_t s) {
   const cuuint64_t dims[2] = {(cuuint64_t)p.w.width, (cuuint64_t)p.rows};
   const cuuint64_t strides[1] = {(cuuint64_t)p.x_row * 2};
   const cuuint32_t box[2] = {kBlockK, (cuuint32_t)a.n}, steps[2] = {1, 1};
-  if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.x), dims, strides, box, steps,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
+  const CUresult made = in_context([&] {
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(p.x), dims, strides, box, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
+  if (made != CUDA_SUCCESS) return cudaErrorInvalidValue;
   return p.f32 ? launch<float>(p, a, map, s) : launch<__nv_bfloat16>(p, a, map, s);
 }
 
