@@ -148,15 +148,18 @@ __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // x / (1 + exp(-x)) to a few of fp32's half steps (the result may be fp32): the rounding of the exponent's product with
-// log2(e) is put back as a factor, and the quotient is one approximate reciprocal.
+// log2(e) is put back as a factor, and the quotient is one approximate reciprocal. Where the exponential passes 2^64 the 1
+// is nothing beside it, and the powers of two that would take it, or its reciprocal, out of range come last: results of
+// gates down to -91.8 are normal numbers, those of -103 the last that are not 0 (320 rows, 2048 to 2 x 6144: 14.7 -> 14.9 us).
 __device__ __forceinline__ float silu(float x) {
-  const float y = fminf(fmaxf(-x, -200.f), 200.f);           // past these the exponential is 0 or infinite
+  const float y = fminf(fmaxf(-x, -200.f), 200.f);           // past these the result is x, or 0
   const float t = __fmul_rn(y, 1.44269502f), rest = __fmaf_rn(y, 1.92596303e-8f, __fmaf_rn(y, 1.44269502f, -t));
+  const bool far = t > 64.f;
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(far ? t - 64.f : t));
   e = __fmul_rn(e, __fmaf_rn(rest, 0.693147182f, 1.f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return x * r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(far ? e : 1.f + e));
+  return __fmul_rn(x * r, far ? 0x1p-64f : 1.f);
 }
 
 // Results of one row from `feature` on, `n` of them (up to four): the residual added, rounded, written.
