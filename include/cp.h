@@ -700,7 +700,8 @@ enum cp_logits_dtype { CP_LOGITS_F32 = 0, CP_LOGITS_BF16 = 1 };
 typedef struct cp_verify_args {
   int sequences;              /* 1 .. 65535                                   */
   int rows;                   /* rows of the row arrays, 1 .. 2^20            */
-  int vocab;                  /* 1 .. 2^24, and rows * vocab up to 2^43       */
+  int vocab;                  /* 1 .. 2^24, and rows times vocab / 4096,
+                                 rounded up, at most 2^30                    */
   int dtype;                  /* enum cp_logits_dtype                         */
   const int32_t* start;       /* device [sequences + 1]                       */
   const void* logits;         /* device [rows][vocab]: the target's           */
