@@ -256,7 +256,7 @@ class Frame:
                     many(weights["heads"], P - 1))
         cuts = list(cuts or [])
         cut_arr = (C.c_int * max(1, len(cuts)))(*cuts)
-        opt = Options(cluster, max_ctas, timeout_ns, int(trace), len(cuts), cut_arr, debug_stall_task,
+        opt = Options(cluster, max_ctas, _int64(timeout_ns, "timeout_ns"), int(trace), len(cuts), cut_arr, debug_stall_task,
                       int(debug_stall_staging), int(generic_kernel), int(phase_waits))
         h = C.c_void_p()
         _check(lib().cp_create(C.byref(make_shape(shape)), C.byref(w), device, C.byref(opt), C.byref(h)),
@@ -321,6 +321,13 @@ def _int32(x, what: str) -> int:
     """x as the C side's int; ctypes would keep its low 32 bits and say nothing."""
     if not -2 ** 31 <= int(x) < 2 ** 31:
         raise ValueError(f"{what}: {x} is past 32 bits")
+    return int(x)
+
+
+def _int64(x, what: str) -> int:
+    """x as the C side's int64_t, likewise."""
+    if not -2 ** 63 <= int(x) < 2 ** 63:
+        raise ValueError(f"{what}: {x} is past 64 bits")
     return int(x)
 
 
@@ -433,7 +440,7 @@ class Cache:
         self.layout = (size, self.kv_heads, self.head_dim, self.page_size)
         self.desc = CacheDesc(int(size == 1), self.kv_heads, self.head_dim, self.page_size, self.pages, _ptr(k), _ptr(v),
                               *(_stride(k, i) for i in range(3)), _ptr(k_scale), _ptr(v_scale), *scale_strides,
-                              timeout_ns, int(debug_stall))
+                              _int64(timeout_ns, "timeout_ns"), int(debug_stall))
         h = C.c_void_p()
         _check(lib().cp_cache_create(C.byref(self.desc), k.device.index, C.byref(h)), "cp_cache_create")
         self._h = h
@@ -664,7 +671,7 @@ class Linear:
         self.outs = n // 2 if gated else n
         self.device_index = index
         self.desc = LinearDesc(_int32(n, "features"), _int32(self.width, "width"), self.group, int(self.gated), _ptr(q), _ptr(scale),
-                               _ptr(zero) or None, timeout_ns, int(debug_stall))
+                               _ptr(zero) or None, _int64(timeout_ns, "timeout_ns"), int(debug_stall))
         self.dtypes = {torch.bfloat16: 0, torch.float32: 1}
         self.x_dtypes = (torch.bfloat16, torch.int16)
         h = C.c_void_p()
