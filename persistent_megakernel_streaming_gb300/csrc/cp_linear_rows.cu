@@ -79,8 +79,10 @@ struct RowsShared {
   int abort;          // a wait gave up
 };
 
-// Bounded: after the timeout, or once another wait of the block gave up, false.
+// Bounded: after the timeout, or once another wait of the block gave up, false. The kernel in front takes as long as it
+// takes: x comes behind it, and the time counts from its end.
 __device__ __noinline__ bool wait_long(RowsShared& sh, uint32_t bar, uint32_t parity) {
+  pdl_wait();
   const uint64_t t0 = gtime();
   for (;;) {
 #pragma unroll 1
