@@ -112,8 +112,9 @@ __device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, ui
 // NT tiles of 8 rows of x; a block has TILES tiles of the weights (of a gated projection the gate's and the same of up),
 // its WARPS warps every so manieth record, U records at a time, whose loads are all under way before the first is used;
 // the first of them before the kernel in front has ended, since nobody writes weights. GROUPS of scales a record.
-// Bound by the chain of loads, widening (some 20 instructions a word of 8 weights) and products of a block, and by how many
-// blocks an SM holds: three of 8 warps, even where registers spill for it (us with that bound and without: 3 rows, 2048 to
+// Bound by the chain of loads, widening (13 operations a word of 8 weights) and products of a block, with nothing saturated (3
+// rows, 2048 to 50001: half of the issue slots, 3 TB/s of DRAM in ncu, warps waiting for loads), and by how many blocks an SM
+// holds: three of 8 warps, even where registers spill for it (us with that bound and without: 3 rows, 2048 to
 // 50001 13.6 and 15.5; 1 row, 8192 to 28672 in groups of 64 26.1 and 29.0; 2 rows, 6144 to 12288 in groups of 32 12.6 and
 // 16.6), but for 4 tiles with zero points of small groups (16.9 becomes 20.3); two of 16 with 2 tiles; with 1 the compiler
 // does better unbound (2.4 and 2.6).

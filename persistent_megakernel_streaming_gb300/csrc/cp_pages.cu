@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(kThreads) clash_kernel(const PagesView v, cons
   }
 }
 
-// A block a pair; some 3 us up to a hundred pairs whatever they copy: a launch and four loads that wait for one another.
+// A block a pair; of pairs of 40 pages 2.8 us for 1, 3.3 for 8, 5.5 for 64, 8.7 for 200: a launch, four loads that wait for one
+// another, and the counts.
 // OWN: whether pairs get in each other's way is looked up among all of them by every block, so that no order between blocks
 // is needed; otherwise the kernel in front says so.
 template <bool OWN>
@@ -293,8 +294,8 @@ struct Take {
   int had, n;
 };
 
-// ONE: no thread has more than one sequence, or more than four pages. From launch to launch 3.4 us for 1 sequence, 4.7 for
-// 1024 of 8192 pages (8.8 through scratch memory, as without ONE), 15 for 8200 of 40000.
+// ONE: no thread has more than one sequence, or more than four pages. From launch to launch 3.9 us for 1 sequence, 5.6 for
+// 1024 of 8192 pages (some 4 more through scratch memory, as without ONE), 16.4 for 8200 of 40000.
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const int32_t* add, int32_t* moves, int32_t* count) {
   __shared__ Told free_told, fresh_told, moved_told;
@@ -452,7 +453,7 @@ __device__ __forceinline__ void remap(const PagesView& v, int i, int t, int thre
 }
 
 // With n pages held, P(p) of them below page p: the free page p < n is the (p - P(p))-th hole, and the held page p >= n the
-// (P(p) - P(n))-th that moves. One prefix sum settles both. 3.1 us of 576 pages, 4.4 of 8256, 11.5 of 65600.
+// (P(p) - P(n))-th that moves. One prefix sum settles both. 3.1 us of 576 pages, 4.5 of 8256, 12.5 of 65600.
 template <bool ONE>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const PagesView v, int32_t* moves, int32_t* count, int tables) {
   __shared__ Told live_told, below_told;
@@ -575,7 +576,7 @@ int check_desc(const cp_pages_desc* d, PagesView* v) {
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // Blocks of the one cluster: the fewest whose threads get four pages and a sequence each (64 pages grown in 3.4 us, with 8
-// blocks 5.0; 4096 in 3.9 and 5.0; 8192 in 4.7 and 4.9), and all 8 where there are more.
+// blocks 5.0; 4096 in 3.9 and 5.0; 8192 in 4.7 and 4.9; some 0.5 more since), and all 8 where there are more.
 int blocks_for(const PagesView& v) {
   int n = 1;
   while (n < kMostBlocks && (v.pages > n * 4 * kThreads || v.sequences > n * kThreads)) n *= 2;

@@ -9,7 +9,7 @@
 // look through the starts of many sequences).
 //
 // Of 48 sequences of 7 drafted tokens over 131075 fp32 logits (378 MB) the
-// first takes 59 us (6.4 TB/s), the second 34 to 38 behind it: 8 to settle what
+// first takes 61 us (6.2 TB/s), the second 34 to 38 behind it: 8 to settle what
 // is taken, 12 for the exponentials, 4 to add them up, 6 for the weights.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -198,7 +198,8 @@ struct Loads {
 // Bound by HBM. A thread holds its 32 logits, so that their maximum comes first and nothing is rescaled; an exponential
 // is a product, a difference, a product, and ex2. Where NaN or infinities spoil that, the piece is done again with clamped
 // logits. Eight blocks of 128 threads an SM: us a call of 48 sequences of 7 over 131075 92.5, four of 256 94.5, two of 512
-// 96.0; three of 256, where no register spills, 103; half as many logits a thread 98.9.
+// 96.0; three of 256, where no register spills, 103; half as many logits a thread 98.9. (With one fused operation for product
+// and difference, which loses the bits that ex2_from keeps; with it each 2.5 more.)
 template <class T>
 __global__ void __launch_bounds__(kStatThreads, 8) stats_kernel(const __grid_constant__ VerifyParams p) {
   __shared__ Piece warps[kStatThreads / 32];
@@ -714,7 +715,8 @@ int check(const cp_verify_args* a, VerifyParams* p, size_t* workspace) {
   if ((int64_t)p->rows * p->splits > 1 << 30) return CP_ERR_UNSUPPORTED;             // blocks
   p->direct = p->vocab <= kDirect;
   // blocks a sequence: more while there is work for them and room for all at once, or until a block's share can be kept
-  // (16 blocks and 8, us: 16 sequences over 131075 26 and 35, 1 12 and 21; room for twice as many: 64 over 32000 16.6 -> 21.8)
+  // (16 blocks and 8, us: plain draws of 16 sequences over 131075 14.3 and 18.3, of 1 9.9 and 11.8, but 48 sequences of 7 92 and
+  // 89; room for twice as many: 64 draws over 32000 13.6 -> 17.6)
   auto cut = [&] { p->chunk = (p->vocab + p->cluster - 1) / p->cluster; };
   for (cut(); !p->direct && p->cluster < kMostCluster &&
               ((p->chunk > 2048 && (int64_t)p->n * p->cluster * 2 <= kResident) || kept_bytes(*p) > kMostKept);
