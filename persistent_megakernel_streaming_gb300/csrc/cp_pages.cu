@@ -445,10 +445,18 @@ __global__ void __launch_bounds__(kThreads) grow_kernel(const PagesView v, const
 __device__ __forceinline__ void remap(const PagesView& v, int i, int t, int threads) {
   const int held = pages_for(v, length_of(v, i));
   int32_t* row = v.table + (int64_t)i * v.stride;
-  for (int k = t; k < held; k += threads) {
-    const int page = row[k], to = in_pool(v, page) ? __ldcg(v.map + page) : -1;
-    if (to < 0) set_status(v);
-    else if (to != page) row[k] = to;
+  for (int k0 = t; k0 < held; k0 += 4 * threads) {
+    int page[4], to[4];                  // loads first: those of four entries do not wait for one another
+#pragma unroll
+    for (int u = 0; u < 4; ++u) page[u] = k0 + u * threads < held ? row[k0 + u * threads] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) to[u] = in_pool(v, page[u]) ? __ldcg(v.map + page[u]) : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (k0 + u * threads >= held) break;
+      if (to[u] < 0) set_status(v);
+      else if (to[u] != page[u]) row[k0 + u * threads] = to[u];
+    }
   }
 }
 
@@ -592,8 +600,8 @@ bool one_each(const PagesView& v, int blocks) {
 // with marks: 1024 10.4 and 11.5, 1536 12.9 and 13.2, 2048 16.9 and 14.3, 8192 69 and 35, 32000 1153 and 119.
 constexpr int kOwnPairs = 1536;
 // Table entries up to which the cluster that compacts rewrites them itself, us that way and with a launch of their own: 64
-// entries 3.2 and 3.5, 4096 4.4 and 4.6, 32768 10.0 and 9.0, 262144 32.7 and 27.4.
-constexpr int64_t kFewEntries = 1 << 13;
+// entries 3.1 and 3.6, 1024 3.8 and 4.1, 2048 5.0 and 4.9, 8000 7.0 and 5.8, 32768 13.5 and 11.3, 262144 77 and 59.
+constexpr int64_t kFewEntries = 1 << 11;
 
 }  // namespace
 
@@ -697,7 +705,8 @@ int cp_pages_compact(cp_pages* p, int32_t* moves, int capacity, int32_t* count, 
   if (!p || !moves || !count || capacity < p->view.pages / 2) return CP_ERR_INVALID_ARG;
   DeviceGuard g(p->device);
   int n = blocks_for(p->view);
-  // a warp rewrites a sequence's entries: 80 of 49 pages with 1970 moves 17 us for the three calls, in one block 20
+  // a warp rewrites a sequence's entries, and moves are shared out: 80 of 49 pages with 1970 moves 17 us for the three calls, in
+  // one block 20
   while (n < kMostBlocks && p->view.sequences > n * kThreads / 32) n *= 2;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int tables = (int64_t)p->view.sequences * p->view.width <= kFewEntries;

@@ -57,6 +57,36 @@ def test_forks_that_get_in_each_others_way(pairs):
     assert not b.plain.bad
 
 
+def test_a_captured_fork_of_many_pairs():
+    """Replayed with other pairs each time, some of them in each other's way."""
+    n = 2000
+    g = np.random.default_rng(0)
+    refs, table, length = np.zeros(2 * n), np.full((2 * n, 2), -1), np.zeros(2 * n)
+    refs[:n], table[:n, 0], length[:n] = 1, np.arange(n), g.integers(1, 17, n)
+    b = Both(refs, table, length, 16)
+    src, dst = i32(np.arange(n)), i32(np.arange(n) + n)
+    b.pool.fork(src, dst)
+    b.plain.fork(np.arange(n), np.arange(n) + n)
+    keep = np.where(np.arange(2 * n) < n, 99, 0)
+    b.trim(keep)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.pool.fork(src, dst)
+    for k in range(4):
+        s, d = g.integers(0, n, n), g.permutation(n) + n
+        if k % 2:
+            d[: n // 10] = d[n // 2: n // 2 + n // 10]
+        src.copy_(i32(s))
+        dst.copy_(i32(d))
+        graph.replay()
+        b.plain.fork(s, d)
+        b.same()
+        assert b.plain.bad == bool(k % 2)
+        b.pool.clear_status()
+        b.plain.bad = False
+        b.trim(keep)
+
+
 def test_the_time_of_a_fork_is_linear():
     times = []
     for n in (4000, 32000):
